@@ -88,7 +88,11 @@ typedef enum {
     WTCONV_ERR_ALIAS = 6        /* an output overlaps an input */
 } wtconv_status_t;
 
-typedef enum { WTCONV_F32 = 0, WTCONV_F16 = 1 } wtconv_dtype_t;
+typedef enum {
+    WTCONV_F32 = 0,
+    WTCONV_F16 = 1,
+    WTCONV_BF16 = 2 /* group norm and Newton-Schulz calls only; the layer's calls refuse it */
+} wtconv_dtype_t;
 
 typedef enum {
     WTCONV_OP_FWD = 0,
@@ -214,6 +218,127 @@ wtconv_status_t wtconv_unfused_backward_weight(const wtconv_desc_t *desc, const 
                                                const float *w_lvl, const float *s_lvl, float *dw_base,
                                                float *dbias, float *ds_base, float *dw_lvl, float *ds_lvl,
                                                void *workspace, size_t workspace_bytes, wtconv_stream_t stream);
+
+/* ---- Group norm with an activation ---------------------------------------
+ * What follows the layer in a block.  Channels c of an image fall into
+ * `groups` groups of C / groups neighbours; over the K = (C / groups) H W
+ * values of a group
+ *   mean = sum x / K,  rstd = 1 / sqrt(sum (x - mean)^2 / K + eps),
+ *   y = act(gamma[c] * (x - mean) * rstd + beta[c]),
+ * act one of wtconv_act_t.
+ * Layouts      x (and dx) lie as x_layout says, y (and dy) as y_layout does:
+ *              planes (WTCONV_NCHW) or channels last (WTCONV_NHWC), each
+ *              without gaps.  The two may differ: planes in and channels last
+ *              out is the step from the layer to a product over the channels.
+ * Types        activations fp32, fp16 or bf16; gamma, beta [C] fp32, each may
+ *              be NULL (ones, zeros); mean, rstd [N][groups] fp32.  All sums,
+ *              statistics and products are fp32 (or wider); an output element
+ *              is rounded once.
+ * Shape rules  n, c, h, w >= 1, groups >= 1 divides c, c * h * w < 2^31,
+ *              n * c < 2^31, eps > 0 and finite.
+ * Alignment    activations are aligned to their element; any such address
+ *              works, 16-byte aligned ones are faster.
+ * Values       a group with a NaN or an infinity comes out as NaN (relu of it
+ *              included); other groups are not touched by it.
+ * Ownership, execution and errors are those of the layer's calls above:
+ * kernels only, no allocation, no state, bitwise reproducible; the workspace
+ * (256-byte aligned, wtconv_group_norm_workspace_size) belongs to one call at
+ * a time. */
+typedef enum { WTCONV_NCHW = 0, WTCONV_NHWC = 1 } wtconv_layout_t;
+
+typedef enum {
+    WTCONV_ACT_NONE = 0,
+    WTCONV_ACT_RELU = 1, /* max(z, 0); slope 0 at z <= 0 */
+    WTCONV_ACT_SILU = 2, /* z / (1 + exp(-z)) */
+    WTCONV_ACT_GELU = 3  /* z / 2 (1 + erf(z / sqrt 2)) */
+} wtconv_act_t;
+
+typedef struct {
+    int64_t n, c, h, w;
+    int32_t groups;
+    int32_t dtype;    /* wtconv_dtype_t of x, y, dy and dx */
+    int32_t act;      /* wtconv_act_t */
+    int32_t x_layout; /* wtconv_layout_t of x and dx */
+    int32_t y_layout; /* wtconv_layout_t of y and dy */
+    float eps;
+} wtconv_norm_desc_t;
+
+/* Bytes of workspace for op WTCONV_OP_FWD or WTCONV_OP_BWD (other ops:
+ * WTCONV_ERR_UNSUPPORTED); may be 0. */
+wtconv_status_t wtconv_group_norm_workspace_size(const wtconv_norm_desc_t *desc, wtconv_op_t op, size_t *bytes);
+
+/* y, mean and rstd from x. */
+wtconv_status_t wtconv_group_norm_forward(const wtconv_norm_desc_t *desc, const void *x, const float *gamma,
+                                          const float *beta, void *y, float *mean, float *rstd, void *workspace,
+                                          size_t workspace_bytes, wtconv_stream_t stream);
+
+/* With dz = dy * act'(z), t = gamma dz, xh = (x - mean) rstd and E_g the mean
+ * over a group:
+ *   dx = rstd (t - E_g[t] - xh E_g[t xh]),
+ *   dgamma = sum_{n,h,w} dz xh,  dbeta = sum_{n,h,w} dz.
+ * mean and rstd are the forward call's.  dgamma and dbeta may each be NULL. */
+wtconv_status_t wtconv_group_norm_backward(const wtconv_norm_desc_t *desc, const void *x, const void *dy,
+                                           const float *gamma, const float *beta, const float *mean,
+                                           const float *rstd, void *dx, float *dgamma, float *dbeta, void *workspace,
+                                           size_t workspace_bytes, wtconv_stream_t stream);
+
+/* ---- Newton-Schulz orthogonalisation and the Muon step --------------------
+ * What is done with a weight gradient.  Each of `batch` matrices G of
+ * rows x cols is divided by its norm and taken towards the nearest matrix with
+ * orthonormal rows (or columns, where rows > cols) by `steps` steps of
+ *   X <- a X + (b A + c A^2) X,  A = X X^T,  X_0 = G / (|G|_F + eps),
+ *   (a, b, c) = (3.4445, -4.7750, 2.0315)
+ * (on X^T where rows > cols), whose odd polynomial lifts every singular value
+ * in (0, 1] towards about 1 (0.7 to 1.2).  The layer's parameters are such
+ * matrices: w_base one of C x k^2, w_lvl L of 4C x k^2.
+ * Types        g and out fp32, fp16 or bf16 (out in g's type, rounded once);
+ *              in the Muon step g may be any of them, weight and momentum are
+ *              fp32.  Products keep 22 bits of each factor and sum in fp32;
+ *              norms sum in fp64.
+ * Shape rules  1 <= batch <= 65535, 1 <= rows, cols <= 2^22, rows * cols < 2^31,
+ *              the smaller of rows and cols <= WTCONV_ORTHO_MAX_SIDE, 1 <=
+ *              steps <= WTCONV_ORTHO_MAX_STEPS, eps >= 0 and finite (a zero matrix
+ *              gives zeros, for eps = 0 NaN).
+ * Layout       row-major, matrices one after the other, no gaps; aligned to the
+ *              element.
+ * Values       a matrix with a NaN or an infinity comes out as NaN; the others
+ *              of the batch are not touched by it.
+ * Ownership, execution and errors as above; one workspace of
+ * wtconv_orthogonalize_workspace_size bytes (256-byte aligned) serves one of
+ * the two calls at a time. */
+#define WTCONV_ORTHO_MAX_SIDE 16384
+#define WTCONV_ORTHO_MAX_STEPS 16
+
+typedef struct {
+    int64_t batch, rows, cols;
+    int32_t dtype; /* wtconv_dtype_t of g (and out) */
+    int32_t steps;
+    float eps;
+} wtconv_ortho_desc_t;
+
+wtconv_status_t wtconv_orthogonalize_workspace_size(const wtconv_ortho_desc_t *desc, size_t *bytes);
+
+/* out = the iteration above on g; out must not overlap g. */
+wtconv_status_t wtconv_orthogonalize(const wtconv_ortho_desc_t *desc, const void *g, void *out, void *workspace,
+                                     size_t workspace_bytes, wtconv_stream_t stream);
+
+typedef struct {
+    float lr, momentum, weight_decay;
+    float scale;      /* factor of the update next to lr, e.g. sqrt(max(1, rows / cols)) */
+    int32_t nesterov; /* 0 or 1 */
+} wtconv_muon_t;
+
+/* One optimiser step:
+ *   momentum_out = mu momentum + (1 - mu) grad,
+ *   u = nesterov ? mu momentum_out + (1 - mu) grad : momentum_out,
+ *   weight_out = (1 - lr weight_decay) weight - lr scale orthogonalize(u).
+ * weight_out may be weight and momentum_out momentum (in place); other
+ * overlaps of an output with an argument are refused.  The hyperparameters
+ * are passed by value: a captured call replays with those it was captured
+ * with. */
+wtconv_status_t wtconv_muon_step(const wtconv_ortho_desc_t *desc, const wtconv_muon_t *hyper, const float *weight,
+                                 const void *grad, const float *momentum, float *weight_out, float *momentum_out,
+                                 void *workspace, size_t workspace_bytes, wtconv_stream_t stream);
 
 /* Human-readable name of a status code (static string). */
 const char *wtconv_status_string(wtconv_status_t status);

@@ -6,6 +6,10 @@ the library's HIP kernels.  Parameter tensors are float32 on the GPU:
     w_base (C, k, k), bias (C,) or None, s_base (C,),
     w_lvl (L, 4C, k, k), s_lvl (L, 4C)   (band b of channel c at index 4c+b).
 Activations are (N, C, H, W) float32 or float16, contiguous.
+
+Next to the layer stand the group norm with its activation that follows it in a
+block (wtconv_group_norm_*; float32, float16 or bfloat16, contiguous or channels
+last) and the update of its weights (wtconv_orthogonalize, wtconv_muon_step).
 """
 from __future__ import annotations
 
@@ -14,7 +18,9 @@ import ctypes
 from . import _native
 
 __all__ = ["wtconv_forward", "wtconv_backward_data", "wtconv_backward_weight", "wtconv_backward",
-           "wtconv_backward_weight_noalloc", "wtconv_workspace_size", "library_path"]
+           "wtconv_backward_weight_noalloc", "wtconv_workspace_size", "library_path",
+           "wtconv_group_norm_forward", "wtconv_group_norm_backward", "wtconv_group_norm_workspace_size",
+           "wtconv_orthogonalize", "wtconv_muon_step", "wtconv_orthogonalize_workspace_size"]
 
 
 def library_path() -> str:
@@ -209,3 +215,8 @@ def wtconv_backward_weight_noalloc(x, dy, w_base, bias, s_base, w_lvl, s_lvl, gr
                                             _ptr(dwl), _ptr(dsl), _stream(stream))
     _native.check(st, "wtconv_backward_weight_noalloc")
     return dw0, db0, ds0, dwl, dsl
+
+
+from ._train import (wtconv_group_norm_backward, wtconv_group_norm_forward,  # noqa: E402
+                     wtconv_group_norm_workspace_size, wtconv_muon_step, wtconv_orthogonalize,
+                     wtconv_orthogonalize_workspace_size)

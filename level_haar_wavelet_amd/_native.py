@@ -16,13 +16,31 @@ LIB_PATH = os.path.join(PKG, "libwtconv.so")
 WTCONV_OK = 0
 STATUS = {0: "WTCONV_OK", 1: "WTCONV_ERR_NULL", 2: "WTCONV_ERR_SHAPE", 3: "WTCONV_ERR_UNSUPPORTED",
           4: "WTCONV_ERR_WORKSPACE", 5: "WTCONV_ERR_HIP", 6: "WTCONV_ERR_ALIAS"}
-F32, F16 = 0, 1
+F32, F16, BF16 = 0, 1, 2
 OP_FWD, OP_BWD_DATA, OP_BWD_WEIGHT, OP_BWD = 0, 1, 2, 3
+NCHW, NHWC = 0, 1
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
 
 class WtconvDesc(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int64), ("c", ctypes.c_int64), ("h", ctypes.c_int64), ("w", ctypes.c_int64),
                 ("k", ctypes.c_int32), ("levels", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("c", ctypes.c_int64), ("h", ctypes.c_int64), ("w", ctypes.c_int64),
+                ("groups", ctypes.c_int32), ("dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("x_layout", ctypes.c_int32), ("y_layout", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class OrthoDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("steps", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class MuonHyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("scale", ctypes.c_float), ("nesterov", ctypes.c_int32)]
 
 
 class WtconvError(RuntimeError):
@@ -35,6 +53,7 @@ _lib = None
 
 # name -> argument types (pointers as void*), all return wtconv_status_t (int)
 _vp, _sz, _dp = ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(WtconvDesc)
+_ndp, _odp = ctypes.POINTER(NormDesc), ctypes.POINTER(OrthoDesc)
 SIGNATURES = {
     "wtconv_workspace_size": [_dp, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)],
     "wtconv_forward": [_dp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
@@ -47,6 +66,12 @@ SIGNATURES = {
     "wtconv_unfused_backward_data": [_dp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
     "wtconv_unfused_backward_weight": [_dp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
                                        _vp],
+    "wtconv_group_norm_workspace_size": [_ndp, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)],
+    "wtconv_group_norm_forward": [_ndp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "wtconv_group_norm_backward": [_ndp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "wtconv_orthogonalize_workspace_size": [_odp, ctypes.POINTER(ctypes.c_size_t)],
+    "wtconv_orthogonalize": [_odp, _vp, _vp, _vp, _sz, _vp],
+    "wtconv_muon_step": [_odp, ctypes.POINTER(MuonHyper), _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
 }
 
 

@@ -2,7 +2,8 @@
 
     python -m level_haar_wavelet_amd.build
 
-compiles every ``csrc/*.hip`` with hipcc for gfx950 into ``_build/`` and links
+compiles every ``csrc/*.hip`` (the layer) and ``csrc/train/*.hip`` (the group
+norm behind it and the Muon update of its weights) with hipcc for gfx950 into ``_build/`` and links
 ``level_haar_wavelet_amd/libwtconv.so``.  Packed fp32 instructions are switched
 off for all device code (``-Xclang -target-feature -Xclang -packed-fp32-ops``).
 """
@@ -16,6 +17,7 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+TRAIN = os.path.join(CSRC, "train")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libwtconv.so")
 ARCH = os.environ.get("WTCONV_ARCH", "gfx950")
@@ -27,7 +29,7 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", "-fno-strict-aliasing", "--offload-arch="
 
 
 def sources():
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".hip"))
+    return sorted(os.path.join(d, f) for d in (CSRC, TRAIN) for f in os.listdir(d) if f.endswith(".hip"))
 
 
 def _compile(src):

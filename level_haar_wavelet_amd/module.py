@@ -9,14 +9,18 @@ WTConv layer it reformulates.  Forward, data backward and parameter gradients
 all run in libwtconv's kernels (wtconv_forward, wtconv_backward_data,
 wtconv_backward_weight); this module only hands tensors to them.  The layer
 saves only its input for the backward pass.
+
+GroupNormAct2d is the normalisation and activation that follow the layer in a
+block, in the same manner.
 """
 from __future__ import annotations
 
 import torch
 
-from . import wtconv_backward_data, wtconv_backward_weight, wtconv_forward
+from . import (wtconv_backward_data, wtconv_backward_weight, wtconv_forward, wtconv_group_norm_backward,
+               wtconv_group_norm_forward)
 
-__all__ = ["WTConvFunction", "WTConv2d"]
+__all__ = ["WTConvFunction", "WTConv2d", "GroupNormActFunction", "GroupNormAct2d"]
 
 
 class WTConvFunction(torch.autograd.Function):
@@ -85,3 +89,65 @@ class WTConv2d(torch.nn.Module):
     def extra_repr(self):
         return "channels=%d, kernel_size=%d, levels=%d, bias=%s" % (self.channels, self.kernel_size, self.levels,
                                                                    self.bias is not None)
+
+
+class GroupNormActFunction(torch.autograd.Function):
+    """y = act(group_norm(x)) (wtconv_group_norm_forward / _backward).
+
+    x: (N, C, H, W) float32, float16 or bfloat16 on the GPU, contiguous or
+    channels last (other strides are made contiguous); gamma, beta: (C,)
+    float32 or None; channels_last: the layout of y (None: x's).  Saves x and the
+    groups' mean and rstd."""
+
+    @staticmethod
+    def forward(ctx, x, gamma, beta, groups, eps, act, channels_last):
+        if not (x.is_contiguous() or x.is_contiguous(memory_format=torch.channels_last)):
+            x = x.contiguous()
+        y, mean, rstd = wtconv_group_norm_forward(x, groups, gamma, beta, eps=eps, act=act,
+                                                  channels_last=channels_last)
+        ctx.save_for_backward(x, gamma, beta, mean, rstd)
+        ctx.groups, ctx.act = groups, act
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, gamma, beta, mean, rstd = ctx.saved_tensors
+        dy = dy.to(x.dtype)
+        if not (dy.is_contiguous() or dy.is_contiguous(memory_format=torch.channels_last)):
+            dy = dy.contiguous()
+        dx, dgamma, dbeta = wtconv_group_norm_backward(x, dy, ctx.groups, mean, rstd, gamma, beta, act=ctx.act)
+        need = ctx.needs_input_grad
+        return (dx if need[0] else None, dgamma if need[1] else None, dbeta if need[2] else None, None, None, None,
+                None)
+
+
+class GroupNormAct2d(torch.nn.Module):
+    """Group norm with its activation, as it follows a WTConv2d: `groups`
+    groups of neighbouring channels, act "none", "relu", "silu" or "gelu".
+    channels_last=True writes the output channels last whatever the input's
+    layout is (what a product over the channels reads); None keeps the input's.
+    Initialisation: gamma one, beta zero (none with affine=False).
+    """
+
+    def __init__(self, groups: int, channels: int, eps: float = 1e-5, act: str = "none", affine: bool = True,
+                 channels_last=None, device=None):
+        super().__init__()
+        if groups < 1 or channels % groups:
+            raise ValueError("groups must divide channels")
+        f = dict(device=device, dtype=torch.float32)
+        self.groups, self.channels, self.eps, self.act, self.channels_last = groups, channels, eps, act, channels_last
+        if affine:
+            self.gamma = torch.nn.Parameter(torch.ones(channels, **f))
+            self.beta = torch.nn.Parameter(torch.zeros(channels, **f))
+        else:
+            self.register_parameter("gamma", None)
+            self.register_parameter("beta", None)
+
+    def forward(self, x):
+        return GroupNormActFunction.apply(x, self.gamma, self.beta, self.groups, self.eps, self.act,
+                                          self.channels_last)
+
+    def extra_repr(self):
+        return "groups=%d, channels=%d, eps=%g, act=%s, affine=%s, channels_last=%s" % (
+            self.groups, self.channels, self.eps, self.act, self.gamma is not None, self.channels_last)

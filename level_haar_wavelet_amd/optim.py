@@ -1,0 +1,83 @@
+"""The Muon optimiser over libwtconv: every update is the momentum of the
+gradient, orthogonalised by the Newton-Schulz iteration (wtconv_muon_step).
+
+It is for parameters that are matrices: the layer's convolution weights and the
+products next to it.  A parameter of shape (*batch, rows, *rest) is a stack of
+matrices of rows x prod(rest):
+    WTConv2d.w_base (C, k, k)       one matrix of C x k^2,
+    WTConv2d.w_lvl  (L, 4C, k, k)   L matrices of 4C x k^2,
+    a product's weight (out, in)    itself.
+`batch_dims` says how many leading dimensions are the stack's; by default none
+for 2 and 3 dimensions and one for 4 (give batch_dims=0 for the (out, in, k, k)
+weight of an ordinary convolution).  Biases and the scales s_base and s_lvl are
+no matrices in that sense: leave them to another optimiser.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import wtconv_muon_step
+
+__all__ = ["Muon"]
+
+
+def _matrices(shape, batch_dims):
+    """(batch, rows, cols) of a parameter's shape."""
+    if batch_dims is None:
+        batch_dims = 1 if len(shape) == 4 else 0
+    if batch_dims < 0 or len(shape) < batch_dims + 2:
+        raise ValueError("Muon takes matrices: shape %s has none behind %d batch dimensions" % (tuple(shape),
+                                                                                               batch_dims))
+    return math.prod(shape[:batch_dims]), shape[batch_dims], math.prod(shape[batch_dims + 1:])
+
+
+class Muon(torch.optim.Optimizer):
+    """momentum <- mu momentum + (1 - mu) grad; u = mu momentum + (1 - mu) grad
+    (nesterov) or momentum; weight <- (1 - lr weight_decay) weight - lr s O(u),
+    with O the Newton-Schulz iteration of `steps` steps and
+    s = sqrt(max(1, rows / cols)).  Parameters are contiguous float32 tensors on
+    the GPU.  The hyperparameters go by value: a step captured into a graph
+    replays with those it was captured with."""
+
+    def __init__(self, params, lr=0.02, momentum=0.95, weight_decay=0.0, nesterov=True, steps=5, eps=1e-7,
+                 batch_dims=None):
+        if lr < 0 or weight_decay < 0 or not 0 <= momentum < 1:
+            raise ValueError("lr and weight_decay must be >= 0 and momentum in [0, 1)")
+        super().__init__(params, dict(lr=lr, momentum=momentum, weight_decay=weight_decay, nesterov=nesterov,
+                                      steps=steps, eps=eps, batch_dims=batch_dims))
+
+    def add_param_group(self, group):
+        super().add_param_group(group)
+        group = self.param_groups[-1]
+        try:
+            for p in group["params"]:
+                _matrices(p.shape, group["batch_dims"])
+                if p.dtype != torch.float32:
+                    raise TypeError("Muon takes float32 parameters, got %s" % p.dtype)
+        except (TypeError, ValueError):
+            self.param_groups.pop()
+            raise
+
+    @torch.no_grad()
+    def step(self, closure=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for group in self.param_groups:
+            for p in group["params"]:
+                if p.grad is None:
+                    continue
+                shape = _matrices(p.shape, group["batch_dims"])
+                if not p.is_contiguous():
+                    raise TypeError("Muon takes contiguous parameters")
+                state = self.state[p]
+                if "momentum_buffer" not in state:
+                    state["momentum_buffer"] = torch.zeros_like(p)
+                wtconv_muon_step(p.view(shape), p.grad.contiguous().view(shape),
+                                 state["momentum_buffer"].view(shape), lr=group["lr"], mu=group["momentum"],
+                                 weight_decay=group["weight_decay"], scale=math.sqrt(max(1.0, shape[1] / shape[2])),
+                                 nesterov=group["nesterov"], steps=group["steps"], eps=group["eps"])
+        return loss

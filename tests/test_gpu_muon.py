@@ -1,0 +1,244 @@
+"""Newton-Schulz orthogonalisation and the Muon step on the GPU against their
+formulas in fp64."""
+import math
+
+import pytest
+import torch
+
+import level_haar_wavelet_amd as wt
+from tests.train_util import DTYPES, U, ortho64, ortho_tol
+
+pytestmark = pytest.mark.gpu
+
+# batch, rows, cols: single values and vectors, both orientations, around the
+# tile sizes 16, 32, 64, 128, odd sizes, the layer's parameters, stacks
+SHAPES = [
+    (1, 1, 1), (3, 1, 7), (2, 9, 1), (1, 2, 3), (5, 3, 2), (2, 16, 16), (1, 15, 17), (2, 31, 33), (1, 32, 500),
+    (3, 384, 25), (1, 96, 25), (4, 32, 9), (2, 200, 49), (1, 49, 49), (2, 63, 65), (1, 64, 64), (2, 66, 64),
+    (1, 96, 384), (1, 127, 129), (1, 128, 128), (2, 130, 300), (1, 257, 255), (1, 100, 1999), (1, 2500, 40),
+    (1, 384, 1536), (2, 512, 512), (1, 700, 333), (1, 1, 5000), (1, 4097, 2),
+]
+
+
+def gradient(shape, seed, dtype=torch.float32):
+    g = torch.Generator().manual_seed(seed)
+    b, r, c = shape
+    k = min(r, c, 3)
+    v = torch.randn(b, r, c, generator=g) + torch.randn(b, r, k, generator=g) @ torch.randn(b, k, c, generator=g)
+    return (1e-3 * v).to(dtype)
+
+
+def within(got, ref, steps, dtype, what):
+    got = got.detach().cpu().double()
+    assert got.shape == ref.shape and torch.isfinite(got).all(), what
+    over = torch.linalg.matrix_norm(got - ref) / ortho_tol(ref, steps, dtype)
+    assert over.max() <= 1, "%s: %.3g times its tolerance" % (what, over.max())
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_against_the_formula(shape):
+    for k, dtype in enumerate(DTYPES.values()):
+        g = gradient(shape, 10 * SHAPES.index(shape) + k, dtype)
+        print(shape, dtype, flush=True)
+        within(wt.wtconv_orthogonalize(g.cuda()), ortho64(g), 5, dtype, "%s %s" % (shape, dtype))
+
+
+@pytest.mark.parametrize("shape", [(1, 25, 96), (2, 100, 80), (1, 130, 600), (1, 300, 300)], ids=str)
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 5, 6, 7])
+def test_number_of_steps(shape, steps):
+    g = gradient(shape, steps)
+    within(wt.wtconv_orthogonalize(g.cuda(), steps=steps), ortho64(g, steps), steps, torch.float32, str(shape))
+
+
+@pytest.mark.parametrize("shape", [(40, 40), (25, 384), (160, 200), (90, 700)], ids=str)
+def test_ranks_that_are_not_full(shape):
+    """One row of values, a matrix of rank 2, repeated rows: directions with
+    no value of their own stay empty."""
+    torch.manual_seed(0)
+    one = torch.zeros(shape)
+    one[shape[0] // 2] = torch.randn(shape[1])
+    low = torch.randn(shape[0], 2) @ torch.randn(2, shape[1])
+    same = torch.randn(1, shape[1]).expand(shape).contiguous()
+    for g in (one, low, same, one.mT.contiguous(), low.mT.contiguous()):
+        got = wt.wtconv_orthogonalize(g.cuda())
+        within(got, ortho64(g), 5, torch.float32, str(shape))
+    assert torch.equal(wt.wtconv_orthogonalize(one.cuda())[0], torch.zeros(shape[1], device="cuda"))
+
+
+@pytest.mark.parametrize("shape", [(2, 25, 64), (2, 150, 170), (2, 90, 700)], ids=str)
+@pytest.mark.parametrize("size", [1e-30, 1e-12, 1.0, 1e15, 1e30])
+def test_size_of_the_gradient(shape, size):
+    """The norm's square passes fp32's range at both ends."""
+    g = gradient(shape, 3) / 1e-3 * size
+    within(wt.wtconv_orthogonalize(g.cuda()), ortho64(g), 5, torch.float32, "%g" % size)
+    within(wt.wtconv_orthogonalize(g.cuda(), eps=0.0), ortho64(g, eps=0.0), 5, torch.float32, "%g, eps 0" % size)
+
+
+@pytest.mark.parametrize("shape", [(25, 64), (150, 170), (90, 700), (700, 90)], ids=str)
+def test_zero_and_bad_matrices_of_a_stack(shape):
+    g = gradient((4,) + shape, 8)
+    clean = wt.wtconv_orthogonalize(g.cuda())
+    g[0] = 0
+    g[2, 3, 4] = float("nan")
+    g[3, 1, 1] = float("inf")
+    got = wt.wtconv_orthogonalize(g.cuda())
+    assert torch.equal(got[0], torch.zeros_like(got[0]))
+    assert torch.equal(got[1], clean[1])
+    assert torch.isnan(got[2]).all() and torch.isnan(got[3]).all()
+
+
+def plain_muon(w, g, m, lr, mu, wd, scale, nesterov, steps, eps):
+    g, m, w = g.double(), m.double(), w.double()
+    m = mu * m + (1 - mu) * g
+    u = (1 - mu) * g + mu * m if nesterov else m
+    return (1 - lr * wd) * w - lr * scale * ortho64(u, steps, eps), m
+
+
+@pytest.mark.parametrize("nesterov", [True, False])
+@pytest.mark.parametrize("shape", [(1, 96, 25), (3, 64, 25), (1, 1, 9), (2, 100, 128), (1, 333, 200), (1, 120, 900)],
+                         ids=str)
+def test_muon_step(shape, nesterov):
+    for k, dtype in enumerate(DTYPES.values()):
+        g = gradient(shape, k, dtype)
+        torch.manual_seed(k)
+        w, m = 0.1 * torch.randn(shape), 1e-3 * torch.randn(shape)
+        # fp32 values of the hyperparameters, as the entry point takes them
+        lr, mu, wd, scale = (float(torch.tensor(v)) for v in (0.5, 0.9, 0.01, 1.5))
+        rw, rm = plain_muon(w, g, m, lr, mu, wd, scale, nesterov, 5, 1e-7)
+        wd_, gd, md = w.cuda(), g.cuda(), m.cuda()
+        wo, mo = torch.full_like(wd_, 9.0), torch.full_like(md, 9.0)
+        kw = dict(lr=lr, mu=mu, weight_decay=wd, scale=scale, nesterov=nesterov)
+        a = wt.wtconv_muon_step(wd_, gd, md, weight_out=wo, momentum_out=mo, **kw)
+        assert a[0] is wo and a[1] is mo
+        assert torch.equal(wd_.cpu(), w) and torch.equal(md.cpu(), m) and torch.equal(gd.cpu(), g)
+        # momentum: four roundings of its two terms
+        assert ((mo.cpu().double() - rm).abs() <= 4 * U * (mu * m.double().abs() + (1 - mu) * g.double().abs())
+                + 1e-40).all()
+        err = torch.linalg.matrix_norm(wo.cpu().double() - rw)
+        # the update's error times lr scale, and four roundings of the weight;
+        # U itself is off by 8 u, which the iteration magnifies as X_0's
+        tol = lr * scale * (ortho_tol(rw, 5, torch.float32) + 8 * U * 3.4445 ** 5) \
+            + 4 * U * torch.linalg.matrix_norm(w.double())
+        assert (err <= tol).all(), (shape, dtype, err / tol)
+        b = wt.wtconv_muon_step(wd_, gd, md, **kw)  # in place
+        assert b[0] is wd_ and b[1] is md and torch.equal(wd_, wo) and torch.equal(md, mo)
+
+
+@pytest.mark.parametrize("shape", [(1, 25, 64), (1, 150, 171), (2, 90, 701), (1, 333, 77)], ids=str)
+def test_unaligned_buffers_and_what_lies_behind_them(shape):
+    k = math.prod(shape)
+    for dtype in DTYPES.values():
+        bufs = [torch.randn(k + 30, device="cuda").to(dtype) for _ in range(2)]
+        g, out = (b[1:k + 1].view(shape) for b in bufs)
+        ref = wt.wtconv_orthogonalize(g.clone())
+        edge = [b[[0] + list(range(k + 1, k + 30))].clone() for b in bufs]
+        wt.wtconv_orthogonalize(g, out=out)
+        tol = 1e-4 if dtype == torch.float32 else 4 * torch.finfo(dtype).eps
+        assert torch.allclose(out.float(), ref.float(), atol=tol, rtol=tol)
+        for b, e in zip(bufs, edge):
+            assert torch.equal(b[[0] + list(range(k + 1, k + 30))], e)
+    f = [torch.randn(k + 30, device="cuda") for _ in range(5)]
+    w, g, m, wo, mo = (b[1:k + 1].view(shape) for b in f)
+    edge = [b[[0] + list(range(k + 1, k + 30))].clone() for b in f]
+    rw, rm = wt.wtconv_muon_step(w.clone(), g.clone(), m.clone(), lr=0.1)
+    wt.wtconv_muon_step(w, g, m, lr=0.1, weight_out=wo, momentum_out=mo)
+    assert torch.allclose(wo, rw, atol=1e-4) and torch.equal(mo, rm)
+    for b, e in zip(f, edge):
+        assert torch.equal(b[[0] + list(range(k + 1, k + 30))], e)
+
+
+def test_refusals_on_the_gpu():
+    g = torch.randn(8, 12, device="cuda")
+    for bad in (g.t(), g[0], g.double(), g.view(1, 2, 4, 12)):
+        with pytest.raises(TypeError):
+            wt.wtconv_orthogonalize(bad)
+    with pytest.raises(TypeError):
+        wt.wtconv_orthogonalize(g, out=torch.empty_like(g, dtype=torch.float16))
+    for kw in (dict(steps=0), dict(steps=17), dict(eps=-1.0), dict(out=g)):
+        with pytest.raises(wt._native.WtconvError):
+            wt.wtconv_orthogonalize(g, **kw)
+    with pytest.raises(wt._native.WtconvError):
+        wt.wtconv_orthogonalize(g[:0])
+    with pytest.raises(wt._native.WtconvError):
+        wt.wtconv_orthogonalize(g, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    w, m = g.clone(), g.clone()
+    with pytest.raises(TypeError):
+        wt.wtconv_muon_step(w.half(), g, m, lr=0.1)
+    with pytest.raises(TypeError):
+        wt.wtconv_muon_step(w[:4], g, m, lr=0.1)
+    with pytest.raises(TypeError):
+        wt.wtconv_muon_step(w, g, m.cpu(), lr=0.1)
+    with pytest.raises(wt._native.WtconvError):
+        wt.wtconv_muon_step(w, g, w, lr=0.1)  # one buffer for both
+
+
+@pytest.mark.parametrize("shape", [(2, 96, 25), (1, 300, 260), (2, 100, 900)], ids=str)
+def test_same_bits_every_time_and_on_other_streams(shape):
+    g = gradient(shape, 5).cuda()
+    ref = wt.wtconv_orthogonalize(g)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        got = []
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+            got.append(wt.wtconv_orthogonalize(g, stream=s))
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, ref) for t in got)
+
+
+@pytest.mark.parametrize("shape", [(2, 96, 25), (1, 300, 260), (2, 100, 900), (1, 64, 90)], ids=str)
+def test_captured_steps_replay_on_new_gradients(shape):
+    w, g, m = torch.randn(shape, device="cuda"), gradient(shape, 1).cuda(), torch.zeros(shape, device="cuda")
+    w2, m2 = w.clone(), m.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        wt.wtconv_muon_step(w.clone(), g, m.clone(), lr=0.1)
+        wt.wtconv_orthogonalize(g)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        wt.wtconv_muon_step(w, g, m, lr=0.1)
+        o = wt.wtconv_orthogonalize(g)
+    for r in range(4):
+        g.copy_(gradient(shape, 30 + r))
+        o.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        wt.wtconv_muon_step(w2, g, m2, lr=0.1)
+        assert torch.equal(w, w2) and torch.equal(m, m2) and torch.equal(o, wt.wtconv_orthogonalize(g))
+
+
+def test_optimizer_on_the_layer_and_its_state():
+    from level_haar_wavelet_amd.module import WTConv2d
+    from level_haar_wavelet_amd.optim import Muon
+
+    torch.manual_seed(0)
+    layer = WTConv2d(16, 5, 2, device="cuda")
+    lin = torch.nn.Linear(16, 40, device="cuda")
+    params = [layer.w_base, layer.w_lvl, lin.weight]
+    opt = Muon(params, lr=0.1, weight_decay=0.1)
+    ref = [(p.detach().cpu(), torch.zeros(p.shape)) for p in params]
+    for it in range(3):
+        for i, p in enumerate(params):
+            p.grad = 1e-2 * torch.randn(p.shape, device="cuda")
+            if i == 2:
+                p.grad = p.grad.t().contiguous().t()  # a gradient that is not contiguous
+        if it == 1:
+            params[0].grad = None  # left as it is
+        opt.step()
+        for i, p in enumerate(params):
+            if p.grad is None:
+                assert torch.equal(p.detach().cpu(), ref[i][0])
+                continue
+            b, r, c = ((1, 16, 25), (2, 64, 25), (1, 40, 16))[i]
+            v = lambda t: t.reshape(b, r, c)
+            rw, rm = plain_muon(v(ref[i][0]), v(p.grad.cpu()), v(ref[i][1]), 0.1, 0.95, 0.1, max(1, r / c) ** 0.5,
+                                True, 5, 1e-7)
+            assert torch.allclose(v(p.detach().cpu()).double(), rw, atol=1e-5)
+            assert torch.allclose(v(opt.state[p]["momentum_buffer"].cpu()).double(), rm, atol=1e-8)
+            ref[i] = (p.detach().cpu().clone(), opt.state[p]["momentum_buffer"].cpu().clone())
+    again = Muon(params, lr=0.1)
+    again.load_state_dict(opt.state_dict())
+    assert torch.equal(again.state[params[1]]["momentum_buffer"], opt.state[params[1]]["momentum_buffer"])
