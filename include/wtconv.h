@@ -296,6 +296,7 @@ wtconv_status_t wtconv_group_norm_backward(const wtconv_norm_desc_t *desc, const
  *              fp32.  Products keep 22 bits of each factor and sum in fp32;
  *              norms sum in fp64.
  * Shape rules  1 <= batch <= 65535, 1 <= rows, cols <= 2^22, rows * cols < 2^31,
+ *              batch * max(rows, 64) * max(cols, 64) < 2^36,
  *              the smaller of rows and cols <= WTCONV_ORTHO_MAX_SIDE, 1 <=
  *              steps <= WTCONV_ORTHO_MAX_STEPS, eps >= 0 and finite (a zero matrix
  *              gives zeros, for eps = 0 NaN).

@@ -1,9 +1,26 @@
 // wtconv_muon.hip -- Newton-Schulz orthogonalisation of a batch of matrices,
 // alone or inside the Muon step.
 //
-// X (n x m, n <= m; the transpose of a tall G) is held in fp32 and every
-// product runs on 16 x 16 tiles in LDS: A = X X^T, B = b A + c A A,
-// X <- a X + B X.
+// X is n x m with n <= m: G, or the transpose of a tall G.  A step is three
+// products: A = X X^T, P = a I + b A + c A A, X <- P X.
+//
+// What the iteration needs of its products: it lifts small singular values by
+// up to a^5 = 485, and every rounding error with them, so 16-bit factors (an
+// error of 2^-12 at the start) would leave errors of a few per cent in the
+// result.  The fp32 matrix instructions are exact enough but run at 1/16 of the
+// fp16 rate.  So every factor is held as the sum of two fp16 numbers, v S = hi
+// + lo with S a power of two (22 bits; S puts the largest possible |v| just
+// under fp16's range, so that lo of values down to 2^-17 is no subnormal), and
+// a product is three fp16 matrix products hi hi + hi lo + lo hi into one fp32
+// accumulator (lo lo is below the 22 bits): 3/16 of the fp32 rate's time.
+//
+// Layout of such a matrix ("planes"): row-major, the columns in blocks of 32,
+// each block 32 hi then 32 lo: 128 bytes, one cache line, one row of a tile.
+// Sides are padded with zeros to the tile, which no product changes.  All
+// products have the form L R^T with both operands' rows along k; X is therefore
+// kept as rows of X (for X X^T) and rows of X^T (for P X), and the products
+// whose results are symmetric (A, P) compute the tiles on and below the
+// diagonal and write each of them twice.
 #include <hip/hip_fp16.h>
 #include <hip/hip_runtime.h>
 
@@ -15,7 +32,12 @@
 namespace {
 
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
-constexpr int kThreads = 256, kTile = 16;
+constexpr int kThreads = 256;
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef float float16v __attribute__((ext_vector_type(16)));
+
+// ---- The update, its norm, and the first planes ----------------------------
 
 // The update the iteration starts from: G itself, or the Muon step's blend of
 // gradient and momentum.
@@ -31,16 +53,18 @@ __device__ inline float blend(const Blend &b, T g, float momentum_out)
     return b.nesterov ? fmaf(b.mu, momentum_out, (1.f - b.mu) * (float)g) : momentum_out;
 }
 
-// |U|_F of each matrix (summed in fp64), and momentum_out.
+// Partial sums of |U|^2 in fp64 (fp32 squares would overflow from 2^64 on and
+// vanish below 2^-75), one for each of gridDim.x workgroups of a matrix, and
+// momentum_out.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ortho_norm(const T *__restrict__ g, const float *momentum,
                                                        float *momentum_out, Blend bl, int64_t size,
-                                                       float *__restrict__ norm)
+                                                       double *__restrict__ parts)
 {
     __shared__ double lds[kThreads / 64];
-    const int64_t base = blockIdx.x * size;
+    const int64_t base = blockIdx.y * size;
     double a = 0.0;
-    for (int64_t i = threadIdx.x; i < size; i += kThreads) {
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < size; i += (int64_t)gridDim.x * kThreads) {
         const T gv = g[base + i];
         float m = 0.f;
         if (bl.muon) {
@@ -55,105 +79,367 @@ __global__ __launch_bounds__(kThreads) void ortho_norm(const T *__restrict__ g, 
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int i = 1; i < kThreads / 64; ++i) a += lds[i];
-        norm[blockIdx.x] = (float)sqrt(a);
+        parts[blockIdx.y * gridDim.x + blockIdx.x] = a;
     }
 }
 
-// X = U / (|U| + eps), transposed for a tall U.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void ortho_init(const T *__restrict__ g,
-                                                       const float *__restrict__ momentum_out, Blend bl, int rows,
-                                                       int cols, float eps, const float *__restrict__ norm,
-                                                       float *__restrict__ x)
+// hi and lo of 8 values.
+__device__ inline void split8(const float (&v)[8], half8 &hi, half8 &lo)
 {
-    const int64_t size = (int64_t)rows * cols, base = blockIdx.y * size;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= size) return;
-    const int r = (int)(i / cols), c = (int)(i % cols);
-    const float u = blend(bl, g[base + i], bl.muon ? momentum_out[base + i] : 0.f);
-    x[base + (rows > cols ? (int64_t)c * rows + r : i)] = u / (norm[blockIdx.y] + eps);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        hi[i] = (_Float16)v[i];
+        lo[i] = (_Float16)(v[i] - (float)hi[i]);
+    }
 }
 
-// D = alpha L op(R) + beta S, L p x k, op(R) k x q: R is q x k (nt) or k x q.
-template <bool NT>
-__global__ __launch_bounds__(kThreads) void product(const float *L, const float *R, const float *S, float *D, int p,
-                                                    int q, int k, float alpha, float beta)
+// Element offset of the 8 values from column k (a multiple of 8) of a row.
+__device__ inline int64_t plane_at(int row, int k, int kp) { return (int64_t)row * 2 * kp + (k >> 5) * 64 + (k & 31); }
+
+__device__ inline void store8(_Float16 *plane, int row, int k, int kp, const float (&v)[8])
 {
-    __shared__ float sl[kTile][kTile + 1], sr[kTile][kTile + 1];
-    const int64_t z = blockIdx.z;
-    L += z * p * k;
-    R += z * k * q;
-    const int tx = threadIdx.x % kTile, ty = threadIdx.x / kTile;
-    const int i = blockIdx.y * kTile + ty, j = blockIdx.x * kTile + tx;
-    float a = 0.f;
-    for (int k0 = 0; k0 < k; k0 += kTile) {
-        sl[ty][tx] = i < p && k0 + tx < k ? L[(int64_t)i * k + k0 + tx] : 0.f;
-        const int jr = blockIdx.x * kTile + ty;
-        if (NT)
-            sr[tx][ty] = jr < q && k0 + tx < k ? R[(int64_t)jr * k + k0 + tx] : 0.f;
-        else
-            sr[ty][tx] = j < q && k0 + ty < k ? R[(int64_t)(k0 + ty) * q + j] : 0.f;
+    half8 hi, lo;
+    split8(v, hi, lo);
+    _Float16 *p = plane + plane_at(row, k, kp);
+    *(half8 *)p = hi;
+    *(half8 *)(p + 32) = lo;
+}
+
+// Planes of S U / (|U| + eps) as rows of U (rp x cp) and of U^T, zero-padded;
+// one workgroup per 64 x 64 tile.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void ortho_split(const T *__restrict__ g,
+                                                        const float *__restrict__ momentum_out, Blend bl, int rows,
+                                                        int cols, int rp, int cp, float eps, float S,
+                                                        const double *__restrict__ parts, int nparts,
+                                                        _Float16 *__restrict__ u, _Float16 *__restrict__ ut)
+{
+    __shared__ float tile[64][65];
+    __shared__ double inv_s;
+    const int t = threadIdx.x, z = blockIdx.y;
+    if (t < 64) {
+        double a = 0.0;
+        for (int i = t; i < nparts; i += 64) a += parts[z * nparts + i];
+        for (int o = 32; o; o >>= 1) a += __shfl_xor(a, o);
+        if (t == 0) inv_s = (double)S / (sqrt(a) + (double)eps);
+    }
+    __syncthreads();
+    const double inv = inv_s;
+    const int64_t base = (int64_t)z * rows * cols;
+    const int r0 = blockIdx.x / (cp / 64) * 64, c0 = blockIdx.x % (cp / 64) * 64;
+#pragma unroll 4
+    for (int i = t >> 6; i < 64; i += 4) {
+        const int r = r0 + i, c = c0 + (t & 63);
+        float v = 0.f;
+        if (r < rows && c < cols) {
+            const int64_t e = base + (int64_t)r * cols + c;
+            v = (float)(blend(bl, g[e], bl.muon ? momentum_out[e] : 0.f) * inv);
+        }
+        tile[i][t & 63] = v;
+    }
+    __syncthreads();
+    u += (int64_t)z * rp * cp * 2;
+    ut += (int64_t)z * rp * cp * 2;
+    for (int i = t; i < 512; i += kThreads) {
+        float v[8];
+        const int r = i >> 3, k = (i & 7) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = tile[r][k + j];
+        store8(u, r0 + r, c0 + k, cp, v);
+        const int c = i & 63, q = (i >> 6) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = tile[q + j][c];
+        store8(ut, c0 + c, r0 + q, rp, v);
+    }
+}
+
+// ---- The products ------------------------------------------------------------
+
+enum Mode {
+    kStore,  // D = f acc
+    kPoly,   // D = a I + b A + c f acc, A the left operand's planes
+    kFinal   // the outputs, in the caller's layout and type
+};
+
+struct Product {
+    const _Float16 *L, *R;   // planes of lp x kp and rp x kp
+    _Float16 *D, *Dt;        // planes of lp x rp and (null or) of its transpose
+    int lp, rp, kp;          // padded sides
+    int sym;                 // D is symmetric: tiles on and below the diagonal only, Dt = D
+    int tiles, batch;        // tiles of a matrix; matrices
+    float f;                 // from the accumulator to D's scale
+    float a, b, c;           // kPoly: b includes the change of scale
+    // kFinal: element (i, j) of the product, i < n, j < m, is the output's
+    // (i, j), or (j, i) where tall
+    int n, m, tall;
+    const float *weight;     // Muon: weight_out = decay weight - step value
+    void *out;
+    float decay, step;
+};
+
+typedef const __attribute__((address_space(1))) void *GlobalPtr;
+typedef __attribute__((address_space(3))) void *LdsPtr;
+
+// D tile (TM x TN) = L R^T over k in steps of 32.  Four waves in 2 x 2, each
+// TM/2 x TN/2 of 32 x 32 matrix instructions.  A step's rows of L and R (128
+// bytes each) go from memory into LDS without registers between; the 16-byte
+// chunks of a row are permuted by chunk ^ (row / 2) % 8 so that the 16 rows a
+// read phase covers fall into different banks.  Two buffers: a step's reads
+// into registers come first, then the next step's loads are sent off, then its
+// 3 x (TM/64) x (TN/64) x 2 matrix instructions run.
+template <int TM, int TN, int MODE, typename T>
+__global__ __launch_bounds__(kThreads, 2) void product(Product a)
+{
+    constexpr int RM = TM / 64, RN = TN / 64;       // 32-row blocks of a wave
+    constexpr int kStage = (TM + TN) * 128;         // bytes of one buffer
+    constexpr int kPitch = TN + 1;                  // of the result's tile in LDS
+    constexpr int kResult = TM * kPitch * 4;
+    __shared__ __attribute__((aligned(128))) char lds[2 * kStage > kResult ? 2 * kStage : kResult];
+
+    // workgroups go to the 8 dies in turn: give each die neighbouring tiles
+    const int total = a.tiles * a.batch;
+    int id = blockIdx.x;
+    {
+        const int per = total / 8, rest = total % 8, die = id % 8, at = id / 8;
+        id = die * per + (die < rest ? die : rest) + at;
+    }
+    const int z = id / a.tiles;
+    int tile = id % a.tiles, ti, tj;
+    if (a.sym) {
+        ti = (int)((sqrtf(8.f * tile + 1.f) - 1.f) * 0.5f);
+        while ((ti + 1) * (ti + 2) / 2 <= tile) ++ti;
+        while (ti * (ti + 1) / 2 > tile) --ti;
+        tj = tile - ti * (ti + 1) / 2;
+    } else {
+        // bands of 8 tile rows, so that the tiles in flight share operands
+        const int nj = a.rp / TN, ni = a.lp / TM, band = tile / (8 * nj), h = ni - 8 * band < 8 ? ni - 8 * band : 8;
+        const int in = tile - band * 8 * nj;
+        ti = band * 8 + in % h;
+        tj = in / h;
+    }
+    const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
+    const int64_t ldb = (int64_t)a.kp * 4;  // bytes of a row
+    const char *L = (const char *)a.L + ((int64_t)z * a.lp + ti * TM) * ldb;
+    const char *R = (const char *)a.R + ((int64_t)z * a.rp + tj * TN) * ldb;
+
+    // this lane's source of each load: 8 rows a load, row lane / 8 of them
+    constexpr int kLoads = (TM + TN) / 32;  // per wave
+    const char *src[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int row = (wave * kLoads + i) * 8 + (lane >> 3);
+        const int chunk = (lane & 7) ^ ((row >> 1) & 7);
+        src[i] = (row < TM ? L + row * ldb : R + (row - TM) * ldb) + chunk * 16;
+    }
+    auto load = [&](int k, int buf) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            __builtin_amdgcn_global_load_lds((GlobalPtr)(src[i] + (int64_t)k * 128),
+                                             (LdsPtr)(lds + buf * kStage + (wave * kLoads + i) * 1024), 16, 0, 0);
+    };
+    auto frag = [&](int buf, int row, int chunk) {
+        return *(const half8 *)(lds + buf * kStage + row * 128 + ((chunk ^ ((row >> 1) & 7)) * 16));
+    };
+
+    float16v acc[RM][RN] = {};
+    const int wi = (wave >> 1) * (TM / 2), wj = TM + (wave & 1) * (TN / 2), lr = lane & 31, lc = lane >> 5;
+    const int steps = a.kp / 32;
+    load(0, 0);
+    for (int k = 0; k < steps; ++k) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
-        for (int t = 0; t < kTile; ++t) a = fmaf(sl[ty][t], sr[t][tx], a);
-        __syncthreads();
+        half8 l[2][RM][2], r[2][RN][2];  // [k half][block][hi, lo]
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+#pragma unroll
+                for (int i = 0; i < RM; ++i) l[kk][i][p] = frag(k & 1, wi + i * 32 + lr, p * 4 + kk * 2 + lc);
+#pragma unroll
+                for (int j = 0; j < RN; ++j) r[kk][j][p] = frag(k & 1, wj + j * 32 + lr, p * 4 + kk * 2 + lc);
+            }
+        __builtin_amdgcn_sched_barrier(0);
+        if (k + 1 < steps) load(k + 1, (k + 1) & 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int i = 0; i < RM; ++i)
+#pragma unroll
+                for (int j = 0; j < RN; ++j) {
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[kk][i][0], r[kk][j][1], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[kk][i][1], r[kk][j][0], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[kk][i][0], r[kk][j][0], acc[i][j], 0, 0, 0);
+                }
     }
-    if (i >= p || j >= q) return;
-    const int64_t o = z * p * q + (int64_t)i * q + j;
-    D[o] = alpha * a + (S ? beta * S[o] : 0.f);
-}
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void ortho_out(const float *__restrict__ x, T *__restrict__ out, int rows,
-                                                      int cols)
-{
-    const int64_t size = (int64_t)rows * cols, base = blockIdx.y * size;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= size) return;
-    const int r = (int)(i / cols), c = (int)(i % cols);
-    out[base + i] = (T)x[base + (rows > cols ? (int64_t)c * rows + r : i)];
-}
+    // the tile through LDS, so that rows and columns go out in 16-byte pieces
+    __syncthreads();
+    float *res = (float *)lds;
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+        for (int j = 0; j < RN; ++j)
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                res[(wi + i * 32 + 8 * (q >> 2) + 4 * lc + (q & 3)) * kPitch + wj - TM + j * 32 + lr] = acc[i][j][q];
+    __syncthreads();
 
-__global__ __launch_bounds__(kThreads) void muon_out(const float *__restrict__ x, const float *weight,
-                                                     float *weight_out, int rows, int cols, float decay, float step)
-{
-    const int64_t size = (int64_t)rows * cols, base = blockIdx.y * size;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= size) return;
-    const int r = (int)(i / cols), c = (int)(i % cols);
-    const float o = x[base + (rows > cols ? (int64_t)c * rows + r : i)];
-    weight_out[base + i] = fmaf(decay, weight[base + i], -step * o);
-}
-
-template <typename T>
-hipError_t run(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &a, void *workspace, hipStream_t stream)
-{
-    const int rows = (int)d.rows, cols = (int)d.cols, n = rows < cols ? rows : cols, m = rows < cols ? cols : rows;
-    const unsigned batch = (unsigned)d.batch;
-    const int64_t size = (int64_t)rows * cols;
-    char *ws = (char *)workspace;
-    float *x = (float *)ws, *y = (float *)(ws += align256(size * 4 * batch));
-    float *p = (float *)(ws += align256(size * 4 * batch));
-    float *q = (float *)(ws += align256((size_t)n * n * 4 * batch));
-    float *norm = (float *)(ws += align256((size_t)n * n * 4 * batch));
-    Blend bl = {a.hyper != nullptr, a.hyper ? a.hyper->nesterov : 0, a.hyper ? a.hyper->momentum : 0.f};
-    const T *g = (const T *)a.g;
-    const dim3 th(kThreads), flat((unsigned)((size + kThreads - 1) / kThreads), batch);
-    ortho_norm<T><<<dim3(batch), th, 0, stream>>>(g, a.momentum, a.momentum_out, bl, size, norm);
-    ortho_init<T><<<flat, th, 0, stream>>>(g, a.momentum_out, bl, rows, cols, d.eps, norm, x);
-    const unsigned tn = (n + kTile - 1) / kTile, tm = (m + kTile - 1) / kTile;
-    for (int s = 0; s < d.steps; ++s) {
-        product<true><<<dim3(tn, tn, batch), th, 0, stream>>>(x, x, nullptr, p, n, n, m, 1.f, 0.f);
-        product<false><<<dim3(tn, tn, batch), th, 0, stream>>>(p, p, p, q, n, n, n, kC, kB);
-        product<false><<<dim3(tm, tn, batch), th, 0, stream>>>(q, x, x, y, n, m, n, 1.f, kA);
-        float *t = x;
-        x = y;
-        y = t;
+    const int i0 = ti * TM, j0 = tj * TN;
+    if (MODE == kFinal) {
+        const int64_t base = (int64_t)z * a.n * a.m;
+        for (int e = t; e < TM * TN; e += kThreads) {
+            const int i = a.tall ? e % TM : e / TN, j = a.tall ? e / TM : e % TN;
+            if (i0 + i >= a.n || j0 + j >= a.m) continue;
+            const float v = res[i * kPitch + j] * a.f;
+            const int64_t o = base + (a.tall ? (int64_t)(j0 + j) * a.n + i0 + i : (int64_t)(i0 + i) * a.m + j0 + j);
+            if (a.weight)
+                ((float *)a.out)[o] = fmaf(a.decay, a.weight[o], -a.step * v);
+            else
+                ((T *)a.out)[o] = (T)v;
+        }
+        return;
     }
-    if (a.hyper)
-        muon_out<<<flat, th, 0, stream>>>(x, a.weight, a.weight_out, rows, cols,
-                                          1.f - a.hyper->lr * a.hyper->weight_decay, a.hyper->lr * a.hyper->scale);
+    _Float16 *D = a.D + (int64_t)z * a.lp * a.rp * 2;
+    const _Float16 *A = a.L + (int64_t)z * a.lp * a.kp * 2;
+    for (int e = t; e < TM * TN / 8; e += kThreads) {
+        const int i = e / (TN / 8), j = (e % (TN / 8)) * 8;
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = res[i * kPitch + j + q] * a.f;
+        if (MODE == kPoly) {
+            const _Float16 *p = A + plane_at(i0 + i, j0 + j, a.kp);
+            const half8 hi = *(const half8 *)p, lo = *(const half8 *)(p + 32);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                v[q] = fmaf(a.b, (float)hi[q] + (float)lo[q], a.c * v[q]);
+                if (i0 + i == j0 + j + q) v[q] += a.a;
+            }
+            if (a.sym && ti != tj)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) res[i * kPitch + j + q] = v[q];
+        }
+        store8(D, i0 + i, j0 + j, a.rp, v);
+    }
+    _Float16 *Dt = a.sym ? (ti != tj ? a.D : nullptr) : a.Dt;
+    if (!Dt) return;
+    if (MODE == kPoly) __syncthreads();
+    Dt += (int64_t)z * a.lp * a.rp * 2;
+    for (int e = t; e < TM * TN / 8; e += kThreads) {
+        const int j = e % TN, i = (e / TN) * 8;
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = res[(i + q) * kPitch + j] * (MODE == kPoly ? 1.f : a.f);
+        store8(Dt, j0 + j, i0 + i, a.lp, v);
+    }
+}
+
+// ---- Host ----------------------------------------------------------------------
+
+int pad(int v, int t) { return (v + t - 1) / t * t; }
+
+// Sides and buffers of the tiled path.
+struct Plan {
+    int n, m, tall, tile, np, mp, parts;
+    size_t xbytes, abytes;  // planes of X and of A, all matrices
+};
+
+Plan make_plan(const wtconv_ortho_desc_t &d)
+{
+    Plan p;
+    p.tall = d.rows > d.cols;
+    p.n = (int)(p.tall ? d.cols : d.rows);
+    p.m = (int)(p.tall ? d.rows : d.cols);
+    const int64_t t128 = (int64_t)((p.n + 127) / 128) * ((p.m + 127) / 128) * d.batch;
+    p.tile = t128 >= 256 ? 128 : 64;
+    p.np = pad(p.n, p.tile);
+    p.mp = pad(p.m, p.tile);
+    p.xbytes = align256((size_t)p.np * p.mp * 4 * d.batch);
+    p.abytes = align256((size_t)p.np * p.np * 4 * d.batch);
+    const int64_t want = ((int64_t)p.n * p.m + 8 * kThreads - 1) / (8 * kThreads);
+    p.parts = (int)(want < 256 ? want : 256);
+    return p;
+}
+
+template <int MODE, typename T = float>
+void launch_product(const Plan &pl, Product a, hipStream_t stream)
+{
+    const int ni = a.lp / pl.tile, nj = a.rp / pl.tile;
+    a.tiles = a.sym ? ni * (ni + 1) / 2 : ni * nj;
+    const dim3 grid((unsigned)(a.tiles * a.batch));
+    if (pl.tile == 128)
+        product<128, 128, MODE, T><<<grid, dim3(kThreads), 0, stream>>>(a);
     else
-        ortho_out<T><<<flat, th, 0, stream>>>(x, (T *)a.out, rows, cols);
+        product<64, 64, MODE, T><<<grid, dim3(kThreads), 0, stream>>>(a);
+}
+
+template <typename T>
+hipError_t run(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &o, void *workspace, hipStream_t stream)
+{
+    const Plan pl = make_plan(d);
+    const unsigned batch = (unsigned)d.batch;
+    const int64_t size = d.rows * d.cols;
+    char *ws = (char *)workspace;
+    _Float16 *x[2], *xt[2];  // rows of X, rows of X^T
+    for (int i = 0; i < 2; ++i) {
+        x[i] = (_Float16 *)ws;
+        xt[i] = (_Float16 *)(ws += pl.xbytes);
+        ws += pl.xbytes;
+    }
+    _Float16 *A = (_Float16 *)ws, *P = (_Float16 *)(ws += pl.abytes);
+    double *parts = (double *)(ws += pl.abytes);
+    const Blend bl = {o.hyper != nullptr, o.hyper ? o.hyper->nesterov : 0, o.hyper ? o.hyper->momentum : 0.f};
+    const T *g = (const T *)o.g;
+    ortho_norm<T><<<dim3(pl.parts, batch), dim3(kThreads), 0, stream>>>(g, o.momentum, o.momentum_out, bl, size,
+                                                                        parts);
+    const int rp = pl.tall ? pl.mp : pl.np, cp = pl.tall ? pl.np : pl.mp;
+    // |X|, |A| and |P| (spectral) stay below 1.21, 1.47 and 3.45: times 2^14
+    // that is within fp16's 65504
+    const float S = 16384.f;
+    ortho_split<T><<<dim3((cp / 64) * (rp / 64), batch), dim3(kThreads), 0, stream>>>(
+        g, o.momentum_out, bl, (int)d.rows, (int)d.cols, rp, cp, d.eps, S, parts, pl.parts, pl.tall ? xt[0] : x[0],
+        pl.tall ? x[0] : xt[0]);
+    for (int s = 0; s < d.steps; ++s) {
+        const int at = s & 1;
+        Product a = {};
+        a.batch = (int)batch;
+        a.L = a.R = x[at];
+        a.D = A;
+        a.lp = a.rp = pl.np;
+        a.kp = pl.mp;
+        a.sym = 1;
+        a.f = 1.f / S;  // acc is in units of S^2, D in units of S
+        launch_product<kStore>(pl, a, stream);
+        a.L = a.R = A;
+        a.D = P;
+        a.kp = pl.np;
+        a.a = kA * S;
+        a.b = kB;
+        a.c = kC;
+        launch_product<kPoly>(pl, a, stream);
+        a.L = P;
+        a.R = xt[at];
+        a.D = x[1 - at];
+        a.Dt = xt[1 - at];
+        a.rp = pl.mp;
+        a.sym = 0;
+        if (s + 1 < d.steps) {
+            launch_product<kStore>(pl, a, stream);
+            continue;
+        }
+        a.f = 1.f / (S * S);
+        a.n = pl.n;
+        a.m = pl.m;
+        a.tall = pl.tall;
+        a.out = o.out;
+        if (o.hyper) {
+            a.weight = o.weight;
+            a.out = o.weight_out;
+            a.decay = 1.f - o.hyper->lr * o.hyper->weight_decay;
+            a.step = o.hyper->lr * o.hyper->scale;
+        }
+        launch_product<kFinal, T>(pl, a, stream);
+    }
     return hipGetLastError();
 }
 
@@ -161,8 +447,8 @@ hipError_t run(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &a, void *worksp
 
 size_t wtc_ortho_workspace(const wtconv_ortho_desc_t &d)
 {
-    const size_t size = (size_t)(d.rows * d.cols), n = (size_t)(d.rows < d.cols ? d.rows : d.cols), b = (size_t)d.batch;
-    return 2 * align256(size * 4 * b) + 2 * align256(n * n * 4 * b) + align256(4 * b);
+    const Plan p = make_plan(d);
+    return 4 * p.xbytes + 2 * p.abytes + align256(sizeof(double) * p.parts * d.batch);
 }
 
 hipError_t wtc_launch_ortho(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &a, void *workspace, hipStream_t stream)

@@ -15,6 +15,8 @@ wtconv_status_t check_desc(const wtconv_ortho_desc_t *d)
     const int64_t lim = ((int64_t)1 << 31) - 1;
     if (d->batch < 1 || d->batch > 65535 || d->rows < 1 || d->cols < 1) return WTCONV_ERR_SHAPE;
     if (d->rows > (1 << 22) || d->cols > (1 << 22) || d->rows * d->cols > lim) return WTCONV_ERR_SHAPE;
+    const int64_t r = d->rows < 64 ? 64 : d->rows, c = d->cols < 64 ? 64 : d->cols;
+    if (d->batch * r * c >= (int64_t)1 << 36) return WTCONV_ERR_SHAPE;
     if (d->rows > WTCONV_ORTHO_MAX_SIDE && d->cols > WTCONV_ORTHO_MAX_SIDE) return WTCONV_ERR_SHAPE;
     if (d->steps < 1 || d->steps > WTCONV_ORTHO_MAX_STEPS) return WTCONV_ERR_SHAPE;
     if (!(d->eps >= 0.f) || !std::isfinite(d->eps)) return WTCONV_ERR_SHAPE;

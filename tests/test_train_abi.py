@@ -88,6 +88,7 @@ BAD_ORTHO = [
     (dict(batch=0), SHAPE), (dict(batch=65536), SHAPE), (dict(rows=0), SHAPE), (dict(cols=-3), SHAPE),
     (dict(rows=1 << 16, cols=1 << 16), SHAPE), (dict(rows=16385, cols=16385), SHAPE), (dict(cols=1 << 62), SHAPE),
     (dict(rows=1, cols=(1 << 22) + 1), SHAPE), (dict(steps=0), SHAPE), (dict(steps=17), SHAPE),
+    (dict(batch=65535, rows=1025, cols=1025), SHAPE), (dict(batch=65535, rows=1, cols=1 << 15), SHAPE),
     (dict(eps=-1e-9), SHAPE), (dict(eps=float("nan")), SHAPE), (dict(eps=float("inf")), SHAPE),
     (dict(dtype=3), UNSUPPORTED), (dict(dtype=-1), UNSUPPORTED),
 ]
