@@ -235,7 +235,7 @@ wtconv_status_t wtconv_unfused_backward_weight(const wtconv_desc_t *desc, const 
  *              statistics and products are fp32 (or wider); an output element
  *              is rounded once.
  * Shape rules  n, c, h, w >= 1, groups >= 1 divides c, c * h * w < 2^31,
- *              n * c < 2^31, eps > 0 and finite.
+ *              n * c < 2^23, eps > 0 and finite.
  * Alignment    activations are aligned to their element; any such address
  *              works, 16-byte aligned ones are faster.
  * Values       a group with a NaN or an infinity comes out as NaN (relu of it

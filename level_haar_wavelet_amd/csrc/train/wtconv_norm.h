@@ -1,4 +1,4 @@
-// wtconv_norm.h -- launch entry points of the group norm kernels.
+// wtconv_norm.h -- plan and launch entry points of the group norm kernels.
 #ifndef WTCONV_NORM_H
 #define WTCONV_NORM_H
 
@@ -6,14 +6,86 @@
 
 #include "../../../include/wtconv.h"
 
+namespace wtc_norm {
+
+constexpr int kThreads = 256;     // a workgroup of the three-launch form
+constexpr int kOneThreads = 512;  // of the one-launch form
+constexpr int kMaxBlock = 512;    // channels of a workgroup
+
+// How a pass over (N, C, H W) is shared out: workgroups of `cb` channels and
+// `ppw` pixels of one image, `blocks` and `splits` of them for each image,
+// `lanes` threads side by side along memory.
+struct Geometry {
+    int c, hw, groups, per, act;
+    int cb, blocks, ppw, splits, lanes;
+    int64_t count;  // workgroups of all images
+};
+
+// (count, mean, sum of squared differences) of a set of values.
+struct Moments {
+    float n, mean, m2;
+};
+
+__device__ inline Moments join(const Moments &a, const Moments &b)
+{
+    const float n = a.n + b.n;
+    if (n == 0.f) return a;
+    const float w = b.n / n, d = b.mean - a.mean;
+    return Moments{n, fmaf(d, w, a.mean), a.m2 + b.m2 + d * d * a.n * w};
+}
+
+// s of all lanes of a wave, joined in a fixed order, on every lane.
+template <typename S, typename J>
+__device__ inline S join_wave(S s, J join2)
+{
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        S q;
+        const float *a = (const float *)&s;
+        float *b = (float *)&q;
+#pragma unroll
+        for (int w = 0; w < (int)(sizeof(S) / 4); ++w) b[w] = __shfl_xor(a[w], o);
+        s = (threadIdx.x & o) ? join2(q, s) : join2(s, q);
+    }
+    return s;
+}
+
+struct Plan {
+    Geometry stats, apply;  // the forward pass's moments; every other pass
+    bool xl, yl, vec, one;
+    float eps;
+    size_t means_at, bytes;  // workspace: partial sums, then the groups' means
+};
+
+// `aligned`: every activation lies on 16 bytes.
+Plan make_plan(const wtconv_norm_desc_t &d, bool bwd, bool aligned);
+
+struct Call {
+    const void *x, *dy;  // dy null: forward
+    const float *gamma, *beta, *mean, *rstd;
+    void *out;  // y or dx
+    float *mean_out, *rstd_out, *dgamma, *dbeta;
+    void *workspace;
+    int64_t n;
+};
+
+template <typename T>
+hipError_t run(const Plan &p, const Call &a, hipStream_t stream);
+
+// mean and rstd of every group from its channels' moments in `part`.
+void launch_finish_forward(const Geometry &g, int64_t n, const float2 *part, float *mean, float *rstd, float eps,
+                           hipStream_t stream);
+
+// From the channels' sums in `part`: every group's means of t and t xh (unless
+// null), and dgamma and dbeta (unless null).
+void launch_finish_backward(const Geometry &g, int64_t n, const float2 *part, const float *gamma, float2 *means,
+                            float *dgamma, float *dbeta, hipStream_t stream);
+
+}  // namespace wtc_norm
+
 // Bytes of workspace of the forward (bwd = 0) or backward call.
 size_t wtc_norm_workspace(const wtconv_norm_desc_t &d, int bwd);
 
-hipError_t wtc_launch_norm_forward(const wtconv_norm_desc_t &d, const void *x, const float *gamma, const float *beta,
-                                   void *y, float *mean, float *rstd, void *workspace, hipStream_t stream);
-
-hipError_t wtc_launch_norm_backward(const wtconv_norm_desc_t &d, const void *x, const void *dy, const float *gamma,
-                                    const float *beta, const float *mean, const float *rstd, void *dx, float *dgamma,
-                                    float *dbeta, void *workspace, hipStream_t stream);
+hipError_t wtc_launch_norm(const wtconv_norm_desc_t &d, const wtc_norm::Call &a, hipStream_t stream);
 
 #endif  // WTCONV_NORM_H

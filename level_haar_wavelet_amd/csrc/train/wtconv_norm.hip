@@ -1,12 +1,5 @@
-// wtconv_norm.hip -- group norm with an activation, forward and backward, for
-// activations as planes or channels last.
-//
-// Forward: mean and variance of every group (n, g) in two passes over the
-// group (the mean first, then the squared differences from it, so nothing
-// cancels), then y = act(gamma (x - mean) rstd + beta), element by element.
-// Backward: per (n, c) the sums of dz = dy act'(z) and of dz xh; per group
-// their gamma-weighted means; per channel dgamma and dbeta, added over n in
-// order; then dx element by element.
+// wtconv_norm.hip -- group norm: the plan of a call, and the small kernels that
+// join the sums of pixel ranges (the walks are in wtconv_norm_body.h).
 #include <hip/hip_fp16.h>
 #include <hip/hip_runtime.h>
 
@@ -15,273 +8,248 @@
 #include "wtconv_check.h"
 #include "wtconv_norm.h"
 
+namespace wtc_norm {
+
 namespace {
 
-constexpr int kThreads = 256;
-
-struct Shape {
-    int c, hw, groups, per;  // per: channels of a group
-    int64_t n;
-    bool xl, yl;  // channels last
-    float eps;
-};
-
-Shape shape_of(const wtconv_norm_desc_t &d)
+// Pixels of range s.
+__device__ inline int pixels(const Geometry &g, int s)
 {
-    return Shape{(int)d.c, (int)(d.h * d.w), d.groups, (int)(d.c / d.groups), d.n, d.x_layout == WTCONV_NHWC,
-                 d.y_layout == WTCONV_NHWC, d.eps};
+    const int p = g.hw - s * g.ppw;
+    return p < g.ppw ? p : g.ppw;
 }
 
-__device__ inline int64_t offset(int64_t n, int c, int p, int C, int HW, bool last)
-{
-    return n * C * (int64_t)HW + (last ? (int64_t)p * C + c : (int64_t)c * HW + p);
-}
-
-template <int ACT>
-__device__ inline float act_fwd(float z)
-{
-    if (ACT == WTCONV_ACT_RELU) return z < 0.f ? 0.f : z;  // NaN stays
-    if (ACT == WTCONV_ACT_SILU) return z / (1.f + __expf(-z));
-    if (ACT == WTCONV_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678f));
-    return z;
-}
-
-// dy act'(z), z = gamma xh + beta, xh = (x - mean) rstd.
-template <int ACT>
-__device__ inline float act_bwd(float dy, float x, float mean, float rstd, float gamma, float beta, float xh)
-{
-    const float z = fmaf(gamma, xh, beta);
-    if (ACT == WTCONV_ACT_RELU) {
-        bool on = z > 0.f;
-        // next to the border the sign is decided in fp64
-        if (fabsf(z) <= 1e-5f * (fabsf(gamma * xh) + fabsf(beta)))
-            on = fma(((double)x - mean) * rstd, (double)gamma, (double)beta) > 0.0;
-        return on ? dy : 0.f;
-    }
-    if (ACT == WTCONV_ACT_SILU) {
-        const float s = 1.f / (1.f + __expf(-z));
-        return dy * s * (1.f + z * (1.f - s));
-    }
-    if (ACT == WTCONV_ACT_GELU)
-        return dy * (0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z));
-    return dy;
-}
-
-// Sum over the block (fixed order); every thread gets it.
-__device__ inline float block_sum(float v, float *lds)
+__device__ inline float wave_sum(float v)
 {
     for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-    const int wave = threadIdx.x >> 6;
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[wave] = v;
-    __syncthreads();
-    float s = 0.f;
-    for (int i = 0; i < kThreads / 64; ++i) s += lds[i];
-    return s;
+    return v;
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void norm_stats(const T *__restrict__ x, Shape s, float *__restrict__ mean,
-                                                       float *__restrict__ rstd)
+// One wave a group.
+__global__ __launch_bounds__(256) void finish_forward(Geometry g, int64_t groups, const float2 *__restrict__ part,
+                                                      float *__restrict__ mean, float *__restrict__ rstd, float eps)
 {
-    __shared__ float lds[kThreads / 64];
-    const int64_t n = blockIdx.x / s.groups;
-    const int g = (int)(blockIdx.x % s.groups);
-    const int k = s.per * s.hw;
-    auto at = [&](int i) {  // the group's values in the order they lie in memory
-        const int c = s.xl ? i % s.per : i / s.hw, p = s.xl ? i / s.per : i % s.hw;
-        return (float)x[offset(n, g * s.per + c, p, s.c, s.hw, s.xl)];
-    };
-    float a = 0.f;
-    for (int i = threadIdx.x; i < k; i += kThreads) a += at(i);
-    const float m = block_sum(a, lds) / (float)k;
-    a = 0.f;
-    for (int i = threadIdx.x; i < k; i += kThreads) {
-        const float d = at(i) - m;
-        a = fmaf(d, d, a);
+    const int64_t ng = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (ng >= groups) return;
+    const int64_t n = ng / g.groups;
+    const int c0 = (int)(ng % g.groups) * g.per, lane = threadIdx.x & 63;
+    const float2 *p = part + n * g.splits * g.c + c0;
+    Moments m = {0.f, 0.f, 0.f};
+    for (int i = lane; i < g.splits * g.per; i += 64) {
+        const int s = i / g.per;
+        const float2 v = p[(int64_t)s * g.c + i % g.per];
+        m = join(m, Moments{(float)pixels(g, s), v.x, v.y});
     }
-    const float var = block_sum(a, lds) / (float)k;
-    if (threadIdx.x == 0) {
-        mean[blockIdx.x] = m;
-        rstd[blockIdx.x] = 1.f / sqrtf(var + s.eps);
+    m = join_wave(m, join);
+    if (lane == 0) {
+        mean[ng] = m.mean;
+        rstd[ng] = 1.f / sqrtf(m.m2 / m.n + eps);
     }
 }
 
-template <typename T, int ACT>
-__global__ __launch_bounds__(kThreads) void norm_apply(const T *__restrict__ x, const float *__restrict__ gamma,
-                                                       const float *__restrict__ beta,
-                                                       const float *__restrict__ mean,
-                                                       const float *__restrict__ rstd, T *__restrict__ y, Shape s)
+// Workgroups 0 .. gblocks - 1: one wave a group, its means of t and t xh.  The
+// others: dgamma and dbeta of 16 channels each, 16 threads a channel.
+__global__ __launch_bounds__(256) void finish_backward(Geometry g, int64_t images, const float2 *__restrict__ part,
+                                                       const float *__restrict__ gamma, int gblocks,
+                                                       float2 *__restrict__ means, float *__restrict__ dgamma,
+                                                       float *__restrict__ dbeta)
 {
-    const int img = s.c * s.hw;
-    for (int64_t b = blockIdx.x;; b += gridDim.x) {
-        const int64_t e = b * kThreads + threadIdx.x;
-        if (b * kThreads >= s.n * img) break;
-        if (e >= s.n * img) continue;
-        const int64_t n = e / img;
-        const int r = (int)(e % img);
-        const int c = s.yl ? r % s.c : r / s.hw, p = s.yl ? r / s.c : r % s.hw;
-        const int64_t ng = n * s.groups + c / s.per;
-        const float xh = ((float)x[offset(n, c, p, s.c, s.hw, s.xl)] - mean[ng]) * rstd[ng];
-        y[e] = (T)act_fwd<ACT>(fmaf(gamma ? gamma[c] : 1.f, xh, beta ? beta[c] : 0.f));
-    }
-}
-
-// Per (n, c): sums over the plane of dz and dz xh.
-template <typename T, int ACT>
-__global__ __launch_bounds__(kThreads) void norm_bwd_sums(const T *__restrict__ x, const T *__restrict__ dy,
-                                                          const float *__restrict__ gamma,
-                                                          const float *__restrict__ beta,
-                                                          const float *__restrict__ mean,
-                                                          const float *__restrict__ rstd, Shape s,
-                                                          float2 *__restrict__ sums)
-{
-    __shared__ float lds[kThreads / 64];
-    const int64_t n = blockIdx.x / s.c;
-    const int c = (int)(blockIdx.x % s.c);
-    const int64_t ng = n * s.groups + c / s.per;
-    const float m = mean[ng], rs = rstd[ng], ga = gamma ? gamma[c] : 1.f, be = beta ? beta[c] : 0.f;
-    float a = 0.f, b = 0.f;
-    for (int p = threadIdx.x; p < s.hw; p += kThreads) {
-        const float xv = (float)x[offset(n, c, p, s.c, s.hw, s.xl)], xh = (xv - m) * rs;
-        const float dz = act_bwd<ACT>((float)dy[offset(n, c, p, s.c, s.hw, s.yl)], xv, m, rs, ga, be, xh);
-        a += dz;
-        b = fmaf(dz, xh, b);
-    }
-    a = block_sum(a, lds);
-    b = block_sum(b, lds);
-    if (threadIdx.x == 0) sums[blockIdx.x] = make_float2(a, b);
-}
-
-// Per (n, g): the means of t and t xh; per c: dbeta and dgamma.
-__global__ __launch_bounds__(kThreads) void norm_bwd_reduce(const float2 *__restrict__ sums,
-                                                            const float *__restrict__ gamma, Shape s,
-                                                            float2 *__restrict__ means, float *__restrict__ dgamma,
-                                                            float *__restrict__ dbeta)
-{
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, ng = s.n * s.groups;
-    if (i < ng) {
-        const int64_t n = i / s.groups;
-        const int g = (int)(i % s.groups);
+    if ((int)blockIdx.x < gblocks) {
+        const int64_t ng = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+        if (ng >= images * g.groups) return;
+        const int64_t n = ng / g.groups;
+        const int c0 = (int)(ng % g.groups) * g.per, lane = threadIdx.x & 63;
+        const float2 *p = part + n * g.splits * g.c + c0;
         float a = 0.f, b = 0.f;
-        for (int c = g * s.per; c < (g + 1) * s.per; ++c) {
-            const float2 v = sums[n * s.c + c];
-            const float ga = gamma ? gamma[c] : 1.f;
+        for (int i = lane; i < g.splits * g.per; i += 64) {
+            const int s = i / g.per, c = i % g.per;
+            const float2 v = p[(int64_t)s * g.c + c];
+            const float ga = gamma ? gamma[c0 + c] : 1.f;
             a = fmaf(ga, v.x, a);
             b = fmaf(ga, v.y, b);
         }
-        const float k = (float)s.per * (float)s.hw;
-        means[i] = make_float2(a / k, b / k);
-    } else if (i - ng < s.c) {
-        const int c = (int)(i - ng);
-        float a = 0.f, b = 0.f;
-        for (int64_t n = 0; n < s.n; ++n) {
-            const float2 v = sums[n * s.c + c];
+        a = wave_sum(a);
+        b = wave_sum(b);
+        const float k = (float)g.per * (float)g.hw;
+        if (lane == 0) means[ng] = make_float2(a / k, b / k);
+        return;
+    }
+    __shared__ float2 lds[16][17];
+    const int j = threadIdx.x & 15, r = threadIdx.x >> 4, c = ((int)blockIdx.x - gblocks) * 16 + j;
+    float a = 0.f, b = 0.f;
+    if (c < g.c)
+#pragma unroll 4
+        for (int64_t i = r; i < images * g.splits; i += 16) {
+            const float2 v = part[i * g.c + c];
             a += v.x;
             b += v.y;
+        }
+    lds[r][j] = make_float2(a, b);
+    __syncthreads();
+    if (r == 0 && c < g.c) {
+        for (int i = 1; i < 16; ++i) {
+            a += lds[i][j].x;
+            b += lds[i][j].y;
         }
         if (dbeta) dbeta[c] = a;
         if (dgamma) dgamma[c] = b;
     }
 }
 
-template <typename T, int ACT>
-__global__ __launch_bounds__(kThreads) void norm_bwd_apply(const T *__restrict__ x, const T *__restrict__ dy,
-                                                           const float *__restrict__ gamma,
-                                                           const float *__restrict__ beta,
-                                                           const float *__restrict__ mean,
-                                                           const float *__restrict__ rstd,
-                                                           const float2 *__restrict__ means, T *__restrict__ dx,
-                                                           Shape s)
-{
-    const int img = s.c * s.hw;
-    for (int64_t b = blockIdx.x;; b += gridDim.x) {
-        const int64_t e = b * kThreads + threadIdx.x;
-        if (b * kThreads >= s.n * img) break;
-        if (e >= s.n * img) continue;
-        const int64_t n = e / img;
-        const int r = (int)(e % img);
-        const int c = s.xl ? r % s.c : r / s.hw, p = s.xl ? r / s.c : r % s.hw;
-        const int64_t ng = n * s.groups + c / s.per;
-        const float m = mean[ng], rs = rstd[ng], ga = gamma ? gamma[c] : 1.f, be = beta ? beta[c] : 0.f;
-        const float xv = (float)x[e], xh = (xv - m) * rs;
-        const float dz = act_bwd<ACT>((float)dy[offset(n, c, p, s.c, s.hw, s.yl)], xv, m, rs, ga, be, xh);
-        const float2 q = means[ng];
-        dx[e] = (T)(rs * (ga * dz - q.x - xh * q.y));
-    }
-}
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-unsigned elem_blocks(const Shape &s)
+// Threads side by side along rows of `chunks` pieces such that the fewest of nt
+// threads idle, at least eight of them (128 bytes) where there are as many.
+int pick_lanes(int chunks, int nt, int most)
 {
-    const int64_t b = (s.n * s.c * s.hw + kThreads - 1) / kThreads;
-    return (unsigned)(b < 65536 ? b : 65536);
-}
-
-template <typename T, int ACT>
-hipError_t forward(const Shape &s, const void *x, const float *gamma, const float *beta, void *y, float *mean,
-                   float *rstd, hipStream_t stream)
-{
-    norm_stats<T><<<dim3((unsigned)(s.n * s.groups)), dim3(kThreads), 0, stream>>>((const T *)x, s, mean, rstd);
-    norm_apply<T, ACT>
-        <<<dim3(elem_blocks(s)), dim3(kThreads), 0, stream>>>((const T *)x, gamma, beta, mean, rstd, (T *)y, s);
-    return hipGetLastError();
-}
-
-template <typename T, int ACT>
-hipError_t backward(const Shape &s, const void *x, const void *dy, const float *gamma, const float *beta,
-                    const float *mean, const float *rstd, void *dx, float *dgamma, float *dbeta, void *workspace,
-                    hipStream_t stream)
-{
-    float2 *sums = (float2 *)workspace;
-    float2 *means = (float2 *)((char *)workspace + align256((size_t)s.n * s.c * sizeof(float2)));
-    norm_bwd_sums<T, ACT><<<dim3((unsigned)(s.n * s.c)), dim3(kThreads), 0, stream>>>(
-        (const T *)x, (const T *)dy, gamma, beta, mean, rstd, s, sums);
-    norm_bwd_reduce<<<dim3((unsigned)((s.n * s.groups + s.c + kThreads - 1) / kThreads)), dim3(kThreads), 0,
-                      stream>>>(sums, gamma, s, means, dgamma, dbeta);
-    norm_bwd_apply<T, ACT><<<dim3(elem_blocks(s)), dim3(kThreads), 0, stream>>>(
-        (const T *)x, (const T *)dy, gamma, beta, mean, rstd, means, (T *)dx, s);
-    return hipGetLastError();
-}
-
-// Calls f with a value of the element type and the activation as a constant.
-template <typename F>
-hipError_t dispatch(const wtconv_norm_desc_t &d, F f)
-{
-    auto with = [&](auto t) {
-        switch (d.act) {
-        case WTCONV_ACT_RELU: return f(t, std::integral_constant<int, WTCONV_ACT_RELU>());
-        case WTCONV_ACT_SILU: return f(t, std::integral_constant<int, WTCONV_ACT_SILU>());
-        case WTCONV_ACT_GELU: return f(t, std::integral_constant<int, WTCONV_ACT_GELU>());
-        default: return f(t, std::integral_constant<int, WTCONV_ACT_NONE>());
+    const int hi = chunks < most ? chunks : most, lo = hi < 8 ? hi : 8;
+    int best = hi;
+    double value = 0.;
+    for (int l = hi; l >= lo; --l) {
+        const double used = (double)chunks / (double)(ceil_div(chunks, l) * l) * (double)(nt / l * l) / nt;
+        if (used > value * 1.02) {
+            value = used;
+            best = l;
         }
-    };
-    if (d.dtype == WTCONV_F32) return with(float());
-    if (d.dtype == WTCONV_F16) return with(_Float16());
-    return with(__bf16());
+    }
+    return best;
+}
+
+// Least common multiple of per and v (a power of two).
+int lcm_pow2(int per, int v)
+{
+    int g = 1;
+    while (g < v && per % (2 * g) == 0) g *= 2;
+    return per / g * v;
+}
+
+enum Walk { kPlanes, kLast, kTiles };
+
+constexpr int kTargetBytes = 32768;  // of one tensor, a workgroup of the three-launch form
+constexpr int kTargetCount = 2048;   // workgroups that fill the chip
+
+// Whole groups of an image for each workgroup: cb channels, all pixels.
+Geometry one_geometry(Geometry g, int64_t n, Walk w, bool tiles, int v, int v16, int unit)
+{
+    const int nt = kOneThreads;
+    g.splits = 1;
+    g.ppw = g.hw;
+    g.cb = unit;
+    // channels last: rows of at least 64 bytes where the workgroups suffice;
+    // tiles: their whole width
+    const int wide = tiles ? 8 * v16 : w == kLast ? 4 * v16 : 1;
+    while (g.cb * 2 <= kMaxBlock && g.cb < wide && g.cb < g.c && n * ceil_div(g.c, 2 * g.cb) >= 256) g.cb *= 2;
+    if (g.cb > g.c) g.cb = g.c;
+    g.blocks = (int)ceil_div(g.c, g.cb);
+    g.lanes = w == kLast ? pick_lanes(g.cb / v, nt, 64) : pick_lanes((int)ceil_div(g.hw, v), nt, nt);
+    g.count = n * g.blocks;
+    return g;
+}
+
+Geometry split_geometry(Geometry g, int64_t n, Walk w, int v, int esize)
+{
+    int step;  // pixels that a workgroup takes at least
+    if (w == kLast) {
+        const int chunks = g.c / v, most = kMaxBlock / v;
+        const int blocks = (int)ceil_div(chunks, most);
+        g.cb = (int)ceil_div(chunks, blocks) * v;
+        g.lanes = pick_lanes(g.cb / v, kThreads, 64);
+        step = kThreads / g.lanes;
+    } else if (w == kTiles) {
+        step = 128 / esize;
+        g.cb = g.c < step ? g.c : step;
+        g.lanes = 1;
+    } else {
+        g.lanes = pick_lanes((int)ceil_div(g.hw, v), kThreads, kThreads);
+        const int rows = kThreads / g.lanes;
+        int64_t cb = kTargetBytes / ((int64_t)g.hw * esize) / rows * rows;
+        if (cb < rows) cb = rows;
+        if (cb > kMaxBlock / rows * rows) cb = kMaxBlock / rows * rows;
+        g.cb = (int)(cb < g.c ? cb : g.c);
+        step = g.lanes * v;
+    }
+    g.blocks = (int)ceil_div(g.c, g.cb);
+    int64_t ppw = kTargetBytes / ((int64_t)g.cb * esize);
+    const int64_t all = n * g.blocks;
+    if (all * ceil_div(g.hw, ppw < 1 ? 1 : ppw) < kTargetCount) ppw = ceil_div(g.hw, ceil_div(kTargetCount, all));
+    ppw = ceil_div(ppw < 1 ? 1 : ppw, step) * step;
+    g.ppw = (int)(ppw < g.hw ? ppw : ceil_div(g.hw, step) * step);
+    g.splits = (int)ceil_div(g.hw, g.ppw);
+    g.count = all * g.splits;
+    return g;
 }
 
 }  // namespace
 
+Plan make_plan(const wtconv_norm_desc_t &d, bool bwd, bool aligned)
+{
+    Plan p = {};
+    p.xl = d.x_layout == WTCONV_NHWC;
+    p.yl = d.y_layout == WTCONV_NHWC;
+    p.eps = d.eps;
+    const int esize = d.dtype == WTCONV_F32 ? 4 : 2, v16 = 16 / esize;
+    Geometry g = {};
+    g.c = (int)d.c;
+    g.hw = (int)(d.h * d.w);
+    g.groups = d.groups;
+    g.per = g.c / g.groups;
+    g.act = d.act;
+    const Walk sw = p.xl ? kLast : kPlanes, aw = p.xl != p.yl ? kTiles : sw;
+    p.vec = aligned && (!(p.xl || p.yl) || g.c % v16 == 0) && ((p.xl && p.yl) || g.hw % v16 == 0);
+    const int v = p.vec ? v16 : 1;
+
+    // one launch where whole groups make enough workgroups, or where the data
+    // are so few that a launch costs more than the pass
+    const int unit = p.xl || p.yl ? lcm_pow2(g.per, v) : g.per;
+    const int64_t bytes = d.n * d.c * (int64_t)g.hw * esize * (bwd ? 2 : 1);
+    if (unit <= kMaxBlock) {
+        const Geometry s = one_geometry(g, d.n, sw, aw == kTiles, v, v16, unit);
+        if (s.count >= 256 || bytes <= 1 << 20) {
+            p.one = true;
+            p.stats = s;
+            p.apply = s;
+            if (aw == kTiles) p.apply.lanes = 1;
+            p.bytes = bwd ? align256((size_t)(d.n * d.c) * sizeof(float2)) : 0;
+            return p;
+        }
+    }
+    p.stats = split_geometry(g, d.n, sw, v, esize);
+    p.apply = split_geometry(g, d.n, aw, v, esize);
+    const Geometry &q = bwd ? p.apply : p.stats;
+    p.means_at = align256((size_t)(d.n * q.splits) * d.c * sizeof(float2));
+    p.bytes = p.means_at + (bwd ? align256((size_t)(d.n * d.groups) * sizeof(float2)) : 0);
+    return p;
+}
+
+void launch_finish_forward(const Geometry &g, int64_t n, const float2 *part, float *mean, float *rstd, float eps,
+                           hipStream_t stream)
+{
+    const int64_t groups = n * g.groups;
+    finish_forward<<<dim3((unsigned)ceil_div(groups, 4)), dim3(256), 0, stream>>>(g, groups, part, mean, rstd, eps);
+}
+
+void launch_finish_backward(const Geometry &g, int64_t n, const float2 *part, const float *gamma, float2 *means,
+                            float *dgamma, float *dbeta, hipStream_t stream)
+{
+    const int64_t gb = means ? ceil_div(n * g.groups, 4) : 0, cb = dgamma || dbeta ? ceil_div(g.c, 16) : 0;
+    finish_backward<<<dim3((unsigned)(gb + cb)), dim3(256), 0, stream>>>(g, n, part, gamma, (int)gb, means, dgamma,
+                                                                         dbeta);
+}
+
+}  // namespace wtc_norm
+
 size_t wtc_norm_workspace(const wtconv_norm_desc_t &d, int bwd)
 {
-    if (!bwd) return 0;
-    return align256((size_t)(d.n * d.c) * sizeof(float2)) + align256((size_t)(d.n * d.groups) * sizeof(float2));
+    // the plan of unaligned activations may take more
+    const size_t a = wtc_norm::make_plan(d, bwd != 0, true).bytes, b = wtc_norm::make_plan(d, bwd != 0, false).bytes;
+    return a > b ? a : b;
 }
 
-hipError_t wtc_launch_norm_forward(const wtconv_norm_desc_t &d, const void *x, const float *gamma, const float *beta,
-                                   void *y, float *mean, float *rstd, void *, hipStream_t stream)
+hipError_t wtc_launch_norm(const wtconv_norm_desc_t &d, const wtc_norm::Call &a, hipStream_t stream)
 {
-    return dispatch(d, [&](auto t, auto act) {
-        return forward<decltype(t), decltype(act)::value>(shape_of(d), x, gamma, beta, y, mean, rstd, stream);
-    });
-}
-
-hipError_t wtc_launch_norm_backward(const wtconv_norm_desc_t &d, const void *x, const void *dy, const float *gamma,
-                                    const float *beta, const float *mean, const float *rstd, void *dx, float *dgamma,
-                                    float *dbeta, void *workspace, hipStream_t stream)
-{
-    return dispatch(d, [&](auto t, auto act) {
-        return backward<decltype(t), decltype(act)::value>(shape_of(d), x, dy, gamma, beta, mean, rstd, dx, dgamma,
-                                                           dbeta, workspace, stream);
-    });
+    const bool aligned = aligned16(a.x) && aligned16(a.out) && (!a.dy || aligned16(a.dy));
+    const wtc_norm::Plan p = wtc_norm::make_plan(d, a.dy != nullptr, aligned);
+    if (d.dtype == WTCONV_F32) return wtc_norm::run<float>(p, a, stream);
+    if (d.dtype == WTCONV_F16) return wtc_norm::run<_Float16>(p, a, stream);
+    return wtc_norm::run<__bf16>(p, a, stream);
 }

@@ -16,7 +16,7 @@ wtconv_status_t check_desc(const wtconv_norm_desc_t *d)
     if (d->n < 1 || d->c < 1 || d->h < 1 || d->w < 1 || d->groups < 1) return WTCONV_ERR_SHAPE;
     if (d->n > lim || d->c > lim || d->h > lim || d->w > lim) return WTCONV_ERR_SHAPE;
     if (d->c % d->groups) return WTCONV_ERR_SHAPE;
-    if (d->h * d->w > lim || d->h * d->w > lim / d->c || d->n > lim / d->c) return WTCONV_ERR_SHAPE;
+    if (d->h * d->w > lim || d->h * d->w > lim / d->c || d->n * d->c >= 1 << 23) return WTCONV_ERR_SHAPE;
     if (!(d->eps > 0.f) || !std::isfinite(d->eps)) return WTCONV_ERR_SHAPE;
     if (d->dtype != WTCONV_F32 && d->dtype != WTCONV_F16 && d->dtype != WTCONV_BF16) return WTCONV_ERR_UNSUPPORTED;
     if (d->act < WTCONV_ACT_NONE || d->act > WTCONV_ACT_GELU) return WTCONV_ERR_UNSUPPORTED;
@@ -86,9 +86,16 @@ extern "C" wtconv_status_t wtconv_group_norm_forward(const wtconv_norm_desc_t *d
     const Span out[] = {{y, ab}, {mean, sb}, {rstd, sb}, {workspace, need}};
     if (any_alias(in, 3, out, 4)) return WTCONV_ERR_ALIAS;
     if ((st = check_workspace(workspace, workspace_bytes, need)) != WTCONV_OK) return st;
-    return wtc_launch_norm_forward(*desc, x, gamma, beta, y, mean, rstd, workspace, (hipStream_t)stream) == hipSuccess
-               ? WTCONV_OK
-               : WTCONV_ERR_HIP;
+    wtc_norm::Call a = {};
+    a.x = x;
+    a.gamma = gamma;
+    a.beta = beta;
+    a.out = y;
+    a.mean_out = mean;
+    a.rstd_out = rstd;
+    a.workspace = workspace;
+    a.n = desc->n;
+    return wtc_launch_norm(*desc, a, (hipStream_t)stream) == hipSuccess ? WTCONV_OK : WTCONV_ERR_HIP;
 }
 
 extern "C" wtconv_status_t wtconv_group_norm_backward(const wtconv_norm_desc_t *desc, const void *x, const void *dy,
@@ -110,8 +117,6 @@ extern "C" wtconv_status_t wtconv_group_norm_backward(const wtconv_norm_desc_t *
     const Span out[] = {{dx, ab}, {dgamma, cb}, {dbeta, cb}, {workspace, need}};
     if (any_alias(in, 6, out, 4)) return WTCONV_ERR_ALIAS;
     if ((st = check_workspace(workspace, workspace_bytes, need)) != WTCONV_OK) return st;
-    return wtc_launch_norm_backward(*desc, x, dy, gamma, beta, mean, rstd, dx, dgamma, dbeta, workspace,
-                                    (hipStream_t)stream) == hipSuccess
-               ? WTCONV_OK
-               : WTCONV_ERR_HIP;
+    const wtc_norm::Call a = {x, dy, gamma, beta, mean, rstd, dx, nullptr, nullptr, dgamma, dbeta, workspace, desc->n};
+    return wtc_launch_norm(*desc, a, (hipStream_t)stream) == hipSuccess ? WTCONV_OK : WTCONV_ERR_HIP;
 }

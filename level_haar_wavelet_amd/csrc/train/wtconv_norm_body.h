@@ -1,0 +1,709 @@
+// wtconv_norm_body.h -- the group norm kernels of one element type; the files
+// wtconv_norm_f32.hip, _f16.hip and _bf16.hip instantiate them.
+//
+// A group's mean and variance, and the backward pass's two means, are needed
+// before the first output, so the data are walked twice: 3 E e bytes forward
+// and 5 E e backward where nothing is kept between, against a floor of 2 E e
+// and 3 E e.  Two forms:
+//   one launch   a workgroup owns whole groups of an image, walks them twice and
+//                finds the second time in the caches what it read the first;
+//   three        for images too large or too few for that: sums of pixel ranges
+//                per channel, a small kernel that joins them, and the
+//                elementwise pass.
+//
+// Walks.  An image lies in memory as rows of contiguous elements: its channels'
+// planes, or its pixels' channels.  A thread takes V contiguous elements (16
+// bytes, or one where sizes or addresses do not allow that), `lanes` threads stand
+// side by side along a row and the rest take rows below, so that every thread
+// keeps its channel (planes) or its V channels (last) and their constants in
+// registers.  Where the two tensors of a pass lie differently the walk is along
+// planes, in tiles of 8 V pixels x 8 V channels, and the tensor that lies
+// channels last goes through LDS: 128 bytes a pixel in 8 chunks of 16, chunk j
+// of pixel p at place j ^ (p / V) % 8, which spreads the column reads over the
+// banks.
+//
+// Numerics.  Values are fp32 from the load on.  A thread sums x - s and
+// (x - s)^2 with s the first value it meets: since s is one of the values, the
+// sum of squares it yields cannot cancel by more than their number.  Threads'
+// (count, mean, M2) are joined by Chan's formula, in fixed order.
+#ifndef WTCONV_NORM_BODY_H
+#define WTCONV_NORM_BODY_H
+
+#include <hip/hip_fp16.h>
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "wtconv_norm.h"
+
+namespace wtc_norm {
+
+template <typename T, int V>
+struct Pack {
+    typedef T type __attribute__((ext_vector_type(V)));
+};
+template <typename T>
+struct Pack<T, 1> {
+    typedef T type;
+};
+
+template <typename T, int V>
+__device__ inline void load(const T *p, float (&v)[V])
+{
+    const typename Pack<T, V>::type r = *(const typename Pack<T, V>::type *)p;
+    if constexpr (V == 1)
+        v[0] = (float)r;
+    else
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = (float)r[i];
+}
+
+template <typename T, int V>
+__device__ inline void store(T *p, const float (&v)[V])
+{
+    typename Pack<T, V>::type r;
+    if constexpr (V == 1)
+        r = (T)v[0];
+    else
+#pragma unroll
+        for (int i = 0; i < V; ++i) r[i] = (T)v[i];
+    *(typename Pack<T, V>::type *)p = r;
+}
+
+// act(z), in place.
+template <int V>
+__device__ inline void act_fwd(int act, float (&z)[V])
+{
+    if (act == WTCONV_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = z[i] / (1.f + __expf(-z[i]));
+    } else if (act == WTCONV_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = 0.5f * z[i] * (1.f + erff(z[i] * 0.70710678f));
+    } else if (act == WTCONV_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = z[i] < 0.f ? 0.f : z[i];  // NaN stays
+    }
+}
+
+// Constants of a channel.
+struct Chan {
+    float mean, rstd, gamma, beta;
+};
+
+// dy act'(z), z = gamma xh + beta, xh = (x - mean) rstd.
+__device__ inline float act_bwd(int act, float dy, float x, float xh, const Chan &k)
+{
+    const float z = fmaf(k.gamma, xh, k.beta);
+    if (act == WTCONV_ACT_SILU) {
+        const float s = 1.f / (1.f + __expf(-z));
+        return dy * s * (1.f + z * (1.f - s));
+    }
+    if (act == WTCONV_ACT_GELU)
+        return dy * (0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z));
+    if (act == WTCONV_ACT_RELU) {
+        bool on = z > 0.f;
+        // next to the border the sign is decided in fp64
+        if (fabsf(z) <= 1e-5f * (fabsf(k.gamma * xh) + fabsf(k.beta)))
+            on = fma(((double)x - k.mean) * k.rstd, (double)k.gamma, (double)k.beta) > 0.0;
+        return on ? dy : 0.f;
+    }
+    return dy;
+}
+
+// What a workgroup walks: `cb` channels from c0 and pixels p0 .. p1 of image n.
+struct Range {
+    int64_t n;
+    int c0, cb, p0, p1;
+};
+
+__device__ inline Range range_of(const Geometry &g, int id)
+{
+    const int64_t u = id / g.splits;
+    const int s = id % g.splits, b = (int)(u % g.blocks);
+    Range r;
+    r.n = u / g.blocks;
+    r.c0 = b * g.cb;
+    r.cb = g.c - r.c0 < g.cb ? g.c - r.c0 : g.cb;
+    r.p0 = s * g.ppw;
+    r.p1 = g.hw - r.p0 < g.ppw ? g.hw : r.p0 + g.ppw;
+    return r;
+}
+
+// Calls f(c, offset) for every V elements of the range that this thread takes;
+// begin(c) before and end(c) after those of one channel (planes) or V channels
+// from c on (last).  Every thread of the workgroup makes the same number of
+// begin and end calls; those without a channel of the range get c < 0.
+template <bool LAST, int V, int NT, typename B, typename F, typename E>
+__device__ inline void walk(const Geometry &g, const Range &r, B begin, F f, E end)
+{
+    const int row = threadIdx.x / g.lanes, rows = NT / g.lanes, i = (threadIdx.x - row * g.lanes) * V;
+    if (LAST) {
+        const int64_t base = r.n * g.hw * (int64_t)g.c;
+        for (int cc = 0; cc < r.cb; cc += V * g.lanes) {
+            const int c = row < rows && cc + i < r.cb ? r.c0 + cc + i : -1;
+            begin(c);
+            if (c >= 0)
+#pragma unroll 4
+                for (int p = r.p0 + row; p < r.p1; p += rows) f(c, base + (int64_t)p * g.c + c);
+            end(c);
+        }
+    } else {
+        const int64_t base = r.n * g.c * (int64_t)g.hw;
+        for (int cc = 0; cc < r.cb; cc += rows) {
+            const int c = row < rows && cc + row < r.cb ? r.c0 + cc + row : -1;
+            begin(c);
+            if (c >= 0)
+#pragma unroll 4
+                for (int p = r.p0 + i; p < r.p1; p += V * g.lanes) f(c, base + (int64_t)c * g.hw + p);
+            end(c);
+        }
+    }
+}
+
+// Joins the K values of every thread over the threads that share its channel
+// (those below it for channels last, its row for planes) by a tree in LDS, and
+// calls done(c + k, value) on one thread of each channel.  lds: K NT values.
+template <bool LAST, int K, int NT, typename S, typename J, typename D>
+__device__ inline void join_threads(const Geometry &g, int c, const S (&v)[K], S *lds, J join2, D done)
+{
+    const int t = threadIdx.x, row = t / g.lanes, rows = NT / g.lanes, i = t - row * g.lanes;
+    const int q = LAST ? row : i, stride = LAST ? g.lanes : 1;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) lds[k * NT + t] = v[k];
+    __syncthreads();
+    for (int h = LAST ? rows : g.lanes; h > 1;) {
+        const int half = (h + 1) / 2;
+        if (row < rows && q < h - half)
+#pragma unroll
+            for (int k = 0; k < K; ++k) lds[k * NT + t] = join2(lds[k * NT + t], lds[k * NT + t + half * stride]);
+        __syncthreads();
+        h = half;
+    }
+    if (c >= 0 && q == 0)
+#pragma unroll
+        for (int k = 0; k < K; ++k) done(c + k, lds[k * NT + t]);
+}
+
+// Moments of every channel of the range: done(c, moments).
+template <typename T, bool LAST, int V, int NT, typename D>
+__device__ inline void moments(const T *__restrict__ x, const Geometry &g, const Range &r, Moments *lds,
+                               D done)
+{
+    constexpr int K = LAST ? V : 1;
+    float s[K], a[K], b[K], n;
+    walk<LAST, V, NT>(
+        g, r,
+        [&](int) {
+            n = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) s[k] = a[k] = b[k] = 0.f;
+        },
+        [&](int, int64_t at) {
+            float v[V];
+            load<T, V>(x + at, v);
+            if (n == 0.f)
+#pragma unroll
+                for (int k = 0; k < K; ++k) s[k] = v[k];
+            n += V / K;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int k = LAST ? i : 0;
+                const float d = v[i] - s[k];
+                a[k] += d;
+                b[k] = fmaf(d, d, b[k]);
+            }
+        },
+        [&](int c) {
+            Moments m[K];
+            const float w = n > 0.f ? 1.f / n : 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                m[k] = Moments{n, fmaf(a[k], w, s[k]), fmaf(-a[k] * w, a[k], b[k])};
+                // rounding only: a sum of squares is not negative (NaN stays)
+                if (m[k].m2 < 0.f) m[k].m2 = 0.f;
+            }
+            join_threads<LAST, K, NT>(g, c, m, lds, join, done);
+        });
+}
+
+// ---- Tiles of differing layouts -----------------------------------------------
+
+// LDS place of channel j of pixel p of a tile.
+template <typename T, int V16>
+__device__ inline T *tile_at(char *tile, int p, int j)
+{
+    return (T *)(tile + p * 128 + (((j / V16) ^ ((p / V16) & 7)) * 16)) + j % V16;
+}
+
+// Brings the tile (pixels p0.., channels c0..) of a channels-last tensor into
+// LDS, or back out of it.
+template <typename T, int V, int NT, bool OUT>
+__device__ inline void move_tile(T *t_, const Geometry &g, const Range &r, int p0, int c0, char *tile)
+{
+    constexpr int V16 = 16 / sizeof(T), kSide = 8 * V16, kChunks = kSide / V;
+    for (int e = threadIdx.x; e < kSide * kChunks; e += NT) {
+        const int p = e / kChunks, j = e % kChunks * V;
+        if (p0 + p >= r.p1 || c0 + j >= r.c0 + r.cb) continue;
+        T *m = t_ + (r.n * g.hw + p0 + p) * (int64_t)g.c + c0 + j;
+        typedef typename Pack<T, V>::type P;
+        if (OUT)
+            *(P *)m = *(const P *)tile_at<T, V16>(tile, p, j);
+        else
+            *(P *)tile_at<T, V16>(tile, p, j) = *(const P *)m;
+    }
+}
+
+// Calls f(c, p, q, offset) for the V pixels from p on of channel c in the order
+// of planes, p's place in the tile being q; before(p0, c0) and after(p0, c0)
+// around every tile.
+template <typename T, int V, int NT, typename A, typename F, typename E>
+__device__ inline void walk_tiles(const Geometry &g, const Range &r, A before, F f, E after)
+{
+    constexpr int V16 = 16 / sizeof(T), kSide = 8 * V16, kChunks = kSide / V;
+    for (int c0 = r.c0; c0 < r.c0 + r.cb; c0 += kSide)
+        for (int p0 = r.p0; p0 < r.p1; p0 += kSide) {
+            before(p0, c0);
+            for (int e = threadIdx.x; e < kSide * kChunks; e += NT) {
+                const int c = e / kChunks, q = e % kChunks * V;
+                if (c0 + c < r.c0 + r.cb && p0 + q < r.p1)
+                    f(c0 + c, c, q, (r.n * g.c + c0 + c) * (int64_t)g.hw + p0 + q);
+            }
+            after(p0, c0);
+        }
+}
+
+// ---- The passes of a range -------------------------------------------------------
+
+// y of the range.
+template <typename T, int V, int NT, bool XL, bool YL>
+__device__ inline void apply(const T *__restrict__ x, T *__restrict__ y, const Geometry &g, const Range &r,
+                             const Chan *lk, char *tile)
+{
+    if constexpr (XL == YL) {
+        constexpr int K = XL ? V : 1;
+        Chan k[K];
+        walk<XL, V, NT>(
+            g, r,
+            [&](int c) {
+                if (c >= 0)
+#pragma unroll
+                    for (int i = 0; i < K; ++i) {
+                        k[i] = lk[c + i - r.c0];
+                        k[i].rstd *= k[i].gamma;
+                    }
+            },
+            [&](int, int64_t at) {
+                float v[V];
+                load<T, V>(x + at, v);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const Chan &q = k[XL ? i : 0];
+                    v[i] = fmaf(v[i] - q.mean, q.rstd, q.beta);
+                }
+                act_fwd<V>(g.act, v);
+                store<T, V>(y + at, v);
+            },
+            [](int) {});
+    } else {
+        constexpr int V16 = 16 / sizeof(T);
+        walk_tiles<T, V, NT>(
+            g, r,
+            [&](int p0, int c0) {
+                if (!XL) return;
+                __syncthreads();
+                move_tile<T, V, NT, false>(const_cast<T *>(x), g, r, p0, c0, tile);
+                __syncthreads();
+            },
+            [&](int c, int j, int q, int64_t at) {
+                float v[V];
+                if (XL)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[i] = (float)*tile_at<T, V16>(tile, q + i, j);
+                else
+                    load<T, V>(x + at, v);
+                const Chan k = lk[c - r.c0];
+                const float a = k.rstd * k.gamma;
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = fmaf(v[i] - k.mean, a, k.beta);
+                act_fwd<V>(g.act, v);
+                if (XL)
+                    store<T, V>(y + at, v);
+                else
+#pragma unroll
+                    for (int i = 0; i < V; ++i) *tile_at<T, V16>(tile, q + i, j) = (T)v[i];
+            },
+            [&](int p0, int c0) {
+                if (XL) return;
+                __syncthreads();
+                move_tile<T, V, NT, true>(y, g, r, p0, c0, tile);
+                __syncthreads();
+            });
+    }
+}
+
+// Sums of dz and dz xh of the range's channels: done(c, sums).  sums: LDS of a
+// channel's sums (tiles).
+template <typename T, int V, int NT, bool XL, bool YL, typename D>
+__device__ inline void sums_bwd(const T *__restrict__ x, const T *__restrict__ dy, const Geometry &g, const Range &r,
+                                const Chan *lk, float2 *lds, char *tile, D done)
+{
+    auto add = [](const float2 &a, const float2 &b) { return make_float2(a.x + b.x, a.y + b.y); };
+    if constexpr (XL == YL) {
+        constexpr int K = XL ? V : 1;
+        Chan k[K];
+        float2 s[K];
+        walk<XL, V, NT>(
+            g, r,
+            [&](int c) {
+#pragma unroll
+                for (int i = 0; i < K; ++i) {
+                    s[i] = make_float2(0.f, 0.f);
+                    if (c >= 0) k[i] = lk[c + i - r.c0];
+                }
+            },
+            [&](int, int64_t at) {
+                float v[V], d[V];
+                load<T, V>(x + at, v);
+                load<T, V>(dy + at, d);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int q = XL ? i : 0;
+                    const float xh = (v[i] - k[q].mean) * k[q].rstd;
+                    const float dz = act_bwd(g.act, d[i], v[i], xh, k[q]);
+                    s[q].x += dz;
+                    s[q].y = fmaf(dz, xh, s[q].y);
+                }
+            },
+            [&](int c) { join_threads<XL, K, NT>(g, c, s, lds, add, done); });
+    } else {
+        // 8 V16 / V threads side by side share a channel of the tile; a thread's
+        // places e, e + NT, .. are kSide * kChunks / NT channels
+        constexpr int V16 = 16 / sizeof(T), kSide = 8 * V16, kChunks = kSide / V;
+        constexpr int kOwn = (kSide * kChunks + NT - 1) / NT;
+        static_assert(kChunks <= 64 && NT % kChunks == 0, "a channel's threads are lanes of one wave");
+        for (int c0 = r.c0; c0 < r.c0 + r.cb; c0 += kSide) {
+            float2 s[kOwn];
+#pragma unroll
+            for (int o = 0; o < kOwn; ++o) s[o] = make_float2(0.f, 0.f);
+            for (int p0 = r.p0; p0 < r.p1; p0 += kSide) {
+                __syncthreads();
+                move_tile<T, V, NT, false>(const_cast<T *>(XL ? x : dy), g, r, p0, c0, tile);
+                __syncthreads();
+#pragma unroll
+                for (int o = 0; o < kOwn; ++o) {
+                    const int e = threadIdx.x + o * NT, j = e / kChunks, q = e % kChunks * V;
+                    if (e >= kSide * kChunks || c0 + j >= r.c0 + r.cb || p0 + q >= r.p1) continue;
+                    const int64_t at = (r.n * g.c + c0 + j) * (int64_t)g.hw + p0 + q;
+                    float v[V];
+                    load<T, V>((XL ? dy : x) + at, v);
+                    const Chan k = lk[c0 + j - r.c0];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float u = (float)*tile_at<T, V16>(tile, q + i, j);
+                        const float xv = XL ? u : v[i], xh = (xv - k.mean) * k.rstd;
+                        const float dz = act_bwd(g.act, XL ? v[i] : u, xv, xh, k);
+                        s[o].x += dz;
+                        s[o].y = fmaf(dz, xh, s[o].y);
+                    }
+                }
+            }
+#pragma unroll
+            for (int o = 0; o < kOwn; ++o) {
+                for (int k = 1; k < kChunks; k <<= 1) {
+                    s[o].x += __shfl_xor(s[o].x, k);
+                    s[o].y += __shfl_xor(s[o].y, k);
+                }
+                const int e = threadIdx.x + o * NT, j = e / kChunks;
+                if (e % kChunks == 0 && e < kSide * kChunks && c0 + j < r.c0 + r.cb) done(c0 + j, s[o]);
+            }
+        }
+    }
+}
+
+// dx of the range; q: the group's means of t and t xh, by channel.
+template <typename T, int V, int NT, bool XL, bool YL>
+__device__ inline void apply_bwd(const T *__restrict__ x, const T *__restrict__ dy, T *__restrict__ dx,
+                                 const Geometry &g, const Range &r, const Chan *lk, const float2 *lq,
+                                 char *tile)
+{
+    auto value = [&](float xv, float d, const Chan &k, const float2 &q) {
+        const float xh = (xv - k.mean) * k.rstd;
+        const float dz = act_bwd(g.act, d, xv, xh, k);
+        return k.rstd * (fmaf(k.gamma, dz, -q.x) - xh * q.y);
+    };
+    if constexpr (XL == YL) {
+        constexpr int K = XL ? V : 1;
+        Chan k[K];
+        float2 q[K];
+        walk<XL, V, NT>(
+            g, r,
+            [&](int c) {
+                if (c >= 0)
+#pragma unroll
+                    for (int i = 0; i < K; ++i) {
+                        k[i] = lk[c + i - r.c0];
+                        q[i] = lq[c + i - r.c0];
+                    }
+            },
+            [&](int, int64_t at) {
+                float v[V], d[V];
+                load<T, V>(x + at, v);
+                load<T, V>(dy + at, d);
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = value(v[i], d[i], k[XL ? i : 0], q[XL ? i : 0]);
+                store<T, V>(dx + at, v);
+            },
+            [](int) {});
+    } else {
+        constexpr int V16 = 16 / sizeof(T);
+        walk_tiles<T, V, NT>(
+            g, r,
+            [&](int p0, int c0) {
+                __syncthreads();
+                move_tile<T, V, NT, false>(const_cast<T *>(XL ? x : dy), g, r, p0, c0, tile);
+                __syncthreads();
+            },
+            [&](int c, int j, int p, int64_t at) {
+                float v[V];
+                load<T, V>((XL ? dy : x) + at, v);
+                const Chan k = lk[c - r.c0];
+                const float2 q = lq[c - r.c0];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    T *u = tile_at<T, V16>(tile, p + i, j);
+                    v[i] = XL ? value((float)*u, v[i], k, q) : value(v[i], (float)*u, k, q);
+                    if (XL) *u = (T)v[i];
+                }
+                if (!XL) store<T, V>(dx + at, v);
+            },
+            [&](int p0, int c0) {
+                if (!XL) return;
+                __syncthreads();
+                move_tile<T, V, NT, true>(dx, g, r, p0, c0, tile);
+            });
+    }
+}
+
+// ---- Kernels -----------------------------------------------------------------------
+
+constexpr int kTileBytes(size_t esize) { return 8 * 16 / (int)esize * 128; }
+
+// Moments of the range's channels: part[(n splits + split) C + c].
+template <typename T, int V, bool XL>
+__global__ __launch_bounds__(kThreads) void norm_moments(const T *__restrict__ x, Geometry g,
+                                                         float2 *__restrict__ part)
+{
+    __shared__ Moments lds[(XL ? V : 1) * kThreads];
+    const Range r = range_of(g, blockIdx.x);
+    const int64_t row = r.n * g.splits + blockIdx.x % g.splits;
+    moments<T, XL, V, kThreads>(x, g, r, lds,
+                                [&](int c, const Moments &m) { part[row * g.c + c] = make_float2(m.mean, m.m2); });
+}
+
+__device__ inline void load_consts(Chan *lk, const Geometry &g, const Range &r, const float *__restrict__ gamma,
+                                   const float *__restrict__ beta, const float *__restrict__ mean,
+                                   const float *__restrict__ rstd)
+{
+    for (int i = threadIdx.x; i < r.cb; i += blockDim.x) {
+        const int c = r.c0 + i;
+        const int64_t ng = r.n * g.groups + c / g.per;
+        lk[i] = Chan{mean[ng], rstd[ng], gamma ? gamma[c] : 1.f, beta ? beta[c] : 0.f};
+    }
+    __syncthreads();
+}
+
+template <typename T, int V, bool XL, bool YL>
+__global__ __launch_bounds__(kThreads) void norm_apply(const T *__restrict__ x, const float *__restrict__ gamma,
+                                                       const float *__restrict__ beta,
+                                                       const float *__restrict__ mean,
+                                                       const float *__restrict__ rstd, T *__restrict__ y, Geometry g)
+{
+    __shared__ Chan lk[kMaxBlock];
+    __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
+    const Range r = range_of(g, blockIdx.x);
+    load_consts(lk, g, r, gamma, beta, mean, rstd);
+    apply<T, V, kThreads, XL, YL>(x, y, g, r, lk, tile);
+}
+
+template <typename T, int V, bool XL, bool YL>
+__global__ __launch_bounds__(kThreads) void norm_sums_bwd(const T *__restrict__ x, const T *__restrict__ dy,
+                                                          const float *__restrict__ gamma,
+                                                          const float *__restrict__ beta,
+                                                          const float *__restrict__ mean,
+                                                          const float *__restrict__ rstd, Geometry g,
+                                                          float2 *__restrict__ part)
+{
+    __shared__ Chan lk[kMaxBlock];
+    __shared__ float2 lds[(XL ? V : 1) * kThreads];
+    __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
+    const Range r = range_of(g, blockIdx.x);
+    const int64_t row = r.n * g.splits + blockIdx.x % g.splits;
+    load_consts(lk, g, r, gamma, beta, mean, rstd);
+    sums_bwd<T, V, kThreads, XL, YL>(x, dy, g, r, lk, lds, tile,
+                                     [&](int c, const float2 &s) { part[row * g.c + c] = s; });
+}
+
+template <typename T, int V, bool XL, bool YL>
+__global__ __launch_bounds__(kThreads) void norm_apply_bwd(const T *__restrict__ x, const T *__restrict__ dy,
+                                                           const float *__restrict__ gamma,
+                                                           const float *__restrict__ beta,
+                                                           const float *__restrict__ mean,
+                                                           const float *__restrict__ rstd,
+                                                           const float2 *__restrict__ means, T *__restrict__ dx,
+                                                           Geometry g)
+{
+    __shared__ Chan lk[kMaxBlock];
+    __shared__ float2 lq[kMaxBlock];
+    __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
+    const Range r = range_of(g, blockIdx.x);
+    for (int i = threadIdx.x; i < r.cb; i += kThreads) lq[i] = means[r.n * g.groups + (r.c0 + i) / g.per];
+    load_consts(lk, g, r, gamma, beta, mean, rstd);
+    apply_bwd<T, V, kThreads, XL, YL>(x, dy, dx, g, r, lk, lq, tile);
+}
+
+// ---- One launch ----------------------------------------------------------------------
+
+// Joins the range's channels' values in LDS over each group, one wave a group:
+// done(first channel's place, joined) on lane 0.
+template <int NT, typename S, typename V, typename J, typename D>
+__device__ inline void join_groups(const Geometry &g, const Range &r, V value, S zero, J join2, D done)
+{
+    const int lane = threadIdx.x & 63;
+    for (int k = threadIdx.x >> 6; k < r.cb / g.per; k += NT / 64) {
+        S s = zero;
+        for (int i = lane; i < g.per; i += 64) s = join2(s, value(k * g.per + i));
+        s = join_wave(s, join2);
+        if (lane == 0) done(k * g.per, s);
+    }
+}
+
+template <typename T, int V, bool XL, bool YL>
+__global__ __launch_bounds__(kOneThreads) void norm_one(const T *__restrict__ x, const float *__restrict__ gamma,
+                                                        const float *__restrict__ beta, T *__restrict__ y,
+                                                        float *__restrict__ mean, float *__restrict__ rstd, Geometry g,
+                                                        Geometry ga, float eps)
+{
+    __shared__ Chan lk[kMaxBlock];
+    __shared__ Moments lm[kMaxBlock];
+    __shared__ Moments lds[(XL ? V : 1) * kOneThreads];
+    __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
+    const Range r = range_of(g, blockIdx.x);
+    moments<T, XL, V, kOneThreads>(x, g, r, lds, [&](int c, const Moments &m) { lm[c - r.c0] = m; });
+    __syncthreads();
+    join_groups<kOneThreads>(
+        g, r, [&](int i) { return lm[i]; }, Moments{0.f, 0.f, 0.f}, join,
+        [&](int i, const Moments &m) {
+            const float rs = 1.f / sqrtf(m.m2 / m.n + eps);
+            const int64_t ng = r.n * g.groups + (r.c0 + i) / g.per;
+            mean[ng] = m.mean;
+            rstd[ng] = rs;
+            lk[i].mean = m.mean;
+            lk[i].rstd = rs;
+        });
+    __syncthreads();
+    for (int i = threadIdx.x; i < r.cb; i += kOneThreads) {
+        const int f = i - i % g.per, c = r.c0 + i;
+        const float m = lk[f].mean, rs = lk[f].rstd;
+        if (i != f) {
+            lk[i].mean = m;
+            lk[i].rstd = rs;
+        }
+        lk[i].gamma = gamma ? gamma[c] : 1.f;
+        lk[i].beta = beta ? beta[c] : 0.f;
+    }
+    __syncthreads();
+    apply<T, V, kOneThreads, XL, YL>(x, y, ga, r, lk, tile);
+}
+
+template <typename T, int V, bool XL, bool YL>
+__global__ __launch_bounds__(kOneThreads) void norm_one_bwd(const T *__restrict__ x, const T *__restrict__ dy,
+                                                            const float *__restrict__ gamma,
+                                                            const float *__restrict__ beta,
+                                                            const float *__restrict__ mean,
+                                                            const float *__restrict__ rstd, T *__restrict__ dx,
+                                                            Geometry g, float2 *__restrict__ part)
+{
+    __shared__ Chan lk[kMaxBlock];
+    __shared__ float2 ls[kMaxBlock], lq[kMaxBlock];
+    __shared__ float2 lds[(XL ? V : 1) * kOneThreads];
+    __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
+    const Range r = range_of(g, blockIdx.x);
+    load_consts(lk, g, r, gamma, beta, mean, rstd);
+    sums_bwd<T, V, kOneThreads, XL, YL>(x, dy, g, r, lk, lds, tile, [&](int c, const float2 &s) {
+        ls[c - r.c0] = s;
+        if (part) part[r.n * g.c + c] = s;
+    });
+    __syncthreads();
+    join_groups<kOneThreads>(
+        g, r, [&](int i) { return make_float2(lk[i].gamma * ls[i].x, lk[i].gamma * ls[i].y); },
+        make_float2(0.f, 0.f), [](const float2 &a, const float2 &b) { return make_float2(a.x + b.x, a.y + b.y); },
+        [&](int i, const float2 &s) {
+            const float k = (float)g.per * (float)g.hw;
+            lq[i] = make_float2(s.x / k, s.y / k);
+        });
+    __syncthreads();
+    for (int i = threadIdx.x; i < r.cb; i += kOneThreads)
+        if (i % g.per) lq[i] = lq[i - i % g.per];
+    __syncthreads();
+    apply_bwd<T, V, kOneThreads, XL, YL>(x, dy, dx, g, r, lk, lq, tile);
+}
+
+// ---- Launches ------------------------------------------------------------------------
+
+template <typename T, int V, bool XL, bool YL>
+hipError_t forward_v(const Plan &p, const Call &a, hipStream_t stream)
+{
+    if (p.one) {
+        norm_one<T, V, XL, YL><<<dim3((unsigned)p.apply.count), dim3(kOneThreads), 0, stream>>>(
+            (const T *)a.x, a.gamma, a.beta, (T *)a.out, a.mean_out, a.rstd_out, p.stats, p.apply, p.eps);
+        return hipGetLastError();
+    }
+    const dim3 th(kThreads);
+    float2 *part = (float2 *)a.workspace;
+    norm_moments<T, V, XL><<<dim3((unsigned)p.stats.count), th, 0, stream>>>((const T *)a.x, p.stats, part);
+    launch_finish_forward(p.stats, a.n, part, a.mean_out, a.rstd_out, p.eps, stream);
+    norm_apply<T, V, XL, YL><<<dim3((unsigned)p.apply.count), th, 0, stream>>>(
+        (const T *)a.x, a.gamma, a.beta, a.mean_out, a.rstd_out, (T *)a.out, p.apply);
+    return hipGetLastError();
+}
+
+template <typename T, int V, bool XL, bool YL>
+hipError_t backward_v(const Plan &p, const Call &a, hipStream_t stream)
+{
+    if (p.one) {
+        float2 *sums = a.dgamma || a.dbeta ? (float2 *)a.workspace : nullptr;
+        norm_one_bwd<T, V, XL, YL><<<dim3((unsigned)p.apply.count), dim3(kOneThreads), 0, stream>>>(
+            (const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean, a.rstd, (T *)a.out, p.apply, sums);
+        if (sums) launch_finish_backward(p.apply, a.n, sums, a.gamma, nullptr, a.dgamma, a.dbeta, stream);
+        return hipGetLastError();
+    }
+    const dim3 th(kThreads);
+    float2 *part = (float2 *)a.workspace, *means = (float2 *)((char *)a.workspace + p.means_at);
+    norm_sums_bwd<T, V, XL, YL><<<dim3((unsigned)p.apply.count), th, 0, stream>>>(
+        (const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean, a.rstd, p.apply, part);
+    launch_finish_backward(p.apply, a.n, part, a.gamma, means, a.dgamma, a.dbeta, stream);
+    norm_apply_bwd<T, V, XL, YL><<<dim3((unsigned)p.apply.count), th, 0, stream>>>(
+        (const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean, a.rstd, means, (T *)a.out, p.apply);
+    return hipGetLastError();
+}
+
+template <typename T, bool XL, bool YL>
+hipError_t run_layout(const Plan &p, const Call &a, hipStream_t stream)
+{
+    constexpr int V = 16 / sizeof(T);
+    if (a.dy) return p.vec ? backward_v<T, V, XL, YL>(p, a, stream) : backward_v<T, 1, XL, YL>(p, a, stream);
+    return p.vec ? forward_v<T, V, XL, YL>(p, a, stream) : forward_v<T, 1, XL, YL>(p, a, stream);
+}
+
+template <typename T>
+hipError_t run(const Plan &p, const Call &a, hipStream_t stream)
+{
+    if (p.xl) return p.yl ? run_layout<T, true, true>(p, a, stream) : run_layout<T, true, false>(p, a, stream);
+    return p.yl ? run_layout<T, false, true>(p, a, stream) : run_layout<T, false, false>(p, a, stream);
+}
+
+}  // namespace wtc_norm
+
+#endif  // WTCONV_NORM_BODY_H
