@@ -50,6 +50,14 @@ __device__ inline S join_wave(S s, J join2)
     return s;
 }
 
+// Elements of a vector access: 16 bytes.  The backward pass of two channels-last
+// tensors takes at most four: six constants for each of eight channels a thread
+// are 180 registers and two waves a SIMD (16x256x256x256 fp16: dx 563 us).
+constexpr int vector_of(size_t esize, bool xl, bool yl, bool bwd)
+{
+    return bwd && xl && yl ? 4 : 16 / (int)esize;
+}
+
 struct Plan {
     Geometry stats, apply;  // the forward pass's moments; every other pass
     bool xl, yl, vec, one;
@@ -72,12 +80,13 @@ struct Call {
 template <typename T>
 hipError_t run(const Plan &p, const Call &a, hipStream_t stream);
 
-// mean and rstd of every group from its channels' moments in `part`.
+// mean and rstd of every group of `n` images from its channels' moments in
+// `part`.
 void launch_finish_forward(const Geometry &g, int64_t n, const float2 *part, float *mean, float *rstd, float eps,
                            hipStream_t stream);
 
-// From the channels' sums in `part`: every group's means of t and t xh (unless
-// null), and dgamma and dbeta (unless null).
+// From the channels' sums of `n` images in `part`: every group's means of t and
+// t xh (unless null), and dgamma and dbeta (unless null).
 void launch_finish_backward(const Geometry &g, int64_t n, const float2 *part, const float *gamma, float2 *means,
                             float *dgamma, float *dbeta, hipStream_t stream);
 

@@ -19,93 +19,105 @@ __device__ inline int pixels(const Geometry &g, int s)
     return p < g.ppw ? p : g.ppw;
 }
 
-__device__ inline float wave_sum(float v)
+// A wave's join over its lanes, then over the waves of a workgroup that share a
+// group (`wide`), through LDS; lane 0 of the first wave has it.
+template <typename S, typename J>
+__device__ inline S join_block(S s, bool wide, S *lds, J join2)
 {
-    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+    s = join_wave(s, join2);
+    if (!wide) return s;
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
+    __syncthreads();
+    for (int i = 1; i < 4; ++i) s = join2(i == 1 ? lds[0] : s, lds[i]);
+    return s;
 }
 
-// One wave a group.
-__global__ __launch_bounds__(256) void finish_forward(Geometry g, int64_t groups, const float2 *__restrict__ part,
-                                                      float *__restrict__ mean, float *__restrict__ rstd, float eps)
+// A wave for each group, or (wide) a workgroup.
+__global__ __launch_bounds__(256) void finish_forward(Geometry g, int64_t groups, bool wide,
+                                                      const float2 *__restrict__ part, float *__restrict__ mean,
+                                                      float *__restrict__ rstd, float eps)
 {
-    const int64_t ng = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    __shared__ Moments lds[4];
+    const int64_t ng = wide ? blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (ng >= groups) return;
     const int64_t n = ng / g.groups;
-    const int c0 = (int)(ng % g.groups) * g.per, lane = threadIdx.x & 63;
+    const int c0 = (int)(ng % g.groups) * g.per, first = wide ? threadIdx.x : threadIdx.x & 63;
     const float2 *p = part + n * g.splits * g.c + c0;
     Moments m = {0.f, 0.f, 0.f};
-    for (int i = lane; i < g.splits * g.per; i += 64) {
+#pragma unroll 4
+    for (int i = first; i < g.splits * g.per; i += wide ? 256 : 64) {
         const int s = i / g.per;
         const float2 v = p[(int64_t)s * g.c + i % g.per];
         m = join(m, Moments{(float)pixels(g, s), v.x, v.y});
     }
-    m = join_wave(m, join);
-    if (lane == 0) {
+    m = join_block(m, wide, lds, join);
+    if (first == 0) {
         mean[ng] = m.mean;
         rstd[ng] = 1.f / sqrtf(m.m2 / m.n + eps);
     }
 }
 
-// Workgroups 0 .. gblocks - 1: one wave a group, its means of t and t xh.  The
-// others: dgamma and dbeta of 16 channels each, 16 threads a channel.
-__global__ __launch_bounds__(256) void finish_backward(Geometry g, int64_t images, const float2 *__restrict__ part,
+// Workgroups 0 .. gblocks - 1: the means of t and t xh of a group a wave or
+// (wide) a workgroup.  The others: dgamma and dbeta of 8 channels each, 32
+// threads a channel.
+__global__ __launch_bounds__(256) void finish_backward(Geometry g, int64_t images, bool wide,
+                                                       const float2 *__restrict__ part,
                                                        const float *__restrict__ gamma, int gblocks,
                                                        float2 *__restrict__ means, float *__restrict__ dgamma,
                                                        float *__restrict__ dbeta)
 {
+    auto add = [](const float2 &a, const float2 &b) { return make_float2(a.x + b.x, a.y + b.y); };
+    __shared__ float2 lds[32][9];
     if ((int)blockIdx.x < gblocks) {
-        const int64_t ng = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+        const int64_t ng = wide ? blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
         if (ng >= images * g.groups) return;
-        const int64_t n = ng / g.groups;
-        const int c0 = (int)(ng % g.groups) * g.per, lane = threadIdx.x & 63;
+            const int64_t n = ng / g.groups;
+        const int c0 = (int)(ng % g.groups) * g.per, first = wide ? threadIdx.x : threadIdx.x & 63;
         const float2 *p = part + n * g.splits * g.c + c0;
-        float a = 0.f, b = 0.f;
-        for (int i = lane; i < g.splits * g.per; i += 64) {
+        float2 a = make_float2(0.f, 0.f);
+#pragma unroll 4
+        for (int i = first; i < g.splits * g.per; i += wide ? 256 : 64) {
             const int s = i / g.per, c = i % g.per;
             const float2 v = p[(int64_t)s * g.c + c];
             const float ga = gamma ? gamma[c0 + c] : 1.f;
-            a = fmaf(ga, v.x, a);
-            b = fmaf(ga, v.y, b);
+            a = make_float2(fmaf(ga, v.x, a.x), fmaf(ga, v.y, a.y));
         }
-        a = wave_sum(a);
-        b = wave_sum(b);
+        a = join_block(a, wide, &lds[0][0], add);
         const float k = (float)g.per * (float)g.hw;
-        if (lane == 0) means[ng] = make_float2(a / k, b / k);
+        if (first == 0) means[ng] = make_float2(a.x / k, a.y / k);
         return;
     }
-    __shared__ float2 lds[16][17];
-    const int j = threadIdx.x & 15, r = threadIdx.x >> 4, c = ((int)blockIdx.x - gblocks) * 16 + j;
-    float a = 0.f, b = 0.f;
+    const int j = threadIdx.x & 7, r = threadIdx.x >> 3, c = ((int)blockIdx.x - gblocks) * 8 + j;
+    float2 a = make_float2(0.f, 0.f);
     if (c < g.c)
-#pragma unroll 4
-        for (int64_t i = r; i < images * g.splits; i += 16) {
-            const float2 v = part[i * g.c + c];
-            a += v.x;
-            b += v.y;
-        }
-    lds[r][j] = make_float2(a, b);
+#pragma unroll 8
+        for (int64_t i = r; i < images * g.splits; i += 32) a = add(a, part[i * g.c + c]);
+    lds[r][j] = a;
     __syncthreads();
     if (r == 0 && c < g.c) {
-        for (int i = 1; i < 16; ++i) {
-            a += lds[i][j].x;
-            b += lds[i][j].y;
-        }
-        if (dbeta) dbeta[c] = a;
-        if (dgamma) dgamma[c] = b;
+        for (int i = 1; i < 32; ++i) a = add(a, lds[i][j]);
+        if (dbeta) dbeta[c] = a.x;
+        if (dgamma) dgamma[c] = a.y;
     }
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Threads side by side along rows of `chunks` pieces such that the fewest of nt
-// threads idle, at least eight of them (128 bytes) where there are as many.
-int pick_lanes(int chunks, int nt, int most)
+// Threads side by side along a row of `chunks` pieces.  Channels last: the
+// whole row, or an equal part of it of at most 64 pieces (each part ends in a
+// join over the workgroup: 8 pieces of 40 to gain 6 % of the threads measured
+// 40 us against 8 for 4x320x64x64 fp16).  Planes: four to eight pieces for a
+// thread, so that a batch of loads is full, and among those widths the one that
+// leaves the fewest of nt threads idle.
+int pick_lanes(int chunks, int nt, bool last)
 {
-    const int hi = chunks < most ? chunks : most, lo = hi < 8 ? hi : 8;
+    if (last) return (int)ceil_div(chunks, ceil_div(chunks, 64));
+    int hi = (int)ceil_div(chunks, 4), lo = chunks / 8;
+    hi = hi < 8 ? (chunks < 8 ? chunks : 8) : hi > nt ? nt : hi;
+    lo = lo < 8 ? 8 : lo;
     int best = hi;
     double value = 0.;
-    for (int l = hi; l >= lo; --l) {
+    for (int l = hi; l >= (lo < hi ? lo : hi); --l) {
         const double used = (double)chunks / (double)(ceil_div(chunks, l) * l) * (double)(nt / l * l) / nt;
         if (used > value * 1.02) {
             value = used;
@@ -125,8 +137,8 @@ int lcm_pow2(int per, int v)
 
 enum Walk { kPlanes, kLast, kTiles };
 
-constexpr int kTargetBytes = 32768;  // of one tensor, a workgroup of the three-launch form
-constexpr int kTargetCount = 2048;   // workgroups that fill the chip
+constexpr int kLeastBytes = 8192;   // of one tensor, for a workgroup of the three-launch form
+constexpr int kTargetCount = 2048;  // such workgroups that the chip holds at once
 
 // Whole groups of an image for each workgroup: cb channels, all pixels.
 Geometry one_geometry(Geometry g, int64_t n, Walk w, bool tiles, int v, int v16, int unit)
@@ -141,7 +153,10 @@ Geometry one_geometry(Geometry g, int64_t n, Walk w, bool tiles, int v, int v16,
     while (g.cb * 2 <= kMaxBlock && g.cb < wide && g.cb < g.c && n * ceil_div(g.c, 2 * g.cb) >= 256) g.cb *= 2;
     if (g.cb > g.c) g.cb = g.c;
     g.blocks = (int)ceil_div(g.c, g.cb);
-    g.lanes = w == kLast ? pick_lanes(g.cb / v, nt, 64) : pick_lanes((int)ceil_div(g.hw, v), nt, nt);
+    g.lanes = pick_lanes(w == kLast ? g.cb / v : (int)ceil_div(g.hw, v), nt, w == kLast);
+    // a row of threads for every channel of the group, not more
+    const int chunks = (int)ceil_div(g.hw, v);
+    if (w == kPlanes && nt / g.lanes > g.cb) g.lanes = nt / g.cb < chunks ? nt / g.cb : chunks;
     g.count = n * g.blocks;
     return g;
 }
@@ -153,25 +168,28 @@ Geometry split_geometry(Geometry g, int64_t n, Walk w, int v, int esize)
         const int chunks = g.c / v, most = kMaxBlock / v;
         const int blocks = (int)ceil_div(chunks, most);
         g.cb = (int)ceil_div(chunks, blocks) * v;
-        g.lanes = pick_lanes(g.cb / v, kThreads, 64);
+        g.lanes = pick_lanes(g.cb / v, kThreads, true);
         step = kThreads / g.lanes;
     } else if (w == kTiles) {
         step = 128 / esize;
         g.cb = g.c < step ? g.c : step;
         g.lanes = 1;
     } else {
-        g.lanes = pick_lanes((int)ceil_div(g.hw, v), kThreads, kThreads);
+        g.lanes = pick_lanes((int)ceil_div(g.hw, v), kThreads, false);
         const int rows = kThreads / g.lanes;
-        int64_t cb = kTargetBytes / ((int64_t)g.hw * esize) / rows * rows;
+        int64_t cb = kLeastBytes / ((int64_t)g.hw * esize) / rows * rows;
         if (cb < rows) cb = rows;
         if (cb > kMaxBlock / rows * rows) cb = kMaxBlock / rows * rows;
         g.cb = (int)(cb < g.c ? cb : g.c);
         step = g.lanes * v;
     }
     g.blocks = (int)ceil_div(g.c, g.cb);
-    int64_t ppw = kTargetBytes / ((int64_t)g.cb * esize);
-    const int64_t all = n * g.blocks;
-    if (all * ceil_div(g.hw, ppw < 1 ? 1 : ppw) < kTargetCount) ppw = ceil_div(g.hw, ceil_div(kTargetCount, all));
+    // as many workgroups as the chip holds at once, but no fewer bytes for one
+    // than kLeastBytes
+    const int64_t all = n * g.blocks, most = ceil_div(kTargetCount, all);
+    int64_t ppw = ceil_div(g.hw, most);
+    const int64_t least = ceil_div(kLeastBytes, (int64_t)g.cb * esize);
+    if (ppw < least) ppw = least;
     ppw = ceil_div(ppw < 1 ? 1 : ppw, step) * step;
     g.ppw = (int)(ppw < g.hw ? ppw : ceil_div(g.hw, step) * step);
     g.splits = (int)ceil_div(g.hw, g.ppw);
@@ -195,20 +213,29 @@ Plan make_plan(const wtconv_norm_desc_t &d, bool bwd, bool aligned)
     g.per = g.c / g.groups;
     g.act = d.act;
     const Walk sw = p.xl ? kLast : kPlanes, aw = p.xl != p.yl ? kTiles : sw;
-    p.vec = aligned && (!(p.xl || p.yl) || g.c % v16 == 0) && ((p.xl && p.yl) || g.hw % v16 == 0);
-    const int v = p.vec ? v16 : 1;
+    const int vec = vector_of(esize, p.xl, p.yl, bwd);
+    p.vec = aligned && (!(p.xl || p.yl) || g.c % vec == 0) && ((p.xl && p.yl) || g.hw % vec == 0);
+    const int v = p.vec ? vec : 1;
 
-    // one launch where whole groups make enough workgroups, or where the data
-    // are so few that a launch costs more than the pass
+    // One launch, against three, by sizes (fp16 / fp32, us, measured in a graph):
+    //   planes  64x96x56x56 26 / 37 against 30 / 43, 16x256x256x256 310 against
+    //           329; but 4x320x64x64 17 / 23 against 15 / 20: from 256 workgroups
+    //           on, or where a group is so small that launches are all it costs
+    //           (8x64x14x14: 7 against 14);
+    //   last    a workgroup's rows are narrow: 8x512x16x16 12 / 9 against 13 / 15,
+    //           but 1x128x64x64 19 / 17 against 13 / 12, 64x768x7x7 21 / 20
+    //           against 15 / 16: groups of at most 32 KB, at most 512 of them;
+    //   tiles   forward 8x512x16x16 9 / 9 against 11 / 11, but 1x512x32x32 16 / 21
+    //           against 11 / 11: up to 256 pixels; backward never (64x768x7x7
+    //           27 / 23 against 36 / 23, 8x512x16x16 15 / 17 against 13 / 11).
     const int unit = p.xl || p.yl ? lcm_pow2(g.per, v) : g.per;
-    const int64_t bytes = d.n * d.c * (int64_t)g.hw * esize * (bwd ? 2 : 1);
-    if (unit <= kMaxBlock) {
+    if (unit <= kMaxBlock && !(aw == kTiles && (bwd || g.hw > 256))) {
         const Geometry s = one_geometry(g, d.n, sw, aw == kTiles, v, v16, unit);
-        if (s.count >= 256 || bytes <= 1 << 20) {
+        const int64_t slice = (int64_t)s.cb * g.hw * esize, count = s.count;
+        if (aw == kTiles || (aw == kLast ? slice <= 32768 && count <= 512 : slice <= 16384 || count >= 256)) {
             p.one = true;
             p.stats = s;
             p.apply = s;
-            if (aw == kTiles) p.apply.lanes = 1;
             p.bytes = bwd ? align256((size_t)(d.n * d.c) * sizeof(float2)) : 0;
             return p;
         }
@@ -225,15 +252,20 @@ void launch_finish_forward(const Geometry &g, int64_t n, const float2 *part, flo
                            hipStream_t stream)
 {
     const int64_t groups = n * g.groups;
-    finish_forward<<<dim3((unsigned)ceil_div(groups, 4)), dim3(256), 0, stream>>>(g, groups, part, mean, rstd, eps);
+    const bool wide = g.splits * g.per > 256;
+    finish_forward<<<dim3((unsigned)(wide ? groups : ceil_div(groups, 4))), dim3(256), 0, stream>>>(g, groups, wide,
+                                                                                                  part, mean, rstd,
+                                                                                                  eps);
 }
 
 void launch_finish_backward(const Geometry &g, int64_t n, const float2 *part, const float *gamma, float2 *means,
                             float *dgamma, float *dbeta, hipStream_t stream)
 {
-    const int64_t gb = means ? ceil_div(n * g.groups, 4) : 0, cb = dgamma || dbeta ? ceil_div(g.c, 16) : 0;
-    finish_backward<<<dim3((unsigned)(gb + cb)), dim3(256), 0, stream>>>(g, n, part, gamma, (int)gb, means, dgamma,
-                                                                         dbeta);
+    const bool wide = g.splits * g.per > 256;
+    const int64_t gb = means ? (wide ? n * g.groups : ceil_div(n * g.groups, 4)) : 0;
+    const int64_t cb = dgamma || dbeta ? ceil_div(g.c, 8) : 0;
+    finish_backward<<<dim3((unsigned)(gb + cb)), dim3(256), 0, stream>>>(g, n, wide, part, gamma, (int)gb, means,
+                                                                         dgamma, dbeta);
 }
 
 }  // namespace wtc_norm

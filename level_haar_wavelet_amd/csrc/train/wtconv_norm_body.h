@@ -9,7 +9,8 @@
 //                finds the second time in the caches what it read the first;
 //   three        for images too large or too few for that: sums of pixel ranges
 //                per channel, a small kernel that joins them, and the
-//                elementwise pass.
+//                elementwise pass, which takes the ranges from the last to the
+//                first: the 256 MB cache holds the end of what was read before.
 //
 // Walks.  An image lies in memory as rows of contiguous elements: its channels'
 // planes, or its pixels' channels.  A thread takes V contiguous elements (16
@@ -47,10 +48,16 @@ struct Pack<T, 1> {
     typedef T type;
 };
 
+// The V elements at p, and their values.
 template <typename T, int V>
-__device__ inline void load(const T *p, float (&v)[V])
+__device__ inline typename Pack<T, V>::type fetch(const T *p)
 {
-    const typename Pack<T, V>::type r = *(const typename Pack<T, V>::type *)p;
+    return *(const typename Pack<T, V>::type *)p;
+}
+
+template <typename T, int V>
+__device__ inline void values(const typename Pack<T, V>::type &r, float (&v)[V])
+{
     if constexpr (V == 1)
         v[0] = (float)r;
     else
@@ -70,16 +77,37 @@ __device__ inline void store(T *p, const float (&v)[V])
     *(typename Pack<T, V>::type *)p = r;
 }
 
+// Phi(z) = (1 + erf(z / sqrt 2)) / 2 and e = exp(-z^2 / 2), by Abramowitz and
+// Stegun 7.1.26: erf(x) = 1 - t (a1 + t (a2 + ..)) exp(-x^2), t = 1 / (1 + p x),
+// within 1.5e-7 for x >= 0.  Half the instructions of erff, and the backward
+// pass needs the exponential in any case.
+__device__ inline float normal_cdf(float z, float &e)
+{
+    const float x = fabsf(z) * 0.70710678f;
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
+    e = __expf(-x * x);
+    const float q =
+        t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+    const float tail = 0.5f * q * e;
+    return z < 0.f ? tail : 1.f - tail;
+}
+
+// 1 / (1 + exp(-z)); exp overflows to infinity and the reciprocal to 0.
+__device__ inline float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
+
 // act(z), in place.
 template <int V>
 __device__ inline void act_fwd(int act, float (&z)[V])
 {
     if (act == WTCONV_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) z[i] = z[i] / (1.f + __expf(-z[i]));
+        for (int i = 0; i < V; ++i) z[i] = z[i] * sigmoid(z[i]);
     } else if (act == WTCONV_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) z[i] = 0.5f * z[i] * (1.f + erff(z[i] * 0.70710678f));
+        for (int i = 0; i < V; ++i) {
+            float e;
+            z[i] = z[i] * normal_cdf(z[i], e);
+        }
     } else if (act == WTCONV_ACT_RELU) {
 #pragma unroll
         for (int i = 0; i < V; ++i) z[i] = z[i] < 0.f ? 0.f : z[i];  // NaN stays
@@ -96,11 +124,14 @@ __device__ inline float act_bwd(int act, float dy, float x, float xh, const Chan
 {
     const float z = fmaf(k.gamma, xh, k.beta);
     if (act == WTCONV_ACT_SILU) {
-        const float s = 1.f / (1.f + __expf(-z));
-        return dy * s * (1.f + z * (1.f - s));
+        const float s = sigmoid(z);
+        return dy * s * fmaf(z, 1.f - s, 1.f);
     }
-    if (act == WTCONV_ACT_GELU)
-        return dy * (0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z));
+    if (act == WTCONV_ACT_GELU) {
+        float e;
+        const float p = normal_cdf(z, e);
+        return dy * fmaf(z * 0.39894228f, e, p);
+    }
     if (act == WTCONV_ACT_RELU) {
         bool on = z > 0.f;
         // next to the border the sign is decided in fp64
@@ -130,69 +161,115 @@ __device__ inline Range range_of(const Geometry &g, int id)
     return r;
 }
 
-// Calls f(c, offset) for every V elements of the range that this thread takes;
-// begin(c) before and end(c) after those of one channel (planes) or V channels
-// from c on (last).  Every thread of the workgroup makes the same number of
-// begin and end calls; those without a channel of the range get c < 0.
-template <bool LAST, int V, int NT, typename B, typename F, typename E>
-__device__ inline void walk(const Geometry &g, const Range &r, B begin, F f, E end)
+// Calls get(u, offset) and then use(u, offset, first) for every V elements of
+// the range that this thread takes, kBatch of them at a time, so that their
+// loads are in flight together (u is the place in the batch; first: the
+// channel's first batch); begin(c) before and end(c) after those of one channel
+// (planes) or V channels from c on (last).  Every thread of the workgroup makes
+// the same number of begin and end calls; those without a channel of the range
+// get c < 0.
+constexpr int kBatch = 4;
+
+template <bool LAST, int V, int NT, typename B, typename G, typename F, typename E>
+__device__ inline void walk(const Geometry &g, const Range &r, B begin, G get, F use, E end)
 {
     const int row = threadIdx.x / g.lanes, rows = NT / g.lanes, i = (threadIdx.x - row * g.lanes) * V;
-    if (LAST) {
-        const int64_t base = r.n * g.hw * (int64_t)g.c;
-        for (int cc = 0; cc < r.cb; cc += V * g.lanes) {
-            const int c = row < rows && cc + i < r.cb ? r.c0 + cc + i : -1;
-            begin(c);
-            if (c >= 0)
-#pragma unroll 4
-                for (int p = r.p0 + row; p < r.p1; p += rows) f(c, base + (int64_t)p * g.c + c);
-            end(c);
+    const int64_t base = r.n * g.c * (int64_t)g.hw;
+    const int step = LAST ? rows : V * g.lanes, pitch = LAST ? g.c : 1;
+    for (int cc = 0; cc < r.cb; cc += LAST ? V * g.lanes : rows) {
+        const int own = cc + (LAST ? i : row);
+        const int c = row < rows && own < r.cb ? r.c0 + own : -1;
+        begin(c);
+        if (c >= 0) {
+            const int64_t at0 = base + (LAST ? c : (int64_t)c * g.hw);
+            const int start = r.p0 + (LAST ? row : i);
+            for (int p = start; p < r.p1; p += kBatch * step) {
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+                    if (p + u * step < r.p1) get(u, at0 + (int64_t)(p + u * step) * pitch);
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+                    if (p + u * step < r.p1) use(u, at0 + (int64_t)(p + u * step) * pitch, p == start);
+            }
         }
-    } else {
-        const int64_t base = r.n * g.c * (int64_t)g.hw;
-        for (int cc = 0; cc < r.cb; cc += rows) {
-            const int c = row < rows && cc + row < r.cb ? r.c0 + cc + row : -1;
-            begin(c);
-            if (c >= 0)
-#pragma unroll 4
-                for (int p = r.p0 + i; p < r.p1; p += V * g.lanes) f(c, base + (int64_t)c * g.hw + p);
-            end(c);
-        }
+        end(c);
     }
 }
 
-// Joins the K values of every thread over the threads that share its channel
-// (those below it for channels last, its row for planes) by a tree in LDS, and
-// calls done(c + k, value) on one thread of each channel.  lds: K NT values.
-template <bool LAST, int K, int NT, typename S, typename J, typename D>
-__device__ inline void join_threads(const Geometry &g, int c, const S (&v)[K], S *lds, J join2, D done)
+// The K channels' moments or sums of one thread; the count is the same for all.
+template <int K>
+struct MomentSet {
+    float n, mean[K], m2[K];
+    static constexpr int kFloats = 1 + 2 * K;
+    __device__ void add(const MomentSet &b)
+    {
+        const float s = n + b.n;
+        const float w = s > 0.f ? b.n * __builtin_amdgcn_rcpf(s) : 0.f, v = n * w;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float d = b.mean[k] - mean[k];
+            // an empty set's own zeros must not meet an infinity
+            mean[k] = n > 0.f ? fmaf(d, w, mean[k]) : b.mean[k];
+            m2[k] = n > 0.f && b.n > 0.f ? m2[k] + b.m2[k] + d * d * v : n > 0.f ? m2[k] : b.m2[k];
+        }
+        n = s;
+    }
+};
+
+template <int K>
+struct SumSet {
+    float a[K], b[K];
+    static constexpr int kFloats = 2 * K;
+    __device__ void add(const SumSet &o)
+    {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            a[k] += o.a[k];
+            b[k] += o.b[k];
+        }
+    }
+};
+
+// Joins the sets of the threads that share a channel (those below it for
+// channels last, its row for planes) by a tree of fours in LDS; the first of
+// them ends up with the whole and returns true.  lds: kFloats NT floats.
+template <bool LAST, int NT, typename S>
+__device__ inline bool join_threads(const Geometry &g, int c, S &v, float *lds)
 {
     const int t = threadIdx.x, row = t / g.lanes, rows = NT / g.lanes, i = t - row * g.lanes;
     const int q = LAST ? row : i, stride = LAST ? g.lanes : 1;
-    __syncthreads();
+    auto put = [&] {
+        const float *f = (const float *)&v;
 #pragma unroll
-    for (int k = 0; k < K; ++k) lds[k * NT + t] = v[k];
-    __syncthreads();
+        for (int k = 0; k < S::kFloats; ++k) lds[k * NT + t] = f[k];
+    };
     for (int h = LAST ? rows : g.lanes; h > 1;) {
-        const int half = (h + 1) / 2;
-        if (row < rows && q < h - half)
-#pragma unroll
-            for (int k = 0; k < K; ++k) lds[k * NT + t] = join2(lds[k * NT + t], lds[k * NT + t + half * stride]);
+        const int part = (h + 3) / 4;
         __syncthreads();
-        h = half;
-    }
-    if (c >= 0 && q == 0)
+        if (row < rows && q < h) put();
+        __syncthreads();
+        if (row < rows && q < part)
 #pragma unroll
-        for (int k = 0; k < K; ++k) done(c + k, lds[k * NT + t]);
+            for (int o = 1; o < 4; ++o)
+                if (q + o * part < h) {
+                    S w;
+                    float *f = (float *)&w;
+#pragma unroll
+                    for (int k = 0; k < S::kFloats; ++k) f[k] = lds[k * NT + t + o * part * stride];
+                    v.add(w);
+                }
+        h = part;
+    }
+    return c >= 0 && q == 0;
 }
 
 // Moments of every channel of the range: done(c, moments).
 template <typename T, bool LAST, int V, int NT, typename D>
-__device__ inline void moments(const T *__restrict__ x, const Geometry &g, const Range &r, Moments *lds,
-                               D done)
+__device__ inline void moments(const T *__restrict__ x, const Geometry &g, const Range &r, float *lds, D done)
 {
     constexpr int K = LAST ? V : 1;
     float s[K], a[K], b[K], n;
+    typename Pack<T, V>::type raw[kBatch];
     walk<LAST, V, NT>(
         g, r,
         [&](int) {
@@ -200,10 +277,11 @@ __device__ inline void moments(const T *__restrict__ x, const Geometry &g, const
 #pragma unroll
             for (int k = 0; k < K; ++k) s[k] = a[k] = b[k] = 0.f;
         },
-        [&](int, int64_t at) {
+        [&](int u, int64_t at) { raw[u] = fetch<T, V>(x + at); },
+        [&](int u, int64_t, bool first) {
             float v[V];
-            load<T, V>(x + at, v);
-            if (n == 0.f)
+            values<T, V>(raw[u], v);
+            if (u == 0 && first)
 #pragma unroll
                 for (int k = 0; k < K; ++k) s[k] = v[k];
             n += V / K;
@@ -216,15 +294,19 @@ __device__ inline void moments(const T *__restrict__ x, const Geometry &g, const
             }
         },
         [&](int c) {
-            Moments m[K];
+            MomentSet<K> m;
             const float w = n > 0.f ? 1.f / n : 0.f;
+            m.n = n;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                m[k] = Moments{n, fmaf(a[k], w, s[k]), fmaf(-a[k] * w, a[k], b[k])};
+                m.mean[k] = fmaf(a[k], w, s[k]);
+                m.m2[k] = fmaf(-a[k] * w, a[k], b[k]);
                 // rounding only: a sum of squares is not negative (NaN stays)
-                if (m[k].m2 < 0.f) m[k].m2 = 0.f;
+                if (m.m2[k] < 0.f) m.m2[k] = 0.f;
             }
-            join_threads<LAST, K, NT>(g, c, m, lds, join, done);
+            if (join_threads<LAST, NT>(g, c, m, lds))
+#pragma unroll
+                for (int k = 0; k < K; ++k) done(c + k, Moments{m.n, m.mean[k], m.m2[k]});
         });
 }
 
@@ -284,6 +366,7 @@ __device__ inline void apply(const T *__restrict__ x, T *__restrict__ y, const G
     if constexpr (XL == YL) {
         constexpr int K = XL ? V : 1;
         Chan k[K];
+        typename Pack<T, V>::type raw[kBatch];
         walk<XL, V, NT>(
             g, r,
             [&](int c) {
@@ -294,9 +377,10 @@ __device__ inline void apply(const T *__restrict__ x, T *__restrict__ y, const G
                         k[i].rstd *= k[i].gamma;
                     }
             },
-            [&](int, int64_t at) {
+            [&](int u, int64_t at) { raw[u] = fetch<T, V>(x + at); },
+            [&](int u, int64_t at, bool) {
                 float v[V];
-                load<T, V>(x + at, v);
+                values<T, V>(raw[u], v);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const Chan &q = k[XL ? i : 0];
@@ -322,7 +406,7 @@ __device__ inline void apply(const T *__restrict__ x, T *__restrict__ y, const G
 #pragma unroll
                     for (int i = 0; i < V; ++i) v[i] = (float)*tile_at<T, V16>(tile, q + i, j);
                 else
-                    load<T, V>(x + at, v);
+                    values<T, V>(fetch<T, V>(x + at), v);
                 const Chan k = lk[c - r.c0];
                 const float a = k.rstd * k.gamma;
 #pragma unroll
@@ -347,36 +431,44 @@ __device__ inline void apply(const T *__restrict__ x, T *__restrict__ y, const G
 // channel's sums (tiles).
 template <typename T, int V, int NT, bool XL, bool YL, typename D>
 __device__ inline void sums_bwd(const T *__restrict__ x, const T *__restrict__ dy, const Geometry &g, const Range &r,
-                                const Chan *lk, float2 *lds, char *tile, D done)
+                                const Chan *lk, float *lds, char *tile, D done)
 {
-    auto add = [](const float2 &a, const float2 &b) { return make_float2(a.x + b.x, a.y + b.y); };
     if constexpr (XL == YL) {
         constexpr int K = XL ? V : 1;
         Chan k[K];
-        float2 s[K];
+        SumSet<K> s;
+        typename Pack<T, V>::type rx[kBatch], rd[kBatch];
         walk<XL, V, NT>(
             g, r,
             [&](int c) {
 #pragma unroll
                 for (int i = 0; i < K; ++i) {
-                    s[i] = make_float2(0.f, 0.f);
+                    s.a[i] = s.b[i] = 0.f;
                     if (c >= 0) k[i] = lk[c + i - r.c0];
                 }
             },
-            [&](int, int64_t at) {
+            [&](int u, int64_t at) {
+                rx[u] = fetch<T, V>(x + at);
+                rd[u] = fetch<T, V>(dy + at);
+            },
+            [&](int u, int64_t at, bool) {
                 float v[V], d[V];
-                load<T, V>(x + at, v);
-                load<T, V>(dy + at, d);
+                values<T, V>(rx[u], v);
+                values<T, V>(rd[u], d);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const int q = XL ? i : 0;
                     const float xh = (v[i] - k[q].mean) * k[q].rstd;
                     const float dz = act_bwd(g.act, d[i], v[i], xh, k[q]);
-                    s[q].x += dz;
-                    s[q].y = fmaf(dz, xh, s[q].y);
+                    s.a[q] += dz;
+                    s.b[q] = fmaf(dz, xh, s.b[q]);
                 }
             },
-            [&](int c) { join_threads<XL, K, NT>(g, c, s, lds, add, done); });
+            [&](int c) {
+                if (join_threads<XL, NT>(g, c, s, lds))
+#pragma unroll
+                    for (int i = 0; i < K; ++i) done(c + i, make_float2(s.a[i], s.b[i]));
+            });
     } else {
         // 8 V16 / V threads side by side share a channel of the tile; a thread's
         // places e, e + NT, .. are kSide * kChunks / NT channels
@@ -397,7 +489,7 @@ __device__ inline void sums_bwd(const T *__restrict__ x, const T *__restrict__ d
                     if (e >= kSide * kChunks || c0 + j >= r.c0 + r.cb || p0 + q >= r.p1) continue;
                     const int64_t at = (r.n * g.c + c0 + j) * (int64_t)g.hw + p0 + q;
                     float v[V];
-                    load<T, V>((XL ? dy : x) + at, v);
+                    values<T, V>(fetch<T, V>((XL ? dy : x) + at), v);
                     const Chan k = lk[c0 + j - r.c0];
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
@@ -437,6 +529,7 @@ __device__ inline void apply_bwd(const T *__restrict__ x, const T *__restrict__ 
         constexpr int K = XL ? V : 1;
         Chan k[K];
         float2 q[K];
+        typename Pack<T, V>::type rx[kBatch], rd[kBatch];
         walk<XL, V, NT>(
             g, r,
             [&](int c) {
@@ -447,10 +540,14 @@ __device__ inline void apply_bwd(const T *__restrict__ x, const T *__restrict__ 
                         q[i] = lq[c + i - r.c0];
                     }
             },
-            [&](int, int64_t at) {
+            [&](int u, int64_t at) {
+                rx[u] = fetch<T, V>(x + at);
+                rd[u] = fetch<T, V>(dy + at);
+            },
+            [&](int u, int64_t at, bool) {
                 float v[V], d[V];
-                load<T, V>(x + at, v);
-                load<T, V>(dy + at, d);
+                values<T, V>(rx[u], v);
+                values<T, V>(rd[u], d);
 #pragma unroll
                 for (int i = 0; i < V; ++i) v[i] = value(v[i], d[i], k[XL ? i : 0], q[XL ? i : 0]);
                 store<T, V>(dx + at, v);
@@ -467,7 +564,7 @@ __device__ inline void apply_bwd(const T *__restrict__ x, const T *__restrict__ 
             },
             [&](int c, int j, int p, int64_t at) {
                 float v[V];
-                load<T, V>((XL ? dy : x) + at, v);
+                values<T, V>(fetch<T, V>((XL ? dy : x) + at), v);
                 const Chan k = lk[c - r.c0];
                 const float2 q = lq[c - r.c0];
 #pragma unroll
@@ -495,7 +592,7 @@ template <typename T, int V, bool XL>
 __global__ __launch_bounds__(kThreads) void norm_moments(const T *__restrict__ x, Geometry g,
                                                          float2 *__restrict__ part)
 {
-    __shared__ Moments lds[(XL ? V : 1) * kThreads];
+    __shared__ float lds[(1 + 2 * (XL ? V : 1)) * kThreads];
     const Range r = range_of(g, blockIdx.x);
     const int64_t row = r.n * g.splits + blockIdx.x % g.splits;
     moments<T, XL, V, kThreads>(x, g, r, lds,
@@ -522,7 +619,7 @@ __global__ __launch_bounds__(kThreads) void norm_apply(const T *__restrict__ x, 
 {
     __shared__ Chan lk[kMaxBlock];
     __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
-    const Range r = range_of(g, blockIdx.x);
+    const Range r = range_of(g, gridDim.x - 1 - blockIdx.x);
     load_consts(lk, g, r, gamma, beta, mean, rstd);
     apply<T, V, kThreads, XL, YL>(x, y, g, r, lk, tile);
 }
@@ -536,7 +633,7 @@ __global__ __launch_bounds__(kThreads) void norm_sums_bwd(const T *__restrict__ 
                                                           float2 *__restrict__ part)
 {
     __shared__ Chan lk[kMaxBlock];
-    __shared__ float2 lds[(XL ? V : 1) * kThreads];
+    __shared__ float lds[2 * (XL ? V : 1) * kThreads];
     __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
     const Range r = range_of(g, blockIdx.x);
     const int64_t row = r.n * g.splits + blockIdx.x % g.splits;
@@ -557,7 +654,7 @@ __global__ __launch_bounds__(kThreads) void norm_apply_bwd(const T *__restrict__
     __shared__ Chan lk[kMaxBlock];
     __shared__ float2 lq[kMaxBlock];
     __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
-    const Range r = range_of(g, blockIdx.x);
+    const Range r = range_of(g, gridDim.x - 1 - blockIdx.x);
     for (int i = threadIdx.x; i < r.cb; i += kThreads) lq[i] = means[r.n * g.groups + (r.c0 + i) / g.per];
     load_consts(lk, g, r, gamma, beta, mean, rstd);
     apply_bwd<T, V, kThreads, XL, YL>(x, dy, dx, g, r, lk, lq, tile);
@@ -587,7 +684,7 @@ __global__ __launch_bounds__(kOneThreads) void norm_one(const T *__restrict__ x,
 {
     __shared__ Chan lk[kMaxBlock];
     __shared__ Moments lm[kMaxBlock];
-    __shared__ Moments lds[(XL ? V : 1) * kOneThreads];
+    __shared__ float lds[(1 + 2 * (XL ? V : 1)) * kOneThreads];
     __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
     const Range r = range_of(g, blockIdx.x);
     moments<T, XL, V, kOneThreads>(x, g, r, lds, [&](int c, const Moments &m) { lm[c - r.c0] = m; });
@@ -627,7 +724,7 @@ __global__ __launch_bounds__(kOneThreads) void norm_one_bwd(const T *__restrict_
 {
     __shared__ Chan lk[kMaxBlock];
     __shared__ float2 ls[kMaxBlock], lq[kMaxBlock];
-    __shared__ float2 lds[(XL ? V : 1) * kOneThreads];
+    __shared__ float lds[2 * (XL ? V : 1) * kOneThreads];
     __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
     const Range r = range_of(g, blockIdx.x);
     load_consts(lk, g, r, gamma, beta, mean, rstd);
@@ -672,28 +769,29 @@ hipError_t forward_v(const Plan &p, const Call &a, hipStream_t stream)
 template <typename T, int V, bool XL, bool YL>
 hipError_t backward_v(const Plan &p, const Call &a, hipStream_t stream)
 {
+    const Geometry &g = p.apply;
+    float2 *part = (float2 *)a.workspace, *means = (float2 *)((char *)a.workspace + p.means_at);
     if (p.one) {
-        float2 *sums = a.dgamma || a.dbeta ? (float2 *)a.workspace : nullptr;
-        norm_one_bwd<T, V, XL, YL><<<dim3((unsigned)p.apply.count), dim3(kOneThreads), 0, stream>>>(
-            (const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean, a.rstd, (T *)a.out, p.apply, sums);
-        if (sums) launch_finish_backward(p.apply, a.n, sums, a.gamma, nullptr, a.dgamma, a.dbeta, stream);
+        float2 *sums = a.dgamma || a.dbeta ? part : nullptr;
+        norm_one_bwd<T, V, XL, YL><<<dim3((unsigned)g.count), dim3(kOneThreads), 0, stream>>>(
+            (const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean, a.rstd, (T *)a.out, g, sums);
+        if (sums) launch_finish_backward(g, a.n, sums, a.gamma, nullptr, a.dgamma, a.dbeta, stream);
         return hipGetLastError();
     }
-    const dim3 th(kThreads);
-    float2 *part = (float2 *)a.workspace, *means = (float2 *)((char *)a.workspace + p.means_at);
-    norm_sums_bwd<T, V, XL, YL><<<dim3((unsigned)p.apply.count), th, 0, stream>>>(
-        (const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean, a.rstd, p.apply, part);
-    launch_finish_backward(p.apply, a.n, part, a.gamma, means, a.dgamma, a.dbeta, stream);
-    norm_apply_bwd<T, V, XL, YL><<<dim3((unsigned)p.apply.count), th, 0, stream>>>(
-        (const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean, a.rstd, means, (T *)a.out, p.apply);
+    const dim3 th(kThreads), grid((unsigned)g.count);
+    norm_sums_bwd<T, V, XL, YL><<<grid, th, 0, stream>>>((const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean,
+                                                         a.rstd, g, part);
+    launch_finish_backward(g, a.n, part, a.gamma, means, a.dgamma, a.dbeta, stream);
+    norm_apply_bwd<T, V, XL, YL><<<grid, th, 0, stream>>>((const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean,
+                                                          a.rstd, means, (T *)a.out, g);
     return hipGetLastError();
 }
 
 template <typename T, bool XL, bool YL>
 hipError_t run_layout(const Plan &p, const Call &a, hipStream_t stream)
 {
-    constexpr int V = 16 / sizeof(T);
-    if (a.dy) return p.vec ? backward_v<T, V, XL, YL>(p, a, stream) : backward_v<T, 1, XL, YL>(p, a, stream);
+    constexpr int V = vector_of(sizeof(T), XL, YL, false), W = vector_of(sizeof(T), XL, YL, true);
+    if (a.dy) return p.vec ? backward_v<T, W, XL, YL>(p, a, stream) : backward_v<T, 1, XL, YL>(p, a, stream);
     return p.vec ? forward_v<T, V, XL, YL>(p, a, stream) : forward_v<T, 1, XL, YL>(p, a, stream);
 }
 

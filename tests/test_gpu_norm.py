@@ -309,7 +309,11 @@ def test_captured_calls_replay_on_new_inputs(shape, layouts):
 
 
 def test_offsets_beyond_32_bits():
-    """Five images of 2^29 values each: the last one's offsets pass 2^31."""
+    """Five images of 2^29 values each: the last one's offsets pass 2^31.  The
+    image alone is cut into other ranges: its statistics may differ by the
+    rounding of their sums (CHAIN u E|x| = 128 2^-24 0.8 = 6e-6), its outputs
+    by that and one fp16 step (2^-10 of the value), as two neighbouring
+    roundings do."""
     x = torch.empty(5, 2, 1 << 14, 1 << 14, device="cuda", dtype=torch.float16)
     for i in range(5):
         x[i].normal_()
@@ -318,6 +322,8 @@ def test_offsets_beyond_32_bits():
     torch.cuda.synchronize()
     y1, m1, r1 = wt.wtconv_group_norm_forward(x[4:].clone(), 2, act="relu")
     dx1, _, _ = wt.wtconv_group_norm_backward(x[4:].clone(), x[4:].clone(), 2, m1, r1, act="relu")
-    assert torch.equal(m1, mean[4:]) and torch.equal(y1, y[4:]) and torch.equal(dx1, dx[4:])
+    assert torch.allclose(m1, mean[4:], atol=6e-6, rtol=0)
+    for a, b in ((y1, y[4:]), (dx1, dx[4:])):
+        assert ((a - b).abs() <= b.abs() * 2.0 ** -10 + 4e-5).all()
     v = x[4, 1].double()
     assert abs(v.mean().item() - m1[0, 1].item()) < 1e-5
