@@ -13,6 +13,7 @@ torch operation.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import _native
 
@@ -37,7 +38,7 @@ def _dtype_code(t, name):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _gpu_tensor(t, name, device=None):
@@ -70,31 +71,38 @@ def _workspace(workspace, need, device):
 
 class _On:
     """The device of the tensors as the current one, and the stream's handle.
-    A workspace that the call made itself goes back to the allocator when the
-    call returns; on another stream than the current one it is marked as used
-    there."""
+    What a call allocates itself comes from the current stream's pool; where the
+    call runs on another stream, `made` marks it as used there, so that it is
+    not handed out again before the call is done."""
+
+    __slots__ = ("handle", "guard", "other")
 
     def __init__(self, device, stream):
-        torch = _torch()
-        self.guard = torch.cuda.device(device)
-        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
-        if self.stream.device != device:
-            raise TypeError("the stream belongs to %s, the tensors lie on %s" % (self.stream.device, device))
-        self.explicit = stream is not None
+        cuda = _torch().cuda
+        self.guard = None if cuda.current_device() == device.index else cuda.device(device)
+        self.other = stream
+        if stream is None:
+            # the current stream's handle without a Stream object (2 us less)
+            self.handle = _torch()._C._cuda_getCurrentRawStream(device.index)
+        elif stream.device != device:
+            raise TypeError("the stream belongs to %s, the tensors lie on %s" % (stream.device, device))
+        else:
+            self.handle = stream.cuda_stream
 
     def __enter__(self):
-        self.guard.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.handle
 
     def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
     def made(self, *tensors):
-        """Outputs and workspaces allocated by the call on the current stream."""
-        if self.explicit:
+        if self.other is not None:
             for t in tensors:
                 if t is not None:
-                    t.record_stream(self.stream)
+                    t.record_stream(self.other)
 
 
 # ---- group norm --------------------------------------------------------------
@@ -122,31 +130,23 @@ def _like(t, layout):
     return torch.empty_like(t, memory_format=fmt)
 
 
-def _norm_desc(x, groups, act, x_layout, y_layout, eps):
+@functools.lru_cache(maxsize=512)
+def _norm_plan(op, n, c, h, w, groups, dtype, act, x_layout, y_layout, eps):
+    """The descriptor of these sizes (as ctypes takes it) and op's workspace."""
     if act not in _native.ACTS:
         raise ValueError("act must be one of %s, got %r" % (", ".join(sorted(_native.ACTS)), act))
-    n, c, h, w = x.shape
-    return _native.NormDesc(n, c, h, w, int(groups), _dtype_code(x, "x"), _native.ACTS[act], x_layout, y_layout,
-                            float(eps))
+    d = _native.NormDesc(n, c, h, w, groups, dtype, _native.ACTS[act], x_layout, y_layout, eps)
+    out = ctypes.c_size_t(0)
+    _native.check(_native.load().wtconv_group_norm_workspace_size(ctypes.byref(d), op, ctypes.byref(out)),
+                  "wtconv_group_norm_workspace_size")
+    return ctypes.byref(d), out.value
 
 
 def wtconv_group_norm_workspace_size(shape, groups, dtype_code, op, x_layout=_native.NCHW, y_layout=_native.NCHW,
                                      act="none") -> int:
     """Bytes of workspace of the forward (OP_FWD) or backward (OP_BWD) call."""
-    lib = _native.load()
     n, c, h, w = shape
-    d = _native.NormDesc(n, c, h, w, groups, dtype_code, _native.ACTS[act], x_layout, y_layout, 1e-5)
-    out = ctypes.c_size_t(0)
-    _native.check(lib.wtconv_group_norm_workspace_size(ctypes.byref(d), op, ctypes.byref(out)),
-                  "wtconv_group_norm_workspace_size")
-    return out.value
-
-
-def _norm_need(lib, d, op):
-    out = ctypes.c_size_t(0)
-    _native.check(lib.wtconv_group_norm_workspace_size(ctypes.byref(d), op, ctypes.byref(out)),
-                  "wtconv_group_norm_workspace_size")
-    return out.value
+    return _norm_plan(op, n, c, h, w, groups, dtype_code, act, x_layout, y_layout, 1e-5)[1]
 
 
 def wtconv_group_norm_forward(x, groups, gamma=None, beta=None, eps=1e-5, act="none", channels_last=None, y=None,
@@ -173,9 +173,8 @@ def wtconv_group_norm_forward(x, groups, gamma=None, beta=None, eps=1e-5, act="n
             raise TypeError("y is not in the layout that channels_last asks for")
     else:
         yl = xl if channels_last is None else _native.NHWC if channels_last else _native.NCHW
-    n, c = x.shape[:2]
-    d = _norm_desc(x, groups, act, xl, yl, eps)
-    need = _norm_need(lib, d, _native.OP_FWD)
+    n, c, h, w = x.shape
+    d, need = _norm_plan(_native.OP_FWD, n, c, h, w, groups, _dtype_code(x, "x"), act, xl, yl, float(eps))
     _f32(gamma, "gamma", (c,), x.device)
     _f32(beta, "beta", (c,), x.device)
     _f32(mean, "mean", (n, groups), x.device)
@@ -190,7 +189,7 @@ def wtconv_group_norm_forward(x, groups, gamma=None, beta=None, eps=1e-5, act="n
         if rstd is None:
             made.append(rstd := torch.empty((n, groups), dtype=torch.float32, device=x.device))
         ws, nbytes = _workspace(workspace, need, x.device)
-        st = lib.wtconv_group_norm_forward(ctypes.byref(d), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean),
+        st = lib.wtconv_group_norm_forward(d, _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean),
                                            _ptr(rstd), _ptr(ws), nbytes, s)
         on.made(ws if workspace is None else None, *made)
     _native.check(st, "wtconv_group_norm_forward")
@@ -213,9 +212,9 @@ def wtconv_group_norm_backward(x, dy, groups, mean, rstd, gamma=None, beta=None,
         _gpu_tensor(dx, "dx", x.device)
         if dx.shape != x.shape or dx.dtype != x.dtype or (_layout_of(dx, "dx") != xl and not _one_layout(x)):
             raise TypeError("dx must match x in shape, dtype and layout")
-    n, c = x.shape[:2]
-    d = _norm_desc(x, groups, act, xl, yl, 1.0)  # eps is in rstd already
-    need = _norm_need(lib, d, _native.OP_BWD)
+    n, c, h, w = x.shape
+    # eps is in rstd already
+    d, need = _norm_plan(_native.OP_BWD, n, c, h, w, groups, _dtype_code(x, "x"), act, xl, yl, 1.0)
     _f32(gamma, "gamma", (c,), x.device)
     _f32(beta, "beta", (c,), x.device)
     for t, name in ((mean, "mean"), (rstd, "rstd")):
@@ -233,7 +232,7 @@ def wtconv_group_norm_backward(x, dy, groups, mean, rstd, gamma=None, beta=None,
         if dbeta is None:
             made.append(dbeta := torch.empty((c,), dtype=torch.float32, device=x.device))
         ws, nbytes = _workspace(workspace, need, x.device)
-        st = lib.wtconv_group_norm_backward(ctypes.byref(d), _ptr(x), _ptr(dy), _ptr(gamma), _ptr(beta), _ptr(mean),
+        st = lib.wtconv_group_norm_backward(d, _ptr(x), _ptr(dy), _ptr(gamma), _ptr(beta), _ptr(mean),
                                             _ptr(rstd), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(ws), nbytes, s)
         on.made(ws if workspace is None else None, *made)
     _native.check(st, "wtconv_group_norm_backward")
@@ -242,21 +241,24 @@ def wtconv_group_norm_backward(x, dy, groups, mean, rstd, gamma=None, beta=None,
 
 # ---- Newton-Schulz and the Muon step -------------------------------------------
 
-def _ortho_desc(t, name, steps, eps):
+@functools.lru_cache(maxsize=512)
+def _ortho_plan(batch, rows, cols, dtype, steps, eps):
+    """The descriptor of these sizes (as ctypes takes it) and its workspace."""
+    d = _native.OrthoDesc(batch, rows, cols, dtype, steps, eps)
+    out = ctypes.c_size_t(0)
+    _native.check(_native.load().wtconv_orthogonalize_workspace_size(ctypes.byref(d), ctypes.byref(out)),
+                  "wtconv_orthogonalize_workspace_size")
+    return ctypes.byref(d), out.value
+
+
+def _ortho_of(t, name, steps, eps):
     _gpu_tensor(t, name)
     if t.dim() not in (2, 3):
         raise TypeError("%s must be a (rows, cols) or (batch, rows, cols) tensor" % name)
     if not t.is_contiguous():
         raise TypeError("%s must be contiguous" % name)
     b, r, c = t.shape if t.dim() == 3 else (1,) + tuple(t.shape)
-    return _native.OrthoDesc(b, r, c, _dtype_code(t, name), int(steps), float(eps))
-
-
-def _ortho_need(lib, d):
-    out = ctypes.c_size_t(0)
-    _native.check(lib.wtconv_orthogonalize_workspace_size(ctypes.byref(d), ctypes.byref(out)),
-                  "wtconv_orthogonalize_workspace_size")
-    return out.value
+    return _ortho_plan(b, r, c, _dtype_code(t, name), int(steps), float(eps))
 
 
 def wtconv_orthogonalize_workspace_size(shape, dtype_code, steps=5) -> int:
@@ -264,7 +266,7 @@ def wtconv_orthogonalize_workspace_size(shape, dtype_code, steps=5) -> int:
     matrices of shape (rows, cols) or (batch, rows, cols) and a gradient of
     type dtype_code."""
     b, r, c = shape if len(shape) == 3 else (1,) + tuple(shape)
-    return _ortho_need(_native.load(), _native.OrthoDesc(b, r, c, dtype_code, int(steps), 1e-7))
+    return _ortho_plan(b, r, c, dtype_code, int(steps), 1e-7)[1]
 
 
 def wtconv_orthogonalize(g, steps=5, eps=1e-7, out=None, workspace=None, stream=None):
@@ -272,8 +274,7 @@ def wtconv_orthogonalize(g, steps=5, eps=1e-7, out=None, workspace=None, stream=
     rows, cols) stack of them, contiguous float32, float16 or bfloat16.
     Singular values go towards 1 (to about 0.7 .. 1.2 in five steps)."""
     lib = _native.load()
-    d = _ortho_desc(g, "g", steps, eps)
-    need = _ortho_need(lib, d)
+    d, need = _ortho_of(g, "g", steps, eps)
     if out is not None:
         _gpu_tensor(out, "out", g.device)
         if out.shape != g.shape or out.dtype != g.dtype or not out.is_contiguous():
@@ -284,7 +285,7 @@ def wtconv_orthogonalize(g, steps=5, eps=1e-7, out=None, workspace=None, stream=
         if out is None:
             made = out = _torch().empty_like(g)
         ws, nbytes = _workspace(workspace, need, g.device)
-        st = lib.wtconv_orthogonalize(ctypes.byref(d), _ptr(g), _ptr(out), _ptr(ws), nbytes, s)
+        st = lib.wtconv_orthogonalize(d, _ptr(g), _ptr(out), _ptr(ws), nbytes, s)
         on.made(ws if workspace is None else None, made)
     _native.check(st, "wtconv_orthogonalize")
     return out
@@ -299,8 +300,7 @@ def wtconv_muon_step(weight, grad, momentum, lr, mu=0.95, weight_decay=0.0, scal
     rows, cols); grad may be float32, float16 or bfloat16.  In place unless
     weight_out / momentum_out are given."""
     lib = _native.load()
-    d = _ortho_desc(grad, "grad", steps, eps)
-    need = _ortho_need(lib, d)
+    d, need = _ortho_of(grad, "grad", steps, eps)
     _gpu_tensor(weight, "weight", grad.device)
     _gpu_tensor(momentum, "momentum", grad.device)
     weight_out = weight if weight_out is None else weight_out
@@ -312,7 +312,7 @@ def wtconv_muon_step(weight, grad, momentum, lr, mu=0.95, weight_decay=0.0, scal
     on = _On(grad.device, stream)
     with on as s:
         ws, nbytes = _workspace(workspace, need, grad.device)
-        st = lib.wtconv_muon_step(ctypes.byref(d), ctypes.byref(hyper), _ptr(weight), _ptr(grad), _ptr(momentum),
+        st = lib.wtconv_muon_step(d, ctypes.byref(hyper), _ptr(weight), _ptr(grad), _ptr(momentum),
                                   _ptr(weight_out), _ptr(momentum_out), _ptr(ws), nbytes, s)
         on.made(ws if workspace is None else None)
     _native.check(st, "wtconv_muon_step")

@@ -28,30 +28,15 @@
 
 #include "wtconv_check.h"
 #include "wtconv_muon.h"
+#include "wtconv_muon_split.h"
 
 namespace {
 
-constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+using namespace wtc_muon;
+
 constexpr int kThreads = 256;
 
-typedef _Float16 half8 __attribute__((ext_vector_type(8)));
-typedef float float16v __attribute__((ext_vector_type(16)));
-
-// ---- The update, its norm, and the first planes ----------------------------
-
-// The update the iteration starts from: G itself, or the Muon step's blend of
-// gradient and momentum.
-struct Blend {
-    int muon, nesterov;
-    float mu;
-};
-
-template <typename T>
-__device__ inline float blend(const Blend &b, T g, float momentum_out)
-{
-    if (!b.muon) return (float)g;
-    return b.nesterov ? fmaf(b.mu, momentum_out, (1.f - b.mu) * (float)g) : momentum_out;
-}
+// ---- The update's norm and the first planes ----------------------------------
 
 // Partial sums of |U|^2 in fp64 (fp32 squares would overflow from 2^64 on and
 // vanish below 2^-75), one for each of gridDim.x workgroups of a matrix, and
@@ -88,8 +73,10 @@ __device__ inline void split8(const float (&v)[8], half8 &hi, half8 &lo)
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        hi[i] = (_Float16)v[i];
-        lo[i] = (_Float16)(v[i] - (float)hi[i]);
+        _Float16 h, l;
+        split(v[i], h, l);
+        hi[i] = h;
+        lo[i] = l;
     }
 }
 
@@ -266,11 +253,8 @@ __global__ __launch_bounds__(kThreads, 2) void product(Product a)
 #pragma unroll
             for (int i = 0; i < RM; ++i)
 #pragma unroll
-                for (int j = 0; j < RN; ++j) {
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[kk][i][0], r[kk][j][1], acc[i][j], 0, 0, 0);
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[kk][i][1], r[kk][j][0], acc[i][j], 0, 0, 0);
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[kk][i][0], r[kk][j][0], acc[i][j], 0, 0, 0);
-                }
+                for (int j = 0; j < RN; ++j)
+                    acc[i][j] = mfma3(l[kk][i][0], l[kk][i][1], r[kk][j][0], r[kk][j][1], acc[i][j]);
     }
 
     // the tile through LDS, so that rows and columns go out in 16-byte pieces
@@ -340,16 +324,19 @@ int pad(int v, int t) { return (v + t - 1) / t * t; }
 
 // Sides and buffers of the tiled path.
 struct Plan {
+    bool one;  // a workgroup a matrix, no workspace
     int n, m, tall, tile, np, mp, parts;
     size_t xbytes, abytes;  // planes of X and of A, all matrices
 };
 
 Plan make_plan(const wtconv_ortho_desc_t &d)
 {
-    Plan p;
+    Plan p = {};
     p.tall = d.rows > d.cols;
     p.n = (int)(p.tall ? d.cols : d.rows);
     p.m = (int)(p.tall ? d.rows : d.cols);
+    p.one = one_fits(p.n, p.m);
+    if (p.one) return p;
     const int64_t t128 = (int64_t)((p.n + 127) / 128) * ((p.m + 127) / 128) * d.batch;
     p.tile = t128 >= 256 ? 128 : 64;
     p.np = pad(p.n, p.tile);
@@ -377,6 +364,7 @@ template <typename T>
 hipError_t run(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &o, void *workspace, hipStream_t stream)
 {
     const Plan pl = make_plan(d);
+    if (pl.one) return launch_one<T>(d, o, stream);
     const unsigned batch = (unsigned)d.batch;
     const int64_t size = d.rows * d.cols;
     char *ws = (char *)workspace;
@@ -393,9 +381,7 @@ hipError_t run(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &o, void *worksp
     ortho_norm<T><<<dim3(pl.parts, batch), dim3(kThreads), 0, stream>>>(g, o.momentum, o.momentum_out, bl, size,
                                                                         parts);
     const int rp = pl.tall ? pl.mp : pl.np, cp = pl.tall ? pl.np : pl.mp;
-    // |X|, |A| and |P| (spectral) stay below 1.21, 1.47 and 3.45: times 2^14
-    // that is within fp16's 65504
-    const float S = 16384.f;
+    const float S = kScale;
     ortho_split<T><<<dim3((cp / 64) * (rp / 64), batch), dim3(kThreads), 0, stream>>>(
         g, o.momentum_out, bl, (int)d.rows, (int)d.cols, rp, cp, d.eps, S, parts, pl.parts, pl.tall ? xt[0] : x[0],
         pl.tall ? x[0] : xt[0]);
@@ -448,6 +434,7 @@ hipError_t run(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &o, void *worksp
 size_t wtc_ortho_workspace(const wtconv_ortho_desc_t &d)
 {
     const Plan p = make_plan(d);
+    if (p.one) return 0;
     return 4 * p.xbytes + 2 * p.abytes + align256(sizeof(double) * p.parts * d.batch);
 }
 

@@ -26,7 +26,9 @@ wtconv_status_t check_desc(const wtconv_ortho_desc_t *d)
 
 wtconv_status_t check_workspace(const wtconv_ortho_desc_t &d, const void *ws, size_t have)
 {
-    if (!ws || have < wtc_ortho_workspace(d)) return WTCONV_ERR_WORKSPACE;
+    const size_t need = wtc_ortho_workspace(d);
+    if (!need) return WTCONV_OK;
+    if (!ws || have < need) return WTCONV_ERR_WORKSPACE;
     return aligned_to(ws, 256) ? WTCONV_OK : WTCONV_ERR_UNSUPPORTED;
 }
 

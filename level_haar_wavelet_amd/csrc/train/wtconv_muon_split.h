@@ -1,0 +1,59 @@
+// wtconv_muon_split.h -- what the Newton-Schulz kernels share: the update that
+// the iteration starts from, the split of a value into two fp16 numbers, and
+// the matrix instruction.
+#ifndef WTCONV_MUON_SPLIT_H
+#define WTCONV_MUON_SPLIT_H
+
+#include <hip/hip_fp16.h>
+#include <hip/hip_runtime.h>
+
+#include "wtconv_muon.h"
+
+namespace wtc_muon {
+
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+
+// Factors are held as v S = hi + lo.  |X|, |A| and |P| (spectral) stay below
+// 1.21, 1.47 and 3.45: times 2^14 that is within fp16's 65504.
+constexpr float kScale = 16384.f;
+
+typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef float float16v __attribute__((ext_vector_type(16)));
+
+// The update the iteration starts from: G itself, or the Muon step's blend of
+// gradient and momentum.
+struct Blend {
+    int muon, nesterov;
+    float mu;
+};
+
+template <typename T>
+__device__ inline float blend(const Blend &b, T g, float momentum_out)
+{
+    if (!b.muon) return (float)g;
+    return b.nesterov ? fmaf(b.mu, momentum_out, (1.f - b.mu) * (float)g) : momentum_out;
+}
+
+__device__ inline void split(float v, _Float16 &hi, _Float16 &lo)
+{
+    hi = (_Float16)v;
+    lo = (_Float16)(v - (float)hi);
+}
+
+// c += l r of 32 x 32 x 16 with split factors (lo lo is below their 22 bits).
+__device__ inline float16v mfma3(const half8 &lhi, const half8 &llo, const half8 &rhi, const half8 &rlo, float16v c)
+{
+    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(lhi, rlo, c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(llo, rhi, c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(lhi, rhi, c, 0, 0, 0);
+}
+
+// The whole iteration of a matrix in one workgroup, where one can hold it.
+bool one_fits(int n, int m);
+template <typename T>
+hipError_t launch_one(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &a, hipStream_t stream);
+
+}  // namespace wtc_muon
+
+#endif  // WTCONV_MUON_SPLIT_H

@@ -17,6 +17,9 @@ SHAPES = [
     (3, 384, 25), (1, 96, 25), (4, 32, 9), (2, 200, 49), (1, 49, 49), (2, 63, 65), (1, 64, 64), (2, 66, 64),
     (1, 96, 384), (1, 127, 129), (1, 128, 128), (2, 130, 300), (1, 257, 255), (1, 100, 1999), (1, 2500, 40),
     (1, 384, 1536), (2, 512, 512), (1, 700, 333), (1, 1, 5000), (1, 4097, 2),
+    # one workgroup's limits: 256, 512, 1024 and 2048 columns of 32 rows, 512 of 64
+    (2, 27, 256), (1, 25, 257), (2, 513, 30), (1, 32, 1025), (1, 2048, 32), (1, 20, 2049), (2, 64, 256), (1, 40, 300),
+    (1, 512, 64), (1, 60, 513), (1, 65, 70),
 ]
 
 
@@ -160,7 +163,8 @@ def test_refusals_on_the_gpu():
     with pytest.raises(wt._native.WtconvError):
         wt.wtconv_orthogonalize(g[:0])
     with pytest.raises(wt._native.WtconvError):
-        wt.wtconv_orthogonalize(g, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        wt.wtconv_orthogonalize(torch.randn(80, 90, device="cuda"),
+                                workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     w, m = g.clone(), g.clone()
     with pytest.raises(TypeError):
         wt.wtconv_muon_step(w.half(), g, m, lr=0.1)

@@ -21,7 +21,7 @@ def norm_desc(n=2, c=8, h=4, w=4, groups=2, dtype=0, act=0, xl=0, yl=0, eps=1e-5
     return _native.NormDesc(n, c, h, w, groups, dtype, act, xl, yl, eps)
 
 
-def ortho_desc(batch=1, rows=8, cols=12, dtype=0, steps=5, eps=1e-7):
+def ortho_desc(batch=1, rows=80, cols=120, dtype=0, steps=5, eps=1e-7):
     return _native.OrthoDesc(batch, rows, cols, dtype, steps, eps)
 
 
@@ -107,13 +107,18 @@ def test_ortho_descriptors_are_refused(lib, kw, expect):
 
 def test_ortho_arguments_are_refused(lib):
     d = ortho_desc()
-    n = 8 * 12 * 4
+    n = 80 * 120 * 4
     need = ctypes.c_size_t(0)
     assert lib.wtconv_orthogonalize_workspace_size(None, ctypes.byref(need)) == NULL
     assert lib.wtconv_orthogonalize_workspace_size(ctypes.byref(d), None) == NULL
     assert lib.wtconv_orthogonalize_workspace_size(ctypes.byref(d), ctypes.byref(need)) == OK
     need = need.value
     big = 1 << 30
+
+    # matrices that one workgroup holds need none
+    small = ortho_desc(rows=25, cols=384)
+    size = ctypes.c_size_t(7)
+    assert lib.wtconv_orthogonalize_workspace_size(ctypes.byref(small), ctypes.byref(size)) == OK and size.value == 0
 
     def ortho(g=0x100000, out=0x200000, ws=0x1000000, nbytes=big):
         return lib.wtconv_orthogonalize(ctypes.byref(d), g, out, ws, nbytes, None)
