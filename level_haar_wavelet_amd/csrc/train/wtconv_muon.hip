@@ -167,20 +167,32 @@ struct Product {
 typedef const __attribute__((address_space(1))) void *GlobalPtr;
 typedef __attribute__((address_space(3))) void *LdsPtr;
 
-// D tile (TM x TN) = L R^T over k in steps of 32.  Four waves in 2 x 2, each
-// TM/2 x TN/2 of 32 x 32 matrix instructions.  A step's rows of L and R (128
-// bytes each) go from memory into LDS without registers between; the 16-byte
-// chunks of a row are permuted by chunk ^ (row / 2) % 8 so that the 16 rows a
-// read phase covers fall into different banks.  Two buffers: a step's reads
-// into registers come first, then the next step's loads are sent off, then its
-// 3 x (TM/64) x (TN/64) x 2 matrix instructions run.
-template <int TM, int TN, int MODE, typename T>
+// D tile (TILE x TILE) = L R^T over k in stages of 32 KB.  128 and 64: the four
+// waves in 2 x 2, each a quarter of the tile in 32 x 32 matrix instructions; 32:
+// each wave the whole tile, over a quarter of every stage, added at the end.
+// A stage's rows of L and R (128 bytes for each 32 of k) go from memory into
+// LDS without registers between; the 16-byte chunks of a row are permuted by
+// chunk ^ (row / 2) % 8 so that the 16 rows a read phase covers fall into
+// different banks.  Two buffers: a stage's reads into registers come first, then
+// the next stage's loads are sent off, then its matrix instructions run.  With
+// few workgroups a stage costs the latency of its loads, so small tiles take
+// more of k at once.
+template <int TILE>
+struct Shape {
+    static constexpr int kWavesK = TILE == 32 ? 4 : 1;          // waves along k
+    static constexpr int kBlocks = TILE == 128 ? 1 : TILE == 64 ? 2 : 4;  // KB
+    static constexpr int kSide = TILE == 32 ? 32 : TILE / 2;    // of a wave's part
+};
+
+template <int TILE, int MODE, typename T>
 __global__ __launch_bounds__(kThreads, 2) void product(Product a)
 {
-    constexpr int RM = TM / 64, RN = TN / 64;       // 32-row blocks of a wave
-    constexpr int kStage = (TM + TN) * 128;         // bytes of one buffer
-    constexpr int kPitch = TN + 1;                  // of the result's tile in LDS
-    constexpr int kResult = TM * kPitch * 4;
+    using Sh = Shape<TILE>;
+    constexpr int KB = Sh::kBlocks, KW = KB / Sh::kWavesK;  // 32-blocks of k: of a stage, of a wave
+    constexpr int RB = Sh::kSide / 32;                      // 32-row blocks of a wave
+    constexpr int kBlock = 2 * TILE * 128, kStage = KB * kBlock;  // bytes
+    constexpr int kPitch = TILE + 1;                        // of the result's tile in LDS
+    constexpr int kResult = TILE * kPitch * 4 * Sh::kWavesK;
     __shared__ __attribute__((aligned(128))) char lds[2 * kStage > kResult ? 2 * kStage : kResult];
 
     // workgroups go to the 8 dies in turn: give each die neighbouring tiles
@@ -199,81 +211,106 @@ __global__ __launch_bounds__(kThreads, 2) void product(Product a)
         tj = tile - ti * (ti + 1) / 2;
     } else {
         // bands of 8 tile rows, so that the tiles in flight share operands
-        const int nj = a.rp / TN, ni = a.lp / TM, band = tile / (8 * nj), h = ni - 8 * band < 8 ? ni - 8 * band : 8;
-        const int in = tile - band * 8 * nj;
+        const int nj = a.rp / TILE, ni = a.lp / TILE, band = tile / (8 * nj);
+        const int h = ni - 8 * band < 8 ? ni - 8 * band : 8, in = tile - band * 8 * nj;
         ti = band * 8 + in % h;
         tj = in / h;
     }
     const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
     const int64_t ldb = (int64_t)a.kp * 4;  // bytes of a row
-    const char *L = (const char *)a.L + ((int64_t)z * a.lp + ti * TM) * ldb;
-    const char *R = (const char *)a.R + ((int64_t)z * a.rp + tj * TN) * ldb;
+    const char *L = (const char *)a.L + ((int64_t)z * a.lp + ti * TILE) * ldb;
+    const char *R = (const char *)a.R + ((int64_t)z * a.rp + tj * TILE) * ldb;
 
-    // this lane's source of each load: 8 rows a load, row lane / 8 of them
-    constexpr int kLoads = (TM + TN) / 32;  // per wave
+    // this lane's source of each load of a block of k: 8 rows a load, row
+    // lane / 8 of them
+    constexpr int kLoads = 2 * TILE / 32;  // per wave
     const char *src[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
         const int row = (wave * kLoads + i) * 8 + (lane >> 3);
         const int chunk = (lane & 7) ^ ((row >> 1) & 7);
-        src[i] = (row < TM ? L + row * ldb : R + (row - TM) * ldb) + chunk * 16;
+        src[i] = (row < TILE ? L + row * ldb : R + (row - TILE) * ldb) + chunk * 16;
     }
-    auto load = [&](int k, int buf) {
+    const int blocks = a.kp / 32, stages = (blocks + KB - 1) / KB;
+    auto load = [&](int s) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            __builtin_amdgcn_global_load_lds((GlobalPtr)(src[i] + (int64_t)k * 128),
-                                             (LdsPtr)(lds + buf * kStage + (wave * kLoads + i) * 1024), 16, 0, 0);
+        for (int b = 0; b < KB; ++b)
+            if (KB == 1 || s * KB + b < blocks)
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i)
+                    __builtin_amdgcn_global_load_lds(
+                        (GlobalPtr)(src[i] + (int64_t)(s * KB + b) * 128),
+                        (LdsPtr)(lds + (s & 1) * kStage + b * kBlock + (wave * kLoads + i) * 1024), 16, 0, 0);
     };
-    auto frag = [&](int buf, int row, int chunk) {
-        return *(const half8 *)(lds + buf * kStage + row * 128 + ((chunk ^ ((row >> 1) & 7)) * 16));
+    auto frag = [&](int s, int b, int row, int chunk) {
+        return *(const half8 *)(lds + (s & 1) * kStage + b * kBlock + row * 128 + ((chunk ^ ((row >> 1) & 7)) * 16));
     };
 
-    float16v acc[RM][RN] = {};
-    const int wi = (wave >> 1) * (TM / 2), wj = TM + (wave & 1) * (TN / 2), lr = lane & 31, lc = lane >> 5;
-    const int steps = a.kp / 32;
-    load(0, 0);
-    for (int k = 0; k < steps; ++k) {
+    float16v acc[RB][RB] = {};
+    const int wi = Sh::kWavesK > 1 ? 0 : (wave >> 1) * Sh::kSide, wj = Sh::kWavesK > 1 ? 0 : (wave & 1) * Sh::kSide;
+    const int b0 = Sh::kWavesK > 1 ? wave * KW : 0, lr = lane & 31, lc = lane >> 5;
+    load(0);
+    for (int s = 0; s < stages; ++s) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
-        half8 l[2][RM][2], r[2][RN][2];  // [k half][block][hi, lo]
+        half8 l[KW][2][RB][2], r[KW][2][RB][2];  // [block of k][half][block of rows][hi, lo]
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
+        for (int b = 0; b < KW; ++b)
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
+            for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int i = 0; i < RM; ++i) l[kk][i][p] = frag(k & 1, wi + i * 32 + lr, p * 4 + kk * 2 + lc);
+                for (int p = 0; p < 2; ++p)
 #pragma unroll
-                for (int j = 0; j < RN; ++j) r[kk][j][p] = frag(k & 1, wj + j * 32 + lr, p * 4 + kk * 2 + lc);
-            }
+                    for (int i = 0; i < RB; ++i) {
+                        l[b][kk][i][p] = frag(s, b0 + b, wi + i * 32 + lr, p * 4 + kk * 2 + lc);
+                        r[b][kk][i][p] = frag(s, b0 + b, TILE + wj + i * 32 + lr, p * 4 + kk * 2 + lc);
+                    }
         __builtin_amdgcn_sched_barrier(0);
-        if (k + 1 < steps) load(k + 1, (k + 1) & 1);
+        if (s + 1 < stages) load(s + 1);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
+        for (int b = 0; b < KW; ++b) {
+            if (KB > 1 && s * KB + b0 + b >= blocks) continue;  // the last stage's missing blocks
 #pragma unroll
-            for (int i = 0; i < RM; ++i)
+            for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int j = 0; j < RN; ++j)
-                    acc[i][j] = mfma3(l[kk][i][0], l[kk][i][1], r[kk][j][0], r[kk][j][1], acc[i][j]);
+                for (int i = 0; i < RB; ++i)
+#pragma unroll
+                    for (int j = 0; j < RB; ++j)
+                        acc[i][j] = mfma3(l[b][kk][i][0], l[b][kk][i][1], r[b][kk][j][0], r[b][kk][j][1], acc[i][j]);
+        }
     }
 
     // the tile through LDS, so that rows and columns go out in 16-byte pieces
     __syncthreads();
     float *res = (float *)lds;
+    {
+        float *own = res + (Sh::kWavesK > 1 ? wave * TILE * kPitch : 0);
 #pragma unroll
-    for (int i = 0; i < RM; ++i)
+        for (int i = 0; i < RB; ++i)
 #pragma unroll
-        for (int j = 0; j < RN; ++j)
+            for (int j = 0; j < RB; ++j)
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
-                res[(wi + i * 32 + 8 * (q >> 2) + 4 * lc + (q & 3)) * kPitch + wj - TM + j * 32 + lr] = acc[i][j][q];
+                for (int q = 0; q < 16; ++q)
+                    own[(wi + i * 32 + 8 * (q >> 2) + 4 * lc + (q & 3)) * kPitch + wj + j * 32 + lr] = acc[i][j][q];
+    }
     __syncthreads();
+    if (Sh::kWavesK > 1) {
+        for (int e = t; e < TILE * TILE; e += kThreads) {
+            const int o = e / TILE * kPitch + e % TILE;
+            float v = res[o];
+#pragma unroll
+            for (int w = 1; w < Sh::kWavesK; ++w) v += res[w * TILE * kPitch + o];
+            res[o] = v;
+        }
+        __syncthreads();
+    }
 
-    const int i0 = ti * TM, j0 = tj * TN;
+    const int i0 = ti * TILE, j0 = tj * TILE;
     if (MODE == kFinal) {
         const int64_t base = (int64_t)z * a.n * a.m;
-        for (int e = t; e < TM * TN; e += kThreads) {
-            const int i = a.tall ? e % TM : e / TN, j = a.tall ? e / TM : e % TN;
+        for (int e = t; e < TILE * TILE; e += kThreads) {
+            const int i = a.tall ? e % TILE : e / TILE, j = a.tall ? e / TILE : e % TILE;
             if (i0 + i >= a.n || j0 + j >= a.m) continue;
             const float v = res[i * kPitch + j] * a.f;
             const int64_t o = base + (a.tall ? (int64_t)(j0 + j) * a.n + i0 + i : (int64_t)(i0 + i) * a.m + j0 + j);
@@ -286,8 +323,8 @@ __global__ __launch_bounds__(kThreads, 2) void product(Product a)
     }
     _Float16 *D = a.D + (int64_t)z * a.lp * a.rp * 2;
     const _Float16 *A = a.L + (int64_t)z * a.lp * a.kp * 2;
-    for (int e = t; e < TM * TN / 8; e += kThreads) {
-        const int i = e / (TN / 8), j = (e % (TN / 8)) * 8;
+    for (int e = t; e < TILE * TILE / 8; e += kThreads) {
+        const int i = e / (TILE / 8), j = (e % (TILE / 8)) * 8;
         float v[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] = res[i * kPitch + j + q] * a.f;
@@ -309,8 +346,8 @@ __global__ __launch_bounds__(kThreads, 2) void product(Product a)
     if (!Dt) return;
     if (MODE == kPoly) __syncthreads();
     Dt += (int64_t)z * a.lp * a.rp * 2;
-    for (int e = t; e < TM * TN / 8; e += kThreads) {
-        const int j = e % TN, i = (e / TN) * 8;
+    for (int e = t; e < TILE * TILE / 8; e += kThreads) {
+        const int j = e % TILE, i = (e / TILE) * 8;
         float v[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] = res[(i + q) * kPitch + j] * (MODE == kPoly ? 1.f : a.f);
@@ -325,9 +362,22 @@ int pad(int v, int t) { return (v + t - 1) / t * t; }
 // Sides and buffers of the tiled path.
 struct Plan {
     bool one;  // a workgroup a matrix, no workspace
-    int n, m, tall, tile, np, mp, parts;
+    int n, m, tall, tile_sym, tile_x, np, mp, parts;
     size_t xbytes, abytes;  // planes of X and of A, all matrices
 };
+
+// The largest tile that still makes enough workgroups (us, ortho fp32 in a
+// graph, tiles 32 / 64 / 128 for both kinds of products): 384x1536 145 / 213 /
+// 398, 1024x1024 247 / 260 / 464, 4x1024x1024 690 / 545 / 516, 2048x2048 1286 /
+// 965 / 870.
+int pick_tile(int rows, int cols, bool sym, int64_t batch)
+{
+    for (int t = 128; t > 32; t /= 2) {
+        const int64_t ni = (rows + t - 1) / t, nj = (cols + t - 1) / t;
+        if ((sym ? ni * (ni + 1) / 2 : ni * nj) * batch >= (t == 128 ? 128 : 192)) return t;
+    }
+    return 32;
+}
 
 Plan make_plan(const wtconv_ortho_desc_t &d)
 {
@@ -337,10 +387,12 @@ Plan make_plan(const wtconv_ortho_desc_t &d)
     p.m = (int)(p.tall ? d.rows : d.cols);
     p.one = one_fits(p.n, p.m);
     if (p.one) return p;
-    const int64_t t128 = (int64_t)((p.n + 127) / 128) * ((p.m + 127) / 128) * d.batch;
-    p.tile = t128 >= 256 ? 128 : 64;
-    p.np = pad(p.n, p.tile);
-    p.mp = pad(p.m, p.tile);
+    // rows and columns are padded to the largest tile in use
+    p.tile_sym = pick_tile(p.n, p.n, true, d.batch);
+    p.tile_x = pick_tile(p.n, p.m, false, d.batch);
+    const int t = p.tile_sym > p.tile_x ? p.tile_sym : p.tile_x;
+    p.np = pad(p.n, t > 64 ? t : 64);
+    p.mp = pad(p.m, t > 64 ? t : 64);
     p.xbytes = align256((size_t)p.np * p.mp * 4 * d.batch);
     p.abytes = align256((size_t)p.np * p.np * 4 * d.batch);
     const int64_t want = ((int64_t)p.n * p.m + 8 * kThreads - 1) / (8 * kThreads);
@@ -351,13 +403,15 @@ Plan make_plan(const wtconv_ortho_desc_t &d)
 template <int MODE, typename T = float>
 void launch_product(const Plan &pl, Product a, hipStream_t stream)
 {
-    const int ni = a.lp / pl.tile, nj = a.rp / pl.tile;
+    const int tile = a.sym ? pl.tile_sym : pl.tile_x, ni = a.lp / tile, nj = a.rp / tile;
     a.tiles = a.sym ? ni * (ni + 1) / 2 : ni * nj;
     const dim3 grid((unsigned)(a.tiles * a.batch));
-    if (pl.tile == 128)
-        product<128, 128, MODE, T><<<grid, dim3(kThreads), 0, stream>>>(a);
+    if (tile == 128)
+        product<128, MODE, T><<<grid, dim3(kThreads), 0, stream>>>(a);
+    else if (tile == 64)
+        product<64, MODE, T><<<grid, dim3(kThreads), 0, stream>>>(a);
     else
-        product<64, 64, MODE, T><<<grid, dim3(kThreads), 0, stream>>>(a);
+        product<32, MODE, T><<<grid, dim3(kThreads), 0, stream>>>(a);
 }
 
 template <typename T>
