@@ -154,6 +154,10 @@ struct Product {
     int lp, rp, kp;          // padded sides
     int sym;                 // D is symmetric: tiles on and below the diagonal only, Dt = D
     int tiles, batch;        // tiles of a matrix; matrices
+    // of all tiles the first `full` are a workgroup's each; the others are cut
+    // into `slices` along k of `cut` 32-blocks, whose sums go to `part`
+    int full, slices, cut;
+    float4 *part;
     float f;                 // from the accumulator to D's scale
     float a, b, c;           // kPoly: b includes the change of scale
     // kFinal: element (i, j) of the product, i < n, j < m, is the output's
@@ -184,26 +188,12 @@ struct Shape {
     static constexpr int kSide = TILE == 32 ? 32 : TILE / 2;    // of a wave's part
 };
 
-template <int TILE, int MODE, typename T>
-__global__ __launch_bounds__(kThreads, 2) void product(Product a)
+// Matrix, tile row and tile column of tile g of all matrices.
+template <int TILE>
+__device__ inline void place(const Product &a, int g, int &z, int &ti, int &tj)
 {
-    using Sh = Shape<TILE>;
-    constexpr int KB = Sh::kBlocks, KW = KB / Sh::kWavesK;  // 32-blocks of k: of a stage, of a wave
-    constexpr int RB = Sh::kSide / 32;                      // 32-row blocks of a wave
-    constexpr int kBlock = 2 * TILE * 128, kStage = KB * kBlock;  // bytes
-    constexpr int kPitch = TILE + 1;                        // of the result's tile in LDS
-    constexpr int kResult = TILE * kPitch * 4 * Sh::kWavesK;
-    __shared__ __attribute__((aligned(128))) char lds[2 * kStage > kResult ? 2 * kStage : kResult];
-
-    // workgroups go to the 8 dies in turn: give each die neighbouring tiles
-    const int total = a.tiles * a.batch;
-    int id = blockIdx.x;
-    {
-        const int per = total / 8, rest = total % 8, die = id % 8, at = id / 8;
-        id = die * per + (die < rest ? die : rest) + at;
-    }
-    const int z = id / a.tiles;
-    int tile = id % a.tiles, ti, tj;
+    z = g / a.tiles;
+    const int tile = g % a.tiles;
     if (a.sym) {
         ti = (int)((sqrtf(8.f * tile + 1.f) - 1.f) * 0.5f);
         while ((ti + 1) * (ti + 2) / 2 <= tile) ++ti;
@@ -216,96 +206,20 @@ __global__ __launch_bounds__(kThreads, 2) void product(Product a)
         ti = band * 8 + in % h;
         tj = in / h;
     }
-    const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
-    const int64_t ldb = (int64_t)a.kp * 4;  // bytes of a row
-    const char *L = (const char *)a.L + ((int64_t)z * a.lp + ti * TILE) * ldb;
-    const char *R = (const char *)a.R + ((int64_t)z * a.rp + tj * TILE) * ldb;
+}
 
-    // this lane's source of each load of a block of k: 8 rows a load, row
-    // lane / 8 of them
-    constexpr int kLoads = 2 * TILE / 32;  // per wave
-    const char *src[kLoads];
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        const int row = (wave * kLoads + i) * 8 + (lane >> 3);
-        const int chunk = (lane & 7) ^ ((row >> 1) & 7);
-        src[i] = (row < TILE ? L + row * ldb : R + (row - TILE) * ldb) + chunk * 16;
-    }
-    const int blocks = a.kp / 32, stages = (blocks + KB - 1) / KB;
-    auto load = [&](int s) {
-#pragma unroll
-        for (int b = 0; b < KB; ++b)
-            if (KB == 1 || s * KB + b < blocks)
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i)
-                    __builtin_amdgcn_global_load_lds(
-                        (GlobalPtr)(src[i] + (int64_t)(s * KB + b) * 128),
-                        (LdsPtr)(lds + (s & 1) * kStage + b * kBlock + (wave * kLoads + i) * 1024), 16, 0, 0);
-    };
-    auto frag = [&](int s, int b, int row, int chunk) {
-        return *(const half8 *)(lds + (s & 1) * kStage + b * kBlock + row * 128 + ((chunk ^ ((row >> 1) & 7)) * 16));
-    };
+template <int TILE>
+struct Lds {
+    static constexpr int kPitch = TILE + 1;  // of the result's tile
+    static constexpr int kResult = TILE * kPitch * 4;
+};
 
-    float16v acc[RB][RB] = {};
-    const int wi = Sh::kWavesK > 1 ? 0 : (wave >> 1) * Sh::kSide, wj = Sh::kWavesK > 1 ? 0 : (wave & 1) * Sh::kSide;
-    const int b0 = Sh::kWavesK > 1 ? wave * KW : 0, lr = lane & 31, lc = lane >> 5;
-    load(0);
-    for (int s = 0; s < stages; ++s) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        half8 l[KW][2][RB][2], r[KW][2][RB][2];  // [block of k][half][block of rows][hi, lo]
-#pragma unroll
-        for (int b = 0; b < KW; ++b)
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-#pragma unroll
-                    for (int i = 0; i < RB; ++i) {
-                        l[b][kk][i][p] = frag(s, b0 + b, wi + i * 32 + lr, p * 4 + kk * 2 + lc);
-                        r[b][kk][i][p] = frag(s, b0 + b, TILE + wj + i * 32 + lr, p * 4 + kk * 2 + lc);
-                    }
-        __builtin_amdgcn_sched_barrier(0);
-        if (s + 1 < stages) load(s + 1);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int b = 0; b < KW; ++b) {
-            if (KB > 1 && s * KB + b0 + b >= blocks) continue;  // the last stage's missing blocks
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int i = 0; i < RB; ++i)
-#pragma unroll
-                    for (int j = 0; j < RB; ++j)
-                        acc[i][j] = mfma3(l[b][kk][i][0], l[b][kk][i][1], r[b][kk][j][0], r[b][kk][j][1], acc[i][j]);
-        }
-    }
-
-    // the tile through LDS, so that rows and columns go out in 16-byte pieces
-    __syncthreads();
-    float *res = (float *)lds;
-    {
-        float *own = res + (Sh::kWavesK > 1 ? wave * TILE * kPitch : 0);
-#pragma unroll
-        for (int i = 0; i < RB; ++i)
-#pragma unroll
-            for (int j = 0; j < RB; ++j)
-#pragma unroll
-                for (int q = 0; q < 16; ++q)
-                    own[(wi + i * 32 + 8 * (q >> 2) + 4 * lc + (q & 3)) * kPitch + wj + j * 32 + lr] = acc[i][j][q];
-    }
-    __syncthreads();
-    if (Sh::kWavesK > 1) {
-        for (int e = t; e < TILE * TILE; e += kThreads) {
-            const int o = e / TILE * kPitch + e % TILE;
-            float v = res[o];
-#pragma unroll
-            for (int w = 1; w < Sh::kWavesK; ++w) v += res[w * TILE * kPitch + o];
-            res[o] = v;
-        }
-        __syncthreads();
-    }
-
+// The result's tile in LDS (rows of kPitch) to where it goes.
+template <int TILE, int MODE, typename T>
+__device__ inline void finish(const Product &a, float *res, int z, int ti, int tj)
+{
+    constexpr int kPitch = Lds<TILE>::kPitch;
+    const int t = threadIdx.x;
     const int i0 = ti * TILE, j0 = tj * TILE;
     if (MODE == kFinal) {
         const int64_t base = (int64_t)z * a.n * a.m;
@@ -355,29 +269,253 @@ __global__ __launch_bounds__(kThreads, 2) void product(Product a)
     }
 }
 
+// A wave's part of the tile in matrix-instruction order to LDS, and the waves'
+// sums along k, so that rows and columns go out in 16-byte pieces.
+template <int TILE>
+__device__ inline void to_lds(const float16v (&acc)[Shape<TILE>::kSide / 32][Shape<TILE>::kSide / 32], float *res)
+{
+    using Sh = Shape<TILE>;
+    constexpr int RB = Sh::kSide / 32, kPitch = Lds<TILE>::kPitch;
+    const int t = threadIdx.x, wave = t >> 6, lane = t & 63, lr = lane & 31, lc = lane >> 5;
+    const int wi = Sh::kWavesK > 1 ? 0 : (wave >> 1) * Sh::kSide, wj = Sh::kWavesK > 1 ? 0 : (wave & 1) * Sh::kSide;
+    float *own = res + (Sh::kWavesK > 1 ? wave * TILE * kPitch : 0);
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < RB; ++j)
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                own[(wi + i * 32 + 8 * (q >> 2) + 4 * lc + (q & 3)) * kPitch + wj + j * 32 + lr] = acc[i][j][q];
+    __syncthreads();
+    if (Sh::kWavesK > 1) {
+        for (int e = t; e < TILE * TILE; e += kThreads) {
+            const int o = e / TILE * kPitch + e % TILE;
+            float v = res[o];
+#pragma unroll
+            for (int w = 1; w < Sh::kWavesK; ++w) v += res[w * TILE * kPitch + o];
+            res[o] = v;
+        }
+        __syncthreads();
+    }
+}
+
+template <int TILE, int MODE, typename T>
+__global__ __launch_bounds__(kThreads, 2) void product(Product a)
+{
+    using Sh = Shape<TILE>;
+    constexpr int KB = Sh::kBlocks, KW = KB / Sh::kWavesK;  // 32-blocks of k: of a stage, of a wave
+    constexpr int RB = Sh::kSide / 32;                      // 32-row blocks of a wave
+    constexpr int kBlock = 2 * TILE * 128, kStage = KB * kBlock;  // bytes
+    constexpr int kResult = Lds<TILE>::kResult * Sh::kWavesK;
+    __shared__ __attribute__((aligned(128))) char lds[2 * kStage > kResult ? 2 * kStage : kResult];
+
+    int g = blockIdx.x, slice = -1, z, ti, tj;
+    if (g < a.full) {
+        // workgroups go to the 8 dies in turn: give each die neighbouring tiles
+        const int per = a.full / 8, rest = a.full % 8, die = g % 8;
+        g = die * per + (die < rest ? die : rest) + g / 8;
+    } else {
+        slice = (g - a.full) % a.slices;
+        g = a.full + (g - a.full) / a.slices;
+    }
+    place<TILE>(a, g, z, ti, tj);
+    const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
+    const int64_t ldb = (int64_t)a.kp * 4;  // bytes of a row
+    const char *L = (const char *)a.L + ((int64_t)z * a.lp + ti * TILE) * ldb;
+    const char *R = (const char *)a.R + ((int64_t)z * a.rp + tj * TILE) * ldb;
+
+    const int64_t k0_bytes = slice < 0 ? 0 : (int64_t)slice * a.cut * 128;
+    // this lane's source of each load of a block of k: 8 rows a load, row
+    // lane / 8 of them
+    constexpr int kLoads = 2 * TILE / 32;  // per wave
+    const char *src[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int row = (wave * kLoads + i) * 8 + (lane >> 3);
+        const int chunk = (lane & 7) ^ ((row >> 1) & 7);
+        src[i] = (row < TILE ? L + row * ldb : R + (row - TILE) * ldb) + chunk * 16 + k0_bytes;
+    }
+    const int all = a.kp / 32, k0 = slice < 0 ? 0 : slice * a.cut;
+    const int blocks = slice < 0 ? all : all - k0 < a.cut ? all - k0 : a.cut, stages = (blocks + KB - 1) / KB;
+    auto load = [&](int s) {
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+            if (KB == 1 || s * KB + b < blocks)
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i)
+                    __builtin_amdgcn_global_load_lds(
+                        (GlobalPtr)(src[i] + (int64_t)(s * KB + b) * 128),
+                        (LdsPtr)(lds + (s & 1) * kStage + b * kBlock + (wave * kLoads + i) * 1024), 16, 0, 0);
+    };
+    auto frag = [&](int s, int b, int row, int chunk) {
+        return *(const half8 *)(lds + (s & 1) * kStage + b * kBlock + row * 128 + ((chunk ^ ((row >> 1) & 7)) * 16));
+    };
+
+    float16v acc[RB][RB] = {};
+    const int wi = Sh::kWavesK > 1 ? 0 : (wave >> 1) * Sh::kSide, wj = Sh::kWavesK > 1 ? 0 : (wave & 1) * Sh::kSide;
+    const int b0 = Sh::kWavesK > 1 ? wave * KW : 0, lr = lane & 31, lc = lane >> 5;
+    load(0);
+    for (int s = 0; s < stages; ++s) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        half8 l[KW][2][RB][2], r[KW][2][RB][2];  // [block of k][half][block of rows][hi, lo]
+#pragma unroll
+        for (int b = 0; b < KW; ++b)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int i = 0; i < RB; ++i) {
+                        l[b][kk][i][p] = frag(s, b0 + b, wi + i * 32 + lr, p * 4 + kk * 2 + lc);
+                        r[b][kk][i][p] = frag(s, b0 + b, TILE + wj + i * 32 + lr, p * 4 + kk * 2 + lc);
+                    }
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + 1 < stages) load(s + 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int b = 0; b < KW; ++b) {
+            if (KB > 1 && s * KB + b0 + b >= blocks) continue;  // the last stage's missing blocks
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+#pragma unroll
+                    for (int j = 0; j < RB; ++j)
+                        acc[i][j] = mfma3(l[b][kk][i][0], l[b][kk][i][1], r[b][kk][j][0], r[b][kk][j][1], acc[i][j]);
+        }
+    }
+
+    if (slice >= 0) {
+        float4 *p = a.part + ((int64_t)(g - a.full) * a.slices + slice) * (RB * RB * 4 * kThreads) + t;
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int j = 0; j < RB; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    p[((i * RB + j) * 4 + q) * kThreads] = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                                                                       acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+        return;
+    }
+    __syncthreads();
+    float *res = (float *)lds;
+    to_lds<TILE>(acc, res);
+    finish<TILE, MODE, T>(a, res, z, ti, tj);
+}
+
+// Adds the slices of the tiles that were cut along k, in order, and finishes
+// them; one workgroup a tile.
+template <int TILE, int MODE, typename T>
+__global__ __launch_bounds__(kThreads) void join(Product a)
+{
+    using Sh = Shape<TILE>;
+    constexpr int RB = Sh::kSide / 32;
+    __shared__ __attribute__((aligned(128))) char lds[Lds<TILE>::kResult * Sh::kWavesK];
+    int z, ti, tj;
+    place<TILE>(a, a.full + blockIdx.x, z, ti, tj);
+    float16v acc[RB][RB] = {};
+    const float4 *p = a.part + (int64_t)blockIdx.x * a.slices * (RB * RB * 4 * kThreads) + threadIdx.x;
+#pragma unroll 2
+    for (int s = 0; s < a.slices; ++s, p += RB * RB * 4 * kThreads)
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int j = 0; j < RB; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float4 v = p[((i * RB + j) * 4 + q) * kThreads];
+                    acc[i][j][4 * q] += v.x;
+                    acc[i][j][4 * q + 1] += v.y;
+                    acc[i][j][4 * q + 2] += v.z;
+                    acc[i][j][4 * q + 3] += v.w;
+                }
+    to_lds<TILE>(acc, (float *)lds);
+    finish<TILE, MODE, T>(a, (float *)lds, z, ti, tj);
+}
+
 // ---- Host ----------------------------------------------------------------------
 
+// How the tiles of a product are dealt to workgroups.  kSlots workgroups run at
+// once (two a compute unit).  A last round of few tiles, or an only round, may
+// be cut along k so that it fills them: 528 tiles of 4096^3 took 1.42 rounds
+// of 512 uncut (268 us a product, 222 cut).
+struct Deal {
+    int tile, tiles, full, slices, cut;
+    size_t bytes;  // of the slices' sums
+    double us;     // what it should take
+};
+
+constexpr int kSlots = 512;
+
+// Of a tile of 32, 64, 128: us of 32 of k, alone on a compute unit and with a
+// second workgroup there; us of a workgroup's start and end; us for adding a
+// slice of a tile.  Measured on products of 96 to 4096.
+constexpr double kAlone[] = {0.15, 0.33, 1.1}, kShared[] = {0.20, 0.46, 1.45}, kEnds[] = {2.0, 2.5, 6.0},
+                 kSlice[] = {0.25, 0.25, 2.5}, kLaunch = 4.0;
+
+double round_us(int64_t groups, int blocks, int t)
+{
+    const int64_t rounds = groups / kSlots, rest = groups % kSlots;
+    double us = (double)rounds * (blocks * kShared[t] + kEnds[t]);
+    if (rest) us += blocks * (rest > kSlots / 2 ? kShared[t] : kAlone[t]) + kEnds[t];
+    return us;
+}
+
+// The tile and the cut that should take the least time, for matrices of
+// rows x k by k x cols before padding.
+Deal make_deal(int rows, int cols, int k, bool sym, int64_t batch)
+{
+    Deal best = {};
+    const int blocks = (k + 31) / 32;
+    for (int t = 0; t < 3; ++t) {
+        const int tile = 32 << t;
+        const int64_t ni = (rows + tile - 1) / tile, nj = (cols + tile - 1) / tile;
+        const int64_t all = (sym ? ni * (ni + 1) / 2 : ni * nj) * batch, rest = all % kSlots;
+        for (int want = 1; want <= 8; ++want) {
+            if (want > 1 && (!rest || rest * want > kSlots || blocks / want < 4)) break;
+            Deal d = {};
+            d.tile = tile;
+            d.full = (int)(want > 1 ? all - rest : all);
+            d.cut = (blocks + want - 1) / want;
+            d.slices = (blocks + d.cut - 1) / d.cut;
+            d.us = kLaunch + round_us(d.full, blocks, t);
+            if (want > 1) {
+                d.us += round_us(rest * d.slices, d.cut, t) + kLaunch + d.slices * kSlice[t];
+                d.bytes = align256((size_t)rest * d.slices * tile * tile * 4 * (tile == 32 ? 4 : 1));
+            }
+            if (!best.tile || d.us < best.us) best = d;
+        }
+    }
+    return best;
+}
+
 int pad(int v, int t) { return (v + t - 1) / t * t; }
+
+// The same deal on the padded sides (a multiple of its tile).
+void fit_deal(Deal &d, int lp, int rp, int kp, bool sym, int64_t batch)
+{
+    const int64_t ni = lp / d.tile, nj = rp / d.tile;
+    d.tiles = (int)(sym ? ni * (ni + 1) / 2 : ni * nj);
+    const int64_t all = d.tiles * batch;
+    if (d.slices < 2) {
+        d.full = (int)all;
+        return;
+    }
+    const int blocks = kp / 32, rest = (int)(all % kSlots);
+    d.full = (int)(all - rest);
+    d.cut = (blocks + d.slices - 1) / d.slices;
+    d.slices = (blocks + d.cut - 1) / d.cut;
+    d.bytes = align256((size_t)rest * d.slices * d.tile * d.tile * 4 * (d.tile == 32 ? 4 : 1));
+}
 
 // Sides and buffers of the tiled path.
 struct Plan {
     bool one;  // a workgroup a matrix, no workspace
-    int n, m, tall, tile_sym, tile_x, np, mp, parts;
-    size_t xbytes, abytes;  // planes of X and of A, all matrices
+    int n, m, tall, np, mp, parts;
+    Deal gram, poly, apply;   // the three products of a step
+    size_t xbytes, abytes, part;  // planes of X and of A, slices' sums
 };
-
-// The largest tile that still makes enough workgroups (us, ortho fp32 in a
-// graph, tiles 32 / 64 / 128 for both kinds of products): 384x1536 145 / 213 /
-// 398, 1024x1024 247 / 260 / 464, 4x1024x1024 690 / 545 / 516, 2048x2048 1286 /
-// 965 / 870.
-int pick_tile(int rows, int cols, bool sym, int64_t batch)
-{
-    for (int t = 128; t > 32; t /= 2) {
-        const int64_t ni = (rows + t - 1) / t, nj = (cols + t - 1) / t;
-        if ((sym ? ni * (ni + 1) / 2 : ni * nj) * batch >= (t == 128 ? 128 : 192)) return t;
-    }
-    return 32;
-}
 
 Plan make_plan(const wtconv_ortho_desc_t &d)
 {
@@ -387,12 +525,18 @@ Plan make_plan(const wtconv_ortho_desc_t &d)
     p.m = (int)(p.tall ? d.rows : d.cols);
     p.one = one_fits(p.n, p.m);
     if (p.one) return p;
-    // rows and columns are padded to the largest tile in use
-    p.tile_sym = pick_tile(p.n, p.n, true, d.batch);
-    p.tile_x = pick_tile(p.n, p.m, false, d.batch);
-    const int t = p.tile_sym > p.tile_x ? p.tile_sym : p.tile_x;
-    p.np = pad(p.n, t > 64 ? t : 64);
-    p.mp = pad(p.m, t > 64 ? t : 64);
+    p.gram = make_deal(p.n, p.n, p.m, true, d.batch);
+    p.poly = make_deal(p.n, p.n, p.n, true, d.batch);
+    p.apply = make_deal(p.n, p.m, p.n, false, d.batch);
+    // sides are padded to the largest tile in use, and to the 64 of ortho_split
+    const int big = p.gram.tile == 128 || p.poly.tile == 128 || p.apply.tile == 128 ? 128 : 64;
+    p.np = pad(p.n, big);
+    p.mp = pad(p.m, big);
+    fit_deal(p.gram, p.np, p.np, p.mp, true, d.batch);
+    fit_deal(p.poly, p.np, p.np, p.np, true, d.batch);
+    fit_deal(p.apply, p.np, p.mp, p.np, false, d.batch);
+    p.part = p.gram.bytes > p.poly.bytes ? p.gram.bytes : p.poly.bytes;
+    if (p.part < p.apply.bytes) p.part = p.apply.bytes;
     p.xbytes = align256((size_t)p.np * p.mp * 4 * d.batch);
     p.abytes = align256((size_t)p.np * p.np * 4 * d.batch);
     const int64_t want = ((int64_t)p.n * p.m + 8 * kThreads - 1) / (8 * kThreads);
@@ -400,18 +544,27 @@ Plan make_plan(const wtconv_ortho_desc_t &d)
     return p;
 }
 
-template <int MODE, typename T = float>
-void launch_product(const Plan &pl, Product a, hipStream_t stream)
+template <int TILE, int MODE, typename T>
+void launch_tile(const Deal &d, const Product &a, hipStream_t stream)
 {
-    const int tile = a.sym ? pl.tile_sym : pl.tile_x, ni = a.lp / tile, nj = a.rp / tile;
-    a.tiles = a.sym ? ni * (ni + 1) / 2 : ni * nj;
-    const dim3 grid((unsigned)(a.tiles * a.batch));
-    if (tile == 128)
-        product<128, MODE, T><<<grid, dim3(kThreads), 0, stream>>>(a);
-    else if (tile == 64)
-        product<64, MODE, T><<<grid, dim3(kThreads), 0, stream>>>(a);
+    const int rest = a.tiles * a.batch - a.full;
+    product<TILE, MODE, T><<<dim3((unsigned)(a.full + rest * a.slices)), dim3(kThreads), 0, stream>>>(a);
+    if (rest) join<TILE, MODE, T><<<dim3((unsigned)rest), dim3(kThreads), 0, stream>>>(a);
+}
+
+template <int MODE, typename T = float>
+void launch_product(const Deal &d, Product a, hipStream_t stream)
+{
+    a.tiles = d.tiles;
+    a.full = d.full;
+    a.slices = d.slices;
+    a.cut = d.cut;
+    if (d.tile == 128)
+        launch_tile<128, MODE, T>(d, a, stream);
+    else if (d.tile == 64)
+        launch_tile<64, MODE, T>(d, a, stream);
     else
-        product<32, MODE, T><<<grid, dim3(kThreads), 0, stream>>>(a);
+        launch_tile<32, MODE, T>(d, a, stream);
 }
 
 template <typename T>
@@ -430,6 +583,7 @@ hipError_t run(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &o, void *worksp
     }
     _Float16 *A = (_Float16 *)ws, *P = (_Float16 *)(ws += pl.abytes);
     double *parts = (double *)(ws += pl.abytes);
+    float4 *part = (float4 *)(ws += align256(sizeof(double) * pl.parts * d.batch));
     const Blend bl = {o.hyper != nullptr, o.hyper ? o.hyper->nesterov : 0, o.hyper ? o.hyper->momentum : 0.f};
     const T *g = (const T *)o.g;
     ortho_norm<T><<<dim3(pl.parts, batch), dim3(kThreads), 0, stream>>>(g, o.momentum, o.momentum_out, bl, size,
@@ -443,20 +597,21 @@ hipError_t run(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &o, void *worksp
         const int at = s & 1;
         Product a = {};
         a.batch = (int)batch;
+        a.part = part;
         a.L = a.R = x[at];
         a.D = A;
         a.lp = a.rp = pl.np;
         a.kp = pl.mp;
         a.sym = 1;
         a.f = 1.f / S;  // acc is in units of S^2, D in units of S
-        launch_product<kStore>(pl, a, stream);
+        launch_product<kStore>(pl.gram, a, stream);
         a.L = a.R = A;
         a.D = P;
         a.kp = pl.np;
         a.a = kA * S;
         a.b = kB;
         a.c = kC;
-        launch_product<kPoly>(pl, a, stream);
+        launch_product<kPoly>(pl.poly, a, stream);
         a.L = P;
         a.R = xt[at];
         a.D = x[1 - at];
@@ -464,7 +619,7 @@ hipError_t run(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &o, void *worksp
         a.rp = pl.mp;
         a.sym = 0;
         if (s + 1 < d.steps) {
-            launch_product<kStore>(pl, a, stream);
+            launch_product<kStore>(pl.apply, a, stream);
             continue;
         }
         a.f = 1.f / (S * S);
@@ -478,7 +633,7 @@ hipError_t run(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &o, void *worksp
             a.decay = 1.f - o.hyper->lr * o.hyper->weight_decay;
             a.step = o.hyper->lr * o.hyper->scale;
         }
-        launch_product<kFinal, T>(pl, a, stream);
+        launch_product<kFinal, T>(pl.apply, a, stream);
     }
     return hipGetLastError();
 }
@@ -489,7 +644,7 @@ size_t wtc_ortho_workspace(const wtconv_ortho_desc_t &d)
 {
     const Plan p = make_plan(d);
     if (p.one) return 0;
-    return 4 * p.xbytes + 2 * p.abytes + align256(sizeof(double) * p.parts * d.batch);
+    return 4 * p.xbytes + 2 * p.abytes + align256(sizeof(double) * p.parts * d.batch) + p.part;
 }
 
 hipError_t wtc_launch_ortho(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &a, void *workspace, hipStream_t stream)
