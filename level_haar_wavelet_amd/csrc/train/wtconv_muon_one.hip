@@ -13,8 +13,8 @@
 //   P X   takes P's and X's: neither moves.
 // Only X X^T needs X by rows: each wave turns its tiles through its own piece
 // of LDS (rows of 80 bytes: neither the writes nor the 16-byte reads collide).
-// The waves' parts of A are added in LDS in order, and every wave forms P for
-// itself.
+// The waves' parts of A are added in LDS in order; every wave forms P for itself
+// (up to 32 rows), or a block of it for all.
 #include "wtconv_muon_split.h"
 
 namespace wtc_muon {
@@ -36,6 +36,34 @@ __device__ inline void operand(const float16v &r, int kk, float s, half8 &hi, ha
         lo[i] = l;
     }
 }
+
+// One matrix in memory: elements by number, reads past the end (kNone) give 0
+// and writes there are dropped, so that no access needs a branch.
+constexpr unsigned kNone = 0x3fffffff;
+
+template <typename T>
+struct Matrix {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ Matrix(const T *p, unsigned count)
+        : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(p), 0, count * sizeof(T), 0x00020000))
+    {
+    }
+    __device__ float get(unsigned o) const
+    {
+        if constexpr (sizeof(T) == 4) {
+            return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, o * 4, 0, 0));
+        } else {
+            return (float)__builtin_bit_cast(T, (short)__builtin_amdgcn_raw_buffer_load_b16(r, o * 2, 0, 0));
+        }
+    }
+    __device__ void put(unsigned o, float v) const
+    {
+        if constexpr (sizeof(T) == 4)
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, v), r, o * 4, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, (T)v), r, o * 2, 0, 0);
+    }
+};
 
 struct Args {
     const void *g;
@@ -59,62 +87,111 @@ __global__ __launch_bounds__(kThreads, 1) void ortho_one(Args a)
 
     const int t = threadIdx.x, wave = t >> 6, lane = t & 63, h = lane >> 5, col = lane & 31;
     const int64_t base = (int64_t)blockIdx.x * a.n * a.m;
-    const T *g = (const T *)a.g + base;
-    // offset of (row of block b and register r; column of tile k), or -1;
-    // from0: the lane's first row and column
-    auto at = [&](int2 from0, int b, int r, int k) {
-        const int i = b * 32 + 8 * (r >> 2) + from0.x + (r & 3), j = k * kWaves * 32 + from0.y;
-        if (i >= a.n || j >= a.m) return -1;
-        return a.tall ? j * a.n + i : i * a.m + j;
+    const unsigned count = (unsigned)(a.n * a.m);
+    const Matrix<T> g((const T *)a.g + base, count);
+    const int tiles = (a.m + 31) / 32;
+
+    // A wave's tile k in memory.  X itself: 32 neighbours of each row, read
+    // into place, lane by lane.  X^T (tall): 32 rows of n, one stretch, read as
+    // it lies and turned through LDS (places spread by one for every 32).
+    float *turn32 = (float *)slots[wave];
+    auto row_of = [&](int b, int r) { return b * 32 + 8 * (r >> 2) + 4 * h + (r & 3); };
+    // element number of register (b, r) of tile k as it lies in memory
+    auto at = [&](int n, int m, int k, int b, int r) {
+        const int j0 = (k * kWaves + wave) * 32;
+        if (a.tall) {
+            const int e = (b * 16 + r) * 64 + lane;
+            return e < (m - j0 < 32 ? m - j0 : 32) * n ? (unsigned)(j0 * n + e) : kNone;
+        }
+        return row_of(b, r) < n && j0 + col < m ? (unsigned)(row_of(b, r) * m + j0 + col) : kNone;
     };
-
-    const int2 from = make_int2(4 * h, wave * 32 + col);
-
     float16v x[NT][NB];
-    double ss = 0.0;
 #pragma unroll
     for (int k = 0; k < NT; ++k)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            __builtin_amdgcn_sched_barrier(0);  // one block's addresses at a time
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[k][b][r] = g.get(at(a.n, a.m, k, b, r));
+    if (a.bl.muon) {
+        const Matrix<float> mi(a.momentum + base, count), mo(a.momentum_out + base, count);
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                float m[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) m[r] = mi.get(at(a.n, a.m, k, b, r));
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float v = x[k][b][r], q = fmaf(a.bl.mu, m[r], (1.f - a.bl.mu) * v);
+                    mo.put(at(a.n, a.m, k, b, r), q);
+                    x[k][b][r] = blend(a.bl, v, q);
+                }
+            }
+    }
+    // |U|^2: squares of each lane's values over its largest one's power of two,
+    // which neither overflow nor vanish; the lanes' sums in fp64
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < NT; ++k)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(x[k][b][r]));
+    const int ex = top > 0.f && top < INFINITY ? ilogbf(top) : 0;
+    float s32 = 0.f;
+#pragma unroll
+    for (int k = 0; k < NT; ++k)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const int o = at(from, b, r, k);
-                float u = 0.f;
-                if (o >= 0) {
-                    const T gv = g[o];
-                    float mo = 0.f;
-                    if (a.bl.muon) {
-                        mo = fmaf(a.bl.mu, a.momentum[base + o], (1.f - a.bl.mu) * (float)gv);
-                        a.momentum_out[base + o] = mo;
-                    }
-                    u = blend(a.bl, gv, mo);
-                }
-                x[k][b][r] = u;
-                ss = fma((double)u, (double)u, ss);
+                const float v = ldexpf(x[k][b][r], -ex);
+                s32 = fmaf(v, v, s32);
             }
-        }
+    double ss = ldexp((double)s32, 2 * ex);
     for (int o = 32; o; o >>= 1) ss += __shfl_xor(ss, o);
     if (lane == 0) norms[wave] = ss;
     __syncthreads();
     ss = norms[0];
     for (int w = 1; w < kWaves; ++w) ss += norms[w];
-    const double inv = (double)kScale / (sqrt(ss) + (double)a.eps);
+    // kScale / (|U| + eps) as inv 2^-nx
+    const double norm = sqrt(ss) + (double)a.eps;
+    const int nx = norm > 0.0 && norm < INFINITY ? ilogb(norm) : 0;
+    const float inv = (float)((double)kScale / ldexp(norm, -nx));
 
     // X as hi + lo, in right-operand order
     half8 xh[NT][NB][2], xl[NT][NB][2];
 #pragma unroll
-    for (int k = 0; k < NT; ++k)
+    for (int k = 0; k < NT; ++k) {
+        if (a.tall) {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int e = (b * 16 + r) * 64 + lane;
+                    turn32[e + (e >> 5)] = x[k][b][r];  // 0 past the tile
+                }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int e = col * a.n + row_of(b, r);
+                    x[k][b][r] = row_of(b, r) < a.n ? turn32[e + (e >> 5)] : 0.f;
+                }
+        }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) x[k][b][r] = (float)(x[k][b][r] * inv);
+            for (int r = 0; r < 16; ++r) x[k][b][r] = ldexpf(x[k][b][r], -nx) * inv;
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) operand(x[k][b], kk, 1.f, xh[k][b][kk], xl[k][b][kk]);
+            __builtin_amdgcn_sched_barrier(0);
         }
+    }
 
-    const int tiles = (a.m + 31) / 32;
     _Float16 *turn = (_Float16 *)slots[wave];
     for (int step = 0; step < a.steps; ++step) {
         // this wave's part of A = X X^T
@@ -129,7 +206,7 @@ __global__ __launch_bounds__(kThreads, 1) void ortho_one(Args a)
             for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const int i = b * 32 + 8 * (r >> 2) + 4 * h + (r & 3);
+                    const int i = row_of(b, r);
                     turn[i * kRow + col] = xh[k][b][r >> 3][r & 7];
                     turn[(NB * 32 + i) * kRow + col] = xl[k][b][r >> 3][r & 7];
                 }
@@ -173,56 +250,70 @@ __global__ __launch_bounds__(kThreads, 1) void ortho_one(Args a)
             sum[e] = s;
         }
         __syncthreads();
-        // A in units of kScale, P = a I + b A + c A A in the same
+        // P = a I + b A + c A A, A and P in units of kScale
         half8 ph[NB][NB][2], pl[NB][NB][2];  // [block of rows][of columns]
-        {
-            half8 ah[NB][NB][2], al[NB][NB][2];
+        auto block = [&](int i, int j) {
+            float16v s;
 #pragma unroll
-            for (int i = 0; i < NB; ++i)
+            for (int q = 0; q < 4; ++q) {
+                const float4 v = sum[((i * NB + j) * 4 + q) * 64 + lane];
+                s[4 * q] = v.x;
+                s[4 * q + 1] = v.y;
+                s[4 * q + 2] = v.z;
+                s[4 * q + 3] = v.w;
+            }
+            return s;
+        };
+        // block (i, j) of P: the rows of block i of A are, by symmetry, blocks
+        // (k, i) with the lane's column as the row
+        auto poly = [&](int i, int j) {
+            float16v s = {};
 #pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    float16v s;
+            for (int k = 0; k < NB; ++k) {
+                const float16v u = block(k, i), v = block(k, j);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float4 v = sum[((i * NB + j) * 4 + q) * 64 + lane];
-                        s[4 * q] = v.x;
-                        s[4 * q + 1] = v.y;
-                        s[4 * q + 2] = v.z;
-                        s[4 * q + 3] = v.w;
-                    }
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) operand(s, kk, 1.f / kScale, ah[i][j][kk], al[i][j][kk]);
-                    __builtin_amdgcn_sched_barrier(0);
+                for (int kk = 0; kk < 2; ++kk) {
+                    half8 uh, ul, vh, vl;
+                    operand(u, kk, 1.f / kScale, uh, ul);
+                    operand(v, kk, 1.f / kScale, vh, vl);
+                    s = mfma3(uh, ul, vh, vl, s);
                 }
+            }
+            const float16v A = block(i, j);
 #pragma unroll
-            for (int i = 0; i < NB; ++i)
+            for (int r = 0; r < 16; ++r) {
+                s[r] = fmaf(kB / kScale, A[r], (kC / kScale) * s[r]);
+                if (i == j && 8 * (r >> 2) + 4 * h + (r & 3) == col) s[r] += kA * kScale;
+            }
+            return s;
+        };
+        if constexpr (NB == 1) {
+            const float16v s = poly(0, 0);  // every wave for itself
 #pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    // rows of block i are, by symmetry, block (k, i) with the
-                    // lane's column as the row
-                    float16v s = {};
+            for (int kk = 0; kk < 2; ++kk) operand(s, kk, 1.f, ph[0][0][kk], pl[0][0][kk]);
+        } else {
+            // a block for each of the first waves, handed round in A's place
+            float16v s;
+            const int i = wave >> 1, j = wave & 1;
+            if (wave < NB * NB) s = poly(i, j);
+            __syncthreads();
+            if (wave < NB * NB)
 #pragma unroll
-                    for (int k = 0; k < NB; ++k)
+                for (int q = 0; q < 4; ++q)
+                    sum[(wave * 4 + q) * 64 + lane] = make_float4(s[4 * q], s[4 * q + 1], s[4 * q + 2], s[4 * q + 3]);
+            __syncthreads();
 #pragma unroll
-                        for (int kk = 0; kk < 2; ++kk)
-                            s = mfma3(ah[k][i][kk], al[k][i][kk], ah[k][j][kk], al[k][j][kk], s);
+            for (int p = 0; p < NB; ++p)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float A = (float)ah[i][j][r >> 3][r & 7] + (float)al[i][j][r >> 3][r & 7];
-                        s[r] = fmaf(kB, A, (kC / kScale) * s[r]);
-                        if (i == j && 8 * (r >> 2) + 4 * h + (r & 3) == col) s[r] += kA * kScale;
-                    }
+                for (int q = 0; q < NB; ++q) {
+                    const float16v v = block(p, q);
 #pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) operand(s, kk, 1.f, ph[i][j][kk], pl[i][j][kk]);
+                    for (int kk = 0; kk < 2; ++kk) operand(v, kk, 1.f, ph[p][q][kk], pl[p][q][kk]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
         }
         // X <- P X
         const bool last = step + 1 == a.steps;
-        // the outputs' offsets are computed again: kept from the loads, they
-        // would be as many registers as X
-        int2 to = from;
-        asm volatile("" : "+v"(to.x), "+v"(to.y));
 #pragma unroll
         for (int k = 0; k < NT; ++k) {
             if (k * kWaves + wave >= tiles) continue;
@@ -237,21 +328,51 @@ __global__ __launch_bounds__(kThreads, 1) void ortho_one(Args a)
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 __builtin_amdgcn_sched_barrier(0);
-                if (!last) {
+                if (!last)
 #pragma unroll
                     for (int kk = 0; kk < 2; ++kk) operand(y[i], kk, 1.f / kScale, xh[k][i][kk], xl[k][i][kk]);
-                    continue;
-                }
+            }
+            if (!last) continue;
+            // the outputs, as the inputs lie; the offsets are computed again
+            // (kept from there, they would be as many registers as X)
+            int n = a.n, m = a.m;
+            asm volatile("" : "+s"(n), "+s"(m));
+            if (a.tall) {
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int o = at(to, i, r, k);
-                    if (o < 0) continue;
-                    const float v = y[i][r] * (1.f / (kScale * kScale));
-                    if (a.weight)
-                        a.weight_out[base + o] = fmaf(a.decay, a.weight[base + o], -a.step * v);
-                    else
-                        ((T *)a.out)[base + o] = (T)v;
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int e = col * n + row_of(i, r);
+                        if (row_of(i, r) < n) turn32[e + (e >> 5)] = y[i][r];
+                    }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int e = (i * 16 + r) * 64 + lane;
+                        y[i][r] = turn32[e + (e >> 5)];
+                    }
+            }
+            const float f = 1.f / (kScale * kScale);
+            if (a.weight) {
+                const Matrix<float> wi(a.weight + base, count), wo(a.weight_out + base, count);
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    float w[16];
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) w[r] = wi.get(at(n, m, k, i, r));
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        wo.put(at(n, m, k, i, r), fmaf(a.decay, w[r], -a.step * (y[i][r] * f)));
                 }
+            } else {
+                const Matrix<T> out((const T *)a.out + base, count);
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) out.put(at(n, m, k, i, r), y[i][r] * f);
             }
         }
     }
@@ -259,8 +380,8 @@ __global__ __launch_bounds__(kThreads, 1) void ortho_one(Args a)
 
 }  // namespace
 
-// One 32-row block: eight tiles a wave; two: two tiles (registers).
-bool one_fits(int n, int m) { return n <= 32 ? m <= 8 * kWaves * 32 : n <= 64 && m <= 2 * kWaves * 32; }
+// One 32-row block: four tiles a wave; two: two tiles (registers).
+bool one_fits(int n, int m) { return n <= 32 ? m <= 4 * kWaves * 32 : n <= 64 && m <= 2 * kWaves * 32; }
 
 template <typename T>
 hipError_t launch_one(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &o, hipStream_t stream)
@@ -289,10 +410,8 @@ hipError_t launch_one(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &o, hipSt
             ortho_one<T, 1, 1><<<grid, th, 0, stream>>>(a);
         else if (need <= 2)
             ortho_one<T, 1, 2><<<grid, th, 0, stream>>>(a);
-        else if (need <= 4)
-            ortho_one<T, 1, 4><<<grid, th, 0, stream>>>(a);
         else
-            ortho_one<T, 1, 8><<<grid, th, 0, stream>>>(a);
+            ortho_one<T, 1, 4><<<grid, th, 0, stream>>>(a);
     } else if (need <= 1) {
         ortho_one<T, 2, 1><<<grid, th, 0, stream>>>(a);
     } else {

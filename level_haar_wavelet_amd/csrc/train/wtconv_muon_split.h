@@ -35,8 +35,13 @@ __device__ inline float blend(const Blend &b, T g, float momentum_out)
     return b.nesterov ? fmaf(b.mu, momentum_out, (1.f - b.mu) * (float)g) : momentum_out;
 }
 
+// v as hi + lo.  hi has to be the rounding of the fp32 v that lo is taken from:
+// left to itself, the compiler may round a v that is a product straight to
+// fp16 in one place and by way of fp32 in the other, and where the two differ
+// hi is off by a step.
 __device__ inline void split(float v, _Float16 &hi, _Float16 &lo)
 {
+    asm("" : "+v"(v));
     hi = (_Float16)v;
     lo = (_Float16)(v - (float)hi);
 }
