@@ -18,6 +18,7 @@ constexpr int kMaxBlock = 512;    // channels of a workgroup
 struct Geometry {
     int c, hw, groups, per, act;
     int cb, blocks, ppw, splits, lanes;
+    int vlast;      // tiles: channels of an access to the tensor that lies channels last
     int64_t count;  // workgroups of all images
 };
 
@@ -50,7 +51,7 @@ __device__ inline S join_wave(S s, J join2)
     return s;
 }
 
-// Elements of a vector access: 16 bytes.  The backward pass of two channels-last
+// Elements of a vector access: 16 bytes, or 8, or one.  The backward pass of two channels-last
 // tensors takes at most four: six constants for each of eight channels a thread
 // are 180 registers and two waves a SIMD (16x256x256x256 fp16: dx 563 us).
 constexpr int vector_of(size_t esize, bool xl, bool yl, bool bwd)
@@ -60,7 +61,8 @@ constexpr int vector_of(size_t esize, bool xl, bool yl, bool bwd)
 
 struct Plan {
     Geometry stats, apply;  // the forward pass's moments; every other pass
-    bool xl, yl, vec, one;
+    bool xl, yl, one;
+    int v;  // elements of an access
     float eps;
     size_t means_at, bytes;  // workspace: partial sums, then the groups' means
 };

@@ -213,9 +213,19 @@ Plan make_plan(const wtconv_norm_desc_t &d, bool bwd, bool aligned)
     g.per = g.c / g.groups;
     g.act = d.act;
     const Walk sw = p.xl ? kLast : kPlanes, aw = p.xl != p.yl ? kTiles : sw;
-    const int vec = vector_of(esize, p.xl, p.yl, bwd);
-    p.vec = aligned && (!(p.xl || p.yl) || g.c % vec == 0) && ((p.xl && p.yl) || g.hw % vec == 0);
-    const int v = p.vec ? vec : 1;
+    // the widest access that rows and addresses allow: rows of channels, of
+    // pixels, or in tiles (the planes' side) of pixels
+    auto widest = [&](int most, bool channels, bool pixels) {
+        if (!aligned) return 1;
+        for (int w = most; w > 1; w = w > v16 / 2 ? v16 / 2 : 1)
+            if (!(channels && g.c % w) && !(pixels && g.hw % w)) return w;
+        return 1;
+    };
+    p.v = widest(vector_of(esize, p.xl, p.yl, bwd), p.xl && p.yl, !(p.xl && p.yl));
+    g.vlast = widest(v16, true, false);
+    // the moments' walk follows x alone, with the same width of access
+    if (aw == kTiles && p.xl && !bwd) p.v = widest(v16, true, true);
+    const int v = p.v;
 
     // One launch, against three, by sizes (fp16 / fp32, us, measured in a graph):
     //   planes  64x96x56x56 26 / 37 against 30 / 43, 16x256x256x256 310 against
@@ -224,15 +234,16 @@ Plan make_plan(const wtconv_norm_desc_t &d, bool bwd, bool aligned)
     //           (8x64x14x14: 7 against 14);
     //   last    a workgroup's rows are narrow: 8x512x16x16 12 / 9 against 13 / 15,
     //           but 1x128x64x64 19 / 17 against 13 / 12, 64x768x7x7 21 / 20
-    //           against 15 / 16: groups of at most 32 KB, at most 512 of them;
+    //           against 15 / 16: up to 1024 pixels and 64 KB, at most 512 of them;
     //   tiles   forward 8x512x16x16 9 / 9 against 11 / 11, but 1x512x32x32 16 / 21
     //           against 11 / 11: up to 256 pixels; backward never (64x768x7x7
     //           27 / 23 against 36 / 23, 8x512x16x16 15 / 17 against 13 / 11).
-    const int unit = p.xl || p.yl ? lcm_pow2(g.per, v) : g.per;
+    const int unit = aw == kTiles ? lcm_pow2(g.per, p.xl && !bwd && v > g.vlast ? v : g.vlast)
+                     : p.xl ? lcm_pow2(g.per, v) : g.per;
     if (unit <= kMaxBlock && !(aw == kTiles && (bwd || g.hw > 256))) {
         const Geometry s = one_geometry(g, d.n, sw, aw == kTiles, v, v16, unit);
         const int64_t slice = (int64_t)s.cb * g.hw * esize, count = s.count;
-        if (aw == kTiles || (aw == kLast ? slice <= 32768 && count <= 512 : slice <= 16384 || count >= 256)) {
+        if (aw == kTiles || (aw == kLast ? slice <= 65536 && g.hw <= 1024 && count <= 512 : slice <= 16384 || count >= 256)) {
             p.one = true;
             p.stats = s;
             p.apply = s;

@@ -146,14 +146,28 @@ __device__ inline float act_bwd(int act, float dy, float x, float xh, const Chan
 struct Range {
     int64_t n;
     int c0, cb, p0, p1;
+    int64_t row;  // of the partial sums
 };
 
-__device__ inline Range range_of(const Geometry &g, int id)
+// The range of this workgroup.  Workgroups go to the 8 dies in turn; each die
+// gets a stretch of neighbouring ranges, so that the parts of a cache line that
+// lie in two channel blocks meet in one L2, and a second pass (kBack: last range
+// first) finds in its L2 what the first pass read there last.  One launch over
+// planes has neither, and runs up to 15 % faster in plain order (kPlain).
+enum Order { kPlain, kForth, kBack };
+
+__device__ inline Range range_of(const Geometry &g, Order order)
 {
+    int id = blockIdx.x;
+    if (order != kPlain) {
+        const int per = gridDim.x / 8, rest = gridDim.x % 8, die = id % 8, own = per + (die < rest), k = id / 8;
+        id = die * per + (die < rest ? die : rest) + (order == kBack ? own - 1 - k : k);
+    }
     const int64_t u = id / g.splits;
     const int s = id % g.splits, b = (int)(u % g.blocks);
     Range r;
     r.n = u / g.blocks;
+    r.row = r.n * g.splits + s;
     r.c0 = b * g.cb;
     r.cb = g.c - r.c0 < g.cb ? g.c - r.c0 : g.cb;
     r.p0 = s * g.ppw;
@@ -320,46 +334,71 @@ __device__ inline T *tile_at(char *tile, int p, int j)
 }
 
 // Brings the tile (pixels p0.., channels c0..) of a channels-last tensor into
-// LDS, or back out of it.
+// LDS, or back out of it, V channels at a time.
 template <typename T, int V, int NT, bool OUT>
-__device__ inline void move_tile(T *t_, const Geometry &g, const Range &r, int p0, int c0, char *tile)
+__device__ inline void move_pieces(T *t_, const Geometry &g, const Range &r, int p0, int c0, char *tile)
 {
-    constexpr int V16 = 16 / sizeof(T), kSide = 8 * V16, kChunks = kSide / V;
-    for (int e = threadIdx.x; e < kSide * kChunks; e += NT) {
-        const int p = e / kChunks, j = e % kChunks * V;
-        if (p0 + p >= r.p1 || c0 + j >= r.c0 + r.cb) continue;
-        T *m = t_ + (r.n * g.hw + p0 + p) * (int64_t)g.c + c0 + j;
-        typedef typename Pack<T, V>::type P;
-        if (OUT)
-            *(P *)m = *(const P *)tile_at<T, V16>(tile, p, j);
-        else
-            *(P *)tile_at<T, V16>(tile, p, j) = *(const P *)m;
+    constexpr int V16 = 16 / sizeof(T), kSide = 8 * V16, kChunks = kSide / V, kOwn = (kSide * kChunks + NT - 1) / NT;
+    typedef typename Pack<T, V>::type P;
+    P v[kOwn];
+    T *m = t_ + (r.n * g.hw + p0) * (int64_t)g.c + c0;
+    auto inside = [&](int e) {
+        return e < kSide * kChunks && p0 + e / kChunks < r.p1 && c0 + e % kChunks * V < r.c0 + r.cb;
+    };
+    auto in_memory = [&](int e) { return (P *)(m + (int64_t)(e / kChunks) * g.c + e % kChunks * V); };
+    auto in_tile = [&](int e) { return (P *)tile_at<T, V16>(tile, e / kChunks, e % kChunks * V); };
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) {
+        const int e = threadIdx.x + o * NT;
+        if (inside(e)) v[o] = OUT ? *in_tile(e) : *in_memory(e);
+    }
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) {
+        const int e = threadIdx.x + o * NT;
+        if (inside(e)) *(OUT ? in_memory(e) : in_tile(e)) = v[o];
     }
 }
 
-// Calls f(c, p, q, offset) for the V pixels from p on of channel c in the order
-// of planes, p's place in the tile being q; before(p0, c0) and after(p0, c0)
-// around every tile.
-template <typename T, int V, int NT, typename A, typename F, typename E>
-__device__ inline void walk_tiles(const Geometry &g, const Range &r, A before, F f, E after)
+// The width follows the channels alone: the planes' side may need another.
+// WIDE: it is 16 bytes (an instance of its own: the registers of the narrow ones
+// would cost it a third of its waves).
+template <typename T, bool WIDE, int NT, bool OUT>
+__device__ inline void move_tile(T *t_, const Geometry &g, const Range &r, int p0, int c0, char *tile)
 {
-    constexpr int V16 = 16 / sizeof(T), kSide = 8 * V16, kChunks = kSide / V;
-    for (int c0 = r.c0; c0 < r.c0 + r.cb; c0 += kSide)
-        for (int p0 = r.p0; p0 < r.p1; p0 += kSide) {
-            before(p0, c0);
-            for (int e = threadIdx.x; e < kSide * kChunks; e += NT) {
-                const int c = e / kChunks, q = e % kChunks * V;
-                if (c0 + c < r.c0 + r.cb && p0 + q < r.p1)
-                    f(c0 + c, c, q, (r.n * g.c + c0 + c) * (int64_t)g.hw + p0 + q);
-            }
-            after(p0, c0);
-        }
+    constexpr int V16 = 16 / sizeof(T);
+    if constexpr (WIDE)
+        move_pieces<T, V16, NT, OUT>(t_, g, r, p0, c0, tile);
+    else if (g.vlast == V16 / 2)
+        move_pieces<T, V16 / 2, NT, OUT>(t_, g, r, p0, c0, tile);
+    else
+        move_pieces<T, 1, NT, OUT>(t_, g, r, p0, c0, tile);
 }
+
+// The pieces of V pixels of a tile that a thread takes in the order of planes.
+template <typename T, int V, int NT>
+struct Pieces {
+    static constexpr int kSide = 128 / sizeof(T), kChunks = kSide / V, kOwn = (kSide * kChunks + NT - 1) / NT;
+    const Range &r;
+    int p0, c0;
+    int64_t base;
+    __device__ Pieces(const Geometry &g, const Range &r_, int p0_, int c0_)
+        : r(r_), p0(p0_), c0(c0_), base((r_.n * g.c + c0_) * (int64_t)g.hw + p0_)
+    {
+    }
+    __device__ static int place(int o) { return threadIdx.x + o * NT; }
+    __device__ static int channel(int o) { return place(o) / kChunks; }
+    __device__ static int pixel(int o) { return place(o) % kChunks * V; }
+    __device__ bool inside(int o) const
+    {
+        return place(o) < kSide * kChunks && c0 + channel(o) < r.c0 + r.cb && p0 + pixel(o) < r.p1;
+    }
+    __device__ int64_t at(const Geometry &g, int o) const { return base + (int64_t)channel(o) * g.hw + pixel(o); }
+};
 
 // ---- The passes of a range -------------------------------------------------------
 
 // y of the range.
-template <typename T, int V, int NT, bool XL, bool YL>
+template <typename T, int V, bool WIDE, int NT, bool XL, bool YL>
 __device__ inline void apply(const T *__restrict__ x, T *__restrict__ y, const Geometry &g, const Range &r,
                              const Chan *lk, char *tile)
 {
@@ -392,44 +431,51 @@ __device__ inline void apply(const T *__restrict__ x, T *__restrict__ y, const G
             [](int) {});
     } else {
         constexpr int V16 = 16 / sizeof(T);
-        walk_tiles<T, V, NT>(
-            g, r,
-            [&](int p0, int c0) {
-                if (!XL) return;
-                __syncthreads();
-                move_tile<T, V, NT, false>(const_cast<T *>(x), g, r, p0, c0, tile);
-                __syncthreads();
-            },
-            [&](int c, int j, int q, int64_t at) {
-                float v[V];
-                if (XL)
+        typedef Pieces<T, V, NT> P;
+        for (int c0 = r.c0; c0 < r.c0 + r.cb; c0 += P::kSide)
+            for (int p0 = r.p0; p0 < r.p1; p0 += P::kSide) {
+                const P w(g, r, p0, c0);
+                typename Pack<T, V>::type raw[P::kOwn];
+                if (!XL)
 #pragma unroll
-                    for (int i = 0; i < V; ++i) v[i] = (float)*tile_at<T, V16>(tile, q + i, j);
-                else
-                    values<T, V>(fetch<T, V>(x + at), v);
-                const Chan k = lk[c - r.c0];
-                const float a = k.rstd * k.gamma;
+                    for (int o = 0; o < P::kOwn; ++o)
+                        if (w.inside(o)) raw[o] = fetch<T, V>(x + w.at(g, o));
+                __syncthreads();  // the tile before is read
+                if (XL) {
+                    move_tile<T, WIDE, NT, false>(const_cast<T *>(x), g, r, p0, c0, tile);
+                    __syncthreads();
+                }
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[i] = fmaf(v[i] - k.mean, a, k.beta);
-                act_fwd<V>(g.act, v);
-                if (XL)
-                    store<T, V>(y + at, v);
-                else
+                for (int o = 0; o < P::kOwn; ++o) {
+                    if (!w.inside(o)) continue;
+                    float v[V];
+                    if (XL)
 #pragma unroll
-                    for (int i = 0; i < V; ++i) *tile_at<T, V16>(tile, q + i, j) = (T)v[i];
-            },
-            [&](int p0, int c0) {
-                if (XL) return;
-                __syncthreads();
-                move_tile<T, V, NT, true>(y, g, r, p0, c0, tile);
-                __syncthreads();
-            });
+                        for (int i = 0; i < V; ++i) v[i] = (float)*tile_at<T, V16>(tile, w.pixel(o) + i, w.channel(o));
+                    else
+                        values<T, V>(raw[o], v);
+                    const Chan k = lk[c0 + w.channel(o) - r.c0];
+                    const float a = k.rstd * k.gamma;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[i] = fmaf(v[i] - k.mean, a, k.beta);
+                    act_fwd<V>(g.act, v);
+                    if (XL)
+                        store<T, V>(y + w.at(g, o), v);
+                    else
+#pragma unroll
+                        for (int i = 0; i < V; ++i) *tile_at<T, V16>(tile, w.pixel(o) + i, w.channel(o)) = (T)v[i];
+                }
+                if (!XL) {
+                    __syncthreads();
+                    move_tile<T, WIDE, NT, true>(y, g, r, p0, c0, tile);
+                }
+            }
     }
 }
 
 // Sums of dz and dz xh of the range's channels: done(c, sums).  sums: LDS of a
 // channel's sums (tiles).
-template <typename T, int V, int NT, bool XL, bool YL, typename D>
+template <typename T, int V, bool WIDE, int NT, bool XL, bool YL, typename D>
 __device__ inline void sums_bwd(const T *__restrict__ x, const T *__restrict__ dy, const Geometry &g, const Range &r,
                                 const Chan *lk, float *lds, char *tile, D done)
 {
@@ -470,30 +516,31 @@ __device__ inline void sums_bwd(const T *__restrict__ x, const T *__restrict__ d
                     for (int i = 0; i < K; ++i) done(c + i, make_float2(s.a[i], s.b[i]));
             });
     } else {
-        // 8 V16 / V threads side by side share a channel of the tile; a thread's
-        // places e, e + NT, .. are kSide * kChunks / NT channels
-        constexpr int V16 = 16 / sizeof(T), kSide = 8 * V16, kChunks = kSide / V;
-        constexpr int kOwn = (kSide * kChunks + NT - 1) / NT;
-        static_assert(kChunks <= 64 && NT % kChunks == 0, "a channel's threads are lanes of one wave");
-        for (int c0 = r.c0; c0 < r.c0 + r.cb; c0 += kSide) {
-            float2 s[kOwn];
+        constexpr int V16 = 16 / sizeof(T);
+        typedef Pieces<T, V, NT> P;
+        static_assert(P::kChunks <= 64 && NT % P::kChunks == 0, "a channel's threads are lanes of one wave");
+        for (int c0 = r.c0; c0 < r.c0 + r.cb; c0 += P::kSide) {
+            float2 s[P::kOwn];
 #pragma unroll
-            for (int o = 0; o < kOwn; ++o) s[o] = make_float2(0.f, 0.f);
-            for (int p0 = r.p0; p0 < r.p1; p0 += kSide) {
+            for (int o = 0; o < P::kOwn; ++o) s[o] = make_float2(0.f, 0.f);
+            for (int p0 = r.p0; p0 < r.p1; p0 += P::kSide) {
+                const P w(g, r, p0, c0);
+                typename Pack<T, V>::type raw[P::kOwn];
+#pragma unroll
+                for (int o = 0; o < P::kOwn; ++o)
+                    if (w.inside(o)) raw[o] = fetch<T, V>((XL ? dy : x) + w.at(g, o));
                 __syncthreads();
-                move_tile<T, V, NT, false>(const_cast<T *>(XL ? x : dy), g, r, p0, c0, tile);
+                move_tile<T, WIDE, NT, false>(const_cast<T *>(XL ? x : dy), g, r, p0, c0, tile);
                 __syncthreads();
 #pragma unroll
-                for (int o = 0; o < kOwn; ++o) {
-                    const int e = threadIdx.x + o * NT, j = e / kChunks, q = e % kChunks * V;
-                    if (e >= kSide * kChunks || c0 + j >= r.c0 + r.cb || p0 + q >= r.p1) continue;
-                    const int64_t at = (r.n * g.c + c0 + j) * (int64_t)g.hw + p0 + q;
+                for (int o = 0; o < P::kOwn; ++o) {
+                    if (!w.inside(o)) continue;
                     float v[V];
-                    values<T, V>(fetch<T, V>((XL ? dy : x) + at), v);
-                    const Chan k = lk[c0 + j - r.c0];
+                    values<T, V>(raw[o], v);
+                    const Chan k = lk[c0 + w.channel(o) - r.c0];
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        const float u = (float)*tile_at<T, V16>(tile, q + i, j);
+                        const float u = (float)*tile_at<T, V16>(tile, w.pixel(o) + i, w.channel(o));
                         const float xv = XL ? u : v[i], xh = (xv - k.mean) * k.rstd;
                         const float dz = act_bwd(g.act, XL ? v[i] : u, xv, xh, k);
                         s[o].x += dz;
@@ -502,20 +549,20 @@ __device__ inline void sums_bwd(const T *__restrict__ x, const T *__restrict__ d
                 }
             }
 #pragma unroll
-            for (int o = 0; o < kOwn; ++o) {
-                for (int k = 1; k < kChunks; k <<= 1) {
+            for (int o = 0; o < P::kOwn; ++o) {
+                for (int k = 1; k < P::kChunks; k <<= 1) {
                     s[o].x += __shfl_xor(s[o].x, k);
                     s[o].y += __shfl_xor(s[o].y, k);
                 }
-                const int e = threadIdx.x + o * NT, j = e / kChunks;
-                if (e % kChunks == 0 && e < kSide * kChunks && c0 + j < r.c0 + r.cb) done(c0 + j, s[o]);
+                const int j = P::channel(o);
+                if (P::pixel(o) == 0 && P::place(o) < P::kSide * P::kChunks && c0 + j < r.c0 + r.cb) done(c0 + j, s[o]);
             }
         }
     }
 }
 
 // dx of the range; q: the group's means of t and t xh, by channel.
-template <typename T, int V, int NT, bool XL, bool YL>
+template <typename T, int V, bool WIDE, int NT, bool XL, bool YL>
 __device__ inline void apply_bwd(const T *__restrict__ x, const T *__restrict__ dy, T *__restrict__ dx,
                                  const Geometry &g, const Range &r, const Chan *lk, const float2 *lq,
                                  char *tile)
@@ -555,31 +602,37 @@ __device__ inline void apply_bwd(const T *__restrict__ x, const T *__restrict__ 
             [](int) {});
     } else {
         constexpr int V16 = 16 / sizeof(T);
-        walk_tiles<T, V, NT>(
-            g, r,
-            [&](int p0, int c0) {
-                __syncthreads();
-                move_tile<T, V, NT, false>(const_cast<T *>(XL ? x : dy), g, r, p0, c0, tile);
-                __syncthreads();
-            },
-            [&](int c, int j, int p, int64_t at) {
-                float v[V];
-                values<T, V>(fetch<T, V>((XL ? dy : x) + at), v);
-                const Chan k = lk[c - r.c0];
-                const float2 q = lq[c - r.c0];
+        typedef Pieces<T, V, NT> P;
+        for (int c0 = r.c0; c0 < r.c0 + r.cb; c0 += P::kSide)
+            for (int p0 = r.p0; p0 < r.p1; p0 += P::kSide) {
+                const P w(g, r, p0, c0);
+                typename Pack<T, V>::type raw[P::kOwn];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    T *u = tile_at<T, V16>(tile, p + i, j);
-                    v[i] = XL ? value((float)*u, v[i], k, q) : value(v[i], (float)*u, k, q);
-                    if (XL) *u = (T)v[i];
-                }
-                if (!XL) store<T, V>(dx + at, v);
-            },
-            [&](int p0, int c0) {
-                if (!XL) return;
+                for (int o = 0; o < P::kOwn; ++o)
+                    if (w.inside(o)) raw[o] = fetch<T, V>((XL ? dy : x) + w.at(g, o));
                 __syncthreads();
-                move_tile<T, V, NT, true>(dx, g, r, p0, c0, tile);
-            });
+                move_tile<T, WIDE, NT, false>(const_cast<T *>(XL ? x : dy), g, r, p0, c0, tile);
+                __syncthreads();
+#pragma unroll
+                for (int o = 0; o < P::kOwn; ++o) {
+                    if (!w.inside(o)) continue;
+                    float v[V];
+                    values<T, V>(raw[o], v);
+                    const Chan k = lk[c0 + w.channel(o) - r.c0];
+                    const float2 q = lq[c0 + w.channel(o) - r.c0];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        T *u = tile_at<T, V16>(tile, w.pixel(o) + i, w.channel(o));
+                        v[i] = XL ? value((float)*u, v[i], k, q) : value(v[i], (float)*u, k, q);
+                        if (XL) *u = (T)v[i];
+                    }
+                    if (!XL) store<T, V>(dx + w.at(g, o), v);
+                }
+                if (XL) {
+                    __syncthreads();
+                    move_tile<T, WIDE, NT, true>(dx, g, r, p0, c0, tile);
+                }
+            }
     }
 }
 
@@ -593,10 +646,9 @@ __global__ __launch_bounds__(kThreads) void norm_moments(const T *__restrict__ x
                                                          float2 *__restrict__ part)
 {
     __shared__ float lds[(1 + 2 * (XL ? V : 1)) * kThreads];
-    const Range r = range_of(g, blockIdx.x);
-    const int64_t row = r.n * g.splits + blockIdx.x % g.splits;
+    const Range r = range_of(g, kForth);
     moments<T, XL, V, kThreads>(x, g, r, lds,
-                                [&](int c, const Moments &m) { part[row * g.c + c] = make_float2(m.mean, m.m2); });
+                                [&](int c, const Moments &m) { part[r.row * g.c + c] = make_float2(m.mean, m.m2); });
 }
 
 __device__ inline void load_consts(Chan *lk, const Geometry &g, const Range &r, const float *__restrict__ gamma,
@@ -611,7 +663,7 @@ __device__ inline void load_consts(Chan *lk, const Geometry &g, const Range &r, 
     __syncthreads();
 }
 
-template <typename T, int V, bool XL, bool YL>
+template <typename T, int V, bool WIDE, bool XL, bool YL>
 __global__ __launch_bounds__(kThreads) void norm_apply(const T *__restrict__ x, const float *__restrict__ gamma,
                                                        const float *__restrict__ beta,
                                                        const float *__restrict__ mean,
@@ -619,12 +671,12 @@ __global__ __launch_bounds__(kThreads) void norm_apply(const T *__restrict__ x, 
 {
     __shared__ Chan lk[kMaxBlock];
     __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
-    const Range r = range_of(g, gridDim.x - 1 - blockIdx.x);
+    const Range r = range_of(g, kBack);
     load_consts(lk, g, r, gamma, beta, mean, rstd);
-    apply<T, V, kThreads, XL, YL>(x, y, g, r, lk, tile);
+    apply<T, V, WIDE, kThreads, XL, YL>(x, y, g, r, lk, tile);
 }
 
-template <typename T, int V, bool XL, bool YL>
+template <typename T, int V, bool WIDE, bool XL, bool YL>
 __global__ __launch_bounds__(kThreads) void norm_sums_bwd(const T *__restrict__ x, const T *__restrict__ dy,
                                                           const float *__restrict__ gamma,
                                                           const float *__restrict__ beta,
@@ -635,14 +687,13 @@ __global__ __launch_bounds__(kThreads) void norm_sums_bwd(const T *__restrict__ 
     __shared__ Chan lk[kMaxBlock];
     __shared__ float lds[2 * (XL ? V : 1) * kThreads];
     __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
-    const Range r = range_of(g, blockIdx.x);
-    const int64_t row = r.n * g.splits + blockIdx.x % g.splits;
+    const Range r = range_of(g, kForth);
     load_consts(lk, g, r, gamma, beta, mean, rstd);
-    sums_bwd<T, V, kThreads, XL, YL>(x, dy, g, r, lk, lds, tile,
-                                     [&](int c, const float2 &s) { part[row * g.c + c] = s; });
+    sums_bwd<T, V, WIDE, kThreads, XL, YL>(x, dy, g, r, lk, lds, tile,
+                                     [&](int c, const float2 &s) { part[r.row * g.c + c] = s; });
 }
 
-template <typename T, int V, bool XL, bool YL>
+template <typename T, int V, bool WIDE, bool XL, bool YL>
 __global__ __launch_bounds__(kThreads) void norm_apply_bwd(const T *__restrict__ x, const T *__restrict__ dy,
                                                            const float *__restrict__ gamma,
                                                            const float *__restrict__ beta,
@@ -654,10 +705,10 @@ __global__ __launch_bounds__(kThreads) void norm_apply_bwd(const T *__restrict__
     __shared__ Chan lk[kMaxBlock];
     __shared__ float2 lq[kMaxBlock];
     __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
-    const Range r = range_of(g, gridDim.x - 1 - blockIdx.x);
+    const Range r = range_of(g, kBack);
     for (int i = threadIdx.x; i < r.cb; i += kThreads) lq[i] = means[r.n * g.groups + (r.c0 + i) / g.per];
     load_consts(lk, g, r, gamma, beta, mean, rstd);
-    apply_bwd<T, V, kThreads, XL, YL>(x, dy, dx, g, r, lk, lq, tile);
+    apply_bwd<T, V, WIDE, kThreads, XL, YL>(x, dy, dx, g, r, lk, lq, tile);
 }
 
 // ---- One launch ----------------------------------------------------------------------
@@ -676,7 +727,7 @@ __device__ inline void join_groups(const Geometry &g, const Range &r, V value, S
     }
 }
 
-template <typename T, int V, bool XL, bool YL>
+template <typename T, int V, bool WIDE, bool XL, bool YL>
 __global__ __launch_bounds__(kOneThreads) void norm_one(const T *__restrict__ x, const float *__restrict__ gamma,
                                                         const float *__restrict__ beta, T *__restrict__ y,
                                                         float *__restrict__ mean, float *__restrict__ rstd, Geometry g,
@@ -686,7 +737,7 @@ __global__ __launch_bounds__(kOneThreads) void norm_one(const T *__restrict__ x,
     __shared__ Moments lm[kMaxBlock];
     __shared__ float lds[(1 + 2 * (XL ? V : 1)) * kOneThreads];
     __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
-    const Range r = range_of(g, blockIdx.x);
+    const Range r = range_of(g, XL || YL ? kForth : kPlain);
     moments<T, XL, V, kOneThreads>(x, g, r, lds, [&](int c, const Moments &m) { lm[c - r.c0] = m; });
     __syncthreads();
     join_groups<kOneThreads>(
@@ -711,10 +762,10 @@ __global__ __launch_bounds__(kOneThreads) void norm_one(const T *__restrict__ x,
         lk[i].beta = beta ? beta[c] : 0.f;
     }
     __syncthreads();
-    apply<T, V, kOneThreads, XL, YL>(x, y, ga, r, lk, tile);
+    apply<T, V, WIDE, kOneThreads, XL, YL>(x, y, ga, r, lk, tile);
 }
 
-template <typename T, int V, bool XL, bool YL>
+template <typename T, int V, bool WIDE, bool XL, bool YL>
 __global__ __launch_bounds__(kOneThreads) void norm_one_bwd(const T *__restrict__ x, const T *__restrict__ dy,
                                                             const float *__restrict__ gamma,
                                                             const float *__restrict__ beta,
@@ -726,9 +777,9 @@ __global__ __launch_bounds__(kOneThreads) void norm_one_bwd(const T *__restrict_
     __shared__ float2 ls[kMaxBlock], lq[kMaxBlock];
     __shared__ float lds[2 * (XL ? V : 1) * kOneThreads];
     __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
-    const Range r = range_of(g, blockIdx.x);
+    const Range r = range_of(g, XL || YL ? kForth : kPlain);
     load_consts(lk, g, r, gamma, beta, mean, rstd);
-    sums_bwd<T, V, kOneThreads, XL, YL>(x, dy, g, r, lk, lds, tile, [&](int c, const float2 &s) {
+    sums_bwd<T, V, WIDE, kOneThreads, XL, YL>(x, dy, g, r, lk, lds, tile, [&](int c, const float2 &s) {
         ls[c - r.c0] = s;
         if (part) part[r.n * g.c + c] = s;
     });
@@ -744,16 +795,16 @@ __global__ __launch_bounds__(kOneThreads) void norm_one_bwd(const T *__restrict_
     for (int i = threadIdx.x; i < r.cb; i += kOneThreads)
         if (i % g.per) lq[i] = lq[i - i % g.per];
     __syncthreads();
-    apply_bwd<T, V, kOneThreads, XL, YL>(x, dy, dx, g, r, lk, lq, tile);
+    apply_bwd<T, V, WIDE, kOneThreads, XL, YL>(x, dy, dx, g, r, lk, lq, tile);
 }
 
 // ---- Launches ------------------------------------------------------------------------
 
-template <typename T, int V, bool XL, bool YL>
+template <typename T, int V, bool WIDE, bool XL, bool YL>
 hipError_t forward_v(const Plan &p, const Call &a, hipStream_t stream)
 {
     if (p.one) {
-        norm_one<T, V, XL, YL><<<dim3((unsigned)p.apply.count), dim3(kOneThreads), 0, stream>>>(
+        norm_one<T, V, WIDE, XL, YL><<<dim3((unsigned)p.apply.count), dim3(kOneThreads), 0, stream>>>(
             (const T *)a.x, a.gamma, a.beta, (T *)a.out, a.mean_out, a.rstd_out, p.stats, p.apply, p.eps);
         return hipGetLastError();
     }
@@ -761,45 +812,57 @@ hipError_t forward_v(const Plan &p, const Call &a, hipStream_t stream)
     float2 *part = (float2 *)a.workspace;
     norm_moments<T, V, XL><<<dim3((unsigned)p.stats.count), th, 0, stream>>>((const T *)a.x, p.stats, part);
     launch_finish_forward(p.stats, a.n, part, a.mean_out, a.rstd_out, p.eps, stream);
-    norm_apply<T, V, XL, YL><<<dim3((unsigned)p.apply.count), th, 0, stream>>>(
+    norm_apply<T, V, WIDE, XL, YL><<<dim3((unsigned)p.apply.count), th, 0, stream>>>(
         (const T *)a.x, a.gamma, a.beta, a.mean_out, a.rstd_out, (T *)a.out, p.apply);
     return hipGetLastError();
 }
 
-template <typename T, int V, bool XL, bool YL>
+template <typename T, int V, bool WIDE, bool XL, bool YL>
 hipError_t backward_v(const Plan &p, const Call &a, hipStream_t stream)
 {
     const Geometry &g = p.apply;
     float2 *part = (float2 *)a.workspace, *means = (float2 *)((char *)a.workspace + p.means_at);
-    if (p.one) {
-        float2 *sums = a.dgamma || a.dbeta ? part : nullptr;
-        norm_one_bwd<T, V, XL, YL><<<dim3((unsigned)g.count), dim3(kOneThreads), 0, stream>>>(
-            (const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean, a.rstd, (T *)a.out, g, sums);
-        if (sums) launch_finish_backward(g, a.n, sums, a.gamma, nullptr, a.dgamma, a.dbeta, stream);
-        return hipGetLastError();
+    if constexpr (XL == YL) {
+        if (p.one) {
+            float2 *sums = a.dgamma || a.dbeta ? part : nullptr;
+            norm_one_bwd<T, V, WIDE, XL, YL><<<dim3((unsigned)g.count), dim3(kOneThreads), 0, stream>>>(
+                (const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean, a.rstd, (T *)a.out, g, sums);
+            if (sums) launch_finish_backward(g, a.n, sums, a.gamma, nullptr, a.dgamma, a.dbeta, stream);
+            return hipGetLastError();
+        }
     }
     const dim3 th(kThreads), grid((unsigned)g.count);
-    norm_sums_bwd<T, V, XL, YL><<<grid, th, 0, stream>>>((const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean,
+    norm_sums_bwd<T, V, WIDE, XL, YL><<<grid, th, 0, stream>>>((const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean,
                                                          a.rstd, g, part);
     launch_finish_backward(g, a.n, part, a.gamma, means, a.dgamma, a.dbeta, stream);
-    norm_apply_bwd<T, V, XL, YL><<<grid, th, 0, stream>>>((const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean,
+    norm_apply_bwd<T, V, WIDE, XL, YL><<<grid, th, 0, stream>>>((const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean,
                                                           a.rstd, means, (T *)a.out, g);
     return hipGetLastError();
 }
 
-template <typename T, bool XL, bool YL>
+template <typename T, bool WIDE, bool XL, bool YL>
 hipError_t run_layout(const Plan &p, const Call &a, hipStream_t stream)
 {
-    constexpr int V = vector_of(sizeof(T), XL, YL, false), W = vector_of(sizeof(T), XL, YL, true);
-    if (a.dy) return p.vec ? backward_v<T, W, XL, YL>(p, a, stream) : backward_v<T, 1, XL, YL>(p, a, stream);
-    return p.vec ? forward_v<T, V, XL, YL>(p, a, stream) : forward_v<T, 1, XL, YL>(p, a, stream);
+    constexpr int V16 = 16 / sizeof(T), V = vector_of(sizeof(T), XL, YL, false), W = vector_of(sizeof(T), XL, YL, true);
+    if (!a.dy) {
+        if (p.v == V) return forward_v<T, V, WIDE, XL, YL>(p, a, stream);
+        if (p.v == V16 / 2) return forward_v<T, V16 / 2, WIDE, XL, YL>(p, a, stream);
+        return forward_v<T, 1, WIDE, XL, YL>(p, a, stream);
+    }
+    if (p.v == W) return backward_v<T, W, WIDE, XL, YL>(p, a, stream);
+    if (p.v == V16 / 2) return backward_v<T, V16 / 2, WIDE, XL, YL>(p, a, stream);
+    return backward_v<T, 1, WIDE, XL, YL>(p, a, stream);
 }
 
 template <typename T>
 hipError_t run(const Plan &p, const Call &a, hipStream_t stream)
 {
-    if (p.xl) return p.yl ? run_layout<T, true, true>(p, a, stream) : run_layout<T, true, false>(p, a, stream);
-    return p.yl ? run_layout<T, false, true>(p, a, stream) : run_layout<T, false, false>(p, a, stream);
+    if (p.xl && p.yl) return run_layout<T, true, true, true>(p, a, stream);
+    if (!p.xl && !p.yl) return run_layout<T, true, false, false>(p, a, stream);
+    const bool wide = p.apply.vlast == 16 / (int)sizeof(T);
+    if (p.xl)
+        return wide ? run_layout<T, true, true, false>(p, a, stream) : run_layout<T, false, true, false>(p, a, stream);
+    return wide ? run_layout<T, true, false, true>(p, a, stream) : run_layout<T, false, false, true>(p, a, stream);
 }
 
 }  // namespace wtc_norm

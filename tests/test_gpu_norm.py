@@ -18,6 +18,8 @@ SHAPES = [
     (2, 33, 9, 11, 3), (3, 100, 37, 23, 20), (2, 96, 28, 28, 32), (1, 192, 14, 14, 32), (2, 64, 56, 56, 8),
     (1, 12, 131, 67, 4), (1, 16, 200, 200, 2), (70, 4, 6, 10, 2), (1, 256, 31, 33, 16), (2, 1030, 3, 3, 5),
     (1, 8, 256, 256, 1), (1, 520, 64, 64, 65),
+    # accesses of 8 bytes: four (two) elements divide the channels, the pixels or both
+    (2, 12, 14, 14, 3), (2, 36, 6, 7, 9), (1, 20, 66, 66, 5), (2, 10, 50, 62, 2), (1, 100, 64, 66, 4),
 ]
 
 
