@@ -40,24 +40,41 @@ constexpr int kThreads = 256;
 
 // Partial sums of |U|^2 in fp64 (fp32 squares would overflow from 2^64 on and
 // vanish below 2^-75), one for each of gridDim.x workgroups of a matrix, and
-// momentum_out.
-template <typename T>
+// momentum_out.  V elements an access (1 where addresses do not allow 4), four
+// accesses in flight.
+template <typename T, int V>
 __global__ __launch_bounds__(kThreads) void ortho_norm(const T *__restrict__ g, const float *momentum,
                                                        float *momentum_out, Blend bl, int64_t size,
                                                        double *__restrict__ parts)
 {
+    typedef T TV __attribute__((ext_vector_type(V)));
+    typedef float FV __attribute__((ext_vector_type(V)));
     __shared__ double lds[kThreads / 64];
-    const int64_t base = blockIdx.y * size;
+    const int64_t base = blockIdx.y * size, step = (int64_t)gridDim.x * kThreads * V;
     double a = 0.0;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < size; i += (int64_t)gridDim.x * kThreads) {
-        const T gv = g[base + i];
-        float m = 0.f;
-        if (bl.muon) {
-            m = fmaf(bl.mu, momentum[base + i], (1.f - bl.mu) * (float)gv);
-            momentum_out[base + i] = m;
-        }
-        const double u = blend(bl, gv, m);
-        a = fma(u, u, a);
+    for (int64_t i0 = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * V; i0 < size; i0 += 4 * step) {
+        TV gv[4];
+        FV mv[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i0 + k * step < size) {
+                gv[k] = *(const TV *)(g + base + i0 + k * step);
+                if (bl.muon) mv[k] = *(const FV *)(momentum + base + i0 + k * step);
+            }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i0 + k * step < size) {
+                if (bl.muon) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) mv[k][j] = fmaf(bl.mu, mv[k][j], (1.f - bl.mu) * (float)gv[k][j]);
+                    *(FV *)(momentum_out + base + i0 + k * step) = mv[k];
+                }
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const double u = blend(bl, gv[k][j], mv[k][j]);
+                    a = fma(u, u, a);
+                }
+            }
     }
     for (int o = 32; o; o >>= 1) a += __shfl_xor(a, o);
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = a;
@@ -102,41 +119,40 @@ __global__ __launch_bounds__(kThreads) void ortho_split(const T *__restrict__ g,
                                                         _Float16 *__restrict__ u, _Float16 *__restrict__ ut)
 {
     __shared__ float tile[64][65];
-    __shared__ double inv_s;
     const int t = threadIdx.x, z = blockIdx.y;
-    if (t < 64) {
-        double a = 0.0;
-        for (int i = t; i < nparts; i += 64) a += parts[z * nparts + i];
-        for (int o = 32; o; o >>= 1) a += __shfl_xor(a, o);
-        if (t == 0) inv_s = (double)S / (sqrt(a) + (double)eps);
-    }
-    __syncthreads();
-    const double inv = inv_s;
     const int64_t base = (int64_t)z * rows * cols;
-    const int r0 = blockIdx.x / (cp / 64) * 64, c0 = blockIdx.x % (cp / 64) * 64;
-#pragma unroll 4
-    for (int i = t >> 6; i < 64; i += 4) {
-        const int r = r0 + i, c = c0 + (t & 63);
-        float v = 0.f;
+    const int r0 = blockIdx.x / (cp / 64) * 64, c0 = blockIdx.x % (cp / 64) * 64, c = c0 + (t & 63);
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int r = r0 + (t >> 6) + i * 4;
+        v[i] = 0.f;
         if (r < rows && c < cols) {
             const int64_t e = base + (int64_t)r * cols + c;
-            v = (float)(blend(bl, g[e], bl.muon ? momentum_out[e] : 0.f) * inv);
+            v[i] = blend(bl, g[e], bl.muon ? momentum_out[e] : 0.f);
         }
-        tile[i][t & 63] = v;
     }
+    // every wave adds the parts for itself, in the same order
+    double a = 0.0;
+    for (int i = t & 63; i < nparts; i += 64) a += parts[z * nparts + i];
+    for (int o = 32; o; o >>= 1) a += __shfl_xor(a, o);
+    const double inv = (double)S / (sqrt(a) + (double)eps);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) tile[(t >> 6) + i * 4][t & 63] = (float)(v[i] * inv);
     __syncthreads();
     u += (int64_t)z * rp * cp * 2;
     ut += (int64_t)z * rp * cp * 2;
+#pragma unroll
     for (int i = t; i < 512; i += kThreads) {
-        float v[8];
+        float w[8];
         const int r = i >> 3, k = (i & 7) * 8;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = tile[r][k + j];
-        store8(u, r0 + r, c0 + k, cp, v);
-        const int c = i & 63, q = (i >> 6) * 8;
+        for (int j = 0; j < 8; ++j) w[j] = tile[r][k + j];
+        store8(u, r0 + r, c0 + k, cp, w);
+        const int q = i >> 3, l = (i & 7) * 8;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = tile[q + j][c];
-        store8(ut, c0 + c, r0 + q, rp, v);
+        for (int j = 0; j < 8; ++j) w[j] = tile[l + j][q];
+        store8(ut, c0 + q, r0 + l, rp, w);
     }
 }
 
@@ -539,8 +555,8 @@ Plan make_plan(const wtconv_ortho_desc_t &d)
     if (p.part < p.apply.bytes) p.part = p.apply.bytes;
     p.xbytes = align256((size_t)p.np * p.mp * 4 * d.batch);
     p.abytes = align256((size_t)p.np * p.np * 4 * d.batch);
-    const int64_t want = ((int64_t)p.n * p.m + 8 * kThreads - 1) / (8 * kThreads);
-    p.parts = (int)(want < 256 ? want : 256);
+    const int64_t want = ((int64_t)p.n * p.m + 16 * kThreads - 1) / (16 * kThreads);
+    p.parts = (int)(want < 1024 ? want : 1024);
     return p;
 }
 
@@ -586,8 +602,13 @@ hipError_t run(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &o, void *worksp
     float4 *part = (float4 *)(ws += align256(sizeof(double) * pl.parts * d.batch));
     const Blend bl = {o.hyper != nullptr, o.hyper ? o.hyper->nesterov : 0, o.hyper ? o.hyper->momentum : 0.f};
     const T *g = (const T *)o.g;
-    ortho_norm<T><<<dim3(pl.parts, batch), dim3(kThreads), 0, stream>>>(g, o.momentum, o.momentum_out, bl, size,
-                                                                        parts);
+    const bool wide = size % 4 == 0 && aligned_to(g, 4 * sizeof(T)) &&
+                      (!o.hyper || (aligned16(o.momentum) && aligned16(o.momentum_out)));
+    const dim3 ngrid((unsigned)pl.parts, batch);
+    if (wide)
+        ortho_norm<T, 4><<<ngrid, dim3(kThreads), 0, stream>>>(g, o.momentum, o.momentum_out, bl, size, parts);
+    else
+        ortho_norm<T, 1><<<ngrid, dim3(kThreads), 0, stream>>>(g, o.momentum, o.momentum_out, bl, size, parts);
     const int rp = pl.tall ? pl.mp : pl.np, cp = pl.tall ? pl.np : pl.mp;
     const float S = kScale;
     ortho_split<T><<<dim3((cp / 64) * (rp / 64), batch), dim3(kThreads), 0, stream>>>(

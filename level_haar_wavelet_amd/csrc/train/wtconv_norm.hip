@@ -138,7 +138,14 @@ int lcm_pow2(int per, int v)
 enum Walk { kPlanes, kLast, kTiles };
 
 constexpr int kLeastBytes = 8192;   // of one tensor, for a workgroup of the three-launch form
-constexpr int kTargetCount = 2048;  // such workgroups that the chip holds at once
+
+// Workgroups of the three-launch form, us for 1024 / 2048 / 4096 of them:
+//   last    forward 64x192x28x28 fp16 21.5 / 23.2 / 23.2, 64x96x56x56 fp16 27.7 /
+//           29.2 / 33.0, 32x128x128x128 fp32 181 / 157 / 158
+//   tiles   backward 64x96x56x56 fp32 68 / 79 / 66, 16x256x256x256 fp16 687 / 731 /
+//           620
+//   planes  within 2 %.
+int target_count(Walk w, int64_t bytes) { return w == kTiles ? 4096 : w == kLast && bytes < 64 << 20 ? 1024 : 2048; }
 
 // Whole groups of an image for each workgroup: cb channels, all pixels.
 Geometry one_geometry(Geometry g, int64_t n, Walk w, bool tiles, int v, int v16, int unit)
@@ -184,9 +191,9 @@ Geometry split_geometry(Geometry g, int64_t n, Walk w, int v, int esize)
         step = g.lanes * v;
     }
     g.blocks = (int)ceil_div(g.c, g.cb);
-    // as many workgroups as the chip holds at once, but no fewer bytes for one
-    // than kLeastBytes
-    const int64_t all = n * g.blocks, most = ceil_div(kTargetCount, all);
+    // that many workgroups, but no fewer bytes for one than kLeastBytes
+    const int64_t all = n * g.blocks;
+    const int64_t most = ceil_div(target_count(w, n * g.c * (int64_t)g.hw * esize), all);
     int64_t ppw = ceil_div(g.hw, most);
     const int64_t least = ceil_div(kLeastBytes, (int64_t)g.cb * esize);
     if (ppw < least) ppw = least;
