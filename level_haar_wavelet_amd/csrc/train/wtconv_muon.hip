@@ -367,7 +367,7 @@ __global__ __launch_bounds__(kThreads, 2) void product(Product a)
         return *(const half8 *)(lds + (s & 1) * kStage + b * kBlock + row * 128 + ((chunk ^ ((row >> 1) & 7)) * 16));
     };
 
-    float16v acc[RB][RB] = {};
+    float16v acc[RB][RB] = {}, term[2] = {};
     const int wi = Sh::kWavesK > 1 ? 0 : (wave >> 1) * Sh::kSide, wj = Sh::kWavesK > 1 ? 0 : (wave & 1) * Sh::kSide;
     const int b0 = Sh::kWavesK > 1 ? wave * KW : 0, lr = lane & 31, lc = lane >> 5;
     load(0);
@@ -393,14 +393,23 @@ __global__ __launch_bounds__(kThreads, 2) void product(Product a)
         for (int b = 0; b < KW; ++b) {
             if (KB > 1 && s * KB + b0 + b >= blocks) continue;  // the last stage's missing blocks
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
+            for (int kk = 0; kk < 2; ++kk) {
+                if constexpr (RB == 1) {  // an accumulator for each term: none waits for the one before
+                    term[0] = mfma(l[b][kk][0][0], r[b][kk][0][1], term[0]);
+                    term[1] = mfma(l[b][kk][0][1], r[b][kk][0][0], term[1]);
+                    acc[0][0] = mfma(l[b][kk][0][0], r[b][kk][0][0], acc[0][0]);
+                } else {
 #pragma unroll
-                for (int i = 0; i < RB; ++i)
+                    for (int i = 0; i < RB; ++i)
 #pragma unroll
-                    for (int j = 0; j < RB; ++j)
-                        acc[i][j] = mfma3(l[b][kk][i][0], l[b][kk][i][1], r[b][kk][j][0], r[b][kk][j][1], acc[i][j]);
+                        for (int j = 0; j < RB; ++j)
+                            acc[i][j] =
+                                mfma3(l[b][kk][i][0], l[b][kk][i][1], r[b][kk][j][0], r[b][kk][j][1], acc[i][j]);
+                }
+            }
         }
     }
+    if (RB == 1) acc[0][0] += term[0] + term[1];
 
     if (slice >= 0) {
         float4 *p = a.part + ((int64_t)(g - a.full) * a.slices + slice) * (RB * RB * 4 * kThreads) + t;

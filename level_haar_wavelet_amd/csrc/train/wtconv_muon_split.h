@@ -46,12 +46,15 @@ __device__ inline void split(float v, _Float16 &hi, _Float16 &lo)
     lo = (_Float16)(v - (float)hi);
 }
 
+__device__ inline float16v mfma(const half8 &l, const half8 &r, float16v c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(l, r, c, 0, 0, 0);
+}
+
 // c += l r of 32 x 32 x 16 with split factors (lo lo is below their 22 bits).
 __device__ inline float16v mfma3(const half8 &lhi, const half8 &llo, const half8 &rhi, const half8 &rlo, float16v c)
 {
-    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(lhi, rlo, c, 0, 0, 0);
-    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(llo, rhi, c, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(lhi, rhi, c, 0, 0, 0);
+    return mfma(lhi, rhi, mfma(llo, rhi, mfma(lhi, rlo, c)));
 }
 
 // The whole iteration of a matrix in one workgroup, where one can hold it.
