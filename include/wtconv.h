@@ -234,7 +234,7 @@ wtconv_status_t wtconv_unfused_backward_weight(const wtconv_desc_t *desc, const 
  *              be NULL (ones, zeros); mean, rstd [N][groups] fp32.  All sums,
  *              statistics and products are fp32 (or wider); an output element
  *              is rounded once.
- * Shape rules  n, c, h, w >= 1, groups >= 1 divides c, c * h * w < 2^31,
+ * Shape rules  n, c, h, w >= 1, groups >= 1 divides c, c * h * w <= 2^31 - 2^16,
  *              n * c < 2^23, eps > 0 and finite.
  * Alignment    activations are aligned to their element; any such address
  *              works, 16-byte aligned ones are faster.

@@ -217,6 +217,16 @@ def wtconv_backward_weight_noalloc(x, dy, w_base, bias, s_base, w_lvl, s_lvl, gr
     return dw0, db0, ds0, dwl, dsl
 
 
-from ._train import (wtconv_group_norm_backward, wtconv_group_norm_forward,  # noqa: E402
-                     wtconv_group_norm_workspace_size, wtconv_muon_step, wtconv_orthogonalize,
-                     wtconv_orthogonalize_workspace_size)
+
+# bound at their first use: their module imports torch, this one does not
+_TRAIN = ("wtconv_group_norm_forward", "wtconv_group_norm_backward", "wtconv_group_norm_workspace_size",
+          "wtconv_orthogonalize", "wtconv_muon_step", "wtconv_orthogonalize_workspace_size")
+
+
+def __getattr__(name):
+    if name in _TRAIN:
+        from . import _train
+
+        globals().update({n: getattr(_train, n) for n in _TRAIN})
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

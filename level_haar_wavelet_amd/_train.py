@@ -15,22 +15,16 @@ from __future__ import annotations
 import ctypes
 import functools
 
+import torch
+
 from . import _native
 
-_DTYPES = None
-
-
-def _torch():
-    import torch
-
-    return torch
+_DTYPES = {torch.float32: _native.F32, torch.float16: _native.F16, torch.bfloat16: _native.BF16}
+_F32 = torch.float32
+_Tensor = torch.Tensor
 
 
 def _dtype_code(t, name):
-    global _DTYPES
-    if _DTYPES is None:
-        torch = _torch()
-        _DTYPES = {torch.float32: _native.F32, torch.float16: _native.F16, torch.bfloat16: _native.BF16}
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError("%s must be float32, float16 or bfloat16, got %s" % (name, t.dtype))
@@ -42,8 +36,7 @@ def _ptr(t):
 
 
 def _gpu_tensor(t, name, device=None):
-    torch = _torch()
-    if not torch.is_tensor(t) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError("%s must be a GPU tensor" % name)
     if device is not None and t.device != device:
         raise TypeError("%s lies on %s, the other tensors on %s" % (name, t.device, device))
@@ -52,8 +45,9 @@ def _gpu_tensor(t, name, device=None):
 def _f32(t, name, shape, device):
     if t is None:
         return
-    _gpu_tensor(t, name, device)
-    if t.dtype != _torch().float32 or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if not isinstance(t, _Tensor) or t.dtype is not _F32 or t.shape != shape or t.device != device or \
+            not t.is_contiguous():
+        _gpu_tensor(t, name, device)
         raise TypeError("%s must be a contiguous float32 tensor of shape %s" % (name, tuple(shape)))
 
 
@@ -62,7 +56,7 @@ def _workspace(workspace, need, device):
     if workspace is None:
         if need == 0:
             return None, 0
-        workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
+        return torch.empty(need, dtype=torch.uint8, device=device), need
     _gpu_tensor(workspace, "workspace", device)
     if not workspace.is_contiguous():
         raise TypeError("workspace must be contiguous")
@@ -78,12 +72,12 @@ class _On:
     __slots__ = ("handle", "guard", "other")
 
     def __init__(self, device, stream):
-        cuda = _torch().cuda
+        cuda = torch.cuda
         self.guard = None if cuda.current_device() == device.index else cuda.device(device)
         self.other = stream
         if stream is None:
             # the current stream's handle without a Stream object (2 us less)
-            self.handle = _torch()._C._cuda_getCurrentRawStream(device.index)
+            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
         elif stream.device != device:
             raise TypeError("the stream belongs to %s, the tensors lie on %s" % (stream.device, device))
         else:
@@ -109,7 +103,6 @@ class _On:
 
 def _layout_of(t, name):
     """WTCONV_NCHW or WTCONV_NHWC of a 4-d tensor without gaps."""
-    torch = _torch()
     if t.dim() != 4:
         raise TypeError("%s must be an (N, C, H, W) tensor" % name)
     if t.is_contiguous():
@@ -125,7 +118,6 @@ def _one_layout(t):
 
 
 def _like(t, layout):
-    torch = _torch()
     fmt = torch.channels_last if layout == _native.NHWC else torch.contiguous_format
     return torch.empty_like(t, memory_format=fmt)
 
@@ -159,7 +151,6 @@ def wtconv_group_norm_forward(x, groups, gamma=None, beta=None, eps=1e-5, act="n
     `channels_last` is True / False (or in the layout of `y`, if given).  gamma,
     beta: (C,) float32 or None.  act: "none", "relu", "silu" or "gelu" (erf).
     mean, rstd: (N, groups) float32, for the backward call."""
-    torch = _torch()
     lib = _native.load()
     _gpu_tensor(x, "x")
     xl = _layout_of(x, "x")
@@ -187,7 +178,7 @@ def wtconv_group_norm_forward(x, groups, gamma=None, beta=None, eps=1e-5, act="n
         if mean is None:
             made.append(mean := torch.empty((n, groups), dtype=torch.float32, device=x.device))
         if rstd is None:
-            made.append(rstd := torch.empty((n, groups), dtype=torch.float32, device=x.device))
+            made.append(rstd := torch.empty_like(mean))
         ws, nbytes = _workspace(workspace, need, x.device)
         st = lib.wtconv_group_norm_forward(d, _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean),
                                            _ptr(rstd), _ptr(ws), nbytes, s)
@@ -201,7 +192,6 @@ def wtconv_group_norm_backward(x, dy, groups, mean, rstd, gamma=None, beta=None,
     """(dx, dgamma, dbeta) of the forward call whose x, mean, rstd, gamma, beta
     and act these are.  dy may lie in either layout; dx lies as x does.
     dgamma, dbeta: (C,) float32, also where gamma or beta is None."""
-    torch = _torch()
     lib = _native.load()
     _gpu_tensor(x, "x")
     _gpu_tensor(dy, "dy", x.device)
@@ -230,7 +220,7 @@ def wtconv_group_norm_backward(x, dy, groups, mean, rstd, gamma=None, beta=None,
         if dgamma is None:
             made.append(dgamma := torch.empty((c,), dtype=torch.float32, device=x.device))
         if dbeta is None:
-            made.append(dbeta := torch.empty((c,), dtype=torch.float32, device=x.device))
+            made.append(dbeta := torch.empty_like(dgamma))
         ws, nbytes = _workspace(workspace, need, x.device)
         st = lib.wtconv_group_norm_backward(d, _ptr(x), _ptr(dy), _ptr(gamma), _ptr(beta), _ptr(mean),
                                             _ptr(rstd), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(ws), nbytes, s)
@@ -283,7 +273,7 @@ def wtconv_orthogonalize(g, steps=5, eps=1e-7, out=None, workspace=None, stream=
     with on as s:
         made = None
         if out is None:
-            made = out = _torch().empty_like(g)
+            made = out = torch.empty_like(g)
         ws, nbytes = _workspace(workspace, need, g.device)
         st = lib.wtconv_orthogonalize(d, _ptr(g), _ptr(out), _ptr(ws), nbytes, s)
         on.made(ws if workspace is None else None, made)

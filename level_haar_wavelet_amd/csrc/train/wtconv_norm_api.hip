@@ -12,7 +12,8 @@ size_t esize(int dtype) { return dtype == WTCONV_F32 ? 4 : 2; }
 wtconv_status_t check_desc(const wtconv_norm_desc_t *d)
 {
     if (!d) return WTCONV_ERR_NULL;
-    const int64_t lim = ((int64_t)1 << 31) - 1;
+    // below 2^31 by more than a batch of accesses, so that their indexes do not wrap
+    const int64_t lim = ((int64_t)1 << 31) - (1 << 16);
     if (d->n < 1 || d->c < 1 || d->h < 1 || d->w < 1 || d->groups < 1) return WTCONV_ERR_SHAPE;
     if (d->n > lim || d->c > lim || d->h > lim || d->w > lim) return WTCONV_ERR_SHAPE;
     if (d->c % d->groups) return WTCONV_ERR_SHAPE;

@@ -39,7 +39,8 @@ class Muon(torch.optim.Optimizer):
     with O the Newton-Schulz iteration of `steps` steps and
     s = sqrt(max(1, rows / cols)).  Parameters are contiguous float32 tensors on
     the GPU.  The hyperparameters go by value: a step captured into a graph
-    replays with those it was captured with."""
+    replays with those it was captured with, and only after a step outside one
+    (the momentum's zeros would be part of the graph)."""
 
     def __init__(self, params, lr=0.02, momentum=0.95, weight_decay=0.0, nesterov=True, steps=5, eps=1e-7,
                  batch_dims=None):
@@ -75,6 +76,9 @@ class Muon(torch.optim.Optimizer):
                     raise TypeError("Muon takes contiguous parameters")
                 state = self.state[p]
                 if "momentum_buffer" not in state:
+                    if torch.cuda.is_current_stream_capturing():
+                        raise RuntimeError("the first step of a parameter cannot be captured: every replay would "
+                                           "start from a momentum of zero")
                     state["momentum_buffer"] = torch.zeros_like(p)
                 wtconv_muon_step(p.view(shape), p.grad.contiguous().view(shape),
                                  state["momentum_buffer"].view(shape), lr=group["lr"], mu=group["momentum"],

@@ -246,3 +246,56 @@ def test_optimizer_on_the_layer_and_its_state():
     again = Muon(params, lr=0.1)
     again.load_state_dict(opt.state_dict())
     assert torch.equal(again.state[params[1]]["momentum_buffer"], opt.state[params[1]]["momentum_buffer"])
+
+
+def test_a_first_step_is_not_captured():
+    from level_haar_wavelet_amd.optim import Muon
+
+    p = torch.nn.Parameter(torch.randn(8, 12, device="cuda"))
+    p.grad = torch.randn_like(p)
+    opt = Muon([p], lr=0.1)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        graph.capture_begin()
+        with pytest.raises(RuntimeError, match="cannot be captured"):
+            opt.step()
+        p.grad.mul_(1.0)  # a capture that holds something
+        graph.capture_end()
+    torch.cuda.current_stream().wait_stream(s)
+    before = p.detach().clone()
+    opt.step()  # and an ordinary step still runs
+    assert not torch.equal(p, before)
+
+
+def test_two_graphs_with_their_own_workspaces_run_side_by_side():
+    """Two captured orthogonalisations replayed on two streams at once: each has
+    its own workspace and gives its own result, every time."""
+    gs = [gradient((1, 300, 260), k).cuda() for k in (1, 2)]
+    ref = [wt.wtconv_orthogonalize(g) for g in gs]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for g in gs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(wt.wtconv_orthogonalize(g))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in gs]
+    for _ in range(4):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, r) for o, r in zip(outs, ref))
+
+
+def test_a_long_narrow_matrix_and_a_large_stack():
+    """2^20 columns of 3 rows (the sum over k is long), and 4000 matrices of 7 x 9
+    in one call."""
+    for shape in ((1, 3, 1 << 20), (4000, 7, 9)):
+        g = gradient(shape, 3)
+        within(wt.wtconv_orthogonalize(g.cuda()), ortho64(g), 5, torch.float32, str(shape))

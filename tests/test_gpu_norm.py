@@ -14,7 +14,7 @@ ACTS = ["none", "relu", "silu", "gelu"]
 # counts that 16-byte vectors do and do not divide; planes shorter than a wave,
 # odd ones, ones that several workgroups share; many images
 SHAPES = [
-    (1, 1, 1, 1, 1), (2, 6, 1, 1, 3), (3, 5, 1, 7, 5), (2, 8, 16, 16, 4), (2, 8, 4, 4, 1), (1, 24, 3, 5, 24),
+    (1, 1, 1, 1, 1), (2, 1, 9, 10, 1), (2, 6, 1, 1, 3), (3, 5, 1, 7, 5), (2, 8, 16, 16, 4), (2, 8, 4, 4, 1), (1, 24, 3, 5, 24),
     (2, 33, 9, 11, 3), (3, 100, 37, 23, 20), (2, 96, 28, 28, 32), (1, 192, 14, 14, 32), (2, 64, 56, 56, 8),
     (1, 12, 131, 67, 4), (1, 16, 200, 200, 2), (70, 4, 6, 10, 2), (1, 256, 31, 33, 16), (2, 1030, 3, 3, 5),
     (1, 8, 256, 256, 1), (1, 520, 64, 64, 65),

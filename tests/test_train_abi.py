@@ -28,7 +28,8 @@ def ortho_desc(batch=1, rows=80, cols=120, dtype=0, steps=5, eps=1e-7):
 BAD_NORM = [
     (dict(n=0), SHAPE), (dict(c=0), SHAPE), (dict(h=0), SHAPE), (dict(w=-1), SHAPE), (dict(groups=0), SHAPE),
     (dict(groups=3), SHAPE), (dict(groups=16), SHAPE), (dict(h=1 << 20, w=1 << 20), SHAPE),
-    (dict(c=1 << 16, h=1 << 8, w=1 << 8, groups=1), SHAPE), (dict(n=1 << 20, c=8), SHAPE),
+    (dict(c=1 << 16, h=1 << 8, w=1 << 8, groups=1), SHAPE),
+    (dict(c=1, h=1, w=(1 << 31) - 1, groups=1), SHAPE), (dict(n=1 << 62, c=2), SHAPE), (dict(n=1 << 20, c=8), SHAPE),
     (dict(n=1 << 62), SHAPE), (dict(h=1 << 62), SHAPE), (dict(eps=0.0), SHAPE), (dict(eps=-1.0), SHAPE),
     (dict(eps=float("nan")), SHAPE), (dict(eps=float("inf")), SHAPE), (dict(dtype=3), UNSUPPORTED),
     (dict(dtype=-1), UNSUPPORTED), (dict(act=4), UNSUPPORTED), (dict(act=-1), UNSUPPORTED), (dict(xl=2), UNSUPPORTED),
