@@ -19,6 +19,7 @@ struct Geometry {
     int c, hw, groups, per, act;
     int cb, blocks, ppw, splits, lanes;
     int vlast;      // tiles: channels of an access to the tensor that lies channels last
+    bool stream;    // the tensors are larger than the L2s together
     int64_t count;  // workgroups of all images
 };
 

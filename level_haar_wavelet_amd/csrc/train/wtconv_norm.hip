@@ -219,6 +219,7 @@ Plan make_plan(const wtconv_norm_desc_t &d, bool bwd, bool aligned)
     g.groups = d.groups;
     g.per = g.c / g.groups;
     g.act = d.act;
+    g.stream = d.n * d.c * (int64_t)g.hw * esize > 32 << 20;
     const Walk sw = p.xl ? kLast : kPlanes, aw = p.xl != p.yl ? kTiles : sw;
     // the widest access that rows and addresses allow: rows of channels, of
     // pixels, or in tiles (the planes' side) of pixels

@@ -55,6 +55,32 @@ __device__ inline typename Pack<T, V>::type fetch(const T *p)
     return *(const typename Pack<T, V>::type *)p;
 }
 
+// The same for the last read of a value, and a store of what this call does not
+// read again: where the tensor is larger than the L2s (STREAM), past them, so
+// that they keep what is still to be read.  us with and without, of inputs not
+// in the caches: forward 64x96x56x56 fp32 42 / 53, 16x256x256x256 fp16 281 /
+// 327, its backward 499 / 549; below that size no difference, and the output
+// stays for its reader.
+// (A constant of the instance: where it is known at run time only, the compiler
+// makes one plain access of both.)
+template <bool STREAM, typename P>
+__device__ inline P fetch_last(const P *p)
+{
+    if constexpr (STREAM)
+        return __builtin_nontemporal_load(p);
+    else
+        return *p;
+}
+
+template <bool STREAM, typename P>
+__device__ inline void store_last(P *p, const P &v)
+{
+    if constexpr (STREAM)
+        __builtin_nontemporal_store(v, p);
+    else
+        *p = v;
+}
+
 template <typename T, int V>
 __device__ inline void values(const typename Pack<T, V>::type &r, float (&v)[V])
 {
@@ -65,7 +91,7 @@ __device__ inline void values(const typename Pack<T, V>::type &r, float (&v)[V])
         for (int i = 0; i < V; ++i) v[i] = (float)r[i];
 }
 
-template <typename T, int V>
+template <typename T, int V, bool STREAM>
 __device__ inline void store(T *p, const float (&v)[V])
 {
     typename Pack<T, V>::type r;
@@ -74,7 +100,7 @@ __device__ inline void store(T *p, const float (&v)[V])
     else
 #pragma unroll
         for (int i = 0; i < V; ++i) r[i] = (T)v[i];
-    *(typename Pack<T, V>::type *)p = r;
+    store_last<STREAM>((typename Pack<T, V>::type *)p, r);
 }
 
 // Phi(z) = (1 + erf(z / sqrt 2)) / 2 and e = exp(-z^2 / 2), by Abramowitz and
@@ -83,12 +109,12 @@ __device__ inline void store(T *p, const float (&v)[V])
 // pass needs the exponential in any case.
 __device__ inline float normal_cdf(float z, float &e)
 {
-    const float x = fabsf(z) * 0.70710678f;
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
-    e = __expf(-x * x);
-    const float q =
-        t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
-    const float tail = 0.5f * q * e;
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.f));
+    e = __builtin_amdgcn_exp2f(z * z * -0.72134752f);  // log2(e) / 2
+    // half the polynomial, the halves of a1 .. a5
+    const float q = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5307027145f, -0.7265760135f), 0.7107068705f), -0.142248368f),
+                             0.127414796f);
+    const float tail = q * e;
     return z < 0.f ? tail : 1.f - tail;
 }
 
@@ -335,7 +361,7 @@ __device__ inline T *tile_at(char *tile, int p, int j)
 
 // Brings the tile (pixels p0.., channels c0..) of a channels-last tensor into
 // LDS, or back out of it, V channels at a time.
-template <typename T, int V, int NT, bool OUT>
+template <typename T, int V, int NT, bool OUT, bool STREAM>
 __device__ inline void move_pieces(T *t_, const Geometry &g, const Range &r, int p0, int c0, char *tile)
 {
     constexpr int V16 = 16 / sizeof(T), kSide = 8 * V16, kChunks = kSide / V, kOwn = (kSide * kChunks + NT - 1) / NT;
@@ -350,28 +376,32 @@ __device__ inline void move_pieces(T *t_, const Geometry &g, const Range &r, int
 #pragma unroll
     for (int o = 0; o < kOwn; ++o) {
         const int e = threadIdx.x + o * NT;
-        if (inside(e)) v[o] = OUT ? *in_tile(e) : *in_memory(e);
+        if (inside(e)) v[o] = OUT ? *in_tile(e) : fetch_last<STREAM>((const P *)in_memory(e));
     }
 #pragma unroll
     for (int o = 0; o < kOwn; ++o) {
         const int e = threadIdx.x + o * NT;
-        if (inside(e)) *(OUT ? in_memory(e) : in_tile(e)) = v[o];
+        if (!inside(e)) continue;
+        if (OUT)
+            store_last<STREAM>(in_memory(e), v[o]);
+        else
+            *in_tile(e) = v[o];
     }
 }
 
 // The width follows the channels alone: the planes' side may need another.
 // WIDE: it is 16 bytes (an instance of its own: the registers of the narrow ones
 // would cost it a third of its waves).
-template <typename T, bool WIDE, int NT, bool OUT>
+template <typename T, bool WIDE, int NT, bool OUT, bool STREAM = false>
 __device__ inline void move_tile(T *t_, const Geometry &g, const Range &r, int p0, int c0, char *tile)
 {
     constexpr int V16 = 16 / sizeof(T);
     if constexpr (WIDE)
-        move_pieces<T, V16, NT, OUT>(t_, g, r, p0, c0, tile);
+        move_pieces<T, V16, NT, OUT, STREAM>(t_, g, r, p0, c0, tile);
     else if (g.vlast == V16 / 2)
-        move_pieces<T, V16 / 2, NT, OUT>(t_, g, r, p0, c0, tile);
+        move_pieces<T, V16 / 2, NT, OUT, STREAM>(t_, g, r, p0, c0, tile);
     else
-        move_pieces<T, 1, NT, OUT>(t_, g, r, p0, c0, tile);
+        move_pieces<T, 1, NT, OUT, STREAM>(t_, g, r, p0, c0, tile);
 }
 
 // The pieces of V pixels of a tile that a thread takes in the order of planes.
@@ -398,7 +428,7 @@ struct Pieces {
 // ---- The passes of a range -------------------------------------------------------
 
 // y of the range.
-template <typename T, int V, bool WIDE, int NT, bool XL, bool YL>
+template <typename T, int V, bool WIDE, bool STREAM, int NT, bool XL, bool YL>
 __device__ inline void apply(const T *__restrict__ x, T *__restrict__ y, const Geometry &g, const Range &r,
                              const Chan *lk, char *tile)
 {
@@ -416,7 +446,7 @@ __device__ inline void apply(const T *__restrict__ x, T *__restrict__ y, const G
                         k[i].rstd *= k[i].gamma;
                     }
             },
-            [&](int u, int64_t at) { raw[u] = fetch<T, V>(x + at); },
+            [&](int u, int64_t at) { raw[u] = fetch_last<STREAM>((const typename Pack<T, V>::type *)(x + at)); },
             [&](int u, int64_t at, bool) {
                 float v[V];
                 values<T, V>(raw[u], v);
@@ -426,7 +456,7 @@ __device__ inline void apply(const T *__restrict__ x, T *__restrict__ y, const G
                     v[i] = fmaf(v[i] - q.mean, q.rstd, q.beta);
                 }
                 act_fwd<V>(g.act, v);
-                store<T, V>(y + at, v);
+                store<T, V, STREAM>(y + at, v);
             },
             [](int) {});
     } else {
@@ -439,10 +469,10 @@ __device__ inline void apply(const T *__restrict__ x, T *__restrict__ y, const G
                 if (!XL)
 #pragma unroll
                     for (int o = 0; o < P::kOwn; ++o)
-                        if (w.inside(o)) raw[o] = fetch<T, V>(x + w.at(g, o));
+                        if (w.inside(o)) raw[o] = fetch_last<STREAM>((const typename Pack<T, V>::type *)(x + w.at(g, o)));
                 __syncthreads();  // the tile before is read
                 if (XL) {
-                    move_tile<T, WIDE, NT, false>(const_cast<T *>(x), g, r, p0, c0, tile);
+                    move_tile<T, WIDE, NT, false, STREAM>(const_cast<T *>(x), g, r, p0, c0, tile);
                     __syncthreads();
                 }
 #pragma unroll
@@ -460,14 +490,14 @@ __device__ inline void apply(const T *__restrict__ x, T *__restrict__ y, const G
                     for (int i = 0; i < V; ++i) v[i] = fmaf(v[i] - k.mean, a, k.beta);
                     act_fwd<V>(g.act, v);
                     if (XL)
-                        store<T, V>(y + w.at(g, o), v);
+                        store<T, V, STREAM>(y + w.at(g, o), v);
                     else
 #pragma unroll
                         for (int i = 0; i < V; ++i) *tile_at<T, V16>(tile, w.pixel(o) + i, w.channel(o)) = (T)v[i];
                 }
                 if (!XL) {
                     __syncthreads();
-                    move_tile<T, WIDE, NT, true>(y, g, r, p0, c0, tile);
+                    move_tile<T, WIDE, NT, true, STREAM>(y, g, r, p0, c0, tile);
                 }
             }
     }
@@ -562,7 +592,7 @@ __device__ inline void sums_bwd(const T *__restrict__ x, const T *__restrict__ d
 }
 
 // dx of the range; q: the group's means of t and t xh, by channel.
-template <typename T, int V, bool WIDE, int NT, bool XL, bool YL>
+template <typename T, int V, bool WIDE, bool STREAM, int NT, bool XL, bool YL>
 __device__ inline void apply_bwd(const T *__restrict__ x, const T *__restrict__ dy, T *__restrict__ dx,
                                  const Geometry &g, const Range &r, const Chan *lk, const float2 *lq,
                                  char *tile)
@@ -588,8 +618,8 @@ __device__ inline void apply_bwd(const T *__restrict__ x, const T *__restrict__ 
                     }
             },
             [&](int u, int64_t at) {
-                rx[u] = fetch<T, V>(x + at);
-                rd[u] = fetch<T, V>(dy + at);
+                rx[u] = fetch_last<STREAM>((const typename Pack<T, V>::type *)(x + at));
+                rd[u] = fetch_last<STREAM>((const typename Pack<T, V>::type *)(dy + at));
             },
             [&](int u, int64_t at, bool) {
                 float v[V], d[V];
@@ -597,7 +627,7 @@ __device__ inline void apply_bwd(const T *__restrict__ x, const T *__restrict__ 
                 values<T, V>(rd[u], d);
 #pragma unroll
                 for (int i = 0; i < V; ++i) v[i] = value(v[i], d[i], k[XL ? i : 0], q[XL ? i : 0]);
-                store<T, V>(dx + at, v);
+                store<T, V, STREAM>(dx + at, v);
             },
             [](int) {});
     } else {
@@ -609,9 +639,9 @@ __device__ inline void apply_bwd(const T *__restrict__ x, const T *__restrict__ 
                 typename Pack<T, V>::type raw[P::kOwn];
 #pragma unroll
                 for (int o = 0; o < P::kOwn; ++o)
-                    if (w.inside(o)) raw[o] = fetch<T, V>((XL ? dy : x) + w.at(g, o));
+                    if (w.inside(o)) raw[o] = fetch_last<STREAM>((const typename Pack<T, V>::type *)((XL ? dy : x) + w.at(g, o)));
                 __syncthreads();
-                move_tile<T, WIDE, NT, false>(const_cast<T *>(XL ? x : dy), g, r, p0, c0, tile);
+                move_tile<T, WIDE, NT, false, STREAM>(const_cast<T *>(XL ? x : dy), g, r, p0, c0, tile);
                 __syncthreads();
 #pragma unroll
                 for (int o = 0; o < P::kOwn; ++o) {
@@ -626,11 +656,11 @@ __device__ inline void apply_bwd(const T *__restrict__ x, const T *__restrict__ 
                         v[i] = XL ? value((float)*u, v[i], k, q) : value(v[i], (float)*u, k, q);
                         if (XL) *u = (T)v[i];
                     }
-                    if (!XL) store<T, V>(dx + w.at(g, o), v);
+                    if (!XL) store<T, V, STREAM>(dx + w.at(g, o), v);
                 }
                 if (XL) {
                     __syncthreads();
-                    move_tile<T, WIDE, NT, true>(dx, g, r, p0, c0, tile);
+                    move_tile<T, WIDE, NT, true, STREAM>(dx, g, r, p0, c0, tile);
                 }
             }
     }
@@ -663,7 +693,7 @@ __device__ inline void load_consts(Chan *lk, const Geometry &g, const Range &r, 
     __syncthreads();
 }
 
-template <typename T, int V, bool WIDE, bool XL, bool YL>
+template <typename T, int V, bool WIDE, bool STREAM, bool XL, bool YL>
 __global__ __launch_bounds__(kThreads) void norm_apply(const T *__restrict__ x, const float *__restrict__ gamma,
                                                        const float *__restrict__ beta,
                                                        const float *__restrict__ mean,
@@ -673,7 +703,7 @@ __global__ __launch_bounds__(kThreads) void norm_apply(const T *__restrict__ x, 
     __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
     const Range r = range_of(g, kBack);
     load_consts(lk, g, r, gamma, beta, mean, rstd);
-    apply<T, V, WIDE, kThreads, XL, YL>(x, y, g, r, lk, tile);
+    apply<T, V, WIDE, STREAM, kThreads, XL, YL>(x, y, g, r, lk, tile);
 }
 
 template <typename T, int V, bool WIDE, bool XL, bool YL>
@@ -693,7 +723,7 @@ __global__ __launch_bounds__(kThreads) void norm_sums_bwd(const T *__restrict__ 
                                      [&](int c, const float2 &s) { part[r.row * g.c + c] = s; });
 }
 
-template <typename T, int V, bool WIDE, bool XL, bool YL>
+template <typename T, int V, bool WIDE, bool STREAM, bool XL, bool YL>
 __global__ __launch_bounds__(kThreads) void norm_apply_bwd(const T *__restrict__ x, const T *__restrict__ dy,
                                                            const float *__restrict__ gamma,
                                                            const float *__restrict__ beta,
@@ -708,7 +738,7 @@ __global__ __launch_bounds__(kThreads) void norm_apply_bwd(const T *__restrict__
     const Range r = range_of(g, kBack);
     for (int i = threadIdx.x; i < r.cb; i += kThreads) lq[i] = means[r.n * g.groups + (r.c0 + i) / g.per];
     load_consts(lk, g, r, gamma, beta, mean, rstd);
-    apply_bwd<T, V, WIDE, kThreads, XL, YL>(x, dy, dx, g, r, lk, lq, tile);
+    apply_bwd<T, V, WIDE, STREAM, kThreads, XL, YL>(x, dy, dx, g, r, lk, lq, tile);
 }
 
 // ---- One launch ----------------------------------------------------------------------
@@ -727,7 +757,7 @@ __device__ inline void join_groups(const Geometry &g, const Range &r, V value, S
     }
 }
 
-template <typename T, int V, bool WIDE, bool XL, bool YL>
+template <typename T, int V, bool WIDE, bool STREAM, bool XL, bool YL>
 __global__ __launch_bounds__(kOneThreads) void norm_one(const T *__restrict__ x, const float *__restrict__ gamma,
                                                         const float *__restrict__ beta, T *__restrict__ y,
                                                         float *__restrict__ mean, float *__restrict__ rstd, Geometry g,
@@ -762,10 +792,10 @@ __global__ __launch_bounds__(kOneThreads) void norm_one(const T *__restrict__ x,
         lk[i].beta = beta ? beta[c] : 0.f;
     }
     __syncthreads();
-    apply<T, V, WIDE, kOneThreads, XL, YL>(x, y, ga, r, lk, tile);
+    apply<T, V, WIDE, STREAM, kOneThreads, XL, YL>(x, y, ga, r, lk, tile);
 }
 
-template <typename T, int V, bool WIDE, bool XL, bool YL>
+template <typename T, int V, bool WIDE, bool STREAM, bool XL, bool YL>
 __global__ __launch_bounds__(kOneThreads) void norm_one_bwd(const T *__restrict__ x, const T *__restrict__ dy,
                                                             const float *__restrict__ gamma,
                                                             const float *__restrict__ beta,
@@ -795,63 +825,71 @@ __global__ __launch_bounds__(kOneThreads) void norm_one_bwd(const T *__restrict_
     for (int i = threadIdx.x; i < r.cb; i += kOneThreads)
         if (i % g.per) lq[i] = lq[i - i % g.per];
     __syncthreads();
-    apply_bwd<T, V, WIDE, kOneThreads, XL, YL>(x, dy, dx, g, r, lk, lq, tile);
+    apply_bwd<T, V, WIDE, STREAM, kOneThreads, XL, YL>(x, dy, dx, g, r, lk, lq, tile);
 }
 
 // ---- Launches ------------------------------------------------------------------------
 
-template <typename T, int V, bool WIDE, bool XL, bool YL>
+template <typename T, int V, bool WIDE, bool STREAM, bool XL, bool YL>
 hipError_t forward_v(const Plan &p, const Call &a, hipStream_t stream)
 {
+    const T *x = (const T *)a.x;
     if (p.one) {
-        norm_one<T, V, WIDE, XL, YL><<<dim3((unsigned)p.apply.count), dim3(kOneThreads), 0, stream>>>(
-            (const T *)a.x, a.gamma, a.beta, (T *)a.out, a.mean_out, a.rstd_out, p.stats, p.apply, p.eps);
+        norm_one<T, V, WIDE, STREAM, XL, YL><<<dim3((unsigned)p.apply.count), dim3(kOneThreads), 0, stream>>>(
+            x, a.gamma, a.beta, (T *)a.out, a.mean_out, a.rstd_out, p.stats, p.apply, p.eps);
         return hipGetLastError();
     }
     const dim3 th(kThreads);
     float2 *part = (float2 *)a.workspace;
-    norm_moments<T, V, XL><<<dim3((unsigned)p.stats.count), th, 0, stream>>>((const T *)a.x, p.stats, part);
+    norm_moments<T, V, XL><<<dim3((unsigned)p.stats.count), th, 0, stream>>>(x, p.stats, part);
     launch_finish_forward(p.stats, a.n, part, a.mean_out, a.rstd_out, p.eps, stream);
-    norm_apply<T, V, WIDE, XL, YL><<<dim3((unsigned)p.apply.count), th, 0, stream>>>(
-        (const T *)a.x, a.gamma, a.beta, a.mean_out, a.rstd_out, (T *)a.out, p.apply);
+    norm_apply<T, V, WIDE, STREAM, XL, YL><<<dim3((unsigned)p.apply.count), th, 0, stream>>>(
+        x, a.gamma, a.beta, a.mean_out, a.rstd_out, (T *)a.out, p.apply);
     return hipGetLastError();
 }
 
-template <typename T, int V, bool WIDE, bool XL, bool YL>
+template <typename T, int V, bool WIDE, bool STREAM, bool XL, bool YL>
 hipError_t backward_v(const Plan &p, const Call &a, hipStream_t stream)
 {
     const Geometry &g = p.apply;
+    const T *x = (const T *)a.x, *dy = (const T *)a.dy;
     float2 *part = (float2 *)a.workspace, *means = (float2 *)((char *)a.workspace + p.means_at);
     if constexpr (XL == YL) {
         if (p.one) {
             float2 *sums = a.dgamma || a.dbeta ? part : nullptr;
-            norm_one_bwd<T, V, WIDE, XL, YL><<<dim3((unsigned)g.count), dim3(kOneThreads), 0, stream>>>(
-                (const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean, a.rstd, (T *)a.out, g, sums);
+            norm_one_bwd<T, V, WIDE, STREAM, XL, YL><<<dim3((unsigned)g.count), dim3(kOneThreads), 0, stream>>>(
+                x, dy, a.gamma, a.beta, a.mean, a.rstd, (T *)a.out, g, sums);
             if (sums) launch_finish_backward(g, a.n, sums, a.gamma, nullptr, a.dgamma, a.dbeta, stream);
             return hipGetLastError();
         }
     }
     const dim3 th(kThreads), grid((unsigned)g.count);
-    norm_sums_bwd<T, V, WIDE, XL, YL><<<grid, th, 0, stream>>>((const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean,
-                                                         a.rstd, g, part);
+    norm_sums_bwd<T, V, WIDE, XL, YL><<<grid, th, 0, stream>>>(x, dy, a.gamma, a.beta, a.mean, a.rstd, g, part);
     launch_finish_backward(g, a.n, part, a.gamma, means, a.dgamma, a.dbeta, stream);
-    norm_apply_bwd<T, V, WIDE, XL, YL><<<grid, th, 0, stream>>>((const T *)a.x, (const T *)a.dy, a.gamma, a.beta, a.mean,
-                                                          a.rstd, means, (T *)a.out, g);
+    norm_apply_bwd<T, V, WIDE, STREAM, XL, YL>
+        <<<grid, th, 0, stream>>>(x, dy, a.gamma, a.beta, a.mean, a.rstd, means, (T *)a.out, g);
     return hipGetLastError();
+}
+
+template <typename T, int V, bool WIDE, bool XL, bool YL>
+hipError_t run_v(const Plan &p, const Call &a, hipStream_t stream)
+{
+    if (!a.dy)
+        return p.apply.stream ? forward_v<T, V, WIDE, true, XL, YL>(p, a, stream)
+                              : forward_v<T, V, WIDE, false, XL, YL>(p, a, stream);
+    if constexpr (V <= vector_of(sizeof(T), XL, YL, true))
+        return p.apply.stream ? backward_v<T, V, WIDE, true, XL, YL>(p, a, stream)
+                              : backward_v<T, V, WIDE, false, XL, YL>(p, a, stream);
+    return hipErrorInvalidValue;  // no such plan
 }
 
 template <typename T, bool WIDE, bool XL, bool YL>
 hipError_t run_layout(const Plan &p, const Call &a, hipStream_t stream)
 {
-    constexpr int V16 = 16 / sizeof(T), V = vector_of(sizeof(T), XL, YL, false), W = vector_of(sizeof(T), XL, YL, true);
-    if (!a.dy) {
-        if (p.v == V) return forward_v<T, V, WIDE, XL, YL>(p, a, stream);
-        if (p.v == V16 / 2) return forward_v<T, V16 / 2, WIDE, XL, YL>(p, a, stream);
-        return forward_v<T, 1, WIDE, XL, YL>(p, a, stream);
-    }
-    if (p.v == W) return backward_v<T, W, WIDE, XL, YL>(p, a, stream);
-    if (p.v == V16 / 2) return backward_v<T, V16 / 2, WIDE, XL, YL>(p, a, stream);
-    return backward_v<T, 1, WIDE, XL, YL>(p, a, stream);
+    constexpr int V16 = 16 / sizeof(T);
+    if (p.v == V16) return run_v<T, V16, WIDE, XL, YL>(p, a, stream);
+    if (p.v == V16 / 2) return run_v<T, V16 / 2, WIDE, XL, YL>(p, a, stream);
+    return run_v<T, 1, WIDE, XL, YL>(p, a, stream);
 }
 
 template <typename T>

@@ -98,6 +98,12 @@ def test_every_activation_in_every_type(act, dtype):
     check((2, 40, 20, 20, 8), dtype, act, False, True, seed=79, eps=0.1)
 
 
+@pytest.mark.parametrize("layouts", LAYOUTS, ids=str)
+@pytest.mark.parametrize("shape,dtype", [((18, 64, 96, 96, 8), "f32"), ((29, 64, 97, 96, 16), "bf16")], ids=str)
+def test_tensors_larger_than_the_caches(shape, dtype, layouts):
+    check(shape, dtype, "gelu", *layouts, seed=11)
+
+
 @pytest.mark.parametrize("last", [False, True])
 @pytest.mark.parametrize("shape", [(2, 16, 40, 40, 4), (1, 8, 256, 256, 2)], ids=str)
 def test_a_mean_far_from_zero_does_not_cancel(shape, last):
