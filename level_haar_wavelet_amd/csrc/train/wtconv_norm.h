@@ -30,8 +30,10 @@ struct Moments {
 
 __device__ inline Moments join(const Moments &a, const Moments &b)
 {
+    // an empty set's own zeros must not meet a mean whose square overflows
+    if (b.n == 0.f) return a;
+    if (a.n == 0.f) return b;
     const float n = a.n + b.n;
-    if (n == 0.f) return a;
     const float w = b.n / n, d = b.mean - a.mean;
     return Moments{n, fmaf(d, w, a.mean), a.m2 + b.m2 + d * d * a.n * w};
 }
@@ -52,9 +54,10 @@ __device__ inline S join_wave(S s, J join2)
     return s;
 }
 
-// Elements of a vector access: 16 bytes, or 8, or one.  The backward pass of two channels-last
-// tensors takes at most four: six constants for each of eight channels a thread
-// are 180 registers and two waves a SIMD (16x256x256x256 fp16: dx 563 us).
+// Elements of a vector access: 16 bytes, or 8, or one.  The backward pass of two
+// channels-last tensors takes at most four: six constants for each of eight
+// channels a thread are 180 registers and two waves a SIMD (16x256x256x256 fp16:
+// 563 us for dx alone, against 315 with four).
 constexpr int vector_of(size_t esize, bool xl, bool yl, bool bwd)
 {
     return bwd && xl && yl ? 4 : 16 / (int)esize;

@@ -111,6 +111,21 @@ def test_a_mean_far_from_zero_does_not_cancel(shape, last):
     check(shape, "f32", "silu", last, last, seed=5, offset=3000.0)
 
 
+@pytest.mark.parametrize("last", [False, True])
+@pytest.mark.parametrize("shape", [(2, 16, 40, 40, 4), (2, 16, 8, 8, 4), (1, 8, 256, 16, 2)], ids=str)
+def test_a_mean_whose_square_overflows(shape, last):
+    # the values' spread, 1e17, has a finite variance: K 1e34 is the largest sum
+    n, c, h, w, groups = shape
+    x = 1e20 + 1e17 * torch.randn(n, c, h, w, generator=torch.Generator().manual_seed(8), dtype=torch.float64)
+    x = x.float()
+    ref = Norm64(x, groups, None, None, 1e-5, "none")
+    _, mean, rstd = wt.wtconv_group_norm_forward(layout(x.cuda(), last), groups)
+    # as in check(); the mean's error there is 128 u 1e20 / 1e17 = 0.8 % of the spread, squared in rstd
+    ex = ref.x.abs().mean(2)
+    within(mean, ref.mean, 2.0 ** -24 * 128 * ex, "mean")
+    within(rstd, ref.rstd, ref.rstd * 2.0 ** -24 * (64 + 8) + ref.rstd ** 3 * (2.0 ** -24 * 128 * ex) ** 2, "rstd")
+
+
 def test_a_constant_group_gives_beta_and_finite_gradients():
     x = torch.full((2, 8, 6, 6), 3.0, device="cuda")
     beta = torch.randn(8, device="cuda")
@@ -281,6 +296,29 @@ def test_same_bits_every_time_and_on_another_stream():
             torch.cuda.synchronize()
             for f, b in got:
                 assert torch.equal(f[0], y0) and all(torch.equal(p, q) for p, q in zip(b, b0))
+
+
+def test_a_call_on_another_stream_takes_no_block_of_the_current_one():
+    # the allocator hands a freed block to the next request on the same stream,
+    # whose work orders it; a call on another stream does not wait for that work
+    x = torch.randn(4, 8, 64, 64, device="cuda")
+    g = torch.randn(512, 600, device="cuda")
+    w, m = torch.zeros_like(g), torch.zeros_like(g)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    freed = []
+    for t in (x, g):
+        freed.append(torch.empty_like(t))
+    freed = {t.untyped_storage().data_ptr() for t in freed}
+    y, mean, rstd = wt.wtconv_group_norm_forward(x, 2, stream=s)
+    s.synchronize()
+    dx = wt.wtconv_group_norm_backward(x, x, 2, mean, rstd, stream=s)[0]
+    o = wt.wtconv_orthogonalize(g, stream=s)
+    wt.wtconv_muon_step(w, g, m, lr=0.1, stream=s)
+    s.synchronize()
+    assert not freed & {t.untyped_storage().data_ptr() for t in (y, dx, o)}
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(y, wt.wtconv_group_norm_forward(x, 2)[0]) and torch.equal(o, wt.wtconv_orthogonalize(g))
 
 
 @pytest.mark.parametrize("shape", [(2, 24, 20, 18, 6), (4, 64, 28, 28, 8), (1, 16, 200, 200, 2)], ids=str)
