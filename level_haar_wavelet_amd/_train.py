@@ -65,16 +65,17 @@ def _workspace(workspace, need, device):
 
 class _On:
     """The device of the tensors as the current one, and the stream's handle.
-    What a call allocates itself comes from the current stream's pool; where the
-    call runs on another stream, `made` marks it as used there, so that it is
-    not handed out again before the call is done."""
+    What a call with a stream of its own allocates comes from that stream's pool
+    (a block of the current stream's may still be in use there, and the call
+    does not wait for it); `made` marks the results as used on the current
+    stream too, which their caller is likely to read them on."""
 
-    __slots__ = ("handle", "guard", "other")
+    __slots__ = ("handle", "guard", "current")
 
     def __init__(self, device, stream):
         cuda = torch.cuda
+        self.current = None
         self.guard = None if cuda.current_device() == device.index else cuda.device(device)
-        self.other = stream
         if stream is None:
             # the current stream's handle without a Stream object (2 us less)
             self.handle = torch._C._cuda_getCurrentRawStream(device.index)
@@ -82,6 +83,8 @@ class _On:
             raise TypeError("the stream belongs to %s, the tensors lie on %s" % (stream.device, device))
         else:
             self.handle = stream.cuda_stream
+            self.current = cuda.current_stream(device)
+            self.guard = cuda.stream(stream)
 
     def __enter__(self):
         if self.guard is not None:
@@ -93,10 +96,10 @@ class _On:
             self.guard.__exit__(*exc)
 
     def made(self, *tensors):
-        if self.other is not None:
+        if self.current is not None:
             for t in tensors:
                 if t is not None:
-                    t.record_stream(self.other)
+                    t.record_stream(self.current)
 
 
 # ---- group norm --------------------------------------------------------------
@@ -182,7 +185,7 @@ def wtconv_group_norm_forward(x, groups, gamma=None, beta=None, eps=1e-5, act="n
         ws, nbytes = _workspace(workspace, need, x.device)
         st = lib.wtconv_group_norm_forward(d, _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean),
                                            _ptr(rstd), _ptr(ws), nbytes, s)
-        on.made(ws if workspace is None else None, *made)
+        on.made(*made)
     _native.check(st, "wtconv_group_norm_forward")
     return y, mean, rstd
 
@@ -224,7 +227,7 @@ def wtconv_group_norm_backward(x, dy, groups, mean, rstd, gamma=None, beta=None,
         ws, nbytes = _workspace(workspace, need, x.device)
         st = lib.wtconv_group_norm_backward(d, _ptr(x), _ptr(dy), _ptr(gamma), _ptr(beta), _ptr(mean),
                                             _ptr(rstd), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(ws), nbytes, s)
-        on.made(ws if workspace is None else None, *made)
+        on.made(*made)
     _native.check(st, "wtconv_group_norm_backward")
     return dx, dgamma, dbeta
 
@@ -276,7 +279,7 @@ def wtconv_orthogonalize(g, steps=5, eps=1e-7, out=None, workspace=None, stream=
             made = out = torch.empty_like(g)
         ws, nbytes = _workspace(workspace, need, g.device)
         st = lib.wtconv_orthogonalize(d, _ptr(g), _ptr(out), _ptr(ws), nbytes, s)
-        on.made(ws if workspace is None else None, made)
+        on.made(made)
     _native.check(st, "wtconv_orthogonalize")
     return out
 
@@ -304,6 +307,5 @@ def wtconv_muon_step(weight, grad, momentum, lr, mu=0.95, weight_decay=0.0, scal
         ws, nbytes = _workspace(workspace, need, grad.device)
         st = lib.wtconv_muon_step(d, ctypes.byref(hyper), _ptr(weight), _ptr(grad), _ptr(momentum),
                                   _ptr(weight_out), _ptr(momentum_out), _ptr(ws), nbytes, s)
-        on.made(ws if workspace is None else None)
     _native.check(st, "wtconv_muon_step")
     return weight_out, momentum_out
