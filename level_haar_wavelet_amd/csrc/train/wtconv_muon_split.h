@@ -17,7 +17,6 @@ constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 // 1.21, 1.47 and 3.45: times 2^14 that is within fp16's 65504.
 constexpr float kScale = 16384.f;
 
-typedef _Float16 half4 __attribute__((ext_vector_type(4)));
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef float float16v __attribute__((ext_vector_type(16)));
 

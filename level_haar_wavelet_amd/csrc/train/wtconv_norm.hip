@@ -71,7 +71,7 @@ __global__ __launch_bounds__(256) void finish_backward(Geometry g, int64_t image
     if ((int)blockIdx.x < gblocks) {
         const int64_t ng = wide ? blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
         if (ng >= images * g.groups) return;
-            const int64_t n = ng / g.groups;
+        const int64_t n = ng / g.groups;
         const int c0 = (int)(ng % g.groups) * g.per, first = wide ? threadIdx.x : threadIdx.x & 63;
         const float2 *p = part + n * g.splits * g.c + c0;
         float2 a = make_float2(0.f, 0.f);

@@ -12,9 +12,15 @@
 //                elementwise pass, which takes the ranges from the last to the
 //                first: the 256 MB cache holds the end of what was read before.
 //
+// Both are bound by memory: of 3 E e and 5 E e bytes, 32x128x128x128 bf16 planes
+// to channels last takes 71 us (5.7 TB/s), the backward pass of 64x96x56x56 fp32
+// 72 us (5.3) and of 16x256x256x256 fp16 484 us (5.5), where an elementwise pass
+// over 4 GiB reaches 6.2.  Below about 20 MB the launches count: 64x192x28x28 fp16
+// takes 24 us, 8 + 4 + 12 in its three kernels.
+//
 // Walks.  An image lies in memory as rows of contiguous elements: its channels'
 // planes, or its pixels' channels.  A thread takes V contiguous elements (16
-// bytes, or one where sizes or addresses do not allow that), `lanes` threads stand
+// or 8 bytes, or one where sizes or addresses allow no more), `lanes` threads stand
 // side by side along a row and the rest take rows below, so that every thread
 // keeps its channel (planes) or its V channels (last) and their constants in
 // registers.  Where the two tensors of a pass lie differently the walk is along
