@@ -204,6 +204,9 @@ typedef __attribute__((address_space(3))) void *LdsPtr;
 // 16.3 without its matrix instructions, so it waits for its operands' way from
 // the L2s.  Three or four buffers instead of two: 15.4 us there, but 9.6 to 13 us
 // instead of 9 for the symmetric products.
+// DEEP (is_deep()): a compute unit has one workgroup only, whose stages take
+// twice the k: X of 384x1536 9.4 -> 9.0 us (tiles of 64), its Gram product 10.8 us in
+// one piece where cut along k and joined it took 12.
 template <int TILE>
 struct Shape {
     static constexpr int kWavesK = TILE == 32 ? 4 : 1;          // waves along k
@@ -322,11 +325,11 @@ __device__ inline void to_lds(const float16v (&acc)[Shape<TILE>::kSide / 32][Sha
     }
 }
 
-template <int TILE, int MODE, typename T>
+template <int TILE, bool DEEP, int MODE, typename T>
 __global__ __launch_bounds__(kThreads, 2) void product(Product a)
 {
     using Sh = Shape<TILE>;
-    constexpr int KB = Sh::kBlocks, KW = KB / Sh::kWavesK;  // 32-blocks of k: of a stage, of a wave
+    constexpr int KB = Sh::kBlocks * (DEEP ? 2 : 1), KW = KB / Sh::kWavesK;  // 32-blocks of k: of a stage, of a wave
     constexpr int RB = Sh::kSide / 32;                      // 32-row blocks of a wave
     constexpr int kBlock = 2 * TILE * 128, kStage = KB * kBlock;  // bytes
     constexpr int kResult = Lds<TILE>::kResult * Sh::kWavesK;
@@ -480,17 +483,26 @@ struct Deal {
 
 constexpr int kSlots = 512;
 
-// Of a tile of 32, 64, 128: us of 32 of k, alone on a compute unit and with a
-// second workgroup there; us of a workgroup's start and end; us for adding a
-// slice of a tile.  Measured on products of 96 to 4096.
-constexpr double kAlone[] = {0.15, 0.33, 1.1}, kShared[] = {0.20, 0.46, 1.45}, kEnds[] = {2.0, 2.5, 6.0},
+// Whether stages of twice the k pay: so few workgroups that each has a compute
+// unit, and its LDS, for itself, and more than three stages of the other kind
+// (1x96x384, of one or three: 71.5 us against 67.6).
+bool is_deep(int64_t groups, int blocks, int tile)
+{
+    return groups <= kSlots / 2 && tile < 128 && blocks > 3 * (tile == 32 ? Shape<32>::kBlocks : Shape<64>::kBlocks);
+}
+
+// Of a tile of 32, 64, 128: us of 32 of k, alone on a compute unit (in stages of
+// twice the k, and without) and with a second workgroup there; us of a
+// workgroup's start and end; us for adding a slice of a tile.  Measured on
+// products of 96 to 4096.
+constexpr double kDeep[] = {0.125, 0.29, 1.1}, kAlone[] = {0.15, 0.33, 1.1}, kShared[] = {0.20, 0.46, 1.45}, kEnds[] = {2.0, 2.5, 6.0},
                  kSlice[] = {0.25, 0.25, 2.5}, kLaunch = 4.0;
 
-double round_us(int64_t groups, int blocks, int t)
+double round_us(int64_t groups, int blocks, int t, bool deep)
 {
     const int64_t rounds = groups / kSlots, rest = groups % kSlots;
     double us = (double)rounds * (blocks * kShared[t] + kEnds[t]);
-    if (rest) us += blocks * (rest > kSlots / 2 ? kShared[t] : kAlone[t]) + kEnds[t];
+    if (rest) us += blocks * (deep ? kDeep[t] : rest > kSlots / 2 ? kShared[t] : kAlone[t]) + kEnds[t];
     return us;
 }
 
@@ -511,9 +523,10 @@ Deal make_deal(int rows, int cols, int k, bool sym, int64_t batch)
             d.full = (int)(want > 1 ? all - rest : all);
             d.cut = (blocks + want - 1) / want;
             d.slices = (blocks + d.cut - 1) / d.cut;
-            d.us = kLaunch + round_us(d.full, blocks, t);
+            const bool deep = is_deep(want > 1 ? d.full + rest * d.slices : all, d.cut, tile);
+            d.us = kLaunch + round_us(d.full, blocks, t, deep);
             if (want > 1) {
-                d.us += round_us(rest * d.slices, d.cut, t) + kLaunch + d.slices * kSlice[t];
+                d.us += round_us(rest * d.slices, d.cut, t, deep) + kLaunch + d.slices * kSlice[t];
                 d.bytes = align256((size_t)rest * d.slices * tile * tile * 4 * (tile == 32 ? 4 : 1));
             }
             if (!best.tile || d.us < best.us) best = d;
@@ -580,7 +593,11 @@ template <int TILE, int MODE, typename T>
 void launch_tile(const Deal &d, const Product &a, hipStream_t stream)
 {
     const int rest = a.tiles * a.batch - a.full;
-    product<TILE, MODE, T><<<dim3((unsigned)(a.full + rest * a.slices)), dim3(kThreads), 0, stream>>>(a);
+    const unsigned groups = (unsigned)(a.full + rest * a.slices);
+    if (is_deep(groups, a.slices > 1 ? a.cut : a.kp / 32, TILE))
+        product<TILE, TILE < 128, MODE, T><<<dim3(groups), dim3(kThreads), 0, stream>>>(a);
+    else
+        product<TILE, false, MODE, T><<<dim3(groups), dim3(kThreads), 0, stream>>>(a);
     if (rest) join<TILE, MODE, T><<<dim3((unsigned)rest), dim3(kThreads), 0, stream>>>(a);
 }
 
