@@ -11,6 +11,7 @@ namespace wtc_norm {
 constexpr int kThreads = 256;     // a workgroup of the three-launch form
 constexpr int kOneThreads = 512;  // of the one-launch form
 constexpr int kMaxBlock = 512;    // channels of a workgroup
+constexpr int kOwnSums = 16;      // ranges' moments that a lane joins in the elementwise pass
 
 // How a pass over (N, C, H W) is shared out: workgroups of `cb` channels and
 // `ppw` pixels of one image, `blocks` and `splits` of them for each image,
@@ -36,6 +37,13 @@ __device__ inline Moments join(const Moments &a, const Moments &b)
     const float n = a.n + b.n;
     const float w = b.n / n, d = b.mean - a.mean;
     return Moments{n, fmaf(d, w, a.mean), a.m2 + b.m2 + d * d * a.n * w};
+}
+
+// Pixels of range s.
+__device__ inline int pixels(const Geometry &g, int s)
+{
+    const int p = g.hw - s * g.ppw;
+    return p < g.ppw ? p : g.ppw;
 }
 
 // s of all lanes of a wave, joined in a fixed order, on every lane.
@@ -66,6 +74,7 @@ constexpr int vector_of(size_t esize, bool xl, bool yl, bool bwd)
 struct Plan {
     Geometry stats, apply;  // the forward pass's moments; every other pass
     bool xl, yl, one;
+    int lanes;  // > 0: forward, the elementwise pass finds mean and rstd itself, so many lanes a group
     int v;  // elements of an access
     float eps;
     size_t means_at, bytes;  // workspace: partial sums, then the groups' means

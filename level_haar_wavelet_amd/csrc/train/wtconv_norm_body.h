@@ -8,15 +8,15 @@
 //   one launch   a workgroup owns whole groups of an image, walks them twice and
 //                finds the second time in the caches what it read the first;
 //   three        for images too large or too few for that: sums of pixel ranges
-//                per channel, a small kernel that joins them, and the
-//                elementwise pass, which takes the ranges from the last to the
+//                per channel, a small kernel that joins them (forward, where they
+//                are few, the next one does it itself), and the elementwise pass, which takes the ranges from the last to the
 //                first: the 256 MB cache holds the end of what was read before.
 //
 // Both are bound by memory: of 3 E e and 5 E e bytes, 32x128x128x128 bf16 planes
 // to channels last takes 71 us (5.7 TB/s), the backward pass of 64x96x56x56 fp32
 // 72 us (5.3) and of 16x256x256x256 fp16 484 us (5.5), where an elementwise pass
 // over 4 GiB reaches 6.2.  Below about 20 MB the launches count: 64x192x28x28 fp16
-// takes 24 us, 8 + 4 + 12 in its three kernels.
+// takes 21 us, its bytes alone 9.
 //
 // Walks.  An image lies in memory as rows of contiguous elements: its channels'
 // planes, or its pixels' channels.  A thread takes V contiguous elements (16
@@ -181,18 +181,17 @@ struct Range {
     int64_t row;  // of the partial sums
 };
 
-// The range of this workgroup.  Workgroups go to the 8 dies in turn; each die
+// The range of workgroup `id` of g.count.  Workgroups go to the 8 dies in turn; each die
 // gets a stretch of neighbouring ranges, so that the parts of a cache line that
 // lie in two channel blocks meet in one L2, and a second pass (kBack: last range
 // first) finds in its L2 what the first pass read there last.  One launch over
 // planes has neither, and runs up to 15 % faster in plain order (kPlain).
 enum Order { kPlain, kForth, kBack };
 
-__device__ inline Range range_of(const Geometry &g, Order order)
+__device__ inline Range range_of(const Geometry &g, Order order, int id)
 {
-    int id = blockIdx.x;
     if (order != kPlain) {
-        const int per = gridDim.x / 8, rest = gridDim.x % 8, die = id % 8, own = per + (die < rest), k = id / 8;
+        const int per = (int)(g.count / 8), rest = (int)(g.count % 8), die = id % 8, own = per + (die < rest), k = id / 8;
         id = die * per + (die < rest ? die : rest) + (order == kBack ? own - 1 - k : k);
     }
     const int64_t u = id / g.splits;
@@ -682,7 +681,7 @@ __global__ __launch_bounds__(kThreads) void norm_moments(const T *__restrict__ x
                                                          float2 *__restrict__ part)
 {
     __shared__ float lds[(1 + 2 * (XL ? V : 1)) * kThreads];
-    const Range r = range_of(g, kForth);
+    const Range r = range_of(g, kForth, blockIdx.x);
     moments<T, XL, V, kThreads>(x, g, r, lds,
                                 [&](int c, const Moments &m) { part[r.row * g.c + c] = make_float2(m.mean, m.m2); });
 }
@@ -699,16 +698,78 @@ __device__ inline void load_consts(Chan *lk, const Geometry &g, const Range &r, 
     __syncthreads();
 }
 
+__device__ inline float add_lanes(float v, int lanes)
+{
+    for (int o = 1; o < lanes; o <<= 1) v += __shfl_xor(v, o);
+    return v;
+}
+
+// mean and rstd of the groups that the range's channels belong to, from the
+// channels' moments in pixel ranges (geometry gs), `lanes` neighbouring lanes a
+// group: mean = sum of n_i mean_i / K, then M2 = sum of M2_i + n_i (mean_i -
+// mean)^2.  lg: by place among those groups; mean, rstd: by each image's first
+// workgroup.
+__device__ inline void own_stats(const Geometry &gs, const Range &r, int lanes, const float2 *__restrict__ part,
+                                 float eps, float2 *lg, float *mean, float *rstd)
+{
+    const int k = threadIdx.x / lanes, lane = threadIdx.x % lanes, group = r.c0 / gs.per + k;
+    if (group > (r.c0 + r.cb - 1) / gs.per) return;
+    const float2 *p = part + r.n * gs.splits * (int64_t)gs.c + group * gs.per;
+    const float inv = 1.f / ((float)gs.per * (float)gs.hw);
+    float2 v[kOwnSums];
+    float n[kOwnSums], m = 0.f, q = 0.f;
+#pragma unroll
+    for (int u = 0; u < kOwnSums; ++u) {
+        const int i = lane + u * lanes, s = i / gs.per;
+        n[u] = 0.f;
+        if (i < gs.splits * gs.per) {
+            v[u] = p[(int64_t)s * gs.c + i - s * gs.per];
+            n[u] = (float)pixels(gs, s) * inv;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kOwnSums; ++u)
+        if (n[u] > 0.f) m = fmaf(n[u], v[u].x, m);
+    m = add_lanes(m, lanes);
+#pragma unroll
+    for (int u = 0; u < kOwnSums; ++u)
+        if (n[u] > 0.f) {
+            const float d = v[u].x - m;
+            q += fmaf(d * n[u], d, v[u].y * inv);
+        }
+    q = add_lanes(q, lanes);
+    if (lane) return;
+    const float rs = 1.f / sqrtf(q + eps);
+    lg[k] = make_float2(m, rs);
+    if (r.p0 == 0 && group * gs.per >= r.c0) {
+        mean[r.n * gs.groups + group] = m;
+        rstd[r.n * gs.groups + group] = rs;
+    }
+}
+
+// lanes > 0: own_stats() in place of a kernel between the two walks.
 template <typename T, int V, bool WIDE, bool STREAM, bool XL, bool YL>
 __global__ __launch_bounds__(kThreads) void norm_apply(const T *__restrict__ x, const float *__restrict__ gamma,
-                                                       const float *__restrict__ beta,
-                                                       const float *__restrict__ mean,
-                                                       const float *__restrict__ rstd, T *__restrict__ y, Geometry g)
+                                                       const float *__restrict__ beta, float *mean, float *rstd,
+                                                       T *__restrict__ y, Geometry g, Geometry gs, int lanes,
+                                                       const float2 *__restrict__ part, float eps)
 {
     __shared__ Chan lk[kMaxBlock];
+    __shared__ float2 lg[kThreads];
     __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
-    const Range r = range_of(g, kBack);
-    load_consts(lk, g, r, gamma, beta, mean, rstd);
+    const Range r = range_of(g, kBack, blockIdx.x);
+    if (lanes) {
+        own_stats(gs, r, lanes, part, eps, lg, mean, rstd);
+        __syncthreads();
+        for (int i = threadIdx.x; i < r.cb; i += kThreads) {
+            const int c = r.c0 + i;
+            const float2 m = lg[c / g.per - r.c0 / g.per];
+            lk[i] = Chan{m.x, m.y, gamma ? gamma[c] : 1.f, beta ? beta[c] : 0.f};
+        }
+        __syncthreads();
+    } else {
+        load_consts(lk, g, r, gamma, beta, mean, rstd);
+    }
     apply<T, V, WIDE, STREAM, kThreads, XL, YL>(x, y, g, r, lk, tile);
 }
 
@@ -723,7 +784,7 @@ __global__ __launch_bounds__(kThreads) void norm_sums_bwd(const T *__restrict__ 
     __shared__ Chan lk[kMaxBlock];
     __shared__ float lds[2 * (XL ? V : 1) * kThreads];
     __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
-    const Range r = range_of(g, kForth);
+    const Range r = range_of(g, kForth, blockIdx.x);
     load_consts(lk, g, r, gamma, beta, mean, rstd);
     sums_bwd<T, V, WIDE, kThreads, XL, YL>(x, dy, g, r, lk, lds, tile,
                                      [&](int c, const float2 &s) { part[r.row * g.c + c] = s; });
@@ -741,7 +802,7 @@ __global__ __launch_bounds__(kThreads) void norm_apply_bwd(const T *__restrict__
     __shared__ Chan lk[kMaxBlock];
     __shared__ float2 lq[kMaxBlock];
     __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
-    const Range r = range_of(g, kBack);
+    const Range r = range_of(g, kBack, blockIdx.x);
     for (int i = threadIdx.x; i < r.cb; i += kThreads) lq[i] = means[r.n * g.groups + (r.c0 + i) / g.per];
     load_consts(lk, g, r, gamma, beta, mean, rstd);
     apply_bwd<T, V, WIDE, STREAM, kThreads, XL, YL>(x, dy, dx, g, r, lk, lq, tile);
@@ -773,7 +834,7 @@ __global__ __launch_bounds__(kOneThreads) void norm_one(const T *__restrict__ x,
     __shared__ Moments lm[kMaxBlock];
     __shared__ float lds[(1 + 2 * (XL ? V : 1)) * kOneThreads];
     __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
-    const Range r = range_of(g, XL || YL ? kForth : kPlain);
+    const Range r = range_of(g, XL || YL ? kForth : kPlain, blockIdx.x);
     moments<T, XL, V, kOneThreads>(x, g, r, lds, [&](int c, const Moments &m) { lm[c - r.c0] = m; });
     __syncthreads();
     join_groups<kOneThreads>(
@@ -813,7 +874,7 @@ __global__ __launch_bounds__(kOneThreads) void norm_one_bwd(const T *__restrict_
     __shared__ float2 ls[kMaxBlock], lq[kMaxBlock];
     __shared__ float lds[2 * (XL ? V : 1) * kOneThreads];
     __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
-    const Range r = range_of(g, XL || YL ? kForth : kPlain);
+    const Range r = range_of(g, XL || YL ? kForth : kPlain, blockIdx.x);
     load_consts(lk, g, r, gamma, beta, mean, rstd);
     sums_bwd<T, V, WIDE, kOneThreads, XL, YL>(x, dy, g, r, lk, lds, tile, [&](int c, const float2 &s) {
         ls[c - r.c0] = s;
@@ -848,9 +909,9 @@ hipError_t forward_v(const Plan &p, const Call &a, hipStream_t stream)
     const dim3 th(kThreads);
     float2 *part = (float2 *)a.workspace;
     norm_moments<T, V, XL><<<dim3((unsigned)p.stats.count), th, 0, stream>>>(x, p.stats, part);
-    launch_finish_forward(p.stats, a.n, part, a.mean_out, a.rstd_out, p.eps, stream);
+    if (!p.lanes) launch_finish_forward(p.stats, a.n, part, a.mean_out, a.rstd_out, p.eps, stream);
     norm_apply<T, V, WIDE, STREAM, XL, YL><<<dim3((unsigned)p.apply.count), th, 0, stream>>>(
-        x, a.gamma, a.beta, a.mean_out, a.rstd_out, (T *)a.out, p.apply);
+        x, a.gamma, a.beta, a.mean_out, a.rstd_out, (T *)a.out, p.apply, p.stats, p.lanes, part, p.eps);
     return hipGetLastError();
 }
 
