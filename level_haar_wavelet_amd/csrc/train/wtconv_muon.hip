@@ -198,9 +198,9 @@ typedef __attribute__((address_space(3))) void *LdsPtr;
 // few workgroups a stage costs the latency of its loads, so small tiles take
 // more of k at once.
 //
-// P X of 4096^3 (tiles of 128) takes 430 us: 0.96 PFLOP/s of fp16 products, where
-// the library's product of that size reaches 1.09; the card's power limit holds
-// both.  1024^3 (tiles of 64, 256 of them) takes 17 us: 12.6 without its loads,
+// P X of 4096^3 (tiles of 128) takes 400 to 430 us: 0.96 to 1.03 PFLOP/s of fp16
+// products, where the library's product of that size reaches 1.09; the card's
+// power limit holds both.  1024^3 (tiles of 64, 256 of them) takes 17 us: 12.6 without its loads,
 // 16.3 without its matrix instructions, so it waits for its operands' way from
 // the L2s.  Three or four buffers instead of two: 15.4 us there, but 9.6 to 13 us
 // instead of 9 for the symmetric products.

@@ -9,14 +9,15 @@
 //                finds the second time in the caches what it read the first;
 //   three        for images too large or too few for that: sums of pixel ranges
 //                per channel, a small kernel that joins them (forward, where they
-//                are few, the next one does it itself), and the elementwise pass, which takes the ranges from the last to the
-//                first: the 256 MB cache holds the end of what was read before.
+//                are few, the next one does it itself), and the elementwise
+//                pass, which takes the ranges from the last to the first: the
+//                256 MB cache holds the end of what was read before.
 //
 // Both are bound by memory: of 3 E e and 5 E e bytes, 32x128x128x128 bf16 planes
-// to channels last takes 71 us (5.7 TB/s), the backward pass of 64x96x56x56 fp32
-// 72 us (5.3) and of 16x256x256x256 fp16 484 us (5.5), where an elementwise pass
+// to channels last takes 68 us (5.9 TB/s), the backward pass of 64x96x56x56 fp32
+// 72 us (5.3) and of 16x256x256x256 fp16 481 us (5.6), where an elementwise pass
 // over 4 GiB reaches 6.2.  Below about 20 MB the launches count: 64x192x28x28 fp16
-// takes 21 us, its bytes alone 9.
+// takes 22 us, its bytes alone 9.
 //
 // Walks.  An image lies in memory as rows of contiguous elements: its channels'
 // planes, or its pixels' channels.  A thread takes V contiguous elements (16
