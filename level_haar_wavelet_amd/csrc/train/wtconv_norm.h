@@ -71,10 +71,17 @@ constexpr int vector_of(size_t esize, bool xl, bool yl, bool bwd)
     return bwd && xl && yl ? 4 : 16 / (int)esize;
 }
 
+// Where lanes > 0, the forward pass's elementwise kernel finds mean and rstd by
+// itself, so many lanes a group; a lane's next moment lies ranges further on and
+// channels more (or one range and channels - per).
+struct Own {
+    int lanes, ranges, channels;
+};
+
 struct Plan {
     Geometry stats, apply;  // the forward pass's moments; every other pass
     bool xl, yl, one;
-    int lanes;  // > 0: forward, the elementwise pass finds mean and rstd itself, so many lanes a group
+    Own own;
     int v;  // elements of an access
     float eps;
     size_t means_at, bytes;  // workspace: partial sums, then the groups' means

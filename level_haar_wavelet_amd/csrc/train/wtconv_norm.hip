@@ -200,19 +200,20 @@ Geometry split_geometry(Geometry g, int64_t n, Walk w, int v, int esize)
 // Lanes for each group, where the forward pass's elementwise kernel finds mean and
 // rstd from the ranges' moments by itself: a launch less, against a few loads
 // and sums at the start of each workgroup.  us without and with, in a graph:
-//   last, planes  32x32x112x112 fp32 34.4 / 29.7 and 30.9 / 28.7, 64x192x28x28 fp16
-//           21.7 / 20.7, 1x512x32x32 fp32 planes 10.5 / 8.8, never 2 % more;
+//   last, planes  32x32x112x112 fp32 34.4 / 29.4 and 30.9 / 28.7, 64x192x28x28 fp16
+//           21.7 / 20.0, 1x512x32x32 fp32 planes 10.5 / 9.0, never 2 % more;
 //   tiles   1x128x64x64 10.4 / 9.0, 32x128x128x128 fp16 78.8 / 76.2, but
 //           32x32x112x112 fp16 22.3 / 24.9, 2x128x256x256 fp16 25.5 / 26.4: not
 //           from 16 to 64 MB.
 // 0 (a kernel in between) there, and where all groups at once and kOwnSums
 // moments a lane do not do.
-int lanes_of(const Geometry &sums, const Geometry &apply)
+Own own_of(const Geometry &sums, const Geometry &apply)
 {
     const int most = (apply.cb - 1) / apply.per + 2, ng = most < apply.groups ? most : apply.groups;
     int lanes = 64;
     while (lanes > 1 && lanes * ng > kThreads) lanes /= 2;
-    return lanes * ng <= kThreads && (int64_t)sums.splits * sums.per <= kOwnSums * lanes ? lanes : 0;
+    if (lanes * ng > kThreads || (int64_t)sums.splits * sums.per > kOwnSums * lanes) return Own{0, 0, 0};
+    return Own{lanes, lanes / sums.per, lanes % sums.per};
 }
 
 }  // namespace
@@ -274,7 +275,7 @@ Plan make_plan(const wtconv_norm_desc_t &d, bool bwd, bool aligned)
     p.apply = split_geometry(g, d.n, aw, v, esize);
     const Geometry &q = bwd ? p.apply : p.stats;
     const int64_t bytes = d.n * d.c * (int64_t)g.hw * esize;
-    if (!bwd && !(aw == kTiles && bytes >= 16 << 20 && bytes < 64 << 20)) p.lanes = lanes_of(p.stats, p.apply);
+    if (!bwd && !(aw == kTiles && bytes >= 16 << 20 && bytes < 64 << 20)) p.own = own_of(p.stats, p.apply);
     p.means_at = align256((size_t)(d.n * q.splits) * d.c * sizeof(float2));
     p.bytes = p.means_at + (bwd ? align256((size_t)(d.n * d.groups) * sizeof(float2)) : 0);
     return p;

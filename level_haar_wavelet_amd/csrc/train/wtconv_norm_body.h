@@ -706,26 +706,32 @@ __device__ inline float add_lanes(float v, int lanes)
 }
 
 // mean and rstd of the groups that the range's channels belong to, from the
-// channels' moments in pixel ranges (geometry gs), `lanes` neighbouring lanes a
+// channels' moments in pixel ranges (geometry gs), w.lanes neighbouring lanes a
 // group: mean = sum of n_i mean_i / K, then M2 = sum of M2_i + n_i (mean_i -
 // mean)^2.  lg: by place among those groups; mean, rstd: by each image's first
 // workgroup.
-__device__ inline void own_stats(const Geometry &gs, const Range &r, int lanes, const float2 *__restrict__ part,
+__device__ inline void own_stats(const Geometry &gs, const Range &r, const Own &w, const float2 *__restrict__ part,
                                  float eps, float2 *lg, float *mean, float *rstd)
 {
-    const int k = threadIdx.x / lanes, lane = threadIdx.x % lanes, group = r.c0 / gs.per + k;
+    const int lanes = w.lanes, k = threadIdx.x / lanes, lane = threadIdx.x % lanes, group = r.c0 / gs.per + k;
     if (group > (r.c0 + r.cb - 1) / gs.per) return;
     const float2 *p = part + r.n * gs.splits * (int64_t)gs.c + group * gs.per;
     const float inv = 1.f / ((float)gs.per * (float)gs.hw);
     float2 v[kOwnSums];
     float n[kOwnSums], m = 0.f, q = 0.f;
+    int s = lane / gs.per, c = lane - s * gs.per;
 #pragma unroll
     for (int u = 0; u < kOwnSums; ++u) {
-        const int i = lane + u * lanes, s = i / gs.per;
         n[u] = 0.f;
-        if (i < gs.splits * gs.per) {
-            v[u] = p[(int64_t)s * gs.c + i - s * gs.per];
+        if (s < gs.splits) {
+            v[u] = p[(int64_t)s * gs.c + c];
             n[u] = (float)pixels(gs, s) * inv;
+        }
+        c += w.channels;
+        s += w.ranges;
+        if (c >= gs.per) {
+            c -= gs.per;
+            ++s;
         }
     }
 #pragma unroll
@@ -748,19 +754,19 @@ __device__ inline void own_stats(const Geometry &gs, const Range &r, int lanes, 
     }
 }
 
-// lanes > 0: own_stats() in place of a kernel between the two walks.
+// own.lanes > 0: own_stats() in place of a kernel between the two walks.
 template <typename T, int V, bool WIDE, bool STREAM, bool XL, bool YL>
 __global__ __launch_bounds__(kThreads) void norm_apply(const T *__restrict__ x, const float *__restrict__ gamma,
                                                        const float *__restrict__ beta, float *mean, float *rstd,
-                                                       T *__restrict__ y, Geometry g, Geometry gs, int lanes,
+                                                       T *__restrict__ y, Geometry g, Geometry gs, Own own,
                                                        const float2 *__restrict__ part, float eps)
 {
     __shared__ Chan lk[kMaxBlock];
     __shared__ float2 lg[kThreads];
     __shared__ __attribute__((aligned(16))) char tile[XL != YL ? kTileBytes(sizeof(T)) : 16];
     const Range r = range_of(g, kBack, blockIdx.x);
-    if (lanes) {
-        own_stats(gs, r, lanes, part, eps, lg, mean, rstd);
+    if (own.lanes) {
+        own_stats(gs, r, own, part, eps, lg, mean, rstd);
         __syncthreads();
         for (int i = threadIdx.x; i < r.cb; i += kThreads) {
             const int c = r.c0 + i;
@@ -910,9 +916,9 @@ hipError_t forward_v(const Plan &p, const Call &a, hipStream_t stream)
     const dim3 th(kThreads);
     float2 *part = (float2 *)a.workspace;
     norm_moments<T, V, XL><<<dim3((unsigned)p.stats.count), th, 0, stream>>>(x, p.stats, part);
-    if (!p.lanes) launch_finish_forward(p.stats, a.n, part, a.mean_out, a.rstd_out, p.eps, stream);
+    if (!p.own.lanes) launch_finish_forward(p.stats, a.n, part, a.mean_out, a.rstd_out, p.eps, stream);
     norm_apply<T, V, WIDE, STREAM, XL, YL><<<dim3((unsigned)p.apply.count), th, 0, stream>>>(
-        x, a.gamma, a.beta, a.mean_out, a.rstd_out, (T *)a.out, p.apply, p.stats, p.lanes, part, p.eps);
+        x, a.gamma, a.beta, a.mean_out, a.rstd_out, (T *)a.out, p.apply, p.stats, p.own, part, p.eps);
     return hipGetLastError();
 }
 
