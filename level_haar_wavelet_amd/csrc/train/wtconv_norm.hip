@@ -271,9 +271,11 @@ Plan make_plan(const wtconv_norm_desc_t &d, bool bwd, bool aligned)
             return p;
         }
     }
-    p.stats = split_geometry(g, d.n, sw, v, esize);
     p.apply = split_geometry(g, d.n, aw, v, esize);
-    const Geometry &q = bwd ? p.apply : p.stats;
+    // the moments' walk is the forward pass's alone; in tiles its rows may be
+    // narrower than the backward pass's accesses to planes
+    p.stats = bwd ? p.apply : split_geometry(g, d.n, sw, v, esize);
+    const Geometry &q = p.stats;
     const int64_t bytes = d.n * d.c * (int64_t)g.hw * esize;
     if (!bwd && !(aw == kTiles && bytes >= 16 << 20 && bytes < 64 << 20)) p.own = own_of(p.stats, p.apply);
     p.means_at = align256((size_t)(d.n * q.splits) * d.c * sizeof(float2));

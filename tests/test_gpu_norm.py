@@ -90,6 +90,16 @@ def test_against_the_formulas(shape, layouts):
         check(shape, dtype, act, *layouts, seed=i * 10 + k)
 
 
+@pytest.mark.parametrize("layouts", LAYOUTS, ids=lambda l: "%s_%s" % tuple("last" if v else "planes" for v in l))
+@pytest.mark.parametrize("shape", [(2, 3, 8, 8, 1), (2, 6, 8, 8, 3), (2, 4, 8, 8, 2), (3, 2, 16, 12, 1), (2, 7, 24, 16, 7),
+                                   (1, 5, 64, 64, 1)], ids=lambda s: "x".join(map(str, s)))
+def test_fewer_channels_than_an_access_has_elements(shape, layouts):
+    # rows of pixels allow accesses of 8 or 16 bytes, rows of channels do not
+    for k, dtype in enumerate(DTYPES):
+        print(shape, layouts, dtype, flush=True)
+        check(shape, dtype, ACTS[k + 1], *layouts, seed=500 + k)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_every_activation_in_every_type(act, dtype):

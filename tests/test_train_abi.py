@@ -2,6 +2,9 @@
 arguments are refused with the documented codes before anything is launched,
 and the binding refuses tensors that the entry points cannot take."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -9,6 +12,7 @@ import torch
 import level_haar_wavelet_amd as wt
 from level_haar_wavelet_amd import _native
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 OK, NULL, SHAPE, UNSUPPORTED, WORKSPACE, HIP, ALIAS = range(7)
 
 
@@ -141,6 +145,40 @@ def test_ortho_arguments_are_refused(lib):
     assert muon(wo=0x100000 + 16) == ALIAS and muon(mo=0x300000 - 16) == ALIAS  # neither in place nor apart
     assert muon(wo=0x300000) == ALIAS and muon(mo=0x100000) == ALIAS and muon(wo=0x200000) == ALIAS
     assert muon(mo=0x400000 + 64) == ALIAS and muon(ws=0x500000) == ALIAS and muon(ws=0x200000) == ALIAS
+
+
+PLAN_SWEEP = """
+import ctypes
+from level_haar_wavelet_amd import _native
+lib = _native.load()
+out = ctypes.c_size_t(0)
+calls = 0
+for c in list(range(1, 18)) + [24, 33, 100, 1030]:
+    for h, w in ((1, 1), (1, 7), (2, 2), (3, 5), (4, 6), (8, 8), (16, 16), (17, 16), (37, 23), (64, 64), (256, 128)):
+        for groups in {1, c, c // 2 if c % 2 == 0 else 1}:
+            for n in (1, 5, 300):
+                for dtype in range(3):
+                    for xl, yl in ((0, 0), (0, 1), (1, 0), (1, 1)):
+                        for op in (_native.OP_FWD, _native.OP_BWD):
+                            d = _native.NormDesc(n, c, h, w, groups, dtype, 0, xl, yl, 1e-5)
+                            case = (c, h, w, groups, n, dtype, xl, yl, op)
+                            out.value = 1 << 62
+                            st = lib.wtconv_group_norm_workspace_size(ctypes.byref(d), op, ctypes.byref(out))
+                            assert st == 0, case
+                            # partial sums of at most the tensor's own size and the last ranges', and means
+                            assert out.value <= 8 * n * c * h * w + 8 * n * groups + 1024, (case, out.value)
+                            calls += 1
+print(calls)
+"""
+
+
+def test_every_small_norm_has_a_plan():
+    """Channels fewer than an access has elements, planes it does and does not
+    divide, all layouts: in a process of its own, which a fault of the host's
+    arithmetic would end."""
+    r = subprocess.run([sys.executable, "-c", PLAN_SWEEP], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
+    assert int(r.stdout) > 40000
 
 
 def test_the_layer_refuses_bf16(lib):
