@@ -8,7 +8,8 @@ A call is enqueued on `stream`, or on the current stream of the device that its
 tensors lie on; that device need not be the current one.  Its buffers are the
 caller's: a tensor that was made on another stream needs that stream's own
 ordering (torch.cuda.Stream.wait_stream, Tensor.record_stream), as with any
-torch operation.
+torch operation.  Those that it writes count as modified for autograd: a
+backward pass that saved one of them raises instead of reading the new values.
 """
 from __future__ import annotations
 
@@ -16,6 +17,7 @@ import ctypes
 import functools
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _native
 
@@ -61,6 +63,13 @@ def _workspace(workspace, need, device):
     if not workspace.is_contiguous():
         raise TypeError("workspace must be contiguous")
     return workspace, workspace.numel() * workspace.element_size()
+
+
+def _written(*tensors):
+    """The kernels write through addresses, which torch does not see."""
+    given = [t for t in tensors if t is not None]
+    if given:
+        increment_version(given)
 
 
 class _On:
@@ -173,6 +182,7 @@ def wtconv_group_norm_forward(x, groups, gamma=None, beta=None, eps=1e-5, act="n
     _f32(beta, "beta", (c,), x.device)
     _f32(mean, "mean", (n, groups), x.device)
     _f32(rstd, "rstd", (n, groups), x.device)
+    given = (y, mean, rstd)
     on = _On(x.device, stream)
     with on as s:
         made = []
@@ -187,6 +197,7 @@ def wtconv_group_norm_forward(x, groups, gamma=None, beta=None, eps=1e-5, act="n
                                            _ptr(rstd), _ptr(ws), nbytes, s)
         on.made(*made)
     _native.check(st, "wtconv_group_norm_forward")
+    _written(*given)
     return y, mean, rstd
 
 
@@ -215,6 +226,7 @@ def wtconv_group_norm_backward(x, dy, groups, mean, rstd, gamma=None, beta=None,
         _f32(t, name, (n, groups), x.device)
     _f32(dgamma, "dgamma", (c,), x.device)
     _f32(dbeta, "dbeta", (c,), x.device)
+    given = (dx, dgamma, dbeta)
     on = _On(x.device, stream)
     with on as s:
         made = []
@@ -229,6 +241,7 @@ def wtconv_group_norm_backward(x, dy, groups, mean, rstd, gamma=None, beta=None,
                                             _ptr(rstd), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(ws), nbytes, s)
         on.made(*made)
     _native.check(st, "wtconv_group_norm_backward")
+    _written(*given)
     return dx, dgamma, dbeta
 
 
@@ -272,6 +285,7 @@ def wtconv_orthogonalize(g, steps=5, eps=1e-7, out=None, workspace=None, stream=
         _gpu_tensor(out, "out", g.device)
         if out.shape != g.shape or out.dtype != g.dtype or not out.is_contiguous():
             raise TypeError("out must match g in shape, dtype and layout")
+    given = out
     on = _On(g.device, stream)
     with on as s:
         made = None
@@ -281,6 +295,7 @@ def wtconv_orthogonalize(g, steps=5, eps=1e-7, out=None, workspace=None, stream=
         st = lib.wtconv_orthogonalize(d, _ptr(g), _ptr(out), _ptr(ws), nbytes, s)
         on.made(made)
     _native.check(st, "wtconv_orthogonalize")
+    _written(given)
     return out
 
 
@@ -308,4 +323,5 @@ def wtconv_muon_step(weight, grad, momentum, lr, mu=0.95, weight_decay=0.0, scal
         st = lib.wtconv_muon_step(d, ctypes.byref(hyper), _ptr(weight), _ptr(grad), _ptr(momentum),
                                   _ptr(weight_out), _ptr(momentum_out), _ptr(ws), nbytes, s)
     _native.check(st, "wtconv_muon_step")
+    _written(weight_out, momentum_out)
     return weight_out, momentum_out
