@@ -82,6 +82,16 @@ class WTConv2d(torch.nn.Module):
         else:
             self.register_parameter("w_lvl", None)
             self.register_parameter("s_lvl", None)
+        self._mark_matrices()
+
+    def _mark_matrices(self):
+        # for optim.Muon: the first dimension counts matrices
+        if self.w_lvl is not None:
+            self.w_lvl.matrix_batch_dims = 1
+
+    def __setstate__(self, state):  # a copied parameter is a new one
+        super().__setstate__(state)
+        self._mark_matrices()
 
     def forward(self, x):
         return WTConvFunction.apply(x, self.w_base, self.bias, self.s_base, self.w_lvl, self.s_lvl)

@@ -7,10 +7,12 @@ matrices of rows x prod(rest):
     WTConv2d.w_base (C, k, k)       one matrix of C x k^2,
     WTConv2d.w_lvl  (L, 4C, k, k)   L matrices of 4C x k^2,
     a product's weight (out, in)    itself.
-`batch_dims` says how many leading dimensions are the stack's; by default none
-for 2 and 3 dimensions and one for 4 (give batch_dims=0 for the (out, in, k, k)
-weight of an ordinary convolution).  Biases and the scales s_base and s_lvl are
-no matrices in that sense: leave them to another optimiser.
+`batch_dims` says how many leading dimensions are the stack's; by default none,
+and one for WTConv2d.w_lvl.  Other 4-d parameters need it: 0 for the (out, in,
+k, k) weight of an ordinary convolution, 1 for a stack laid out as w_lvl is (a
+parameter whose attribute `matrix_batch_dims` is 1 counts as one by itself).
+Biases and the scales s_base and s_lvl are no matrices in that sense: leave them
+to another optimiser.
 """
 from __future__ import annotations
 
@@ -31,6 +33,17 @@ def _matrices(shape, batch_dims):
         raise ValueError("Muon takes matrices: shape %s has none behind %d batch dimensions" % (tuple(shape),
                                                                                                batch_dims))
     return math.prod(shape[:batch_dims]), shape[batch_dims], math.prod(shape[batch_dims + 1:])
+
+
+def _matrices_of(p, batch_dims):
+    """The same of a parameter.  Nothing in a 4-d shape tells a convolution's
+    weight from a stack, and each taken for the other is updated wrongly."""
+    if batch_dims is None and p.dim() == 4:
+        batch_dims = getattr(p, "matrix_batch_dims", None)
+        if batch_dims is None:
+            raise ValueError("a parameter of shape %s needs batch_dims: 0 for a convolution's weight (out, in, k, k), "
+                             "1 for a stack of matrices (L, rows, k, k)" % (tuple(p.shape),))
+    return _matrices(p.shape, batch_dims)
 
 
 class Muon(torch.optim.Optimizer):
@@ -54,7 +67,7 @@ class Muon(torch.optim.Optimizer):
         group = self.param_groups[-1]
         try:
             for p in group["params"]:
-                _matrices(p.shape, group["batch_dims"])
+                _matrices_of(p, group["batch_dims"])
                 if p.dtype != torch.float32:
                     raise TypeError("Muon takes float32 parameters, got %s" % p.dtype)
         except (TypeError, ValueError):
@@ -71,7 +84,7 @@ class Muon(torch.optim.Optimizer):
             for p in group["params"]:
                 if p.grad is None:
                     continue
-                shape = _matrices(p.shape, group["batch_dims"])
+                shape = _matrices_of(p, group["batch_dims"])
                 if not p.is_contiguous():
                     raise TypeError("Muon takes contiguous parameters")
                 state = self.state[p]

@@ -299,3 +299,23 @@ def test_a_long_narrow_matrix_and_a_large_stack():
     for shape in ((1, 3, 1 << 20), (4000, 7, 9)):
         g = gradient(shape, 3)
         within(wt.wtconv_orthogonalize(g.cuda()), ortho64(g), 5, torch.float32, str(shape))
+
+
+def test_ordinary_convolution_weights():
+    """(out, in, k, k) and (out, in, 1, 1), batch_dims=0, against the formula."""
+    from level_haar_wavelet_amd.optim import Muon
+
+    for k in (1, 3):
+        torch.manual_seed(k)
+        conv = torch.nn.Conv2d(12, 20, k, device="cuda")
+        opt = Muon([conv.weight], lr=0.1, batch_dims=0)
+        old = conv.weight.detach().cpu()
+        conv.weight.grad = 1e-2 * torch.randn_like(conv.weight)
+        opt.step()
+        r, c = 20, 12 * k * k
+        v = lambda t: t.detach().cpu().reshape(1, r, c)
+        rw, _ = plain_muon(v(old), v(conv.weight.grad), torch.zeros(1, r, c), 0.1, 0.95, 0.0, max(1, r / c) ** 0.5, True,
+                           5, 1e-7)
+        # lr scale <= 0.13 times the iteration's bound, and 4 u of the weights
+        tol = 0.13 * (ortho_tol(rw, 5, torch.float32) + 8 * U * 3.4445 ** 5) + 4 * U * v(old).norm().item()
+        assert (torch.linalg.matrix_norm(v(conv.weight).double() - rw) <= tol).all()

@@ -220,3 +220,39 @@ def test_norm_module_checks_its_groups():
     m = GroupNormAct2d(4, 8, act="gelu", channels_last=True)
     assert "gelu" in repr(m) and m.gamma.shape == (8,)
     assert GroupNormAct2d(4, 8, affine=False).gamma is None
+
+
+def test_optimizer_asks_how_an_ordinary_4d_weight_is_meant():
+    """(out, in, k, k) of a convolution and (L, 4C, k, k) of the layer look alike:
+    only the layer's own parameter, which says so, is a stack by itself."""
+    import copy
+    import io
+
+    from level_haar_wavelet_amd.module import WTConv2d
+    from level_haar_wavelet_amd.optim import Muon
+
+    for k in (1, 3):
+        conv = torch.nn.Conv2d(16, 64, k)
+        with pytest.raises(ValueError, match="batch_dims"):
+            Muon([conv.weight])
+        opt = Muon([torch.nn.Parameter(torch.zeros(4, 4))])
+        with pytest.raises(ValueError, match="batch_dims"):
+            opt.add_param_group({"params": [conv.weight]})
+        assert len(opt.param_groups) == 1
+        Muon([conv.weight], batch_dims=0)
+        Muon([{"params": [conv.weight], "batch_dims": 1}])
+        # options of another optimiser's state do not bring the guess back
+        opt = Muon([conv.weight], batch_dims=0)
+        state = opt.state_dict()
+        state["param_groups"][0]["batch_dims"] = None
+        opt.load_state_dict(state)
+        conv.weight.grad = torch.zeros_like(conv.weight)
+        with pytest.raises(ValueError, match="batch_dims"):
+            opt.step()
+    layer = WTConv2d(4, 3, 2)
+    buf = io.BytesIO()
+    torch.save(layer, buf)
+    buf.seek(0)
+    for m in (layer, copy.deepcopy(layer), torch.load(buf, weights_only=False), layer.double().float()):
+        Muon([m.w_base, m.w_lvl])
+    Muon([WTConv2d(4, 3, 0).w_base])
