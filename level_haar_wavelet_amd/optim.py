@@ -20,7 +20,7 @@ import math
 
 import torch
 
-from . import wtconv_muon_step
+from . import _native, _train, wtconv_muon_step
 
 __all__ = ["Muon"]
 
@@ -80,6 +80,8 @@ class Muon(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        # everything is checked before the first update
+        todo = []
         for group in self.param_groups:
             for p in group["params"]:
                 if p.grad is None:
@@ -87,14 +89,20 @@ class Muon(torch.optim.Optimizer):
                 shape = _matrices_of(p, group["batch_dims"])
                 if not p.is_contiguous():
                     raise TypeError("Muon takes contiguous parameters")
-                state = self.state[p]
-                if "momentum_buffer" not in state:
-                    if torch.cuda.is_current_stream_capturing():
-                        raise RuntimeError("the first step of a parameter cannot be captured: every replay would "
-                                           "start from a momentum of zero")
-                    state["momentum_buffer"] = torch.zeros_like(p)
-                wtconv_muon_step(p.view(shape), p.grad.contiguous().view(shape),
-                                 state["momentum_buffer"].view(shape), lr=group["lr"], mu=group["momentum"],
-                                 weight_decay=group["weight_decay"], scale=math.sqrt(max(1.0, shape[1] / shape[2])),
-                                 nesterov=group["nesterov"], steps=group["steps"], eps=group["eps"])
+                if not p.is_cuda:
+                    raise TypeError("Muon takes parameters on the GPU")
+                # the step's own plan: sizes, steps and eps that the call would refuse
+                _train._ortho_plan(*shape, _native.F32, int(group["steps"]), float(group["eps"]))
+                if "momentum_buffer" not in self.state.get(p, ()) and torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("the first step of a parameter cannot be captured: every replay would "
+                                       "start from a momentum of zero")
+                todo.append((group, p, shape))
+        for group, p, shape in todo:
+            state = self.state[p]
+            if "momentum_buffer" not in state:
+                state["momentum_buffer"] = torch.zeros_like(p)
+            wtconv_muon_step(p.view(shape), p.grad.contiguous().view(shape), state["momentum_buffer"].view(shape),
+                             lr=group["lr"], mu=group["momentum"], weight_decay=group["weight_decay"],
+                             scale=math.sqrt(max(1.0, shape[1] / shape[2])), nesterov=group["nesterov"],
+                             steps=group["steps"], eps=group["eps"])
         return loss

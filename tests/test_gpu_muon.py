@@ -301,6 +301,29 @@ def test_a_long_narrow_matrix_and_a_large_stack():
         within(wt.wtconv_orthogonalize(g.cuda()), ortho64(g), 5, torch.float32, str(shape))
 
 
+@pytest.mark.parametrize("bad", ["channels_last", "cpu", "too_large", "no_stack"])
+def test_a_parameter_that_is_refused_stops_a_step_before_its_first_update(bad):
+    from level_haar_wavelet_amd.optim import Muon
+
+    good = torch.nn.Parameter(torch.randn(8, 8, device="cuda"))
+    if bad == "channels_last":
+        last = torch.nn.Parameter(torch.zeros(8, 4, 3, 3, device="cuda").contiguous(memory_format=torch.channels_last))
+    elif bad == "cpu":
+        last = torch.nn.Parameter(torch.zeros(8, 4, 3, 3))
+    elif bad == "too_large":  # more columns than the entry point takes
+        last = torch.nn.Parameter(torch.zeros(1, (1 << 22) + 1, device="cuda"))
+    else:
+        last = torch.nn.Parameter(torch.zeros(8, 4, 3, 3, device="cuda"))
+    opt = Muon([good, last], lr=0.1, batch_dims=0)
+    if bad == "no_stack":
+        opt.param_groups[0]["batch_dims"] = 7
+    good.grad, last.grad = torch.randn_like(good), torch.zeros_like(last)
+    before, version = good.detach().clone(), good._version
+    with pytest.raises((TypeError, ValueError, wt._native.WtconvError)):
+        opt.step()
+    assert torch.equal(good, before) and good._version == version and not opt.state
+
+
 def test_ordinary_convolution_weights():
     """(out, in, k, k) and (out, in, 1, 1), batch_dims=0, against the formula."""
     from level_haar_wavelet_amd.optim import Muon
