@@ -29,7 +29,7 @@ def _matrices(shape, batch_dims):
     """(batch, rows, cols) of a parameter's shape."""
     if batch_dims is None:
         batch_dims = 1 if len(shape) == 4 else 0
-    if batch_dims < 0 or len(shape) < batch_dims + 2:
+    if batch_dims < 0 or len(shape) < batch_dims + 2 or 0 in shape:
         raise ValueError("Muon takes matrices: shape %s has none behind %d batch dimensions" % (tuple(shape),
                                                                                                batch_dims))
     return math.prod(shape[:batch_dims]), shape[batch_dims], math.prod(shape[batch_dims + 1:])
@@ -57,8 +57,6 @@ class Muon(torch.optim.Optimizer):
 
     def __init__(self, params, lr=0.02, momentum=0.95, weight_decay=0.0, nesterov=True, steps=5, eps=1e-7,
                  batch_dims=None):
-        if lr < 0 or weight_decay < 0 or not 0 <= momentum < 1:
-            raise ValueError("lr and weight_decay must be >= 0 and momentum in [0, 1)")
         super().__init__(params, dict(lr=lr, momentum=momentum, weight_decay=weight_decay, nesterov=nesterov,
                                       steps=steps, eps=eps, batch_dims=batch_dims))
 
@@ -66,6 +64,10 @@ class Muon(torch.optim.Optimizer):
         super().add_param_group(group)
         group = self.param_groups[-1]
         try:
+            if not group["lr"] >= 0 or not group["weight_decay"] >= 0 or not 0 <= group["momentum"] < 1:
+                raise ValueError("lr and weight_decay must be >= 0 and momentum in [0, 1)")
+            if not 1 <= group["steps"] <= 16 or not 0 <= group["eps"] < math.inf:
+                raise ValueError("steps must be 1 to 16 and eps >= 0 and finite")
             for p in group["params"]:
                 _matrices_of(p, group["batch_dims"])
                 if p.dtype != torch.float32:

@@ -256,3 +256,28 @@ def test_optimizer_asks_how_an_ordinary_4d_weight_is_meant():
     for m in (layer, copy.deepcopy(layer), torch.load(buf, weights_only=False), layer.double().float()):
         Muon([m.w_base, m.w_lvl])
     Muon([WTConv2d(4, 3, 0).w_base])
+
+
+@pytest.mark.parametrize("kw", [dict(lr=-0.1), dict(lr=float("nan")), dict(momentum=1.0), dict(momentum=-0.1),
+                                dict(weight_decay=-1.0), dict(steps=0), dict(steps=17), dict(eps=-1.0),
+                                dict(eps=float("inf"))], ids=str)
+def test_optimizer_checks_the_options_of_every_group(kw):
+    from level_haar_wavelet_amd.optim import Muon
+
+    p = [torch.nn.Parameter(torch.zeros(4, 4)) for _ in range(2)]
+    with pytest.raises(ValueError):
+        Muon(p, **kw)
+    with pytest.raises(ValueError):
+        Muon([dict(params=p, **kw)])
+    opt = Muon(p[:1])
+    with pytest.raises(ValueError):
+        opt.add_param_group(dict(params=p[1:], **kw))
+    assert len(opt.param_groups) == 1
+
+
+def test_optimizer_refuses_empty_matrices():
+    from level_haar_wavelet_amd.optim import Muon
+
+    for shape in ((0, 4), (4, 0), (2, 0, 3)):
+        with pytest.raises(ValueError):
+            Muon([torch.nn.Parameter(torch.zeros(shape))])
