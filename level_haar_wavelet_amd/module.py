@@ -15,8 +15,11 @@ block, in the same manner.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
+from . import _native
 from . import (wtconv_backward_data, wtconv_backward_weight, wtconv_forward, wtconv_group_norm_backward,
                wtconv_group_norm_forward)
 
@@ -145,6 +148,10 @@ class GroupNormAct2d(torch.nn.Module):
         super().__init__()
         if groups < 1 or channels % groups:
             raise ValueError("groups must divide channels")
+        if act not in _native.ACTS:
+            raise ValueError("act must be one of %s, got %r" % (", ".join(sorted(_native.ACTS)), act))
+        if not 0 < eps < math.inf:
+            raise ValueError("eps must be positive and finite")
         f = dict(device=device, dtype=torch.float32)
         self.groups, self.channels, self.eps, self.act, self.channels_last = groups, channels, eps, act, channels_last
         if affine:
@@ -155,6 +162,8 @@ class GroupNormAct2d(torch.nn.Module):
             self.register_parameter("beta", None)
 
     def forward(self, x):
+        if x.dim() != 4 or x.shape[1] != self.channels:
+            raise ValueError("expected (N, C, H, W) with C = %d channels, got %s" % (self.channels, tuple(x.shape)))
         return GroupNormActFunction.apply(x, self.gamma, self.beta, self.groups, self.eps, self.act,
                                           self.channels_last)
 

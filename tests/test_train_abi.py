@@ -281,3 +281,18 @@ def test_optimizer_refuses_empty_matrices():
     for shape in ((0, 4), (4, 0), (2, 0, 3)):
         with pytest.raises(ValueError):
             Muon([torch.nn.Parameter(torch.zeros(shape))])
+
+
+def test_norm_module_checks_its_options_and_its_input():
+    from level_haar_wavelet_amd.module import GroupNormAct2d
+
+    with pytest.raises(ValueError):
+        GroupNormAct2d(4, 8, act="tanh")
+    for eps in (0.0, -1.0, float("nan"), float("inf")):
+        with pytest.raises(ValueError):
+            GroupNormAct2d(4, 8, eps=eps)
+    for affine in (True, False):  # 16 channels fall into 4 groups too, but are not the module's
+        m = GroupNormAct2d(4, 8, affine=affine)
+        for shape in ((1, 16, 2, 2), (8, 2, 2), (1, 8, 4)):
+            with pytest.raises(ValueError, match="channels"):
+                m(torch.zeros(shape))
