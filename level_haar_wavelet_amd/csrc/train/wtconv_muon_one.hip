@@ -15,13 +15,14 @@
 // of LDS (rows of 80 bytes: neither the writes nor the 16-byte reads collide).
 // The waves' parts of A are added in LDS in order; every wave forms P for itself
 // (up to 32 rows), or a block of it for all.
+#include "wtconv_muon_plan.h"
 #include "wtconv_muon_split.h"
 
 namespace wtc_muon {
 
 namespace {
 
-constexpr int kWaves = 8, kThreads = 64 * kWaves;
+constexpr int kWaves = kOneWaves, kThreads = 64 * kWaves;
 constexpr int kRow = 40;  // halves of a row in LDS: 32 and a gap
 
 // Left or right operand (hi, lo), k in the result's order: rows 16 kk .. + 15 of
@@ -379,9 +380,6 @@ __global__ __launch_bounds__(kThreads, 1) void ortho_one(Args a)
 }
 
 }  // namespace
-
-// One 32-row block: four tiles a wave; two: two tiles (registers).
-bool one_fits(int n, int m) { return n <= 32 ? m <= 4 * kWaves * 32 : n <= 64 && m <= 2 * kWaves * 32; }
 
 template <typename T>
 hipError_t launch_one(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &o, hipStream_t stream)

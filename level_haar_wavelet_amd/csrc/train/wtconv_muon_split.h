@@ -56,8 +56,7 @@ __device__ inline float16v mfma3(const half8 &lhi, const half8 &llo, const half8
     return mfma(lhi, rhi, mfma(llo, rhi, mfma(lhi, rlo, c)));
 }
 
-// The whole iteration of a matrix in one workgroup, where one can hold it.
-bool one_fits(int n, int m);
+// The whole iteration of a matrix in one workgroup, where one_fits().
 template <typename T>
 hipError_t launch_one(const wtconv_ortho_desc_t &d, const WtcOrthoArgs &a, hipStream_t stream);
 

@@ -23,6 +23,16 @@ SHAPES = [
 ]
 
 
+# with those above, every kernel instance of the tiled path (tests/test_muon_plan.py):
+# products and joins of tiles of 32, 64 and 128, stages of both depths, whole
+# rounds of tiles with a last one cut along k, cuts over several matrices
+LARGE = [
+    (4, 1024, 1024), (1, 2048, 2048), (6, 1024, 700), (1, 1999, 3001), (6, 1675, 1632), (8, 3416, 483),
+    (1, 1644, 1904), (4, 2570, 225), (4, 2892, 65), (1, 611, 3325), (1, 385, 397), (2, 1796, 1818), (4, 4201, 612),
+    (8, 1282, 1241), (8, 673, 641), (3, 635, 1010),
+]
+
+
 def gradient(shape, seed, dtype=torch.float32):
     g = torch.Generator().manual_seed(seed)
     b, r, c = shape
@@ -342,3 +352,41 @@ def test_ordinary_convolution_weights():
         # lr scale <= 0.13 times the iteration's bound, and 4 u of the weights
         tol = 0.13 * (ortho_tol(rw, 5, torch.float32) + 8 * U * 3.4445 ** 5) + 4 * U * v(old).norm().item()
         assert (torch.linalg.matrix_norm(v(conv.weight).double() - rw) <= tol).all()
+
+
+def ortho64_gpu(g, **kw):
+    """ortho64 of a stack, on the GPU matrix by matrix."""
+    return torch.stack([ortho64(m.cuda(), **kw).cpu() for m in g])
+
+
+@pytest.mark.parametrize("shape", LARGE, ids=lambda s: "x".join(map(str, s)))
+def test_every_instance_of_the_products(shape):
+    i = LARGE.index(shape)
+    half = (torch.float16, torch.bfloat16)[i % 2]
+    for d in (torch.float32, half):
+        g = gradient(shape, 900 + i, d)
+        print(shape, d, flush=True)
+        got = wt.wtconv_orthogonalize(g.cuda())
+        within(got, ortho64_gpu(g), 5, d, "%s %s" % (shape, d))
+        assert torch.equal(got, wt.wtconv_orthogonalize(g.cuda()))  # the same bits each time
+    # a 16-bit result is the fp32 one of the same values, rounded once
+    assert torch.equal(got, wt.wtconv_orthogonalize(g.cuda().float()).to(half))
+
+
+@pytest.mark.parametrize("shape", [(1, 2048, 2048), (6, 1024, 700), (1, 1999, 3001), (6, 1675, 1632), (4, 1024, 1024)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_muon_step_of_large_matrices(shape):
+    dtype = torch.float32 if shape[0] == 1 else torch.bfloat16
+    g = gradient(shape, 3, dtype)
+    torch.manual_seed(3)
+    w, m = 0.1 * torch.randn(shape), 1e-3 * torch.randn(shape)
+    lr, mu, wd, scale = (float(torch.tensor(v)) for v in (0.5, 0.9, 0.01, 1.5))
+    wo, mo = wt.wtconv_muon_step(w.cuda(), g.cuda(), m.cuda(), lr=lr, mu=mu, weight_decay=wd, scale=scale)
+    rm = mu * m.double() + (1 - mu) * g.double()
+    rw = (1 - lr * wd) * w.double() - lr * scale * ortho64_gpu((1 - mu) * g.double() + mu * rm)
+    # as in test_muon_step
+    assert ((mo.cpu().double() - rm).abs() <= 4 * U * (mu * m.double().abs() + (1 - mu) * g.double().abs())
+            + 1e-40).all()
+    tol = lr * scale * (ortho_tol(rw, 5, torch.float32) + 8 * U * 3.4445 ** 5) + 4 * U * torch.linalg.matrix_norm(w.double())
+    err = torch.linalg.matrix_norm(wo.cpu().double() - rw)
+    assert (err <= tol).all(), (shape, err / tol)
