@@ -12,6 +12,11 @@ constexpr int kThreads = 256;     // a workgroup of the three-launch form
 constexpr int kOneThreads = 512;  // of the one-launch form
 constexpr int kMaxBlock = 512;    // channels of a workgroup
 constexpr int kOwnSums = 16;      // ranges' moments that a lane joins in the elementwise pass
+// Values of a channel that a thread sums at most: in chains that it joins; and
+// in one chain, where it sums several channels: moments along channels and tiles,
+// and the backward sums along channels (16x256x256x256 fp16 483 us, with 96 of
+// them, which is 2731 workgroups in place of 2048, 503).
+constexpr int kMostValues = 2048, kMostUnjoined = 96, kMostBackward = 128;
 
 // How a pass over (N, C, H W) is shared out: workgroups of `cb` channels and
 // `ppw` pixels of one image, `blocks` and `splits` of them for each image,

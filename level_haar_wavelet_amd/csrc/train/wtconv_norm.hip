@@ -12,41 +12,55 @@ namespace wtc_norm {
 
 namespace {
 
-// A wave's join over its lanes, then over the waves of a workgroup that share a
+// A lane's sums over many images or channels are in fp64: it may have thousands.
+struct Double2 {
+    double x, y;
+};
+
+__device__ inline Double2 add(const Double2 &a, const Double2 &b) { return Double2{a.x + b.x, a.y + b.y}; }
+__device__ inline float2 add(const float2 &a, const float2 &b) { return make_float2(a.x + b.x, a.y + b.y); }
+
+// A wave's sum over its lanes, then over the waves of a workgroup that share a
 // group (`wide`), through LDS; lane 0 of the first wave has it.
-template <typename S, typename J>
-__device__ inline S join_block(S s, bool wide, S *lds, J join2)
+template <typename S>
+__device__ inline S add_block(S s, bool wide, S *lds)
 {
-    s = join_wave(s, join2);
+    auto add2 = [](const S &a, const S &b) { return add(a, b); };
+    s = join_wave(s, add2);
     if (!wide) return s;
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
     __syncthreads();
-    for (int i = 1; i < 4; ++i) s = join2(i == 1 ? lds[0] : s, lds[i]);
+    for (int i = 1; i < 4; ++i) s = add(i == 1 ? lds[0] : s, lds[i]);
     return s;
 }
 
-// A wave for each group, or (wide) a workgroup.
+// A wave for each group, or (wide) a workgroup: with d_i a set's mean less the
+// first one's, mean = first + sum n_i d_i / K, var = sum (M2_i + n_i d_i^2) / K -
+// (sum n_i d_i / K)^2, which cancels by at most the number of sets, of 53 bits.
 __global__ __launch_bounds__(256) void finish_forward(Geometry g, int64_t groups, bool wide,
                                                       const float2 *__restrict__ part, float *__restrict__ mean,
                                                       float *__restrict__ rstd, float eps)
 {
-    __shared__ Moments lds[4];
+    __shared__ Double2 lds[4];
     const int64_t ng = wide ? blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (ng >= groups) return;
     const int64_t n = ng / g.groups;
     const int c0 = (int)(ng % g.groups) * g.per, first = wide ? threadIdx.x : threadIdx.x & 63;
     const float2 *p = part + n * g.splits * g.c + c0;
-    Moments m = {0.f, 0.f, 0.f};
+    const double pivot = p[0].x;
+    Double2 a = {0.0, 0.0};
 #pragma unroll 4
     for (int i = first; i < g.splits * g.per; i += wide ? 256 : 64) {
         const int s = i / g.per;
         const float2 v = p[(int64_t)s * g.c + i % g.per];
-        m = join(m, Moments{(float)pixels(g, s), v.x, v.y});
+        const double d = v.x - pivot, nd = pixels(g, s) * d;
+        a = add(a, Double2{nd, fma(nd, d, (double)v.y)});
     }
-    m = join_block(m, wide, lds, join);
+    a = add_block(a, wide, lds);
     if (first == 0) {
-        mean[ng] = m.mean;
-        rstd[ng] = 1.f / sqrtf(m.m2 / m.n + eps);
+        const double k = (double)g.per * g.hw, m = a.x / k, var = a.y / k - m * m;
+        mean[ng] = (float)(pivot + m);
+        rstd[ng] = 1.f / sqrtf((float)(var < 0.0 ? 0.0 : var) + eps);  // NaN stays
     }
 }
 
@@ -59,38 +73,58 @@ __global__ __launch_bounds__(256) void finish_backward(Geometry g, int64_t image
                                                        float2 *__restrict__ means, float *__restrict__ dgamma,
                                                        float *__restrict__ dbeta)
 {
-    auto add = [](const float2 &a, const float2 &b) { return make_float2(a.x + b.x, a.y + b.y); };
-    __shared__ float2 lds[32][9];
+    __shared__ Double2 lds[32][9];
     if ((int)blockIdx.x < gblocks) {
         const int64_t ng = wide ? blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
         if (ng >= images * g.groups) return;
         const int64_t n = ng / g.groups;
         const int c0 = (int)(ng % g.groups) * g.per, first = wide ? threadIdx.x : threadIdx.x & 63;
         const float2 *p = part + n * g.splits * g.c + c0;
-        float2 a = make_float2(0.f, 0.f);
+        // 32 sets at a time (fp64 here, or a kernel of its own, costs more than it gives)
+        float2 a = make_float2(0.f, 0.f), total = a;
+        int left = 32;
 #pragma unroll 4
         for (int i = first; i < g.splits * g.per; i += wide ? 256 : 64) {
             const int s = i / g.per, c = i % g.per;
             const float2 v = p[(int64_t)s * g.c + c];
             const float ga = gamma ? gamma[c0 + c] : 1.f;
             a = make_float2(fmaf(ga, v.x, a.x), fmaf(ga, v.y, a.y));
+            if (--left == 0) {
+                total = add(total, a);
+                a = make_float2(0.f, 0.f);
+                left = 32;
+            }
         }
-        a = join_block(a, wide, &lds[0][0], add);
+        a = add_block(add(total, a), wide, (float2 *)lds);
         const float k = (float)g.per * (float)g.hw;
         if (first == 0) means[ng] = make_float2(a.x / k, a.y / k);
         return;
     }
     const int j = threadIdx.x & 7, r = threadIdx.x >> 3, c = ((int)blockIdx.x - gblocks) * 8 + j;
-    float2 a = make_float2(0.f, 0.f);
-    if (c < g.c)
+    Double2 a = {0.0, 0.0};
+    if (c < g.c) {
+        const int64_t rows = images * g.splits;
+        int64_t i = r;
+        for (; i + 15 * 32 < rows; i += 16 * 32) {
+            float2 v[16];  // as they come, then in fp64
+#pragma unroll
+            for (int u = 0; u < 16; ++u) v[u] = part[(i + u * 32) * g.c + c];
+#pragma unroll
+            for (int u = 1; u < 16; ++u) v[0] = add(v[0], v[u]);
+            a = add(a, Double2{v[0].x, v[0].y});
+        }
+        float2 b = make_float2(0.f, 0.f);
 #pragma unroll 8
-        for (int64_t i = r; i < images * g.splits; i += 32) a = add(a, part[i * g.c + c]);
+        for (; i < rows; i += 32) b = add(b, part[i * g.c + c]);
+        a = add(a, Double2{b.x, b.y});
+    }
     lds[r][j] = a;
     __syncthreads();
     if (r == 0 && c < g.c) {
+#pragma unroll 4
         for (int i = 1; i < 32; ++i) a = add(a, lds[i][j]);
-        if (dbeta) dbeta[c] = a.x;
-        if (dgamma) dgamma[c] = a.y;
+        if (dbeta) dbeta[c] = (float)a.x;
+        if (dgamma) dgamma[c] = (float)a.y;
     }
 }
 
@@ -161,19 +195,24 @@ Geometry one_geometry(Geometry g, int64_t n, Walk w, bool tiles, int v, int v16,
     return g;
 }
 
-Geometry split_geometry(Geometry g, int64_t n, Walk w, int v, int esize)
+enum Sums { kNone, kMoments, kBackward };  // what a walk adds up
+
+Geometry split_geometry(Geometry g, int64_t n, Walk w, int v, int esize, Sums sums)
 {
-    int step;  // pixels that a workgroup takes at least
+    int step;     // pixels that a workgroup takes at least
+    int64_t far;  // and at most, where it sums them
     if (w == kLast) {
         const int chunks = g.c / v, most = kMaxBlock / v;
         const int blocks = (int)ceil_div(chunks, most);
         g.cb = (int)ceil_div(chunks, blocks) * v;
         g.lanes = pick_lanes(g.cb / v, kThreads, true);
         step = kThreads / g.lanes;
+        far = (int64_t)(sums == kBackward ? kMostBackward : kMostUnjoined) * step;
     } else if (w == kTiles) {
         step = 128 / esize;
         g.cb = g.c < step ? g.c : step;
         g.lanes = 1;
+        far = (v * esize == 16 && esize == 4 ? kMostValues : kMostUnjoined) / v * step;  // one channel a thread or more
     } else {
         g.lanes = pick_lanes((int)ceil_div(g.hw, v), kThreads, false);
         const int rows = kThreads / g.lanes;
@@ -182,6 +221,7 @@ Geometry split_geometry(Geometry g, int64_t n, Walk w, int v, int esize)
         if (cb > kMaxBlock / rows * rows) cb = kMaxBlock / rows * rows;
         g.cb = (int)(cb < g.c ? cb : g.c);
         step = g.lanes * v;
+        far = (int64_t)kMostValues * g.lanes;
     }
     g.blocks = (int)ceil_div(g.c, g.cb);
     // that many workgroups, but no fewer bytes for one than kLeastBytes
@@ -190,6 +230,8 @@ Geometry split_geometry(Geometry g, int64_t n, Walk w, int v, int esize)
     int64_t ppw = ceil_div(g.hw, most);
     const int64_t least = ceil_div(kLeastBytes, (int64_t)g.cb * esize);
     if (ppw < least) ppw = least;
+    // (no more than 2^22 workgroups for that: beyond some 2^32 values of few channels)
+    if (sums != kNone && ppw > far && ceil_div(g.hw, far) * all <= 1 << 22) ppw = far;
     ppw = ceil_div(ppw < 1 ? 1 : ppw, step) * step;
     g.ppw = (int)(ppw < g.hw ? ppw : ceil_div(g.hw, step) * step);
     g.splits = (int)ceil_div(g.hw, g.ppw);
@@ -263,7 +305,10 @@ Plan make_plan(const wtconv_norm_desc_t &d, bool bwd, bool aligned)
     if (unit <= kMaxBlock && !(aw == kTiles && (bwd || g.hw > 256))) {
         const Geometry s = one_geometry(g, d.n, sw, aw == kTiles, v, v16, unit);
         const int64_t slice = (int64_t)s.cb * g.hw * esize, count = s.count;
-        if (aw == kTiles || (aw == kLast ? slice <= 65536 && g.hw <= 1024 && count <= 512 : slice <= 16384 || count >= 256)) {
+        const bool pays = aw == kTiles ? true
+                          : aw == kLast ? slice <= 65536 && g.hw <= 1024 && count <= 512
+                                        : (slice <= 16384 || count >= 256) && g.hw <= (int64_t)kMostValues * s.lanes;
+        if (pays) {
             p.one = true;
             p.stats = s;
             p.apply = s;
@@ -271,10 +316,10 @@ Plan make_plan(const wtconv_norm_desc_t &d, bool bwd, bool aligned)
             return p;
         }
     }
-    p.apply = split_geometry(g, d.n, aw, v, esize);
+    p.apply = split_geometry(g, d.n, aw, v, esize, bwd ? kBackward : kNone);
     // the moments' walk is the forward pass's alone; in tiles its rows may be
     // narrower than the backward pass's accesses to planes
-    p.stats = bwd ? p.apply : split_geometry(g, d.n, sw, v, esize);
+    p.stats = bwd ? p.apply : split_geometry(g, d.n, sw, v, esize, kMoments);
     const Geometry &q = p.stats;
     const int64_t bytes = d.n * d.c * (int64_t)g.hw * esize;
     if (!bwd && !(aw == kTiles && bytes >= 16 << 20 && bytes < 64 << 20)) p.own = own_of(p.stats, p.apply);

@@ -31,9 +31,16 @@
 // banks.
 //
 // Numerics.  Values are fp32 from the load on.  A thread sums x - s and
-// (x - s)^2 with s the first value it meets: since s is one of the values, the
-// sum of squares it yields cannot cancel by more than their number.  Threads'
-// (count, mean, M2) are joined by Chan's formula, in fixed order.
+// (x - s)^2 of a chain of values, s the first of them: since s is one of the
+// values, the sum of squares cannot cancel by more than their number.  Along
+// planes a chain is kChain values and s, from the second on, the mean of those
+// before, so that a border that differs from the rest does not shift all that
+// follows it.  Chains' and threads' (count, mean, M2) are joined by Chan's formula,
+// in fixed order.  The backward sums go to the thread's total kChain at a time
+// where it sums one channel.  With the limits of wtconv_norm.h on what a thread
+// takes, a sum is a chain of at most 96 additions (128 in the backward pass along
+// channels) and a tree; longer sums over ranges and images after that are in fp64
+// or 32 at a time.
 #ifndef WTCONV_NORM_BODY_H
 #define WTCONV_NORM_BODY_H
 
@@ -216,6 +223,10 @@ __device__ inline Range range_of(const Geometry &g, Order order, int id)
 // get c < 0.
 constexpr int kBatch = 4;
 
+// Values of a channel that a thread sums before they join the rest: whole
+// batches.
+constexpr int kChain = 32;
+
 template <bool LAST, int V, int NT, typename B, typename G, typename F, typename E>
 __device__ inline void walk(const Geometry &g, const Range &r, B begin, G get, F use, E end)
 {
@@ -309,12 +320,30 @@ __device__ inline bool join_threads(const Geometry &g, int c, S &v, float *lds)
     return c >= 0 && q == 0;
 }
 
-// Moments of every channel of the range: done(c, moments).
+// Moments of every channel of the range: done(c, moments).  Along channels
+// a thread has at most kMostUnjoined of each, one chain (the set to join it with
+// would be half as many registers again, 58 -> 80: 64x192x28x28 fp16 21.8 -> 22.9 us).
 template <typename T, bool LAST, int V, int NT, typename D>
 __device__ inline void moments(const T *__restrict__ x, const Geometry &g, const Range &r, float *lds, D done)
 {
     constexpr int K = LAST ? V : 1;
     float s[K], a[K], b[K], n;
+    MomentSet<K> m, total;
+    auto end_chain = [&] {
+        const float w = n > 0.f ? 1.f / n : 0.f;
+        m.n = n;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            m.mean[k] = fmaf(a[k], w, s[k]);
+            m.m2[k] = fmaf(-a[k] * w, a[k], b[k]);
+            // rounding only: a sum of squares is not negative (NaN stays)
+            if (m.m2[k] < 0.f) m.m2[k] = 0.f;
+        }
+        if constexpr (!LAST) {
+            total.add(m);
+            m = total;
+        }
+    };
     typename Pack<T, V>::type raw[kBatch];
     walk<LAST, V, NT>(
         g, r,
@@ -322,6 +351,7 @@ __device__ inline void moments(const T *__restrict__ x, const Geometry &g, const
             n = 0.f;
 #pragma unroll
             for (int k = 0; k < K; ++k) s[k] = a[k] = b[k] = 0.f;
+            if constexpr (!LAST) total.n = total.mean[0] = total.m2[0] = 0.f;
         },
         [&](int u, int64_t at) { raw[u] = fetch<T, V>(x + at); },
         [&](int u, int64_t, bool first) {
@@ -330,6 +360,12 @@ __device__ inline void moments(const T *__restrict__ x, const Geometry &g, const
             if (u == 0 && first)
 #pragma unroll
                 for (int k = 0; k < K; ++k) s[k] = v[k];
+            if constexpr (!LAST)
+                if (u == 0 && n >= (float)kChain) {
+                    end_chain();
+                    s[0] = total.mean[0];
+                    n = a[0] = b[0] = 0.f;
+                }
             n += V / K;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -340,16 +376,7 @@ __device__ inline void moments(const T *__restrict__ x, const Geometry &g, const
             }
         },
         [&](int c) {
-            MomentSet<K> m;
-            const float w = n > 0.f ? 1.f / n : 0.f;
-            m.n = n;
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                m.mean[k] = fmaf(a[k], w, s[k]);
-                m.m2[k] = fmaf(-a[k] * w, a[k], b[k]);
-                // rounding only: a sum of squares is not negative (NaN stays)
-                if (m.m2[k] < 0.f) m.m2[k] = 0.f;
-            }
+            end_chain();
             if (join_threads<LAST, NT>(g, c, m, lds))
 #pragma unroll
                 for (int k = 0; k < K; ++k) done(c + k, Moments{m.n, m.mean[k], m.m2[k]});
@@ -518,7 +545,8 @@ __device__ inline void sums_bwd(const T *__restrict__ x, const T *__restrict__ d
     if constexpr (XL == YL) {
         constexpr int K = XL ? V : 1;
         Chan k[K];
-        SumSet<K> s;
+        SumSet<K> s, total;  // total and left: along planes
+        int left;
         typename Pack<T, V>::type rx[kBatch], rd[kBatch];
         walk<XL, V, NT>(
             g, r,
@@ -528,12 +556,25 @@ __device__ inline void sums_bwd(const T *__restrict__ x, const T *__restrict__ d
                     s.a[i] = s.b[i] = 0.f;
                     if (c >= 0) k[i] = lk[c + i - r.c0];
                 }
+                if constexpr (!XL) {
+                    total.a[0] = total.b[0] = 0.f;
+                    left = kChain;
+                }
             },
             [&](int u, int64_t at) {
                 rx[u] = fetch<T, V>(x + at);
                 rd[u] = fetch<T, V>(dy + at);
             },
             [&](int u, int64_t at, bool) {
+                if constexpr (!XL)
+                    if (u == 0) {
+                        if (left == 0) {
+                            total.add(s);
+                            s.a[0] = s.b[0] = 0.f;
+                            left = kChain;
+                        }
+                        left -= kBatch * V;
+                    }
                 float v[V], d[V];
                 values<T, V>(rx[u], v);
                 values<T, V>(rd[u], d);
@@ -547,6 +588,7 @@ __device__ inline void sums_bwd(const T *__restrict__ x, const T *__restrict__ d
                 }
             },
             [&](int c) {
+                if constexpr (!XL) s.add(total);
                 if (join_threads<XL, NT>(g, c, s, lds))
 #pragma unroll
                     for (int i = 0; i < K; ++i) done(c + i, make_float2(s.a[i], s.b[i]));
@@ -556,10 +598,25 @@ __device__ inline void sums_bwd(const T *__restrict__ x, const T *__restrict__ d
         typedef Pieces<T, V, NT> P;
         static_assert(P::kChunks <= 64 && NT % P::kChunks == 0, "a channel's threads are lanes of one wave");
         for (int c0 = r.c0; c0 < r.c0 + r.cb; c0 += P::kSide) {
-            float2 s[P::kOwn];
+            // a total only where a thread has one channel; else shorter ranges
+            // (kMostUnjoined): 16x256x256x256 fp16, of two channels, 550 us
+            // without either, 505 with shorter ranges, 587 with totals (a wave
+            // less a SIMD), but fp32 910, 958 and 911
+            constexpr bool kTotal = P::kOwn == 1;
+            float2 s[P::kOwn], total = make_float2(0.f, 0.f);
 #pragma unroll
             for (int o = 0; o < P::kOwn; ++o) s[o] = make_float2(0.f, 0.f);
+            int left = kChain;
+            auto end_chain = [&] {
+                total = make_float2(total.x + s[0].x, total.y + s[0].y);
+                s[0] = make_float2(0.f, 0.f);
+            };
             for (int p0 = r.p0; p0 < r.p1; p0 += P::kSide) {
+                if (kTotal && left == 0) {
+                    end_chain();
+                    left = kChain;
+                }
+                left -= V;
                 const P w(g, r, p0, c0);
                 typename Pack<T, V>::type raw[P::kOwn];
 #pragma unroll
@@ -583,6 +640,10 @@ __device__ inline void sums_bwd(const T *__restrict__ x, const T *__restrict__ d
                         s[o].y = fmaf(dz, xh, s[o].y);
                     }
                 }
+            }
+            if constexpr (kTotal) {
+                end_chain();
+                s[0] = total;
             }
 #pragma unroll
             for (int o = 0; o < P::kOwn; ++o) {

@@ -383,3 +383,76 @@ def test_offsets_beyond_32_bits():
         assert ((a - b).abs() <= b.abs() * 2.0 ** -10 + 4e-5).all()
     v = x[4, 1].double()
     assert abs(v.mean().item() - m1[0, 1].item()) < 1e-5
+
+
+def stats64(x, groups):
+    """mean, biased variance and E|x| of every group in fp64, on the GPU image by image."""
+    out = []
+    for v in x:
+        v = v.double().reshape(groups, -1)
+        m = v.mean(1)
+        out.append((m, (v - m[:, None]).square().mean(1), v.abs().mean(1)))
+    return [torch.stack(t).cpu() for t in zip(*out)]
+
+
+@pytest.mark.parametrize("dtype,last,shape", [("f32", False, (64, 4, 1024, 1024, 4)), ("f16", False, (64, 4, 1448, 1448, 4)),
+                                              ("f32", False, (2, 3, 3000, 3000, 3)), ("f32", True, (8, 4, 2048, 2048, 1)),
+                                              ("f32", True, (1, 2, 8192, 8192, 2))], ids=str)
+def test_long_planes_whose_first_rows_differ(dtype, last, shape):
+    """Every thread's first values are a border's: shifted by 1000 spreads from
+    the rest.  Tolerances as in check(): chains of at most 128 additions."""
+    n, c, h, w, groups = shape
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(n, c, h, w, generator=g, device="cuda")
+    x[:, :, :2 if not last else 1] += 1000.0
+    x = layout(x.to(DTYPES[dtype]), last)
+    _, mean, rstd = wt.wtconv_group_norm_forward(x, groups)
+    m, var, ex = stats64(x, groups)
+    r = 1 / torch.sqrt(var + 1e-5)
+    within(mean, m, 2.0 ** -24 * 128 * ex, "mean")
+    within(rstd, r, r * 2.0 ** -24 * (64 + 8) + r ** 3 * (2.0 ** -24 * 128 * ex) ** 2, "rstd")
+
+
+@pytest.mark.parametrize("shape,dtype,layouts", [
+    ((64, 4, 1024, 1024, 4), "f32", (False, False)), ((2, 2, 4096, 4096, 2), "f32", (True, True)),
+    ((65536, 8, 8, 8, 2), "f32", (True, True)), ((65536, 8, 7, 9, 2), "f32", (False, False)),
+    ((1, 64, 4096, 4096, 8), "f32", (False, True)), ((1, 64, 4096, 4096, 8), "bf16", (True, False)),
+    ((1, 33, 4001, 2999, 3), "f16", (False, True)),
+], ids=str)
+def test_long_sums_of_equal_gradients(shape, dtype, layouts):
+    """dy = 0.3 everywhere: each addition to a growing sum is rounded the same
+    way, so that a chain of 2000 is off by 350 u.  dbeta and dgamma within the
+    bounds of Norm64.backward (act none: the slope is 1), dx's two means through
+    dx itself, which is zero for a constant dy but for their error."""
+    n, c, h, w, groups = shape
+    lx, ly = layouts
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = layout(torch.randn(n, c, h, w, generator=g, device="cuda").to(DTYPES[dtype]), lx)
+    dy = layout(torch.full((n, c, h, w), 0.3, device="cuda", dtype=DTYPES[dtype]), ly)
+    step = max(1, 2 ** 26 // (c * h * w))
+    sums = torch.zeros(3, c, dtype=torch.float64, device="cuda")
+    mean, rstd = (torch.empty(n, groups, device="cuda") for _ in range(2))
+    for i in range(0, n, step):
+        v = x[i:i + step].double().reshape(-1, groups, c // groups * h * w)
+        m = v.mean(2)
+        r = 1 / torch.sqrt((v - m[..., None]).square().mean(2) + 1e-5)
+        mean[i:i + step], rstd[i:i + step] = m, r
+        # from the rounded statistics, as the call gets them
+        xh = (v - mean[i:i + step].double()[..., None]) * rstd[i:i + step].double()[..., None]
+        xh = xh.view(-1, c, h * w)
+        sums[0] += xh.sum((0, 2))
+        sums[1] += xh.abs().sum((0, 2))
+        sums[2] += xh.square().sum((0, 2))
+    d = dy.flatten()[0].item()
+    count = n * h * w
+    sx, sa, sq = (t.cpu() for t in sums)
+    dx, dg, db = wt.wtconv_group_norm_backward(x, dy, groups, mean, rstd)
+    u = 2.0 ** -24
+    # e = |dy| u (16 (1 + |z|) + 8 |xh| + 4 |z|), z = xh
+    within(db, torch.full((c,), d * count, dtype=torch.float64), u * d * (16 * count + 28 * sa + 128 * count), "dbeta")
+    within(dg, d * sx, u * d * (16 * sa + 28 * sq + 136 * sa), "dgamma")
+    # E[t xh] is about 0 as well, so dx = rstd (t - E[t] - xh E[t xh]): errors of
+    # E[t] and of E[t xh] (of magnitudes |t| and |t| E|xh|, E|xh| < 1), 8 u of |t|
+    # for the rest, xh up to 7; half a step of 16 bits is below that
+    tol = rstd.max().item() * d * u * ((16 + 28 + 128 + 8) + 7 * (16 + 28 + 136 + 8))
+    assert dx.float().abs().max().item() <= tol
