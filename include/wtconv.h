@@ -293,8 +293,9 @@ wtconv_status_t wtconv_group_norm_backward(const wtconv_norm_desc_t *desc, const
  * matrices: w_base one of C x k^2, w_lvl L of 4C x k^2.
  * Types        g and out fp32, fp16 or bf16 (out in g's type, rounded once);
  *              in the Muon step g may be any of them, weight and momentum are
- *              fp32.  Products keep 22 bits of each factor and sum in fp32;
- *              norms sum in fp64.
+ *              fp32.  Norms sum in fp64.  Products keep 22 bits of each entry
+ *              of their factors down to 2^-28 of the matrix's norm (an absolute
+ *              2^-49 of it below) and sum in fp32.
  * Shape rules  1 <= batch <= 65535, 1 <= rows, cols <= 2^22, rows * cols < 2^31,
  *              batch * max(rows, 64) * max(cols, 64) < 2^36,
  *              the smaller of rows and cols <= WTCONV_ORTHO_MAX_SIDE, 1 <=

@@ -8,11 +8,16 @@
 // up to a^5 = 485, and every rounding error with them, so 16-bit factors (an
 // error of 2^-12 at the start) would leave errors of a few per cent in the
 // result.  The fp32 matrix instructions are exact enough but run at 1/16 of the
-// fp16 rate.  So every factor is held as the sum of two fp16 numbers, v S = hi
-// + lo with S a power of two (22 bits; S puts the largest possible |v| just
-// under fp16's range, so that lo of values down to 2^-17 is no subnormal), and
-// a product is three fp16 matrix products hi hi + hi lo + lo hi into one fp32
-// accumulator (lo lo is below the 22 bits): 3/16 of the fp32 rate's time.
+// fp16 rate.  So every factor is held as two fp16 numbers, v S = hi + lo / 2^11, S
+// = 2^14, which puts the largest possible |v| just under fp16's range.  hi is off
+// by at most 2^-11 of v S and lo by 2^-11 of that: 22 bits, where fp32 has 24, for
+// |v| down to 2^-28.  Below, hi is a subnormal number (the matrix instructions take
+// it as it is) and v is off by up to 2^-49.  Since v is an entry of a matrix of
+// norm 1, rows and columns of very different sizes keep their own digits.  (With
+// lo in hi's units the error was 2^-39 from 2^-17 down, and the last row of 384 x
+// 1536 graded over 2^-24 was off by 2.5e-3 of itself.)  A product is three fp16
+// matrix products, hi hi into one fp32 accumulator and hi lo + lo hi into another
+// (lo lo is below the 22 bits): 3/16 of the fp32 rate's time.
 //
 // Layout of such a matrix ("planes"): row-major, the columns in blocks of 32,
 // each block 32 hi then 32 lo: 128 bytes, one cache line, one row of a tile.
@@ -268,7 +273,7 @@ __device__ inline void finish(const Product &a, float *res, int z, int ti, int t
             const half8 hi = *(const half8 *)p, lo = *(const half8 *)(p + 32);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                v[q] = fmaf(a.b, (float)hi[q] + (float)lo[q], a.c * v[q]);
+                v[q] = fmaf(a.b, fmaf((float)lo[q], 1.f / kLo, (float)hi[q]), a.c * v[q]);
                 if (i0 + i == j0 + j + q) v[q] += a.a;
             }
             if (a.sym && ti != tj)
@@ -372,7 +377,8 @@ __global__ __launch_bounds__(kThreads, 2) void product(Product a)
         return *(const half8 *)(lds + (s & 1) * kStage + b * kBlock + row * 128 + ((chunk ^ ((row >> 1) & 7)) * 16));
     };
 
-    float16v acc[RB][RB] = {}, term[2] = {};
+    // hi hi, and hi lo + lo hi (RB = 1: each its own, none waits for the one before)
+    float16v acc[RB][RB] = {}, cross[RB][RB] = {}, term = {};
     const int wi = Sh::kWavesK > 1 ? 0 : (wave >> 1) * Sh::kSide, wj = Sh::kWavesK > 1 ? 0 : (wave & 1) * Sh::kSide;
     const int b0 = Sh::kWavesK > 1 ? wave * KW : 0, lr = lane & 31, lc = lane >> 5;
     load(0);
@@ -399,22 +405,28 @@ __global__ __launch_bounds__(kThreads, 2) void product(Product a)
             if (KB > 1 && s * KB + b0 + b >= blocks) continue;  // the last stage's missing blocks
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
-                if constexpr (RB == 1) {  // an accumulator for each term: none waits for the one before
-                    term[0] = mfma(l[b][kk][0][0], r[b][kk][0][1], term[0]);
-                    term[1] = mfma(l[b][kk][0][1], r[b][kk][0][0], term[1]);
+                if constexpr (RB == 1) {
+                    term = mfma(l[b][kk][0][0], r[b][kk][0][1], term);
+                    cross[0][0] = mfma(l[b][kk][0][1], r[b][kk][0][0], cross[0][0]);
                     acc[0][0] = mfma(l[b][kk][0][0], r[b][kk][0][0], acc[0][0]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < RB; ++i)
 #pragma unroll
-                        for (int j = 0; j < RB; ++j)
-                            acc[i][j] =
-                                mfma3(l[b][kk][i][0], l[b][kk][i][1], r[b][kk][j][0], r[b][kk][j][1], acc[i][j]);
+                        for (int j = 0; j < RB; ++j) {
+                            cross[i][j] =
+                                mfma_cross(l[b][kk][i][0], l[b][kk][i][1], r[b][kk][j][0], r[b][kk][j][1], cross[i][j]);
+                            acc[i][j] = mfma(l[b][kk][i][0], r[b][kk][j][0], acc[i][j]);
+                        }
                 }
             }
         }
     }
-    if (RB == 1) acc[0][0] += term[0] + term[1];
+    if (RB == 1) cross[0][0] += term;
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < RB; ++j) acc[i][j] += cross[i][j] * (1.f / kLo);
 
     if (slice >= 0) {
         float4 *p = a.part + ((int64_t)(g - a.full) * a.slices + slice) * (RB * RB * 4 * kThreads) + t;

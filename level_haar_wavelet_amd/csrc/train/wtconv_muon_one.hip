@@ -196,7 +196,7 @@ __global__ __launch_bounds__(kThreads, 1) void ortho_one(Args a)
     _Float16 *turn = (_Float16 *)slots[wave];
     for (int step = 0; step < a.steps; ++step) {
         // this wave's part of A = X X^T
-        float16v acc[NB][NB] = {};
+        float16v acc[NB][NB] = {}, cross[NB][NB] = {};
 #pragma unroll
         for (int k = 0; k < NT; ++k) {
             if (k * kWaves + wave >= tiles) continue;
@@ -224,7 +224,10 @@ __global__ __launch_bounds__(kThreads, 1) void ortho_one(Args a)
 #pragma unroll
                 for (int i = 0; i < NB; ++i)
 #pragma unroll
-                    for (int j = 0; j < NB; ++j) acc[i][j] = mfma3(hi[i], lo[i], hi[j], lo[j], acc[i][j]);
+                    for (int j = 0; j < NB; ++j) {
+                        cross[i][j] = mfma_cross(hi[i], lo[i], hi[j], lo[j], cross[i][j]);
+                        acc[i][j] = mfma(hi[i], hi[j], acc[i][j]);
+                    }
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -232,11 +235,13 @@ __global__ __launch_bounds__(kThreads, 1) void ortho_one(Args a)
 #pragma unroll
         for (int i = 0; i < NB; ++i)
 #pragma unroll
-            for (int j = 0; j < NB; ++j)
+            for (int j = 0; j < NB; ++j) {
+                acc[i][j] += cross[i][j] * (1.f / kLo);
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     part[((i * NB + j) * 4 + q) * 64 + lane] = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1],
                                                                            acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+            }
         __syncthreads();
         for (int e = t; e < NB * NB * 256; e += kThreads) {
             float4 s = ((const float4 *)slots[0])[e];
@@ -268,7 +273,7 @@ __global__ __launch_bounds__(kThreads, 1) void ortho_one(Args a)
         // block (i, j) of P: the rows of block i of A are, by symmetry, blocks
         // (k, i) with the lane's column as the row
         auto poly = [&](int i, int j) {
-            float16v s = {};
+            float16v s = {}, cross = {};
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
                 const float16v u = block(k, i), v = block(k, j);
@@ -277,9 +282,11 @@ __global__ __launch_bounds__(kThreads, 1) void ortho_one(Args a)
                     half8 uh, ul, vh, vl;
                     operand(u, kk, 1.f / kScale, uh, ul);
                     operand(v, kk, 1.f / kScale, vh, vl);
-                    s = mfma3(uh, ul, vh, vl, s);
+                    cross = mfma_cross(uh, ul, vh, vl, cross);
+                    s = mfma(uh, vh, s);
                 }
             }
+            s += cross * (1.f / kLo);
             const float16v A = block(i, j);
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
@@ -318,17 +325,20 @@ __global__ __launch_bounds__(kThreads, 1) void ortho_one(Args a)
 #pragma unroll
         for (int k = 0; k < NT; ++k) {
             if (k * kWaves + wave >= tiles) continue;
-            float16v y[NB] = {};
+            float16v y[NB] = {}, lows[NB] = {};
 #pragma unroll
             for (int i = 0; i < NB; ++i)
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int kk = 0; kk < 2; ++kk)
-                        y[i] = mfma3(ph[b][i][kk], pl[b][i][kk], xh[k][b][kk], xl[k][b][kk], y[i]);
+                    for (int kk = 0; kk < 2; ++kk) {
+                        lows[i] = mfma_cross(ph[b][i][kk], pl[b][i][kk], xh[k][b][kk], xl[k][b][kk], lows[i]);
+                        y[i] = mfma(ph[b][i][kk], xh[k][b][kk], y[i]);
+                    }
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 __builtin_amdgcn_sched_barrier(0);
+                y[i] += lows[i] * (1.f / kLo);
                 if (!last)
 #pragma unroll
                     for (int kk = 0; kk < 2; ++kk) operand(y[i], kk, 1.f / kScale, xh[k][i][kk], xl[k][i][kk]);

@@ -390,3 +390,43 @@ def test_muon_step_of_large_matrices(shape):
     tol = lr * scale * (ortho_tol(rw, 5, torch.float32) + 8 * U * 3.4445 ** 5) + 4 * U * torch.linalg.matrix_norm(w.double())
     err = torch.linalg.matrix_norm(wo.cpu().double() - rw)
     assert (err <= tol).all(), (shape, err / tol)
+
+
+@pytest.mark.parametrize("n", [30, 60, 130], ids=["one_block", "two_blocks", "tiles"])
+def test_small_entries_next_to_large_ones(n):
+    """One step on diag(d), d from 1 down to 2^-44: element i comes out as
+    p(x_i) = a x + b x^3 + c x^5, x = d / |d|.  x is off by 2^-22 x or, below 2^-28
+    (hi is a subnormal fp16 number of x 2^14, whose rest, up to 2^-25, is held to
+    half of 2^-24 2^-11), by 2^-50; the diagonal of the polynomial's matrix by 2^-22
+    of 3.45 and by about 40 2^-22 x^2 from x^2 and x^4; the fp32 sums add 2^-22 p
+    at most.  The lo lo that is left out is 2^-22 p too, and below 2^-28, where lo
+    holds a rest of up to 2^-39, 2^-11 3.45 of that: another 3.45 2^-50."""
+    torch.manual_seed(n)
+    d = (1 + torch.rand(n)) * torch.pow(2.0, -torch.arange(n) * 44.0 / (n - 1))
+    for copies in ((1, 1), (1, 2), (2, 1)):  # two equal blocks: sums over both, singular values sqrt 2 larger
+        g = torch.diag(d).repeat(copies)
+        got = wt.wtconv_orthogonalize(g.cuda(), steps=1, eps=0.0).cpu().double()
+        ref = ortho64(g, 1, 0.0)
+        x = (d.double() * math.sqrt(max(copies)) / g.double().norm()).repeat(copies[0])
+        tol = 2.0 ** -22 * (3.45 * 4 * x + 40 * x ** 3) + 3.45 * 2.0 ** -49
+        assert ((got - ref).abs() <= tol[:, None]).all(), ((got - ref).abs() / tol[:, None]).max()
+        assert torch.equal(got[ref == 0], torch.zeros_like(got[ref == 0]))
+
+
+@pytest.mark.parametrize("shape", [(25, 384), (64, 512), (64, 1024), (384, 1536), (1030, 300), (1, 2048, 2048)], ids=str)
+def test_rows_graded_over_many_powers_of_two(shape):
+    """Every row keeps its own digits.  Row i of size x_i among others of up to 1:
+    its entries and the polynomial's are off by 2^-22 of themselves (down to
+    2^-28; here 2^-24 2^-6), lo lo by as much, and A_ij, about x_i x_j, by 2^-22 of
+    itself, which P X brings to row i as 4.8 2^-22 x_i x_j^2, with sum x_j^2 = 1:
+    8 2^-22 a step, five steps."""
+    g = torch.Generator().manual_seed(1)
+    *b, r, c = shape
+    n = min(r, c)
+    scale = torch.pow(2.0, -torch.arange(n) * 24.0 / (n - 1))
+    m = torch.randn(shape, generator=g) * (scale[:, None] if r <= c else scale)
+    got = wt.wtconv_orthogonalize(m.cuda()).cpu().double().view(r, c)
+    ref = ortho64(m.view(r, c).cuda()).cpu()
+    dim = 1 if r <= c else 0
+    over = (got - ref).norm(dim=dim) / ref.norm(dim=dim) / (40 * 2.0 ** -22)
+    assert over.max() <= 1, over.max()
