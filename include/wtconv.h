@@ -239,7 +239,9 @@ wtconv_status_t wtconv_unfused_backward_weight(const wtconv_desc_t *desc, const 
  * Alignment    activations are aligned to their element; any such address
  *              works, 16-byte aligned ones are faster.
  * Values       a group with a NaN or an infinity comes out as NaN (relu of it
- *              included); other groups are not touched by it.
+ *              included); other groups are not touched by it.  A group whose sum
+ *              of squared differences passes fp32's range has an infinite
+ *              variance: rstd 0, y = act(beta).  gelu's erf is within 1.5e-7.
  * Ownership, execution and errors are those of the layer's calls above:
  * kernels only, no allocation, no state, bitwise reproducible; the workspace
  * (256-byte aligned, wtconv_group_norm_workspace_size) belongs to one call at

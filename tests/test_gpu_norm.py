@@ -456,3 +456,20 @@ def test_long_sums_of_equal_gradients(shape, dtype, layouts):
     # for the rest, xh up to 7; half a step of 16 bits is below that
     tol = rstd.max().item() * d * u * ((16 + 28 + 128 + 8) + 7 * (16 + 28 + 136 + 8))
     assert dx.float().abs().max().item() <= tol
+
+
+@pytest.mark.parametrize("layouts", LAYOUTS, ids=str)
+@pytest.mark.parametrize("shape", [(2, 16, 40, 40, 4), (2, 16, 8, 8, 4), (1, 8, 256, 16, 2), (300, 2, 64, 64, 2),
+                                   (1, 512, 64, 64, 1)], ids=str)
+def test_a_variance_beyond_fp32(shape, layouts):
+    """A spread of 1e20: the variance is infinite, as include/wtconv.h says."""
+    n, c, h, w, groups = shape
+    lx, ly = layouts
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = layout(1e20 * torch.randn(n, c, h, w, generator=g, device="cuda"), lx)
+    beta = torch.randn(c, generator=g, device="cuda")
+    y, mean, rstd = wt.wtconv_group_norm_forward(x, groups, None, beta, channels_last=ly)
+    assert torch.equal(rstd, torch.zeros_like(rstd)) and torch.isfinite(mean).all()
+    assert torch.equal(y, beta.view(1, c, 1, 1).expand_as(y))
+    dx, _, _ = wt.wtconv_group_norm_backward(x, layout(torch.ones_like(x), ly), groups, mean, rstd, None, beta)
+    assert torch.equal(dx, torch.zeros_like(dx))
