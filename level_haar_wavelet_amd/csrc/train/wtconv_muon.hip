@@ -206,10 +206,11 @@ typedef __attribute__((address_space(3))) void *LdsPtr;
 //
 // P X of 4096^3 (tiles of 128) takes 400 to 430 us: 0.96 to 1.03 PFLOP/s of fp16
 // products, where the library's product of that size reaches 1.09; the card's
-// power limit holds both.  1024^3 (tiles of 64, 256 of them) takes 17 us: 12.6 without its loads,
-// 16.3 without its matrix instructions, so it waits for its operands' way from
-// the L2s.  Three or four buffers instead of two: 15.4 us there, but 9.6 to 13 us
-// instead of 9 for the symmetric products.
+// power limit holds both.  The last one, with the weights, takes 450 to 480.  1024^3
+// (tiles of 64, 256 of them) takes 17 us: 12.6 without its loads, 16.3 without its
+// matrix instructions, so it waits for its operands' way from the L2s.  Three or
+// four buffers instead of two: 15.4 us there, but 9.6 to 13 us instead of 9 for the
+// symmetric products.
 // DEEP (is_deep()): a compute unit has one workgroup only, whose stages take
 // twice the k: X of 384x1536 9.4 -> 9.0 us (tiles of 64), its Gram product 10.8 us in
 // one piece where cut along k and joined it took 12.

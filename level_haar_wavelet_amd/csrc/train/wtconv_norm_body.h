@@ -13,11 +13,11 @@
 //                pass, which takes the ranges from the last to the first: the
 //                256 MB cache holds the end of what was read before.
 //
-// Both are bound by memory: of 3 E e and 5 E e bytes, 32x128x128x128 bf16 planes
-// to channels last takes 68 us (5.9 TB/s), the backward pass of 64x96x56x56 fp32
-// 72 us (5.3) and of 16x256x256x256 fp16 481 us (5.6), where an elementwise pass
-// over 4 GiB reaches 6.2.  Below about 20 MB the launches count: 64x192x28x28 fp16
-// takes 22 us, its bytes alone 9.
+// Large ones are bound by memory, whose counters show those 3 E e and 5 E e:
+// 32x128x128x128 bf16 planes to channels last takes 69 us (5.9 TB/s), the backward
+// pass of 64x96x56x56 fp32 73 us (5.3) and of 16x256x256x256 fp16 481 us (5.6), where
+// an elementwise pass over 4 GiB reaches 6.2.  Below about 20 MB latency counts: the
+// two kernels of 64x192x28x28 fp16 take 8.1 and 14.8 us, their bytes 3.1 and 6.2.
 //
 // Walks.  An image lies in memory as rows of contiguous elements: its channels'
 // planes, or its pixels' channels.  A thread takes V contiguous elements (16
