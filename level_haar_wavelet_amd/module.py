@@ -140,7 +140,8 @@ class GroupNormAct2d(torch.nn.Module):
     groups of neighbouring channels, act "none", "relu", "silu" or "gelu".
     channels_last=True writes the output channels last whatever the input's
     layout is (what a product over the channels reads); None keeps the input's.
-    Initialisation: gamma one, beta zero (none with affine=False).
+    Initialisation: gamma one, beta zero (none with affine=False).  Both stay
+    float32, whatever the input's type; an empty batch is refused.
     """
 
     def __init__(self, groups: int, channels: int, eps: float = 1e-5, act: str = "none", affine: bool = True,

@@ -473,3 +473,30 @@ def test_a_variance_beyond_fp32(shape, layouts):
     assert torch.equal(y, beta.view(1, c, 1, 1).expand_as(y))
     dx, _, _ = wt.wtconv_group_norm_backward(x, layout(torch.ones_like(x), ly), groups, mean, rstd, None, beta)
     assert torch.equal(dx, torch.zeros_like(dx))
+
+
+@pytest.mark.parametrize("layouts", LAYOUTS, ids=str)
+@pytest.mark.parametrize("shape", [(1, 512, 64, 64, 1), (2, 1024, 7, 8, 512), (1, 6, 600, 600, 2)], ids=str)
+def test_a_bad_value_in_groups_of_many_channels_and_of_few(shape, layouts):
+    """Groups whose ranges a kernel between the walks joins, a workgroup or a wave
+    each: the bad value, in the first set of its group or a later one, stays there."""
+    n, c, h, w, groups = shape
+    lx, ly = layouts
+    x, dy, gamma, beta = inputs(shape, "f32", 12)
+    clean = wt.wtconv_group_norm_forward(layout(x.cuda(), lx), groups, gamma.cuda(), beta.cuda(), act="silu",
+                                         channels_last=ly)[0]
+    per = c // groups
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for ch, row in ((0, 0), (per - 1, h - 1)):
+            v = x.clone()
+            v[n - 1, ch, row, w - 1] = bad
+            v = layout(v.cuda(), lx)
+            y, mean, rstd = wt.wtconv_group_norm_forward(v, groups, gamma.cuda(), beta.cuda(), act="silu",
+                                                         channels_last=ly)
+            dx, _, _ = wt.wtconv_group_norm_backward(v, layout(dy.cuda(), ly), groups, mean, rstd, gamma.cuda(),
+                                                     beta.cuda(), act="silu")
+            hit = torch.zeros(n, c, 1, 1, dtype=torch.bool)
+            hit[n - 1, :per] = True
+            hit = hit.expand_as(x).cuda()
+            assert torch.isnan(y[hit]).all() and torch.isnan(dx[hit]).all(), (bad, ch)
+            assert torch.equal(y[~hit], clean[~hit]) and torch.isfinite(dx[~hit]).all(), (bad, ch)
