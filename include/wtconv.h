@@ -91,7 +91,7 @@ typedef enum {
 typedef enum {
     WTCONV_F32 = 0,
     WTCONV_F16 = 1,
-    WTCONV_BF16 = 2 /* group norm and Newton-Schulz calls only; the layer's calls refuse it */
+    WTCONV_BF16 = 2 /* the calls around the layer only; the layer's own refuse it */
 } wtconv_dtype_t;
 
 typedef enum {
@@ -343,6 +343,129 @@ typedef struct {
 wtconv_status_t wtconv_muon_step(const wtconv_ortho_desc_t *desc, const wtconv_muon_t *hyper, const float *weight,
                                  const void *grad, const float *momentum, float *weight_out, float *momentum_out,
                                  void *workspace, size_t workspace_bytes, wtconv_stream_t stream);
+
+/* ---- Root-mean-square norm with the residual's addition --------------------
+ * In front of the products over the channels, channels last: for each of `rows`
+ * rows of c values
+ *   h = x + residual (as stored, in the activations' type; h = x where residual is NULL),
+ *   rstd = 1 / sqrt(sum h^2 / c + eps),  y = gamma h rstd.
+ * Layout       x, residual, y, h and their gradients row-major [rows][c], no
+ *              gaps; gamma [c] fp32 or NULL (ones); rstd [rows] fp32.
+ * Types        fp32, fp16 or bf16, one for all of a call's activations.  Sums and
+ *              products are fp32 (or wider); an output element is rounded once.
+ * Shape rules  rows, c >= 1, c <= 2^24, rows * c < 2^40, rows < 2^31, eps > 0 and
+ *              finite.
+ * Alignment    to the element; 16-byte aligned activations are faster.
+ * Values       a row with a NaN or an infinity comes out as NaN or zero times it;
+ *              no other row is touched by it.  A row whose sum of squares passes
+ *              fp32's range has rstd 0 and y = 0.
+ * Ownership, execution and errors are those of the layer's calls above. */
+typedef struct {
+    int64_t rows, c;
+    int32_t dtype; /* wtconv_dtype_t of the activations */
+    float eps;
+} wtconv_rms_desc_t;
+
+/* Bytes of workspace for op WTCONV_OP_FWD (0) or WTCONV_OP_BWD. */
+wtconv_status_t wtconv_rms_norm_workspace_size(const wtconv_rms_desc_t *desc, wtconv_op_t op, size_t *bytes);
+
+/* y, rstd and, where residual is given, h (else h is not written and may be
+ * NULL).  h may be x or residual themselves (in place); other overlaps of an
+ * output with an argument are refused. */
+wtconv_status_t wtconv_rms_norm_forward(const wtconv_rms_desc_t *desc, const void *x, const void *residual,
+                                        const float *gamma, void *y, void *h, float *rstd, wtconv_stream_t stream);
+
+/* With t = gamma dy and hh = h rstd:
+ *   dx = rstd (t - hh sum(t hh) / c) + dh   (also the residual's gradient),
+ *   dgamma = sum over the rows of dy hh.
+ * h and rstd are the forward call's; dh (the gradient that reaches h by its other
+ * way) may be NULL, and so may dgamma.  dx may be dh itself (in place). */
+wtconv_status_t wtconv_rms_norm_backward(const wtconv_rms_desc_t *desc, const void *h, const void *dy,
+                                         const void *dh, const float *gamma, const float *rstd, void *dx,
+                                         float *dgamma, void *workspace, size_t workspace_bytes,
+                                         wtconv_stream_t stream);
+
+/* ---- Gated product over the channels ---------------------------------------
+ * The first half of a gated feed-forward block, both projections, the activation
+ * and the product in one kernel: for each row of x (a pixel, channels last)
+ *   g = x w_gate^T + b_gate,  u = x w_up^T + b_up,  h = act(g) * u,
+ * act one of wtconv_act_t.
+ * Layout       x [rows][c], h [rows][f], w_gate and w_up [f][c], all row-major, no
+ *              gaps; b_gate, b_up [f] fp32, each may be NULL (zeros).
+ * Types        activations, weights and their gradients fp32, fp16 or bf16, one
+ *              for all of a call's; biases and their gradients fp32.  Products of
+ *              16-bit types are exact and sum in fp32.  fp32 factors are taken as
+ *              three bf16 numbers each (24 bits), whose products of up to 2^-16 of
+ *              the whole are kept.  The backward pass holds dg and du in the
+ *              activations' type between its products (fp16: their size is limited
+ *              to 65504, as that of any fp16 gradient); the biases' gradients sum
+ *              them before that rounding.
+ * Shape rules  rows, c, f >= 1, c and f <= 65536, rows < 2^30, rows * c and rows * f
+ *              < 2^36.
+ * Alignment    x and the weights 16 bytes in 16-bit types where 8 divides c, else to the
+ *              element; the others to the element (16 bytes is faster).
+ * Values       a row with a NaN or an infinity gives NaN or an infinity in that
+ *              row of h and dx, and in the weights' gradients; no other row is
+ *              touched by it.  gelu's erf is within 1.5e-7; relu's slope at a g that
+ *              rounds to zero is 0.
+ * Ownership, execution and errors are those of the layer's calls above; one
+ * workspace of wtconv_gated_workspace_size bytes serves one call at a time. */
+typedef struct {
+    int64_t rows, c, f;
+    int32_t dtype; /* wtconv_dtype_t of activations and weights */
+    int32_t act;   /* wtconv_act_t */
+} wtconv_gated_desc_t;
+
+/* Bytes of workspace for op WTCONV_OP_FWD or WTCONV_OP_BWD; may be 0. */
+wtconv_status_t wtconv_gated_workspace_size(const wtconv_gated_desc_t *desc, wtconv_op_t op, size_t *bytes);
+
+wtconv_status_t wtconv_gated_forward(const wtconv_gated_desc_t *desc, const void *x, const void *w_gate,
+                                     const void *w_up, const float *b_gate, const float *b_up, void *h,
+                                     void *workspace, size_t workspace_bytes, wtconv_stream_t stream);
+
+/* With dg = dh u act'(g) and du = dh act(g), g and u computed again from x:
+ *   dx = dg w_gate + du w_up,
+ *   dw_gate = dg^T x,  dw_up = du^T x,  db_gate = sum dg,  db_up = sum du.
+ * dx may be NULL, dw_gate and dw_up both, and db_gate and db_up both: what is
+ * not asked for is not computed (at least one output is). */
+wtconv_status_t wtconv_gated_backward(const wtconv_gated_desc_t *desc, const void *x, const void *dh,
+                                      const void *w_gate, const void *w_up, const float *b_gate, const float *b_up,
+                                      void *dx, void *dw_gate, void *dw_up, float *db_gate, float *db_up,
+                                      void *workspace, size_t workspace_bytes, wtconv_stream_t stream);
+
+/* ---- Global gradient norm and clipping --------------------------------------
+ * What stands between a backward pass and the optimiser's step: over all elements
+ * g of `count` tensors, of any types among fp32, fp16 and bf16,
+ *   norm = sqrt(sum g^2),  out = g * min(1, max_norm / (norm + eps)).
+ * The squares and their sum are fp64 (fp32's range of g has no effect on it), the
+ * result is rounded to fp32 once (infinity beyond fp32's range), an element of out
+ * once to its type.  A NaN among the elements makes the norm and every output NaN,
+ * an infinity makes the norm infinite, the finite elements' outputs zero and its own
+ * NaN.
+ * Shape rules  0 <= count <= 65536 (0: norm 0), elems >= 0 each, less than 2^40
+ *              together; max_norm >= 0 and eps >= 0, both finite, and not both 0.
+ * Layout       contiguous elements, aligned to the element (16 bytes is faster).  The
+ *              table is host memory, read before the call returns; a captured
+ *              call replays with the addresses it was captured with.
+ * An out may be its own grad (in place; where nothing is clipped nothing is then
+ * written); other overlaps of an output with a tensor are refused.
+ * Ownership, execution and errors are those of the layer's calls above; a workspace
+ * of wtconv_grad_norm_workspace_size bytes serves one of the two calls at a time. */
+typedef struct {
+    const void *grad;
+    void *out;      /* wtconv_clip_grad_norm only */
+    int64_t elems;
+    int32_t dtype;  /* wtconv_dtype_t of grad and out */
+    int32_t unused; /* 0 */
+} wtconv_tensor_t;
+
+wtconv_status_t wtconv_grad_norm_workspace_size(int64_t count, size_t *bytes);
+
+wtconv_status_t wtconv_grad_norm(const wtconv_tensor_t *tensors, int64_t count, float *norm, void *workspace,
+                                 size_t workspace_bytes, wtconv_stream_t stream);
+
+wtconv_status_t wtconv_clip_grad_norm(const wtconv_tensor_t *tensors, int64_t count, float max_norm, float eps,
+                                      float *norm, void *workspace, size_t workspace_bytes, wtconv_stream_t stream);
 
 /* Human-readable name of a status code (static string). */
 const char *wtconv_status_string(wtconv_status_t status);

@@ -9,7 +9,11 @@ Activations are (N, C, H, W) float32 or float16, contiguous.
 
 Next to the layer stand the group norm with its activation that follows it in a
 block (wtconv_group_norm_*; float32, float16 or bfloat16, contiguous or channels
-last) and the update of its weights (wtconv_orthogonalize, wtconv_muon_step).
+last) and the update of its weights (wtconv_orthogonalize, wtconv_muon_step); for
+the block's half over the channels, the root-mean-square norm with the residual's
+addition (wtconv_rms_norm_*) and the gated product (wtconv_gated_*); and between
+the backward pass and the update, the gradients' global norm and clipping
+(wtconv_grad_norm, wtconv_clip_grad_norm).
 """
 from __future__ import annotations
 
@@ -20,7 +24,10 @@ from . import _native
 __all__ = ["wtconv_forward", "wtconv_backward_data", "wtconv_backward_weight", "wtconv_backward",
            "wtconv_backward_weight_noalloc", "wtconv_workspace_size", "library_path",
            "wtconv_group_norm_forward", "wtconv_group_norm_backward", "wtconv_group_norm_workspace_size",
-           "wtconv_orthogonalize", "wtconv_muon_step", "wtconv_orthogonalize_workspace_size"]
+           "wtconv_orthogonalize", "wtconv_muon_step", "wtconv_orthogonalize_workspace_size",
+           "wtconv_rms_norm_forward", "wtconv_rms_norm_backward", "wtconv_rms_norm_workspace_size",
+           "wtconv_gated_forward", "wtconv_gated_backward", "wtconv_gated_workspace_size",
+           "wtconv_grad_norm", "wtconv_clip_grad_norm", "wtconv_grad_norm_workspace_size"]
 
 
 def library_path() -> str:
@@ -218,9 +225,12 @@ def wtconv_backward_weight_noalloc(x, dy, w_base, bias, s_base, w_lvl, s_lvl, gr
 
 
 
-# bound at their first use: their module imports torch, this one does not
+# bound at their first use: their modules import torch, this one does not
 _TRAIN = ("wtconv_group_norm_forward", "wtconv_group_norm_backward", "wtconv_group_norm_workspace_size",
           "wtconv_orthogonalize", "wtconv_muon_step", "wtconv_orthogonalize_workspace_size")
+_BLOCK = ("wtconv_rms_norm_forward", "wtconv_rms_norm_backward", "wtconv_rms_norm_workspace_size",
+          "wtconv_gated_forward", "wtconv_gated_backward", "wtconv_gated_workspace_size",
+          "wtconv_grad_norm", "wtconv_clip_grad_norm", "wtconv_grad_norm_workspace_size")
 
 
 def __getattr__(name):
@@ -228,5 +238,10 @@ def __getattr__(name):
         from . import _train
 
         globals().update({n: getattr(_train, n) for n in _TRAIN})
+        return globals()[name]
+    if name in _BLOCK:
+        from . import _block
+
+        globals().update({n: getattr(_block, n) for n in _BLOCK})
         return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -43,6 +43,20 @@ class MuonHyper(ctypes.Structure):
                 ("scale", ctypes.c_float), ("nesterov", ctypes.c_int32)]
 
 
+class RmsDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("c", ctypes.c_int64), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class GatedDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("c", ctypes.c_int64), ("f", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32)]
+
+
+class TensorEntry(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("elems", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("unused", ctypes.c_int32)]
+
+
 class WtconvError(RuntimeError):
     def __init__(self, status, what):
         super().__init__("%s returned %s" % (what, STATUS.get(status, status)))
@@ -54,6 +68,7 @@ _lib = None
 # name -> argument types (pointers as void*), all return wtconv_status_t (int)
 _vp, _sz, _dp = ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(WtconvDesc)
 _ndp, _odp = ctypes.POINTER(NormDesc), ctypes.POINTER(OrthoDesc)
+_rdp, _gdp, _szp = ctypes.POINTER(RmsDesc), ctypes.POINTER(GatedDesc), ctypes.POINTER(ctypes.c_size_t)
 SIGNATURES = {
     "wtconv_workspace_size": [_dp, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)],
     "wtconv_forward": [_dp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
@@ -72,6 +87,15 @@ SIGNATURES = {
     "wtconv_orthogonalize_workspace_size": [_odp, ctypes.POINTER(ctypes.c_size_t)],
     "wtconv_orthogonalize": [_odp, _vp, _vp, _vp, _sz, _vp],
     "wtconv_muon_step": [_odp, ctypes.POINTER(MuonHyper), _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "wtconv_rms_norm_workspace_size": [_rdp, ctypes.c_int, _szp],
+    "wtconv_rms_norm_forward": [_rdp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "wtconv_rms_norm_backward": [_rdp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "wtconv_gated_workspace_size": [_gdp, ctypes.c_int, _szp],
+    "wtconv_gated_forward": [_gdp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "wtconv_gated_backward": [_gdp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "wtconv_grad_norm_workspace_size": [ctypes.c_int64, _szp],
+    "wtconv_grad_norm": [_vp, ctypes.c_int64, _vp, _vp, _sz, _vp],
+    "wtconv_clip_grad_norm": [_vp, ctypes.c_int64, ctypes.c_float, ctypes.c_float, _vp, _vp, _sz, _vp],
 }
 
 

@@ -1,0 +1,35 @@
+// wtconv_clip.h -- launch entry points of the gradient norm and clipping kernels.
+#ifndef WTCONV_CLIP_H
+#define WTCONV_CLIP_H
+
+#include <hip/hip_runtime.h>
+
+#include "../../../include/wtconv.h"
+
+namespace wtc_clip {
+
+constexpr int64_t kRanges = 2048;   // ranges that the elements are cut into, about
+constexpr int64_t kLeast = 8192;    // elements of a range at least
+constexpr int64_t kOwnSums = 4096;  // ranges whose sums every workgroup of the clip joins itself
+
+// Elements of a range.  A tensor's last range may be shorter, so there are at most
+// kRanges + count of them.
+inline int64_t range_elems(int64_t elems)
+{
+    const int64_t r = (elems + kRanges - 1) / kRanges;
+    return r < kLeast ? kLeast : (r + 2047) / 2048 * 2048;
+}
+
+// fp64 sums of all ranges, and the total of more than kOwnSums.
+inline size_t workspace_bytes(int64_t count)
+{
+    return ((size_t)(kRanges + count + 1) * sizeof(double) + 255) / 256 * 256;
+}
+
+}  // namespace wtc_clip
+
+// norm alone (clip false), or norm and the outputs.
+hipError_t wtc_launch_clip(const wtconv_tensor_t *t, int64_t count, bool clip, float max_norm, float eps, float *norm,
+                           double *parts, hipStream_t stream);
+
+#endif  // WTCONV_CLIP_H

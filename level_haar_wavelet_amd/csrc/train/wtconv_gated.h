@@ -1,0 +1,58 @@
+// wtconv_gated.h -- plan and launch entry points of the gated product's kernels.
+#ifndef WTCONV_GATED_H
+#define WTCONV_GATED_H
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../../include/wtconv.h"
+
+namespace wtc_gated {
+
+constexpr int kFewRows = 64;  // rows up to which the forward call takes the weights' rows one by one
+
+struct Forward {
+    const void *x, *w_gate, *w_up;
+    const float *b_gate, *b_up;
+    void *h;
+};
+
+struct Backward {
+    const void *x, *dh, *w_gate, *w_up;
+    const float *b_gate, *b_up;
+    void *dx, *dw_gate, *dw_up;
+    float *db_gate, *db_up;
+};
+
+// A product's tile (side of the rows, of the columns) and its cut along k into
+// `slices` of `cut` stages each.
+struct Tiles {
+    int bm, bn;
+    int64_t tm;
+    int tn, slices;
+    int64_t cut;
+};
+
+// The calls' plan, a function of the sizes and types alone.
+struct Plan {
+    int planes;          // 16-bit numbers of a factor: 1, fp32: 3
+    bool pack;           // x and the weights are laid out anew (fp32, or rows of no whole accesses)
+    int cp, fp;          // row lengths in the workspace: c and f up to a multiple of 8
+    Tiles dual, dx, dw;  // g and u; dx; the weights' gradients
+    int64_t bias_rows;   // rows of the biases' partial sums
+    // bytes
+    size_t x, w, grads, wt, bias, part;
+};
+
+Plan make_plan(const wtconv_gated_desc_t &d);
+size_t workspace_bytes(const wtconv_gated_desc_t &d, bool backward);
+
+template <typename T>
+hipError_t forward(const wtconv_gated_desc_t &d, const Forward &a, void *workspace, hipStream_t stream);
+template <typename T>
+hipError_t backward(const wtconv_gated_desc_t &d, const Backward &a, void *workspace, hipStream_t stream);
+
+}  // namespace wtc_gated
+
+#endif  // WTCONV_GATED_H

@@ -1,0 +1,5 @@
+// wtconv_gated_bf16.hip -- the gated product's kernels for bf16 activations.
+#include "wtconv_gated_body.h"
+
+template hipError_t wtc_gated::forward<__bf16>(const wtconv_gated_desc_t &, const wtc_gated::Forward &, void *, hipStream_t);
+template hipError_t wtc_gated::backward<__bf16>(const wtconv_gated_desc_t &, const wtc_gated::Backward &, void *, hipStream_t);

@@ -36,25 +36,6 @@ wtconv_status_t check_workspace(const void *ws, size_t have, size_t need)
     return aligned_to(ws, 256) ? WTCONV_OK : WTCONV_ERR_UNSUPPORTED;
 }
 
-struct Span {
-    const void *p;
-    size_t bytes;
-};
-
-// Whether one of the outputs overlaps an input or another output (null ones
-// and those of no bytes do not).
-bool any_alias(const Span *in, int nin, const Span *out, int nout)
-{
-    for (int i = 0; i < nout; ++i) {
-        if (!out[i].p || !out[i].bytes) continue;
-        for (int j = 0; j < nin; ++j)
-            if (in[j].p && in[j].bytes && overlaps2(out[i].p, out[i].bytes, in[j].p, in[j].bytes)) return true;
-        for (int j = 0; j < i; ++j)
-            if (out[j].p && out[j].bytes && overlaps2(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return true;
-    }
-    return false;
-}
-
 bool float_aligned(const void *p) { return aligned_to(p, 4); }
 
 }  // namespace

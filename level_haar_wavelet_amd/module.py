@@ -11,7 +11,8 @@ wtconv_backward_weight); this module only hands tensors to them.  The layer
 saves only its input for the backward pass.
 
 GroupNormAct2d is the normalisation and activation that follow the layer in a
-block, in the same manner.
+block, RMSNorm and GatedLinear the norm with the residual's addition and the gated
+product of its half over the channels (channels last), in the same manner.
 """
 from __future__ import annotations
 
@@ -20,10 +21,12 @@ import math
 import torch
 
 from . import _native
-from . import (wtconv_backward_data, wtconv_backward_weight, wtconv_forward, wtconv_group_norm_backward,
-               wtconv_group_norm_forward)
+from . import (wtconv_backward_data, wtconv_backward_weight, wtconv_forward, wtconv_gated_backward,
+               wtconv_gated_forward, wtconv_group_norm_backward, wtconv_group_norm_forward, wtconv_rms_norm_backward,
+               wtconv_rms_norm_forward)
 
-__all__ = ["WTConvFunction", "WTConv2d", "GroupNormActFunction", "GroupNormAct2d"]
+__all__ = ["WTConvFunction", "WTConv2d", "GroupNormActFunction", "GroupNormAct2d", "RMSNormFunction", "RMSNorm",
+           "GatedFunction", "GatedLinear"]
 
 
 class WTConvFunction(torch.autograd.Function):
@@ -171,3 +174,135 @@ class GroupNormAct2d(torch.nn.Module):
     def extra_repr(self):
         return "groups=%d, channels=%d, eps=%g, act=%s, affine=%s, channels_last=%s" % (
             self.groups, self.channels, self.eps, self.act, self.gamma is not None, self.channels_last)
+
+
+class RMSNormFunction(torch.autograd.Function):
+    """(y, h): h = x + residual, y = gamma h / rms(h) over the last dimension
+    (wtconv_rms_norm_forward / _backward); without a residual y alone.
+
+    x, residual: (..., C) float32, float16 or bfloat16 on the GPU (strided ones are
+    made contiguous); gamma: (C,) float32 or None.  Saves h and 1 / rms."""
+
+    @staticmethod
+    def forward(ctx, x, residual, gamma, eps):
+        x = x.contiguous()
+        if residual is not None:
+            residual = residual.contiguous()
+        y, h, rstd = wtconv_rms_norm_forward(x, residual, gamma, eps=eps)
+        ctx.save_for_backward(h, gamma, rstd)
+        ctx.set_materialize_grads(False)
+        return y if residual is None else (y, h)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, gamma, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        if dy is None:  # y was not used
+            return dh if need[0] else None, dh if need[1] else None, None, None
+        dy = dy.to(h.dtype).contiguous()
+        if dh is not None:
+            dh = dh.to(h.dtype).contiguous()
+        dx, dgamma = wtconv_rms_norm_backward(h, dy, rstd, gamma, dh=dh)
+        return dx if need[0] else None, dx if need[1] else None, dgamma if need[2] else None, None
+
+
+class RMSNorm(torch.nn.Module):
+    """Root-mean-square norm over the last dimension (channels last), alone or
+    with a residual's addition in front: norm(x) is y, norm(x, residual) is (y, h)
+    with h = x + residual, which goes on as the residual of what follows.
+    Initialisation: gamma one (none with affine=False).  It stays float32, whatever
+    the input's type; an empty batch is refused.
+    """
+
+    def __init__(self, channels: int, eps: float = 1e-6, affine: bool = True, device=None):
+        super().__init__()
+        if channels < 1:
+            raise ValueError("channels must be >= 1")
+        if not 0 < eps < math.inf:
+            raise ValueError("eps must be positive and finite")
+        self.channels, self.eps = channels, eps
+        if affine:
+            self.gamma = torch.nn.Parameter(torch.ones(channels, device=device, dtype=torch.float32))
+        else:
+            self.register_parameter("gamma", None)
+
+    def forward(self, x, residual=None):
+        if x.dim() < 1 or x.shape[-1] != self.channels:
+            raise ValueError("expected (..., C) with C = %d channels, got %s" % (self.channels, tuple(x.shape)))
+        if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
+            raise ValueError("the residual must match x in shape and type")
+        return RMSNormFunction.apply(x, residual, self.gamma, self.eps)
+
+    def extra_repr(self):
+        return "channels=%d, eps=%g, affine=%s" % (self.channels, self.eps, self.gamma is not None)
+
+
+class GatedFunction(torch.autograd.Function):
+    """h = act(x w_gate^T + b_gate) * (x w_up^T + b_up) (wtconv_gated_forward /
+    _backward).
+
+    x: (..., C) float32, float16 or bfloat16 on the GPU (a strided one is made
+    contiguous); w_gate, w_up: (F, C) of x's type, or of another one and then
+    rounded to it for the products (float32 weights under 16-bit activations), and
+    their gradients come back in theirs; b_gate, b_up: (F,) float32 or None.  Saves
+    x and the weights; the backward pass computes both projections again."""
+
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, b_gate, b_up, act):
+        x = x.contiguous()
+        h = wtconv_gated_forward(x, w_gate.to(x.dtype).contiguous(), w_up.to(x.dtype).contiguous(), b_gate, b_up,
+                                 act=act)
+        ctx.save_for_backward(x, w_gate, w_up, b_gate, b_up)
+        ctx.act = act
+        return h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh):
+        x, w_gate, w_up, b_gate, b_up = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        asked = (need[0], need[1] or need[2], need[3] or need[4])
+        dx, dwg, dwu, dbg, dbu = wtconv_gated_backward(
+            x, dh.to(x.dtype).contiguous(), w_gate.to(x.dtype).contiguous(), w_up.to(x.dtype).contiguous(), b_gate,
+            b_up, act=ctx.act, need=asked)
+        return (dx, dwg.to(w_gate.dtype) if need[1] else None, dwu.to(w_up.dtype) if need[2] else None,
+                dbg if need[3] else None, dbu if need[4] else None, None)
+
+
+class GatedLinear(torch.nn.Module):
+    """The first half of a gated feed-forward block over the last dimension
+    (channels last): two projections from `channels` to `hidden`, the one through
+    `act` ("none", "relu", "silu" or "gelu") times the other.  A linear layer back to
+    `channels` usually follows.  Parameters w_gate, w_up (hidden, channels) and, with
+    bias=True, b_gate, b_up (hidden,) stay float32, whatever the input's type; 16-bit
+    inputs take the weights rounded to their type.  Initialisation: weights
+    uniform within 1 / sqrt(channels), biases zero; an empty batch is refused.
+    """
+
+    def __init__(self, channels: int, hidden: int, act: str = "silu", bias: bool = True, device=None):
+        super().__init__()
+        if channels < 1 or hidden < 1:
+            raise ValueError("channels and hidden must be >= 1")
+        if act not in _native.ACTS:
+            raise ValueError("act must be one of %s, got %r" % (", ".join(sorted(_native.ACTS)), act))
+        f = dict(device=device, dtype=torch.float32)
+        self.channels, self.hidden, self.act = channels, hidden, act
+        bound = channels ** -0.5
+        self.w_gate = torch.nn.Parameter(torch.empty(hidden, channels, **f).uniform_(-bound, bound))
+        self.w_up = torch.nn.Parameter(torch.empty(hidden, channels, **f).uniform_(-bound, bound))
+        if bias:
+            self.b_gate = torch.nn.Parameter(torch.zeros(hidden, **f))
+            self.b_up = torch.nn.Parameter(torch.zeros(hidden, **f))
+        else:
+            self.register_parameter("b_gate", None)
+            self.register_parameter("b_up", None)
+
+    def forward(self, x):
+        if x.dim() < 1 or x.shape[-1] != self.channels:
+            raise ValueError("expected (..., C) with C = %d channels, got %s" % (self.channels, tuple(x.shape)))
+        return GatedFunction.apply(x, self.w_gate, self.w_up, self.b_gate, self.b_up, self.act)
+
+    def extra_repr(self):
+        return "channels=%d, hidden=%d, act=%s, bias=%s" % (self.channels, self.hidden, self.act,
+                                                           self.b_gate is not None)

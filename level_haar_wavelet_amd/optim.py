@@ -1,5 +1,7 @@
-"""The Muon optimiser over libwtconv: every update is the momentum of the
-gradient, orthogonalised by the Newton-Schulz iteration (wtconv_muon_step).
+"""The Muon optimiser and the clipping of gradients over libwtconv.
+
+Muon: every update is the momentum of the gradient, orthogonalised by the
+Newton-Schulz iteration (wtconv_muon_step).
 
 It is for parameters that are matrices: the layer's convolution weights and the
 products next to it.  A parameter of shape (*batch, rows, *rest) is a stack of
@@ -20,9 +22,27 @@ import math
 
 import torch
 
-from . import _native, _train, wtconv_muon_step
+from . import _native, _train, wtconv_clip_grad_norm, wtconv_muon_step
 
-__all__ = ["Muon"]
+__all__ = ["Muon", "clip_grad_norm_"]
+
+
+@torch.no_grad()
+def clip_grad_norm_(parameters, max_norm, eps=1e-6):
+    """Scales the gradients of `parameters` (one or an iterable; those without a
+    gradient are passed over, one that is there twice counts once) in place so that
+    the norm over all of them is at most max_norm, and returns the norm before, a
+    float32 tensor on their device (wtconv_clip_grad_norm; no synchronisation).
+    Gradients are float32, float16 or bfloat16 on one GPU."""
+    parameters = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
+    grads = list({id(p.grad): p.grad for p in parameters if p.grad is not None}.values())
+    # a strided gradient is scaled in a copy
+    dense = [g.contiguous() for g in grads]
+    norm, _ = wtconv_clip_grad_norm(dense, max_norm, eps=eps, device=parameters[0].device if parameters else None)
+    for g, d in zip(grads, dense):
+        if d is not g:
+            g.copy_(d)
+    return norm
 
 
 def _matrices(shape, batch_dims):

@@ -1,0 +1,262 @@
+"""Root-mean-square norm, gated product and clipping entry points without a GPU:
+descriptors and arguments are refused with the documented codes before anything is
+launched, and the binding and the modules refuse what the entry points cannot take."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import level_haar_wavelet_amd as wt
+from level_haar_wavelet_amd import _native
+from level_haar_wavelet_amd.module import GatedLinear, RMSNorm
+from level_haar_wavelet_amd.optim import clip_grad_norm_
+
+OK, NULL, SHAPE, UNSUPPORTED, WORKSPACE, HIP, ALIAS = range(7)
+BIG = 1 << 50
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return _native.load()
+
+
+def ref(d):
+    return ctypes.byref(d)
+
+
+def at(i):
+    return 0x10000000 * (i + 1)
+
+
+BAD_RMS = [
+    (dict(rows=0), SHAPE), (dict(c=0), SHAPE), (dict(rows=-1), SHAPE), (dict(rows=1 << 31), SHAPE),
+    (dict(c=(1 << 24) + 1), SHAPE), (dict(rows=1 << 20, c=1 << 20), SHAPE), (dict(rows=1 << 62), SHAPE),
+    (dict(eps=0.0), SHAPE), (dict(eps=-1.0), SHAPE), (dict(eps=float("nan")), SHAPE), (dict(eps=float("inf")), SHAPE),
+    (dict(dtype=3), UNSUPPORTED), (dict(dtype=-1), UNSUPPORTED),
+]
+
+
+@pytest.mark.parametrize("kw,expect", BAD_RMS, ids=str)
+def test_rms_descriptors_are_refused(lib, kw, expect):
+    v = dict(rows=4, c=8, dtype=0, eps=1e-6, **{}) | kw
+    d = _native.RmsDesc(v["rows"], v["c"], v["dtype"], v["eps"])
+    out = ctypes.c_size_t(7)
+    for op in (0, 3):
+        assert lib.wtconv_rms_norm_workspace_size(ref(d), op, ref(out)) == expect and out.value == 7
+    assert lib.wtconv_rms_norm_forward(ref(d), *(at(i) for i in range(6)), None) == expect
+    assert lib.wtconv_rms_norm_backward(ref(d), *(at(i) for i in range(8)), BIG, None) == expect
+
+
+def test_rms_arguments_are_refused(lib):
+    d = _native.RmsDesc(64, 96, 0, 1e-6)
+    n = 64 * 96 * 4
+    out = ctypes.c_size_t(0)
+    assert lib.wtconv_rms_norm_workspace_size(None, 3, ref(out)) == NULL
+    assert lib.wtconv_rms_norm_workspace_size(ref(d), 3, None) == NULL
+    for op in (1, 2, 4):
+        assert lib.wtconv_rms_norm_workspace_size(ref(d), op, ref(out)) == UNSUPPORTED
+    assert lib.wtconv_rms_norm_workspace_size(ref(d), 0, ref(out)) == OK and out.value == 0
+    assert lib.wtconv_rms_norm_workspace_size(ref(d), 3, ref(out)) == OK
+    need = out.value
+    assert need > 0
+
+    def fwd(x=at(0), residual=at(1), gamma=at(2), y=at(3), h=at(4), rstd=at(5)):
+        return lib.wtconv_rms_norm_forward(ref(d), x, residual, gamma, y, h, rstd, None)
+
+    def bwd(h=at(0), dy=at(1), dh=at(2), gamma=at(3), rstd=at(4), dx=at(5), dgamma=at(6), ws=at(7), nbytes=need):
+        return lib.wtconv_rms_norm_backward(ref(d), h, dy, dh, gamma, rstd, dx, dgamma, ws, nbytes, None)
+
+    for k in ("x", "y", "h", "rstd"):
+        assert fwd(**{k: None}) == NULL
+    for k in ("x", "residual", "gamma", "y", "h", "rstd"):
+        assert fwd(**{k: at(9) + 2}) == UNSUPPORTED
+    assert fwd(y=at(0)) == ALIAS and fwd(y=at(1) + n - 4) == ALIAS and fwd(y=at(4)) == ALIAS and fwd(rstd=at(3)) == ALIAS
+    assert fwd(h=at(0) + 4) == ALIAS and fwd(h=at(1) - 4) == ALIAS and fwd(h=at(2)) == ALIAS and fwd(h=at(5)) == ALIAS
+    for k in ("h", "dy", "rstd", "dx"):
+        assert bwd(**{k: None}) == NULL
+    for k in ("h", "dy", "dh", "gamma", "rstd", "dx", "dgamma"):
+        assert bwd(**{k: at(9) + 2}) == UNSUPPORTED
+    assert bwd(ws=None) == WORKSPACE and bwd(nbytes=need - 1) == WORKSPACE and bwd(ws=at(7) + 16) == UNSUPPORTED
+    assert bwd(dx=at(0)) == ALIAS and bwd(dx=at(1) + 8) == ALIAS and bwd(dx=at(2) + 8) == ALIAS
+    assert bwd(dgamma=at(5)) == ALIAS and bwd(dgamma=at(2)) == ALIAS and bwd(dgamma=at(3)) == ALIAS
+    assert bwd(ws=at(0)) == ALIAS and bwd(ws=at(5)) == ALIAS and bwd(ws=at(6)) == ALIAS and bwd(ws=at(2)) == ALIAS
+
+
+BAD_GATED = [
+    (dict(rows=0), SHAPE), (dict(c=0), SHAPE), (dict(f=0), SHAPE), (dict(rows=-5), SHAPE), (dict(rows=1 << 30), SHAPE),
+    (dict(c=65537), SHAPE), (dict(f=65537), SHAPE), (dict(rows=1 << 20, c=1 << 16), SHAPE),
+    (dict(rows=1 << 20, f=1 << 16), SHAPE), (dict(rows=1 << 62), SHAPE), (dict(dtype=3), UNSUPPORTED),
+    (dict(dtype=-1), UNSUPPORTED), (dict(act=4), UNSUPPORTED), (dict(act=-1), UNSUPPORTED),
+]
+
+
+@pytest.mark.parametrize("kw,expect", BAD_GATED, ids=str)
+def test_gated_descriptors_are_refused(lib, kw, expect):
+    v = dict(rows=100, c=64, f=96, dtype=2, act=2) | kw
+    d = _native.GatedDesc(v["rows"], v["c"], v["f"], v["dtype"], v["act"])
+    out = ctypes.c_size_t(7)
+    for op in (0, 3):
+        assert lib.wtconv_gated_workspace_size(ref(d), op, ref(out)) == expect and out.value == 7
+    assert lib.wtconv_gated_forward(ref(d), *(at(i) for i in range(7)), BIG, None) == expect
+    assert lib.wtconv_gated_backward(ref(d), *(at(i) for i in range(12)), BIG, None) == expect
+
+
+@pytest.mark.parametrize("dtype", [0, 2])
+def test_gated_arguments_are_refused(lib, dtype):
+    d = _native.GatedDesc(100, 64, 96, dtype, 2)
+    e = 2 if dtype else 4
+    n = 100 * 64 * e
+    sizes = []
+    for op in (0, 3):
+        out = ctypes.c_size_t(0)
+        assert lib.wtconv_gated_workspace_size(None, op, ref(out)) == NULL
+        assert lib.wtconv_gated_workspace_size(ref(d), op, None) == NULL
+        assert lib.wtconv_gated_workspace_size(ref(d), op, ref(out)) == OK
+        sizes.append(out.value)
+    for op in (1, 2, 4):
+        assert lib.wtconv_gated_workspace_size(ref(d), op, ref(out)) == UNSUPPORTED
+    assert sizes[0] == (0 if dtype else sizes[0]) and sizes[1] > 0
+
+    def fwd(x=at(0), wg=at(1), wu=at(2), bg=at(3), bu=at(4), h=at(5), ws=at(6), nbytes=sizes[0]):
+        return lib.wtconv_gated_forward(ref(d), x, wg, wu, bg, bu, h, ws, nbytes, None)
+
+    def bwd(x=at(0), dh=at(1), wg=at(2), wu=at(3), bg=at(4), bu=at(5), dx=at(6), dwg=at(7), dwu=at(8), dbg=at(9),
+            dbu=at(10), ws=at(11), nbytes=sizes[1]):
+        return lib.wtconv_gated_backward(ref(d), x, dh, wg, wu, bg, bu, dx, dwg, dwu, dbg, dbu, ws, nbytes, None)
+
+    for k in ("x", "wg", "wu", "h"):
+        assert fwd(**{k: None}) == NULL
+    for k in ("x", "dh", "wg", "wu", "dwg", "dwu", "dbg", "dbu"):
+        assert bwd(**{k: None}) == NULL
+    assert bwd(dx=None, dwg=None, dwu=None, dbg=None, dbu=None) == NULL
+    for k in ("x", "wg", "wu", "bg", "bu", "h"):
+        assert fwd(**{k: at(20) + 1}) == UNSUPPORTED
+    for k in ("x", "dh", "wg", "wu", "bg", "bu", "dx", "dwg", "dwu", "dbg", "dbu"):
+        assert bwd(**{k: at(20) + 1}) == UNSUPPORTED
+    if dtype:  # read in whole accesses
+        for k in ("x", "wg", "wu"):
+            assert fwd(**{k: at(20) + 8}) == UNSUPPORTED and bwd(**{k: at(20) + 8}) == UNSUPPORTED
+    for k in (0, 1, 2):
+        assert fwd(h=at(k) + 16) == ALIAS
+    for k in ("dx", "dwg", "dwu"):
+        for i in range(4):
+            assert bwd(**{k: at(i) + 16}) == ALIAS
+    assert bwd(dx=at(7)) == ALIAS and bwd(dwg=at(8)) == ALIAS and bwd(dbg=at(10)) == ALIAS and bwd(dbu=at(4)) == ALIAS
+    assert bwd(ws=None) == WORKSPACE and bwd(nbytes=sizes[1] - 1) == WORKSPACE and bwd(ws=at(11) + 16) == UNSUPPORTED
+    for i in range(11):
+        assert bwd(ws=at(i)) == ALIAS
+    if not dtype:
+        assert fwd(ws=None) == WORKSPACE and fwd(nbytes=sizes[0] - 1) == WORKSPACE
+        assert fwd(ws=at(6) + 8) == UNSUPPORTED and fwd(ws=at(0)) == ALIAS and fwd(ws=at(5)) == ALIAS
+    assert n  # sizes above keep the arguments apart by default
+    assert 0x10000000 > max(sizes)
+
+
+def test_every_gated_plan_is_whole(lib):
+    """Workspaces of a sweep of sizes: nonnegative, and of the order of the gradients they keep."""
+    out = ctypes.c_size_t(0)
+    for rows in (1, 2, 63, 64, 65, 127, 128, 129, 1000, 4097, 200704, 1 << 24):
+        for c in (1, 7, 8, 9, 63, 64, 96, 100, 1000, 4096, 65536):
+            for f in (1, 8, 31, 64, 65, 300, 5632, 65536):
+                if rows * max(c, f) >= 1 << 36:
+                    continue
+                for dtype in range(3):
+                    d = _native.GatedDesc(rows, c, f, dtype, 2)
+                    for op in (0, 3):
+                        assert lib.wtconv_gated_workspace_size(ref(d), op, ref(out)) == OK
+                        cp, fp = c + 8, f + 8
+                        keep = 6 * (rows * cp + 2 * f * cp + (rows * 2 * fp + c * 2 * fp if op else 0))
+                        part = 64 * 4 * max(min(rows, 1 << 15) * c, 2 * fp * c) + 8 * rows * fp if op else 0
+                        assert out.value <= keep + part + 4096, (rows, c, f, dtype, op, out.value)
+
+
+def tensors(*rows):
+    t = (_native.TensorEntry * max(len(rows), 1))()
+    for i, (grad, out, elems, dtype) in enumerate(rows):
+        t[i].grad, t[i].out, t[i].elems, t[i].dtype = grad, out, elems, dtype
+    return t
+
+
+def test_clip_arguments_are_refused(lib):
+    out = ctypes.c_size_t(7)
+    for count in (-1, 65537):
+        assert lib.wtconv_grad_norm_workspace_size(count, ref(out)) == SHAPE and out.value == 7
+    assert lib.wtconv_grad_norm_workspace_size(3, None) == NULL
+    assert lib.wtconv_grad_norm_workspace_size(2, ref(out)) == OK
+    need = out.value
+
+    def both(rows, count=None, norm=at(8), ws=at(9), nbytes=need, max_norm=1.0, eps=1e-6, table=True):
+        t = tensors(*rows) if table else None
+        n = len(rows) if count is None else count
+        a = lib.wtconv_grad_norm(t, n, norm, ws, nbytes, None)
+        b = lib.wtconv_clip_grad_norm(t, n, max_norm, eps, norm, ws, nbytes, None)
+        return a, b
+
+    good = [(at(0), at(1), 100, 0), (at(2), at(2), 50, 2)]
+    assert both(good, count=-1) == (SHAPE, SHAPE) and both(good, count=65537) == (SHAPE, SHAPE)
+    assert both(good, table=False) == (NULL, NULL) and both(good, norm=None) == (NULL, NULL)
+    assert both(good, ws=None) == (WORKSPACE, WORKSPACE) and both(good, nbytes=need - 1) == (WORKSPACE, WORKSPACE)
+    assert both(good, ws=at(9) + 8) == (UNSUPPORTED, UNSUPPORTED) and both(good, norm=at(8) + 2) == (UNSUPPORTED,) * 2
+    for bad, expect in (((None, at(1), 4, 0), NULL), ((at(0), at(1), -1, 0), SHAPE), ((at(0), at(1), 1 << 40, 0), SHAPE),
+                        ((at(0), at(1), 1 << 62, 0), SHAPE), ((at(0), at(1), 4, 3), UNSUPPORTED),
+                        ((at(0), at(1), 4, -1), UNSUPPORTED), ((at(0) + 2, at(1), 4, 0), UNSUPPORTED),
+                        ((at(0) + 1, at(1), 4, 1), UNSUPPORTED), ((at(8), at(1), 4, 0), ALIAS),
+                        ((at(9) + 64, at(1), 4, 0), ALIAS)):
+        assert both([good[1], bad]) == (expect, expect), bad
+    assert both([(at(0), at(1), 1 << 39, 0), (at(2), at(3), 1 << 39, 0)]) == (SHAPE, SHAPE)
+
+    def clip(*rows, max_norm=1.0, eps=1e-6):
+        return both(rows, max_norm=max_norm, eps=eps)[1]
+
+    for kw in (dict(max_norm=-1.0), dict(max_norm=math.nan), dict(max_norm=math.inf), dict(eps=-1e-9),
+               dict(eps=math.nan), dict(eps=math.inf), dict(max_norm=0.0, eps=0.0)):
+        t = tensors(*good)
+        v = dict(max_norm=1.0, eps=1e-6) | kw
+        assert lib.wtconv_clip_grad_norm(t, 2, v["max_norm"], v["eps"], at(8), at(9), need, None) == SHAPE
+    for rows, expect in ((((at(0), None, 4, 0),), NULL), (((at(0), at(1) + 2, 4, 0),), UNSUPPORTED),
+                         (((at(0), at(0) + 4, 4, 0),), ALIAS), (((at(0), at(8), 4, 0),), ALIAS),
+                         (((at(0), at(0), 4, 0), (at(0), at(0), 4, 0)), ALIAS),
+                         (((at(0), at(1), 4, 0), (at(2), at(1), 4, 0)), ALIAS),
+                         (((at(0), at(1), 8, 0), (at(1) + 16, at(3), 4, 0)), ALIAS),
+                         (((at(1), at(3), 4, 0), (at(0), at(1), 8, 0)), ALIAS)):
+        t = tensors(*rows)
+        assert lib.wtconv_clip_grad_norm(t, len(rows), 1.0, 1e-6, at(8), at(9), need, None) == expect, rows
+
+
+def test_binding_refuses_cpu_tensors():
+    x, w = torch.zeros(4, 8), torch.zeros(6, 8)
+    for call in (lambda: wt.wtconv_rms_norm_forward(x), lambda: wt.wtconv_rms_norm_backward(x, x, torch.zeros(4)),
+                 lambda: wt.wtconv_gated_forward(x, w, w), lambda: wt.wtconv_gated_backward(x, torch.zeros(4, 6), w, w),
+                 lambda: wt.wtconv_grad_norm([x]), lambda: wt.wtconv_clip_grad_norm([x], 1.0),
+                 lambda: wt.wtconv_clip_grad_norm(x, 1.0)):
+        with pytest.raises(TypeError, match="GPU tensor"):
+            call()
+    with pytest.raises(TypeError, match="not on a GPU"):
+        wt.wtconv_grad_norm([], device="cpu")
+    p = torch.nn.Parameter(x)
+    with pytest.raises(TypeError, match="GPU"):
+        clip_grad_norm_([p], 1.0)
+    p.grad = torch.ones_like(x)
+    with pytest.raises(TypeError, match="GPU"):
+        clip_grad_norm_([p], 1.0)
+
+
+def test_modules_check_their_options_and_inputs():
+    for kw in (dict(channels=0), dict(channels=8, eps=0.0), dict(channels=8, eps=float("nan")),
+               dict(channels=8, eps=float("inf"))):
+        with pytest.raises(ValueError):
+            RMSNorm(**kw)
+    for kw in (dict(channels=0, hidden=8), dict(channels=8, hidden=0), dict(channels=8, hidden=8, act="tanh")):
+        with pytest.raises(ValueError):
+            GatedLinear(**kw)
+    for m in (RMSNorm(8), RMSNorm(8, affine=False), GatedLinear(8, 12), GatedLinear(8, 12, bias=False)):
+        assert "8" in repr(m)
+        for shape in ((3, 4), (8, 3), ()):
+            with pytest.raises(ValueError, match="channels"):
+                m(torch.zeros(shape))
+    with pytest.raises(ValueError, match="residual"):
+        RMSNorm(8)(torch.zeros(3, 8), torch.zeros(4, 8))
+    with pytest.raises(ValueError, match="residual"):
+        RMSNorm(8)(torch.zeros(3, 8), torch.zeros(3, 8, dtype=torch.bfloat16))
+    assert GatedLinear(8, 12).w_gate.shape == (12, 8) and RMSNorm(8, affine=False).gamma is None
