@@ -45,19 +45,18 @@ Plan make_plan(const wtconv_gated_desc_t &d)
     p.cp = (int)((d.c + 7) / 8 * 8);
     p.fp = (int)((d.f + 7) / 8 * 8);
     const bool one = p.planes == 1;
-    const int bk = one ? 64 : 32;  // of a stage along k
+    constexpr int bk = 32;  // of a stage along k
     const int64_t kc = (d.c + bk - 1) / bk, kf = (2 * p.fp + bk - 1) / bk, km = (d.rows + bk - 1) / bk;
     // the large tile where there are enough of them
-    const int big = one ? 256 : 128;
     auto pick = [&](int64_t m, int64_t n, int64_t stages, bool cut, int half) {
-        const Tiles t = tiles_of(m, n, 256, big / half, stages, cut);
-        if (t.tm * t.tn >= kUnits) return t;
+        const Tiles t = tiles_of(m, n, 256, 256 / half, stages, cut);
+        if (one && t.tm * t.tn >= kUnits) return t;
         return tiles_of(m, n, 128, 128 / half, stages, cut);
     };
     p.dual = pick(d.rows, d.f, kc, false, 2);
     p.dx = pick(d.rows, d.c, kf, true, 1);
-    p.dw = one ? pick(2 * p.fp, d.c, km, true, 1) : tiles_of(2 * p.fp, d.c, 128, 128, km, true);
-    p.bias_rows = p.dual.tm * (p.dual.bm == 256 && !one ? 4 : 2);
+    p.dw = pick(2 * p.fp, d.c, km, true, 1);
+    p.bias_rows = p.dual.tm * 2;  // of the waves along the rows
     if (p.pack) {
         p.x = align256((size_t)(d.rows * p.cp) * p.planes * 2);
         p.w = align256((size_t)(d.f * 2 * p.cp) * p.planes * 2);

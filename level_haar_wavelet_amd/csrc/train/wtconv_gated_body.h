@@ -73,20 +73,19 @@ __device__ inline float4v mfma16(const Vec<float, 4> &l, const Vec<float, 4> &r,
     return c;
 }
 
-// The smaller products first.
-template <typename F, int P>
-__device__ inline float16v mfma_planes(const F (&l)[P], const F (&r)[P], float16v c)
-{
-    if constexpr (P == 1) return mfma(l[0], r[0], c);
-    else {
-        c = mfma(l[2], r[0], c);
-        c = mfma(l[0], r[2], c);
-        c = mfma(l[1], r[1], c);
-        c = mfma(l[1], r[0], c);
-        c = mfma(l[0], r[1], c);
-        return mfma(l[0], r[0], c);
-    }
-}
+// The products of P x P numbers that count, the smaller ones first.
+template <int P>
+struct Pairs;
+template <>
+struct Pairs<1> {
+    static constexpr int kCount = 1;
+    static constexpr int l[1] = {0}, r[1] = {0};
+};
+template <>
+struct Pairs<3> {
+    static constexpr int kCount = 6;
+    static constexpr int l[6] = {2, 0, 1, 1, 0, 0}, r[6] = {0, 2, 1, 0, 1, 0};
+};
 
 // v as the sum of P numbers.  fp32: its bits from the top, eight at a time; an
 // infinity or NaN whole in the first (what is left of it would be NaN).
@@ -142,16 +141,69 @@ __device__ inline float act_slope(int kind, float z, float &slope)
     return z;
 }
 
-// What a lane loads in place of a row's missing end.
-__device__ const uint32_t kZeros[4] = {0, 0, 0, 0};
+// ---- Memory to LDS -------------------------------------------------------------
+//
+// Loads that go from memory into LDS without registers between, in rings of
+// buffers: written as assembly, since the compiler would wait for every such load
+// before any read of LDS.  The waits are wait_loads() and the barrier behind it.
 
-typedef const __attribute__((address_space(1))) void *GlobalPtr;
-typedef __attribute__((address_space(3))) void *LdsPtr;
+typedef uint32_t Descriptor __attribute__((ext_vector_type(4)));
 
-// 16 bytes a lane from memory into LDS, lanes side by side from `to` on.
-__device__ inline void load_lds(const void *from, char *to)
+// Memory from `base` on, `bytes` long; reads beyond it give zeros.
+__device__ inline Descriptor descriptor(const void *base, int64_t bytes)
 {
-    __builtin_amdgcn_global_load_lds((GlobalPtr)from, (LdsPtr)to, 16, 0, 0);
+    const uint64_t b = (uint64_t)base;
+    const uint32_t n = bytes < 0 ? 0u : bytes > 0x7fffffff ? 0x7fffffffu : (uint32_t)bytes;
+    Descriptor d;
+    d[0] = __builtin_amdgcn_readfirstlane((uint32_t)b);
+    d[1] = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32) & 0xffffu);
+    d[2] = __builtin_amdgcn_readfirstlane(n);
+    d[3] = 0x00020000u;
+    return d;
+}
+
+constexpr uint32_t kOutside = 0x7ffffff0u;  // an offset that no descriptor reaches
+
+// 16 bytes a lane from offset `lane + wave` into LDS, lanes side by side from `to` on.
+__device__ inline void load_lds(const Descriptor &d, uint32_t lane, uint32_t wave, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :
+                 : "v"(lane), "s"(d), "s"(wave), "s"(to)
+                 : "memory", "m0");
+}
+
+__device__ inline uint32_t lds_offset(const void *p)
+{
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
+}
+
+// Waits until at most N of this wave's loads are in flight, and for its reads of LDS.
+template <int N>
+__device__ inline void wait_loads()
+{
+    static_assert(N < 64, "of the counter");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
+}
+
+// The same for the N stages behind the next that are in flight, L loads each; at the
+// end of a sum there are fewer.
+template <int N, int L>
+__device__ inline void wait_stage(int behind)
+{
+    if constexpr (N == 0)
+        wait_loads<0>();
+    else {
+        if (behind >= N)
+            wait_loads<N * L>();
+        else
+            wait_stage<N - 1, L>(behind);
+    }
+}
+
+__device__ inline void barrier()
+{
+    asm volatile("s_barrier" : : : "memory");
 }
 
 // ---- Laying out ----------------------------------------------------------------
@@ -293,115 +345,152 @@ __device__ inline void load4(const T *p, int c, int n, bool wide, float (&v)[4])
     }
 }
 
-// Sums of s[0..15] over the 32 lanes of a half wave, by halves: lane l ends up
-// with that of index (l & 31) / 2.
-__device__ inline float sum_lanes(float (&s)[16])
+// Sums of s[0 .. N) over the 2 N lanes that differ in the bits below 2 N, by halves: lane l
+// ends up with that of index (l % 2 N) / 2.
+template <int N>
+__device__ inline float sum_lanes(const float (&s)[N])
 {
-    const int lane = threadIdx.x & 63;
+    if constexpr (N == 1) {
+        return s[0] + __shfl_xor(s[0], 1);
+    } else {
+        const bool up = threadIdx.x & N;
+        float h[N / 2];
 #pragma unroll
-    for (int o = 16, n = 8; o > 1; o >>= 1, n >>= 1) {
-        const bool up = lane & o;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) {
-                const float keep = up ? s[i + n] : s[i], send = up ? s[i] : s[i + n];
-                s[i] = keep + __shfl_xor(send, o);
-            }
+        for (int i = 0; i < N / 2; ++i)
+            h[i] = (up ? s[i + N / 2] : s[i]) + __shfl_xor(up ? s[i] : s[i + N / 2], N);
+        return sum_lanes<N / 2>(h);
     }
-    return s[0] + __shfl_xor(s[0], 1);
 }
 
-// A tile of BM rows of A and BN rows of B; WM x WN waves.  A stage is 128 (P = 1)
-// or 64 (P = 3) bytes of each row, from memory into LDS without registers between.
-// The 16-byte chunks of a row are permuted so that the rows that a read phase
-// covers fall into different banks.  Two buffers: a stage's reads into registers
-// come first, then the next stage's loads are sent off, then its matrix
-// instructions run.
-template <typename T, int BM, int BN, int WM, int WN, int MODE>
-__global__ __launch_bounds__(WM *WN * 64) void gated_nt(Nt<T> a)
+// One step (16 of the sum's index) of a wave's blocks.
+template <int P, int RM, int RN, typename F>
+__device__ inline void products(float16v (&acc)[RN][RM], const F (&fb)[RN][P], const F (&fa)[RM][P])
+{
+#pragma unroll
+    for (int q = 0; q < Pairs<P>::kCount; ++q)
+#pragma unroll
+        for (int j = 0; j < RN; ++j)
+#pragma unroll
+            for (int i = 0; i < RM; ++i) acc[j][i] = mfma(fb[j][Pairs<P>::l[q]], fa[i][Pairs<P>::r[q]], acc[j][i]);
+}
+
+// A sum of `stages` stages of two steps each, out of a ring of NB buffers in LDS:
+// issue(s) sends off stage s's L loads, read(s, k, f) takes step k's factors out of LDS,
+// multiply(f) runs a step's matrix instructions.  A step's factors are read while the
+// one before is multiplied.  The barrier in the middle of a stage says that all waves
+// have read it whole, so that its buffer can be filled anew, and that the next one
+// is there.
+template <int NB, int L, typename F, typename I, typename R, typename M>
+__device__ inline void ring(int stages, I issue, R read, M multiply)
+{
+    F even, odd;
+#pragma unroll
+    for (int s = 0; s < NB; ++s)
+        if (s < stages) issue(s);
+    wait_stage<NB - 1, L>(stages - 1);
+    barrier();
+    read(0, 0, even);
+    for (int s = 0; s < stages; ++s) {
+        read(s, 1, odd);
+        multiply(even);
+        wait_stage<NB - 2, L>(stages - 2 - s);
+        barrier();
+        if (s + NB < stages) issue(s + NB);
+        if (s + 1 < stages) read(s + 1, 0, even);
+        multiply(odd);
+    }
+}
+
+template <typename E, int P, int RM, int RN>
+struct Factors {
+    Vec<E, 8> a[RM][P], b[RN][P];
+};
+
+// A tile of BM rows of A and BN rows of B; WM x WN waves, NB buffers.  A stage is 64
+// bytes of each row, whose 16-byte chunks are permuted so that the rows that a read
+// phase covers fall into different banks.
+template <typename T, int BM, int BN, int WM, int WN, int NB, int MODE>
+__global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
 {
     typedef typename Factor<T>::type E;
-    typedef Vec<E, 8> Frag;
-    constexpr int P = Factor<T>::kPlanes;
-    constexpr int kRow = P == 1 ? 128 : 64, BK = kRow / 2;          // bytes and elements of a row in a stage
-    constexpr int kRows = BM + BN, kStage = kRows * P * kRow;
-    constexpr int kPerLoad = 1024 / kRow, kLoads = kRows * P / kPerLoad / (WM * WN);
-    static_assert(kLoads * kPerLoad * WM * WN == kRows * P, "rows are shared out evenly");
-    constexpr int RM = BM / WM / 32, RN = BN / WN / 32, KK = BK / 16;  // blocks of a wave; steps of a stage
-    static_assert(MODE == kProduct || RN == 2, "a wave has a block of g and the same of u");
-    __shared__ __attribute__((aligned(128))) char lds[2 * kStage];
+    constexpr int P = Factor<T>::kPlanes, W = WM * WN;
+    constexpr int kRow = 64, BK = 32, kStage = (BM + BN) * P * kRow;
+    // a load takes 16 rows; the waves' loads follow each other
+    constexpr int kA = BM / 16 / W, kB = BN / 16 / W;
+    static_assert(kA * 16 * W == BM && kB * 16 * W == BN, "rows are shared out evenly");
+    constexpr int RM = BM / WM / 32, RN = BN / WN / 32;
+    static_assert(MODE == kProduct || RN % 2 == 0, "a wave has as many blocks of g as of u");
+    typedef Factors<E, P, RM, RN> F;
+    __shared__ __attribute__((aligned(128))) char lds[NB * kStage];
 
     const int slice = MODE == kProduct ? blockIdx.y : 0;
     int64_t ti;
     int tj;
     place(blockIdx.x, a.tm, a.tn, ti, tj);
-    const int t = threadIdx.x, wave = t >> 6, lane = t & 63, lr = lane & 31, lc = lane >> 5;
+    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63, lr = lane & 31, lc = lane >> 5;
     const int64_t m0 = ti * BM;
     const int n0 = tj * (MODE == kProduct ? BN : BN / 2);
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
 
-    auto swizzle = [](int row) { return P == 1 ? (row >> 1) & 7 : (row >> 2) & 3; };
-    const E *src[kLoads];
-    int at[kLoads];  // this lane's place along the sum in a stage
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        const int q = (wave * kLoads + i) * kPerLoad + lane / (kRow / 16), p = q / kRows, row = q % kRows;
-        at[i] = ((lane % (kRow / 16)) ^ swizzle(row)) * 8;
-        if (row < BM) {
-            const int64_t m = m0 + row < a.m ? m0 + row : a.m - 1;
-            src[i] = a.a.p + p * a.a.plane + m * a.a.pitch;
-        } else {
-            const int r = row - BM;
-            const bool up = MODE != kProduct && (r / 32) % 2;
-            int n = MODE == kProduct ? n0 + r : n0 + r / 64 * 32 + r % 32;
-            n = n < a.n ? n : a.n - 1;
-            const Rows<E> &b = up ? a.b1 : a.b0;
-            src[i] = b.p + p * b.plane + n * b.pitch;
-        }
-    }
     const int64_t all = (a.k + BK - 1) / BK, s0 = slice * a.cut;
     const int stages = (int)(MODE == kProduct ? (all - s0 < a.cut ? all - s0 : a.cut) : all);
-    auto load = [&](int s) {
-        const int64_t k = (s0 + s) * BK;
-        char *to = lds + (s & 1) * kStage + wave * kLoads * 1024;
-        if (k + BK <= a.k) {
+    const int k0 = (int)(s0 * BK);
+
+    // Row 16 wave + lane / 4 of the first of this wave's loads, the i-th 16 W i rows
+    // on; the chunk's place in it depends on the row modulo 16 only.
+    const int row = lane >> 2, chunk = (lane & 3) ^ ((row >> 2) & 3);
+    const uint32_t apitch = (uint32_t)a.a.pitch * 2, bpitch = (uint32_t)a.b0.pitch * 2;
+    const uint32_t alane = (row + 16 * wave) * apitch + chunk * 16;
+    // B's rows in memory; g and u: tile rows 64 i .. 64 i + 31 are the gate's rows from
+    // 32 i on, the next 32 the up projection's
+    uint32_t blane, bstep;
+    const E *bp = a.b0.p;
+    if (MODE == kProduct) {
+        blane = (row + 16 * wave) * bpitch + chunk * 16;
+        bstep = 16 * W * bpitch;
+    } else {
+        static_assert(W % 4 == 0, "a wave's loads are all of one matrix");
+        const int first = 16 * wave;
+        if ((first / 32) % 2) bp = a.b1.p;
+        blane = (first / 64 * 32 + first % 32 + row) * bpitch + chunk * 16;
+        bstep = 8 * W * bpitch;
+    }
+    Descriptor da[P], db[P];
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) load_lds(src[i] + k + at[i], to + i * 1024);
-        } else {
+    for (int p = 0; p < P; ++p) {
+        da[p] = descriptor(a.a.p + p * a.a.plane + m0 * a.a.pitch, (a.m - m0) * apitch);
+        db[p] = descriptor(bp + p * a.b0.plane + (int64_t)n0 * a.b0.pitch, (int64_t)(a.n - n0) * bpitch);
+    }
+    const uint32_t base = lds_offset(lds);
+    auto issue = [&](int s) {
+        const int k = k0 + s * BK;
+        // a row's end inside the stage: zeros, not the next row
+        const bool in = k + chunk * 8 < a.k;
+        const uint32_t la = in ? alane : kOutside, lb = in ? blane : kOutside;
+        const uint32_t to = base + s % NB * kStage + wave * 1024;
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                load_lds(k + at[i] < a.k ? (const void *)(src[i] + k + at[i]) : (const void *)kZeros, to + i * 1024);
+        for (int p = 0; p < P; ++p) {
+#pragma unroll
+            for (int i = 0; i < kA; ++i)
+                load_lds(da[p], la, k * 2 + i * 16 * W * apitch, to + p * BM * kRow + i * W * 1024);
+#pragma unroll
+            for (int i = 0; i < kB; ++i)
+                load_lds(db[p], lb, k * 2 + i * bstep, to + P * BM * kRow + p * BN * kRow + i * W * 1024);
         }
     };
-    auto frag = [&](int s, int p, int row, int chunk) {
-        return *(const Frag *)(lds + (s & 1) * kStage + (p * kRows + row) * kRow + ((chunk ^ swizzle(row)) * 16));
-    };
-
-    float16v acc[RN][RM] = {};  // rows: B's, columns: A's
-    load(0);
-    for (int s = 0; s < stages; ++s) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        Frag fa[KK][RM][P], fb[KK][RN][P];
+    auto read = [&](int s, int kk, F &f) {
+        const char *at = lds + s % NB * kStage + (((kk * 2 + lc) ^ ((lr >> 2) & 3)) * 16) + lr * kRow;
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-#pragma unroll
-                for (int i = 0; i < RM; ++i) fa[kk][i][p] = frag(s, p, wm + i * 32 + lr, kk * 2 + lc);
-#pragma unroll
-                for (int j = 0; j < RN; ++j) fb[kk][j][p] = frag(s, p, BM + wn + j * 32 + lr, kk * 2 + lc);
-            }
-        __builtin_amdgcn_sched_barrier(0);
-        if (s + 1 < stages) load(s + 1);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
+        for (int p = 0; p < P; ++p) {
 #pragma unroll
             for (int j = 0; j < RN; ++j)
+                f.b[j][p] = *(const Vec<E, 8> *)(at + P * BM * kRow + (p * BN + wn + j * 32) * kRow);
 #pragma unroll
-                for (int i = 0; i < RM; ++i) acc[j][i] = mfma_planes<Frag, P>(fb[kk][j], fa[kk][i], acc[j][i]);
-    }
+            for (int i = 0; i < RM; ++i) f.a[i][p] = *(const Vec<E, 8> *)(at + (p * BM + wm + i * 32) * kRow);
+        }
+    };
+    float16v acc[RN][RM] = {};  // rows: B's, columns: A's
+    ring<NB, P *(kA + kB), F>(stages, issue, read, [&](const F &f) { products<P, RM, RN>(acc, f.b, f.a); });
 
     // A lane has column m = lr of A's rows and, of B's rows, 8 (q / 4) + 4 lc + q % 4.
     if constexpr (MODE == kProduct) {
@@ -424,70 +513,73 @@ __global__ __launch_bounds__(WM *WN * 64) void gated_nt(Nt<T> a)
         }
         return;
     } else {
-        const int f0 = n0 + wn / 2 + 4 * lc;
-        float bg[16], bu[16];
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-            const int f = f0 + 8 * (q >> 2) + (q & 3);
-            bg[q] = a.bias0 && f < a.n ? a.bias0[f] : 0.f;
-            bu[q] = a.bias1 && f < a.n ? a.bias1[f] : 0.f;
-        }
-        float sg[16] = {}, su[16] = {};
+        for (int j = 0; j < RN; j += 2) {
+            const int f0 = n0 + wn / 2 + j * 16 + 4 * lc;
+            float bg[16], bu[16];
 #pragma unroll
-        for (int i = 0; i < RM; ++i) {
-            const int64_t m = m0 + wm + i * 32 + lr;
-            if (m >= a.m) continue;
+            for (int q = 0; q < 16; ++q) {
+                const int f = f0 + 8 * (q >> 2) + (q & 3);
+                bg[q] = a.bias0 && f < a.n ? a.bias0[f] : 0.f;
+                bu[q] = a.bias1 && f < a.n ? a.bias1[f] : 0.f;
+            }
+            float sg[16] = {}, su[16] = {};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int f = f0 + 8 * q;
-                float g[4], u[4], d[4];
+            for (int i = 0; i < RM; ++i) {
+                const int64_t m = m0 + wm + i * 32 + lr;
+                if (m >= a.m) continue;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    g[e] = acc[0][i][4 * q + e] + bg[4 * q + e];
-                    u[e] = acc[1][i][4 * q + e] + bu[4 * q + e];
-                }
-                if constexpr (MODE == kForward) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) g[e] = act(a.act, g[e]) * u[e];
-                    store4(a.out + m * a.n, f, a.n, a.wide, g);
-                } else {
-                    load4(a.dh + m * a.n, f, a.n, a.wide, d);
-                    // dg and du of columns behind f are zero: dh is
-                    Vec<E, 4> og[P], ou[P];
+                for (int q = 0; q < 4; ++q) {
+                    const int f = f0 + 8 * q;
+                    float g[4], u[4], d[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float slope;
-                        const float y = act_slope(a.act, g[e], slope);
-                        const bool in = f + e < a.n;
-                        const float dg = in ? d[e] * u[e] * slope : 0.f, du = in ? d[e] * y : 0.f;
-                        sg[4 * q + e] += dg;
-                        su[4 * q + e] += du;
-                        E eg[P], eu[P];
-                        split<T, P>(dg, eg);
-                        split<T, P>(du, eu);
-#pragma unroll
-                        for (int p = 0; p < P; ++p) {
-                            og[p][e] = eg[p];
-                            ou[p][e] = eu[p];
-                        }
+                        g[e] = acc[j][i][4 * q + e] + bg[4 * q + e];
+                        u[e] = acc[j + 1][i][4 * q + e] + bu[4 * q + e];
                     }
-                    if (f < a.fp)
+                    if constexpr (MODE == kForward) {
 #pragma unroll
-                        for (int p = 0; p < P; ++p) {
-                            E *row = a.grads + p * a.grads_plane + m * 2 * a.fp + f;
-                            *(Vec<E, 4> *)row = og[p];
-                            *(Vec<E, 4> *)(row + a.fp) = ou[p];
+                        for (int e = 0; e < 4; ++e) g[e] = act(a.act, g[e]) * u[e];
+                        store4(a.out + m * a.n, f, a.n, a.wide, g);
+                    } else {
+                        load4(a.dh + m * a.n, f, a.n, a.wide, d);
+                        // dg and du of columns behind f are zero
+                        Vec<E, 4> og[P], ou[P];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float slope;
+                            const float y = act_slope(a.act, g[e], slope);
+                            const bool in = f + e < a.n;
+                            const float dg = in ? d[e] * u[e] * slope : 0.f, du = in ? d[e] * y : 0.f;
+                            sg[4 * q + e] += dg;
+                            su[4 * q + e] += du;
+                            E eg[P], eu[P];
+                            split<T, P>(dg, eg);
+                            split<T, P>(du, eu);
+#pragma unroll
+                            for (int p = 0; p < P; ++p) {
+                                og[p][e] = eg[p];
+                                ou[p][e] = eu[p];
+                            }
                         }
+                        if (f < a.fp)
+#pragma unroll
+                            for (int p = 0; p < P; ++p) {
+                                E *out = a.grads + p * a.grads_plane + m * 2 * a.fp + f;
+                                *(Vec<E, 4> *)out = og[p];
+                                *(Vec<E, 4> *)(out + a.fp) = ou[p];
+                            }
+                    }
                 }
             }
-        }
-        if (MODE == kBackward && a.bias_part) {
-            const float g = sum_lanes(sg), u = sum_lanes(su);
-            const int q = lr >> 1, f = f0 + 8 * (q >> 2) + (q & 3);
-            if (!(lane & 1) && f < a.n) {
-                float *row = a.bias_part + (ti * WM + wave / WN) * 2 * a.fp;
-                row[f] = g;
-                row[a.fp + f] = u;
+            if (MODE == kBackward && a.bias_part) {
+                const float g = sum_lanes(sg), u = sum_lanes(su);
+                const int q = lr >> 1, f = f0 + 8 * (q >> 2) + (q & 3);
+                if (!(lane & 1) && f < a.n) {
+                    float *out = a.bias_part + (ti * WM + wave / WN) * 2 * a.fp;
+                    out[f] = g;
+                    out[a.fp + f] = u;
+                }
             }
         }
     }
@@ -511,105 +603,87 @@ struct Tn {
 };
 
 // D = A^T B, a tile of BM columns of A (gradients) and BN of B (x), over a slice
-// of the rows, BK of them a stage.  LDS holds rows as they come; the transposing
+// of the rows, 32 of them a stage.  LDS holds rows as they come; the transposing
 // read gives a lane four rows' values of its column: 16 lanes take 4 rows of 32
 // bytes, and these 32-byte pieces are permuted by row so that a read's rows lie in
 // different banks.
-template <typename T, int BM, int BN, int WM, int WN, int BK>
-__global__ __launch_bounds__(WM *WN * 64) void gated_tn(Tn<T> a)
+template <typename T, int BM, int BN, int WM, int WN, int NB>
+__global__ __launch_bounds__(WM *WN * 64, 1) void gated_tn(Tn<T> a)
 {
     typedef typename Factor<T>::type E;
-    typedef Vec<E, 8> Frag;
-    constexpr int P = Factor<T>::kPlanes;
-    constexpr int kA = BM * 2, kB = BN * 2;  // bytes of a row
-    constexpr int kLoadsA = BK * P * kA / 1024 / (WM * WN), kLoadsB = BK * P * kB / 1024 / (WM * WN);
-    static_assert(kLoadsA * 1024 * WM * WN == BK * P * kA && kLoadsB * 1024 * WM * WN == BK * P * kB, "even shares");
-    constexpr int kStageA = BK * P * kA, kStage = kStageA + BK * P * kB;
-    constexpr int RM = BM / WM / 32, RN = BN / WN / 32, KK = BK / 16;
-    __shared__ __attribute__((aligned(128))) char lds[2 * kStage];
+    constexpr int P = Factor<T>::kPlanes, W = WM * WN, BK = 32;
+    constexpr int kRowA = BM * 2, kRowB = BN * 2;  // bytes of a row
+    constexpr int kA = BK * kRowA / 1024 / W, kB = BK * kRowB / 1024 / W;
+    static_assert(kA * 1024 * W == BK * kRowA && kB * 1024 * W == BK * kRowB, "rows are shared out evenly");
+    constexpr int kStageA = BK * P * kRowA, kStage = kStageA + BK * P * kRowB;
+    constexpr int RM = BM / WM / 32, RN = BN / WN / 32;
+    typedef Factors<E, P, RM, RN> F;
+    __shared__ __attribute__((aligned(128))) char lds[NB * kStage];
 
     int64_t ti;
     int tj;
     place(blockIdx.x, a.tm, a.tn, ti, tj);
-    const int t = threadIdx.x, wave = t >> 6, lane = t & 63, lr = lane & 31, lc = lane >> 5;
+    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63, lr = lane & 31, lc = lane >> 5;
     const int f0 = (int)ti * BM, c0 = tj * BN, slice = blockIdx.y;
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
     const int64_t all = (a.m + BK - 1) / BK, s0 = slice * a.cut;
     const int stages = (int)(all - s0 < a.cut ? all - s0 : a.cut);
 
-    const E *srca[kLoadsA], *srcb[kLoadsB];
-    int rowa[kLoadsA], rowb[kLoadsB];  // row of a stage, or a row that none has where there is no such column
+    // A load takes the rows of 1024 bytes, the waves' loads follow each other; where a
+    // chunk goes depends on its row modulo 4, which is the same for all of a wave's.
+    const uint32_t apitch = (uint32_t)a.fp * 4, bpitch = (uint32_t)a.b_pitch * 2;
+    constexpr int kPerA = 1024 / kRowA, kPerB = 1024 / kRowB;
+    static_assert(kPerA * W % 4 == 0 && kPerB * W % 4 == 0, "rows modulo 4");
+    auto place_of = [&](int per, uint32_t pitch) {
+        const int chunks = 64 / per, in = wave * per + lane / chunks, chunk = lane % chunks;
+        return in * pitch + ((((chunk >> 1) ^ ((in & 3) * 2)) * 2) + (chunk & 1)) * 16;
+    };
+    const uint32_t alane = place_of(kPerA, apitch), blane = place_of(kPerB, bpitch);
+    const uint32_t base = lds_offset(lds);
+    auto issue = [&](int s) {
+        const int64_t k = (s0 + s) * BK;  // first row; behind the last one there are zeros
+        const uint32_t to = base + s % NB * kStage + wave * 1024;
 #pragma unroll
-    for (int i = 0; i < kLoadsA; ++i) {
-        const int byte = (wave * kLoadsA + i) * 1024 + lane * 16, q = byte / kA, p = q / BK, row = q % BK,
-                  chunk = byte % kA / 16;
-        const int col = f0 + (((chunk >> 1) ^ ((row & 3) * 2)) * 2 + (chunk & 1)) * 8;
-        srca[i] = a.a + p * a.a_plane + (s0 * BK + row) * 2 * a.fp + col;
-        rowa[i] = col < 2 * a.fp ? row : 1 << 30;
-    }
+        for (int p = 0; p < P; ++p) {
+            // columns behind a row's end come out of the next row, into results that nobody takes
+            const Descriptor da = descriptor(a.a + p * a.a_plane + k * 2 * a.fp + f0, (a.m - k) * apitch - f0 * 2);
+            const Descriptor db = descriptor(a.b + p * a.b_plane + k * a.b_pitch + c0, (a.m - k) * bpitch - c0 * 2);
 #pragma unroll
-    for (int i = 0; i < kLoadsB; ++i) {
-        const int byte = (wave * kLoadsB + i) * 1024 + lane * 16, q = byte / kB, p = q / BK, row = q % BK,
-                  chunk = byte % kB / 16;
-        const int col = c0 + (((chunk >> 1) ^ ((row & 3) * 2)) * 2 + (chunk & 1)) * 8;
-        srcb[i] = a.b + p * a.b_plane + (s0 * BK + row) * a.b_pitch + col;
-        rowb[i] = col < a.b_pitch ? row : 1 << 30;
-    }
-    auto load = [&](int s) {
-        const int64_t k = (s0 + s) * BK;  // first row
-        const int left = a.m - k < BK ? (int)(a.m - k) : BK;
-        char *to = lds + (s & 1) * kStage;
+            for (int i = 0; i < kA; ++i)
+                load_lds(da, alane, i * W * kPerA * apitch, to + p * BK * kRowA + i * W * 1024);
 #pragma unroll
-        for (int i = 0; i < kLoadsA; ++i)
-            load_lds(rowa[i] < left ? (const void *)(srca[i] + (int64_t)s * BK * 2 * a.fp) : (const void *)kZeros,
-                     to + (wave * kLoadsA + i) * 1024);
-#pragma unroll
-        for (int i = 0; i < kLoadsB; ++i)
-            load_lds(rowb[i] < left ? (const void *)(srcb[i] + (int64_t)s * BK * a.b_pitch) : (const void *)kZeros,
-                     to + kStageA + (wave * kLoadsB + i) * 1024);
+            for (int i = 0; i < kB; ++i)
+                load_lds(db, blane, i * W * kPerB * bpitch, to + kStageA + p * BK * kRowB + i * W * 1024);
+        }
     };
     // rows k .. k + 8 (by lc) of columns col .. col + 32
     const int trow = lc * 8 + ((lane & 15) >> 2), tcol = ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
-    auto frag = [&](const char *base, int bytes, int k, int col) {
+    auto frag = [&](const char *from, int bytes, int k, int col) {
         union {
             short4v h[2];
-            Frag f;
+            Vec<E, 8> f;
         } r;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int row = k + trow + 4 * h, c = col + tcol;
-            const char *p = base + row * bytes + (((c >> 4) ^ ((row & 3) * 2)) * 32) + (c & 15) * 2;
+            const int c = col + tcol;
+            const char *p = from + (k + trow + 4 * h) * bytes + (((c >> 4) ^ ((trow & 3) * 2)) * 32) + (c & 15) * 2;
             r.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v *)p);
         }
         return r.f;
     };
+    auto read = [&](int s, int kk, F &f) {
+        const char *la = lds + s % NB * kStage, *lb = la + kStageA;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+#pragma unroll
+            for (int j = 0; j < RN; ++j) f.b[j][p] = frag(lb + p * BK * kRowB, kRowB, kk * 16, wn + j * 32);
+#pragma unroll
+            for (int i = 0; i < RM; ++i) f.a[i][p] = frag(la + p * BK * kRowA, kRowA, kk * 16, wm + i * 32);
+        }
+    };
+    float16v acc[RN][RM] = {};  // [x][gradients]; rows: x's columns, columns: the gradients'
+    ring<NB, P *(kA + kB), F>(stages, issue, read, [&](const F &f) { products<P, RM, RN>(acc, f.b, f.a); });
 
-    float16v acc[RM][RN] = {};  // [gradients][x]; rows: x's columns, columns: the gradients'
-    load(0);
-    for (int s = 0; s < stages; ++s) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        const char *la = lds + (s & 1) * kStage, *lb = la + kStageA;
-        Frag fa[KK][RM][P], fb[KK][RN][P];
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-#pragma unroll
-                for (int i = 0; i < RM; ++i) fa[kk][i][p] = frag(la + p * BK * kA, kA, kk * 16, wm + i * 32);
-#pragma unroll
-                for (int j = 0; j < RN; ++j) fb[kk][j][p] = frag(lb + p * BK * kB, kB, kk * 16, wn + j * 32);
-            }
-        __builtin_amdgcn_sched_barrier(0);
-        if (s + 1 < stages) load(s + 1);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-            for (int i = 0; i < RM; ++i)
-#pragma unroll
-                for (int j = 0; j < RN; ++j) acc[i][j] = mfma_planes<Frag, P>(fb[kk][j], fa[kk][i], acc[i][j]);
-    }
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
         const int f = f0 + wm + i * 32 + lr;
@@ -622,7 +696,7 @@ __global__ __launch_bounds__(WM *WN * 64) void gated_tn(Tn<T> a)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int c = c0 + wn + j * 32 + 8 * q + 4 * lc;
-                const float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                const float v[4] = {acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
                 if (a.slices > 1)
                     store4(a.part + ((int64_t)slice * 2 * a.fp + f) * a.c, c, a.c, a.c % 4 == 0, v);
                 else
@@ -761,14 +835,11 @@ void launch_nt(const Tiles &t, Nt<T> &a, hipStream_t stream)
     const dim3 grid((unsigned)(t.tm * t.tn), (unsigned)t.slices);
     if constexpr (Factor<T>::kPlanes == 1) {
         if (t.bm == 256)
-            gated_nt<T, 256, 256, 2, 4, MODE><<<grid, dim3(512), 0, stream>>>(a);
+            gated_nt<T, 256, 256, 2, 2, 4, MODE><<<grid, dim3(256), 0, stream>>>(a);
         else
-            gated_nt<T, 128, 128, 2, 2, MODE><<<grid, dim3(256), 0, stream>>>(a);
+            gated_nt<T, 128, 128, 2, 2, 4, MODE><<<grid, dim3(256), 0, stream>>>(a);
     } else {
-        if (t.bm == 256)
-            gated_nt<T, 256, 128, 4, 2, MODE><<<grid, dim3(512), 0, stream>>>(a);
-        else
-            gated_nt<T, 128, 128, 2, 2, MODE><<<grid, dim3(256), 0, stream>>>(a);
+        gated_nt<T, 128, 128, 2, 2, 3, MODE><<<grid, dim3(256), 0, stream>>>(a);
     }
 }
 
@@ -856,11 +927,11 @@ void launch_tn(const Tiles &t, Tn<T> &a, hipStream_t stream)
     const dim3 grid((unsigned)(t.tm * t.tn), (unsigned)t.slices);
     if constexpr (Factor<T>::kPlanes == 1) {
         if (t.bm == 256)
-            gated_tn<T, 256, 256, 2, 4, 64><<<grid, dim3(512), 0, stream>>>(a);
+            gated_tn<T, 256, 256, 2, 2, 4><<<grid, dim3(256), 0, stream>>>(a);
         else
-            gated_tn<T, 128, 128, 2, 2, 64><<<grid, dim3(256), 0, stream>>>(a);
+            gated_tn<T, 128, 128, 2, 2, 4><<<grid, dim3(256), 0, stream>>>(a);
     } else {
-        gated_tn<T, 128, 128, 2, 2, 32><<<grid, dim3(256), 0, stream>>>(a);
+        gated_tn<T, 128, 128, 2, 2, 3><<<grid, dim3(256), 0, stream>>>(a);
     }
 }
 
