@@ -186,21 +186,6 @@ __device__ inline void wait_loads()
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
 }
 
-// The same for the N stages behind the next that are in flight, L loads each; at the
-// end of a sum there are fewer.
-template <int N, int L>
-__device__ inline void wait_stage(int behind)
-{
-    if constexpr (N == 0)
-        wait_loads<0>();
-    else {
-        if (behind >= N)
-            wait_loads<N * L>();
-        else
-            wait_stage<N - 1, L>(behind);
-    }
-}
-
 __device__ inline void barrier()
 {
     asm volatile("s_barrier" : : : "memory");
@@ -362,43 +347,66 @@ __device__ inline float sum_lanes(const float (&s)[N])
     }
 }
 
-// One step (16 of the sum's index) of a wave's blocks.
-template <int P, int RM, int RN, typename F>
-__device__ inline void products(float16v (&acc)[RN][RM], const F (&fb)[RN][P], const F (&fa)[RM][P])
+// One step (16 of the sum's index) of a wave's blocks; between(n) goes between its
+// instructions, n = 0 .. kCount RM RN - 1.
+template <int P, int RM, int RN, typename F, typename B>
+__device__ inline void products(float16v (&acc)[RN][RM], const F &f, B between)
 {
 #pragma unroll
     for (int q = 0; q < Pairs<P>::kCount; ++q)
 #pragma unroll
         for (int j = 0; j < RN; ++j)
 #pragma unroll
-            for (int i = 0; i < RM; ++i) acc[j][i] = mfma(fb[j][Pairs<P>::l[q]], fa[i][Pairs<P>::r[q]], acc[j][i]);
+            for (int i = 0; i < RM; ++i) {
+                acc[j][i] = mfma(f.b[j][Pairs<P>::l[q]], f.a[i][Pairs<P>::r[q]], acc[j][i]);
+                between((q * RN + j) * RM + i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
 }
 
 // A sum of `stages` stages of two steps each, out of a ring of NB buffers in LDS:
-// issue(s) sends off stage s's L loads, read(s, k, f) takes step k's factors out of LDS,
-// multiply(f) runs a step's matrix instructions.  A step's factors are read while the
-// one before is multiplied.  The barrier in the middle of a stage says that all waves
-// have read it whole, so that its buffer can be filled anew, and that the next one
-// is there.
-template <int NB, int L, typename F, typename I, typename R, typename M>
-__device__ inline void ring(int stages, I issue, R read, M multiply)
+// issue(s, i) sends off load i (of L) of stage s, read(s, k, i, f) takes factor i (of R) of
+// step k out of LDS.  A step's factors are read while the one before is multiplied:
+// one read behind each of the first half of its matrix instructions (M), one load
+// behind each of the second, so that neither keeps the matrix unit waiting.  The
+// barrier in the middle of a stage says that all waves have read it whole, so that
+// its buffer can be filled anew, and that the next one is there.  Stages behind the
+// last are issued and read like the others, for the sake of the count; issue() gives
+// them zeros and nothing is multiplied by them.
+template <int NB, int L, int R, int M, int P, int RM, int RN, typename F, typename I, typename G>
+__device__ inline void ring(float16v (&acc)[RN][RM], int stages, I issue, G read)
 {
+    constexpr int kHalf = M / 2, kReads = (R + kHalf - 1) / kHalf, kIssues = (L + M - kHalf - 1) / (M - kHalf);
     F even, odd;
 #pragma unroll
     for (int s = 0; s < NB; ++s)
-        if (s < stages) issue(s);
-    wait_stage<NB - 1, L>(stages - 1);
+#pragma unroll
+        for (int i = 0; i < L; ++i) issue(s, i);
+    wait_loads<(NB - 1) * L>();
     barrier();
-    read(0, 0, even);
+#pragma unroll
+    for (int i = 0; i < R; ++i) read(0, 0, i, even);
     for (int s = 0; s < stages; ++s) {
-        read(s, 1, odd);
-        multiply(even);
-        wait_stage<NB - 2, L>(stages - 2 - s);
+        products<P, RM, RN>(acc, even, [&](int n) {
+#pragma unroll
+            for (int i = 0; i < kReads; ++i)
+                if (n * kReads + i < R) read(s, 1, n * kReads + i, odd);
+        });
+        wait_loads<(NB - 2) * L>();
         barrier();
-        if (s + NB < stages) issue(s + NB);
-        if (s + 1 < stages) read(s + 1, 0, even);
-        multiply(odd);
+        products<P, RM, RN>(acc, odd, [&](int n) {
+            if (n < kHalf) {
+#pragma unroll
+                for (int i = 0; i < kReads; ++i)
+                    if (n * kReads + i < R) read(s + 1, 0, n * kReads + i, even);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kIssues; ++i)
+                    if ((n - kHalf) * kIssues + i < L) issue(s + NB, (n - kHalf) * kIssues + i);
+            }
+        });
     }
+    wait_loads<0>();
 }
 
 template <typename E, int P, int RM, int RN>
@@ -434,7 +442,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
 
     const int64_t all = (a.k + BK - 1) / BK, s0 = slice * a.cut;
     const int stages = (int)(MODE == kProduct ? (all - s0 < a.cut ? all - s0 : a.cut) : all);
-    const int k0 = (int)(s0 * BK);
+    const int k0 = (int)(s0 * BK), k1 = k0 + stages * BK < a.k ? k0 + stages * BK : a.k;
 
     // Row 16 wave + lane / 4 of the first of this wave's loads, the i-th 16 W i rows
     // on; the chunk's place in it depends on the row modulo 16 only.
@@ -462,35 +470,27 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
         db[p] = descriptor(bp + p * a.b0.plane + (int64_t)n0 * a.b0.pitch, (int64_t)(a.n - n0) * bpitch);
     }
     const uint32_t base = lds_offset(lds);
-    auto issue = [&](int s) {
-        const int k = k0 + s * BK;
+    auto issue = [&](int s, int n) {
+        const int k = k0 + s * BK, p = n / (kA + kB), i = n % (kA + kB);
         // a row's end inside the stage: zeros, not the next row
-        const bool in = k + chunk * 8 < a.k;
-        const uint32_t la = in ? alane : kOutside, lb = in ? blane : kOutside;
+        const bool in = k + chunk * 8 < k1;
         const uint32_t to = base + s % NB * kStage + wave * 1024;
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-#pragma unroll
-            for (int i = 0; i < kA; ++i)
-                load_lds(da[p], la, k * 2 + i * 16 * W * apitch, to + p * BM * kRow + i * W * 1024);
-#pragma unroll
-            for (int i = 0; i < kB; ++i)
-                load_lds(db[p], lb, k * 2 + i * bstep, to + P * BM * kRow + p * BN * kRow + i * W * 1024);
-        }
+        if (i < kA)
+            load_lds(da[p], in ? alane : kOutside, k * 2 + i * 16 * W * apitch, to + p * BM * kRow + i * W * 1024);
+        else
+            load_lds(db[p], in ? blane : kOutside, k * 2 + (i - kA) * bstep,
+                     to + P * BM * kRow + p * BN * kRow + (i - kA) * W * 1024);
     };
-    auto read = [&](int s, int kk, F &f) {
+    auto read = [&](int s, int kk, int n, F &f) {
         const char *at = lds + s % NB * kStage + (((kk * 2 + lc) ^ ((lr >> 2) & 3)) * 16) + lr * kRow;
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-#pragma unroll
-            for (int j = 0; j < RN; ++j)
-                f.b[j][p] = *(const Vec<E, 8> *)(at + P * BM * kRow + (p * BN + wn + j * 32) * kRow);
-#pragma unroll
-            for (int i = 0; i < RM; ++i) f.a[i][p] = *(const Vec<E, 8> *)(at + (p * BM + wm + i * 32) * kRow);
-        }
+        const int p = n % P, i = n / P;
+        if (i < RN)
+            f.b[i][p] = *(const Vec<E, 8> *)(at + P * BM * kRow + (p * BN + wn + i * 32) * kRow);
+        else
+            f.a[i - RN][p] = *(const Vec<E, 8> *)(at + (p * BM + wm + (i - RN) * 32) * kRow);
     };
     float16v acc[RN][RM] = {};  // rows: B's, columns: A's
-    ring<NB, P *(kA + kB), F>(stages, issue, read, [&](const F &f) { products<P, RM, RN>(acc, f.b, f.a); });
+    ring<NB, P *(kA + kB), P *(RM + RN), Pairs<P>::kCount * RM * RN, P, RM, RN, F>(acc, stages, issue, read);
 
     // A lane has column m = lr of A's rows and, of B's rows, 8 (q / 4) + 4 lc + q % 4.
     if constexpr (MODE == kProduct) {
@@ -629,6 +629,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_tn(Tn<T> a)
     const int64_t all = (a.m + BK - 1) / BK, s0 = slice * a.cut;
     const int stages = (int)(all - s0 < a.cut ? all - s0 : a.cut);
 
+    const int64_t m1 = (s0 + stages) * BK < a.m ? (s0 + stages) * BK : a.m;
     // A load takes the rows of 1024 bytes, the waves' loads follow each other; where a
     // chunk goes depends on its row modulo 4, which is the same for all of a wave's.
     const uint32_t apitch = (uint32_t)a.fp * 4, bpitch = (uint32_t)a.b_pitch * 2;
@@ -640,21 +641,17 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_tn(Tn<T> a)
     };
     const uint32_t alane = place_of(kPerA, apitch), blane = place_of(kPerB, bpitch);
     const uint32_t base = lds_offset(lds);
-    auto issue = [&](int s) {
+    auto issue = [&](int s, int n) {
         const int64_t k = (s0 + s) * BK;  // first row; behind the last one there are zeros
+        const int p = n / (kA + kB), i = n % (kA + kB);
         const uint32_t to = base + s % NB * kStage + wave * 1024;
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            // columns behind a row's end come out of the next row, into results that nobody takes
-            const Descriptor da = descriptor(a.a + p * a.a_plane + k * 2 * a.fp + f0, (a.m - k) * apitch - f0 * 2);
-            const Descriptor db = descriptor(a.b + p * a.b_plane + k * a.b_pitch + c0, (a.m - k) * bpitch - c0 * 2);
-#pragma unroll
-            for (int i = 0; i < kA; ++i)
-                load_lds(da, alane, i * W * kPerA * apitch, to + p * BK * kRowA + i * W * 1024);
-#pragma unroll
-            for (int i = 0; i < kB; ++i)
-                load_lds(db, blane, i * W * kPerB * bpitch, to + kStageA + p * BK * kRowB + i * W * 1024);
-        }
+        // columns behind a row's end come out of the next row, into results that nobody takes
+        if (i < kA)
+            load_lds(descriptor(a.a + p * a.a_plane + k * 2 * a.fp + f0, (m1 - k) * apitch - f0 * 2), alane,
+                     i * W * kPerA * apitch, to + p * BK * kRowA + i * W * 1024);
+        else
+            load_lds(descriptor(a.b + p * a.b_plane + k * a.b_pitch + c0, (m1 - k) * bpitch - c0 * 2), blane,
+                     (i - kA) * W * kPerB * bpitch, to + kStageA + p * BK * kRowB + (i - kA) * W * 1024);
     };
     // rows k .. k + 8 (by lc) of columns col .. col + 32
     const int trow = lc * 8 + ((lane & 15) >> 2), tcol = ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
@@ -671,19 +668,16 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_tn(Tn<T> a)
         }
         return r.f;
     };
-    auto read = [&](int s, int kk, F &f) {
+    auto read = [&](int s, int kk, int n, F &f) {
         const char *la = lds + s % NB * kStage, *lb = la + kStageA;
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-#pragma unroll
-            for (int j = 0; j < RN; ++j) f.b[j][p] = frag(lb + p * BK * kRowB, kRowB, kk * 16, wn + j * 32);
-#pragma unroll
-            for (int i = 0; i < RM; ++i) f.a[i][p] = frag(la + p * BK * kRowA, kRowA, kk * 16, wm + i * 32);
-        }
+        const int p = n % P, i = n / P;
+        if (i < RN)
+            f.b[i][p] = frag(lb + p * BK * kRowB, kRowB, kk * 16, wn + i * 32);
+        else
+            f.a[i - RN][p] = frag(la + p * BK * kRowA, kRowA, kk * 16, wm + (i - RN) * 32);
     };
     float16v acc[RN][RM] = {};  // [x][gradients]; rows: x's columns, columns: the gradients'
-    ring<NB, P *(kA + kB), F>(stages, issue, read, [&](const F &f) { products<P, RM, RN>(acc, f.b, f.a); });
-
+    ring<NB, P *(kA + kB), P *(RM + RN), Pairs<P>::kCount * RM * RN, P, RM, RN, F>(acc, stages, issue, read);
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
         const int f = f0 + wm + i * 32 + lr;
