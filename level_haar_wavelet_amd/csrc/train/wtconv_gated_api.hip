@@ -45,8 +45,8 @@ Plan make_plan(const wtconv_gated_desc_t &d)
     p.cp = (int)((d.c + 7) / 8 * 8);
     p.fp = (int)((d.f + 7) / 8 * 8);
     const bool one = p.planes == 1;
-    constexpr int bk = 32;  // of a stage along k
-    const int64_t kc = (d.c + bk - 1) / bk, kf = (2 * p.fp + bk - 1) / bk, km = (d.rows + bk - 1) / bk;
+    const int bk = one ? 64 : 32;  // of a stage along c and f; along the rows 32
+    const int64_t kc = (d.c + bk - 1) / bk, kf = (2 * p.fp + bk - 1) / bk, km = (d.rows + 31) / 32;
     // the large tile where there are enough of them
     auto pick = [&](int64_t m, int64_t n, int64_t stages, bool cut, int half) {
         const Tiles t = tiles_of(m, n, 256, 256 / half, stages, cut);

@@ -364,47 +364,55 @@ __device__ inline void products(float16v (&acc)[RN][RM], const F &f, B between)
             }
 }
 
-// A sum of `stages` stages of two steps each, out of a ring of NB buffers in LDS:
+// A sum of `stages` stages of KK steps each, out of a ring of NB buffers in LDS:
 // issue(s, i) sends off load i (of L) of stage s, read(s, k, i, f) takes factor i (of R) of
-// step k out of LDS.  A step's factors are read while the one before is multiplied:
-// one read behind each of the first half of its matrix instructions (M), one load
-// behind each of the second, so that neither keeps the matrix unit waiting.  The
-// barrier in the middle of a stage says that all waves have read it whole, so that
-// its buffer can be filled anew, and that the next one is there.  Stages behind the
-// last are issued and read like the others, for the sake of the count; issue() gives
+// step k out of LDS.  A step's factors are read while the one before is multiplied,
+// one read behind each of the first half of its matrix instructions (M), so that
+// they do not keep the matrix unit waiting.  The barrier before a stage's last step says
+// that all waves have read it whole, so that its buffer can be filled anew, and that
+// the next one is there.  The loads go behind the second half of the instructions of
+// that step and, where there are more, of the next stage's first.  Stages behind the last
+// are issued and read like the others, for the sake of the count; issue() gives
 // them zeros and nothing is multiplied by them.
-template <int NB, int L, int R, int M, int P, int RM, int RN, typename F, typename I, typename G>
+template <int NB, int KK, int L, int R, int M, int P, int RM, int RN, typename F, typename I, typename G>
 __device__ inline void ring(float16v (&acc)[RN][RM], int stages, I issue, G read)
 {
-    constexpr int kHalf = M / 2, kReads = (R + kHalf - 1) / kHalf, kIssues = (L + M - kHalf - 1) / (M - kHalf);
-    F even, odd;
+    constexpr int kHalf = M / 2, kSecond = M - kHalf, kReads = (R + kHalf - 1) / kHalf;
+    constexpr int kSpread = KK > 2 ? 2 : 1;  // steps that the loads are spread over
+    constexpr int kIssues = (L + kSpread * kSecond - 1) / (kSpread * kSecond);
+    static_assert(KK % 2 == 0 && NB >= 2, "steps alternate between two sets of factors");
+    F f[2];
 #pragma unroll
     for (int s = 0; s < NB; ++s)
 #pragma unroll
-        for (int i = 0; i < L; ++i) issue(s, i);
-    wait_loads<(NB - 1) * L>();
+        for (int i = 0; i < L; ++i)
+            if (s < NB - 1 || kSpread == 1 || i < kSecond * kIssues) issue(s, i);
+    wait_loads<(NB - 2) * L + (kSpread == 1 ? L : kSecond * kIssues)>();
     barrier();
 #pragma unroll
-    for (int i = 0; i < R; ++i) read(0, 0, i, even);
+    for (int i = 0; i < R; ++i) read(0, 0, i, f[0]);
     for (int s = 0; s < stages; ++s) {
-        products<P, RM, RN>(acc, even, [&](int n) {
 #pragma unroll
-            for (int i = 0; i < kReads; ++i)
-                if (n * kReads + i < R) read(s, 1, n * kReads + i, odd);
-        });
-        wait_loads<(NB - 2) * L>();
-        barrier();
-        products<P, RM, RN>(acc, odd, [&](int n) {
-            if (n < kHalf) {
-#pragma unroll
-                for (int i = 0; i < kReads; ++i)
-                    if (n * kReads + i < R) read(s + 1, 0, n * kReads + i, even);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kIssues; ++i)
-                    if ((n - kHalf) * kIssues + i < L) issue(s + NB, (n - kHalf) * kIssues + i);
+        for (int k = 0; k < KK; ++k) {
+            const bool last = k == KK - 1;
+            if (last) {
+                wait_loads<(NB - 2) * L>();
+                barrier();
             }
-        });
+            products<P, RM, RN>(acc, f[k % 2], [&](int n) {
+                if (n < kHalf) {
+#pragma unroll
+                    for (int i = 0; i < kReads; ++i)
+                        if (n * kReads + i < R)
+                            read(last ? s + 1 : s, last ? 0 : k + 1, n * kReads + i, f[(k + 1) % 2]);
+                } else if (last || (kSpread == 2 && k == 0)) {
+                    const int first = ((last ? 0 : kSecond) + n - kHalf) * kIssues;
+#pragma unroll
+                    for (int i = 0; i < kIssues; ++i)
+                        if (first + i < L) issue(last ? s + NB : s + NB - 1, first + i);
+                }
+            });
+        }
     }
     wait_loads<0>();
 }
@@ -414,18 +422,19 @@ struct Factors {
     Vec<E, 8> a[RM][P], b[RN][P];
 };
 
-// A tile of BM rows of A and BN rows of B; WM x WN waves, NB buffers.  A stage is 64
-// bytes of each row, whose 16-byte chunks are permuted so that the rows that a read
-// phase covers fall into different banks.
-template <typename T, int BM, int BN, int WM, int WN, int NB, int MODE>
+// A tile of BM rows of A and BN rows of B; WM x WN waves, NB buffers.  A stage is BK
+// elements (64 or 128 bytes) of each row, whose 16-byte chunks are permuted so that the
+// rows that a read phase covers fall into different banks.
+template <typename T, int BM, int BN, int WM, int WN, int BK, int NB, int MODE>
 __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
 {
     typedef typename Factor<T>::type E;
     constexpr int P = Factor<T>::kPlanes, W = WM * WN;
-    constexpr int kRow = 64, BK = 32, kStage = (BM + BN) * P * kRow;
-    // a load takes 16 rows; the waves' loads follow each other
-    constexpr int kA = BM / 16 / W, kB = BN / 16 / W;
-    static_assert(kA * 16 * W == BM && kB * 16 * W == BN, "rows are shared out evenly");
+    constexpr int kRow = BK * 2, kStage = (BM + BN) * P * kRow, kChunks = kRow / 16;
+    // a load takes kPer rows; the waves' loads follow each other
+    constexpr int kPer = 1024 / kRow, kA = BM / kPer / W, kB = BN / kPer / W;
+    static_assert(kA * kPer * W == BM && kB * kPer * W == BN, "rows are shared out evenly");
+    static_assert(kPer * W % 32 == 0 && (MODE == kProduct || kPer * W == 64 || kPer * W == 32), "see blane");
     constexpr int RM = BM / WM / 32, RN = BN / WN / 32;
     static_assert(MODE == kProduct || RN % 2 == 0, "a wave has as many blocks of g as of u");
     typedef Factors<E, P, RM, RN> F;
@@ -444,30 +453,27 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
     const int stages = (int)(MODE == kProduct ? (all - s0 < a.cut ? all - s0 : a.cut) : all);
     const int k0 = (int)(s0 * BK), k1 = k0 + stages * BK < a.k ? k0 + stages * BK : a.k;
 
-    // Row 16 wave + lane / 4 of the first of this wave's loads, the i-th 16 W i rows
-    // on; the chunk's place in it depends on the row modulo 16 only.
-    const int row = lane >> 2, chunk = (lane & 3) ^ ((row >> 2) & 3);
+    // Row `row` of the first of this wave's loads, the i-th kPer W i rows on; a chunk's
+    // place depends on the row modulo 16 only.
+    auto swizzle = [](int r) { return kChunks == 8 ? (r >> 1) & 7 : (r >> 2) & 3; };
+    const int row = wave * kPer + lane / kChunks, chunk = (lane % kChunks) ^ swizzle(row);
     const uint32_t apitch = (uint32_t)a.a.pitch * 2, bpitch = (uint32_t)a.b0.pitch * 2;
-    const uint32_t alane = (row + 16 * wave) * apitch + chunk * 16;
+    const uint32_t alane = row * apitch + chunk * 16;
     // B's rows in memory; g and u: tile rows 64 i .. 64 i + 31 are the gate's rows from
     // 32 i on, the next 32 the up projection's
-    uint32_t blane, bstep;
-    const E *bp = a.b0.p;
-    if (MODE == kProduct) {
-        blane = (row + 16 * wave) * bpitch + chunk * 16;
-        bstep = 16 * W * bpitch;
-    } else {
-        static_assert(W % 4 == 0, "a wave's loads are all of one matrix");
-        const int first = 16 * wave;
-        if ((first / 32) % 2) bp = a.b1.p;
-        blane = (first / 64 * 32 + first % 32 + row) * bpitch + chunk * 16;
-        bstep = 8 * W * bpitch;
+    uint32_t blane = row * bpitch + chunk * 16;
+    bool up = false;  // 64 rows a step: this wave's are all of one matrix; 32: they take turns
+    if (MODE != kProduct && kPer * W == 64) {
+        up = wave * kPer / 32;
+        blane -= up ? 32 * bpitch : 0;
     }
-    Descriptor da[P], db[P];
+    Descriptor da[P], db[P], dup[P];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         da[p] = descriptor(a.a.p + p * a.a.plane + m0 * a.a.pitch, (a.m - m0) * apitch);
-        db[p] = descriptor(bp + p * a.b0.plane + (int64_t)n0 * a.b0.pitch, (int64_t)(a.n - n0) * bpitch);
+        const int64_t first = p * a.b0.plane + (int64_t)n0 * a.b0.pitch, bytes = (int64_t)(a.n - n0) * bpitch;
+        db[p] = descriptor((up ? a.b1.p : a.b0.p) + first, bytes);
+        dup[p] = MODE != kProduct && kPer * W == 32 ? descriptor(a.b1.p + first, bytes) : db[p];
     }
     const uint32_t base = lds_offset(lds);
     auto issue = [&](int s, int n) {
@@ -476,13 +482,16 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
         const bool in = k + chunk * 8 < k1;
         const uint32_t to = base + s % NB * kStage + wave * 1024;
         if (i < kA)
-            load_lds(da[p], in ? alane : kOutside, k * 2 + i * 16 * W * apitch, to + p * BM * kRow + i * W * 1024);
-        else
-            load_lds(db[p], in ? blane : kOutside, k * 2 + (i - kA) * bstep,
-                     to + P * BM * kRow + p * BN * kRow + (i - kA) * W * 1024);
+            load_lds(da[p], in ? alane : kOutside, k * 2 + i * kPer * W * apitch, to + p * BM * kRow + i * W * 1024);
+        else {
+            // rows of g's and u's weights: half as many as of the tile
+            const int j = i - kA, rows = MODE == kProduct ? j * kPer * W : kPer * W == 64 ? j * 32 : j / 2 * 32;
+            load_lds(j % 2 ? dup[p] : db[p], in ? blane : kOutside, k * 2 + rows * bpitch,
+                     to + P * BM * kRow + p * BN * kRow + j * W * 1024);
+        }
     };
     auto read = [&](int s, int kk, int n, F &f) {
-        const char *at = lds + s % NB * kStage + (((kk * 2 + lc) ^ ((lr >> 2) & 3)) * 16) + lr * kRow;
+        const char *at = lds + s % NB * kStage + (((kk * 2 + lc) ^ swizzle(lr)) * 16) + lr * kRow;
         const int p = n % P, i = n / P;
         if (i < RN)
             f.b[i][p] = *(const Vec<E, 8> *)(at + P * BM * kRow + (p * BN + wn + i * 32) * kRow);
@@ -490,7 +499,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
             f.a[i - RN][p] = *(const Vec<E, 8> *)(at + (p * BM + wm + (i - RN) * 32) * kRow);
     };
     float16v acc[RN][RM] = {};  // rows: B's, columns: A's
-    ring<NB, P *(kA + kB), P *(RM + RN), Pairs<P>::kCount * RM * RN, P, RM, RN, F>(acc, stages, issue, read);
+    ring<NB, BK / 16, P *(kA + kB), P *(RM + RN), Pairs<P>::kCount * RM * RN, P, RM, RN, F>(acc, stages, issue, read);
 
     // A lane has column m = lr of A's rows and, of B's rows, 8 (q / 4) + 4 lc + q % 4.
     if constexpr (MODE == kProduct) {
@@ -677,7 +686,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_tn(Tn<T> a)
             f.a[i - RN][p] = frag(la + p * BK * kRowA, kRowA, kk * 16, wm + (i - RN) * 32);
     };
     float16v acc[RN][RM] = {};  // [x][gradients]; rows: x's columns, columns: the gradients'
-    ring<NB, P *(kA + kB), P *(RM + RN), Pairs<P>::kCount * RM * RN, P, RM, RN, F>(acc, stages, issue, read);
+    ring<NB, BK / 16, P *(kA + kB), P *(RM + RN), Pairs<P>::kCount * RM * RN, P, RM, RN, F>(acc, stages, issue, read);
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
         const int f = f0 + wm + i * 32 + lr;
@@ -829,11 +838,11 @@ void launch_nt(const Tiles &t, Nt<T> &a, hipStream_t stream)
     const dim3 grid((unsigned)(t.tm * t.tn), (unsigned)t.slices);
     if constexpr (Factor<T>::kPlanes == 1) {
         if (t.bm == 256)
-            gated_nt<T, 256, 256, 2, 2, 4, MODE><<<grid, dim3(256), 0, stream>>>(a);
+            gated_nt<T, 256, 256, 2, 2, 64, 2, MODE><<<grid, dim3(256), 0, stream>>>(a);
         else
-            gated_nt<T, 128, 128, 2, 2, 4, MODE><<<grid, dim3(256), 0, stream>>>(a);
+            gated_nt<T, 128, 128, 2, 2, 64, 2, MODE><<<grid, dim3(256), 0, stream>>>(a);
     } else {
-        gated_nt<T, 128, 128, 2, 2, 3, MODE><<<grid, dim3(256), 0, stream>>>(a);
+        gated_nt<T, 128, 128, 2, 2, 32, 3, MODE><<<grid, dim3(256), 0, stream>>>(a);
     }
 }
 
