@@ -377,17 +377,14 @@ __device__ inline void products(float16v (&acc)[RN][RM], const F &f, B between)
 template <int NB, int KK, int L, int R, int M, int P, int RM, int RN, typename F, typename I, typename G>
 __device__ inline void ring(float16v (&acc)[RN][RM], int stages, I issue, G read)
 {
-    constexpr int kHalf = M / 2, kSecond = M - kHalf, kReads = (R + kHalf - 1) / kHalf;
-    constexpr int kSpread = KK > 2 ? 2 : 1;  // steps that the loads are spread over
-    constexpr int kIssues = (L + kSpread * kSecond - 1) / (kSpread * kSecond);
+    constexpr int kHalf = M / 2, kReads = (R + kHalf - 1) / kHalf, kIssues = (L + M - 1) / M;
     static_assert(KK % 2 == 0 && NB >= 2, "steps alternate between two sets of factors");
     F f[2];
 #pragma unroll
     for (int s = 0; s < NB; ++s)
 #pragma unroll
-        for (int i = 0; i < L; ++i)
-            if (s < NB - 1 || kSpread == 1 || i < kSecond * kIssues) issue(s, i);
-    wait_loads<(NB - 2) * L + (kSpread == 1 ? L : kSecond * kIssues)>();
+        for (int i = 0; i < L; ++i) issue(s, i);
+    wait_loads<(NB - 1) * L>();
     barrier();
 #pragma unroll
     for (int i = 0; i < R; ++i) read(0, 0, i, f[0]);
@@ -400,17 +397,13 @@ __device__ inline void ring(float16v (&acc)[RN][RM], int stages, I issue, G read
                 barrier();
             }
             products<P, RM, RN>(acc, f[k % 2], [&](int n) {
-                if (n < kHalf) {
 #pragma unroll
-                    for (int i = 0; i < kReads; ++i)
-                        if (n * kReads + i < R)
-                            read(last ? s + 1 : s, last ? 0 : k + 1, n * kReads + i, f[(k + 1) % 2]);
-                } else if (last || (kSpread == 2 && k == 0)) {
-                    const int first = ((last ? 0 : kSecond) + n - kHalf) * kIssues;
+                for (int i = 0; i < kReads; ++i)
+                    if (n * kReads + i < R) read(last ? s + 1 : s, last ? 0 : k + 1, n * kReads + i, f[(k + 1) % 2]);
+                if (last)
 #pragma unroll
                     for (int i = 0; i < kIssues; ++i)
-                        if (first + i < L) issue(last ? s + NB : s + NB - 1, first + i);
-                }
+                        if (n * kIssues + i < L) issue(s + NB, n * kIssues + i);
             });
         }
     }
