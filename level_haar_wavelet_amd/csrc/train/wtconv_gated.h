@@ -40,7 +40,8 @@ struct Plan {
     bool pack;           // x and the weights are laid out anew (fp32, or rows of no whole accesses)
     int cp, fp;          // row lengths in the workspace: c and f up to a multiple of 8
     Tiles dual, dx, dw;  // g and u; dx; the weights' gradients
-    int64_t bias_rows;   // rows of the biases' partial sums
+    int64_t row_tiles;   // of the kernel for short rows (0: rows are too long for it)
+    int parts, part_cut; // its workgroups for a tile of rows, and their chunks
     // bytes
     size_t x, w, grads, wt, bias, part;
 };

@@ -56,14 +56,23 @@ Plan make_plan(const wtconv_gated_desc_t &d)
     p.dual = pick(d.rows, d.f, kc, false, 2);
     p.dx = pick(d.rows, d.c, kf, true, 1);
     p.dw = pick(2 * p.fp, d.c, km, true, 1);
-    p.bias_rows = p.dual.tm * 2;  // of the waves along the rows
+    if (p.cp <= (one ? 256 : 192) && d.c % (one ? 8 : 4) == 0 && d.f % 4 == 0) {
+        const int64_t rows = one ? 256 : 128, chunks = (d.f + 31) / 32;
+        p.row_tiles = (d.rows + rows - 1) / rows;
+        // workgroups for several rounds, of at least two chunks
+        int64_t parts = (8 * kUnits + p.row_tiles - 1) / p.row_tiles;
+        parts = parts > (chunks + 1) / 2 ? (chunks + 1) / 2 : parts;
+        p.part_cut = (int)((chunks + parts - 1) / parts);
+        p.parts = (int)((chunks + p.part_cut - 1) / p.part_cut);
+    }
+    const int64_t bias_rows = p.dual.tm * 2 > p.row_tiles * 4 ? p.dual.tm * 2 : p.row_tiles * 4;
     if (p.pack) {
         p.x = align256((size_t)(d.rows * p.cp) * p.planes * 2);
         p.w = align256((size_t)(d.f * 2 * p.cp) * p.planes * 2);
     }
     p.grads = align256((size_t)(d.rows * 2 * p.fp) * p.planes * 2);
     p.wt = align256((size_t)(d.c * 2 * p.fp) * p.planes * 2);
-    p.bias = align256((size_t)(p.bias_rows * 2 * p.fp) * 4);
+    p.bias = align256((size_t)(bias_rows * 2 * p.fp) * 4);
     const size_t px = p.dx.slices > 1 ? (size_t)(p.dx.slices * d.rows * d.c) * 4 : 0;
     const size_t pw = p.dw.slices > 1 ? (size_t)((int64_t)p.dw.slices * 2 * p.fp * d.c) * 4 : 0;
     p.part = align256(px > pw ? px : pw);

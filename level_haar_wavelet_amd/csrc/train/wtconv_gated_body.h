@@ -587,6 +587,12 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
     }
 }
 
+}  // namespace wtc_gated
+
+#include "wtconv_gated_short.h"
+
+namespace wtc_gated {
+
 // ---- The weights' gradients -------------------------------------------------------
 
 template <typename T>
@@ -845,6 +851,9 @@ bool wide4(const void *p, int64_t n)
     return n % 4 == 0 && aligned_to(p, 4 * sizeof(T));
 }
 
+template <typename T>
+bool wide4(const void *p, int64_t n);
+
 // x, the weights as the products read them.
 template <typename T>
 struct Operands {
@@ -852,9 +861,10 @@ struct Operands {
     Rows<E> x, gate, up;
 };
 
+// ... laid out anew where the plan says so, x only where it is asked for.
 template <typename T>
 Operands<T> operands(const wtconv_gated_desc_t &d, const Plan &pl, const void *x, const void *w_gate, const void *w_up,
-                     char *&ws, hipStream_t stream)
+                     bool pack_x, char *&ws, hipStream_t stream)
 {
     typedef typename Factor<T>::type E;
     if (!pl.pack)
@@ -862,13 +872,51 @@ Operands<T> operands(const wtconv_gated_desc_t &d, const Plan &pl, const void *x
     E *xp = (E *)ws, *wp = (E *)(ws + pl.x);
     ws += pl.x + pl.w;
     const int64_t plane = d.f * 2 * pl.cp, half = d.f * pl.cp;
-    gated_pack<T><<<dim3(blocks_of(d.rows * pl.cp / 8, 8192)), dim3(256), 0, stream>>>((const T *)x, d.rows, (int)d.c, pl.cp,
-                                                                                  xp, d.rows * pl.cp);
+    if (pack_x)
+        gated_pack<T><<<dim3(blocks_of(d.rows * pl.cp / 8, 8192)), dim3(256), 0, stream>>>((const T *)x, d.rows, (int)d.c,
+                                                                                      pl.cp, xp, d.rows * pl.cp);
     gated_pack<T><<<dim3(blocks_of(half / 8, 8192)), dim3(256), 0, stream>>>((const T *)w_gate, d.f, (int)d.c, pl.cp, wp,
                                                                             plane);
     gated_pack<T><<<dim3(blocks_of(half / 8, 8192)), dim3(256), 0, stream>>>((const T *)w_up, d.f, (int)d.c, pl.cp,
                                                                             wp + half, plane);
     return {{xp, d.rows * pl.cp, pl.cp}, {wp, plane, pl.cp}, {wp + half, plane, pl.cp}};
+}
+
+template <typename T, int MODE>
+void launch_short(const wtconv_gated_desc_t &d, const Plan &pl, const Operands<T> &o, Short<T> &a, hipStream_t stream)
+{
+    constexpr int MB = Factor<T>::kPlanes == 1 ? 2 : 1;
+    a.gate = o.gate;
+    a.up = o.up;
+    a.m = d.rows;
+    a.n = (int)d.f;
+    a.c = (int)d.c;
+    a.act = d.act;
+    a.tiles = pl.row_tiles;
+    a.parts = pl.parts;
+    a.cut = pl.part_cut;
+    const dim3 grid((unsigned)(a.tiles * a.parts));
+    auto run = [&](auto ks) { gated_short<T, ks, MB, MODE><<<grid, dim3(256), 0, stream>>>(a); };
+    const int steps = (pl.cp + 15) / 16;
+    if (steps <= 2)
+        run(std::integral_constant<int, 2>{});
+    else if (steps <= 4)
+        run(std::integral_constant<int, 4>{});
+    else if (steps <= 6)
+        run(std::integral_constant<int, 6>{});
+    else if (steps <= 8)
+        run(std::integral_constant<int, 8>{});
+    else if (steps <= 12)
+        run(std::integral_constant<int, 12>{});
+    else if constexpr (Factor<T>::kPlanes == 1)
+        run(std::integral_constant<int, 16>{});
+}
+
+// Whether a call's addresses allow the kernel for short rows that its plan has.
+template <typename T>
+bool short_rows(const wtconv_gated_desc_t &d, const Plan &pl, const void *x, const void *h)
+{
+    return pl.row_tiles && wide4<T>(h, d.f) && aligned16(x);
 }
 
 template <typename T, int G>
@@ -896,7 +944,17 @@ hipError_t forward(const wtconv_gated_desc_t &d, const Forward &a, void *workspa
     }
     const Plan pl = make_plan(d);
     char *ws = (char *)workspace;
-    const Operands<T> o = operands<T>(d, pl, a.x, a.w_gate, a.w_up, ws, stream);
+    const bool brief = short_rows<T>(d, pl, a.x, a.h);
+    const Operands<T> o = operands<T>(d, pl, a.x, a.w_gate, a.w_up, !brief, ws, stream);
+    if (brief) {
+        Short<T> p = {};
+        p.x = (const T *)a.x;
+        p.bias0 = a.b_gate;
+        p.bias1 = a.b_up;
+        p.out = (T *)a.h;
+        launch_short<T, kForward>(d, pl, o, p, stream);
+        return hipGetLastError();
+    }
     Nt<T> p = {};
     p.a = o.x;
     p.b0 = o.gate;
@@ -937,30 +995,46 @@ hipError_t backward(const wtconv_gated_desc_t &d, const Backward &a, void *works
     typedef typename Factor<T>::type E;
     const Plan pl = make_plan(d);
     char *ws = (char *)workspace;
-    const Operands<T> o = operands<T>(d, pl, a.x, a.w_gate, a.w_up, ws, stream);
+    const bool brief = short_rows<T>(d, pl, a.x, a.dh);
+    const Operands<T> o = operands<T>(d, pl, a.x, a.w_gate, a.w_up, !brief || a.dw_gate, ws, stream);
     E *grads = (E *)ws, *wt = (E *)(ws + pl.grads);
     float *bias = (float *)(ws + pl.grads + pl.wt), *part = (float *)(ws + pl.grads + pl.wt + pl.bias);
     const int64_t gplane = d.rows * 2 * pl.fp;
-
-    Nt<T> p = {};
-    p.a = o.x;
-    p.b0 = o.gate;
-    p.b1 = o.up;
-    p.m = d.rows;
-    p.n = (int)d.f;
-    p.k = pl.pack ? pl.cp : (int)d.c;
-    p.act = d.act;
-    p.bias0 = a.b_gate;
-    p.bias1 = a.b_up;
-    p.dh = (const T *)a.dh;
-    p.wide = wide4<T>(a.dh, d.f);
-    p.grads = grads;
-    p.grads_plane = gplane;
-    p.fp = pl.fp;
-    p.bias_part = a.db_gate || a.db_up ? bias : nullptr;
-    launch_nt<T, kBackward>(pl.dual, p, stream);
+    int64_t bias_rows;
+    if (brief) {
+        Short<T> p = {};
+        p.x = (const T *)a.x;
+        p.bias0 = a.b_gate;
+        p.bias1 = a.b_up;
+        p.dh = (const T *)a.dh;
+        p.grads = grads;
+        p.grads_plane = gplane;
+        p.fp = pl.fp;
+        p.bias_part = a.db_gate ? bias : nullptr;
+        bias_rows = pl.row_tiles * 4;
+        launch_short<T, kBackward>(d, pl, o, p, stream);
+    } else {
+        Nt<T> p = {};
+        p.a = o.x;
+        p.b0 = o.gate;
+        p.b1 = o.up;
+        p.m = d.rows;
+        p.n = (int)d.f;
+        p.k = pl.pack ? pl.cp : (int)d.c;
+        p.act = d.act;
+        p.bias0 = a.b_gate;
+        p.bias1 = a.b_up;
+        p.dh = (const T *)a.dh;
+        p.wide = wide4<T>(a.dh, d.f);
+        p.grads = grads;
+        p.grads_plane = gplane;
+        p.fp = pl.fp;
+        p.bias_part = a.db_gate ? bias : nullptr;
+        bias_rows = pl.dual.tm * 2;  // of the waves along the rows
+        launch_nt<T, kBackward>(pl.dual, p, stream);
+    }
     if (a.db_gate)
-        gated_bias<T><<<dim3((unsigned)((d.f + 63) / 64), 2), dim3(1024), 0, stream>>>(bias, pl.bias_rows, (int)d.f, pl.fp,
+        gated_bias<T><<<dim3((unsigned)((d.f + 63) / 64), 2), dim3(1024), 0, stream>>>(bias, bias_rows, (int)d.f, pl.fp,
                                                                                     a.db_gate, a.db_up);
     if (a.dx) {
         const int64_t plane = d.c * 2 * pl.fp;
