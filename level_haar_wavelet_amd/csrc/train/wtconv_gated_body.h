@@ -108,37 +108,54 @@ __device__ inline void split(float v, typename Factor<T>::type (&o)[P])
     }
 }
 
-__device__ inline float act(int kind, float z)
+template <int KIND>
+__device__ inline float act(float z)
 {
-    if (kind == WTCONV_ACT_SILU) return z * sigmoid(z);
-    if (kind == WTCONV_ACT_GELU) {
+    if (KIND == WTCONV_ACT_SILU) return z * sigmoid(z);
+    if (KIND == WTCONV_ACT_GELU) {
         float e;
         return z * normal_cdf(z, e);
     }
-    if (kind == WTCONV_ACT_RELU) return z < 0.f ? 0.f : z;  // NaN stays
+    if (KIND == WTCONV_ACT_RELU) return z < 0.f ? 0.f : z;  // NaN stays
     return z;
 }
 
 // act(z) and its slope.
-__device__ inline float act_slope(int kind, float z, float &slope)
+template <int KIND>
+__device__ inline float act_slope(float z, float &slope)
 {
-    if (kind == WTCONV_ACT_SILU) {
+    if (KIND == WTCONV_ACT_SILU) {
         const float s = sigmoid(z);
         slope = s * fmaf(z, 1.f - s, 1.f);
         return z * s;
     }
-    if (kind == WTCONV_ACT_GELU) {
+    if (KIND == WTCONV_ACT_GELU) {
         float e;
         const float p = normal_cdf(z, e);
         slope = fmaf(z * 0.39894228f, e, p);
         return z * p;
     }
-    if (kind == WTCONV_ACT_RELU) {
+    if (KIND == WTCONV_ACT_RELU) {
         slope = z > 0.f ? 1.f : 0.f;
         return z < 0.f ? 0.f : z;
     }
     slope = 1.f;
     return z;
+}
+
+// f(kind) once for all of a wave's values: with a branch at each, one exponential
+// waits for the other.
+template <typename F>
+__device__ inline void with_act(int kind, F f)
+{
+    if (kind == WTCONV_ACT_SILU)
+        f(std::integral_constant<int, WTCONV_ACT_SILU>{});
+    else if (kind == WTCONV_ACT_GELU)
+        f(std::integral_constant<int, WTCONV_ACT_GELU>{});
+    else if (kind == WTCONV_ACT_RELU)
+        f(std::integral_constant<int, WTCONV_ACT_RELU>{});
+    else
+        f(std::integral_constant<int, WTCONV_ACT_NONE>{});
 }
 
 // ---- Memory to LDS -------------------------------------------------------------
@@ -350,7 +367,7 @@ __device__ inline float sum_lanes(const float (&s)[N])
 // One step (16 of the sum's index) of a wave's blocks; between(n) goes between its
 // instructions, n = 0 .. kCount RM RN - 1.
 template <int P, int RM, int RN, typename F, typename B>
-__device__ inline void products(float16v (&acc)[RN][RM], const F &f, B between)
+__device__ inline void products(float16v (&acc)[RN][RM], const F (&fb)[RN][P], const F (&fa)[RM][P], B between)
 {
 #pragma unroll
     for (int q = 0; q < Pairs<P>::kCount; ++q)
@@ -358,7 +375,7 @@ __device__ inline void products(float16v (&acc)[RN][RM], const F &f, B between)
         for (int j = 0; j < RN; ++j)
 #pragma unroll
             for (int i = 0; i < RM; ++i) {
-                acc[j][i] = mfma(f.b[j][Pairs<P>::l[q]], f.a[i][Pairs<P>::r[q]], acc[j][i]);
+                acc[j][i] = mfma(fb[j][Pairs<P>::l[q]], fa[i][Pairs<P>::r[q]], acc[j][i]);
                 between((q * RN + j) * RM + i);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -396,7 +413,7 @@ __device__ inline void ring(float16v (&acc)[RN][RM], int stages, I issue, G read
                 wait_loads<(NB - 2) * L>();
                 barrier();
             }
-            products<P, RM, RN>(acc, f[k % 2], [&](int n) {
+            products<P, RM, RN>(acc, f[k % 2].b, f[k % 2].a, [&](int n) {
 #pragma unroll
                 for (int i = 0; i < kReads; ++i)
                     if (n * kReads + i < R) read(last ? s + 1 : s, last ? 0 : k + 1, n * kReads + i, f[(k + 1) % 2]);
@@ -514,7 +531,8 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
                 }
         }
         return;
-    } else {
+    } else
+        with_act(a.act, [&](auto kind) {
 #pragma unroll
         for (int j = 0; j < RN; j += 2) {
             const int f0 = n0 + wn / 2 + j * 16 + 4 * lc;
@@ -541,7 +559,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
                     }
                     if constexpr (MODE == kForward) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) g[e] = act(a.act, g[e]) * u[e];
+                        for (int e = 0; e < 4; ++e) g[e] = act<kind>(g[e]) * u[e];
                         store4(a.out + m * a.n, f, a.n, a.wide, g);
                     } else {
                         load4(a.dh + m * a.n, f, a.n, a.wide, d);
@@ -550,7 +568,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             float slope;
-                            const float y = act_slope(a.act, g[e], slope);
+                            const float y = act_slope<kind>(g[e], slope);
                             const bool in = f + e < a.n;
                             const float dg = in ? d[e] * u[e] * slope : 0.f, du = in ? d[e] * y : 0.f;
                             sg[4 * q + e] += dg;
@@ -584,7 +602,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
                 }
             }
         }
-    }
+        });
 }
 
 }  // namespace wtc_gated
@@ -810,11 +828,13 @@ __global__ __launch_bounds__(256) void gated_few(const T *__restrict__ x, const 
         const int row = i * 16 + r, at = f0 + kq * 4;
         if (row >= m) continue;
         float v[4];
+        with_act(kind, [&](auto k) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const bool in = at + e < f;
-            v[e] = act(kind, g[e] + (b0 && in ? b0[at + e] : 0.f)) * (u[e] + (b1 && in ? b1[at + e] : 0.f));
-        }
+            for (int e = 0; e < 4; ++e) {
+                const bool in = at + e < f;
+                v[e] = act<k>(g[e] + (b0 && in ? b0[at + e] : 0.f)) * (u[e] + (b1 && in ? b1[at + e] : 0.f));
+            }
+        });
         store4(h + (int64_t)row * f, at, f, wide, v);
     }
 }

@@ -176,76 +176,74 @@ __global__ __launch_bounds__(256, 2) void gated_short(Short<T> a)
                     d[i][q] = get4<T>(io, f0 + 8 * q < a.n ? (rows[i] * a.n + f0 + 8 * q) * S : kOutside);
         if (chunk + 1 < c1) issue(chunk + 1, buffer ^ 1);
         const char *w = lds + buffer * kBuffer + lr * kRow;
+        // the next step's factors are read while one is multiplied
+        constexpr int kReads = (4 * P + Pairs<P>::kCount * 2 * MB - 1) / (Pairs<P>::kCount * 2 * MB);
+        Vec<E, 8> fw[2][2][P];
+        auto read = [&](int k, int n) {
+            const int p = n / 2, j = n % 2;
+            fw[k & 1][j][p] = *(const Vec<E, 8> *)(w + (p * 2 + j) * kMatrix + ((k * 2 + lc) ^ swizzle(lr)) * 16);
+        };
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-            Vec<E, 8> fw[2][P];
+        for (int n = 0; n < 2 * P; ++n) read(0, n);
 #pragma unroll
-            for (int p = 0; p < P; ++p)
+        for (int k = 0; k < KS; ++k)
+            products<P, MB, 2>(acc, fw[k & 1], xf[k], [&](int n) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    fw[j][p] = *(const Vec<E, 8> *)(w + (p * 2 + j) * kMatrix + ((k * 2 + lc) ^ swizzle(lr)) * 16);
+                for (int i = 0; i < kReads; ++i)
+                    if (k + 1 < KS && n * kReads + i < 2 * P) read(k + 1, n * kReads + i);
+            });
+        with_act(a.act, [&](auto kind) {
 #pragma unroll
-            for (int q = 0; q < Pairs<P>::kCount; ++q)
+            for (int q = 0; q < 4; ++q) {
+                const int f = f0 + 8 * q;
+                float sums[8] = {};  // dg, du
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int i = 0; i < MB; ++i) {
+                    if constexpr (MODE == kForward) {
+                        float v[4];
 #pragma unroll
-                    for (int i = 0; i < MB; ++i)
-                        acc[j][i] = mfma(fw[j][Pairs<P>::l[q]], xf[k][i][Pairs<P>::r[q]], acc[j][i]);
-        }
-        if constexpr (MODE == kForward) {
+                        for (int e = 0; e < 4; ++e) v[e] = act<kind>(acc[0][i][4 * q + e]) * acc[1][i][4 * q + e];
+                        put4<T>(v, io, f < a.n ? (rows[i] * a.n + f) * S : kOutside);
+                    } else {
+                        Vec<E, 4> og[P], ou[P];
 #pragma unroll
-            for (int i = 0; i < MB; ++i)
+                        for (int e = 0; e < 4; ++e) {
+                            float slope;
+                            const float y = act_slope<kind>(acc[0][i][4 * q + e], slope), dv = (float)d[i][q][e];
+                            const float dg = dv * acc[1][i][4 * q + e] * slope, du = dv * y;
+                            // rows behind the last: dh is zero there
+                            sums[e] += dg;
+                            sums[4 + e] += du;
+                            E eg[P], eu[P];
+                            split<T, P>(dg, eg);
+                            split<T, P>(du, eu);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = act(a.act, acc[0][i][4 * q + e]) * acc[1][i][4 * q + e];
-                    put4<T>(v, io, f0 + 8 * q < a.n ? (rows[i] * a.n + f0 + 8 * q) * S : kOutside);
-                }
-        } else {
-            float sg[16] = {}, su[16] = {};
-#pragma unroll
-            for (int i = 0; i < MB; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    Vec<E, 4> og[P], ou[P];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float slope;
-                        const float y = act_slope(a.act, acc[0][i][4 * q + e], slope), dv = (float)d[i][q][e];
-                        const float dg = dv * acc[1][i][4 * q + e] * slope, du = dv * y;
-                        // rows behind the last: dh is zero there
-                        sg[4 * q + e] += dg;
-                        su[4 * q + e] += du;
-                        E eg[P], eu[P];
-                        split<T, P>(dg, eg);
-                        split<T, P>(du, eu);
+                            for (int p = 0; p < P; ++p) {
+                                og[p][e] = eg[p];
+                                ou[p][e] = eu[p];
+                            }
+                        }
+                        // columns behind f are zeros, as dh is there
+                        const uint32_t at = f < a.fp ? (rows[i] * 2 * a.fp + f) * 2 : kOutside;
 #pragma unroll
                         for (int p = 0; p < P; ++p) {
-                            og[p][e] = eg[p];
-                            ou[p][e] = eu[p];
+                            const __amdgpu_buffer_rsrc_t to =
+                                resource(a.grads + p * a.grads_plane + m0 * 2 * a.fp, (a.m - m0) * 4 * a.fp);
+                            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uint2v, og[p]), to, at, 0, 0);
+                            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uint2v, ou[p]), to, at, a.fp * 2, 0);
                         }
                     }
-                    // columns behind f are zeros, as dh is there
-                    const uint32_t at = f0 + 8 * q < a.fp ? (rows[i] * 2 * a.fp + f0 + 8 * q) * 2 : kOutside;
-#pragma unroll
-                    for (int p = 0; p < P; ++p) {
-                        const __amdgpu_buffer_rsrc_t to =
-                            resource(a.grads + p * a.grads_plane + m0 * 2 * a.fp, (a.m - m0) * 4 * a.fp);
-                        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uint2v, og[p]), to, at, 0, 0);
-                        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uint2v, ou[p]), to, at, a.fp * 2, 0);
-                    }
                 }
-            if (a.bias_part) {
-                const float g = sum_lanes(sg), u = sum_lanes(su);
-                const int q = lr >> 1, f = f0 + 8 * (q >> 2) + (q & 3);
-                if (!(lane & 1) && f < a.n) {
-                    float *to = a.bias_part + (ti * 4 + wave) * 2 * a.fp;
-                    to[f] = g;
-                    to[a.fp + f] = u;
+                if (MODE == kBackward && a.bias_part) {
+                    float v = sum_lanes(sums);
+                    v += __shfl_xor(v, 16);
+                    const int e = (lr & 15) >> 1;
+                    if (!(lr & 17) && f + (e & 3) < a.n)
+                        a.bias_part[(ti * 4 + wave) * 2 * a.fp + (e >> 2) * a.fp + f + (e & 3)] = v;
                 }
+                __builtin_amdgcn_sched_barrier(0);  // fewer values live at once
             }
-        }
+        });
     }
 }
 
