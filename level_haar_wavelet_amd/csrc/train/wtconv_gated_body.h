@@ -190,6 +190,15 @@ __device__ inline void load_lds(const Descriptor &d, uint32_t lane, uint32_t wav
                  : "memory", "m0");
 }
 
+// The same, 4 bytes a lane.
+__device__ inline void load_lds4(const Descriptor &d, uint32_t lane, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+                 :
+                 : "v"(lane), "s"(d), "s"(to)
+                 : "memory", "m0");
+}
+
 __device__ inline uint32_t lds_offset(const void *p)
 {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;

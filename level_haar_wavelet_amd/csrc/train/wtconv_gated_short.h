@@ -71,6 +71,9 @@ __global__ __launch_bounds__(256, 2) void gated_short(Short<T> a)
     constexpr int kLoads = P * KS / 2;                                             // of a wave for a chunk
     constexpr int kStores = MODE == kForward ? 4 * MB : 8 * MB * P;
     __shared__ __attribute__((aligned(128))) char lds[2 * kBuffer];
+    // the biases come the same way: a load into registers would be waited for, with
+    // all that was sent off after it, before a chunk's first instruction
+    __shared__ __attribute__((aligned(128))) float biases[2][2][64];
 
     int64_t ti;
     int part;
@@ -104,6 +107,12 @@ __global__ __launch_bounds__(256, 2) void gated_short(Short<T> a)
             const int n = i * 4 + wave, matrix = n / KS;  // plane by plane, g's and u's
             const E *w = (matrix & 1 ? a.up.p : a.gate.p) + (matrix >> 1) * a.gate.plane + first;
             load_lds(descriptor(w, bytes), from[i], 0, base + buffer * kBuffer + n * 1024);
+        }
+        if (wave < 2) {
+            const float *b = wave ? a.bias1 : a.bias0;
+            const int f = chunk * 32 + lane;
+            load_lds4(descriptor(b, b ? (int64_t)a.n * 4 : 0), lane < 32 && f < a.n ? f * 4 : kOutside,
+                      lds_offset(&biases[buffer][wave][0]));
         }
     };
     issue(c0, 0);
@@ -154,19 +163,15 @@ __global__ __launch_bounds__(256, 2) void gated_short(Short<T> a)
         const int f0 = chunk * 32 + 4 * lc;
         float16v acc[2][MB];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int f = f0 + 8 * q;
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                acc[0][0][4 * q + e] = a.bias0 && f < a.n ? a.bias0[f + e] : 0.f;
-                acc[1][0][4 * q + e] = a.bias1 && f < a.n ? a.bias1[f + e] : 0.f;
+            for (int q = 0; q < 4; ++q) {
+                const float4v v = *(const float4v *)&biases[buffer][j][4 * lc + 8 * q];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int i = 0; i < MB; ++i) acc[j][i][4 * q + e] = v[e];
             }
-        }
-#pragma unroll
-        for (int i = 1; i < MB; ++i) {
-            acc[0][i] = acc[0][0];
-            acc[1][i] = acc[1][0];
-        }
         Vec<T, 4> d[MB][4];
         if (MODE == kBackward)
 #pragma unroll
