@@ -41,10 +41,17 @@ struct Plan {
     int cp, fp;          // row lengths in the workspace: c and f up to a multiple of 8
     Tiles dual, dx, dw;  // g and u; dx; the weights' gradients
     int64_t row_tiles;   // of the kernel for short rows (0: rows are too long for it)
-    int parts, part_cut; // its workgroups for a tile of rows, and their chunks
+    int steps, waves;    // its steps of 16 in a row, its waves of 32 rows
+    int parts, part_cut; // its workgroups for a tile of rows, and their chunks of 64 columns
     // bytes
     size_t x, w, grads, wt, bias, part;
 };
+
+// Waves of a workgroup of the kernel for short rows.
+constexpr int short_waves(int planes, int steps)
+{
+    return planes == 1 ? 4 : steps == 6 ? 6 : steps > 6 ? 8 : 4;
+}
 
 Plan make_plan(const wtconv_gated_desc_t &d);
 size_t workspace_bytes(const wtconv_gated_desc_t &d, bool backward);

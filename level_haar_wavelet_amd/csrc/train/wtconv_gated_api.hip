@@ -57,15 +57,23 @@ Plan make_plan(const wtconv_gated_desc_t &d)
     p.dx = pick(d.rows, d.c, kf, true, 1);
     p.dw = pick(2 * p.fp, d.c, km, true, 1);
     if (p.cp <= (one ? 256 : 192) && d.c % (one ? 8 : 4) == 0 && d.f % 4 == 0) {
-        const int64_t rows = one ? 256 : 128, chunks = (d.f + 31) / 32;
+        p.steps = 2;
+        for (int k : {2, 4, 6, 8, 12, 16})
+            if (k * 16 >= p.cp) {
+                p.steps = k;
+                break;
+            }
+        p.waves = short_waves(p.planes, p.steps);
+        const int64_t rows = p.waves * 32, chunks = (d.f + 63) / 64;
         p.row_tiles = (d.rows + rows - 1) / rows;
-        // workgroups for several rounds, of at least two chunks
+        // workgroups for several rounds
         int64_t parts = (8 * kUnits + p.row_tiles - 1) / p.row_tiles;
-        parts = parts > (chunks + 1) / 2 ? (chunks + 1) / 2 : parts;
+        parts = parts > chunks ? chunks : parts;
         p.part_cut = (int)((chunks + parts - 1) / parts);
         p.parts = (int)((chunks + p.part_cut - 1) / p.part_cut);
     }
-    const int64_t bias_rows = p.dual.tm * 2 > p.row_tiles * 4 ? p.dual.tm * 2 : p.row_tiles * 4;
+    // rows of partial sums: at most four waves along a tile's rows, eight of the short kernel's
+    const int64_t bias_rows = p.dual.tm * 4 > p.row_tiles * 8 ? p.dual.tm * 4 : p.row_tiles * 8;
     if (p.pack) {
         p.x = align256((size_t)(d.rows * p.cp) * p.planes * 2);
         p.w = align256((size_t)(d.f * 2 * p.cp) * p.planes * 2);

@@ -247,33 +247,42 @@ __global__ __launch_bounds__(256) void gated_pack(const T *__restrict__ src, int
     }
 }
 
-// The weights' columns as rows: dst[c] = gate's column c, then up's, each of fp
-// elements, zeros behind f.  One workgroup a 64 x 64 tile; blockIdx.z: gate, up.
+// The weights' columns as rows: dst[c] = column c of both, g's and u's elements in
+// turn, 2 fp of them, zeros behind f.  One workgroup a 64 x 64 tile.
 template <typename T>
 __global__ __launch_bounds__(256) void gated_turn(const T *__restrict__ w_gate, const T *__restrict__ w_up, int f, int c,
                                                   int fp, typename Factor<T>::type *__restrict__ dst, int64_t plane)
 {
     typedef typename Factor<T>::type E;
     constexpr int P = Factor<T>::kPlanes;
-    __shared__ T tile[64][66];
-    const T *w = blockIdx.z ? w_up : w_gate;
+    __shared__ T tile[2][64][66];
     const int f0 = blockIdx.y * 64, c0 = blockIdx.x * 64, x = threadIdx.x & 63, y = threadIdx.x >> 6;
 #pragma unroll
-    for (int i = 0; i < 64; i += 4)
-        tile[y + i][x] = f0 + y + i < f && c0 + x < c ? w[(int64_t)(f0 + y + i) * c + c0 + x] : (T)0.f;
+    for (int i = 0; i < 64; i += 4) {
+        const bool in = f0 + y + i < f && c0 + x < c;
+        const int64_t at = (int64_t)(f0 + y + i) * c + c0 + x;
+        tile[0][y + i][x] = in ? w_gate[at] : (T)0.f;
+        tile[1][y + i][x] = in ? w_up[at] : (T)0.f;
+    }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 64; i += 4)
         if (c0 + y + i < c && f0 + x < fp) {
-            E e[P];
-            const T v = tile[x][y + i];
-            if constexpr (P == 1)
-                e[0] = v;
-            else
-                split<T, P>(v, e);
+            Vec<E, 2> o[P];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                E e[P];
+                const T v = tile[z][x][y + i];
+                if constexpr (P == 1)
+                    e[0] = v;
+                else
+                    split<T, P>(v, e);
+#pragma unroll
+                for (int p = 0; p < P; ++p) o[p][z] = e[p];
+            }
 #pragma unroll
             for (int p = 0; p < P; ++p)
-                dst[p * plane + (int64_t)(c0 + y + i) * 2 * fp + blockIdx.z * fp + f0 + x] = e[p];
+                *(Vec<E, 2> *)(dst + p * plane + (int64_t)(c0 + y + i) * 2 * fp + 2 * (f0 + x)) = o[p];
         }
 }
 
@@ -305,11 +314,11 @@ struct Nt {
     const T *dh;
     T *out;             // [m][n]
     float *part;        // kProduct cut into slices: [slice][m][n]
-    E *grads;           // kBackward: [plane][m][2 fp]
+    E *grads;           // kBackward: [plane][m][2 fp], dg and du in turn
     int64_t grads_plane;
     int fp;
     float *bias_part;   // kBackward, or null: [tm * waves along m][2 fp]
-    bool wide;          // rows of out and dh in accesses of four elements
+    bool wide;          // rows of out and dh in accesses of two elements
 };
 
 // Tile of workgroup g: workgroups go to the 8 dies in turn, each die gets
@@ -356,27 +365,48 @@ __device__ inline void load4(const T *p, int c, int n, bool wide, float (&v)[4])
     }
 }
 
-// Sums of s[0 .. N) over the 2 N lanes that differ in the bits below 2 N, by halves: lane l
-// ends up with that of index (l % 2 N) / 2.
-template <int N>
-__device__ inline float sum_lanes(const float (&s)[N])
+typedef __amdgpu_buffer_rsrc_t Resource;
+
+__device__ inline Resource resource(const void *base, int64_t bytes)
 {
-    if constexpr (N == 1) {
-        return s[0] + __shfl_xor(s[0], 1);
-    } else {
-        const bool up = threadIdx.x & N;
-        float h[N / 2];
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i)
-            h[i] = (up ? s[i + N / 2] : s[i]) + __shfl_xor(up ? s[i] : s[i + N / 2], N);
-        return sum_lanes<N / 2>(h);
-    }
+    return __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, bytes < 0 ? 0 : bytes > 0x7fffffff ? 0x7fffffff : (int)bytes,
+                                             0x00020000);
 }
+
+// N elements at `lane + wave` bytes; beyond the resource nothing is written, and
+// zeros are read.
+template <typename T, int N>
+__device__ inline void put(const Vec<T, N> &v, const Resource &to, uint32_t lane, uint32_t wave)
+{
+    constexpr int kBytes = N * sizeof(T);
+    if constexpr (kBytes == 2)
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), to, lane, wave, 0);
+    else if constexpr (kBytes == 4)
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), to, lane, wave, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(Vec<uint32_t, 2>, v), to, lane, wave, 0);
+}
+
+template <typename T, int N>
+__device__ inline Vec<T, N> get(const Resource &from, uint32_t lane, uint32_t wave)
+{
+    constexpr int kBytes = N * sizeof(T);
+    if constexpr (kBytes == 2)
+        return __builtin_bit_cast(Vec<T, N>, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(from, lane, wave, 0));
+    else if constexpr (kBytes == 4)
+        return __builtin_bit_cast(Vec<T, N>, __builtin_amdgcn_raw_buffer_load_b32(from, lane, wave, 0));
+    else
+        return __builtin_bit_cast(Vec<T, N>, __builtin_amdgcn_raw_buffer_load_b64(from, lane, wave, 0));
+}
+
+// Row of a 32 x 32 block that a lane's accumulator q holds, without its 4 (lane / 32); the
+// column is lane % 32.
+__device__ constexpr int row_of(int q) { return 8 * (q >> 2) + (q & 3); }
 
 // One step (16 of the sum's index) of a wave's blocks; between(n) goes between its
 // instructions, n = 0 .. kCount RM RN - 1.
 template <int P, int RM, int RN, typename F, typename B>
-__device__ inline void products(float16v (&acc)[RN][RM], const F (&fb)[RN][P], const F (&fa)[RM][P], B between)
+__device__ inline void products(float16v (&acc)[RM][RN], const F (&fa)[RM][P], const F (&fb)[RN][P], B between)
 {
 #pragma unroll
     for (int q = 0; q < Pairs<P>::kCount; ++q)
@@ -384,7 +414,7 @@ __device__ inline void products(float16v (&acc)[RN][RM], const F (&fb)[RN][P], c
         for (int j = 0; j < RN; ++j)
 #pragma unroll
             for (int i = 0; i < RM; ++i) {
-                acc[j][i] = mfma(fb[j][Pairs<P>::l[q]], fa[i][Pairs<P>::r[q]], acc[j][i]);
+                acc[i][j] = mfma(fa[i][Pairs<P>::l[q]], fb[j][Pairs<P>::r[q]], acc[i][j]);
                 between((q * RN + j) * RM + i);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -401,7 +431,7 @@ __device__ inline void products(float16v (&acc)[RN][RM], const F (&fb)[RN][P], c
 // are issued and read like the others, for the sake of the count; issue() gives
 // them zeros and nothing is multiplied by them.
 template <int NB, int KK, int L, int R, int M, int P, int RM, int RN, typename F, typename I, typename G>
-__device__ inline void ring(float16v (&acc)[RN][RM], int stages, I issue, G read)
+__device__ inline void ring(float16v (&acc)[RM][RN], int stages, I issue, G read)
 {
     constexpr int kHalf = M / 2, kReads = (R + kHalf - 1) / kHalf, kIssues = (L + M - 1) / M;
     static_assert(KK % 2 == 0 && NB >= 2, "steps alternate between two sets of factors");
@@ -422,7 +452,7 @@ __device__ inline void ring(float16v (&acc)[RN][RM], int stages, I issue, G read
                 wait_loads<(NB - 2) * L>();
                 barrier();
             }
-            products<P, RM, RN>(acc, f[k % 2].b, f[k % 2].a, [&](int n) {
+            products<P, RM, RN>(acc, f[k % 2].a, f[k % 2].b, [&](int n) {
 #pragma unroll
                 for (int i = 0; i < kReads; ++i)
                     if (n * kReads + i < R) read(last ? s + 1 : s, last ? 0 : k + 1, n * kReads + i, f[(k + 1) % 2]);
@@ -444,18 +474,25 @@ struct Factors {
 // A tile of BM rows of A and BN rows of B; WM x WN waves, NB buffers.  A stage is BK
 // elements (64 or 128 bytes) of each row, whose 16-byte chunks are permuted so that the
 // rows that a read phase covers fall into different banks.
+//
+// A lane ends up with one column of every block of 32.  Rows of B are dealt to the
+// blocks so that a lane's columns are neighbours where a wave has enough of them, and
+// a row of the output goes out as 32 lanes' contiguous 4 or 8 bytes: whole cache
+// lines (of lines written in parts the L2s wrote 1.7 times as much).
 template <typename T, int BM, int BN, int WM, int WN, int BK, int NB, int MODE>
 __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
 {
     typedef typename Factor<T>::type E;
-    constexpr int P = Factor<T>::kPlanes, W = WM * WN;
+    constexpr int P = Factor<T>::kPlanes, W = WM * WN, S = sizeof(T);
     constexpr int kRow = BK * 2, kStage = (BM + BN) * P * kRow, kChunks = kRow / 16;
     // a load takes kPer rows; the waves' loads follow each other
-    constexpr int kPer = 1024 / kRow, kA = BM / kPer / W, kB = BN / kPer / W;
-    static_assert(kA * kPer * W == BM && kB * kPer * W == BN, "rows are shared out evenly");
-    static_assert(kPer * W % 32 == 0 && (MODE == kProduct || kPer * W == 64 || kPer * W == 32), "see blane");
+    constexpr int kPer = 1024 / kRow, kTurn = kPer * W, kA = BM / kTurn, kB = BN / kTurn;
+    static_assert(kA * kTurn == BM && kB * kTurn == BN, "rows are shared out evenly");
+    static_assert(kTurn == 32 || kTurn == 64, "see the rows of B");
     constexpr int RM = BM / WM / 32, RN = BN / WN / 32;
-    static_assert(MODE == kProduct || RN % 2 == 0, "a wave has as many blocks of g as of u");
+    // columns of a lane that are neighbours: blocks 0 and 1, or (g, u) pairs 0 and 1
+    constexpr int kPair = MODE == kProduct || RN % 4 == 0 ? 2 : 1;
+    static_assert(RN % 2 == 0 && (kPair == 1 || MODE == kProduct || kTurn == 32), "blocks of g and u, or of two columns");
     typedef Factors<E, P, RM, RN> F;
     __shared__ __attribute__((aligned(128))) char lds[NB * kStage];
 
@@ -472,27 +509,30 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
     const int stages = (int)(MODE == kProduct ? (all - s0 < a.cut ? all - s0 : a.cut) : all);
     const int k0 = (int)(s0 * BK), k1 = k0 + stages * BK < a.k ? k0 + stages * BK : a.k;
 
-    // Row `row` of the first of this wave's loads, the i-th kPer W i rows on; a chunk's
+    // Row `row` of the first of this wave's loads, the i-th kTurn i rows on; a chunk's
     // place depends on the row modulo 16 only.
     auto swizzle = [](int r) { return kChunks == 8 ? (r >> 1) & 7 : (r >> 2) & 3; };
     const int row = wave * kPer + lane / kChunks, chunk = (lane % kChunks) ^ swizzle(row);
     const uint32_t apitch = (uint32_t)a.a.pitch * 2, bpitch = (uint32_t)a.b0.pitch * 2;
     const uint32_t alane = row * apitch + chunk * 16;
-    // B's rows in memory; g and u: tile rows 64 i .. 64 i + 31 are the gate's rows from
-    // 32 i on, the next 32 the up projection's
-    uint32_t blane = row * bpitch + chunk * 16;
-    bool up = false;  // 64 rows a step: this wave's are all of one matrix; 32: they take turns
-    if (MODE != kProduct && kPer * W == 64) {
-        up = wave * kPer / 32;
-        blane -= up ? 32 * bpitch : 0;
-    }
+    // Rows of B in the tile, blocks of 32:
+    //   product            columns 64 i + 2 r, 64 i + 2 r + 1
+    //   g and u, pairs     g and u of 64 i + 2 r, g and u of 64 i + 2 r + 1
+    //   g and u            g and u of 32 i + r
+    const bool odd = kTurn == 64 && wave * kPer >= 32;  // all of this wave's rows are of the second block
+    const uint32_t blane = (kPair * (row % 32) + (MODE == kProduct && odd ? 1 : 0)) * bpitch + chunk * 16;
+    auto first_row = [](int i) {  // of load i
+        if (MODE == kProduct) return kTurn == 32 ? i / 2 * 64 + i % 2 : i * 64;
+        if (kPair == 2) return i / 4 * 64 + i / 2 % 2;
+        return kTurn == 32 ? i / 2 * 32 : i * 32;
+    };
     Descriptor da[P], db[P], dup[P];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         da[p] = descriptor(a.a.p + p * a.a.plane + m0 * a.a.pitch, (a.m - m0) * apitch);
         const int64_t first = p * a.b0.plane + (int64_t)n0 * a.b0.pitch, bytes = (int64_t)(a.n - n0) * bpitch;
-        db[p] = descriptor((up ? a.b1.p : a.b0.p) + first, bytes);
-        dup[p] = MODE != kProduct && kPer * W == 32 ? descriptor(a.b1.p + first, bytes) : db[p];
+        db[p] = descriptor((MODE != kProduct && odd ? a.b1.p : a.b0.p) + first, bytes);
+        dup[p] = MODE != kProduct && kTurn == 32 ? descriptor(a.b1.p + first, bytes) : db[p];
     }
     const uint32_t base = lds_offset(lds);
     auto issue = [&](int s, int n) {
@@ -501,13 +541,10 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
         const bool in = k + chunk * 8 < k1;
         const uint32_t to = base + s % NB * kStage + wave * 1024;
         if (i < kA)
-            load_lds(da[p], in ? alane : kOutside, k * 2 + i * kPer * W * apitch, to + p * BM * kRow + i * W * 1024);
-        else {
-            // rows of g's and u's weights: half as many as of the tile
-            const int j = i - kA, rows = MODE == kProduct ? j * kPer * W : kPer * W == 64 ? j * 32 : j / 2 * 32;
-            load_lds(j % 2 ? dup[p] : db[p], in ? blane : kOutside, k * 2 + rows * bpitch,
-                     to + P * BM * kRow + p * BN * kRow + j * W * 1024);
-        }
+            load_lds(da[p], in ? alane : kOutside, k * 2 + i * kTurn * apitch, to + p * BM * kRow + i * W * 1024);
+        else
+            load_lds((i - kA) % 2 ? dup[p] : db[p], in ? blane : kOutside, k * 2 + first_row(i - kA) * bpitch,
+                     to + P * BM * kRow + p * BN * kRow + (i - kA) * W * 1024);
     };
     auto read = [&](int s, int kk, int n, F &f) {
         const char *at = lds + s % NB * kStage + (((kk * 2 + lc) ^ swizzle(lr)) * 16) + lr * kRow;
@@ -517,101 +554,135 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
         else
             f.a[i - RN][p] = *(const Vec<E, 8> *)(at + (p * BM + wm + (i - RN) * 32) * kRow);
     };
-    float16v acc[RN][RM] = {};  // rows: B's, columns: A's
+    float16v acc[RM][RN] = {};  // rows: A's, columns: B's
     ring<NB, BK / 16, P *(kA + kB), P *(RM + RN), Pairs<P>::kCount * RM * RN, P, RM, RN, F>(acc, stages, issue, read);
 
-    // A lane has column m = lr of A's rows and, of B's rows, 8 (q / 4) + 4 lc + q % 4.
+    // this lane's first row
+    const int64_t mine = m0 + wm + 4 * lc;
     if constexpr (MODE == kProduct) {
+        auto write = [&](auto *out, auto two) {
+            typedef typename std::remove_pointer<decltype(out)>::type O;
+            const Resource to = resource(out + m0 * a.n, (a.m - m0) * a.n * (int)sizeof(O));
 #pragma unroll
-        for (int i = 0; i < RM; ++i) {
-            const int64_t m = m0 + wm + i * 32 + lr;
-            if (m >= a.m) continue;
+            for (int j = 0; j < RN; j += 2) {
+                const int n = n0 + wn + j * 32 + 2 * lr;
+                const uint32_t at = ((uint32_t)(mine - m0) * a.n + n) * sizeof(O);
 #pragma unroll
-            for (int j = 0; j < RN; ++j)
+                for (int i = 0; i < RM; ++i)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int n = n0 + wn + j * 32 + 8 * q + 4 * lc;
-                    const float v[4] = {acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2],
-                                        acc[j][i][4 * q + 3]};
-                    if (a.slices > 1)
-                        store4(a.part + (slice * a.m + m) * a.n, n, a.n, a.n % 4 == 0, v);
-                    else
-                        store4(a.out + m * a.n, n, a.n, a.wide, v);
-                }
-        }
-        return;
-    } else
+                    for (int q = 0; q < 16; ++q) {
+                        const uint32_t rows = (i * 32 + row_of(q)) * a.n * (uint32_t)sizeof(O);
+                        const O v0 = (O)acc[i][j][q], v1 = (O)acc[i][j + 1][q];
+                        if constexpr (two) {
+                            put<O, 2>(Vec<O, 2>{v0, v1}, to, n < a.n ? at : kOutside, rows);
+                        } else {
+                            put<O, 1>(Vec<O, 1>{v0}, to, n < a.n ? at : kOutside, rows);
+                            put<O, 1>(Vec<O, 1>{v1}, to, n + 1 < a.n ? at + (uint32_t)sizeof(O) : kOutside, rows);
+                        }
+                    }
+            }
+        };
+        if (a.slices > 1) {
+            float *part = a.part + slice * a.m * a.n;
+            if (a.n % 2 == 0)
+                write(part, std::true_type{});
+            else
+                write(part, std::false_type{});
+        } else if (a.wide)
+            write(a.out, std::true_type{});
+        else
+            write(a.out, std::false_type{});
+    } else {
+        // dh, or h: kPair neighbours at once where they lie so
+        const T *io = MODE == kForward ? a.out : a.dh;
+        const Resource rio = resource(io + m0 * a.n, (a.m - m0) * a.n * S);
         with_act(a.act, [&](auto kind) {
 #pragma unroll
-        for (int j = 0; j < RN; j += 2) {
-            const int f0 = n0 + wn / 2 + j * 16 + 4 * lc;
-            float bg[16], bu[16];
+            for (int j = 0; j < RN; j += 2 * kPair) {
+                const int f0 = n0 + wn / 2 + j * 16 + kPair * lr;
+                float bg[kPair], bu[kPair], sg[kPair] = {}, su[kPair] = {};
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
-                const int f = f0 + 8 * (q >> 2) + (q & 3);
-                bg[q] = a.bias0 && f < a.n ? a.bias0[f] : 0.f;
-                bu[q] = a.bias1 && f < a.n ? a.bias1[f] : 0.f;
-            }
-            float sg[16] = {}, su[16] = {};
+                for (int h = 0; h < kPair; ++h) {
+                    bg[h] = a.bias0 && f0 + h < a.n ? a.bias0[f0 + h] : 0.f;
+                    bu[h] = a.bias1 && f0 + h < a.n ? a.bias1[f0 + h] : 0.f;
+                }
+                const uint32_t at = ((uint32_t)(mine - m0) * a.n + f0) * S;
+                const uint32_t at0 = f0 < a.n ? at : kOutside, at1 = f0 + 1 < a.n ? at + S : kOutside;
 #pragma unroll
-            for (int i = 0; i < RM; ++i) {
-                const int64_t m = m0 + wm + i * 32 + lr;
-                if (m >= a.m) continue;
+                for (int i = 0; i < RM; ++i) {
+                    Vec<T, kPair> d[16];
+                    if constexpr (MODE == kBackward)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int f = f0 + 8 * q;
-                    float g[4], u[4], d[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        g[e] = acc[j][i][4 * q + e] + bg[4 * q + e];
-                        u[e] = acc[j + 1][i][4 * q + e] + bu[4 * q + e];
-                    }
-                    if constexpr (MODE == kForward) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) g[e] = act<kind>(g[e]) * u[e];
-                        store4(a.out + m * a.n, f, a.n, a.wide, g);
-                    } else {
-                        load4(a.dh + m * a.n, f, a.n, a.wide, d);
-                        // dg and du of columns behind f are zero
-                        Vec<E, 4> og[P], ou[P];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float slope;
-                            const float y = act_slope<kind>(g[e], slope);
-                            const bool in = f + e < a.n;
-                            const float dg = in ? d[e] * u[e] * slope : 0.f, du = in ? d[e] * y : 0.f;
-                            sg[4 * q + e] += dg;
-                            su[4 * q + e] += du;
-                            E eg[P], eu[P];
-                            split<T, P>(dg, eg);
-                            split<T, P>(du, eu);
-#pragma unroll
-                            for (int p = 0; p < P; ++p) {
-                                og[p][e] = eg[p];
-                                ou[p][e] = eu[p];
+                        for (int q = 0; q < 16; ++q) {
+                            const uint32_t rows = (i * 32 + row_of(q)) * a.n * S;
+                            if (kPair == 1 || a.wide) {
+                                d[q] = get<T, kPair>(rio, at0, rows);
+                            } else {
+                                d[q][0] = get<T, 1>(rio, at0, rows)[0];
+                                d[q][kPair - 1] = get<T, 1>(rio, at1, rows)[0];
                             }
                         }
-                        if (f < a.fp)
 #pragma unroll
-                            for (int p = 0; p < P; ++p) {
-                                E *out = a.grads + p * a.grads_plane + m * 2 * a.fp + f;
-                                *(Vec<E, 4> *)out = og[p];
-                                *(Vec<E, 4> *)(out + a.fp) = ou[p];
+                    for (int q = 0; q < 16; ++q) {
+                        float g[kPair], u[kPair];
+#pragma unroll
+                        for (int h = 0; h < kPair; ++h) {
+                            g[h] = acc[i][j + 2 * h][q] + bg[h];
+                            u[h] = acc[i][j + 2 * h + 1][q] + bu[h];
+                        }
+                        if constexpr (MODE == kForward) {
+                            const uint32_t rows = (i * 32 + row_of(q)) * a.n * S;
+                            Vec<T, kPair> o;
+#pragma unroll
+                            for (int h = 0; h < kPair; ++h) o[h] = (T)(act<kind>(g[h]) * u[h]);
+                            if (kPair == 1 || a.wide) {
+                                put<T, kPair>(o, rio, at0, rows);
+                            } else {
+                                put<T, 1>(Vec<T, 1>{o[0]}, rio, at0, rows);
+                                put<T, 1>(Vec<T, 1>{o[kPair - 1]}, rio, at1, rows);
                             }
+                        } else {
+                            // columns and rows behind the last: dh is zero there
+                            Vec<E, 2 * kPair> o[P];
+#pragma unroll
+                            for (int h = 0; h < kPair; ++h) {
+                                float slope;
+                                const float y = act_slope<kind>(g[h], slope), dv = (float)d[q][h];
+                                const float dg = dv * u[h] * slope, du = dv * y;
+                                sg[h] += dg;
+                                su[h] += du;
+                                E eg[P], eu[P];
+                                split<T, P>(dg, eg);
+                                split<T, P>(du, eu);
+#pragma unroll
+                                for (int p = 0; p < P; ++p) {
+                                    o[p][2 * h] = eg[p];
+                                    o[p][2 * h + 1] = eu[p];
+                                }
+                            }
+#pragma unroll
+                            for (int p = 0; p < P; ++p)
+                                put<E, 2 * kPair>(o[p], resource(a.grads + p * a.grads_plane + m0 * 2 * a.fp,
+                                                                 (a.m - m0) * 4 * a.fp),
+                                                  f0 < a.fp ? ((uint32_t)(mine - m0) * a.fp + f0) * 4 : kOutside,
+                                                  (i * 32 + row_of(q)) * a.fp * 4);
+                        }
                     }
+                    __builtin_amdgcn_sched_barrier(0);  // fewer values live at once
                 }
+                if (MODE == kBackward && a.bias_part)
+#pragma unroll
+                    for (int h = 0; h < kPair; ++h) {
+                        const float g = sg[h] + __shfl_xor(sg[h], 32), u = su[h] + __shfl_xor(su[h], 32);
+                        if (!lc && f0 + h < a.n) {
+                            float *out = a.bias_part + (ti * WM + wave / WN) * 2 * a.fp + f0 + h;
+                            out[0] = g;
+                            out[a.fp] = u;
+                        }
+                    }
             }
-            if (MODE == kBackward && a.bias_part) {
-                const float g = sum_lanes(sg), u = sum_lanes(su);
-                const int q = lr >> 1, f = f0 + 8 * (q >> 2) + (q & 3);
-                if (!(lane & 1) && f < a.n) {
-                    float *out = a.bias_part + (ti * WM + wave / WN) * 2 * a.fp;
-                    out[f] = g;
-                    out[a.fp + f] = u;
-                }
-            }
-        }
         });
+    }
 }
 
 }  // namespace wtc_gated
@@ -625,7 +696,7 @@ namespace wtc_gated {
 template <typename T>
 struct Tn {
     typedef typename Factor<T>::type E;
-    const E *a, *b;  // [plane][m][2 fp], [plane][m][pitch]
+    const E *a, *b;  // [plane][m][2 fp] (dg and du in turn), [plane][m][pitch]
     int64_t a_plane, b_plane, b_pitch;
     int64_t m;
     int f, fp, c;
@@ -634,7 +705,6 @@ struct Tn {
     int64_t cut;     // stages of a slice
     T *gate, *up;    // [f][c]
     float *part;     // [slice][2 fp][c]
-    bool wide;
 };
 
 // D = A^T B, a tile of BM columns of A (gradients) and BN of B (x), over a slice
@@ -711,40 +781,60 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_tn(Tn<T> a)
         else
             f.a[i - RN][p] = frag(la + p * BK * kRowA, kRowA, kk * 16, wm + (i - RN) * 32);
     };
-    float16v acc[RN][RM] = {};  // [x][gradients]; rows: x's columns, columns: the gradients'
+    float16v acc[RM][RN] = {};  // rows: the gradients' columns, columns: x's
     ring<NB, BK / 16, P *(kA + kB), P *(RM + RN), Pairs<P>::kCount * RM * RN, P, RM, RN, F>(acc, stages, issue, read);
+
+    const int mine = wm + 4 * lc;  // this lane's first row of the tile
 #pragma unroll
-    for (int i = 0; i < RM; ++i) {
-        const int f = f0 + wm + i * 32 + lr;
-        if (f >= 2 * a.fp) continue;
-        const bool up = f >= a.fp;
-        const int own = up ? f - a.fp : f;
-        if (own >= a.f) continue;
+    for (int j = 0; j < RN; ++j) {
+        const int c = c0 + wn + j * 32 + lr;
+        if (a.slices > 1) {
+            const Resource to = resource(a.part + ((int64_t)slice * 2 * a.fp + f0) * a.c, (int64_t)(2 * a.fp - f0) * a.c * 4);
+            const uint32_t at = c < a.c ? ((uint32_t)mine * a.c + c) * 4 : kOutside;
 #pragma unroll
-        for (int j = 0; j < RN; ++j)
+            for (int i = 0; i < RM; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int c = c0 + wn + j * 32 + 8 * q + 4 * lc;
-                const float v[4] = {acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
-                if (a.slices > 1)
-                    store4(a.part + ((int64_t)slice * 2 * a.fp + f) * a.c, c, a.c, a.c % 4 == 0, v);
-                else
-                    store4((up ? a.up : a.gate) + (int64_t)own * a.c, c, a.c, a.wide, v);
-            }
+                for (int q = 0; q < 16; ++q)
+                    put<float, 1>(Vec<float, 1>{acc[i][j][q]}, to, at, (uint32_t)(i * 32 + row_of(q)) * a.c * 4);
+        } else {
+            // rows of g and of u in turn
+            const int64_t first = (int64_t)(f0 / 2) * a.c, bytes = (int64_t)(a.f - f0 / 2) * a.c * (int)sizeof(T);
+            const Resource to[2] = {resource(a.gate + first, bytes), resource(a.up + first, bytes)};
+            const uint32_t at = c < a.c ? ((uint32_t)(mine / 2) * a.c + c) * sizeof(T) : kOutside;
+#pragma unroll
+            for (int i = 0; i < RM; ++i)
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                    put<T, 1>(Vec<T, 1>{(T)acc[i][j][q]}, to[q & 1], at,
+                              (uint32_t)((i * 32 + row_of(q)) / 2) * a.c * (uint32_t)sizeof(T));
+        }
     }
 }
 
 // ---- Sums of slices ---------------------------------------------------------------
 
-// out = sum over slices of part[slice][rows][n], where out is one matrix, or two
-// of `f` rows each that are `fp` rows of part apart.
+// out[size] = sum over slices of part[slice][size].
 template <typename T>
-__global__ __launch_bounds__(256) void gated_join(const float *__restrict__ part, int64_t slice, int slices, int64_t size,
-                                                  int64_t second, T *__restrict__ out0, T *__restrict__ out1)
+__global__ __launch_bounds__(256) void gated_join(const float *__restrict__ part, int slices, int64_t size,
+                                                  T *__restrict__ out)
 {
-    const float *p = part + (blockIdx.y ? second : 0);
-    T *out = blockIdx.y ? out1 : out0;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < size; i += (int64_t)gridDim.x * 256) {
+        float v = 0.f;
+#pragma unroll 8
+        for (int s = 0; s < slices; ++s) v += part[s * size + i];
+        out[i] = (T)v;
+    }
+}
+
+// The same for the weights' gradients, whose rows are g's and u's in turn; a workgroup a
+// row of c, blockIdx.y: g, u.
+template <typename T>
+__global__ __launch_bounds__(256) void gated_join_rows(const float *__restrict__ part, int64_t slice, int slices, int c,
+                                                       T *__restrict__ gate, T *__restrict__ up)
+{
+    const float *p = part + ((int64_t)blockIdx.x * 2 + blockIdx.y) * c;
+    T *out = (blockIdx.y ? up : gate) + (int64_t)blockIdx.x * c;
+    for (int i = threadIdx.x; i < c; i += 256) {
         float v = 0.f;
 #pragma unroll 8
         for (int s = 0; s < slices; ++s) v += p[s * slice + i];
@@ -867,8 +957,10 @@ void launch_nt(const Tiles &t, Nt<T> &a, hipStream_t stream)
     if constexpr (Factor<T>::kPlanes == 1) {
         if (t.bm == 256)
             gated_nt<T, 256, 256, 2, 2, 64, 2, MODE><<<grid, dim3(256), 0, stream>>>(a);
-        else
+        else if constexpr (MODE == kProduct)
             gated_nt<T, 128, 128, 2, 2, 64, 2, MODE><<<grid, dim3(256), 0, stream>>>(a);
+        else
+            gated_nt<T, 128, 128, 4, 1, 64, 2, MODE><<<grid, dim3(256), 0, stream>>>(a);
     } else {
         gated_nt<T, 128, 128, 2, 2, 32, 3, MODE><<<grid, dim3(256), 0, stream>>>(a);
     }
@@ -878,6 +970,12 @@ template <typename T>
 bool wide4(const void *p, int64_t n)
 {
     return n % 4 == 0 && aligned_to(p, 4 * sizeof(T));
+}
+
+template <typename T>
+bool wide2(const void *p, int64_t n)
+{
+    return n % 2 == 0 && aligned_to(p, 2 * sizeof(T));
 }
 
 template <typename T>
@@ -911,10 +1009,16 @@ Operands<T> operands(const wtconv_gated_desc_t &d, const Plan &pl, const void *x
     return {{xp, d.rows * pl.cp, pl.cp}, {wp, plane, pl.cp}, {wp + half, plane, pl.cp}};
 }
 
+// Waves along a tile's rows, each with its own sums for the biases.
+template <typename T>
+int bias_waves(const Tiles &t)
+{
+    return Factor<T>::kPlanes == 1 && t.bm == 128 ? 4 : 2;
+}
+
 template <typename T, int MODE>
 void launch_short(const wtconv_gated_desc_t &d, const Plan &pl, const Operands<T> &o, Short<T> &a, hipStream_t stream)
 {
-    constexpr int MB = Factor<T>::kPlanes == 1 ? 2 : 1;
     a.gate = o.gate;
     a.up = o.up;
     a.m = d.rows;
@@ -924,18 +1028,18 @@ void launch_short(const wtconv_gated_desc_t &d, const Plan &pl, const Operands<T
     a.tiles = pl.row_tiles;
     a.parts = pl.parts;
     a.cut = pl.part_cut;
-    const dim3 grid((unsigned)(a.tiles * a.parts));
-    auto run = [&](auto ks) { gated_short<T, ks, MB, MODE><<<grid, dim3(256), 0, stream>>>(a); };
-    const int steps = (pl.cp + 15) / 16;
-    if (steps <= 2)
+    auto run = [&](auto ks) {
+        gated_short<T, ks, MODE><<<dim3((unsigned)(a.tiles * a.parts)), dim3(pl.waves * 64), 0, stream>>>(a);
+    };
+    if (pl.steps == 2)
         run(std::integral_constant<int, 2>{});
-    else if (steps <= 4)
+    else if (pl.steps == 4)
         run(std::integral_constant<int, 4>{});
-    else if (steps <= 6)
+    else if (pl.steps == 6)
         run(std::integral_constant<int, 6>{});
-    else if (steps <= 8)
+    else if (pl.steps == 8)
         run(std::integral_constant<int, 8>{});
-    else if (steps <= 12)
+    else if (pl.steps == 12)
         run(std::integral_constant<int, 12>{});
     else if constexpr (Factor<T>::kPlanes == 1)
         run(std::integral_constant<int, 16>{});
@@ -995,7 +1099,7 @@ hipError_t forward(const wtconv_gated_desc_t &d, const Forward &a, void *workspa
     p.bias0 = a.b_gate;
     p.bias1 = a.b_up;
     p.out = (T *)a.h;
-    p.wide = wide4<T>(a.h, d.f);
+    p.wide = wide2<T>(a.h, d.f);
     launch_nt<T, kForward>(pl.dual, p, stream);
     return hipGetLastError();
 }
@@ -1040,7 +1144,7 @@ hipError_t backward(const wtconv_gated_desc_t &d, const Backward &a, void *works
         p.grads_plane = gplane;
         p.fp = pl.fp;
         p.bias_part = a.db_gate ? bias : nullptr;
-        bias_rows = pl.row_tiles * 4;
+        bias_rows = pl.row_tiles * pl.waves;
         launch_short<T, kBackward>(d, pl, o, p, stream);
     } else {
         Nt<T> p = {};
@@ -1054,12 +1158,12 @@ hipError_t backward(const wtconv_gated_desc_t &d, const Backward &a, void *works
         p.bias0 = a.b_gate;
         p.bias1 = a.b_up;
         p.dh = (const T *)a.dh;
-        p.wide = wide4<T>(a.dh, d.f);
+        p.wide = wide2<T>(a.dh, d.f);
         p.grads = grads;
         p.grads_plane = gplane;
         p.fp = pl.fp;
         p.bias_part = a.db_gate ? bias : nullptr;
-        bias_rows = pl.dual.tm * 2;  // of the waves along the rows
+        bias_rows = bias_waves<T>(pl.dual) * pl.dual.tm;
         launch_nt<T, kBackward>(pl.dual, p, stream);
     }
     if (a.db_gate)
@@ -1067,7 +1171,7 @@ hipError_t backward(const wtconv_gated_desc_t &d, const Backward &a, void *works
                                                                                     a.db_gate, a.db_up);
     if (a.dx) {
         const int64_t plane = d.c * 2 * pl.fp;
-        gated_turn<T><<<dim3((unsigned)((d.c + 63) / 64), (unsigned)((pl.fp + 63) / 64), 2), dim3(256), 0, stream>>>(
+        gated_turn<T><<<dim3((unsigned)((d.c + 63) / 64), (unsigned)((pl.fp + 63) / 64)), dim3(256), 0, stream>>>(
             (const T *)a.w_gate, (const T *)a.w_up, (int)d.f, (int)d.c, pl.fp, wt, plane);
         Nt<T> q = {};
         q.a = {grads, gplane, 2 * pl.fp};
@@ -1076,13 +1180,12 @@ hipError_t backward(const wtconv_gated_desc_t &d, const Backward &a, void *works
         q.n = (int)d.c;
         q.k = 2 * pl.fp;
         q.out = (T *)a.dx;
-        q.wide = wide4<T>(a.dx, d.c);
+        q.wide = wide2<T>(a.dx, d.c);
         q.part = part;
         launch_nt<T, kProduct>(pl.dx, q, stream);
         const int64_t size = d.rows * d.c;
         if (pl.dx.slices > 1)
-            gated_join<T><<<dim3(blocks_of(size, 4096)), dim3(256), 0, stream>>>(part, size, pl.dx.slices, size, 0,
-                                                                             (T *)a.dx, nullptr);
+            gated_join<T><<<dim3(blocks_of(size, 4096)), dim3(256), 0, stream>>>(part, pl.dx.slices, size, (T *)a.dx);
     }
     if (a.dw_gate) {
         Tn<T> q = {};
@@ -1097,13 +1200,11 @@ hipError_t backward(const wtconv_gated_desc_t &d, const Backward &a, void *works
         q.c = (int)d.c;
         q.gate = (T *)a.dw_gate;
         q.up = (T *)a.dw_up;
-        q.wide = wide4<T>(a.dw_gate, d.c) && wide4<T>(a.dw_up, d.c);
         q.part = part;
         launch_tn<T>(pl.dw, q, stream);
-        const int64_t size = d.f * d.c;
         if (pl.dw.slices > 1)
-            gated_join<T><<<dim3(blocks_of(size, 4096), 2), dim3(256), 0, stream>>>(
-                part, (int64_t)2 * pl.fp * d.c, pl.dw.slices, size, (int64_t)pl.fp * d.c, (T *)a.dw_gate, (T *)a.dw_up);
+            gated_join_rows<T><<<dim3((unsigned)d.f, 2), dim3(256), 0, stream>>>(
+                part, (int64_t)2 * pl.fp * d.c, pl.dw.slices, (int)d.c, (T *)a.dw_gate, (T *)a.dw_up);
     }
     return hipGetLastError();
 }
