@@ -50,7 +50,7 @@ struct Plan {
 // Waves of a workgroup of the kernel for short rows.
 constexpr int short_waves(int planes, int steps)
 {
-    return planes == 1 ? 4 : steps == 6 ? 6 : steps > 6 ? 8 : 4;
+    return planes > 1 && steps > 6 ? 8 : 4;
 }
 
 Plan make_plan(const wtconv_gated_desc_t &d);

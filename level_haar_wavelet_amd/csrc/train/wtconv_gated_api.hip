@@ -67,7 +67,7 @@ Plan make_plan(const wtconv_gated_desc_t &d)
         const int64_t rows = p.waves * 32, chunks = (d.f + 63) / 64;
         p.row_tiles = (d.rows + rows - 1) / rows;
         // workgroups for several rounds
-        int64_t parts = (8 * kUnits + p.row_tiles - 1) / p.row_tiles;
+        int64_t parts = (16 * kUnits + p.row_tiles - 1) / p.row_tiles;
         parts = parts > chunks ? chunks : parts;
         p.part_cut = (int)((chunks + parts - 1) / parts);
         p.parts = (int)((chunks + p.part_cut - 1) / p.part_cut);

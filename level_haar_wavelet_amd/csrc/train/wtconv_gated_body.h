@@ -87,19 +87,16 @@ struct Pairs<3> {
     static constexpr int l[6] = {2, 0, 1, 1, 0, 0}, r[6] = {0, 2, 1, 0, 1, 0};
 };
 
-// v as the sum of P numbers.  fp32: its bits from the top, eight at a time; an
-// infinity or NaN whole in the first (what is left of it would be NaN).
+// v as the sum of P numbers.  fp32: its bits from the top, eight at a time.  (Of an
+// infinity or a NaN the second is a NaN, and with it every sum it is in.)
 template <typename T, int P>
 __device__ inline void split(float v, typename Factor<T>::type (&o)[P])
 {
     if constexpr (P == 1) {
         o[0] = (T)v;
     } else {
-        const uint32_t u = __builtin_bit_cast(uint32_t, v);
-        const bool finite = (u & 0x7f800000u) != 0x7f800000u;
-        // a NaN whose bits all lie below stays one
-        const uint32_t top = (u & 0xffff0000u) | (!finite && (u & 0x7fffffu) ? 0x400000u : 0u);
-        const float r1 = finite ? v - __builtin_bit_cast(float, top) : 0.f;
+        const uint32_t top = __builtin_bit_cast(uint32_t, v) & 0xffff0000u;
+        const float r1 = v - __builtin_bit_cast(float, top);
         const uint32_t mid = __builtin_bit_cast(uint32_t, r1) & 0xffff0000u;
         const float r2 = r1 - __builtin_bit_cast(float, mid);
         o[0] = __builtin_bit_cast(__bf16, (uint16_t)(top >> 16));
@@ -219,11 +216,15 @@ __device__ inline void barrier()
 
 // ---- Laying out ----------------------------------------------------------------
 
-// Rows of k elements as `planes` matrices of rows of kp, zeros behind.
+// Rows of k elements as `planes` matrices of rows of kp, zeros behind; blockIdx.y: the
+// first of two sources, or the second, whose rows follow.
 template <typename T>
-__global__ __launch_bounds__(256) void gated_pack(const T *__restrict__ src, int64_t rows, int k, int kp,
-                                                  typename Factor<T>::type *__restrict__ dst, int64_t plane)
+__global__ __launch_bounds__(256) void gated_pack(const T *__restrict__ src0, const T *__restrict__ src1, int64_t rows,
+                                                  int k, int kp, typename Factor<T>::type *__restrict__ dst,
+                                                  int64_t plane)
 {
+    const T *__restrict__ src = blockIdx.y ? src1 : src0;
+    dst += blockIdx.y ? rows * kp : 0;
     typedef typename Factor<T>::type E;
     constexpr int P = Factor<T>::kPlanes;
     const int per = kp / 8;
@@ -1000,12 +1001,10 @@ Operands<T> operands(const wtconv_gated_desc_t &d, const Plan &pl, const void *x
     ws += pl.x + pl.w;
     const int64_t plane = d.f * 2 * pl.cp, half = d.f * pl.cp;
     if (pack_x)
-        gated_pack<T><<<dim3(blocks_of(d.rows * pl.cp / 8, 8192)), dim3(256), 0, stream>>>((const T *)x, d.rows, (int)d.c,
-                                                                                      pl.cp, xp, d.rows * pl.cp);
-    gated_pack<T><<<dim3(blocks_of(half / 8, 8192)), dim3(256), 0, stream>>>((const T *)w_gate, d.f, (int)d.c, pl.cp, wp,
-                                                                            plane);
-    gated_pack<T><<<dim3(blocks_of(half / 8, 8192)), dim3(256), 0, stream>>>((const T *)w_up, d.f, (int)d.c, pl.cp,
-                                                                            wp + half, plane);
+        gated_pack<T><<<dim3(blocks_of(d.rows * pl.cp / 8, 8192)), dim3(256), 0, stream>>>(
+            (const T *)x, nullptr, d.rows, (int)d.c, pl.cp, xp, d.rows * pl.cp);
+    gated_pack<T><<<dim3(blocks_of(half / 8, 8192), 2), dim3(256), 0, stream>>>(
+        (const T *)w_gate, (const T *)w_up, d.f, (int)d.c, pl.cp, wp, plane);
     return {{xp, d.rows * pl.cp, pl.cp}, {wp, plane, pl.cp}, {wp + half, plane, pl.cp}};
 }
 
