@@ -20,10 +20,25 @@ inline int64_t range_elems(int64_t elems)
     return r < kLeast ? kLeast : (r + 2047) / 2048 * 2048;
 }
 
-// fp64 sums of all ranges, and the total of more than kOwnSums.
-inline size_t workspace_bytes(int64_t count)
+constexpr int kByValue = 120;  // tensors whose table goes with a launch: 28 bytes each of 4 KB
+
+struct Entry {
+    const void *in;
+    void *out;
+    int64_t elems_type;  // elements * 4 + type
+    int64_t first;       // the tensor's first range
+};
+
+// fp64 sums of all ranges, and the total of more than kOwnSums; the table of more
+// than kByValue tensors.
+inline size_t sums_bytes(int64_t count)
 {
     return ((size_t)(kRanges + count + 1) * sizeof(double) + 255) / 256 * 256;
+}
+
+inline size_t workspace_bytes(int64_t count)
+{
+    return sums_bytes(count) + (count > kByValue ? ((size_t)count * sizeof(Entry) + 255) / 256 * 256 : 0);
 }
 
 }  // namespace wtc_clip

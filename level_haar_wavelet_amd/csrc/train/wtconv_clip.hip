@@ -9,8 +9,11 @@
 // second pass takes the ranges from the last to the first: the 256 MB cache holds
 // the end of what the first read.
 //
-// The table of tensors goes by value with the launch (it is then the captured
-// call's own, and needs no copy), so a launch takes kTensors of them.
+// The table of tensors goes by value with a launch (it is then the captured call's
+// own, and needs no copy from host memory that has to stay): of up to kByValue of
+// them with both kernels, of more with small launches in front that write it to the
+// workspace, so that the passes run whole (416 tensors in four launches for each
+// pass, with four ends to wait for: 576 us).
 //
 // Squares and sums are fp64: fp32 squares overflow from 2^64 on and vanish below
 // 2^-75, and 10^9 of them would lose digits; the fp64 rate is above memory's.
@@ -27,26 +30,53 @@ namespace {
 using namespace wtc_clip;
 
 constexpr int kThreads = 256;
-constexpr int kTensors = 120;  // of a launch: 28 bytes each in the 4 KB of a kernel's arguments
+constexpr int kWritten = 100;  // entries of a launch that writes the table
 
+// The table with the launch, or in the workspace.
 struct Table {
-    const void *in[kTensors];
-    void *out[kTensors];
-    int64_t elems_type[kTensors];  // elements * 4 + type
-    int first[kTensors];           // this launch's first range of the tensor
-    int n, ranges;
+    const void *in_[kByValue];
+    void *out_[kByValue];
+    int64_t elems_type_[kByValue];
+    int first_[kByValue];
+    int n;
+    int ranges;
     int64_t range;  // elements of a range
-    int64_t base;   // ranges of the launches before
+    __device__ const void *in(int i) const { return in_[i]; }
+    __device__ void *out(int i) const { return out_[i]; }
+    __device__ int64_t elems_type(int i) const { return elems_type_[i]; }
+    __device__ int first(int i) const { return first_[i]; }
 };
-static_assert(sizeof(Table) <= 3500 && sizeof(Table) + 64 <= 4096, "a kernel's arguments");
+static_assert(sizeof(Table) + 64 <= 4096, "a kernel's arguments");
+
+struct FarTable {
+    const Entry *e;
+    int n;
+    int ranges;
+    int64_t range;
+    __device__ const void *in(int i) const { return e[i].in; }
+    __device__ void *out(int i) const { return e[i].out; }
+    __device__ int64_t elems_type(int i) const { return e[i].elems_type; }
+    __device__ int first(int i) const { return (int)e[i].first; }
+};
+
+struct Entries {
+    Entry e[kWritten];
+};
+static_assert(sizeof(Entries) + 64 <= 4096, "a kernel's arguments");
+
+__global__ void write_table(Entries from, Entry *to, int n)
+{
+    if ((int)threadIdx.x < n) to[threadIdx.x] = from.e[threadIdx.x];
+}
 
 // The tensor that range r belongs to.
-__device__ inline int find(const Table &t, int r)
+template <typename T>
+__device__ inline int find(const T &t, int r)
 {
     int lo = 0, hi = t.n;
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (t.first[mid] <= r)
+        if (t.first(mid) <= r)
             lo = mid;
         else
             hi = mid;
@@ -163,19 +193,22 @@ __device__ inline void scale_any(const void *p, void *o, int64_t e, int64_t end,
         scale<T, 1>((const T *)p, (T *)o, e, end, f);
 }
 
-__global__ __launch_bounds__(kThreads) void norm_ranges(Table t, double *parts)
+template <typename L>
+__global__ __launch_bounds__(kThreads) void norm_ranges(L t, double *parts)
 {
-    const int r = blockIdx.x, i = find(t, r), type = (int)(t.elems_type[i] & 3);
-    const int64_t n = t.elems_type[i] >> 2, e = (r - t.first[i]) * t.range, end = n - e < t.range ? n : e + t.range;
+    const int r = blockIdx.x, i = find(t, r);
+    const int64_t et = t.elems_type(i), n = et >> 2, e = (r - t.first(i)) * t.range, end = n - e < t.range ? n : e + t.range;
+    const int type = (int)(et & 3);
+    const void *in = t.in(i);
     double a;
     if (type == WTCONV_F32)
-        a = squares_of<float>(t.in[i], e, end);
+        a = squares_of<float>(in, e, end);
     else if (type == WTCONV_F16)
-        a = squares_of<_Float16>(t.in[i], e, end);
+        a = squares_of<_Float16>(in, e, end);
     else
-        a = squares_of<__bf16>(t.in[i], e, end);
+        a = squares_of<__bf16>(in, e, end);
     a = sum_group(a);
-    if (threadIdx.x == 0) parts[t.base + r] = a;
+    if (threadIdx.x == 0) parts[r] = a;
 }
 
 // The sum of n parts on every thread of the workgroup, in the same order in every
@@ -196,21 +229,44 @@ __global__ __launch_bounds__(kThreads) void norm_join(const double *parts, int64
     if (norm) *norm = (float)sqrt(a);
 }
 
-__global__ __launch_bounds__(kThreads) void clip_ranges(Table t, const double *parts, int64_t n, float max_norm,
-                                                        float eps, float *norm)
+template <typename L>
+__global__ __launch_bounds__(kThreads) void clip_ranges(L t, const double *parts, int64_t n, float max_norm, float eps,
+                                                        float *norm)
 {
     const double root = sqrt(total_of(parts, n));
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)root;
     const Scale f = scale_of((double)max_norm / (root + (double)eps));
-    const int r = t.ranges - 1 - blockIdx.x, i = find(t, r), type = (int)(t.elems_type[i] & 3);
-    if (f.two == 1.f && f.f == 1.f && t.in[i] == t.out[i]) return;
-    const int64_t m = t.elems_type[i] >> 2, e = (r - t.first[i]) * t.range, end = m - e < t.range ? m : e + t.range;
+    const int r = t.ranges - 1 - blockIdx.x, i = find(t, r);
+    const void *in = t.in(i);
+    void *out = t.out(i);
+    if (f.two == 1.f && f.f == 1.f && in == out) return;
+    const int64_t et = t.elems_type(i), m = et >> 2, e = (r - t.first(i)) * t.range, end = m - e < t.range ? m : e + t.range;
+    const int type = (int)(et & 3);
     if (type == WTCONV_F32)
-        scale_any<float>(t.in[i], t.out[i], e, end, f);
+        scale_any<float>(in, out, e, end, f);
     else if (type == WTCONV_F16)
-        scale_any<_Float16>(t.in[i], t.out[i], e, end, f);
+        scale_any<_Float16>(in, out, e, end, f);
     else
-        scale_any<__bf16>(t.in[i], t.out[i], e, end, f);
+        scale_any<__bf16>(in, out, e, end, f);
+}
+
+struct Clip {
+    bool clip;
+    float max_norm, eps;
+    float *norm;
+    double *parts, *total;
+};
+
+template <typename L>
+void passes(const L &t, const Clip &c, hipStream_t stream)
+{
+    const dim3 grid((unsigned)t.ranges), block(kThreads);
+    const bool joined = t.ranges > kOwnSums;
+    norm_ranges<L><<<grid, block, 0, stream>>>(t, c.parts);
+    if (!c.clip || joined) norm_join<<<dim3(1), block, 0, stream>>>(c.parts, t.ranges, c.total, c.norm);
+    if (c.clip)
+        clip_ranges<L><<<grid, block, 0, stream>>>(t, joined ? c.total : c.parts, joined ? 1 : t.ranges, c.max_norm, c.eps,
+                                                  joined ? nullptr : c.norm);
 }
 
 }  // namespace
@@ -221,44 +277,46 @@ hipError_t wtc_launch_clip(const wtconv_tensor_t *t, int64_t count, bool clip, f
     int64_t all = 0;
     for (int64_t i = 0; i < count; ++i) all += t[i].elems;
     const int64_t range = range_elems(all);
-    int64_t ranges = 0;
-    // every launch's table, once for the sums and once for the scaling
-    auto each = [&](auto launch) {
-        Table tab;
-        tab.n = 0;
-        tab.ranges = 0;
-        tab.range = range;
-        tab.base = 0;
-        for (int64_t i = 0; i < count; ++i) {
+    const Clip c = {clip, max_norm, eps, norm, parts, parts + kRanges + count};
+    int ranges = 0, n = 0;
+    // f(n-th tensor with elements, its entry)
+    auto each = [&](auto f) {
+        for (int64_t i = 0; i < count; ++i)
             if (t[i].elems) {
-                tab.in[tab.n] = t[i].grad;
-                tab.out[tab.n] = t[i].out;
-                tab.elems_type[tab.n] = t[i].elems * 4 + t[i].dtype;
-                tab.first[tab.n++] = tab.ranges;
-                tab.ranges += (int)((t[i].elems + range - 1) / range);
+                f(n++, Entry{t[i].grad, t[i].out, t[i].elems * 4 + t[i].dtype, ranges});
+                ranges += (int)((t[i].elems + range - 1) / range);
             }
-            if (tab.n == kTensors || (i + 1 == count && tab.n)) {
-                launch(tab);
-                tab.base += tab.ranges;
-                tab.n = tab.ranges = 0;
-            }
-        }
-        ranges = tab.base;
     };
-    each([&](const Table &tab) {
-        norm_ranges<<<dim3((unsigned)tab.ranges), dim3(kThreads), 0, stream>>>(tab, parts);
-    });
-    double *total = parts + kRanges + count;
-    if (!clip || ranges > kOwnSums || !ranges)
-        norm_join<<<dim3(1), dim3(kThreads), 0, stream>>>(parts, ranges, total, norm);
-    if (!clip) return hipGetLastError();
-    const bool joined = ranges > kOwnSums;
-    float *own = joined ? nullptr : norm;
-    const double *from = joined ? total : parts;
-    const int64_t n = joined ? 1 : ranges;
-    each([&](const Table &tab) {
-        clip_ranges<<<dim3((unsigned)tab.ranges), dim3(kThreads), 0, stream>>>(tab, from, n, max_norm, eps, own);
-        own = nullptr;
-    });
+    if (!all) {
+        norm_join<<<dim3(1), dim3(kThreads), 0, stream>>>(parts, 0, nullptr, norm);
+    } else if (count <= kByValue) {
+        Table tab;
+        each([&](int i, const Entry &e) {
+            tab.in_[i] = e.in;
+            tab.out_[i] = e.out;
+            tab.elems_type_[i] = e.elems_type;
+            tab.first_[i] = (int)e.first;
+        });
+        tab.n = n;
+        tab.ranges = ranges;
+        tab.range = range;
+        passes(tab, c, stream);
+    } else {
+        Entry *to = (Entry *)((char *)parts + sums_bytes(count));
+        Entries some;
+        int k = 0;
+        auto flush = [&] {
+            if (k) write_table<<<dim3(1), dim3(128), 0, stream>>>(some, to, k);
+            to += k;
+            k = 0;
+        };
+        const Entry *table = to;
+        each([&](int, const Entry &e) {
+            some.e[k++] = e;
+            if (k == kWritten) flush();
+        });
+        flush();
+        passes(FarTable{table, n, ranges, range}, c, stream);
+    }
     return hipGetLastError();
 }

@@ -9,14 +9,15 @@
 //
 // A thread takes V elements an access, 16 bytes where the addresses allow it.
 // Rows whose length V does not divide start at any place between two such
-// accesses; they are covered by the accesses that touch them, and the first and
-// the last of these go element by element (RAGGED).  Row r's start repeats with
-// period V, and a backward slot takes rows a multiple of V apart, so that its
-// threads keep their columns, and the sums of dgamma stay in registers over all of
-// a slot's rows.
+// accesses (RAGGED): the accesses that lie in the row whole are taken so, and the
+// fewer than V elements in front of them and behind one a thread.  Row r's start
+// repeats with period V, and a backward slot takes rows a multiple of V apart, so
+// that its threads keep their columns, and the sums of dgamma stay in registers over
+// all of a slot's rows.  (With guards at every element of the first and the last
+// access instead, 31 instructions an element: 2049x5003 fp16 backward 59 us.)
 //
 // Numerics.  Values are fp32 from the load on (h first rounded to its type, since
-// that is what the backward pass finds).  A thread sums at most 64 squares, then a
+// that is what the backward pass finds).  A thread sums at most 65 squares, then a
 // tree; longer rows sum in fp64.
 #include <hip/hip_fp16.h>
 #include <hip/hip_runtime.h>
@@ -43,55 +44,73 @@ struct Access<T, 1> {
     typedef T type;
 };
 
-// Elements e .. e + V of p as fp32, those outside [lo, hi) as zeros.
-template <typename T, int V, bool RAGGED>
-__device__ inline void load(const T *p, int64_t e, int64_t lo, int64_t hi, float (&v)[V])
+template <typename T, int V>
+__device__ inline typename Access<T, V>::type fetch(const T *p)
 {
-    if (!RAGGED || (e >= lo && e + V <= hi)) {
-        const typename Access<T, V>::type r = *(const typename Access<T, V>::type *)(p + e);
-        if constexpr (V == 1)
-            v[0] = (float)r;
-        else
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = (float)r[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = e + i >= lo && e + i < hi ? (float)p[e + i] : 0.f;
-    }
+    return *(const typename Access<T, V>::type *)p;
 }
 
-template <typename T, int V, bool RAGGED>
-__device__ inline void store(T *p, int64_t e, int64_t lo, int64_t hi, const float (&v)[V])
+template <typename T, int V>
+__device__ inline void values(const typename Access<T, V>::type &r, float (&v)[V])
 {
-    if (!RAGGED || (e >= lo && e + V <= hi)) {
-        typename Access<T, V>::type r;
-        if constexpr (V == 1)
-            r = (T)v[0];
-        else
+    if constexpr (V == 1)
+        v[0] = (float)r;
+    else
 #pragma unroll
-            for (int i = 0; i < V; ++i) r[i] = (T)v[i];
-        *(typename Access<T, V>::type *)(p + e) = r;
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (e + i >= lo && e + i < hi) p[e + i] = (T)v[i];
-    }
+        for (int i = 0; i < V; ++i) v[i] = (float)r[i];
 }
 
-// gamma of columns c .. c + V, zeros outside the row.
-template <int V, bool RAGGED>
-__device__ inline void weights(const float *gamma, int64_t c, int64_t n, float (&g)[V])
+template <typename T, int V>
+__device__ inline void store(T *p, const float (&v)[V])
 {
+    typename Access<T, V>::type r;
+    if constexpr (V == 1)
+        r = (T)v[0];
+    else
 #pragma unroll
-    for (int i = 0; i < V; ++i) g[i] = !gamma ? 1.f : !RAGGED || (c + i >= 0 && c + i < n) ? gamma[c + i] : 0.f;
+        for (int i = 0; i < V; ++i) r[i] = (T)v[i];
+    *(typename Access<T, V>::type *)p = r;
 }
 
 struct Shape {
     int64_t rows, c;
     int lanes;    // threads of a row, a power of two
-    int per;      // accesses that touch a row, at most
     float eps, inv_c;
 };
+
+// A row in accesses: `head` elements, `whole` accesses of V, the rest.
+struct Parts {
+    int head, whole;
+    int64_t edge;  // the column of this thread's single element, or -1
+};
+
+template <int V, bool RAGGED>
+__device__ inline Parts parts_of_row(const Shape &s, int64_t row, int lane)
+{
+    Parts p = {0, (int)(s.c / V), -1};
+    if (RAGGED) {
+        const int off = (int)(row * s.c % V), head = off ? V - off : 0, rest = (int)((s.c - head) % V);
+        p.head = head;
+        p.whole = (int)((s.c - head) / V);
+        if (lane < head)
+            p.edge = lane;
+        else if (lane - head < rest)
+            p.edge = s.c - rest + (lane - head);
+    }
+    return p;
+}
+
+// gamma of columns c .. c + V.
+template <int V>
+__device__ inline void weights(const float *gamma, int64_t c, float (&g)[V])
+{
+    if (gamma)
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] = gamma[c + i];
+    else
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] = 1.f;
+}
 
 // Sum over the `lanes` threads of a row, on each of them; lds has a float for
 // every wave where they are more than a wave.
@@ -120,11 +139,10 @@ __device__ inline double sum_row(double v, double *lds)
 }
 
 // The sum that is normed, rounded as it is stored.
-template <typename T, int V>
-__device__ inline void add(float (&v)[V], const float (&r)[V])
+template <typename T>
+__device__ inline float add(float x, float r)
 {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = (float)(T)(v[i] + r[i]);
+    return (float)(T)(x + r);
 }
 
 template <typename T, int V, bool RAGGED, int HELD>
@@ -134,42 +152,53 @@ __global__ __launch_bounds__(kThreads) void rms_fwd(Shape s, const T *x, const T
     __shared__ float lds[kThreads / 64];
     const int slots = kThreads / s.lanes, slot = threadIdx.x / s.lanes, lane = threadIdx.x % s.lanes;
     for (int64_t r0 = (int64_t)blockIdx.x * slots; r0 < s.rows; r0 += (int64_t)gridDim.x * slots) {
-        const int64_t row = r0 + slot, lo = row * s.c, hi = row < s.rows ? lo + s.c : lo;
-        const int64_t base = RAGGED ? lo / V * V : lo;
-        float v[HELD][V], ss = 0.f;
+        const int64_t row = r0 + slot, lo = row * s.c;
+        Parts p = parts_of_row<V, RAGGED>(s, row, lane);
+        if (row >= s.rows) p = {0, 0, -1};
+        float v[HELD][V], single = 0.f, ss;
 #pragma unroll
         for (int k = 0; k < HELD; ++k) {
-            const int64_t e = base + (int64_t)(lane + k * s.lanes) * V;
-            if (e < hi) {
-                load<T, V, RAGGED>(x, e, lo, hi, v[k]);
+            const int j = lane + k * s.lanes;
+            if (j < p.whole) {
+                const int64_t e = lo + p.head + (int64_t)j * V;
+                values<T, V>(fetch<T, V>(x + e), v[k]);
                 if (residual) {
                     float q[V];
-                    load<T, V, RAGGED>(residual, e, lo, hi, q);
-                    add<T, V>(v[k], q);
+                    values<T, V>(fetch<T, V>(residual + e), q);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[k][i] = add<T>(v[k][i], q[i]);
                 }
             }
         }
+        if (RAGGED && p.edge >= 0) {
+            single = (float)x[lo + p.edge];
+            if (residual) single = add<T>(single, (float)residual[lo + p.edge]);
+        }
+        ss = single * single;
 #pragma unroll
         for (int k = 0; k < HELD; ++k) {
-            const int64_t e = base + (int64_t)(lane + k * s.lanes) * V;
-            if (e < hi) {
+            const int j = lane + k * s.lanes;
+            if (j < p.whole) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) ss = fmaf(v[k][i], v[k][i], ss);
-                if (residual) store<T, V, RAGGED>(h, e, lo, hi, v[k]);
+                if (residual) store<T, V>(h + lo + p.head + (int64_t)j * V, v[k]);
             }
         }
+        if (RAGGED && residual && p.edge >= 0) h[lo + p.edge] = (T)single;
         const float rs = 1.f / sqrtf(fmaf(sum_row(ss, s.lanes, lds), s.inv_c, s.eps));
 #pragma unroll
         for (int k = 0; k < HELD; ++k) {
-            const int64_t e = base + (int64_t)(lane + k * s.lanes) * V;
-            if (e < hi) {
+            const int j = lane + k * s.lanes;
+            if (j < p.whole) {
+                const int64_t c = p.head + (int64_t)j * V;
                 float g[V];
-                weights<V, RAGGED>(gamma, e - lo, s.c, g);
+                weights<V>(gamma, c, g);
 #pragma unroll
                 for (int i = 0; i < V; ++i) v[k][i] = v[k][i] * rs * g[i];
-                store<T, V, RAGGED>(y, e, lo, hi, v[k]);
+                store<T, V>(y + lo + c, v[k]);
             }
         }
+        if (RAGGED && p.edge >= 0) y[lo + p.edge] = (T)(gamma ? single * rs * gamma[p.edge] : single * rs);
         if (lane == 0 && row < s.rows) rstd[row] = rs;
     }
 }
@@ -181,107 +210,170 @@ __global__ __launch_bounds__(kThreads) void rms_fwd_long(Shape s, const T *x, co
 {
     __shared__ double lds[kThreads / 64];
     for (int64_t row = blockIdx.x; row < s.rows; row += gridDim.x) {
-        const int64_t lo = row * s.c, hi = lo + s.c, start = (RAGGED ? lo / V * V : lo) + threadIdx.x * V;
+        const int64_t lo = row * s.c;
+        const Parts p = parts_of_row<V, RAGGED>(s, row, threadIdx.x);
         double ss = 0.0;
-        for (int64_t e = start; e < hi; e += kThreads * V) {
+        for (int j = threadIdx.x; j < p.whole; j += kThreads) {
+            const int64_t e = lo + p.head + (int64_t)j * V;
             float v[V];
-            load<T, V, RAGGED>(x, e, lo, hi, v);
+            values<T, V>(fetch<T, V>(x + e), v);
             if (residual) {
                 float q[V];
-                load<T, V, RAGGED>(residual, e, lo, hi, q);
-                add<T, V>(v, q);
-                store<T, V, RAGGED>(h, e, lo, hi, v);
+                values<T, V>(fetch<T, V>(residual + e), q);
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = add<T>(v[i], q[i]);
+                store<T, V>(h + e, v);
             }
 #pragma unroll
             for (int i = 0; i < V; ++i) ss = fma((double)v[i], (double)v[i], ss);
         }
+        float single = 0.f;
+        if (RAGGED && p.edge >= 0) {
+            single = (float)x[lo + p.edge];
+            if (residual) {
+                single = add<T>(single, (float)residual[lo + p.edge]);
+                h[lo + p.edge] = (T)single;
+            }
+            ss = fma((double)single, (double)single, ss);
+        }
         const float rs = 1.f / sqrtf(fmaf((float)sum_row(ss, lds), s.inv_c, s.eps));
         // a thread finds its own elements of h
         const T *from = residual ? h : x;
-        for (int64_t e = start; e < hi; e += kThreads * V) {
+        for (int j = threadIdx.x; j < p.whole; j += kThreads) {
+            const int64_t c = p.head + (int64_t)j * V;
             float v[V], g[V];
-            load<T, V, RAGGED>(from, e, lo, hi, v);
-            weights<V, RAGGED>(gamma, e - lo, s.c, g);
+            values<T, V>(fetch<T, V>(from + lo + c), v);
+            weights<V>(gamma, c, g);
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = v[i] * rs * g[i];
-            store<T, V, RAGGED>(y, e, lo, hi, v);
+            store<T, V>(y + lo + c, v);
         }
+        if (RAGGED && p.edge >= 0) y[lo + p.edge] = (T)(gamma ? single * rs * gamma[p.edge] : single * rs);
         if (threadIdx.x == 0) rstd[row] = rs;
     }
 }
 
-// dx, and dgamma's sums of this workgroup's rows: parts[blockIdx.x][c].
+// dx of an element.
+__device__ inline float back(float h, float dy, float g, float rs, float mean)
+{
+    return rs * fmaf(-(h * rs), mean, dy * g);
+}
+
+// dx, and dgamma's sums of this workgroup's rows: parts[blockIdx.x][c].  A row's loads
+// are sent off before the row in front of it is summed.
 template <typename T, int V, bool RAGGED, int HELD>
 __global__ __launch_bounds__(kThreads) void rms_bwd(Shape s, const T *h, const T *dy, const T *dh, const float *gamma,
                                                     const float *rstd, T *dx, float *parts)
 {
+    typedef typename Access<T, V>::type A;
     __shared__ float lds[kThreads / 64];
     extern __shared__ float sums[];  // [c], where dgamma is asked for
     const int slots = kThreads / s.lanes, slot = threadIdx.x / s.lanes, lane = threadIdx.x % s.lanes;
-    const int64_t first = (int64_t)blockIdx.x * slots + slot;  // this slot's first row; the others a multiple of V on
-    const int64_t shift = RAGGED ? first * s.c % V : 0;        // elements in front of the row in its first access
-    float acc[HELD][V], g[HELD][V];
+    // this slot's first row; the others are a multiple of V further, with the same parts
+    const int64_t first = (int64_t)blockIdx.x * slots + slot;
+    const Parts p = parts_of_row<V, RAGGED>(s, first, lane);
+    struct Row {
+        A h[HELD], dy[HELD], dh[HELD];
+        T sh, sdy, sdh;
+        float rs;
+    };
+    auto fetch_row = [&](int64_t row, Row &r) {
+        if (row >= s.rows) return;
+        const int64_t lo = row * s.c + p.head;
+        r.rs = rstd[row];
+#pragma unroll
+        for (int k = 0; k < HELD; ++k) {
+            const int j = lane + k * s.lanes;
+            if (j < p.whole) {
+                const int64_t e = lo + (int64_t)j * V;
+                r.h[k] = fetch<T, V>(h + e);
+                r.dy[k] = fetch<T, V>(dy + e);
+                if (dh) r.dh[k] = fetch<T, V>(dh + e);
+            }
+        }
+        if (RAGGED && p.edge >= 0) {
+            const int64_t e = row * s.c + p.edge;
+            r.sh = h[e];
+            r.sdy = dy[e];
+            if (dh) r.sdh = dh[e];
+        }
+    };
+    Row now, next;
+    fetch_row(first, now);
+    float acc[HELD][V] = {}, single = 0.f, g[HELD][V], gs = 1.f;
 #pragma unroll
     for (int k = 0; k < HELD; ++k) {
-        const int64_t c = (int64_t)(lane + k * s.lanes) * V - shift;
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[k][i] = 0.f;
-        if (c < s.c)
-            weights<V, RAGGED>(gamma, c, s.c, g[k]);
+        const int j = lane + k * s.lanes;
+        if (j < p.whole) weights<V>(gamma, p.head + (int64_t)j * V, g[k]);
     }
-    for (int64_t r0 = (int64_t)blockIdx.x * slots; r0 < s.rows; r0 += (int64_t)gridDim.x * slots) {
-        const int64_t row = r0 + slot, lo = row * s.c, hi = row < s.rows ? lo + s.c : lo, base = lo - shift;
-        const float rs = row < s.rows ? rstd[row] : 0.f;
-        float hv[HELD][V], d[HELD][V], dot = 0.f;
+    if (RAGGED && gamma && p.edge >= 0) gs = gamma[p.edge];
+    const int64_t step = (int64_t)gridDim.x * slots;
+    for (int64_t r0 = (int64_t)blockIdx.x * slots; r0 < s.rows; r0 += step) {
+        const int64_t row = r0 + slot;
+        const bool in = row < s.rows;
+        fetch_row(row + step, next);
+        float dot = 0.f;
+        if (in) {
 #pragma unroll
-        for (int k = 0; k < HELD; ++k) {
-            const int64_t e = base + (int64_t)(lane + k * s.lanes) * V;
-            if (e < hi) {
-                load<T, V, RAGGED>(h, e, lo, hi, hv[k]);
-                load<T, V, RAGGED>(dy, e, lo, hi, d[k]);
-            }
-        }
+            for (int k = 0; k < HELD; ++k)
+                if (lane + k * s.lanes < p.whole) {
+                    float v[V], d[V];
+                    values<T, V>(now.h[k], v);
+                    values<T, V>(now.dy[k], d);
 #pragma unroll
-        for (int k = 0; k < HELD; ++k) {
-            const int64_t e = base + (int64_t)(lane + k * s.lanes) * V;
-            if (e < hi)
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    hv[k][i] *= rs;
-                    acc[k][i] = fmaf(d[k][i], hv[k][i], acc[k][i]);
-                    d[k][i] *= g[k][i];
-                    dot = fmaf(d[k][i], hv[k][i], dot);
+                    for (int i = 0; i < V; ++i) {
+                        v[i] *= now.rs;
+                        acc[k][i] = fmaf(d[i], v[i], acc[k][i]);
+                        dot = fmaf(d[i] * g[k][i], v[i], dot);
+                    }
                 }
+            if (RAGGED && p.edge >= 0) {
+                const float v = (float)now.sh * now.rs;
+                single = fmaf((float)now.sdy, v, single);
+                dot = fmaf((float)now.sdy * gs, v, dot);
+            }
         }
         const float mean = sum_row(dot, s.lanes, lds) * s.inv_c;
+        if (in) {
+            const int64_t lo = row * s.c + p.head;
 #pragma unroll
-        for (int k = 0; k < HELD; ++k) {
-            const int64_t e = base + (int64_t)(lane + k * s.lanes) * V;
-            if (e < hi) {
-                float q[V];
-                if (dh) load<T, V, RAGGED>(dh, e, lo, hi, q);
+            for (int k = 0; k < HELD; ++k) {
+                const int j = lane + k * s.lanes;
+                if (j < p.whole) {
+                    float v[V], d[V], q[V];
+                    values<T, V>(now.h[k], v);
+                    values<T, V>(now.dy[k], d);
+                    if (dh) values<T, V>(now.dh[k], q);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float v = rs * fmaf(-hv[k][i], mean, d[k][i]);
-                    d[k][i] = dh ? v + q[i] : v;
+                    for (int i = 0; i < V; ++i) {
+                        const float w = back(v[i], d[i], g[k][i], now.rs, mean);
+                        d[i] = dh ? w + q[i] : w;
+                    }
+                    store<T, V>(dx + lo + (int64_t)j * V, d);
                 }
-                store<T, V, RAGGED>(dx, e, lo, hi, d[k]);
+            }
+            if (RAGGED && p.edge >= 0) {
+                const float w = back((float)now.sh, (float)now.sdy, gs, now.rs, mean);
+                dx[row * s.c + p.edge] = (T)(dh ? w + (float)now.sdh : w);
             }
         }
+        now = next;
     }
     if (!parts) return;
     // the slots' sums, one after the other
     for (int64_t c = threadIdx.x; c < s.c; c += kThreads) sums[c] = 0.f;
     for (int q = 0; q < slots; ++q) {
         __syncthreads();
-        if (slot == q)
+        if (slot == q) {
 #pragma unroll
             for (int k = 0; k < HELD; ++k) {
-                const int64_t c = (int64_t)(lane + k * s.lanes) * V - shift;
+                const int j = lane + k * s.lanes;
+                if (j < p.whole)
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (c + i >= 0 && c + i < s.c) sums[c + i] += acc[k][i];
+                    for (int i = 0; i < V; ++i) sums[p.head + j * V + i] += acc[k][i];
             }
+            if (RAGGED && p.edge >= 0) sums[p.edge] += single;
+        }
     }
     __syncthreads();
     for (int64_t c = threadIdx.x; c < s.c; c += kThreads) parts[blockIdx.x * s.c + c] = sums[c];
@@ -294,30 +386,41 @@ __global__ __launch_bounds__(kThreads) void rms_bwd_long(Shape s, const T *h, co
 {
     __shared__ double lds[kThreads / 64];
     for (int64_t row = blockIdx.x; row < s.rows; row += gridDim.x) {
-        const int64_t lo = row * s.c, hi = lo + s.c, start = (RAGGED ? lo / V * V : lo) + threadIdx.x * V;
+        const int64_t lo = row * s.c;
+        const Parts p = parts_of_row<V, RAGGED>(s, row, threadIdx.x);
         const float rs = rstd[row];
         double dot = 0.0;
-        for (int64_t e = start; e < hi; e += kThreads * V) {
+        for (int j = threadIdx.x; j < p.whole; j += kThreads) {
+            const int64_t c = p.head + (int64_t)j * V;
             float v[V], d[V], g[V];
-            load<T, V, RAGGED>(h, e, lo, hi, v);
-            load<T, V, RAGGED>(dy, e, lo, hi, d);
-            weights<V, RAGGED>(gamma, e - lo, s.c, g);
+            values<T, V>(fetch<T, V>(h + lo + c), v);
+            values<T, V>(fetch<T, V>(dy + lo + c), d);
+            weights<V>(gamma, c, g);
 #pragma unroll
             for (int i = 0; i < V; ++i) dot = fma((double)(d[i] * g[i]), (double)(v[i] * rs), dot);
         }
+        const float gs = RAGGED && gamma && p.edge >= 0 ? gamma[p.edge] : 1.f;
+        if (RAGGED && p.edge >= 0)
+            dot = fma((double)((float)dy[lo + p.edge] * gs), (double)((float)h[lo + p.edge] * rs), dot);
         const float mean = (float)sum_row(dot, lds) * s.inv_c;
-        for (int64_t e = start; e < hi; e += kThreads * V) {
-            float v[V], d[V], g[V], q[V];
-            load<T, V, RAGGED>(h, e, lo, hi, v);
-            load<T, V, RAGGED>(dy, e, lo, hi, d);
-            weights<V, RAGGED>(gamma, e - lo, s.c, g);
-            if (dh) load<T, V, RAGGED>(dh, e, lo, hi, q);
+        for (int j = threadIdx.x; j < p.whole; j += kThreads) {
+            const int64_t c = p.head + (int64_t)j * V;
+            float v[V], d[V], q[V], g[V];
+            values<T, V>(fetch<T, V>(h + lo + c), v);
+            values<T, V>(fetch<T, V>(dy + lo + c), d);
+            weights<V>(gamma, c, g);
+            if (dh) values<T, V>(fetch<T, V>(dh + lo + c), q);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float w = rs * fmaf(-(v[i] * rs), mean, d[i] * g[i]);
+                const float w = back(v[i], d[i], g[i], rs, mean);
                 d[i] = dh ? w + q[i] : w;
             }
-            store<T, V, RAGGED>(dx, e, lo, hi, d);
+            store<T, V>(dx + lo + c, d);
+        }
+        if (RAGGED && p.edge >= 0) {
+            const int64_t e = lo + p.edge;
+            const float w = back((float)h[e], (float)dy[e], gs, rs, mean);
+            dx[e] = (T)(dh ? w + (float)dh[e] : w);
         }
     }
 }
@@ -336,25 +439,30 @@ __global__ __launch_bounds__(kThreads) void rms_dgamma_long(Shape s, const T *h,
     parts[blockIdx.y * s.c + c] = (float)a;
 }
 
-// dgamma: `n` rows of parts added up, 64 columns a workgroup, 16 threads each.
+// dgamma: `n` rows of parts added up, 32 columns a workgroup, 32 threads each.
 __global__ __launch_bounds__(1024) void rms_join(const float *parts, int64_t n, int64_t c, float *dgamma)
 {
-    __shared__ double lds[16][65];
-    const int x = threadIdx.x & 63, q = threadIdx.x >> 6;
-    const int64_t at = (int64_t)blockIdx.x * 64 + x;
+    __shared__ double lds[32][33];
+    const int x = threadIdx.x & 31, q = threadIdx.x >> 5;
+    const int64_t at = (int64_t)blockIdx.x * 32 + x;
     double a = 0.0;
     if (at < c)
 #pragma unroll 8
-        for (int64_t i = q; i < n; i += 16) a += (double)parts[i * c + at];
+        for (int64_t i = q; i < n; i += 32) a += (double)parts[i * c + at];
     lds[q][x] = a;
     __syncthreads();
     if (q == 0 && at < c) {
-        for (int i = 1; i < 16; ++i) a += lds[i][x];
+        for (int i = 1; i < 32; ++i) a += lds[i][x];
         dgamma[at] = (float)a;
     }
 }
 
 // ---- Host ----------------------------------------------------------------------
+
+// Whether rows of c elements, V an access, have single elements next to whole
+// accesses (a thread each, so that short rows go element by element), and the
+// elements of an access that they take then.
+int access_of(int64_t c, int wide) { return c % wide == 0 || c >= 8 * wide ? wide : 1; }
 
 // The shape for accesses of V elements; held: accesses a thread keeps (0: too
 // long a row for `most`).
@@ -365,29 +473,30 @@ Shape shape_of(const wtconv_rms_desc_t &d, int v, int most, int &held)
     s.c = d.c;
     s.eps = d.eps;
     s.inv_c = (float)(1.0 / (double)d.c);
-    const int64_t per = (d.c + v - 1) / v + (d.c % v ? 1 : 0);
+    const int64_t per = d.c < v ? 1 : d.c / v;
     if (per > (int64_t)most * kThreads) {
         held = 0;
         s.lanes = kThreads;
         return s;
     }
-    s.per = (int)per;
-    // a wave's lanes or fewer with two accesses each, then the workgroup's
-    int lanes = 1;
+    // a wave's lanes or fewer with two accesses each, then the workgroup's; lanes for
+    // the single elements
+    int lanes = d.c % v ? 16 : 1;
     while (lanes < 64 && lanes < per) lanes *= 2;
     if (per > 2 * lanes) lanes = kThreads;
     s.lanes = lanes;
-    held = 1;
-    while ((int64_t)held * lanes < per) held *= 2;
+    held = (int)((per + lanes - 1) / lanes);
+    if (held > 4) held = 8;
     return s;
 }
 
 // Workgroups of the backward pass: rows are shared out evenly, at most kChain
-// of them for each slot unless that is more workgroups than kGroups.
+// of them for each slot unless that is more workgroups than kGroups, and where there
+// are few rows at least 4 (each workgroup writes a row of dgamma's sums).
 int64_t backward_groups(int64_t rows, int slots)
 {
     const int64_t turns = (rows + slots - 1) / slots;
-    int64_t n = turns < kGroups ? turns : kGroups;
+    int64_t n = turns < 256 ? turns : turns / 4 < 256 ? 256 : turns / 4 < kGroups ? turns / 4 : kGroups;
     if ((turns + kChain - 1) / kChain > n) n = (turns + kChain - 1) / kChain;
     return n + (8 - n % 8) % 8;  // a slot's rows are a multiple of 8 apart
 }
@@ -407,7 +516,7 @@ int64_t parts_of(const wtconv_rms_desc_t &d)
 {
     int64_t most = 0;
     const int wide = d.dtype == WTCONV_F32 ? 4 : 8;
-    for (int v : {1, wide}) {
+    for (int v : {1, access_of(d.c, wide)}) {
         int held;
         const Shape s = shape_of(d, v, kMaxHeldBack, held);
         const int64_t n = held ? backward_groups(d.rows, kThreads / s.lanes) : long_ranges(d);
@@ -421,6 +530,7 @@ void with_held(int held, F f)
 {
     if (held == 1) f(std::integral_constant<int, 1>{});
     if (held == 2) f(std::integral_constant<int, 2>{});
+    if (held == 3) f(std::integral_constant<int, 3>{});
     if (held == 4) f(std::integral_constant<int, 4>{});
     if (held == 8) f(std::integral_constant<int, 8>{});
 }
@@ -470,7 +580,7 @@ void backward(const wtconv_rms_desc_t &d, const WtcRmsBackward &a, hipStream_t s
         rms_bwd_long<T, V, RAGGED><<<grid, dim3(kThreads), 0, stream>>>(s, h, dy, dh, a.gamma, a.rstd, (T *)a.dx);
     }
     if (a.dgamma)
-        rms_join<<<dim3((unsigned)((d.c + 63) / 64)), dim3(1024), 0, stream>>>(a.parts, n, d.c, a.dgamma);
+        rms_join<<<dim3((unsigned)((d.c + 31) / 32)), dim3(1024), 0, stream>>>(a.parts, n, d.c, a.dgamma);
 }
 
 // f(V, RAGGED) of these sizes and addresses.
@@ -478,7 +588,7 @@ template <typename T, typename F>
 void with_access(const wtconv_rms_desc_t &d, bool aligned, F f)
 {
     constexpr int V = 16 / sizeof(T);
-    if (!aligned)
+    if (!aligned || access_of(d.c, V) == 1)
         f(std::integral_constant<int, 1>{}, std::false_type{});
     else if (d.c % V)
         f(std::integral_constant<int, V>{}, std::true_type{});
