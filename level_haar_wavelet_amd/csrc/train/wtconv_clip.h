@@ -8,9 +8,11 @@
 
 namespace wtc_clip {
 
-constexpr int64_t kRanges = 2048;   // ranges that the elements are cut into, about
+constexpr int64_t kRanges = 8192;   // ranges that the elements are cut into, about
 constexpr int64_t kLeast = 8192;    // elements of a range at least
-constexpr int64_t kOwnSums = 4096;  // ranges whose sums every workgroup of the clip joins itself
+constexpr int64_t kOwnSums = 2560;  // ranges whose sums every workgroup of the clip joins itself
+constexpr int64_t kStream = 1 << 24;  // elements from which the outputs are larger than the L2s together
+                                      // (414e6 bf16 elements 577 us, with stores past the L2s 548)
 
 // Elements of a range.  A tensor's last range may be shorter, so there are at most
 // kRanges + count of them.

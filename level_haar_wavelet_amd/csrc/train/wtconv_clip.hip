@@ -3,9 +3,10 @@
 //
 // Two passes over the data, both bound by memory: the squares' sums, and the
 // scaling, which cannot begin before the last of them.  The elements of all tensors
-// are cut into about 2048 ranges of the same length; a workgroup sums one, and the
-// scaling's workgroups each add the ranges' sums for themselves (2048 of them: 16 KB
-// out of the L2), in the same order everywhere, which saves a launch between.  The
+// are cut into ranges of the same length, at most about 8192 (with 2048 of them, about as many workgroups
+// as the chip holds, 414e6 elements took 577 us in place of 527: the last few run alone); a workgroup sums one, and the
+// scaling's workgroups each add the ranges' sums for themselves (up to kOwnSums of
+// them: 20 KB out of the L2), in the same order everywhere, which saves a launch between.  The
 // second pass takes the ranges from the last to the first: the 256 MB cache holds
 // the end of what the first read.
 //
@@ -151,7 +152,8 @@ __device__ inline Scale scale_of(double q)
     return {1.f, (float)q};  // NaN stays
 }
 
-template <typename T, int V>
+// STREAM: stores past the L2s, which keep what is still to be read.
+template <typename T, int V, bool STREAM>
 __device__ inline void scale(const T *p, T *o, int64_t e, int64_t end, const Scale &f)
 {
     typedef typename Access<T, V>::type P;
@@ -170,7 +172,12 @@ __device__ inline void scale(const T *p, T *o, int64_t e, int64_t end, const Sca
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = *(const P *)(p + e + k * step);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) *(P *)(o + e + k * step) = times(v[k]);
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (STREAM)
+                __builtin_nontemporal_store(times(v[k]), (P *)(o + e + k * step));
+            else
+                *(P *)(o + e + k * step) = times(v[k]);
+        }
     }
     for (; e + V <= end; e += step) *(P *)(o + e) = times(*(const P *)(p + e));
     if (V > 1)
@@ -184,13 +191,13 @@ __device__ inline double squares_of(const void *p, int64_t e, int64_t end)
     return squares<T, 1>((const T *)p, e, end);
 }
 
-template <typename T>
+template <typename T, bool STREAM>
 __device__ inline void scale_any(const void *p, void *o, int64_t e, int64_t end, const Scale &f)
 {
     if ((((uintptr_t)p | (uintptr_t)o) & 15) == 0)
-        scale<T, 16 / sizeof(T)>((const T *)p, (T *)o, e, end, f);
+        scale<T, 16 / sizeof(T), STREAM>((const T *)p, (T *)o, e, end, f);
     else
-        scale<T, 1>((const T *)p, (T *)o, e, end, f);
+        scale<T, 1, STREAM>((const T *)p, (T *)o, e, end, f);
 }
 
 template <typename L>
@@ -229,7 +236,7 @@ __global__ __launch_bounds__(kThreads) void norm_join(const double *parts, int64
     if (norm) *norm = (float)sqrt(a);
 }
 
-template <typename L>
+template <typename L, bool STREAM>
 __global__ __launch_bounds__(kThreads) void clip_ranges(L t, const double *parts, int64_t n, float max_norm, float eps,
                                                         float *norm)
 {
@@ -243,11 +250,11 @@ __global__ __launch_bounds__(kThreads) void clip_ranges(L t, const double *parts
     const int64_t et = t.elems_type(i), m = et >> 2, e = (r - t.first(i)) * t.range, end = m - e < t.range ? m : e + t.range;
     const int type = (int)(et & 3);
     if (type == WTCONV_F32)
-        scale_any<float>(in, out, e, end, f);
+        scale_any<float, STREAM>(in, out, e, end, f);
     else if (type == WTCONV_F16)
-        scale_any<_Float16>(in, out, e, end, f);
+        scale_any<_Float16, STREAM>(in, out, e, end, f);
     else
-        scale_any<__bf16>(in, out, e, end, f);
+        scale_any<__bf16, STREAM>(in, out, e, end, f);
 }
 
 struct Clip {
@@ -255,6 +262,7 @@ struct Clip {
     float max_norm, eps;
     float *norm;
     double *parts, *total;
+    int64_t elems;
 };
 
 template <typename L>
@@ -264,9 +272,10 @@ void passes(const L &t, const Clip &c, hipStream_t stream)
     const bool joined = t.ranges > kOwnSums;
     norm_ranges<L><<<grid, block, 0, stream>>>(t, c.parts);
     if (!c.clip || joined) norm_join<<<dim3(1), block, 0, stream>>>(c.parts, t.ranges, c.total, c.norm);
-    if (c.clip)
-        clip_ranges<L><<<grid, block, 0, stream>>>(t, joined ? c.total : c.parts, joined ? 1 : t.ranges, c.max_norm, c.eps,
-                                                  joined ? nullptr : c.norm);
+    if (!c.clip) return;
+    auto *k = c.elems >= kStream ? clip_ranges<L, true> : clip_ranges<L, false>;
+    k<<<grid, block, 0, stream>>>(t, joined ? c.total : c.parts, joined ? 1 : t.ranges, c.max_norm, c.eps,
+                                  joined ? nullptr : c.norm);
 }
 
 }  // namespace
@@ -277,7 +286,7 @@ hipError_t wtc_launch_clip(const wtconv_tensor_t *t, int64_t count, bool clip, f
     int64_t all = 0;
     for (int64_t i = 0; i < count; ++i) all += t[i].elems;
     const int64_t range = range_elems(all);
-    const Clip c = {clip, max_norm, eps, norm, parts, parts + kRanges + count};
+    const Clip c = {clip, max_norm, eps, norm, parts, parts + kRanges + count, all};
     int ranges = 0, n = 0;
     // f(n-th tensor with elements, its entry)
     auto each = [&](auto f) {
