@@ -44,7 +44,7 @@ struct Plan {
     int steps, waves;    // its steps of 16 in a row, its waves of 32 rows
     int parts, part_cut; // its workgroups for a tile of rows, and their chunks of 64 columns
     // bytes
-    size_t x, w, grads, wt, bias, part;
+    size_t x, w, grads, bias, part;
 };
 
 // Waves of a workgroup of the kernel for short rows.

@@ -79,7 +79,6 @@ Plan make_plan(const wtconv_gated_desc_t &d)
         p.w = align256((size_t)(d.f * 2 * p.cp) * p.planes * 2);
     }
     p.grads = align256((size_t)(d.rows * 2 * p.fp) * p.planes * 2);
-    p.wt = align256((size_t)(d.c * 2 * p.fp) * p.planes * 2);
     p.bias = align256((size_t)(bias_rows * 2 * p.fp) * 4);
     const size_t px = p.dx.slices > 1 ? (size_t)(p.dx.slices * d.rows * d.c) * 4 : 0;
     const size_t pw = p.dw.slices > 1 ? (size_t)((int64_t)p.dw.slices * 2 * p.fp * d.c) * 4 : 0;
@@ -90,7 +89,7 @@ Plan make_plan(const wtconv_gated_desc_t &d)
 size_t workspace_bytes(const wtconv_gated_desc_t &d, bool backward)
 {
     const Plan p = make_plan(d);
-    if (backward) return p.x + p.w + p.grads + p.wt + p.bias + p.part;
+    if (backward) return p.x + p.w + p.grads + p.bias + p.part;
     return d.rows <= kFewRows ? 0 : p.x + p.w;
 }
 

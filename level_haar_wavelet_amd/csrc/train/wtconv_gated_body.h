@@ -5,9 +5,10 @@
 // sums):
 //   dual   g = x Wg^T and u = x Wu^T side by side, a wave holding both of the same
 //          place, so that act(g) u, or dg and du from dh, are made of registers;
-//   dx     [dg du] [Wg; Wu], over 2 F;
-//   dw     [dg du]^T x, over the rows: both factors lie across the sum's index and
-//          come out of LDS through the transposing reads.
+//   dx     [dg du] [Wg; Wu], over 2 F: the weights lie across the sum's index and come out of
+//          LDS through the transposing reads (as columns laid out anew by a kernel
+//          before, they cost 37 us of 1140 in 8192x2048x5632 bf16);
+//   dw     [dg du]^T x, over the rows: so do both factors.
 // fp32 factors are three bf16 numbers each, which hold all 24 bits, and a product
 // six: those whose size is at least 2^-16 of the first (what is left out is below
 // 2^-23 of the whole).  The fp32 matrix instructions run at 1/16 of the 16-bit rate.
@@ -248,51 +249,11 @@ __global__ __launch_bounds__(256) void gated_pack(const T *__restrict__ src0, co
     }
 }
 
-// The weights' columns as rows: dst[c] = column c of both, g's and u's elements in
-// turn, 2 fp of them, zeros behind f.  One workgroup a 64 x 64 tile.
-template <typename T>
-__global__ __launch_bounds__(256) void gated_turn(const T *__restrict__ w_gate, const T *__restrict__ w_up, int f, int c,
-                                                  int fp, typename Factor<T>::type *__restrict__ dst, int64_t plane)
-{
-    typedef typename Factor<T>::type E;
-    constexpr int P = Factor<T>::kPlanes;
-    __shared__ T tile[2][64][66];
-    const int f0 = blockIdx.y * 64, c0 = blockIdx.x * 64, x = threadIdx.x & 63, y = threadIdx.x >> 6;
-#pragma unroll
-    for (int i = 0; i < 64; i += 4) {
-        const bool in = f0 + y + i < f && c0 + x < c;
-        const int64_t at = (int64_t)(f0 + y + i) * c + c0 + x;
-        tile[0][y + i][x] = in ? w_gate[at] : (T)0.f;
-        tile[1][y + i][x] = in ? w_up[at] : (T)0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 64; i += 4)
-        if (c0 + y + i < c && f0 + x < fp) {
-            Vec<E, 2> o[P];
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                E e[P];
-                const T v = tile[z][x][y + i];
-                if constexpr (P == 1)
-                    e[0] = v;
-                else
-                    split<T, P>(v, e);
-#pragma unroll
-                for (int p = 0; p < P; ++p) o[p][z] = e[p];
-            }
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-                *(Vec<E, 2> *)(dst + p * plane + (int64_t)(c0 + y + i) * 2 * fp + 2 * (f0 + x)) = o[p];
-        }
-}
-
-// ---- Products with both factors' rows along the sum's index ---------------------
+// ---- g and u ---------------------------------------------------------------------
 
 enum Mode {
-    kForward,   // h = act(g + bg) (u + bu)
-    kBackward,  // dg, du (and the biases' sums)
-    kProduct    // the product itself: dx
+    kForward,  // h = act(g + bg) (u + bu)
+    kBackward  // dg, du (and the biases' sums)
 };
 
 template <typename E>
@@ -304,17 +265,15 @@ struct Rows {
 template <typename T>
 struct Nt {
     typedef typename Factor<T>::type E;
-    Rows<E> a, b0, b1;  // rows of A; of B (dual: of the gate's and of the up projection's weights)
+    Rows<E> a, b0, b1;  // rows of x; of the gate's and of the up projection's weights
     int64_t m;
-    int n, k;           // columns (dual: f), length of the sum
+    int n, k;           // columns, length of the sum
     int64_t tm;
-    int tn, slices;
-    int64_t cut;        // stages of a slice
+    int tn;
     int act;
     const float *bias0, *bias1;
     const T *dh;
     T *out;             // [m][n]
-    float *part;        // kProduct cut into slices: [slice][m][n]
     E *grads;           // kBackward: [plane][m][2 fp], dg and du in turn
     int64_t grads_plane;
     int fp;
@@ -491,24 +450,18 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
     static_assert(kA * kTurn == BM && kB * kTurn == BN, "rows are shared out evenly");
     static_assert(kTurn == 32 || kTurn == 64, "see the rows of B");
     constexpr int RM = BM / WM / 32, RN = BN / WN / 32;
-    // columns of a lane that are neighbours: blocks 0 and 1, or (g, u) pairs 0 and 1
-    constexpr int kPair = MODE == kProduct || RN % 4 == 0 ? 2 : 1;
-    static_assert(RN % 2 == 0 && (kPair == 1 || MODE == kProduct || kTurn == 32), "blocks of g and u, or of two columns");
+    constexpr int kPair = RN % 4 == 0 ? 2 : 1;  // neighbouring columns of a lane: (g, u) pairs of blocks
+    static_assert(RN % 2 == 0 && (kPair == 1 || kTurn == 32), "blocks of g and u");
     typedef Factors<E, P, RM, RN> F;
     __shared__ __attribute__((aligned(128))) char lds[NB * kStage];
 
-    const int slice = MODE == kProduct ? blockIdx.y : 0;
     int64_t ti;
     int tj;
     place(blockIdx.x, a.tm, a.tn, ti, tj);
     const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63, lr = lane & 31, lc = lane >> 5;
     const int64_t m0 = ti * BM;
-    const int n0 = tj * (MODE == kProduct ? BN : BN / 2);
+    const int n0 = tj * (BN / 2);
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
-
-    const int64_t all = (a.k + BK - 1) / BK, s0 = slice * a.cut;
-    const int stages = (int)(MODE == kProduct ? (all - s0 < a.cut ? all - s0 : a.cut) : all);
-    const int k0 = (int)(s0 * BK), k1 = k0 + stages * BK < a.k ? k0 + stages * BK : a.k;
 
     // Row `row` of the first of this wave's loads, the i-th kTurn i rows on; a chunk's
     // place depends on the row modulo 16 only.
@@ -517,13 +470,11 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
     const uint32_t apitch = (uint32_t)a.a.pitch * 2, bpitch = (uint32_t)a.b0.pitch * 2;
     const uint32_t alane = row * apitch + chunk * 16;
     // Rows of B in the tile, blocks of 32:
-    //   product            columns 64 i + 2 r, 64 i + 2 r + 1
-    //   g and u, pairs     g and u of 64 i + 2 r, g and u of 64 i + 2 r + 1
-    //   g and u            g and u of 32 i + r
-    const bool odd = kTurn == 64 && wave * kPer >= 32;  // all of this wave's rows are of the second block
-    const uint32_t blane = (kPair * (row % 32) + (MODE == kProduct && odd ? 1 : 0)) * bpitch + chunk * 16;
+    //   pairs   g and u of 64 i + 2 r, g and u of 64 i + 2 r + 1
+    //   else    g and u of 32 i + r
+    const bool odd = kTurn == 64 && wave * kPer >= 32;  // all of this wave's rows are of u
+    const uint32_t blane = kPair * (row % 32) * bpitch + chunk * 16;
     auto first_row = [](int i) {  // of load i
-        if (MODE == kProduct) return kTurn == 32 ? i / 2 * 64 + i % 2 : i * 64;
         if (kPair == 2) return i / 4 * 64 + i / 2 % 2;
         return kTurn == 32 ? i / 2 * 32 : i * 32;
     };
@@ -532,14 +483,14 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
     for (int p = 0; p < P; ++p) {
         da[p] = descriptor(a.a.p + p * a.a.plane + m0 * a.a.pitch, (a.m - m0) * apitch);
         const int64_t first = p * a.b0.plane + (int64_t)n0 * a.b0.pitch, bytes = (int64_t)(a.n - n0) * bpitch;
-        db[p] = descriptor((MODE != kProduct && odd ? a.b1.p : a.b0.p) + first, bytes);
-        dup[p] = MODE != kProduct && kTurn == 32 ? descriptor(a.b1.p + first, bytes) : db[p];
+        db[p] = descriptor((odd ? a.b1.p : a.b0.p) + first, bytes);
+        dup[p] = kTurn == 32 ? descriptor(a.b1.p + first, bytes) : db[p];
     }
     const uint32_t base = lds_offset(lds);
     auto issue = [&](int s, int n) {
-        const int k = k0 + s * BK, p = n / (kA + kB), i = n % (kA + kB);
+        const int k = s * BK, p = n / (kA + kB), i = n % (kA + kB);
         // a row's end inside the stage: zeros, not the next row
-        const bool in = k + chunk * 8 < k1;
+        const bool in = k + chunk * 8 < a.k;
         const uint32_t to = base + s % NB * kStage + wave * 1024;
         if (i < kA)
             load_lds(da[p], in ? alane : kOutside, k * 2 + i * kTurn * apitch, to + p * BM * kRow + i * W * 1024);
@@ -556,134 +507,99 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
             f.a[i - RN][p] = *(const Vec<E, 8> *)(at + (p * BM + wm + (i - RN) * 32) * kRow);
     };
     float16v acc[RM][RN] = {};  // rows: A's, columns: B's
-    ring<NB, BK / 16, P *(kA + kB), P *(RM + RN), Pairs<P>::kCount * RM * RN, P, RM, RN, F>(acc, stages, issue, read);
+    ring<NB, BK / 16, P *(kA + kB), P *(RM + RN), Pairs<P>::kCount * RM * RN, P, RM, RN, F>(acc, (a.k + BK - 1) / BK, issue, read);
 
     // this lane's first row
     const int64_t mine = m0 + wm + 4 * lc;
-    if constexpr (MODE == kProduct) {
-        auto write = [&](auto *out, auto two) {
-            typedef typename std::remove_pointer<decltype(out)>::type O;
-            const Resource to = resource(out + m0 * a.n, (a.m - m0) * a.n * (int)sizeof(O));
+    // dh, or h: kPair neighbours at once where they lie so
+    const T *io = MODE == kForward ? a.out : a.dh;
+    const Resource rio = resource(io + m0 * a.n, (a.m - m0) * a.n * S);
+    with_act(a.act, [&](auto kind) {
 #pragma unroll
-            for (int j = 0; j < RN; j += 2) {
-                const int n = n0 + wn + j * 32 + 2 * lr;
-                const uint32_t at = ((uint32_t)(mine - m0) * a.n + n) * sizeof(O);
+        for (int j = 0; j < RN; j += 2 * kPair) {
+            const int f0 = n0 + wn / 2 + j * 16 + kPair * lr;
+            float bg[kPair], bu[kPair], sg[kPair] = {}, su[kPair] = {};
 #pragma unroll
-                for (int i = 0; i < RM; ++i)
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const uint32_t rows = (i * 32 + row_of(q)) * a.n * (uint32_t)sizeof(O);
-                        const O v0 = (O)acc[i][j][q], v1 = (O)acc[i][j + 1][q];
-                        if constexpr (two) {
-                            put<O, 2>(Vec<O, 2>{v0, v1}, to, n < a.n ? at : kOutside, rows);
-                        } else {
-                            put<O, 1>(Vec<O, 1>{v0}, to, n < a.n ? at : kOutside, rows);
-                            put<O, 1>(Vec<O, 1>{v1}, to, n + 1 < a.n ? at + (uint32_t)sizeof(O) : kOutside, rows);
-                        }
-                    }
+            for (int h = 0; h < kPair; ++h) {
+                bg[h] = a.bias0 && f0 + h < a.n ? a.bias0[f0 + h] : 0.f;
+                bu[h] = a.bias1 && f0 + h < a.n ? a.bias1[f0 + h] : 0.f;
             }
-        };
-        if (a.slices > 1) {
-            float *part = a.part + slice * a.m * a.n;
-            if (a.n % 2 == 0)
-                write(part, std::true_type{});
-            else
-                write(part, std::false_type{});
-        } else if (a.wide)
-            write(a.out, std::true_type{});
-        else
-            write(a.out, std::false_type{});
-    } else {
-        // dh, or h: kPair neighbours at once where they lie so
-        const T *io = MODE == kForward ? a.out : a.dh;
-        const Resource rio = resource(io + m0 * a.n, (a.m - m0) * a.n * S);
-        with_act(a.act, [&](auto kind) {
+            const uint32_t at = ((uint32_t)(mine - m0) * a.n + f0) * S;
+            const uint32_t at0 = f0 < a.n ? at : kOutside, at1 = f0 + 1 < a.n ? at + S : kOutside;
 #pragma unroll
-            for (int j = 0; j < RN; j += 2 * kPair) {
-                const int f0 = n0 + wn / 2 + j * 16 + kPair * lr;
-                float bg[kPair], bu[kPair], sg[kPair] = {}, su[kPair] = {};
-#pragma unroll
-                for (int h = 0; h < kPair; ++h) {
-                    bg[h] = a.bias0 && f0 + h < a.n ? a.bias0[f0 + h] : 0.f;
-                    bu[h] = a.bias1 && f0 + h < a.n ? a.bias1[f0 + h] : 0.f;
-                }
-                const uint32_t at = ((uint32_t)(mine - m0) * a.n + f0) * S;
-                const uint32_t at0 = f0 < a.n ? at : kOutside, at1 = f0 + 1 < a.n ? at + S : kOutside;
-#pragma unroll
-                for (int i = 0; i < RM; ++i) {
-                    Vec<T, kPair> d[16];
-                    if constexpr (MODE == kBackward)
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) {
-                            const uint32_t rows = (i * 32 + row_of(q)) * a.n * S;
-                            if (kPair == 1 || a.wide) {
-                                d[q] = get<T, kPair>(rio, at0, rows);
-                            } else {
-                                d[q][0] = get<T, 1>(rio, at0, rows)[0];
-                                d[q][kPair - 1] = get<T, 1>(rio, at1, rows)[0];
-                            }
-                        }
+            for (int i = 0; i < RM; ++i) {
+                Vec<T, kPair> d[16];
+                if constexpr (MODE == kBackward)
 #pragma unroll
                     for (int q = 0; q < 16; ++q) {
-                        float g[kPair], u[kPair];
-#pragma unroll
-                        for (int h = 0; h < kPair; ++h) {
-                            g[h] = acc[i][j + 2 * h][q] + bg[h];
-                            u[h] = acc[i][j + 2 * h + 1][q] + bu[h];
-                        }
-                        if constexpr (MODE == kForward) {
-                            const uint32_t rows = (i * 32 + row_of(q)) * a.n * S;
-                            Vec<T, kPair> o;
-#pragma unroll
-                            for (int h = 0; h < kPair; ++h) o[h] = (T)(act<kind>(g[h]) * u[h]);
-                            if (kPair == 1 || a.wide) {
-                                put<T, kPair>(o, rio, at0, rows);
-                            } else {
-                                put<T, 1>(Vec<T, 1>{o[0]}, rio, at0, rows);
-                                put<T, 1>(Vec<T, 1>{o[kPair - 1]}, rio, at1, rows);
-                            }
+                        const uint32_t rows = (i * 32 + row_of(q)) * a.n * S;
+                        if (kPair == 1 || a.wide) {
+                            d[q] = get<T, kPair>(rio, at0, rows);
                         } else {
-                            // columns and rows behind the last: dh is zero there
-                            Vec<E, 2 * kPair> o[P];
-#pragma unroll
-                            for (int h = 0; h < kPair; ++h) {
-                                float slope;
-                                const float y = act_slope<kind>(g[h], slope), dv = (float)d[q][h];
-                                const float dg = dv * u[h] * slope, du = dv * y;
-                                sg[h] += dg;
-                                su[h] += du;
-                                E eg[P], eu[P];
-                                split<T, P>(dg, eg);
-                                split<T, P>(du, eu);
-#pragma unroll
-                                for (int p = 0; p < P; ++p) {
-                                    o[p][2 * h] = eg[p];
-                                    o[p][2 * h + 1] = eu[p];
-                                }
-                            }
-#pragma unroll
-                            for (int p = 0; p < P; ++p)
-                                put<E, 2 * kPair>(o[p], resource(a.grads + p * a.grads_plane + m0 * 2 * a.fp,
-                                                                 (a.m - m0) * 4 * a.fp),
-                                                  f0 < a.fp ? ((uint32_t)(mine - m0) * a.fp + f0) * 4 : kOutside,
-                                                  (i * 32 + row_of(q)) * a.fp * 4);
+                            d[q][0] = get<T, 1>(rio, at0, rows)[0];
+                            d[q][kPair - 1] = get<T, 1>(rio, at1, rows)[0];
                         }
                     }
-                    __builtin_amdgcn_sched_barrier(0);  // fewer values live at once
-                }
-                if (MODE == kBackward && a.bias_part)
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    float g[kPair], u[kPair];
 #pragma unroll
                     for (int h = 0; h < kPair; ++h) {
-                        const float g = sg[h] + __shfl_xor(sg[h], 32), u = su[h] + __shfl_xor(su[h], 32);
-                        if (!lc && f0 + h < a.n) {
-                            float *out = a.bias_part + (ti * WM + wave / WN) * 2 * a.fp + f0 + h;
-                            out[0] = g;
-                            out[a.fp] = u;
-                        }
+                        g[h] = acc[i][j + 2 * h][q] + bg[h];
+                        u[h] = acc[i][j + 2 * h + 1][q] + bu[h];
                     }
+                    if constexpr (MODE == kForward) {
+                        const uint32_t rows = (i * 32 + row_of(q)) * a.n * S;
+                        Vec<T, kPair> o;
+#pragma unroll
+                        for (int h = 0; h < kPair; ++h) o[h] = (T)(act<kind>(g[h]) * u[h]);
+                        if (kPair == 1 || a.wide) {
+                            put<T, kPair>(o, rio, at0, rows);
+                        } else {
+                            put<T, 1>(Vec<T, 1>{o[0]}, rio, at0, rows);
+                            put<T, 1>(Vec<T, 1>{o[kPair - 1]}, rio, at1, rows);
+                        }
+                    } else {
+                        // columns and rows behind the last: dh is zero there
+                        Vec<E, 2 * kPair> o[P];
+#pragma unroll
+                        for (int h = 0; h < kPair; ++h) {
+                            float slope;
+                            const float y = act_slope<kind>(g[h], slope), dv = (float)d[q][h];
+                            const float dg = dv * u[h] * slope, du = dv * y;
+                            sg[h] += dg;
+                            su[h] += du;
+                            E eg[P], eu[P];
+                            split<T, P>(dg, eg);
+                            split<T, P>(du, eu);
+#pragma unroll
+                            for (int p = 0; p < P; ++p) {
+                                o[p][2 * h] = eg[p];
+                                o[p][2 * h + 1] = eu[p];
+                            }
+                        }
+#pragma unroll
+                        for (int p = 0; p < P; ++p)
+                            put<E, 2 * kPair>(o[p], resource(a.grads + p * a.grads_plane + m0 * 2 * a.fp,
+                                                             (a.m - m0) * 4 * a.fp),
+                                              f0 < a.fp ? ((uint32_t)(mine - m0) * a.fp + f0) * 4 : kOutside,
+                                              (i * 32 + row_of(q)) * a.fp * 4);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);  // fewer values live at once
             }
-        });
-    }
+            if (MODE == kBackward && a.bias_part)
+#pragma unroll
+                for (int h = 0; h < kPair; ++h) {
+                    const float g = sg[h] + __shfl_xor(sg[h], 32), u = su[h] + __shfl_xor(su[h], 32);
+                    if (!lc && f0 + h < a.n) {
+                        float *out = a.bias_part + (ti * WM + wave / WN) * 2 * a.fp + f0 + h;
+                        out[0] = g;
+                        out[a.fp] = u;
+                    }
+                }
+        }
+    });
 }
 
 }  // namespace wtc_gated
@@ -691,6 +607,139 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
 #include "wtconv_gated_short.h"
 
 namespace wtc_gated {
+
+// ---- dx ------------------------------------------------------------------------------
+
+template <typename T>
+struct Nn {
+    typedef typename Factor<T>::type E;
+    const E *a;            // [plane][m][2 fp], dg and du in turn
+    int64_t a_plane;
+    Rows<E> gate, up;      // [plane][f][c]
+    int64_t m;
+    int n, f, fp;          // columns: c
+    int64_t tm;
+    int tn, slices;
+    int64_t cut;           // stages of a slice
+    T *out;                // [m][n]
+    float *part;           // [slice][m][n]
+};
+
+// What a lane gives the transposing read of 16 rows of the sum's index and 32 columns:
+// 16 lanes take 4 rows of 32 bytes, and a lane gets its column's values of the four;
+// rows lc 8 + 4 h + trow (h: the first and the second read).
+struct Transposed {
+    int trow, tcol;
+};
+__device__ inline Transposed transposed(int lane)
+{
+    return {(lane & 15) >> 2, ((lane >> 4) & 1) * 16 + (lane & 3) * 4};
+}
+
+__device__ inline short4v read_transposed(const char *p)
+{
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v *)p);
+}
+
+// D = A [Wg; Wu], rows of the weights in turn, as the columns of A.  A's rows lie in LDS as
+// in gated_nt.  A stage's rows of Wg come first, then those of Wu; their 32-byte pieces
+// are permuted so that the four rows of a read, two of each, lie in different banks.
+template <typename T, int BM, int BN, int WM, int WN, int BK, int NB>
+__global__ __launch_bounds__(WM *WN * 64, 1) void gated_nn(Nn<T> a)
+{
+    typedef typename Factor<T>::type E;
+    constexpr int P = Factor<T>::kPlanes, W = WM * WN;
+    constexpr int kRow = BK * 2, kChunks = kRow / 16, kRowB = BN * 2;  // bytes
+    constexpr int kStageA = BM * P * kRow, kStage = kStageA + BK * P * kRowB;
+    constexpr int kPer = 1024 / kRow, kTurn = kPer * W, kA = BM / kTurn;
+    constexpr int kPerB = 1024 / kRowB, kTurnB = kPerB * W, kB = BK / kTurnB;
+    static_assert(kA * kTurn == BM && kB * kTurnB == BK && BK / 2 % kTurnB == 0, "rows are shared out evenly");
+    constexpr int RM = BM / WM / 32, RN = BN / WN / 32;
+    typedef Factors<E, P, RM, RN> F;
+    __shared__ __attribute__((aligned(128))) char lds[NB * kStage];
+
+    int64_t ti;
+    int tj;
+    place(blockIdx.x, a.tm, a.tn, ti, tj);
+    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63, lr = lane & 31, lc = lane >> 5;
+    const int64_t m0 = ti * BM;
+    const int n0 = tj * BN, slice = blockIdx.y;
+    const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
+    const int64_t all = (2 * a.fp + BK - 1) / BK, s0 = slice * a.cut;
+    const int stages = (int)(all - s0 < a.cut ? all - s0 : a.cut);
+    const int k0 = (int)(s0 * BK), k1 = k0 + stages * BK < 2 * a.fp ? k0 + stages * BK : 2 * a.fp;
+
+    auto swizzle = [](int r) { return kChunks == 8 ? (r >> 1) & 7 : (r >> 2) & 3; };
+    const int row = wave * kPer + lane / kChunks, chunk = (lane % kChunks) ^ swizzle(row);
+    const uint32_t apitch = (uint32_t)a.fp * 4, bpitch = (uint32_t)a.gate.pitch * 2;
+    const uint32_t alane = row * apitch + chunk * 16;
+    const int brow = wave * kPerB + lane / (kRowB / 16), bchunk = lane % (kRowB / 16);
+    auto key = [](int r, int up) { return ((r & 1) * 2 + up) * 2; };  // of the 32-byte pieces
+    uint32_t blane[2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) blane[z] = brow * bpitch + ((((bchunk >> 1) ^ key(brow, z)) * 2) + (bchunk & 1)) * 16;
+    const uint32_t base = lds_offset(lds);
+    auto issue = [&](int s, int n) {
+        const int k = k0 + s * BK, p = n / (kA + kB), i = n % (kA + kB);
+        const uint32_t to = base + s % NB * kStage + wave * 1024;
+        if (i < kA) {
+            const bool in = k + chunk * 8 < k1;
+            load_lds(descriptor(a.a + p * a.a_plane + m0 * 2 * a.fp, (a.m - m0) * apitch), in ? alane : kOutside,
+                     k * 2 + i * kTurn * apitch, to + p * BM * kRow + i * W * 1024);
+        } else {
+            // columns behind a row's end come out of the next row, into results that nobody takes;
+            // behind the last row, and behind this slice's, there are zeros
+            const int j = i - kA, z = j >= kB / 2, f = k / 2 + (j - z * (kB / 2)) * kTurnB;
+            const Rows<E> &w = z ? a.up : a.gate;
+            const int end = k1 / 2 < a.f ? k1 / 2 : a.f;
+            load_lds(descriptor(w.p + p * w.plane + (int64_t)f * w.pitch + n0, (int64_t)(end - f) * bpitch - n0 * 2), blane[z],
+                     0, to + kStageA + p * BK * kRowB + j * W * 1024);
+        }
+    };
+    const Transposed tr = transposed(lane);
+    auto read = [&](int s, int kk, int n, F &f) {
+        const char *la = lds + s % NB * kStage, *lb = la + kStageA;
+        const int p = n % P, i = n / P;
+        if (i < RN) {
+            union {
+                short4v h[2];
+                Vec<E, 8> f;
+            } r;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int up = tr.trow & 1, own = kk * 8 + lc * 4 + h * 2 + (tr.trow >> 1), c = wn + i * 32 + tr.tcol;
+                r.h[h] = read_transposed(lb + p * BK * kRowB + (up * (BK / 2) + own) * kRowB +
+                                         (((c >> 4) ^ key(own, up)) * 32) + (c & 15) * 2);
+            }
+            f.b[i][p] = r.f;
+        } else {
+            f.a[i - RN][p] = *(const Vec<E, 8> *)(la + (p * BM + wm + (i - RN) * 32 + lr) * kRow +
+                                                  (((kk * 2 + lc) ^ swizzle(lr)) * 16));
+        }
+    };
+    float16v acc[RM][RN] = {};
+    ring<NB, BK / 16, P *(kA + kB), P *(RM + RN), Pairs<P>::kCount * RM * RN, P, RM, RN, F>(acc, stages, issue, read);
+
+    auto write = [&](auto *out) {
+        typedef typename std::remove_pointer<decltype(out)>::type O;
+        const Resource to = resource(out + m0 * a.n, (a.m - m0) * a.n * (int)sizeof(O));
+#pragma unroll
+        for (int i = 0; i < RM; ++i)
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+#pragma unroll
+                for (int j = 0; j < RN; ++j) {
+                    const int n = n0 + wn + j * 32 + lr;
+                    put<O, 1>(Vec<O, 1>{(O)acc[i][j][q]}, to,
+                              n < a.n ? ((uint32_t)(wm + 4 * lc) * a.n + n) * (uint32_t)sizeof(O) : kOutside,
+                              (i * 32 + row_of(q)) * a.n * (uint32_t)sizeof(O));
+                }
+    };
+    if (a.slices > 1)
+        write(a.part + slice * a.m * a.n);
+    else
+        write(a.out);
+}
 
 // ---- The weights' gradients -------------------------------------------------------
 
@@ -760,7 +809,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_tn(Tn<T> a)
                      (i - kA) * W * kPerB * bpitch, to + kStageA + p * BK * kRowB + (i - kA) * W * 1024);
     };
     // rows k .. k + 8 (by lc) of columns col .. col + 32
-    const int trow = lc * 8 + ((lane & 15) >> 2), tcol = ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+    const Transposed tr = transposed(lane);
     auto frag = [&](const char *from, int bytes, int k, int col) {
         union {
             short4v h[2];
@@ -768,9 +817,9 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_tn(Tn<T> a)
         } r;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int c = col + tcol;
-            const char *p = from + (k + trow + 4 * h) * bytes + (((c >> 4) ^ ((trow & 3) * 2)) * 32) + (c & 15) * 2;
-            r.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v *)p);
+            const int c = col + tr.tcol;
+            r.h[h] = read_transposed(from + (k + lc * 8 + tr.trow + 4 * h) * bytes + (((c >> 4) ^ (tr.trow * 2)) * 32) +
+                                     (c & 15) * 2);
         }
         return r.f;
     };
@@ -952,18 +1001,32 @@ void launch_nt(const Tiles &t, Nt<T> &a, hipStream_t stream)
 {
     a.tm = t.tm;
     a.tn = t.tn;
+    const dim3 grid((unsigned)(t.tm * t.tn));
+    if constexpr (Factor<T>::kPlanes == 1) {
+        if (t.bm == 256)
+            gated_nt<T, 256, 256, 2, 2, 64, 2, MODE><<<grid, dim3(256), 0, stream>>>(a);
+        else
+            gated_nt<T, 128, 128, 4, 1, 64, 2, MODE><<<grid, dim3(256), 0, stream>>>(a);
+    } else {
+        gated_nt<T, 128, 128, 2, 2, 32, 3, MODE><<<grid, dim3(256), 0, stream>>>(a);
+    }
+}
+
+template <typename T>
+void launch_nn(const Tiles &t, Nn<T> &a, hipStream_t stream)
+{
+    a.tm = t.tm;
+    a.tn = t.tn;
     a.slices = t.slices;
     a.cut = t.cut;
     const dim3 grid((unsigned)(t.tm * t.tn), (unsigned)t.slices);
     if constexpr (Factor<T>::kPlanes == 1) {
         if (t.bm == 256)
-            gated_nt<T, 256, 256, 2, 2, 64, 2, MODE><<<grid, dim3(256), 0, stream>>>(a);
-        else if constexpr (MODE == kProduct)
-            gated_nt<T, 128, 128, 2, 2, 64, 2, MODE><<<grid, dim3(256), 0, stream>>>(a);
+            gated_nn<T, 256, 256, 2, 2, 64, 2><<<grid, dim3(256), 0, stream>>>(a);
         else
-            gated_nt<T, 128, 128, 4, 1, 64, 2, MODE><<<grid, dim3(256), 0, stream>>>(a);
+            gated_nn<T, 128, 128, 2, 2, 64, 2><<<grid, dim3(256), 0, stream>>>(a);
     } else {
-        gated_nt<T, 128, 128, 2, 2, 32, 3, MODE><<<grid, dim3(256), 0, stream>>>(a);
+        gated_nn<T, 128, 128, 2, 2, 32, 3><<<grid, dim3(256), 0, stream>>>(a);
     }
 }
 
@@ -1129,8 +1192,8 @@ hipError_t backward(const wtconv_gated_desc_t &d, const Backward &a, void *works
     char *ws = (char *)workspace;
     const bool brief = short_rows<T>(d, pl, a.x, a.dh);
     const Operands<T> o = operands<T>(d, pl, a.x, a.w_gate, a.w_up, !brief || a.dw_gate, ws, stream);
-    E *grads = (E *)ws, *wt = (E *)(ws + pl.grads);
-    float *bias = (float *)(ws + pl.grads + pl.wt), *part = (float *)(ws + pl.grads + pl.wt + pl.bias);
+    E *grads = (E *)ws;
+    float *bias = (float *)(ws + pl.grads), *part = (float *)(ws + pl.grads + pl.bias);
     const int64_t gplane = d.rows * 2 * pl.fp;
     int64_t bias_rows;
     if (brief) {
@@ -1169,19 +1232,18 @@ hipError_t backward(const wtconv_gated_desc_t &d, const Backward &a, void *works
         gated_bias<T><<<dim3((unsigned)((d.f + 63) / 64), 2), dim3(1024), 0, stream>>>(bias, bias_rows, (int)d.f, pl.fp,
                                                                                     a.db_gate, a.db_up);
     if (a.dx) {
-        const int64_t plane = d.c * 2 * pl.fp;
-        gated_turn<T><<<dim3((unsigned)((d.c + 63) / 64), (unsigned)((pl.fp + 63) / 64)), dim3(256), 0, stream>>>(
-            (const T *)a.w_gate, (const T *)a.w_up, (int)d.f, (int)d.c, pl.fp, wt, plane);
-        Nt<T> q = {};
-        q.a = {grads, gplane, 2 * pl.fp};
-        q.b0 = {wt, plane, 2 * pl.fp};
+        Nn<T> q = {};
+        q.a = grads;
+        q.a_plane = gplane;
+        q.gate = o.gate;
+        q.up = o.up;
         q.m = d.rows;
         q.n = (int)d.c;
-        q.k = 2 * pl.fp;
+        q.f = (int)d.f;
+        q.fp = pl.fp;
         q.out = (T *)a.dx;
-        q.wide = wide2<T>(a.dx, d.c);
         q.part = part;
-        launch_nt<T, kProduct>(pl.dx, q, stream);
+        launch_nn<T>(pl.dx, q, stream);
         const int64_t size = d.rows * d.c;
         if (pl.dx.slices > 1)
             gated_join<T><<<dim3(blocks_of(size, 4096)), dim3(256), 0, stream>>>(part, pl.dx.slices, size, (T *)a.dx);
