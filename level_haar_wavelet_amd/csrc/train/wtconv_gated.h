@@ -25,13 +25,14 @@ struct Backward {
     float *db_gate, *db_up;
 };
 
-// A product's tile (side of the rows, of the columns) and its cut along k into
-// `slices` of `cut` stages each.
+// A product's tile (side of the rows, of the columns), and its cut along the sum's
+// index into `slices` of `cut` stages, whose sums are joined.
 struct Tiles {
     int bm, bn;
     int64_t tm;
     int tn, slices;
     int64_t cut;
+    int64_t groups() const { return tm * tn * slices; }
 };
 
 // The calls' plan, a function of the sizes and types alone.

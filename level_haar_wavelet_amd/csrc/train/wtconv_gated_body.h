@@ -514,32 +514,43 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
     // dh, or h: kPair neighbours at once where they lie so
     const T *io = MODE == kForward ? a.out : a.dh;
     const Resource rio = resource(io + m0 * a.n, (a.m - m0) * a.n * S);
+    constexpr int kSets = RN / (2 * kPair);  // of blocks with the same columns of a lane
+    auto column = [&](int set) { return n0 + wn / 2 + set * kPair * 32 + kPair * lr; };
+    auto place_of = [&](int f) { return ((uint32_t)(mine - m0) * a.n + f) * S; };
+    // dh of a block of rows is sent for before the one in front of it is used: with one wave
+    // a SIMD there is nothing else to do while it comes
+    Vec<T, kPair> d[2][16];
+    auto fetch = [&](int n) {
+        const int f = column(n / RM), i = n % RM;
+        const uint32_t at0 = f < a.n ? place_of(f) : kOutside, at1 = f + 1 < a.n ? place_of(f + 1) : kOutside;
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+            const uint32_t rows = (i * 32 + row_of(q)) * a.n * S;
+            if (kPair == 1 || a.wide) {
+                d[n & 1][q] = get<T, kPair>(rio, at0, rows);
+            } else {
+                d[n & 1][q][0] = get<T, 1>(rio, at0, rows)[0];
+                d[n & 1][q][kPair - 1] = get<T, 1>(rio, at1, rows)[0];
+            }
+        }
+    };
+    if (MODE == kBackward) fetch(0);
     with_act(a.act, [&](auto kind) {
 #pragma unroll
-        for (int j = 0; j < RN; j += 2 * kPair) {
-            const int f0 = n0 + wn / 2 + j * 16 + kPair * lr;
+        for (int set = 0; set < kSets; ++set) {
+            const int f = column(set), j = set * 2 * kPair;
             float bg[kPair], bu[kPair], sg[kPair] = {}, su[kPair] = {};
 #pragma unroll
             for (int h = 0; h < kPair; ++h) {
-                bg[h] = a.bias0 && f0 + h < a.n ? a.bias0[f0 + h] : 0.f;
-                bu[h] = a.bias1 && f0 + h < a.n ? a.bias1[f0 + h] : 0.f;
+                bg[h] = a.bias0 && f + h < a.n ? a.bias0[f + h] : 0.f;
+                bu[h] = a.bias1 && f + h < a.n ? a.bias1[f + h] : 0.f;
             }
-            const uint32_t at = ((uint32_t)(mine - m0) * a.n + f0) * S;
-            const uint32_t at0 = f0 < a.n ? at : kOutside, at1 = f0 + 1 < a.n ? at + S : kOutside;
+            const uint32_t at0 = f < a.n ? place_of(f) : kOutside, at1 = f + 1 < a.n ? place_of(f + 1) : kOutside;
+            const uint32_t to = f < a.fp ? ((uint32_t)(mine - m0) * a.fp + f) * 4 : kOutside;
 #pragma unroll
             for (int i = 0; i < RM; ++i) {
-                Vec<T, kPair> d[16];
-                if constexpr (MODE == kBackward)
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const uint32_t rows = (i * 32 + row_of(q)) * a.n * S;
-                        if (kPair == 1 || a.wide) {
-                            d[q] = get<T, kPair>(rio, at0, rows);
-                        } else {
-                            d[q][0] = get<T, 1>(rio, at0, rows)[0];
-                            d[q][kPair - 1] = get<T, 1>(rio, at1, rows)[0];
-                        }
-                    }
+                const int n = set * RM + i;
+                if (MODE == kBackward && n + 1 < kSets * RM) fetch(n + 1);
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
                     float g[kPair], u[kPair];
@@ -565,7 +576,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
 #pragma unroll
                         for (int h = 0; h < kPair; ++h) {
                             float slope;
-                            const float y = act_slope<kind>(g[h], slope), dv = (float)d[q][h];
+                            const float y = act_slope<kind>(g[h], slope), dv = (float)d[n & 1][q][h];
                             const float dg = dv * u[h] * slope, du = dv * y;
                             sg[h] += dg;
                             su[h] += du;
@@ -582,18 +593,17 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
                         for (int p = 0; p < P; ++p)
                             put<E, 2 * kPair>(o[p], resource(a.grads + p * a.grads_plane + m0 * 2 * a.fp,
                                                              (a.m - m0) * 4 * a.fp),
-                                              f0 < a.fp ? ((uint32_t)(mine - m0) * a.fp + f0) * 4 : kOutside,
-                                              (i * 32 + row_of(q)) * a.fp * 4);
+                                              to, (i * 32 + row_of(q)) * a.fp * 4);
                     }
+                    if (q % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // fewer values live at once
                 }
-                __builtin_amdgcn_sched_barrier(0);  // fewer values live at once
             }
             if (MODE == kBackward && a.bias_part)
 #pragma unroll
                 for (int h = 0; h < kPair; ++h) {
                     const float g = sg[h] + __shfl_xor(sg[h], 32), u = su[h] + __shfl_xor(su[h], 32);
-                    if (!lc && f0 + h < a.n) {
-                        float *out = a.bias_part + (ti * WM + wave / WN) * 2 * a.fp + f0 + h;
+                    if (!lc && f + h < a.n) {
+                        float *out = a.bias_part + (ti * WM + wave / WN) * 2 * a.fp + f + h;
                         out[0] = g;
                         out[a.fp] = u;
                     }
@@ -608,6 +618,60 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
 
 namespace wtc_gated {
 
+// ---- Tiles that are cut along the sum's index ------------------------------------------
+
+struct Cut {
+    int64_t tm;
+    int tn, slices;
+    int64_t stages;  // of a slice
+    float *part;     // [tile][slice][bm][bn], where there are several
+};
+
+// Tile and slice (or -1) of workgroup g.
+__device__ inline int place(const Cut &c, int64_t g, int64_t &ti, int &tj, int64_t &tile)
+{
+    tile = g / c.slices;
+    place(tile, c.tm, c.tn, ti, tj);
+    return c.slices > 1 ? (int)(g % c.slices) : -1;
+}
+
+// A wave's accumulators to its slice's place; `mine` and `col`: this lane's first row and
+// its column of the first block.
+template <int BM, int BN, int RM, int RN>
+__device__ inline void write_part(const Cut &c, int64_t tile, int slice, const float16v (&acc)[RM][RN], int mine, int col)
+{
+    float *to = c.part + (tile * c.slices + slice) * (BM * BN) + mine * BN + col;
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+#pragma unroll
+            for (int j = 0; j < RN; ++j) to[(i * 32 + row_of(q)) * BN + j * 32] = acc[i][j][q];
+}
+
+// The slices' sums of a tile added up, four columns a thread and 1024 / bn rows a
+// workgroup (blockIdx.y).  dx: [rows][cols] of one matrix; TURNS: rows of g's and u's
+// gradients in turn.
+template <typename T, bool TURNS>
+__global__ __launch_bounds__(256) void gated_join(Cut c, int bm, int bn, int64_t rows, int cols, T *__restrict__ out0,
+                                                  T *__restrict__ out1)
+{
+    int64_t ti;
+    int tj;
+    place(blockIdx.x, c.tm, c.tn, ti, tj);
+    const int e = (blockIdx.y * 256 + threadIdx.x) * 4, col = tj * bn + e % bn;
+    const int64_t row = ti * bm + e / bn, own = TURNS ? row >> 1 : row;
+    if (col >= cols || own >= rows) return;
+    const float *part = c.part + (int64_t)blockIdx.x * c.slices * bm * bn + e;
+    float4v v = {};
+#pragma unroll 8
+    for (int s = 0; s < c.slices; ++s) v += *(const float4v *)(part + (int64_t)s * bm * bn);
+    T *out = (TURNS && (row & 1) ? out1 : out0) + own * cols;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (col + i < cols) out[col + i] = (T)v[i];
+}
+
 // ---- dx ------------------------------------------------------------------------------
 
 template <typename T>
@@ -618,11 +682,8 @@ struct Nn {
     Rows<E> gate, up;      // [plane][f][c]
     int64_t m;
     int n, f, fp;          // columns: c
-    int64_t tm;
-    int tn, slices;
-    int64_t cut;           // stages of a slice
+    Cut cut;
     T *out;                // [m][n]
-    float *part;           // [slice][m][n]
 };
 
 // What a lane gives the transposing read of 16 rows of the sum's index and 32 columns:
@@ -658,15 +719,15 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nn(Nn<T> a)
     typedef Factors<E, P, RM, RN> F;
     __shared__ __attribute__((aligned(128))) char lds[NB * kStage];
 
-    int64_t ti;
+    int64_t ti, tile;
     int tj;
-    place(blockIdx.x, a.tm, a.tn, ti, tj);
+    const int slice = place(a.cut, blockIdx.x, ti, tj, tile);
     const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63, lr = lane & 31, lc = lane >> 5;
     const int64_t m0 = ti * BM;
-    const int n0 = tj * BN, slice = blockIdx.y;
+    const int n0 = tj * BN;
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
-    const int64_t all = (2 * a.fp + BK - 1) / BK, s0 = slice * a.cut;
-    const int stages = (int)(all - s0 < a.cut ? all - s0 : a.cut);
+    const int64_t all = (2 * a.fp + BK - 1) / BK, s0 = slice < 0 ? 0 : slice * a.cut.stages;
+    const int stages = (int)(slice < 0 || all - s0 < a.cut.stages ? all - s0 : a.cut.stages);
     const int k0 = (int)(s0 * BK), k1 = k0 + stages * BK < 2 * a.fp ? k0 + stages * BK : 2 * a.fp;
 
     auto swizzle = [](int r) { return kChunks == 8 ? (r >> 1) & 7 : (r >> 2) & 3; };
@@ -720,25 +781,23 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nn(Nn<T> a)
     float16v acc[RM][RN] = {};
     ring<NB, BK / 16, P *(kA + kB), P *(RM + RN), Pairs<P>::kCount * RM * RN, P, RM, RN, F>(acc, stages, issue, read);
 
-    auto write = [&](auto *out) {
-        typedef typename std::remove_pointer<decltype(out)>::type O;
-        const Resource to = resource(out + m0 * a.n, (a.m - m0) * a.n * (int)sizeof(O));
+    const int mine = wm + 4 * lc;  // this lane's first row of the tile
+    if (slice >= 0) {
+        write_part<BM, BN>(a.cut, tile, slice, acc, mine, wn + lr);
+        return;
+    }
+    const Resource to = resource(a.out + m0 * a.n, (a.m - m0) * a.n * (int)sizeof(T));
 #pragma unroll
-        for (int i = 0; i < RM; ++i)
+    for (int i = 0; i < RM; ++i)
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
+        for (int q = 0; q < 16; ++q)
 #pragma unroll
-                for (int j = 0; j < RN; ++j) {
-                    const int n = n0 + wn + j * 32 + lr;
-                    put<O, 1>(Vec<O, 1>{(O)acc[i][j][q]}, to,
-                              n < a.n ? ((uint32_t)(wm + 4 * lc) * a.n + n) * (uint32_t)sizeof(O) : kOutside,
-                              (i * 32 + row_of(q)) * a.n * (uint32_t)sizeof(O));
-                }
-    };
-    if (a.slices > 1)
-        write(a.part + slice * a.m * a.n);
-    else
-        write(a.out);
+            for (int j = 0; j < RN; ++j) {
+                const int n = n0 + wn + j * 32 + lr;
+                put<T, 1>(Vec<T, 1>{(T)acc[i][j][q]}, to,
+                          n < a.n ? ((uint32_t)mine * a.n + n) * (uint32_t)sizeof(T) : kOutside,
+                          (i * 32 + row_of(q)) * a.n * (uint32_t)sizeof(T));
+            }
 }
 
 // ---- The weights' gradients -------------------------------------------------------
@@ -750,11 +809,8 @@ struct Tn {
     int64_t a_plane, b_plane, b_pitch;
     int64_t m;
     int f, fp, c;
-    int64_t tm;
-    int tn, slices;
-    int64_t cut;     // stages of a slice
+    Cut cut;
     T *gate, *up;    // [f][c]
-    float *part;     // [slice][2 fp][c]
 };
 
 // D = A^T B, a tile of BM columns of A (gradients) and BN of B (x), over a slice
@@ -775,14 +831,14 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_tn(Tn<T> a)
     typedef Factors<E, P, RM, RN> F;
     __shared__ __attribute__((aligned(128))) char lds[NB * kStage];
 
-    int64_t ti;
+    int64_t ti, tile;
     int tj;
-    place(blockIdx.x, a.tm, a.tn, ti, tj);
+    const int slice = place(a.cut, blockIdx.x, ti, tj, tile);
     const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63, lr = lane & 31, lc = lane >> 5;
-    const int f0 = (int)ti * BM, c0 = tj * BN, slice = blockIdx.y;
+    const int f0 = (int)ti * BM, c0 = tj * BN;
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
-    const int64_t all = (a.m + BK - 1) / BK, s0 = slice * a.cut;
-    const int stages = (int)(all - s0 < a.cut ? all - s0 : a.cut);
+    const int64_t all = (a.m + BK - 1) / BK, s0 = slice < 0 ? 0 : slice * a.cut.stages;
+    const int stages = (int)(slice < 0 || all - s0 < a.cut.stages ? all - s0 : a.cut.stages);
 
     const int64_t m1 = (s0 + stages) * BK < a.m ? (s0 + stages) * BK : a.m;
     // A load takes the rows of 1024 bytes, the waves' loads follow each other; where a
@@ -835,80 +891,52 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_tn(Tn<T> a)
     ring<NB, BK / 16, P *(kA + kB), P *(RM + RN), Pairs<P>::kCount * RM * RN, P, RM, RN, F>(acc, stages, issue, read);
 
     const int mine = wm + 4 * lc;  // this lane's first row of the tile
-#pragma unroll
-    for (int j = 0; j < RN; ++j) {
-        const int c = c0 + wn + j * 32 + lr;
-        if (a.slices > 1) {
-            const Resource to = resource(a.part + ((int64_t)slice * 2 * a.fp + f0) * a.c, (int64_t)(2 * a.fp - f0) * a.c * 4);
-            const uint32_t at = c < a.c ? ((uint32_t)mine * a.c + c) * 4 : kOutside;
-#pragma unroll
-            for (int i = 0; i < RM; ++i)
-#pragma unroll
-                for (int q = 0; q < 16; ++q)
-                    put<float, 1>(Vec<float, 1>{acc[i][j][q]}, to, at, (uint32_t)(i * 32 + row_of(q)) * a.c * 4);
-        } else {
-            // rows of g and of u in turn
-            const int64_t first = (int64_t)(f0 / 2) * a.c, bytes = (int64_t)(a.f - f0 / 2) * a.c * (int)sizeof(T);
-            const Resource to[2] = {resource(a.gate + first, bytes), resource(a.up + first, bytes)};
-            const uint32_t at = c < a.c ? ((uint32_t)(mine / 2) * a.c + c) * sizeof(T) : kOutside;
-#pragma unroll
-            for (int i = 0; i < RM; ++i)
-#pragma unroll
-                for (int q = 0; q < 16; ++q)
-                    put<T, 1>(Vec<T, 1>{(T)acc[i][j][q]}, to[q & 1], at,
-                              (uint32_t)((i * 32 + row_of(q)) / 2) * a.c * (uint32_t)sizeof(T));
-        }
+    if (slice >= 0) {
+        write_part<BM, BN>(a.cut, tile, slice, acc, mine, wn + lr);
+        return;
     }
+    // rows of g and of u in turn
+    const int64_t first = (int64_t)(f0 / 2) * a.c, bytes = (int64_t)(a.f - f0 / 2) * a.c * (int)sizeof(T);
+    const Resource to[2] = {resource(a.gate + first, bytes), resource(a.up + first, bytes)};
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+#pragma unroll
+            for (int j = 0; j < RN; ++j) {
+                const int c = c0 + wn + j * 32 + lr;
+                put<T, 1>(Vec<T, 1>{(T)acc[i][j][q]}, to[q & 1],
+                          c < a.c ? ((uint32_t)(mine / 2) * a.c + c) * (uint32_t)sizeof(T) : kOutside,
+                          (uint32_t)((i * 32 + row_of(q)) / 2) * a.c * (uint32_t)sizeof(T));
+            }
 }
 
-// ---- Sums of slices ---------------------------------------------------------------
+// ---- The biases' gradients ------------------------------------------------------------
 
-// out[size] = sum over slices of part[slice][size].
-template <typename T>
-__global__ __launch_bounds__(256) void gated_join(const float *__restrict__ part, int slices, int64_t size,
-                                                  T *__restrict__ out)
-{
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < size; i += (int64_t)gridDim.x * 256) {
-        float v = 0.f;
-#pragma unroll 8
-        for (int s = 0; s < slices; ++s) v += part[s * size + i];
-        out[i] = (T)v;
-    }
-}
-
-// The same for the weights' gradients, whose rows are g's and u's in turn; a workgroup a
-// row of c, blockIdx.y: g, u.
-template <typename T>
-__global__ __launch_bounds__(256) void gated_join_rows(const float *__restrict__ part, int64_t slice, int slices, int c,
-                                                       T *__restrict__ gate, T *__restrict__ up)
-{
-    const float *p = part + ((int64_t)blockIdx.x * 2 + blockIdx.y) * c;
-    T *out = (blockIdx.y ? up : gate) + (int64_t)blockIdx.x * c;
-    for (int i = threadIdx.x; i < c; i += 256) {
-        float v = 0.f;
-#pragma unroll 8
-        for (int s = 0; s < slices; ++s) v += p[s * slice + i];
-        out[i] = (T)v;
-    }
-}
-
-// The biases' gradients: `n` rows of 2 fp sums added up, 64 columns a workgroup, 16
-// threads each; blockIdx.y: gate, up.
+// `n` rows of 2 fp sums added up, 16 columns a workgroup, 64 threads each; blockIdx.y:
+// gate, up.
 template <typename T>
 __global__ __launch_bounds__(1024) void gated_bias(const float *__restrict__ part, int64_t n, int f, int fp,
                                                    float *__restrict__ gate, float *__restrict__ up)
 {
-    __shared__ double lds[16][65];
-    const int x = threadIdx.x & 63, q = threadIdx.x >> 6, at = blockIdx.x * 64 + x;
+    __shared__ double lds[64][17];
+    const int x = threadIdx.x & 15, q = threadIdx.x >> 4, at = blockIdx.x * 16 + x;
     const float *p = part + (blockIdx.y ? fp : 0);
     double a = 0.0;
     if (at < f)
 #pragma unroll 8
-        for (int64_t i = q; i < n; i += 16) a += (double)p[i * 2 * fp + at];
+        for (int64_t i = q; i < n; i += 64) a += (double)p[i * 2 * fp + at];
     lds[q][x] = a;
     __syncthreads();
+    if (q < 8) {
+        a = 0.0;
+        for (int i = 0; i < 8; ++i) a += lds[q * 8 + i][x];
+    }
+    __syncthreads();
+    if (q < 8) lds[q][x] = a;
+    __syncthreads();
     if (q == 0 && at < f) {
-        for (int i = 1; i < 16; ++i) a += lds[i][x];
+        for (int i = 1; i < 8; ++i) a += lds[i][x];
         (blockIdx.y ? up : gate)[at] = (float)a;
     }
 }
@@ -1012,14 +1040,20 @@ void launch_nt(const Tiles &t, Nt<T> &a, hipStream_t stream)
     }
 }
 
-template <typename T>
-void launch_nn(const Tiles &t, Nn<T> &a, hipStream_t stream)
+inline Cut cut_of(const Tiles &t, float *part) { return {t.tm, t.tn, t.slices, t.cut, part}; }
+
+template <typename T, bool TURNS>
+void launch_join(const Tiles &t, const Cut &c, int64_t rows, int64_t cols, void *out0, void *out1, hipStream_t stream)
 {
-    a.tm = t.tm;
-    a.tn = t.tn;
-    a.slices = t.slices;
-    a.cut = t.cut;
-    const dim3 grid((unsigned)(t.tm * t.tn), (unsigned)t.slices);
+    if (t.slices > 1)
+        gated_join<T, TURNS><<<dim3((unsigned)(t.tm * t.tn), (unsigned)(t.bm * t.bn / 1024)), dim3(256), 0, stream>>>(
+            c, t.bm, t.bn, rows, (int)cols, (T *)out0, (T *)out1);
+}
+
+template <typename T>
+void launch_nn(const Tiles &t, const Nn<T> &a, hipStream_t stream)
+{
+    const dim3 grid((unsigned)t.groups());
     if constexpr (Factor<T>::kPlanes == 1) {
         if (t.bm == 256)
             gated_nn<T, 256, 256, 2, 2, 64, 2><<<grid, dim3(256), 0, stream>>>(a);
@@ -1167,13 +1201,9 @@ hipError_t forward(const wtconv_gated_desc_t &d, const Forward &a, void *workspa
 }
 
 template <typename T>
-void launch_tn(const Tiles &t, Tn<T> &a, hipStream_t stream)
+void launch_tn(const Tiles &t, const Tn<T> &a, hipStream_t stream)
 {
-    a.tm = t.tm;
-    a.tn = t.tn;
-    a.slices = t.slices;
-    a.cut = t.cut;
-    const dim3 grid((unsigned)(t.tm * t.tn), (unsigned)t.slices);
+    const dim3 grid((unsigned)t.groups());
     if constexpr (Factor<T>::kPlanes == 1) {
         if (t.bm == 256)
             gated_tn<T, 256, 256, 2, 2, 4><<<grid, dim3(256), 0, stream>>>(a);
@@ -1229,7 +1259,7 @@ hipError_t backward(const wtconv_gated_desc_t &d, const Backward &a, void *works
         launch_nt<T, kBackward>(pl.dual, p, stream);
     }
     if (a.db_gate)
-        gated_bias<T><<<dim3((unsigned)((d.f + 63) / 64), 2), dim3(1024), 0, stream>>>(bias, bias_rows, (int)d.f, pl.fp,
+        gated_bias<T><<<dim3((unsigned)((d.f + 15) / 16), 2), dim3(1024), 0, stream>>>(bias, bias_rows, (int)d.f, pl.fp,
                                                                                     a.db_gate, a.db_up);
     if (a.dx) {
         Nn<T> q = {};
@@ -1242,11 +1272,9 @@ hipError_t backward(const wtconv_gated_desc_t &d, const Backward &a, void *works
         q.f = (int)d.f;
         q.fp = pl.fp;
         q.out = (T *)a.dx;
-        q.part = part;
+        q.cut = cut_of(pl.dx, part);
         launch_nn<T>(pl.dx, q, stream);
-        const int64_t size = d.rows * d.c;
-        if (pl.dx.slices > 1)
-            gated_join<T><<<dim3(blocks_of(size, 4096)), dim3(256), 0, stream>>>(part, pl.dx.slices, size, (T *)a.dx);
+        launch_join<T, false>(pl.dx, q.cut, d.rows, d.c, a.dx, nullptr, stream);
     }
     if (a.dw_gate) {
         Tn<T> q = {};
@@ -1261,11 +1289,9 @@ hipError_t backward(const wtconv_gated_desc_t &d, const Backward &a, void *works
         q.c = (int)d.c;
         q.gate = (T *)a.dw_gate;
         q.up = (T *)a.dw_up;
-        q.part = part;
+        q.cut = cut_of(pl.dw, part);
         launch_tn<T>(pl.dw, q, stream);
-        if (pl.dw.slices > 1)
-            gated_join_rows<T><<<dim3((unsigned)d.f, 2), dim3(256), 0, stream>>>(
-                part, (int64_t)2 * pl.fp * d.c, pl.dw.slices, (int)d.c, (T *)a.dw_gate, (T *)a.dw_up);
+        launch_join<T, true>(pl.dw, q.cut, d.f, d.c, a.dw_gate, a.dw_up, stream);
     }
     return hipGetLastError();
 }
