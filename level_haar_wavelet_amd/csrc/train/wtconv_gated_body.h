@@ -164,11 +164,22 @@ __device__ inline void with_act(int kind, F f)
 
 typedef uint32_t Descriptor __attribute__((ext_vector_type(4)));
 
+// What a descriptor reaches at most, and an offset that is beyond it.  A tile's accesses
+// are within 2^27 bytes of its first row (256 rows of 2^17 values of 4 bytes), so that the
+// limit keeps none of them out; without it an offset in a matrix of 2 GB would not be
+// outside.
+constexpr uint32_t kReach = 0x40000000u, kOutside = 0x7ffffff0u;
+
+__device__ inline uint32_t reach(int64_t bytes)
+{
+    return bytes < 0 ? 0u : bytes > kReach ? kReach : (uint32_t)bytes;
+}
+
 // Memory from `base` on, `bytes` long; reads beyond it give zeros.
 __device__ inline Descriptor descriptor(const void *base, int64_t bytes)
 {
     const uint64_t b = (uint64_t)base;
-    const uint32_t n = bytes < 0 ? 0u : bytes > 0x7fffffff ? 0x7fffffffu : (uint32_t)bytes;
+    const uint32_t n = reach(bytes);
     Descriptor d;
     d[0] = __builtin_amdgcn_readfirstlane((uint32_t)b);
     d[1] = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32) & 0xffffu);
@@ -176,8 +187,6 @@ __device__ inline Descriptor descriptor(const void *base, int64_t bytes)
     d[3] = 0x00020000u;
     return d;
 }
-
-constexpr uint32_t kOutside = 0x7ffffff0u;  // an offset that no descriptor reaches
 
 // 16 bytes a lane from offset `lane + wave` into LDS, lanes side by side from `to` on.
 __device__ inline void load_lds(const Descriptor &d, uint32_t lane, uint32_t wave, uint32_t to)
@@ -329,8 +338,7 @@ typedef __amdgpu_buffer_rsrc_t Resource;
 
 __device__ inline Resource resource(const void *base, int64_t bytes)
 {
-    return __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, bytes < 0 ? 0 : bytes > 0x7fffffff ? 0x7fffffff : (int)bytes,
-                                             0x00020000);
+    return __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)reach(bytes), 0x00020000);
 }
 
 // N elements at `lane + wave` bytes; beyond the resource nothing is written, and

@@ -90,6 +90,27 @@ def test_large(m, c, f, dtype):
     run(m, c, f, dtype, "silu")
 
 
+# outputs and gradients beyond 2 GB, columns that end inside a tile: every part of the
+# rows comes out as it does by itself, and nothing is written behind its place
+@pytest.mark.parametrize("m,c,f,dtype", [(1100000, 16, 1028, "bf16"), (1100000, 264, 1026, "f16"),
+                                         (560000, 32, 1028, "f32")])
+def test_beyond_2_gb(m, c, f, dtype):
+    g = torch.Generator(device="cuda").manual_seed(1)
+    dt = DTYPES[dtype]
+    x = torch.randn(m, c, generator=g, device="cuda").to(dt)
+    wg, wu = ((torch.randn(f, c, generator=g, device="cuda") / c ** 0.5).to(dt) for _ in range(2))
+    dh = torch.empty(m, f, dtype=dt, device="cuda")
+    for part in dh.split(100000):
+        part.copy_(torch.randn(part.shape, generator=g, device="cuda"))
+    assert dh.numel() * dh.element_size() > 2 ** 31
+    h = wt.wtconv_gated_forward(x, wg, wu)
+    dx = wt.wtconv_gated_backward(x, dh, wg, wu, need=(True, False, False))[0]
+    for at in range(0, m, 204800):  # whole tiles
+        rows = slice(at, at + 204800)
+        assert torch.equal(h[rows], wt.wtconv_gated_forward(x[rows], wg, wu)), at
+        assert torch.equal(dx[rows], wt.wtconv_gated_backward(x[rows], dh[rows], wg, wu, need=(True, False, False))[0]), at
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("m,c,f", [(3, 64, 40), (150, 64, 40), (150, 61, 43)])
 def test_addresses(m, c, f, dtype):
