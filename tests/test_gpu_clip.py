@@ -64,6 +64,17 @@ def test_norm_and_clip(name, types, offset):
     check_all(grads, scaled(keep, n, 0.37 * n))
 
 
+def test_beyond_2_31_elements():
+    g = torch.randn(1 << 20, device="cuda").bfloat16()
+    big = [g.repeat(2200), torch.randn(1000, device="cuda")]
+    n = math.sqrt(2200 * norm64([g]) ** 2 + norm64(big[1:]) ** 2)
+    norm, _ = wt.wtconv_clip_grad_norm(big, 1.0)
+    assert float(norm) == pytest.approx(n, rel=2 * U)
+    small = (g.float() * (1.0 / (n + 1e-6))).bfloat16()
+    diff = (big[0].view(2200, -1).float() - small.float()).abs()
+    assert bool((diff <= torch.finfo(torch.bfloat16).eps * small.float().abs()).all())
+
+
 def test_no_tensors():
     norm, out = wt.wtconv_clip_grad_norm([], 1.0)
     assert float(norm) == 0 and out == [] and float(wt.wtconv_grad_norm([])) == 0

@@ -61,6 +61,22 @@ def test_many_rows(rows, c, dtype):
     assert torch.equal(again[0], dx) and torch.equal(again[1], dgamma)
 
 
+@pytest.mark.parametrize("rows,c", [(2200000, 1000), (2200000, 1001), (70000, 33000)])
+def test_beyond_2_31_elements(rows, c):
+    """Rows repeat, and so do their outputs wherever they lie."""
+    few = 40  # whole periods of a row's start
+    x = torch.randn(few, c, device="cuda").bfloat16().repeat(rows // few, 1)
+    assert x.numel() > 2 ** 31
+    y, h, rstd = wt.wtconv_rms_norm_forward(x, x)
+    dx, dgamma = wt.wtconv_rms_norm_backward(h, x, rstd)
+    del h
+    small, hs, rs = wt.wtconv_rms_norm_forward(x[:few], x[:few])
+    ds, gs = wt.wtconv_rms_norm_backward(hs, x[:few], rs)
+    assert bool((y.view(-1, few, c) == small).all()) and bool((rstd.view(-1, few) == rs).all())
+    assert bool((dx.view(-1, few, c) == ds).all())
+    assert float((dgamma.double() - gs.double() * (rows // few)).norm() / dgamma.double().norm()) < 1e-5
+
+
 @pytest.mark.parametrize("c", [100, 103, 20000])
 def test_in_place(c):
     x, r, dy, dh, gamma = make(37, c, "bf16", 5)
