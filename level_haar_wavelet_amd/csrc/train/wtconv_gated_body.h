@@ -290,17 +290,21 @@ struct Nt {
     bool wide;          // rows of out and dh in accesses of two elements
 };
 
-// Tile of workgroup g: workgroups go to the 8 dies in turn, each die gets
-// neighbouring tiles, in bands of 8 tile rows, so that tiles in flight share
-// operands in its L2.
-__device__ inline void place(int64_t g, int64_t tm, int tn, int64_t &ti, int &tj)
+// Workgroups go to the 8 dies in turn: the place of workgroup g among `all` where each die
+// gets a stretch of neighbours, which share operands in its L2.
+__device__ inline int64_t place_of(int64_t g, int64_t all)
 {
-    const int64_t all = tm * tn, per = all / 8;
+    const int64_t per = all / 8;
     const int rest = (int)(all % 8), die = (int)(g % 8);
-    g = die * per + (die < rest ? die : rest) + g / 8;
-    const int64_t band = g / (8 * (int64_t)tn);
+    return die * per + (die < rest ? die : rest) + g / 8;
+}
+
+// Tile n in bands of 8 tile rows.
+__device__ inline void tile_of(int64_t n, int64_t tm, int tn, int64_t &ti, int &tj)
+{
+    const int64_t band = n / (8 * (int64_t)tn);
     const int h = tm - 8 * band < 8 ? (int)(tm - 8 * band) : 8;
-    const int in = (int)(g - band * 8 * tn);
+    const int in = (int)(n - band * 8 * tn);
     ti = band * 8 + in % h;
     tj = in / h;
 }
@@ -465,7 +469,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
 
     int64_t ti;
     int tj;
-    place(blockIdx.x, a.tm, a.tn, ti, tj);
+    tile_of(place_of(blockIdx.x, a.tm * a.tn), a.tm, a.tn, ti, tj);
     const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63, lr = lane & 31, lc = lane >> 5;
     const int64_t m0 = ti * BM;
     const int n0 = tj * (BN / 2);
@@ -524,13 +528,13 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
     const Resource rio = resource(io + m0 * a.n, (a.m - m0) * a.n * S);
     constexpr int kSets = RN / (2 * kPair);  // of blocks with the same columns of a lane
     auto column = [&](int set) { return n0 + wn / 2 + set * kPair * 32 + kPair * lr; };
-    auto place_of = [&](int f) { return ((uint32_t)(mine - m0) * a.n + f) * S; };
+    auto offset = [&](int f) { return ((uint32_t)(mine - m0) * a.n + f) * S; };
     // dh of a block of rows is sent for before the one in front of it is used: with one wave
     // a SIMD there is nothing else to do while it comes
     Vec<T, kPair> d[2][16];
     auto fetch = [&](int n) {
         const int f = column(n / RM), i = n % RM;
-        const uint32_t at0 = f < a.n ? place_of(f) : kOutside, at1 = f + 1 < a.n ? place_of(f + 1) : kOutside;
+        const uint32_t at0 = f < a.n ? offset(f) : kOutside, at1 = f + 1 < a.n ? offset(f + 1) : kOutside;
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
             const uint32_t rows = (i * 32 + row_of(q)) * a.n * S;
@@ -553,7 +557,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
                 bg[h] = a.bias0 && f + h < a.n ? a.bias0[f + h] : 0.f;
                 bu[h] = a.bias1 && f + h < a.n ? a.bias1[f + h] : 0.f;
             }
-            const uint32_t at0 = f < a.n ? place_of(f) : kOutside, at1 = f + 1 < a.n ? place_of(f + 1) : kOutside;
+            const uint32_t at0 = f < a.n ? offset(f) : kOutside, at1 = f + 1 < a.n ? offset(f + 1) : kOutside;
             const uint32_t to = f < a.fp ? ((uint32_t)(mine - m0) * a.fp + f) * 4 : kOutside;
 #pragma unroll
             for (int i = 0; i < RM; ++i) {
@@ -635,12 +639,15 @@ struct Cut {
     float *part;     // [tile][slice][bm][bn], where there are several
 };
 
-// Tile and slice (or -1) of workgroup g.
+// Tile and slice (or -1) of workgroup g: slice by slice, whose tiles read the same stretch
+// of the sum's index (tile by tile, the gradients of 50176x192x768 fp16 came from memory
+// twice, 361 MiB).
 __device__ inline int place(const Cut &c, int64_t g, int64_t &ti, int &tj, int64_t &tile)
 {
-    tile = g / c.slices;
-    place(tile, c.tm, c.tn, ti, tj);
-    return c.slices > 1 ? (int)(g % c.slices) : -1;
+    const int64_t tiles = c.tm * c.tn, n = place_of(g, tiles * c.slices);
+    tile = n % tiles;
+    tile_of(tile, c.tm, c.tn, ti, tj);
+    return c.slices > 1 ? (int)(n / tiles) : -1;
 }
 
 // A wave's accumulators to its slice's place; `mine` and `col`: this lane's first row and
@@ -666,7 +673,7 @@ __global__ __launch_bounds__(256) void gated_join(Cut c, int bm, int bn, int64_t
 {
     int64_t ti;
     int tj;
-    place(blockIdx.x, c.tm, c.tn, ti, tj);
+    tile_of(blockIdx.x, c.tm, c.tn, ti, tj);
     const int e = (blockIdx.y * 256 + threadIdx.x) * 4, col = tj * bn + e % bn;
     const int64_t row = ti * bm + e / bn, own = TURNS ? row >> 1 : row;
     if (col >= cols || own >= rows) return;
@@ -854,11 +861,11 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_tn(Tn<T> a)
     const uint32_t apitch = (uint32_t)a.fp * 4, bpitch = (uint32_t)a.b_pitch * 2;
     constexpr int kPerA = 1024 / kRowA, kPerB = 1024 / kRowB;
     static_assert(kPerA * W % 4 == 0 && kPerB * W % 4 == 0, "rows modulo 4");
-    auto place_of = [&](int per, uint32_t pitch) {
+    auto lane_offset = [&](int per, uint32_t pitch) {
         const int chunks = 64 / per, in = wave * per + lane / chunks, chunk = lane % chunks;
         return in * pitch + ((((chunk >> 1) ^ ((in & 3) * 2)) * 2) + (chunk & 1)) * 16;
     };
-    const uint32_t alane = place_of(kPerA, apitch), blane = place_of(kPerB, bpitch);
+    const uint32_t alane = lane_offset(kPerA, apitch), blane = lane_offset(kPerB, bpitch);
     const uint32_t base = lds_offset(lds);
     auto issue = [&](int s, int n) {
         const int64_t k = (s0 + s) * BK;  // first row; behind the last one there are zeros

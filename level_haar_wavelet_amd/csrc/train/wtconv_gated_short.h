@@ -52,9 +52,7 @@ __global__ __launch_bounds__(short_waves(Factor<T>::kPlanes, KS) * 64, Factor<T>
     int part;
     {
         // neighbours, which share rows of x, on one die
-        const int64_t g = blockIdx.x, all = a.tiles * a.parts, per = all / 8;
-        const int rest = (int)(all % 8), die = (int)(g % 8);
-        const int64_t id = die * per + (die < rest ? die : rest) + g / 8;
+        const int64_t id = place_of(blockIdx.x, a.tiles * a.parts);
         ti = id / a.parts;
         part = (int)(id % a.parts);
     }
