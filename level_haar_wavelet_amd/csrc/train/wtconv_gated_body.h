@@ -755,21 +755,24 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nn(Nn<T> a)
 #pragma unroll
     for (int z = 0; z < 2; ++z) blane[z] = brow * bpitch + ((((bchunk >> 1) ^ key(brow, z)) * 2) + (bchunk & 1)) * 16;
     const uint32_t base = lds_offset(lds);
+    Descriptor da[P], dw[2][P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) da[p] = descriptor(a.a + p * a.a_plane + m0 * 2 * a.fp, (a.m - m0) * apitch);
+    const int end = k1 / 2 < a.f ? k1 / 2 : a.f;
     auto issue = [&](int s, int n) {
         const int k = k0 + s * BK, p = n / (kA + kB), i = n % (kA + kB);
         const uint32_t to = base + s % NB * kStage + wave * 1024;
         if (i < kA) {
             const bool in = k + chunk * 8 < k1;
-            load_lds(descriptor(a.a + p * a.a_plane + m0 * 2 * a.fp, (a.m - m0) * apitch), in ? alane : kOutside,
-                     k * 2 + i * kTurn * apitch, to + p * BM * kRow + i * W * 1024);
+            load_lds(da[p], in ? alane : kOutside, k * 2 + i * kTurn * apitch, to + p * BM * kRow + i * W * 1024);
         } else {
             // columns behind a row's end come out of the next row, into results that nobody takes;
             // behind the last row, and behind this slice's, there are zeros
-            const int j = i - kA, z = j >= kB / 2, f = k / 2 + (j - z * (kB / 2)) * kTurnB;
+            const int j = i - kA, z = j >= kB / 2, own = j - z * (kB / 2), f = k / 2;
             const Rows<E> &w = z ? a.up : a.gate;
-            const int end = k1 / 2 < a.f ? k1 / 2 : a.f;
-            load_lds(descriptor(w.p + p * w.plane + (int64_t)f * w.pitch + n0, (int64_t)(end - f) * bpitch - n0 * 2), blane[z],
-                     0, to + kStageA + p * BK * kRowB + j * W * 1024);
+            if (own == 0)  // once for a stage: beside few matrix instructions its arithmetic counts
+                dw[z][p] = descriptor(w.p + p * w.plane + (int64_t)f * w.pitch + n0, (int64_t)(end - f) * bpitch - n0 * 2);
+            load_lds(dw[z][p], blane[z], own * kTurnB * bpitch, to + kStageA + p * BK * kRowB + j * W * 1024);
         }
     };
     const Transposed tr = transposed(lane);
@@ -867,17 +870,28 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_tn(Tn<T> a)
     };
     const uint32_t alane = lane_offset(kPerA, apitch), blane = lane_offset(kPerB, bpitch);
     const uint32_t base = lds_offset(lds);
+    // A stage's descriptors follow from those of the stage before: beside few matrix
+    // instructions their arithmetic counts.
+    Descriptor da[P], db[P];
+    const E *pa = a.a + s0 * BK * 2 * a.fp + f0, *pb = a.b + s0 * BK * a.b_pitch + c0;
+    int64_t left_a = (m1 - s0 * BK) * apitch - f0 * 2, left_b = (m1 - s0 * BK) * bpitch - c0 * 2;  // bytes
     auto issue = [&](int s, int n) {
-        const int64_t k = (s0 + s) * BK;  // first row; behind the last one there are zeros
         const int p = n / (kA + kB), i = n % (kA + kB);
         const uint32_t to = base + s % NB * kStage + wave * 1024;
-        // columns behind a row's end come out of the next row, into results that nobody takes
+        // columns behind a row's end come out of the next row, into results that nobody takes;
+        // behind the last row there are zeros
+        if (i == 0) da[p] = descriptor(pa + p * a.a_plane, left_a);
+        if (i == kA) db[p] = descriptor(pb + p * a.b_plane, left_b);
         if (i < kA)
-            load_lds(descriptor(a.a + p * a.a_plane + k * 2 * a.fp + f0, (m1 - k) * apitch - f0 * 2), alane,
-                     i * W * kPerA * apitch, to + p * BK * kRowA + i * W * 1024);
+            load_lds(da[p], alane, i * W * kPerA * apitch, to + p * BK * kRowA + i * W * 1024);
         else
-            load_lds(descriptor(a.b + p * a.b_plane + k * a.b_pitch + c0, (m1 - k) * bpitch - c0 * 2), blane,
-                     (i - kA) * W * kPerB * bpitch, to + kStageA + p * BK * kRowB + (i - kA) * W * 1024);
+            load_lds(db[p], blane, (i - kA) * W * kPerB * bpitch, to + kStageA + p * BK * kRowB + (i - kA) * W * 1024);
+        if (n + 1 == P * (kA + kB)) {
+            pa += BK * 2 * a.fp;
+            pb += BK * a.b_pitch;
+            left_a -= BK * (int64_t)apitch;
+            left_b -= BK * (int64_t)bpitch;
+        }
     };
     // rows k .. k + 8 (by lc) of columns col .. col + 32
     const Transposed tr = transposed(lane);
