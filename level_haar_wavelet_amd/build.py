@@ -2,8 +2,8 @@
 
     python -m level_haar_wavelet_amd.build
 
-compiles every ``csrc/*.hip`` (the layer) and ``csrc/train/*.hip`` (the group
-norm behind it and the Muon update of its weights) with hipcc for gfx950 into ``_build/`` and links
+compiles every ``csrc/*.hip`` (the layer) and ``csrc/train/*.hip`` (the operators
+around it in a training step) with hipcc for gfx950 into ``_build/`` and links
 ``level_haar_wavelet_amd/libwtconv.so``.  Packed fp32 instructions are switched
 off for all device code (``-Xclang -target-feature -Xclang -packed-fp32-ops``).
 """

@@ -3,12 +3,14 @@
 //
 // Two passes over the data, both bound by memory: the squares' sums, and the
 // scaling, which cannot begin before the last of them.  The elements of all tensors
-// are cut into ranges of the same length, at most about 8192 (with 2048 of them, about as many workgroups
-// as the chip holds, 414e6 elements took 577 us in place of 527: the last few run alone); a workgroup sums one, and the
-// scaling's workgroups each add the ranges' sums for themselves (up to kOwnSums of
-// them: 20 KB out of the L2), in the same order everywhere, which saves a launch between.  The
-// second pass takes the ranges from the last to the first: the 256 MB cache holds
-// the end of what the first read.
+// are cut into ranges of the same length, at most about 8192 (with 2048 of them, about
+// as many workgroups as the chip holds, 414e6 elements took 577 us in place of 527: the
+// last few run alone); a workgroup sums one, and the scaling's workgroups each add the
+// ranges' sums for themselves, in the same order everywhere, which saves a launch
+// between (more than kOwnSums of them, 20 KB out of the L2, one workgroup adds first).
+// The second pass takes the ranges from the last to the first: the 256 MB cache holds
+// the end of what the first read.  414e6 bf16 elements in 416 tensors: 139 us for the sums
+// (6.0 TB/s), 298 for the scaling (5.6).
 //
 // The table of tensors goes by value with a launch (it is then the captured call's
 // own, and needs no copy from host memory that has to stay): of up to kByValue of

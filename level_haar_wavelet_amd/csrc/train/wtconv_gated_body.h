@@ -11,7 +11,19 @@
 //   dw     [dg du]^T x, over the rows: so do both factors.
 // fp32 factors are three bf16 numbers each, which hold all 24 bits, and a product
 // six: those whose size is at least 2^-16 of the first (what is left out is below
-// 2^-23 of the whole).  The fp32 matrix instructions run at 1/16 of the 16-bit rate.
+// 2^-21 of the whole, and 2^-23 mostly).  The fp32 matrix instructions run at 1/16 of
+// the 16-bit rate.
+//
+// dg and du are held in the activations' type between the products (fp32: as the three
+// numbers): the matrix instructions take no more, and the outputs are rounded to the
+// type after them (the backward pass is off by 1.4 times the rounding alone).
+//
+// What they take, back to back (bf16, 8192x2048x5632): g, u and h 340 us, 1.11
+// PFLOP/s, where the library's product of that size alone takes 357 us; with dh in and
+// dg, du out 400 to 440; dx 330 to 360; the weights' gradients 410 to 480.  All are held
+// by the power limit: the matrix unit is busy half the time at 1.85 of 2.4 GHz.  Products
+// of short sums and few columns wait for their loads: 50176x192x768 fp16, g and u 84 us,
+// dx 56, the weights' gradients 62, whose bytes take 44, 30 and 31.
 #ifndef WTCONV_GATED_BODY_H
 #define WTCONV_GATED_BODY_H
 
@@ -325,19 +337,6 @@ __device__ inline void store4(T *p, int c, int n, bool wide, const float (&v)[4]
     }
 }
 
-template <typename T>
-__device__ inline void load4(const T *p, int c, int n, bool wide, float (&v)[4])
-{
-    if (wide && c + 4 <= n) {
-        const Vec<T, 4> r = *(const Vec<T, 4> *)(p + c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = (float)r[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = c + i < n ? (float)p[c + i] : 0.f;
-    }
-}
-
 typedef __amdgpu_buffer_rsrc_t Resource;
 
 __device__ inline Resource resource(const void *base, int64_t bytes)
@@ -444,8 +443,16 @@ struct Factors {
 };
 
 // A tile of BM rows of A and BN rows of B; WM x WN waves, NB buffers.  A stage is BK
-// elements (64 or 128 bytes) of each row, whose 16-byte chunks are permuted so that the
-// rows that a read phase covers fall into different banks.
+// elements of each row, whose 16-byte chunks are permuted so that the rows that a read
+// phase covers fall into different banks (no conflicts counted).  128 bytes of a row, a
+// cache line, in two buffers: with 64 in four, the L2s had twice the requests and dx of
+// 8192x2048x5632 bf16 took 396 us in place of 352.  fp32 factors take 64 in three: three
+// planes of 128 would not fit twice.
+//
+// Four waves of 128 x 128 each, one a SIMD, since the factors' reads from LDS then take
+// half of its rate beside the stages' writes (eight waves of 128 x 64: all of it);
+// where such tiles are fewer than the compute units, 128 x 128 for the workgroup, two of
+// them on a compute unit.
 //
 // A lane ends up with one column of every block of 32.  Rows of B are dealt to the
 // blocks so that a lane's columns are neighbours where a wave has enough of them, and
@@ -973,7 +980,8 @@ __global__ __launch_bounds__(1024) void gated_bias(const float *__restrict__ par
 // ---- Few rows ----------------------------------------------------------------------
 
 // h for at most 16 G rows: bound by the weights, which are read once, straight into
-// registers.  A workgroup takes 16 columns of g and of u; its four waves share out
+// registers (1x1024x4096 bf16: 5.5 us, 3.0 TB/s, of the weights' 16 MiB, most of it the
+// latency of a workgroup's two turns).  A workgroup takes 16 columns of g and of u; its four waves share out
 // the sum's index in stretches of 4 accesses of each row.
 template <typename T, int G, bool WIDE>
 __global__ __launch_bounds__(256) void gated_few(const T *__restrict__ x, const T *__restrict__ wg,

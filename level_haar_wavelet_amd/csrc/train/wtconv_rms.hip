@@ -3,7 +3,10 @@
 //
 // A row is read once: a row's `lanes` threads keep it in registers between the sum
 // of its squares and the outputs, so the bytes are the operator's own (x and the
-// residual in, y and the sum out), and both directions are bound by memory.
+// residual in, y and the sum out), and both directions are bound by memory: 524288x128
+// bf16 forward 92 to 99 us (5.6 TB/s), 200704x96 fp32 backward 52 us (6.0) and 5 for the join
+// of dgamma's sums, 2049x5003 fp16 backward 24 us (3.4; rows of an odd length) and 5.  An
+// elementwise pass over 4 GiB reaches 6.2.
 // Rows longer than the registers hold (kMaxHeld accesses of 256 threads) are
 // walked twice.
 //
