@@ -338,7 +338,8 @@ def wtconv_clip_grad_norm(grads, max_norm, eps=1e-6, out=None, norm=None, worksp
         if norm is None:
             made = norm = torch.empty((), dtype=_F32, device=device)
         ws, nbytes = _workspace(workspace, wtconv_grad_norm_workspace_size(len(grads)), device)
-        st = lib.wtconv_clip_grad_norm(table.buffer_info()[0], len(grads), float(max_norm), float(eps), _ptr(norm), _ptr(ws), nbytes, s)
+        st = lib.wtconv_clip_grad_norm(table.buffer_info()[0], len(grads), float(max_norm), float(eps), _ptr(norm),
+                                       _ptr(ws), nbytes, s)
         on.made(made)
     _native.check(st, "wtconv_clip_grad_norm")
     _written(given, *out)

@@ -206,7 +206,8 @@ template <typename L>
 __global__ __launch_bounds__(kThreads) void norm_ranges(L t, double *parts)
 {
     const int r = blockIdx.x, i = find(t, r);
-    const int64_t et = t.elems_type(i), n = et >> 2, e = (r - t.first(i)) * t.range, end = n - e < t.range ? n : e + t.range;
+    const int64_t et = t.elems_type(i), n = et >> 2, e = (r - t.first(i)) * t.range;
+    const int64_t end = n - e < t.range ? n : e + t.range;
     const int type = (int)(et & 3);
     const void *in = t.in(i);
     double a;
@@ -249,7 +250,8 @@ __global__ __launch_bounds__(kThreads) void clip_ranges(L t, const double *parts
     const void *in = t.in(i);
     void *out = t.out(i);
     if (f.two == 1.f && f.f == 1.f && in == out) return;
-    const int64_t et = t.elems_type(i), m = et >> 2, e = (r - t.first(i)) * t.range, end = m - e < t.range ? m : e + t.range;
+    const int64_t et = t.elems_type(i), m = et >> 2, e = (r - t.first(i)) * t.range;
+    const int64_t end = m - e < t.range ? m : e + t.range;
     const int type = (int)(et & 3);
     if (type == WTCONV_F32)
         scale_any<float, STREAM>(in, out, e, end, f);

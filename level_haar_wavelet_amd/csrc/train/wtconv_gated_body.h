@@ -20,10 +20,11 @@
 //
 // What they take, back to back (bf16, 8192x2048x5632): g, u and h 340 us, 1.11
 // PFLOP/s, where the library's product of that size alone takes 357 us; with dh in and
-// dg, du out 400 to 440; dx 330 to 360; the weights' gradients 410 to 480.  All are held
-// by the power limit: the matrix unit is busy half the time at 1.85 of 2.4 GHz.  Products
-// of short sums and few columns wait for their loads: 50176x192x768 fp16, g and u 84 us,
-// dx 56, the weights' gradients 62, whose bytes take 44, 30 and 31.
+// dg, du out 400 to 440; dx 310 to 360; the weights' gradients 410 to 480.  The counters of dx
+// show the matrix unit busy 55 % of the time, and cycles that make 1.85 GHz of 2.4: taken
+// for the power limit.  Products of short sums and few columns are further off: 50176x192x768
+// fp16 (medians), g and u 89 us, dx 60, the weights' gradients 67; the bytes that they were
+// counted to move take 45, 34 and 37.
 #ifndef WTCONV_GATED_BODY_H
 #define WTCONV_GATED_BODY_H
 
@@ -477,7 +478,8 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
     int64_t ti;
     int tj;
     tile_of(place_of(blockIdx.x, a.tm * a.tn), a.tm, a.tn, ti, tj);
-    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63, lr = lane & 31, lc = lane >> 5;
+    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int lane = t & 63, lr = lane & 31, lc = lane >> 5;
     const int64_t m0 = ti * BM;
     const int n0 = tj * (BN / 2);
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
@@ -526,7 +528,8 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
             f.a[i - RN][p] = *(const Vec<E, 8> *)(at + (p * BM + wm + (i - RN) * 32) * kRow);
     };
     float16v acc[RM][RN] = {};  // rows: A's, columns: B's
-    ring<NB, BK / 16, P *(kA + kB), P *(RM + RN), Pairs<P>::kCount * RM * RN, P, RM, RN, F>(acc, (a.k + BK - 1) / BK, issue, read);
+    ring<NB, BK / 16, P *(kA + kB), P *(RM + RN), Pairs<P>::kCount * RM * RN, P, RM, RN, F>(acc, (a.k + BK - 1) / BK,
+                                                                                            issue, read);
 
     // this lane's first row
     const int64_t mine = m0 + wm + 4 * lc;
@@ -744,7 +747,8 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nn(Nn<T> a)
     int64_t ti, tile;
     int tj;
     const int slice = place(a.cut, blockIdx.x, ti, tj, tile);
-    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63, lr = lane & 31, lc = lane >> 5;
+    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int lane = t & 63, lr = lane & 31, lc = lane >> 5;
     const int64_t m0 = ti * BM;
     const int n0 = tj * BN;
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
@@ -859,7 +863,8 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_tn(Tn<T> a)
     int64_t ti, tile;
     int tj;
     const int slice = place(a.cut, blockIdx.x, ti, tj, tile);
-    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63, lr = lane & 31, lc = lane >> 5;
+    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int lane = t & 63, lr = lane & 31, lc = lane >> 5;
     const int f0 = (int)ti * BM, c0 = tj * BN;
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
     const int64_t all = (a.m + BK - 1) / BK, s0 = slice < 0 ? 0 : slice * a.cut.stages;

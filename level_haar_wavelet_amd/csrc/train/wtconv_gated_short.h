@@ -10,12 +10,13 @@
 // two neighbouring ones and a row goes out in whole cache lines (of half lines the L2s
 // wrote 1.7 times as much to memory).
 //
-// 200704x96x384 fp32 with gelu: 182 to 198 us, 1.9 TB/s in and out; its matrix instructions
-// alone take 80, its bytes 63, and what is between is not found: without the stores it took
-// 44 us less, without the weights' loads 10.  The outputs of a chunk between the matrix
-// instructions of the next one measured the same (201) and slower in 16 bits (gelu 200704x96x384
-// bf16 81 -> 87).  In 16 bits the activation counts: that size in bf16 41 us without
-// one, 81 to 93 with gelu (bytes: 31).
+// 200704x96x384 fp32 with gelu: 179 to 198 us, 2.0 TB/s in and out.  Its bytes take 63 and its
+// matrix instructions, at the rate of a loop of nothing else, 79; what is between is not
+// found.  An earlier build of 228 us took 184 without the stores and 217 without the weights'
+// loads.  In it, the outputs of a chunk between the matrix instructions of the next one gave
+// 201, and in bf16 43 us from 41 (without activation) and 87 from 81 (gelu and biases):
+// left out.  In 16 bits the activation counts: 41 us without one, 81 to 93 with gelu
+// (bytes: 31).
 #ifndef WTCONV_GATED_SHORT_H
 #define WTCONV_GATED_SHORT_H
 
@@ -41,10 +42,11 @@ struct Short {
 };
 
 // KS steps of 16 hold a row of x, zeros behind its end.  Eight waves share the weights where
-// their two buffers leave room for one workgroup on a compute unit (50176x192x1536 fp32
-// 394 -> 358 us), else four.
+// their two buffers leave room for one workgroup on a compute unit (fp32, gelu, four and eight:
+// 50176x192x1536 382 and 337 us, 524288x128x512 842 and 758), else four.
 template <typename T, int KS, int MODE>
-__global__ __launch_bounds__(short_waves(Factor<T>::kPlanes, KS) * 64, Factor<T>::kPlanes == 1 ? 2 : 1) void gated_short(Short<T> a)
+__global__ __launch_bounds__(short_waves(Factor<T>::kPlanes, KS) * 64,
+                             Factor<T>::kPlanes == 1 ? 2 : 1) void gated_short(Short<T> a)
 {
     typedef typename Factor<T>::type E;
     constexpr int P = Factor<T>::kPlanes, S = sizeof(T), NW = short_waves(P, KS);
@@ -66,7 +68,8 @@ __global__ __launch_bounds__(short_waves(Factor<T>::kPlanes, KS) * 64, Factor<T>
         ti = id / a.parts;
         part = (int)(id % a.parts);
     }
-    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63, lr = lane & 31, lc = lane >> 5;
+    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int lane = t & 63, lr = lane & 31, lc = lane >> 5;
     const int64_t m0 = ti * 32 * NW;
     // chunks of 32 columns; two of them share 64: column 64 i + 2 r + h, or 32 i + r
     const int all = (a.n + 63) / 64 * 2, c0 = part * a.cut * 2, c1 = c0 + a.cut * 2 < all ? c0 + a.cut * 2 : all;
