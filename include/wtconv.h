@@ -396,7 +396,7 @@ wtconv_status_t wtconv_rms_norm_backward(const wtconv_rms_desc_t *desc, const vo
  *              for all of a call's; biases and their gradients fp32.  Products of
  *              16-bit types are exact and sum in fp32.  fp32 factors are taken as
  *              three bf16 numbers each (24 bits), whose products of up to 2^-16 of
- *              the whole are kept.  The backward pass holds dg and du in the
+ *              the whole are kept (those left out are at most 2^-24 of it).  The backward pass holds dg and du in the
  *              activations' type between its products (fp16: their size is limited
  *              to 65504, as that of any fp16 gradient); the biases' gradients sum
  *              them before that rounding.

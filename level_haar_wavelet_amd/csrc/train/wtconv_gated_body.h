@@ -10,8 +10,8 @@
 //          before, they cost 37 us of 1140 in 8192x2048x5632 bf16);
 //   dw     [dg du]^T x, over the rows: so do both factors.
 // fp32 factors are three bf16 numbers each, which hold all 24 bits, and a product
-// six: those whose size is at least 2^-16 of the first (what is left out is below
-// 2^-21 of the whole, and 2^-23 mostly).  The fp32 matrix instructions run at 1/16 of
+// six: those whose size is at least 2^-16 of the first (what is left out is at most
+// 2^-24 of the whole, of either sign).  The fp32 matrix instructions run at 1/16 of
 // the 16-bit rate.
 //
 // dg and du are held in the activations' type between the products (fp32: as the three
@@ -101,21 +101,34 @@ struct Pairs<3> {
     static constexpr int l[6] = {2, 0, 1, 1, 0, 0}, r[6] = {0, 2, 1, 0, 1, 0};
 };
 
-// v as the sum of P numbers.  fp32: its bits from the top, eight at a time.  (Of an
-// infinity or a NaN the second is a NaN, and with it every sum it is in.)
+// The nearest bf16 numbers to a and b, and what is left of them.
+__device__ inline Vec<__bf16, 2> nearest(float a, float b, float &ra, float &rb)
+{
+    const Vec<__bf16, 2> o = __builtin_convertvector((Vec<float, 2>{a, b}), Vec<__bf16, 2>);
+    const uint32_t both = __builtin_bit_cast(uint32_t, o);
+    ra -= __builtin_bit_cast(float, both << 16);
+    rb -= __builtin_bit_cast(float, both & 0xffff0000u);
+    return o;
+}
+
+// a and b as sums of P numbers each.  fp32: the nearest bf16 number, the nearest to the
+// rest and what is left, which fits whole (of a value in [1, 2) the last bit is 2^-23, and
+// the second rest at most 2^-17).  Cut off instead of rounded, all three had the value's
+// sign, and the three products left out had the sign of the whole: up to 2^-21.2 of it and
+// 2^-24.7 on average, now 2^-24 and zero.  Beyond the largest bf16 number that one is
+// taken, since the nearest would be infinity.  (Of an infinity or a NaN the third is a
+// NaN, and with it every sum it is in.)
 template <typename T, int P>
-__device__ inline void split(float v, typename Factor<T>::type (&o)[P])
+__device__ inline void split(float a, float b, Vec<typename Factor<T>::type, 2> (&o)[P])
 {
     if constexpr (P == 1) {
-        o[0] = (T)v;
+        o[0] = Vec<T, 2>{(T)a, (T)b};
     } else {
-        const uint32_t top = __builtin_bit_cast(uint32_t, v) & 0xffff0000u;
-        const float r1 = v - __builtin_bit_cast(float, top);
-        const uint32_t mid = __builtin_bit_cast(uint32_t, r1) & 0xffff0000u;
-        const float r2 = r1 - __builtin_bit_cast(float, mid);
-        o[0] = __builtin_bit_cast(__bf16, (uint16_t)(top >> 16));
-        o[1] = __builtin_bit_cast(__bf16, (uint16_t)(mid >> 16));
-        o[2] = __builtin_bit_cast(__bf16, (uint16_t)(__builtin_bit_cast(uint32_t, r2) >> 16));
+        constexpr float kMost = 0x1.fep127f;
+        float ra = a, rb = b, none = 0.f;
+        o[0] = nearest(__builtin_amdgcn_fmed3f(a, -kMost, kMost), __builtin_amdgcn_fmed3f(b, -kMost, kMost), ra, rb);
+        o[1] = nearest(ra, rb, ra, rb);
+        o[2] = nearest(ra, rb, none, none);
     }
 }
 
@@ -256,15 +269,17 @@ __global__ __launch_bounds__(256) void gated_pack(const T *__restrict__ src0, co
         const int64_t row = i / per;
         const int at = (int)(i - row * per) * 8;
         Vec<E, 8> o[P];
+        const T *from = src + row * k + at;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            E e[P];
-            if constexpr (P == 1)
-                e[0] = at + j < k ? src[row * k + at + j] : (T)0.f;
-            else
-                split<T, P>(at + j < k ? src[row * k + at + j] : 0.f, e);
+        for (int j = 0; j < 8; j += 2) {
+            const T v0 = at + j < k ? from[j] : (T)0.f, v1 = at + j + 1 < k ? from[j + 1] : (T)0.f;
+            Vec<E, 2> e[P];
+            split<T, P>((float)v0, (float)v1, e);
 #pragma unroll
-            for (int p = 0; p < P; ++p) o[p][j] = e[p];
+            for (int p = 0; p < P; ++p) {
+                o[p][j] = e[p][0];
+                o[p][j + 1] = e[p][1];
+            }
         }
 #pragma unroll
         for (int p = 0; p < P; ++p) *(Vec<E, 8> *)(dst + p * plane + row * kp + at) = o[p];
@@ -602,13 +617,12 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nt(Nt<T> a)
                             const float dg = dv * u[h] * slope, du = dv * y;
                             sg[h] += dg;
                             su[h] += du;
-                            E eg[P], eu[P];
-                            split<T, P>(dg, eg);
-                            split<T, P>(du, eu);
+                            Vec<E, 2> e[P];
+                            split<T, P>(dg, du, e);
 #pragma unroll
                             for (int p = 0; p < P; ++p) {
-                                o[p][2 * h] = eg[p];
-                                o[p][2 * h + 1] = eu[p];
+                                o[p][2 * h] = e[p][0];
+                                o[p][2 * h + 1] = e[p][1];
                             }
                         }
 #pragma unroll

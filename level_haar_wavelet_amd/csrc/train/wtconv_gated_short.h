@@ -120,11 +120,14 @@ __global__ __launch_bounds__(short_waves(Factor<T>::kPlanes, KS) * 64,
                         float4v, __builtin_amdgcn_raw_buffer_load_b128(
                                      x, at + h * 4 < a.c ? (row + at + h * 4) * S : kOutside, 0, 0));
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        E e[P];
-                        split<T, P>(v[j], e);
+                    for (int j = 0; j < 4; j += 2) {
+                        Vec<E, 2> e[P];
+                        split<T, P>(v[j], v[j + 1], e);
 #pragma unroll
-                        for (int p = 0; p < P; ++p) xf[k][0][p][h * 4 + j] = e[p];
+                        for (int p = 0; p < P; ++p) {
+                            xf[k][0][p][h * 4 + j] = e[p][0];
+                            xf[k][0][p][h * 4 + j + 1] = e[p][1];
+                        }
                     }
                 }
             }
@@ -200,16 +203,15 @@ __global__ __launch_bounds__(short_waves(Factor<T>::kPlanes, KS) * 64,
                     const float dg = dv * acc[0][1][q] * slope, du = dv * y;
                     sg += dg;
                     su += du;
-                    E eg[P], eu[P];
-                    split<T, P>(dg, eg);
-                    split<T, P>(du, eu);
+                    Vec<E, 2> e[P];
+                    split<T, P>(dg, du, e);
                     if constexpr (kPair == 1) {
 #pragma unroll
-                        for (int p = 0; p < P; ++p) put<E, 2>(Vec<E, 2>{eg[p], eu[p]}, grads[p], to, row_of(q) * a.fp * 4);
+                        for (int p = 0; p < P; ++p) put<E, 2>(e[p], grads[p], to, row_of(q) * a.fp * 4);
                     } else if constexpr (h == 0) {
-                        kept[q] = Vec<E, 2>{eg[0], eu[0]};
+                        kept[q] = e[0];
                     } else {
-                        put<E, 4>(Vec<E, 4>{kept[q][0], kept[q][1], eg[0], eu[0]}, grads[0], to, row_of(q) * a.fp * 4);
+                        put<E, 4>(Vec<E, 4>{kept[q][0], kept[q][1], e[0][0], e[0][1]}, grads[0], to, row_of(q) * a.fp * 4);
                     }
                 }
                 if (q % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // fewer values live at once

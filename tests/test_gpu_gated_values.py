@@ -1,0 +1,54 @@
+"""The gated product's digits and ranges on the GPU: fp32 factors in full."""
+import pytest
+import torch
+
+import level_haar_wavelet_amd as wt
+from tests.block_util import U, check
+
+pytestmark = pytest.mark.gpu
+
+
+def spread(*shape, seed=0):
+    """fp32 values with random last bits, of both signs and several powers of two."""
+    g = torch.Generator().manual_seed(seed)
+    v = (1 + torch.rand(shape, generator=g)) * 2.0 ** torch.randint(-3, 4, shape, generator=g)
+    return (v * (1 - 2 * torch.randint(0, 2, shape, generator=g))).cuda()
+
+
+def single(rows, cols, values):
+    """Rows with one value each, the r-th in column r modulo cols."""
+    t = torch.zeros(rows, cols, device="cuda")
+    r = torch.arange(rows, device="cuda")
+    t[r, r % cols] = values
+    return t
+
+
+# Sums of one product each, so that nothing but that product is off.  Of its factors' nine
+# partial products three are left out: with each number the nearest to what is left
+# before it, they are at most 2 2^-8 2^-17 + 2^-34 of the whole.  The sums of the five
+# smaller ones are below 2^-7 of it, five roundings of 2 U each; the last sum's rounding
+# is at most 2 U, to whichever side it goes.
+ONE = (1 + 2.0 ** -9 + 10 * 2.0 ** -7 + 2) * U
+
+
+# few rows, short rows (32 and 192 channels), longer ones, rows that no access divides
+@pytest.mark.parametrize("m,c,f", [(40, 32, 64), (200, 32, 256), (300, 192, 304), (200, 200, 204), (130, 33, 135)])
+def test_fp32_products_keep_their_digits(m, c, f):
+    wg, wu = spread(f, c, seed=1), torch.zeros(f, c, device="cuda")
+    up = torch.ones(f, device="cuda")  # u = 1
+    x = single(m, c, spread(m, seed=2))
+    x[3, 3] = 0.999999 * torch.finfo(torch.float32).max  # beyond the largest bf16 number
+    wg_small = wg / 16
+    h = wt.wtconv_gated_forward(x, wg_small, wu, None, up, act="none")
+    col = torch.arange(m, device="cuda") % c
+    want = x.double().sum(1, keepdim=True) * wg_small.double()[:, col].t()
+    check("h", h, want, ONE * want.abs())
+
+    x, v = spread(m, c, seed=3), spread(m, seed=4)
+    dh = single(m, f, v)  # f >= m: a column has one row
+    dx, dw, _, _, _ = wt.wtconv_gated_backward(x, dh, wg, wu, None, up, act="none")
+    want = v.double()[:, None] * wg.double()[:m]
+    check("dx", dx, want, ONE * want.abs())
+    want = v.double()[:, None] * x.double()
+    check("dw_gate", dw[:m], want, ONE * want.abs())
+    assert not bool(dw[m:].any())
