@@ -433,6 +433,15 @@ wtconv_status_t wtconv_gated_backward(const wtconv_gated_desc_t *desc, const voi
                                       void *dx, void *dw_gate, void *dw_up, float *db_gate, float *db_up,
                                       void *workspace, size_t workspace_bytes, wtconv_stream_t stream);
 
+/* The same with the weights' gradients in fp32, whatever the activations' type, for
+ * parameters that are kept in fp32 under 16-bit activations: the sums come out as they
+ * are, with their digits and beyond 65504. */
+wtconv_status_t wtconv_gated_backward_f32_grads(const wtconv_gated_desc_t *desc, const void *x, const void *dh,
+                                                const void *w_gate, const void *w_up, const float *b_gate,
+                                                const float *b_up, void *dx, float *dw_gate, float *dw_up,
+                                                float *db_gate, float *db_up, void *workspace,
+                                                size_t workspace_bytes, wtconv_stream_t stream);
+
 /* ---- Global gradient norm and clipping --------------------------------------
  * What stands between a backward pass and the optimiser's step: over all elements
  * g of `count` tensors, of any types among fp32, fp16 and bf16,

@@ -28,14 +28,15 @@ def _rows_of(t, name):
     return (t.numel() // c if c else 0), c
 
 
-def _same(t, name, like, shape=None):
-    if isinstance(t, torch.Tensor) and t.dtype is like.dtype and t.shape == (like.shape if shape is None else shape) and \
+def _same(t, name, like, shape=None, dtype=None):
+    dtype = like.dtype if dtype is None else dtype
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (like.shape if shape is None else shape) and \
             t.device == like.device and t.is_contiguous():
         return
     _gpu_tensor(t, name, like.device)
-    if t.shape != (like.shape if shape is None else shape) or t.dtype != like.dtype or not t.is_contiguous():
+    if t.shape != (like.shape if shape is None else shape) or t.dtype != dtype or not t.is_contiguous():
         raise TypeError("%s must be a contiguous %s tensor of shape %s" % (
-            name, like.dtype, tuple(like.shape if shape is None else shape)))
+            name, dtype, tuple(like.shape if shape is None else shape)))
 
 
 # ---- root-mean-square norm -------------------------------------------------------
@@ -198,25 +199,32 @@ def wtconv_gated_forward(x, w_gate, w_up, b_gate=None, b_up=None, act="silu", h=
 
 
 def wtconv_gated_backward(x, dh, w_gate, w_up, b_gate=None, b_up=None, act="silu", need=(True, True, True), dx=None,
-                          dw_gate=None, dw_up=None, db_gate=None, db_up=None, workspace=None, stream=None):
+                          dw_gate=None, dw_up=None, db_gate=None, db_up=None, workspace=None, stream=None,
+                          dw_dtype=None):
     """(dx, dw_gate, dw_up, db_gate, db_up) of the forward call whose x, weights,
     biases and act these are; dh: the gradient of h.  db_gate, db_up: (F,) float32,
-    also where a bias is None; the others have x's type.  need: whether dx, the
-    weights' and the biases' gradients are wanted; the others come as None."""
+    also where a bias is None; the others have x's type, dw_gate and dw_up where
+    dw_dtype is torch.float32 that one (their sums unrounded, for parameters that are
+    kept in it).  need: whether dx, the weights' and the biases' gradients are wanted;
+    the others come as None."""
     lib = _native.load()
     d, size, f = _gated_of(_native.OP_BWD, x, w_gate, w_up, b_gate, b_up, act)
     _same(dh, "dh", x, x.shape[:-1] + (f,))
     need_dx, need_dw, need_db = need
     if not (need_dx or need_dw or need_db):
         raise ValueError("need asks for none of the gradients")
+    if dw_dtype is None:
+        dw_dtype = x.dtype
+    elif dw_dtype not in (x.dtype, _F32):
+        raise ValueError("dw_dtype must be %s or float32, got %s" % (x.dtype, dw_dtype))
     for t, wanted, name in ((dx, need_dx, "dx"), (dw_gate, need_dw, "dw_gate"), (dw_up, need_dw, "dw_up"),
                             (db_gate, need_db, "db_gate"), (db_up, need_db, "db_up")):
         if t is not None and not wanted:
             raise ValueError("%s is given, but need does not ask for it" % name)
-    for t, name, shape in ((dx, "dx", x.shape), (dw_gate, "dw_gate", (f, x.shape[-1])),
-                           (dw_up, "dw_up", (f, x.shape[-1]))):
+    for t, name, shape, dtype in ((dx, "dx", x.shape, x.dtype), (dw_gate, "dw_gate", w_gate.shape, dw_dtype),
+                                  (dw_up, "dw_up", w_gate.shape, dw_dtype)):
         if t is not None:
-            _same(t, name, x, shape)
+            _same(t, name, x, shape, dtype)
     _f32(db_gate, "db_gate", (f,), x.device)
     _f32(db_up, "db_up", (f,), x.device)
     given = (dx, dw_gate, dw_up, db_gate, db_up)
@@ -226,17 +234,18 @@ def wtconv_gated_backward(x, dh, w_gate, w_up, b_gate=None, b_up=None, act="silu
         if dx is None and need_dx:
             made.append(dx := torch.empty_like(x))
         if dw_gate is None and need_dw:
-            made.append(dw_gate := torch.empty_like(w_gate))
+            made.append(dw_gate := torch.empty_like(w_gate, dtype=dw_dtype))
         if dw_up is None and need_dw:
-            made.append(dw_up := torch.empty_like(w_up))
+            made.append(dw_up := torch.empty_like(w_up, dtype=dw_dtype))
         if db_gate is None and need_db:
             made.append(db_gate := torch.empty((f,), dtype=_F32, device=x.device))
         if db_up is None and need_db:
             made.append(db_up := torch.empty((f,), dtype=_F32, device=x.device))
         ws, nbytes = _workspace(workspace, size, x.device)
         xa, ga, ua = _aligned(x), _aligned(w_gate), _aligned(w_up)
-        st = lib.wtconv_gated_backward(d, _ptr(xa), _ptr(dh), _ptr(ga), _ptr(ua), _ptr(b_gate), _ptr(b_up), _ptr(dx),
-                                       _ptr(dw_gate), _ptr(dw_up), _ptr(db_gate), _ptr(db_up), _ptr(ws), nbytes, s)
+        call = lib.wtconv_gated_backward if dw_dtype is x.dtype else lib.wtconv_gated_backward_f32_grads
+        st = call(d, _ptr(xa), _ptr(dh), _ptr(ga), _ptr(ua), _ptr(b_gate), _ptr(b_up), _ptr(dx), _ptr(dw_gate),
+                  _ptr(dw_up), _ptr(db_gate), _ptr(db_up), _ptr(ws), nbytes, s)
         on.made(*made)
     _native.check(st, "wtconv_gated_backward")
     _written(*given)

@@ -93,6 +93,7 @@ SIGNATURES = {
     "wtconv_gated_workspace_size": [_gdp, ctypes.c_int, _szp],
     "wtconv_gated_forward": [_gdp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
     "wtconv_gated_backward": [_gdp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "wtconv_gated_backward_f32_grads": [_gdp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
     "wtconv_grad_norm_workspace_size": [ctypes.c_int64, _szp],
     "wtconv_grad_norm": [_vp, ctypes.c_int64, _vp, _vp, _sz, _vp],
     "wtconv_clip_grad_norm": [_vp, ctypes.c_int64, ctypes.c_float, ctypes.c_float, _vp, _vp, _sz, _vp],

@@ -22,6 +22,7 @@ struct Backward {
     const void *x, *dh, *w_gate, *w_up;
     const float *b_gate, *b_up;
     void *dx, *dw_gate, *dw_up;
+    bool dw_f32;  // the weights' gradients are fp32, whatever the activations' type
     float *db_gate, *db_up;
 };
 

@@ -136,6 +136,39 @@ wtconv_status_t check_workspace(size_t need, const void *ws, size_t have)
     return aligned_to(ws, 256) ? WTCONV_OK : WTCONV_ERR_UNSUPPORTED;
 }
 
+// dw_f32: the weights' gradients are fp32.
+wtconv_status_t backward_of(const wtconv_gated_desc_t *desc, const void *x, const void *dh, const void *w_gate,
+                            const void *w_up, const float *b_gate, const float *b_up, void *dx, void *dw_gate,
+                            void *dw_up, bool dw_f32, float *db_gate, float *db_up, void *workspace,
+                            size_t workspace_bytes, hipStream_t stream)
+{
+    wtconv_status_t st = check_desc(desc);
+    if (st != WTCONV_OK) return st;
+    if (!x || !dh || !w_gate || !w_up || !dw_gate != !dw_up || !db_gate != !db_up || (!dx && !dw_gate && !db_gate))
+        return WTCONV_ERR_NULL;
+    const size_t e = esize(desc->dtype), we = dw_f32 ? 4 : e, fa = factor_alignment(*desc);
+    if (!aligned_to(x, fa) || !aligned_to(w_gate, fa) || !aligned_to(w_up, fa) || !aligned_to(dh, e) ||
+        !aligned_to(b_gate, 4) || !aligned_to(b_up, 4) || !aligned_to(dx, e) || !aligned_to(dw_gate, we) ||
+        !aligned_to(dw_up, we) || !aligned_to(db_gate, 4) || !aligned_to(db_up, 4))
+        return WTCONV_ERR_UNSUPPORTED;
+    const Sizes s = sizes_of(*desc);
+    const size_t need = wtc_gated::workspace_bytes(*desc, true), dw = s.w / e * we;
+    const Span in[] = {{x, s.x}, {dh, s.h}, {w_gate, s.w}, {w_up, s.w}, {b_gate, s.b}, {b_up, s.b}},
+               out[] = {{dx, s.x}, {dw_gate, dw}, {dw_up, dw}, {db_gate, s.b}, {db_up, s.b}, {workspace, need}};
+    if (any_alias(in, 6, out, 5)) return WTCONV_ERR_ALIAS;
+    if ((st = check_workspace(need, workspace, workspace_bytes)) != WTCONV_OK) return st;
+    if (any_alias(in, 6, out, 6)) return WTCONV_ERR_ALIAS;
+    const Backward a = {x, dh, w_gate, w_up, b_gate, b_up, dx, dw_gate, dw_up, dw_f32, db_gate, db_up};
+    hipError_t err;
+    if (desc->dtype == WTCONV_F32)
+        err = backward<float>(*desc, a, workspace, stream);
+    else if (desc->dtype == WTCONV_F16)
+        err = backward<_Float16>(*desc, a, workspace, stream);
+    else
+        err = backward<__bf16>(*desc, a, workspace, stream);
+    return err == hipSuccess ? WTCONV_OK : WTCONV_ERR_HIP;
+}
+
 }  // namespace
 
 extern "C" wtconv_status_t wtconv_gated_workspace_size(const wtconv_gated_desc_t *desc, wtconv_op_t op, size_t *bytes)
@@ -183,29 +216,17 @@ extern "C" wtconv_status_t wtconv_gated_backward(const wtconv_gated_desc_t *desc
                                                  float *db_gate, float *db_up, void *workspace, size_t workspace_bytes,
                                                  wtconv_stream_t stream)
 {
-    wtconv_status_t st = check_desc(desc);
-    if (st != WTCONV_OK) return st;
-    if (!x || !dh || !w_gate || !w_up || !dw_gate != !dw_up || !db_gate != !db_up || (!dx && !dw_gate && !db_gate))
-        return WTCONV_ERR_NULL;
-    const size_t e = esize(desc->dtype), fa = factor_alignment(*desc);
-    if (!aligned_to(x, fa) || !aligned_to(w_gate, fa) || !aligned_to(w_up, fa) || !aligned_to(dh, e) ||
-        !aligned_to(b_gate, 4) || !aligned_to(b_up, 4) || !aligned_to(dx, e) || !aligned_to(dw_gate, e) ||
-        !aligned_to(dw_up, e) || !aligned_to(db_gate, 4) || !aligned_to(db_up, 4))
-        return WTCONV_ERR_UNSUPPORTED;
-    const Sizes s = sizes_of(*desc);
-    const size_t need = wtc_gated::workspace_bytes(*desc, true);
-    const Span in[] = {{x, s.x}, {dh, s.h}, {w_gate, s.w}, {w_up, s.w}, {b_gate, s.b}, {b_up, s.b}},
-               out[] = {{dx, s.x}, {dw_gate, s.w}, {dw_up, s.w}, {db_gate, s.b}, {db_up, s.b}, {workspace, need}};
-    if (any_alias(in, 6, out, 5)) return WTCONV_ERR_ALIAS;
-    if ((st = check_workspace(need, workspace, workspace_bytes)) != WTCONV_OK) return st;
-    if (any_alias(in, 6, out, 6)) return WTCONV_ERR_ALIAS;
-    const Backward a = {x, dh, w_gate, w_up, b_gate, b_up, dx, dw_gate, dw_up, db_gate, db_up};
-    hipError_t err;
-    if (desc->dtype == WTCONV_F32)
-        err = backward<float>(*desc, a, workspace, (hipStream_t)stream);
-    else if (desc->dtype == WTCONV_F16)
-        err = backward<_Float16>(*desc, a, workspace, (hipStream_t)stream);
-    else
-        err = backward<__bf16>(*desc, a, workspace, (hipStream_t)stream);
-    return err == hipSuccess ? WTCONV_OK : WTCONV_ERR_HIP;
+    return backward_of(desc, x, dh, w_gate, w_up, b_gate, b_up, dx, dw_gate, dw_up, false, db_gate, db_up, workspace,
+                       workspace_bytes, (hipStream_t)stream);
+}
+
+extern "C" wtconv_status_t wtconv_gated_backward_f32_grads(const wtconv_gated_desc_t *desc, const void *x,
+                                                           const void *dh, const void *w_gate, const void *w_up,
+                                                           const float *b_gate, const float *b_up, void *dx,
+                                                           float *dw_gate, float *dw_up, float *db_gate,
+                                                           float *db_up, void *workspace, size_t workspace_bytes,
+                                                           wtconv_stream_t stream)
+{
+    return backward_of(desc, x, dh, w_gate, w_up, b_gate, b_up, dx, dw_gate, dw_up, true, db_gate, db_up, workspace,
+                       workspace_bytes, (hipStream_t)stream);
 }

@@ -691,9 +691,9 @@ __device__ inline void write_part(const Cut &c, int64_t tile, int slice, const f
 // The slices' sums of a tile added up, four columns a thread and 1024 / bn rows a
 // workgroup (blockIdx.y).  dx: [rows][cols] of one matrix; TURNS: rows of g's and u's
 // gradients in turn.
-template <typename T, bool TURNS>
-__global__ __launch_bounds__(256) void gated_join(Cut c, int bm, int bn, int64_t rows, int cols, T *__restrict__ out0,
-                                                  T *__restrict__ out1)
+template <typename O, bool TURNS>
+__global__ __launch_bounds__(256) void gated_join(Cut c, int bm, int bn, int64_t rows, int cols, O *__restrict__ out0,
+                                                  O *__restrict__ out1)
 {
     int64_t ti;
     int tj;
@@ -705,10 +705,10 @@ __global__ __launch_bounds__(256) void gated_join(Cut c, int bm, int bn, int64_t
     float4v v = {};
 #pragma unroll 8
     for (int s = 0; s < c.slices; ++s) v += *(const float4v *)(part + (int64_t)s * bm * bn);
-    T *out = (TURNS && (row & 1) ? out1 : out0) + own * cols;
+    O *out = (TURNS && (row & 1) ? out1 : out0) + own * cols;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (col + i < cols) out[col + i] = (T)v[i];
+        if (col + i < cols) out[col + i] = (O)v[i];
 }
 
 // ---- dx ------------------------------------------------------------------------------
@@ -845,7 +845,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_nn(Nn<T> a)
 
 // ---- The weights' gradients -------------------------------------------------------
 
-template <typename T>
+template <typename T, typename O>
 struct Tn {
     typedef typename Factor<T>::type E;
     const E *a, *b;  // [plane][m][2 fp] (dg and du in turn), [plane][m][pitch]
@@ -853,7 +853,7 @@ struct Tn {
     int64_t m;
     int f, fp, c;
     Cut cut;
-    T *gate, *up;    // [f][c]
+    O *gate, *up;    // [f][c]; O: T, or fp32 for parameters that are kept so
 };
 
 // D = A^T B, a tile of BM columns of A (gradients) and BN of B (x), over a slice
@@ -861,8 +861,8 @@ struct Tn {
 // read gives a lane four rows' values of its column: 16 lanes take 4 rows of 32
 // bytes, and these 32-byte pieces are permuted by row so that a read's rows lie in
 // different banks.
-template <typename T, int BM, int BN, int WM, int WN, int NB>
-__global__ __launch_bounds__(WM *WN * 64, 1) void gated_tn(Tn<T> a)
+template <typename T, typename O, int BM, int BN, int WM, int WN, int NB>
+__global__ __launch_bounds__(WM *WN * 64, 1) void gated_tn(Tn<T, O> a)
 {
     typedef typename Factor<T>::type E;
     constexpr int P = Factor<T>::kPlanes, W = WM * WN, BK = 32;
@@ -951,7 +951,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_tn(Tn<T> a)
         return;
     }
     // rows of g and of u in turn
-    const int64_t first = (int64_t)(f0 / 2) * a.c, bytes = (int64_t)(a.f - f0 / 2) * a.c * (int)sizeof(T);
+    const int64_t first = (int64_t)(f0 / 2) * a.c, bytes = (int64_t)(a.f - f0 / 2) * a.c * (int)sizeof(O);
     const Resource to[2] = {resource(a.gate + first, bytes), resource(a.up + first, bytes)};
 #pragma unroll
     for (int i = 0; i < RM; ++i)
@@ -960,9 +960,9 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gated_tn(Tn<T> a)
 #pragma unroll
             for (int j = 0; j < RN; ++j) {
                 const int c = c0 + wn + j * 32 + lr;
-                put<T, 1>(Vec<T, 1>{(T)acc[i][j][q]}, to[q & 1],
-                          c < a.c ? ((uint32_t)(mine / 2) * a.c + c) * (uint32_t)sizeof(T) : kOutside,
-                          (uint32_t)((i * 32 + row_of(q)) / 2) * a.c * (uint32_t)sizeof(T));
+                put<O, 1>(Vec<O, 1>{(O)acc[i][j][q]}, to[q & 1],
+                          c < a.c ? ((uint32_t)(mine / 2) * a.c + c) * (uint32_t)sizeof(O) : kOutside,
+                          (uint32_t)((i * 32 + row_of(q)) / 2) * a.c * (uint32_t)sizeof(O));
             }
 }
 
@@ -1098,12 +1098,12 @@ void launch_nt(const Tiles &t, Nt<T> &a, hipStream_t stream)
 
 inline Cut cut_of(const Tiles &t, float *part) { return {t.tm, t.tn, t.slices, t.cut, part}; }
 
-template <typename T, bool TURNS>
+template <typename O, bool TURNS>
 void launch_join(const Tiles &t, const Cut &c, int64_t rows, int64_t cols, void *out0, void *out1, hipStream_t stream)
 {
     if (t.slices > 1)
-        gated_join<T, TURNS><<<dim3((unsigned)(t.tm * t.tn), (unsigned)(t.bm * t.bn / 1024)), dim3(256), 0, stream>>>(
-            c, t.bm, t.bn, rows, (int)cols, (T *)out0, (T *)out1);
+        gated_join<O, TURNS><<<dim3((unsigned)(t.tm * t.tn), (unsigned)(t.bm * t.bn / 1024)), dim3(256), 0, stream>>>(
+            c, t.bm, t.bn, rows, (int)cols, (O *)out0, (O *)out1);
 }
 
 template <typename T>
@@ -1256,18 +1256,39 @@ hipError_t forward(const wtconv_gated_desc_t &d, const Forward &a, void *workspa
     return hipGetLastError();
 }
 
-template <typename T>
-void launch_tn(const Tiles &t, const Tn<T> &a, hipStream_t stream)
+template <typename T, typename O>
+void launch_tn(const Tiles &t, const Tn<T, O> &a, hipStream_t stream)
 {
     const dim3 grid((unsigned)t.groups());
     if constexpr (Factor<T>::kPlanes == 1) {
         if (t.bm == 256)
-            gated_tn<T, 256, 256, 2, 2, 4><<<grid, dim3(256), 0, stream>>>(a);
+            gated_tn<T, O, 256, 256, 2, 2, 4><<<grid, dim3(256), 0, stream>>>(a);
         else
-            gated_tn<T, 128, 128, 2, 2, 4><<<grid, dim3(256), 0, stream>>>(a);
+            gated_tn<T, O, 128, 128, 2, 2, 4><<<grid, dim3(256), 0, stream>>>(a);
     } else {
-        gated_tn<T, 128, 128, 2, 2, 3><<<grid, dim3(256), 0, stream>>>(a);
+        gated_tn<T, O, 128, 128, 2, 2, 3><<<grid, dim3(256), 0, stream>>>(a);
     }
+}
+
+template <typename T, typename O>
+void weights_backward(const wtconv_gated_desc_t &d, const Plan &pl, const Backward &a, const Operands<T> &o,
+                      const typename Factor<T>::type *grads, float *part, hipStream_t stream)
+{
+    Tn<T, O> q = {};
+    q.a = grads;
+    q.a_plane = d.rows * 2 * pl.fp;
+    q.b = o.x.p;
+    q.b_plane = o.x.plane;
+    q.b_pitch = o.x.pitch;
+    q.m = d.rows;
+    q.f = (int)d.f;
+    q.fp = pl.fp;
+    q.c = (int)d.c;
+    q.gate = (O *)a.dw_gate;
+    q.up = (O *)a.dw_up;
+    q.cut = cut_of(pl.dw, part);
+    launch_tn<T, O>(pl.dw, q, stream);
+    launch_join<O, true>(pl.dw, q.cut, d.f, d.c, a.dw_gate, a.dw_up, stream);
 }
 
 template <typename T>
@@ -1332,23 +1353,10 @@ hipError_t backward(const wtconv_gated_desc_t &d, const Backward &a, void *works
         launch_nn<T>(pl.dx, q, stream);
         launch_join<T, false>(pl.dx, q.cut, d.rows, d.c, a.dx, nullptr, stream);
     }
-    if (a.dw_gate) {
-        Tn<T> q = {};
-        q.a = grads;
-        q.a_plane = gplane;
-        q.b = o.x.p;
-        q.b_plane = o.x.plane;
-        q.b_pitch = o.x.pitch;
-        q.m = d.rows;
-        q.f = (int)d.f;
-        q.fp = pl.fp;
-        q.c = (int)d.c;
-        q.gate = (T *)a.dw_gate;
-        q.up = (T *)a.dw_up;
-        q.cut = cut_of(pl.dw, part);
-        launch_tn<T>(pl.dw, q, stream);
-        launch_join<T, true>(pl.dw, q.cut, d.f, d.c, a.dw_gate, a.dw_up, stream);
-    }
+    if (a.dw_gate && a.dw_f32)
+        weights_backward<T, float>(d, pl, a, o, grads, part, stream);
+    else if (a.dw_gate)
+        weights_backward<T, T>(d, pl, a, o, grads, part, stream);
     return hipGetLastError();
 }
 

@@ -245,7 +245,7 @@ class GatedFunction(torch.autograd.Function):
     x: (..., C) float32, float16 or bfloat16 on the GPU (a strided one is made
     contiguous); w_gate, w_up: (F, C) of x's type, or of another one and then
     rounded to it for the products (float32 weights under 16-bit activations), and
-    their gradients come back in theirs; b_gate, b_up: (F,) float32 or None.  Saves
+    their gradients come back in theirs, from float32 sums; b_gate, b_up: (F,) float32 or None.  Saves
     x and the weights; the backward pass computes both projections again."""
 
     @staticmethod
@@ -263,9 +263,11 @@ class GatedFunction(torch.autograd.Function):
         x, w_gate, w_up, b_gate, b_up = ctx.saved_tensors
         need = ctx.needs_input_grad
         asked = (need[0], need[1] or need[2], need[3] or need[4])
+        # of another type than x, the gradients are not rounded to x's on the way
+        own = w_gate.dtype == w_up.dtype == x.dtype
         dx, dwg, dwu, dbg, dbu = wtconv_gated_backward(
             x, dh.to(x.dtype).contiguous(), w_gate.to(x.dtype).contiguous(), w_up.to(x.dtype).contiguous(), b_gate,
-            b_up, act=ctx.act, need=asked)
+            b_up, act=ctx.act, need=asked, dw_dtype=x.dtype if own else torch.float32)
         return (dx, dwg.to(w_gate.dtype) if need[1] else None, dwu.to(w_up.dtype) if need[2] else None,
                 dbg if need[3] else None, dbu if need[4] else None, None)
 
