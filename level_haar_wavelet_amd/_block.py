@@ -292,8 +292,10 @@ def _norm_call(grads, device, norm):
     grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
     if grads:
         _gpu_tensor(grads[0], "grads[0]")
-        if device is not None and torch.device(device) != grads[0].device:
-            raise TypeError("grads[0] lies on %s, not on %s" % (grads[0].device, device))
+        if device is not None:
+            asked = torch.device(device)  # without an index: any
+            if asked != grads[0].device and (asked.type != "cuda" or asked.index is not None):
+                raise TypeError("grads[0] lies on %s, not on %s" % (grads[0].device, device))
         device = grads[0].device
     else:
         device = torch.device("cuda" if device is None else device)
