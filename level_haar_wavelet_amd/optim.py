@@ -38,7 +38,11 @@ def clip_grad_norm_(parameters, max_norm, eps=1e-6):
     grads = list({id(p.grad): p.grad for p in parameters if p.grad is not None}.values())
     # a strided gradient is scaled in a copy
     dense = [g.contiguous() for g in grads]
-    norm, _ = wtconv_clip_grad_norm(dense, max_norm, eps=eps, device=parameters[0].device if parameters else None)
+    # without any gradient, the norm comes on the parameters' GPU
+    device = None
+    if parameters and not grads:
+        device = next((p.device for p in parameters if p.is_cuda), parameters[0].device)
+    norm, _ = wtconv_clip_grad_norm(dense, max_norm, eps=eps, device=device)
     for g, d in zip(grads, dense):
         if d is not g:
             g.copy_(d)
