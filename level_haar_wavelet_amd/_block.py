@@ -166,9 +166,12 @@ def _gated_of(op, x, w_gate, w_up, b_gate, b_up, act):
     return d, need, f
 
 
-def _aligned(t):
-    """t, or a copy of it that starts on 16 bytes."""
-    return t if t.data_ptr() % 16 == 0 else t.clone()
+def _factors(*tensors):
+    """x and the weights, or copies that start on 16 bytes where the call asks for
+    that: rows of 16-bit elements that 8 divides are read as they lie."""
+    if tensors[0].dtype is _F32 or tensors[0].shape[-1] % 8:
+        return tensors
+    return [t if t.data_ptr() % 16 == 0 else t.clone() for t in tensors]
 
 
 def wtconv_gated_forward(x, w_gate, w_up, b_gate=None, b_up=None, act="silu", h=None, workspace=None, stream=None):
@@ -189,7 +192,7 @@ def wtconv_gated_forward(x, w_gate, w_up, b_gate=None, b_up=None, act="silu", h=
         if h is None:
             made = h = torch.empty(shape, dtype=x.dtype, device=x.device)
         ws, nbytes = _workspace(workspace, need, x.device)
-        xa, ga, ua = _aligned(x), _aligned(w_gate), _aligned(w_up)
+        xa, ga, ua = _factors(x, w_gate, w_up)
         st = lib.wtconv_gated_forward(d, _ptr(xa), _ptr(ga), _ptr(ua), _ptr(b_gate), _ptr(b_up), _ptr(h), _ptr(ws),
                                       nbytes, s)
         on.made(made)
@@ -242,7 +245,7 @@ def wtconv_gated_backward(x, dh, w_gate, w_up, b_gate=None, b_up=None, act="silu
         if db_up is None and need_db:
             made.append(db_up := torch.empty((f,), dtype=_F32, device=x.device))
         ws, nbytes = _workspace(workspace, size, x.device)
-        xa, ga, ua = _aligned(x), _aligned(w_gate), _aligned(w_up)
+        xa, ga, ua = _factors(x, w_gate, w_up)
         call = lib.wtconv_gated_backward if dw_dtype is x.dtype else lib.wtconv_gated_backward_f32_grads
         st = call(d, _ptr(xa), _ptr(dh), _ptr(ga), _ptr(ua), _ptr(b_gate), _ptr(b_up), _ptr(dx), _ptr(dw_gate),
                   _ptr(dw_up), _ptr(db_gate), _ptr(db_up), _ptr(ws), nbytes, s)
