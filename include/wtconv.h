@@ -396,10 +396,13 @@ wtconv_status_t wtconv_rms_norm_backward(const wtconv_rms_desc_t *desc, const vo
  *              for all of a call's; biases and their gradients fp32.  Products of
  *              16-bit types are exact and sum in fp32.  fp32 factors are taken as
  *              three bf16 numbers each (24 bits), whose products of up to 2^-16 of
- *              the whole are kept (those left out are at most 2^-24 of it).  The backward pass holds dg and du in the
- *              activations' type between its products (fp16: their size is limited
- *              to 65504, as that of any fp16 gradient); the biases' gradients sum
- *              them before that rounding.
+ *              the whole are kept (those left out are at most 2^-24 of it).  The
+ *              backward pass holds dg and du in the activations' type between its
+ *              products: dx and the weights' gradients see them rounded by half a step
+ *              of it.  fp16: they become infinite beyond 65504, lose digits below 2^-14
+ *              (steps of 2^-24) and are zero below 2^-25, as any fp16 gradient, so that
+ *              losses are to be scaled as for those.  The biases' gradients sum them
+ *              before that rounding.
  * Shape rules  rows, c, f >= 1, c and f <= 65536, rows < 2^30, rows * c and rows * f
  *              < 2^36.
  * Alignment    x and the weights 16 bytes in 16-bit types where 8 divides c, else to the

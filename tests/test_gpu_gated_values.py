@@ -1,9 +1,11 @@
-"""The gated product's digits and ranges on the GPU: fp32 factors in full."""
+"""The gated product's digits and ranges on the GPU: fp32 factors in full, fp16
+gradients that are small or large."""
 import pytest
 import torch
 
 import level_haar_wavelet_amd as wt
-from tests.block_util import U, check
+from tests.block_util import U, Gated64, check
+from tests.test_gpu_gated import NAMES, make
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +54,42 @@ def test_fp32_products_keep_their_digits(m, c, f):
     want = v.double()[:, None] * x.double()
     check("dw_gate", dw[:m], want, ONE * want.abs())
     assert not bool(dw[m:].any())
+
+
+# dg and du below 2^-14 have steps of 2^-24 (half_step counts them), below 2^-25 they are zero;
+# the biases' gradients sum them before that
+@pytest.mark.parametrize("scale", [1e-4, 2e-6, 1e3])
+@pytest.mark.parametrize("m,c,f", [(5, 64, 40), (150, 96, 72), (140, 33, 65), (300, 264, 130)])
+def test_fp16_gradients_of_any_size(m, c, f, scale):
+    x, wg, wu, bg, bu, dh = make(m, c, f, "f16", seed=m)
+    dh = (dh.float() * scale).half()
+    want = Gated64(x, wg, wu, bg, bu, "silu").backward(dh)
+    # (the weights' gradients in float32: at the largest size some of them pass 65504)
+    for name, got in zip(NAMES, wt.wtconv_gated_backward(x, dh, wg, wu, bg, bu, dw_dtype=torch.float32)):
+        check(name, got, *want[name])
+    # ... and beyond fp16's range in the weights' gradients alone
+    if scale > 1:
+        x = x.abs()
+        dh = (dh.float().abs() * 8).clamp(max=3e4).half()
+        wu.zero_()
+        want = Gated64(x, wg, wu, None, torch.ones_like(bu), "none").backward(dh)
+        out = wt.wtconv_gated_backward(x, dh, wg, wu, None, torch.ones_like(bu), act="none", dw_dtype=torch.float32)
+        check("dw_gate", out[1], *want["dw_gate"])
+        own = wt.wtconv_gated_backward(x, dh, wg, wu, None, torch.ones_like(bu), act="none")
+        assert torch.equal(own[1], out[1].half())
+        if m > 100:
+            assert float(out[1].min()) > 65504 and bool(own[1].isinf().all())
+
+
+def test_fp16_gradients_beyond_their_range():
+    """dg beyond 65504 is infinite, and with it the row of dx that it is in; no other row."""
+    x, wg, wu, bg, bu, dh = make(200, 64, 48, "f16", seed=5)
+    good = wt.wtconv_gated_backward(x, dh, wg, wu, bg, bu)
+    dh[7] = 6e4
+    x[7] *= 8
+    dx, _, _, dbg, _ = wt.wtconv_gated_backward(x, dh, wg, wu, bg, bu)
+    rows = [i for i in range(200) if i != 7]
+    assert torch.equal(dx[rows], good[0][rows])
+    want = Gated64(x, wg, wu, bg, bu, "silu").backward(dh)["db_gate"]
+    check("db_gate", dbg, *want)  # sums of fp32
+    assert not bool(dx[7].isfinite().any())
