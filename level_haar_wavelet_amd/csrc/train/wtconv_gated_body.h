@@ -25,8 +25,8 @@
 // dg, du out 400 to 440; dx 310 to 360; the weights' gradients 410 to 480.  The counters of dx
 // show the matrix unit busy 55 % of the time, and cycles that make 1.85 GHz of 2.4: taken
 // for the power limit.  Products of short sums and few columns are further off: 50176x192x768
-// fp16 (medians), g and u 89 us, dx 60, the weights' gradients 67; the bytes that they were
-// counted to move take 45, 34 and 37.
+// fp16 (medians), g and u 84 to 89 us, dx 54 to 60, the weights' gradients 61 to 67; the bytes that
+// they were counted to move take 45, 34 and 37.
 #ifndef WTCONV_GATED_BODY_H
 #define WTCONV_GATED_BODY_H
 
@@ -1137,9 +1137,6 @@ bool wide2(const void *p, int64_t n)
 {
     return n % 2 == 0 && aligned_to(p, 2 * sizeof(T));
 }
-
-template <typename T>
-bool wide4(const void *p, int64_t n);
 
 // x, the weights as the products read them.
 template <typename T>

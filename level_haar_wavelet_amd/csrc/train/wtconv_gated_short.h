@@ -15,8 +15,8 @@
 // found.  An earlier build of 228 us took 184 without the stores and 217 without the weights'
 // loads.  In it, the outputs of a chunk between the matrix instructions of the next one gave
 // 201, and in bf16 43 us from 41 (without activation) and 87 from 81 (gelu and biases):
-// left out.  In 16 bits the activation counts: 41 us without one, 81 to 93 with gelu
-// (bytes: 31).
+// left out.  In 16 bits the activation counts: 40 us without one, 59 to 74 with gelu and
+// biases (bytes: 31).
 #ifndef WTCONV_GATED_SHORT_H
 #define WTCONV_GATED_SHORT_H
 

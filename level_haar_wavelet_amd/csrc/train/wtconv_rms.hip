@@ -34,7 +34,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxHeld = 8;     // accesses of a row that a thread keeps, forward
-constexpr int kMaxHeldBack = 4;  // backward: three values of each element
+// Backward: three values of each element.  us with rows in registers, and walked twice with
+// dgamma's sums in a kernel of their own: fp32 8192x2048 (two accesses) 47, 75; 4096x4096
+// (four) 57, 81; bf16 4096x4096 (two) 33, 46; 2048x8192 (four) 35, 43.
+constexpr int kMaxHeldBack = 4;
 constexpr int kGroups = 1024;   // workgroups of the backward pass, which share out the rows
 constexpr int kChain = 64;      // rows of a slot, where there are more for it
 
