@@ -210,8 +210,8 @@ def wtconv_gated_backward(x, dh, w_gate, w_up, b_gate=None, b_up=None, act="silu
     dw_dtype is torch.float32 that one (their sums unrounded, for parameters that are
     kept in it).  The gradients of both projections are rounded to x's type before the
     products that dx and the weights' gradients are: in float16 they keep their digits
-    between 2^-14 and 65504, as any float16 gradient.  need: whether dx, the weights' and the biases' gradients are wanted;
-    the others come as None."""
+    between 2^-14 and 65504, as any float16 gradient.  need: whether dx, the weights'
+    and the biases' gradients are wanted; the others come as None."""
     lib = _native.load()
     d, size, f = _gated_of(_native.OP_BWD, x, w_gate, w_up, b_gate, b_up, act)
     _same(dh, "dh", x, x.shape[:-1] + (f,))
